@@ -56,6 +56,8 @@ extern "C" {
 #define PULSAR_ERR_TIMEOUT  -6  /* a bounded wait on the tensor cores gave up: the frame is
                                   invalid and, since work may still have been in flight,
                                   the context should be destroyed and recreated */
+#define PULSAR_ERR_WORKSPACE -8 /* a learn handle's workspace is smaller than the call needs */
+#define PULSAR_ERR_INDEX     -9 /* a token is at or above the table's rows (latched) */
 
 /* --------------------------------------------------------------- flags -- */
 /* Drop position/radius gradients (and the sphere's share of the camera
@@ -311,6 +313,107 @@ int pulsar_render_noalloc(const float* pos, const float* radius, const float* op
                           const float* features, int64_t n, const pulsar_camera_t* cam,
                           const pulsar_params_t* params, const float* bg, float* image,
                           void* stream);
+
+/* ------------------------------------------------------- learned parts --
+ * What a model trained through the renderer needs next to it: a codebook from
+ * which spheres (or any tokens) read their features, with its gradient; the
+ * normalisation and activation of a feature image, with its gradients; and
+ * the orthogonalisation of a matrix's update.  No camera or frame is
+ * involved: the calls work on a handle that owns one block of workspace.
+ *
+ * Conventions as above: caller-owned, C-contiguous device tensors, calls
+ * asynchronous on the caller's stream and issued in order on one stream per
+ * handle, argument errors found on the host before anything is enqueued.
+ * `dtype` is the type of the tensors given as void*; every sum, statistic and
+ * norm is held in 32 bits or more, and a bfloat16 result is rounded once.
+ * Tensors need their element's alignment; where they (and their rows) are
+ * 16-byte aligned the kernels move 16 bytes at a time.  Results do not depend
+ * on the launch: the same inputs give the same bits. */
+typedef struct pulsar_learn* pulsar_learn_t;
+
+#define PULSAR_F32  0   /* dtype */
+#define PULSAR_BF16 1
+#define PULSAR_I32  0   /* index: the type of tokens */
+#define PULSAR_I64  1
+#define PULSAR_ACT_NONE 0   /* act: y = z */
+#define PULSAR_ACT_SILU 1   /* y = z / (1 + exp(-z)) */
+#define PULSAR_ACT_RELU 2   /* y = max(z, 0) */
+
+/* Create a handle on CUDA device `device` with `workspace_bytes` (>= 0) of
+ * workspace; the *_workspace functions say what a call needs, and one handle
+ * serves every call that needs no more.  Errors: PULSAR_ERR_ARG,
+ * PULSAR_ERR_NOMEM, PULSAR_ERR_CUDA. */
+int pulsar_learn_create(pulsar_learn_t* out, int device, int64_t workspace_bytes);
+
+/* Release the handle and its workspace (synchronises the device). */
+int pulsar_learn_destroy(pulsar_learn_t h);
+
+/* Synchronise `stream`, then report and clear the latched device error:
+ * PULSAR_OK, PULSAR_ERR_INDEX (a token at or above the table's rows; it was
+ * treated as masked), PULSAR_ERR_TIMEOUT (a tensor-core wait gave up: the
+ * result is invalid and the handle should be destroyed). */
+int pulsar_learn_status(pulsar_learn_t h, void* stream);
+
+/* Bytes of workspace a call of these sizes needs (the forward embedding needs
+ * none), or PULSAR_ERR_ARG. */
+int64_t pulsar_embed_workspace(int64_t n, int64_t rows, int64_t dim);
+int64_t pulsar_group_norm_workspace(int64_t images, int64_t pixels, int32_t channels,
+                                    int32_t groups);
+int64_t pulsar_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int dtype);
+
+/* Codebook embedding: out_i = scale * table[tokens_i], a row of zeros where
+ * tokens_i is negative (masked).
+ *   table  [rows,dim] dtype    tokens [n] int32 or int64 (`index`)
+ *   out    [n,dim]    dtype, overwritten
+ * 0 <= n <= 0x7fff0000, 1 <= rows <= 0x7fff0000, 1 <= dim <= 65536. */
+int pulsar_embed_forward(pulsar_learn_t h, const void* table, const void* tokens, int64_t n,
+                         int64_t rows, int64_t dim, float scale, int dtype, int index, void* out,
+                         void* stream);
+
+/* Its gradient: grad_table_v = scale * sum over {i: tokens_i = v} of
+ * grad_out_i, summed by sorted tokens without floating-point atomics.
+ *   grad_out [n,dim] dtype;  grad_table [rows,dim] dtype, overwritten (zero
+ *   where no token names a row).  Errors: PULSAR_ERR_ARG,
+ *   PULSAR_ERR_WORKSPACE. */
+int pulsar_embed_backward(pulsar_learn_t h, const void* grad_out, const void* tokens, int64_t n,
+                          int64_t rows, int64_t dim, float scale, int dtype, int index,
+                          void* grad_table, void* stream);
+
+/* Group normalisation of channels-last images with an activation: over the
+ * pixels of an image and the channels / groups adjacent channels of a group,
+ *   z = weight_c (x - mean) / sqrt(var + eps) + bias_c,   y = act(z).
+ *   x, y   [images,pixels,channels] dtype (a feature image [K,H,W,C] has
+ *          K images of H*W pixels); y may be x
+ *   weight, bias [channels] float32; NULL: ones, zeros
+ *   stats  [images,groups,2] float32, 8-byte aligned, overwritten: mean,
+ *          1 / sqrt(var + eps)
+ * 0 <= images <= 65535, 0 <= pixels <= 2^40, 1 <= channels <= 4096, channels
+ * a multiple of groups, eps >= 0. */
+int pulsar_group_norm_forward(pulsar_learn_t h, const void* x, int64_t images, int64_t pixels,
+                              int32_t channels, int32_t groups, const float* weight,
+                              const float* bias, float eps, int act, int dtype, void* y,
+                              float* stats, void* stream);
+
+/* Its gradients for dL/dy = grad_y, with x and stats of the forward call:
+ *   grad_x [images,pixels,channels] dtype; grad_weight, grad_bias [channels]
+ *   float32; each overwritten, each may be NULL (not requested).  grad_x may
+ *   be grad_y or x. */
+int pulsar_group_norm_backward(pulsar_learn_t h, const void* grad_y, const void* x,
+                               const float* stats, int64_t images, int64_t pixels,
+                               int32_t channels, int32_t groups, const float* weight,
+                               const float* bias, int act, int dtype, void* grad_x,
+                               float* grad_weight, float* grad_bias, void* stream);
+
+/* Orthogonalisation of the matrices of a batch by `steps` Newton-Schulz
+ * products with the polynomial coeffs = (a, b, c) (a host array of 3):
+ *   X_0 = G / (|G|_F + eps),  X' = a X + (b A + c A^2) X,  A = X X^T,
+ * on the orientation with the fewer rows.  It drives the singular values
+ * towards 1 and keeps the singular vectors; a zero matrix stays zero.
+ *   grad, out [batch,m,n] dtype, out overwritten; out may be grad
+ * 0 <= batch <= 65535, 0 <= m, n <= 65536, 0 <= steps <= 100, eps >= 0. */
+int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int64_t m, int64_t n,
+                         int steps, const float* coeffs, float eps, int dtype, void* out,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -25,7 +25,8 @@ LIB = os.path.join(HERE, "libpulsar.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["project.cu", "bin.cu", "forward.cu", "backward.cu", "shade.cu", "pulsar.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "learn.cu", "embed.cu", "norm.cu", "orth.cu"]
+HEADERS = ["pulsar_internal.cuh", "learn_internal.cuh", "host_util.cuh"]
 
 
 def nvcc() -> str:
@@ -63,7 +64,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
           debug: bool = False, nvtx: bool = False) -> str:
     lib = lib_path(debug, nvtx)
     deps = [os.path.join(CSRC, s) for s in SOURCES] + [
-        os.path.join(CSRC, "pulsar_internal.cuh"), os.path.join(INCLUDE, "pulsar.h"), __file__]
+        os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "pulsar.h"), __file__]
     if not force and not ptxas_info and not _stale(lib, deps):
         return lib
     out_dir = os.path.join(OUT_DIR, os.path.basename(lib)[:-3]) if (debug or nvtx) else OUT_DIR

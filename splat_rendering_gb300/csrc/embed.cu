@@ -1,0 +1,585 @@
+// Codebook embedding with scaling, and its gradient by sorted tokens.
+//
+//   out_i = s table[t_i]                    (a zero row where t_i < 0)
+//   dtable_v = s sum_{i: t_i = v} dout_i    (in the order of i)
+//
+// Forward: one pass, bound by the bytes of `out`.  Lanes take 16-byte vectors
+// of a row; four rows per thread are in flight.
+//
+// Backward: the tokens are sorted (a stable radix sort of (token, i) pairs),
+// so that a table row's terms lie in a run of sorted positions and are summed
+// in the order of i by threads that own the run's columns: no floating-point
+// atomics, the same result every time.  Runs longer than a thread's share are
+// cut, and the parts joined in order, first inside a block and then between
+// blocks, so a token that takes every position costs no more than others.
+// Sums are held in 32 bits and scaled and rounded once.
+#include "learn_internal.cuh"
+
+namespace pulsar {
+namespace {
+
+constexpr int kThreads = 256;
+
+// --------------------------------------------------------------- forward --
+constexpr int kFwdRows = 4;   // rows in flight per thread
+
+// A thread's lane covers columns lane, lane + L, ... (vectors of V elements)
+// of the rows slot, slot + S, ... of its block, S = kThreads / L.
+template <typename T, typename I, int V>
+__global__ void __launch_bounds__(kThreads)
+k_embed_rows(const T* __restrict__ table, const I* __restrict__ tokens, int64_t n, int64_t rows,
+             int nv, int lshift, float scale, T* __restrict__ out, LearnState* st) {
+    pdl_begin();
+    const int lane = threadIdx.x & ((1 << lshift) - 1);
+    const int slots = kThreads >> lshift;
+    const int64_t i0 = (int64_t)blockIdx.x * (slots * kFwdRows) + (threadIdx.x >> lshift);
+    int64_t t[kFwdRows];
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kFwdRows; ++u) {
+        const int64_t i = i0 + (int64_t)u * slots;
+        t[u] = i < n ? (int64_t)tokens[i] : -1;
+        if (t[u] >= rows) {
+            t[u] = -1;
+            bad = true;
+        }
+    }
+    if (bad) atomicOr(&st->error, kErrIndex);
+    for (int v = lane; v < nv; v += 1 << lshift) {
+        float x[kFwdRows][V];
+#pragma unroll
+        for (int u = 0; u < kFwdRows; ++u) {
+            if (t[u] >= 0) {
+                Pack<T, V>::load(table + (t[u] * nv + v) * V, x[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[u][j] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kFwdRows; ++u) {
+            const int64_t i = i0 + (int64_t)u * slots;
+            if (i >= n) break;
+            // a masked row stays zero whatever the scale
+            if (t[u] >= 0) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[u][j] *= scale;
+            }
+            Pack<T, V>::store(out + (i * nv + v) * V, x[u]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ sort --
+// Stable LSD radix sort of (key, position) pairs.  A pass is two launches:
+// every block counts the digits of its contiguous chunk; then every block
+// sums the count matrix to its own offsets and scatters its chunk in order.
+// Keys are the tokens, `rows` standing for a token that contributes nothing.
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortItems = 16;                              // per thread and sub-tile
+constexpr int kSortTile = kSortThreads * kSortItems;        // 8192
+constexpr int kMaxDigit = 8;                                // bits
+constexpr int kMaxBins = 1 << kMaxDigit;
+
+template <typename I>
+__device__ __forceinline__ uint32_t token_key(I t, uint32_t rows, bool* bad) {
+    const int64_t v = (int64_t)t;
+    if (v >= (int64_t)rows) *bad = true;
+    return v >= 0 && v < (int64_t)rows ? (uint32_t)v : rows;
+}
+
+// counts[digit][block] of one pass; `keys` NULL: from the tokens.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads)
+k_sort_count(const I* __restrict__ tokens, const uint32_t* __restrict__ keys, uint32_t n,
+             uint32_t rows, uint32_t chunk, int shift, int bits, uint32_t* __restrict__ counts,
+             LearnState* st) {
+    pdl_begin();
+    __shared__ uint32_t h[kSortWarps][kMaxBins];
+    const int bins = 1 << bits, warp = threadIdx.x >> 5;
+    for (int e = threadIdx.x; e < kSortWarps * kMaxBins; e += kSortThreads) (&h[0][0])[e] = 0u;
+    __syncthreads();
+    const uint32_t lo = blockIdx.x * chunk, hi = min(n, lo + chunk);
+    bool bad = false;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
+        const uint32_t k = keys ? keys[i] : token_key(tokens[i], rows, &bad);
+        atomicAdd(&h[warp][(k >> shift) & (bins - 1)], 1u);
+    }
+    if (bad) atomicOr(&st->error, kErrIndex);
+    __syncthreads();
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+        uint32_t s = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) s += h[w][d];
+        counts[(size_t)d * gridDim.x + blockIdx.x] = s;
+    }
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads)
+k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
+               const uint32_t* __restrict__ pos, uint32_t n, uint32_t rows, uint32_t chunk,
+               int shift, int bits, const uint32_t* __restrict__ counts,
+               uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
+    pdl_begin();
+    __shared__ uint32_t base[kMaxBins];               // next output position of each digit
+    __shared__ uint32_t total[kMaxBins];
+    __shared__ uint32_t wh[kSortWarps][kMaxBins];     // per warp: count, then offset
+    const int bins = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t nb = gridDim.x, b = blockIdx.x;
+    for (int d = warp; d < bins; d += kSortWarps) {
+        uint32_t all = 0, before = 0;
+        for (uint32_t q = lane; q < nb; q += 32) {
+            const uint32_t c = counts[(size_t)d * nb + q];
+            all += c;
+            before += q < b ? c : 0u;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) {
+            total[d] = all;
+            base[d] = before;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {   // exclusive scan of the digit totals
+        uint32_t run = 0;
+        for (int d0 = 0; d0 < bins; d0 += 32) {
+            const uint32_t c = d0 + lane < bins ? total[d0 + lane] : 0u;
+            uint32_t s = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += up;
+            }
+            if (d0 + lane < bins) base[d0 + lane] += run + s - c;
+            run += __shfl_sync(0xffffffffu, s, 31);
+        }
+    }
+    const uint32_t lo = b * chunk, hi = min(n, lo + chunk);
+    bool bad = false;
+    for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
+        for (int e = threadIdx.x; e < kSortWarps * kMaxBins; e += kSortThreads)
+            (&wh[0][0])[e] = 0u;
+        __syncthreads();
+        uint32_t key[kSortItems], val[kSortItems], rank[kSortItems];
+        const uint32_t i0 = t0 + warp * (32 * kSortItems) + lane;
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            const uint32_t i = i0 + 32 * j;
+            key[j] = 0;
+            val[j] = i;
+            if (i < hi) {
+                key[j] = keys ? keys[i] : token_key(tokens[i], rows, &bad);
+                if (pos) val[j] = pos[i];
+            }
+        }
+        // rank inside the warp's 512 items, in their order
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            const bool on = i0 + 32 * j < hi;
+            const uint32_t d = (key[j] >> shift) & (bins - 1);
+            uint32_t same = __ballot_sync(0xffffffffu, on);
+            for (int q = 0; q < bits; ++q) {
+                const uint32_t m = __ballot_sync(0xffffffffu, (d >> q) & 1u);
+                same &= (d >> q) & 1u ? m : ~m;
+            }
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            rank[j] = on ? wh[warp][d] + before : 0u;
+            __syncwarp();
+            if (on && before == 0) wh[warp][d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
+            uint32_t run = base[d];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = wh[w][d];
+                wh[w][d] = run;
+                run += c;
+            }
+            base[d] = run;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortItems; ++j) {
+            if (i0 + 32 * j < hi) {
+                const uint32_t at = wh[warp][(key[j] >> shift) & (bins - 1)] + rank[j];
+                keys_out[at] = key[j];
+                pos_out[at] = val[j];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------- reduction --
+// First sorted position whose key is at least `key`.
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ keys, uint32_t n,
+                                                uint32_t key) {
+    uint32_t lo = 0, len = n;
+    while (len > 0) {
+        const uint32_t half = len >> 1;
+        if (keys[lo + half] < key) {
+            lo += half + 1;
+            len -= half + 1;
+        } else {
+            len = half;
+        }
+    }
+    return lo;
+}
+
+constexpr int kAhead = 8;   // gathered rows in flight per thread
+
+// A block's tile is S slots x q sorted positions, S = kThreads / L; the L
+// lanes of a slot own columns (vectors of V) and walk the slot's positions.
+// A run that lies inside a slot goes straight to the table.  A slot keeps two
+// parts of runs that do not: `head`, of a run that began before the slot (and
+// may pass through it), and `tail`, of a run that begins in it and goes on.
+// The slot where a run begins joins its parts in order; what leaves the tile
+// goes to tile_head / tile_tail for k_embed_join.
+enum : int { kHasHead = 1, kThrough = 2, kHasTail = 4 };
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
+               const uint32_t* __restrict__ pos, uint32_t n, uint32_t rows, int nv, int lshift,
+               int q, uint32_t tiles, float scale, T* __restrict__ out, float* __restrict__ tile_head,
+               float* __restrict__ tile_tail, int* __restrict__ tile_flag) {
+    pdl_begin();
+    const int L = 1 << lshift, S = kThreads >> lshift;
+    const int lane = threadIdx.x & (L - 1), slot = threadIdx.x >> lshift;
+    const int v = blockIdx.y * L + lane;
+    if (blockIdx.x >= tiles) {
+        // ---- the rows without a token: 32 rows per warp, one search per lane
+        const int wl = threadIdx.x & 31;
+        const uint32_t r0 = ((blockIdx.x - tiles) * (kThreads / 32) + (threadIdx.x >> 5)) * 32u;
+        if (r0 >= rows) return;
+        bool empty = false;
+        if (r0 + wl < rows) {
+            const uint32_t at = lower_bound(keys, n, r0 + wl);
+            empty = at >= n || keys[at] != r0 + wl;
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, empty);
+        const float zero[V] = {};
+        const int c1 = min(nv, (int)(blockIdx.y + 1) * L);
+        while (todo) {
+            const uint32_t r = r0 + __ffs(todo) - 1;
+            todo &= todo - 1;
+            for (int c = blockIdx.y * L + wl; c < c1; c += 32)
+                Pack<T, V>::store(out + ((size_t)r * nv + c) * V, zero);
+        }
+        return;
+    }
+    __shared__ float s_head[kThreads * V], s_tail[kThreads * V];
+    __shared__ int s_flag[kThreads];
+    __shared__ uint32_t s_key[kThreads];   // key of the slot's last position
+    const uint32_t p0 = min(n, (blockIdx.x * S + slot) * (uint32_t)q), p1 = min(n, p0 + q);
+    const bool col = v < nv;
+    int flag = 0;
+    uint32_t cur = rows;
+    auto emit = [&](uint32_t row, const float (&a)[V]) {
+        if (!col || row >= rows) return;
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = a[j] * scale;
+        Pack<T, V>::store(out + ((size_t)row * nv + v) * V, y);
+    };
+    if (p0 < p1) {
+        cur = keys[p0];
+        bool head = p0 > 0 && keys[p0 - 1] == cur;   // the current run began before the slot
+        float acc[V] = {};
+        for (uint32_t p = p0; p < p1; p += kAhead) {
+            uint32_t k[kAhead];
+            float x[kAhead][V];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                k[u] = p + u < p1 ? keys[p + u] : rows;
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[u][j] = 0.0f;
+                if (k[u] < rows && col)
+                    Pack<T, V>::load(grad + ((size_t)pos[p + u] * nv + v) * V, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (p + u >= p1) break;
+                if (k[u] != cur) {
+                    if (head) {
+                        flag |= kHasHead;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) s_head[threadIdx.x * V + j] = acc[j];
+                        head = false;
+                    } else {
+                        emit(cur, acc);
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+                    cur = k[u];
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] += x[u][j];
+            }
+        }
+        const bool goes_on = p1 < n && keys[p1] == cur;
+        if (head) {
+            flag |= kHasHead | (goes_on ? kThrough : 0);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_head[threadIdx.x * V + j] = acc[j];
+        } else if (goes_on) {
+            flag |= kHasTail;
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_tail[threadIdx.x * V + j] = acc[j];
+        } else {
+            emit(cur, acc);
+        }
+    }
+    if (lane == 0) {
+        s_flag[slot] = flag;
+        s_key[slot] = cur;
+    }
+    __syncthreads();
+    // ---- join the parts of the runs that begin in this slot, and (slot 0)
+    // of the run that began before the tile
+    const size_t at = ((size_t)blockIdx.x * nv + v) * V;
+    auto follow = [&](float (&a)[V], int s) {   // parts of the slots from s on; true: to the tile's end
+        for (; s < S; ++s) {
+            const int f = s_flag[s];
+            if (!(f & kHasHead)) return false;
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[j] += s_head[((s << lshift) + lane) * V + j];
+            if (!(f & kThrough)) return false;
+        }
+        return true;
+    };
+    int tile_bits = 0;
+    if (slot == 0 && (flag & kHasHead)) {
+        float a[V] = {};
+        const bool through = follow(a, 0);
+        tile_bits |= kHasHead | (through ? kThrough : 0);
+        if (col) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) tile_head[at + j] = a[j];
+        }
+    }
+    bool leaves = false;
+    if (flag & kHasTail) {
+        float a[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = s_tail[threadIdx.x * V + j];
+        const uint32_t key = s_key[slot];
+        leaves = follow(a, slot + 1);
+        // at the tile's end the run goes on if the next tile begins with its key
+        const uint32_t end = min(n, (blockIdx.x + 1) * (uint32_t)(S * q));
+        if (leaves) leaves = end < n && keys[end] == key;
+        if (!leaves) {
+            emit(key, a);
+        } else if (col) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) tile_tail[at + j] = a[j];
+        }
+    }
+    const bool any_leaves = __syncthreads_or(leaves);
+    if (threadIdx.x == 0 && blockIdx.y == 0)
+        tile_flag[blockIdx.x] = tile_bits | (any_leaves ? kHasTail : 0);
+}
+
+// The runs that leave the tile they begin in: one block per tile (and column
+// block), its slots striding over the tiles the run covers, joined in order
+// of the slots.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+k_embed_join(const uint32_t* __restrict__ keys, uint32_t n, uint32_t rows, int nv, int lshift, int q,
+             float scale, T* __restrict__ out, const float* __restrict__ tile_head,
+             const float* __restrict__ tile_tail, const int* __restrict__ tile_flag) {
+    pdl_begin();
+    if (!(tile_flag[blockIdx.x] & kHasTail)) return;
+    const int L = 1 << lshift, S = kThreads >> lshift;
+    const int lane = threadIdx.x & (L - 1), slot = threadIdx.x >> lshift;
+    const int v = blockIdx.y * L + lane;
+    const uint32_t tile = S * q;
+    const uint32_t key = keys[(blockIdx.x + 1) * tile - 1];
+    if (key >= rows) return;
+    const uint32_t last = (lower_bound(keys, n, key + 1) - 1) / tile;   // the run's last tile
+    __shared__ float part[kThreads * V];
+    float a[V] = {};
+    if (v < nv) {
+        for (uint32_t t = blockIdx.x + 1 + slot; t <= last; t += S) {
+            const float* h = tile_head + ((size_t)t * nv + v) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[j] += h[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[threadIdx.x * V + j] = a[j];
+    __syncthreads();
+    if (slot == 0 && v < nv) {
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = tile_tail[((size_t)blockIdx.x * nv + v) * V + j];
+        for (int s = 0; s < S; ++s) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[j] += part[((s << lshift) + lane) * V + j];
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] *= scale;
+        Pack<T, V>::store(out + ((size_t)key * nv + v) * V, y);
+    }
+}
+
+// ----------------------------------------------------------------- plans --
+int log2_up(int64_t v) {
+    int s = 0;
+    while (((int64_t)1 << s) < v) ++s;
+    return s;
+}
+
+struct SortPlan {
+    int passes, bits;
+    uint32_t blocks, chunk;
+};
+constexpr uint32_t kSortBlocks = 152;   // one per SM: the count matrix stays small
+SortPlan sort_plan(int64_t n, int64_t rows) {
+    SortPlan p;
+    const int kb = log2_up(rows + 1) > 0 ? log2_up(rows + 1) : 1;   // keys 0 .. rows
+    p.passes = (kb + kMaxDigit - 1) / kMaxDigit;
+    p.bits = (kb + p.passes - 1) / p.passes;
+    const int64_t per = ceil_div(n, kSortBlocks);
+    p.chunk = (uint32_t)(ceil_div(per < 2048 ? 2048 : per, 32) * 32);
+    p.blocks = (uint32_t)ceil_div(n, p.chunk);
+    return p;
+}
+
+// Tile shape of the reduction for rows of nv vectors.
+struct ReducePlan {
+    int lshift, q;
+    uint32_t tiles;
+    unsigned cols;
+};
+ReducePlan reduce_plan(int64_t n, int64_t nv) {
+    ReducePlan r;
+    r.lshift = log2_up(nv);
+    r.lshift = r.lshift < 2 ? 2 : r.lshift > 8 ? 8 : r.lshift;
+    const int64_t S = kThreads >> r.lshift;
+    // as many positions per slot as leave two blocks per SM, 8 to 32
+    r.q = 32;
+    while (r.q > kAhead && S * r.q * 304 > n) r.q >>= 1;
+    r.tiles = (uint32_t)ceil_div(n, S * r.q);
+    r.cols = (unsigned)ceil_div(nv, 1 << r.lshift);
+    return r;
+}
+
+struct BackwardSpace {
+    uint32_t *keys[2], *pos[2], *counts;
+    float *head, *tail;
+    int* flag;
+};
+// V only splits a row: nv * V is dim, so the pieces have one size for both.
+BackwardSpace carve(Carve& w, int64_t n, int64_t dim, uint32_t tiles) {
+    BackwardSpace s;
+    for (int k = 0; k < 2; ++k) {
+        s.keys[k] = w.take<uint32_t>(n);
+        s.pos[k] = w.take<uint32_t>(n);
+    }
+    s.counts = w.take<uint32_t>((size_t)kMaxBins * kSortBlocks);
+    s.head = w.take<float>((size_t)tiles * dim);
+    s.tail = w.take<float>((size_t)tiles * dim);
+    s.flag = w.take<int>(tiles);
+    return s;
+}
+
+template <typename T, typename I, int V>
+cudaError_t forward(const EmbedCall& c, LearnState* st, cudaStream_t s) {
+    const int64_t nv = c.dim / V;
+    int ls = log2_up(nv);
+    ls = ls > 5 ? 5 : ls;
+    const int64_t per = (int64_t)(kThreads >> ls) * kFwdRows;
+    return launch_pdl(k_embed_rows<T, I, V>, dim3((unsigned)ceil_div(c.n, per)), dim3(kThreads), 0,
+                      s, (const T*)c.src, (const I*)c.tokens, c.n, c.rows, (int)nv, ls, c.scale,
+                      (T*)c.dst, st);
+}
+
+template <typename T, int V>
+cudaError_t reduce(const EmbedCall& c, const BackwardSpace& w, int from, const ReducePlan& r,
+                   cudaStream_t s) {
+    const int nv = (int)(c.dim / V);
+    const uint32_t n = (uint32_t)c.n, rows = (uint32_t)c.rows;
+    const unsigned zero_blocks = (unsigned)ceil_div(rows, kThreads);
+    cudaError_t e = launch_pdl(k_embed_reduce<T, V>, dim3(r.tiles + zero_blocks, r.cols),
+                               dim3(kThreads), 0, s, (const T*)c.src, (const uint32_t*)w.keys[from],
+                               (const uint32_t*)w.pos[from], n, rows, nv, r.lshift, r.q, r.tiles,
+                               c.scale, (T*)c.dst, w.head, w.tail, w.flag);
+    if (e != cudaSuccess || r.tiles < 2) return e;
+    return launch_pdl(k_embed_join<T, V>, dim3(r.tiles - 1, r.cols), dim3(kThreads), 0, s,
+                      (const uint32_t*)w.keys[from], n, rows, nv, r.lshift, r.q, c.scale,
+                      (T*)c.dst, (const float*)w.head, (const float*)w.tail, (const int*)w.flag);
+}
+
+template <typename T, typename I>
+cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t s) {
+    const bool wide = c.dim % VecOf<T>::n == 0 && aligned16(c.src) && aligned16(c.dst);
+    const ReducePlan r = reduce_plan(c.n, wide ? c.dim / VecOf<T>::n : c.dim);
+    Carve cv{static_cast<unsigned char*>(ws)};
+    const BackwardSpace w = carve(cv, c.n, c.dim, r.tiles);
+    const SortPlan p = sort_plan(c.n, c.rows);
+    const uint32_t n = (uint32_t)c.n, rows = (uint32_t)c.rows;
+    for (int k = 0; k < p.passes; ++k) {
+        const uint32_t* ki = k ? w.keys[(k - 1) & 1] : nullptr;
+        const uint32_t* pi = k ? w.pos[(k - 1) & 1] : nullptr;
+        cudaError_t e = launch_pdl(k_sort_count<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                                   (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits, p.bits,
+                                   w.counts, st);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                           (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
+                           (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
+        if (e != cudaSuccess) return e;
+    }
+    const int from = (p.passes - 1) & 1;
+    return wide ? reduce<T, VecOf<T>::n>(c, w, from, r, s) : reduce<T, 1>(c, w, from, r, s);
+}
+
+}  // namespace
+
+size_t embed_workspace(int64_t n, int64_t rows, int64_t dim) {
+    if (n == 0) return 0;
+    // the larger of the plans of the vector and the element form
+    uint32_t tiles = reduce_plan(n, dim).tiles;
+    for (int v = 4; v <= 8; v += 4)
+        if (dim % v == 0 && reduce_plan(n, dim / v).tiles > tiles) tiles = reduce_plan(n, dim / v).tiles;
+    Carve cv{nullptr};
+    carve(cv, n, dim, tiles);
+    return cv.used;
+}
+
+cudaError_t launch_embed_forward(const EmbedCall& c, LearnState* st, cudaStream_t s) {
+    if (c.n == 0) return cudaSuccess;
+    using B = __nv_bfloat16;
+    const int v = c.dtype == kBf16 ? 8 : 4;
+    const bool wide = c.dim % v == 0 && aligned16(c.src) && aligned16(c.dst);
+    if (c.dtype == kF32)
+        return c.index == kI32 ? (wide ? forward<float, int32_t, 4>(c, st, s)
+                                       : forward<float, int32_t, 1>(c, st, s))
+                               : (wide ? forward<float, int64_t, 4>(c, st, s)
+                                       : forward<float, int64_t, 1>(c, st, s));
+    return c.index == kI32 ? (wide ? forward<B, int32_t, 8>(c, st, s)
+                                   : forward<B, int32_t, 1>(c, st, s))
+                           : (wide ? forward<B, int64_t, 8>(c, st, s)
+                                   : forward<B, int64_t, 1>(c, st, s));
+}
+
+cudaError_t launch_embed_backward(const EmbedCall& c, LearnState* st, void* ws, int n_sms,
+                                  cudaStream_t s) {
+    (void)n_sms;
+    if (c.n == 0)
+        return cudaMemsetAsync(c.dst, 0, (size_t)c.rows * c.dim * (c.dtype == kBf16 ? 2 : 4), s);
+    if (c.dtype == kF32)
+        return c.index == kI32 ? backward<float, int32_t>(c, st, ws, s)
+                               : backward<float, int64_t>(c, st, ws, s);
+    return c.index == kI32 ? backward<__nv_bfloat16, int32_t>(c, st, ws, s)
+                           : backward<__nv_bfloat16, int64_t>(c, st, ws, s);
+}
+
+}  // namespace pulsar

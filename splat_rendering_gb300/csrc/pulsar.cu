@@ -10,23 +10,8 @@
 #include <vector>
 
 #include "../../include/pulsar.h"
+#include "host_util.cuh"
 #include "pulsar_internal.cuh"
-
-// NVTX ranges around the entry points (build with -DPULSAR_NVTX: header-only
-// NVTX3, no link dependency, no cost when no tool is attached); compiled out
-// by default.
-#ifdef PULSAR_NVTX
-#include <nvtx3/nvToolsExt.h>
-namespace {
-struct NvtxScope {
-    explicit NvtxScope(const char* name) { nvtxRangePushA(name); }
-    ~NvtxScope() { nvtxRangePop(); }
-};
-}  // namespace
-#define PULSAR_TRACE(name) NvtxScope pulsar_trace_scope_(name)
-#else
-#define PULSAR_TRACE(name) ((void)0)
-#endif
 
 using namespace pulsar;
 
@@ -51,22 +36,6 @@ struct pulsar_ctx {
 };
 
 namespace {
-
-cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-
-int cuda_err(cudaError_t e) { return e == cudaSuccess ? PULSAR_OK : PULSAR_ERR_CUDA; }
-
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        if (prev != dev) cudaSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
 
 template <typename T>
 bool alloc(pulsar_ctx* c, T** p, size_t count) {
@@ -100,6 +69,8 @@ const char* pulsar_strerror(int code) {
         case PULSAR_ERR_STATE: return "call out of order";
         case PULSAR_ERR_NOMEM: return "workspace allocation failed";
         case PULSAR_ERR_TIMEOUT: return "a bounded wait on the tensor cores gave up";
+        case PULSAR_ERR_WORKSPACE: return "the handle's workspace is smaller than the call needs";
+        case PULSAR_ERR_INDEX: return "a token is outside the table";
         case PULSAR_ERR_INTERNAL: return "a device index check failed (debug build)";
         default: return "unknown error";
     }

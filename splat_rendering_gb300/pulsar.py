@@ -7,6 +7,9 @@ PyTorch is used only for device memory and streams.
 Functions mirror the C entry points:
     create, destroy, project, bin, forward, backward, status, strerror,
     debug_copy
+and, for the learned parts around the renderer (codebook embedding, group
+norm, orthogonalised updates), the Learner class and the *_workspace
+functions.
 Tensor arguments are CUDA torch tensors (float32, contiguous) or raw device
 pointers (int); streams are torch.cuda.Stream objects, raw handles (int) or
 None for the current torch stream.
@@ -23,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libpulsar.so")
 
 OK, ERR_ARG, ERR_CUDA, ERR_CAPACITY, ERR_STATE, ERR_NOMEM, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
 ERR_INTERNAL = -7   # debug build: a device index check failed
+ERR_WORKSPACE, ERR_INDEX = -8, -9
 FLAG_GEOM_CUTOFF = 0x1
 FLAG_COUNT_HITS = 0x2
 FLAG_NORMALIZE_GRADS = 0x4
@@ -56,7 +60,11 @@ class Params(ctypes.Structure):
 EXPORTS = ("pulsar_create", "pulsar_create_cams", "pulsar_destroy", "pulsar_project",
            "pulsar_project_cams", "pulsar_bin", "pulsar_shade_forward", "pulsar_shade_backward",
            "pulsar_forward", "pulsar_backward", "pulsar_status", "pulsar_strerror",
-           "pulsar_debug_copy", "pulsar_debug_inject", "pulsar_render_noalloc")
+           "pulsar_debug_copy", "pulsar_debug_inject", "pulsar_render_noalloc",
+           "pulsar_learn_create", "pulsar_learn_destroy", "pulsar_learn_status",
+           "pulsar_embed_workspace", "pulsar_group_norm_workspace",
+           "pulsar_orthogonalize_workspace", "pulsar_embed_forward", "pulsar_embed_backward",
+           "pulsar_group_norm_forward", "pulsar_group_norm_backward", "pulsar_orthogonalize")
 
 
 def load(path: str = LIB_PATH):
@@ -90,8 +98,25 @@ def load(path: str = LIB_PATH):
     lib.pulsar_debug_copy.restype = I64
     lib.pulsar_render_noalloc.argtypes = [P, P, P, P, I64, ctypes.POINTER(Camera),
                                           ctypes.POINTER(Params), P, P, P]
+    I, F = ctypes.c_int, ctypes.c_float
+    lib.pulsar_learn_create.argtypes = [ctypes.POINTER(P), I, I64]
+    lib.pulsar_learn_destroy.argtypes = [P]
+    lib.pulsar_learn_status.argtypes = [P, P]
+    lib.pulsar_embed_workspace.argtypes = [I64, I64, I64]
+    lib.pulsar_group_norm_workspace.argtypes = [I64, I64, I32, I32]
+    lib.pulsar_orthogonalize_workspace.argtypes = [I64, I64, I64, I]
+    workspaces = ("pulsar_embed_workspace", "pulsar_group_norm_workspace",
+                  "pulsar_orthogonalize_workspace")
+    for name in workspaces:
+        getattr(lib, name).restype = I64
+    lib.pulsar_embed_forward.argtypes = [P, P, P, I64, I64, I64, F, I, I, P, P]
+    lib.pulsar_embed_backward.argtypes = [P, P, P, I64, I64, I64, F, I, I, P, P]
+    lib.pulsar_group_norm_forward.argtypes = [P, P, I64, I64, I32, I32, P, P, F, I, I, P, P, P]
+    lib.pulsar_group_norm_backward.argtypes = [P, P, P, P, I64, I64, I32, I32, P, P, I, I, P, P, P,
+                                               P]
+    lib.pulsar_orthogonalize.argtypes = [P, P, I64, I64, I64, I, P, F, I, P, P]
     for name in EXPORTS:
-        if name not in ("pulsar_strerror", "pulsar_debug_copy"):
+        if name not in ("pulsar_strerror", "pulsar_debug_copy") + workspaces:
             getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -349,3 +374,219 @@ INJECT_SHADE_TIMEOUT = 1
 def debug_inject(ctx, what: int, stream=None):
     """Arm a test failure (see pulsar_debug_inject in include/pulsar.h)."""
     _check(load().pulsar_debug_inject(ctx, int(what), _stream(stream)), "pulsar_debug_inject")
+
+
+# ---------------------------------------------------------- learned parts --
+ACT = dict(none=0, silu=1, relu=2)
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    if dtype == torch.float32:
+        return 0
+    if dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"float32 or bfloat16 is wanted, got {dtype}")
+
+
+def _index_code(dtype) -> int:
+    import torch
+    if dtype == torch.int32:
+        return 0
+    if dtype == torch.int64:
+        return 1
+    raise TypeError(f"tokens are int32 or int64, got {dtype}")
+
+
+def _bytes(code: int, what: str) -> int:
+    if code < 0:
+        raise PulsarError(int(code), what)
+    return int(code)
+
+
+def embed_workspace(n: int, rows: int, dim: int) -> int:
+    """Bytes of workspace of Learner.embed_backward for n tokens."""
+    return _bytes(load().pulsar_embed_workspace(n, rows, dim), "pulsar_embed_workspace")
+
+
+def group_norm_workspace(images: int, pixels: int, channels: int, groups: int) -> int:
+    """Bytes of workspace of Learner.group_norm and group_norm_backward."""
+    return _bytes(load().pulsar_group_norm_workspace(images, pixels, channels, groups),
+                  "pulsar_group_norm_workspace")
+
+
+def orthogonalize_workspace(batch: int, m: int, n: int, dtype) -> int:
+    """Bytes of workspace of Learner.orthogonalize for `batch` m x n matrices."""
+    return _bytes(load().pulsar_orthogonalize_workspace(batch, m, n, _dtype_code(dtype)),
+                  "pulsar_orthogonalize_workspace")
+
+
+class Learner:
+    """A handle for the learned parts around the renderer, and its calls on
+    torch tensors of one device (see include/pulsar.h for what they compute).
+
+        ops = Learner(workspace_bytes=embed_workspace(n, rows, dim))
+        features = ops.embed(codebook, tokens)          # -> Renderer.render
+        y, stats = ops.group_norm(image, groups, weight, bias, act="silu")
+        grad_image, gw, gb = ops.group_norm_backward(grad_y, image, stats, groups, weight, bias)
+        grad_codebook = ops.embed_backward(grad_features, tokens, rows)
+        update = ops.orthogonalize(grad_matrix)
+
+    Tensors are contiguous and on the handle's device; anything else raises
+    before a kernel is launched.  Outputs are allocated unless given."""
+
+    def __init__(self, workspace_bytes: int, device: int = 0):
+        self.device, self.workspace_bytes = int(device), int(workspace_bytes)
+        self.handle = 0
+        h = ctypes.c_void_p()
+        _check(load().pulsar_learn_create(ctypes.byref(h), self.device, self.workspace_bytes),
+               "pulsar_learn_create")
+        self.handle = h.value
+
+    def close(self):
+        if self.handle:
+            _check(load().pulsar_learn_destroy(self.handle), "pulsar_learn_destroy")
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def status(self, stream=None, raise_on_error: bool = True) -> int:
+        """Synchronise the stream and report the latched device error."""
+        code = load().pulsar_learn_status(self.handle, self._stream(stream))
+        if raise_on_error:
+            _check(code, "pulsar_learn_status")
+        return code
+
+    def _stream(self, s):
+        if s is None:
+            import torch
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return _stream(s)
+
+    def _tensor(self, t, what: str, shape=None, dtype=None):
+        """Checks a tensor argument and returns its pointer (None stays None)."""
+        if t is None:
+            return None
+        if not t.is_cuda or t.get_device() != self.device:
+            raise ValueError(f"{what} is not on cuda:{self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} is not contiguous")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, wanted {tuple(shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{what} is {t.dtype}, wanted {dtype}")
+        return t.data_ptr()
+
+    def _empty(self, shape, dtype):
+        import torch
+        return torch.empty(shape, device=f"cuda:{self.device}", dtype=dtype)
+
+    def embed(self, table, tokens, scale: float = 1.0, out=None, stream=None):
+        """scale * table[tokens] ([*tokens.shape, dim]); zeros where a token is negative."""
+        if table.dim() != 2:
+            raise ValueError(f"table has shape {tuple(table.shape)}, wanted [rows, dim]")
+        rows, dim = table.shape
+        shape = tuple(tokens.shape) + (dim,)
+        dt, ix = _dtype_code(table.dtype), _index_code(tokens.dtype)
+        if out is None:
+            out = self._empty(shape, table.dtype)
+        _check(load().pulsar_embed_forward(
+            self.handle, self._tensor(table, "table"), self._tensor(tokens, "tokens"),
+            tokens.numel(), rows, dim, scale, dt, ix,
+            self._tensor(out, "out", shape, table.dtype), self._stream(stream)),
+            "pulsar_embed_forward")
+        return out
+
+    def embed_backward(self, grad_out, tokens, rows: int, scale: float = 1.0, grad_table=None,
+                       stream=None):
+        """Gradient [rows, dim] of `embed` for grad_out [*tokens.shape, dim]."""
+        if tuple(grad_out.shape[:-1]) != tuple(tokens.shape):
+            raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, wanted "
+                             f"{tuple(tokens.shape) + ('dim',)}")
+        dim = grad_out.shape[-1]
+        dt, ix = _dtype_code(grad_out.dtype), _index_code(tokens.dtype)
+        if grad_table is None:
+            grad_table = self._empty((rows, dim), grad_out.dtype)
+        _check(load().pulsar_embed_backward(
+            self.handle, self._tensor(grad_out, "grad_out"), self._tensor(tokens, "tokens"),
+            tokens.numel(), rows, dim, scale, dt, ix,
+            self._tensor(grad_table, "grad_table", (rows, dim), grad_out.dtype),
+            self._stream(stream)), "pulsar_embed_backward")
+        return grad_table
+
+    @staticmethod
+    def _image_shape(x, act):
+        if x.dim() < 2:
+            raise ValueError(f"x has shape {tuple(x.shape)}, wanted [images, ..., channels]")
+        if act not in ACT:
+            raise ValueError(f"act is one of {sorted(ACT)}, got {act!r}")
+        pixels = 1
+        for d in x.shape[1:-1]:
+            pixels *= int(d)
+        return int(x.shape[0]), pixels, int(x.shape[-1]), ACT[act]
+
+    def group_norm(self, x, groups: int, weight=None, bias=None, eps: float = 1e-5,
+                   act: str = "none", out=None, stats=None, stream=None):
+        """(y, stats): act(group norm) of x [images, ..., channels], channels
+        last, and the (mean, 1/std) [images, groups, 2] its backward needs."""
+        import torch
+        images, pixels, C, a = self._image_shape(x, act)
+        dt, f32 = _dtype_code(x.dtype), torch.float32
+        if out is None:
+            out = self._empty(x.shape, x.dtype)
+        if stats is None:
+            stats = self._empty((images, groups, 2), f32)
+        _check(load().pulsar_group_norm_forward(
+            self.handle, self._tensor(x, "x"), images, pixels, C, groups,
+            self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32),
+            eps, a, dt, self._tensor(out, "out", x.shape, x.dtype),
+            self._tensor(stats, "stats", (images, groups, 2), f32), self._stream(stream)),
+            "pulsar_group_norm_forward")
+        return out, stats
+
+    def group_norm_backward(self, grad_y, x, stats, groups: int, weight=None, bias=None,
+                            act: str = "none", grad_x=None, grad_weight=None, grad_bias=None,
+                            want=("x", "weight", "bias"), stream=None):
+        """(grad_x, grad_weight, grad_bias) of `group_norm`; those not in
+        `want` (and not given) are None and not computed."""
+        import torch
+        images, pixels, C, a = self._image_shape(x, act)
+        dt, f32 = _dtype_code(x.dtype), torch.float32
+        if grad_x is None and "x" in want:
+            grad_x = self._empty(x.shape, x.dtype)
+        if grad_weight is None and "weight" in want:
+            grad_weight = self._empty((C,), f32)
+        if grad_bias is None and "bias" in want:
+            grad_bias = self._empty((C,), f32)
+        _check(load().pulsar_group_norm_backward(
+            self.handle, self._tensor(grad_y, "grad_y", x.shape, x.dtype), self._tensor(x, "x"),
+            self._tensor(stats, "stats", (images, groups, 2), f32), images, pixels, C, groups,
+            self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32), a, dt,
+            self._tensor(grad_x, "grad_x", x.shape, x.dtype),
+            self._tensor(grad_weight, "grad_weight", (C,), f32),
+            self._tensor(grad_bias, "grad_bias", (C,), f32), self._stream(stream)),
+            "pulsar_group_norm_backward")
+        return grad_x, grad_weight, grad_bias
+
+    def orthogonalize(self, grad, steps: int = 5, coeffs=(3.4445, -4.775, 2.0315),
+                      eps: float = 1e-7, out=None, stream=None):
+        """`steps` Newton-Schulz products on each matrix of grad [..., m, n]."""
+        if grad.dim() < 2:
+            raise ValueError(f"grad has shape {tuple(grad.shape)}, wanted [..., m, n]")
+        m, n = grad.shape[-2:]
+        batch = 1
+        for d in grad.shape[:-2]:
+            batch *= int(d)
+        dt = _dtype_code(grad.dtype)
+        if out is None:
+            out = self._empty(grad.shape, grad.dtype)
+        abc = (ctypes.c_float * 3)(*[float(v) for v in coeffs])
+        _check(load().pulsar_orthogonalize(
+            self.handle, self._tensor(grad, "grad"), batch, m, n, steps, abc, eps, dt,
+            self._tensor(out, "out", grad.shape, grad.dtype), self._stream(stream)),
+            "pulsar_orthogonalize")
+        return out
