@@ -26,7 +26,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["project.cu", "bin.cu", "forward.cu", "backward.cu", "shade.cu", "pulsar.cu",
            "noalloc.cu", "learn.cu", "embed.cu", "norm.cu", "orth.cu"]
-HEADERS = ["pulsar_internal.cuh", "learn_internal.cuh", "host_util.cuh"]
+HEADERS = ["pulsar_internal.cuh", "tensor_core.cuh", "learn_internal.cuh", "host_util.cuh"]
 
 
 def nvcc() -> str:

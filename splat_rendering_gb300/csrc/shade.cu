@@ -28,7 +28,7 @@
 // place and accumulates the CTA's share of dW in tensor memory across all
 // its tiles; a ones column in the x and h2 tiles turns the same MMAs into
 // the bias gradients.
-#include "pulsar_internal.cuh"
+#include "tensor_core.cuh"
 
 #include <cuda_bf16.h>
 
@@ -49,7 +49,6 @@ constexpr int kOffB3 = kOffW3 + 3 * kHid;
 static_assert(kOffB3 + 3 == kShadeParams, "shading parameter layout");
 
 // ------------------------------------------------------------ tcgen05 --
-
 // Shared-memory matrix descriptor, no swizzle: start address, the byte offset
 // between core matrices along K (lbo) and along M/N (sbo) -- the same roles
 // for K-major and MN-major operands -- and descriptor version 1 (bit 46).
@@ -64,37 +63,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool mn_major = false) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (mn_major ? (3u << 15) : 0u) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* mbar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(mbar))
-        : "memory");
-}
-
-
-// 16 consecutive fp32 columns of this thread's TMEM lane (warp w owns lanes
-// 32w .. 32w + 31); the values are valid after tmem_wait_ld().
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // Store 16 / 32 consecutive 32-bit columns of this thread's TMEM lane; the
@@ -134,17 +102,6 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// generic-proxy shared-memory writes become visible to the tensor cores
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // The operands the threads wrote are complete, and every thread's earlier
 // tensor-memory reads are ordered before the MMAs issued next.
 __device__ __forceinline__ void operands_ready() {
@@ -152,16 +109,6 @@ __device__ __forceinline__ void operands_ready() {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-}
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* s_taddr, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(s_taddr)),
-                 "r"(cols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
 }
 
 // Byte offset of element (row, k) in a no-swizzle K-major operand with K
@@ -337,7 +284,7 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return
 __device__ __forceinline__ void mma_chain(uint32_t d, uint64_t a, uint64_t b, int steps,
                                           uint32_t idesc, uint32_t acc0) {
     for (int s = 0; s < steps; ++s)
-        mma_bf16(d, desc_at(a, 256u * s), desc_at(b, 256u * s), idesc, s > 0 ? 1u : acc0);
+        mma_f16(d, desc_at(a, 256u * s), desc_at(b, 256u * s), idesc, s > 0 ? 1u : acc0);
 }
 
 // ================================================================ weights --
@@ -723,7 +670,7 @@ k_shade_backward(Frames fs, Workspace w, const float* __restrict__ features,
         // ---- round 2: z2 = W2 Q(h1) + b2 (bias step over x's columns 16-31), and W3^T Q(dY)
         if (tid == 0) {
             mma_chain(tmem + kColZ2, desc_at(d_xh, 256), d_w2, kKB / 16, idesc_bf16(kRows, kHid), 0);
-            mma_bf16(tmem + kColG2, d_dy, d_w3t, idesc_bf16(kRows, kHid), 0);
+            mma_f16(tmem + kColG2, d_dy, d_w3t, idesc_bf16(kRows, kHid), 0);
             mma_commit(mbar);
         }
         ok = __syncthreads_and(mbar_wait(mbar, phase & 1));
@@ -740,9 +687,9 @@ k_shade_backward(Frames fs, Workspace w, const float* __restrict__ features,
                       idesc_bf16(kRows, kHid), 0);
             mma_commit(mbar);
             for (int q = 0; q < kRows; q += 16)
-                mma_bf16(tmem + kColAccY, desc_at(m_h2, (q / 8) * (kH2 / 8) * 128),
-                         desc_at(m_dy, (q / 8) * (kDY / 8) * 128), idesc_bf16(kRows, kDY, true),
-                         acc | (uint32_t)(q > 0));
+                mma_f16(tmem + kColAccY, desc_at(m_h2, (q / 8) * (kH2 / 8) * 128),
+                        desc_at(m_dy, (q / 8) * (kDY / 8) * 128), idesc_bf16(kRows, kDY, true),
+                        acc | (uint32_t)(q > 0));
         }
         ok = __syncthreads_and(mbar_wait(mbar, phase & 1));
         ++phase;
@@ -756,9 +703,9 @@ k_shade_backward(Frames fs, Workspace w, const float* __restrict__ features,
             mma_chain(tmem + kColDX, d_gg, d_w1t, kHid / 16, idesc_bf16(kRows, 16), 0);
             mma_commit(mbar);
             for (int q = 0; q < kRows; q += 16)
-                mma_bf16(tmem + kColAccXH, desc_at(m_gg, (q / 8) * (kGG / 8) * 128),
-                         desc_at(m_xh, (q / 8) * (kXH / 8) * 128), idesc_bf16(kRows, kXH, true),
-                         acc | (uint32_t)(q > 0));
+                mma_f16(tmem + kColAccXH, desc_at(m_gg, (q / 8) * (kGG / 8) * 128),
+                        desc_at(m_xh, (q / 8) * (kXH / 8) * 128), idesc_bf16(kRows, kXH, true),
+                        acc | (uint32_t)(q > 0));
             mma_commit(gbar);
         }
         acc = 1;
