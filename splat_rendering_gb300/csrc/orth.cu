@@ -45,7 +45,7 @@ __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, in
 // Sums of squares, a block per chunk of a matrix.  The second sum is of the
 // values times 2^-64, and is taken where the first overflows.
 constexpr float kDown = 5.421010862427522e-20f;   // 2^-64
-constexpr int kNormBlocks = 128;                  // at most, per matrix
+constexpr int kNormBlocks = 304;                  // at most, per matrix
 
 __device__ __forceinline__ float2 block_sum(float2 v) {
     __shared__ float2 s[kThreads / 32];
@@ -66,18 +66,22 @@ __device__ __forceinline__ float2 block_sum(float2 v) {
     return t;
 }
 
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
 k_orth_norm(const T* __restrict__ g, int64_t elems, float2* __restrict__ part) {
     pdl_begin();
     const T* m = g + (size_t)blockIdx.y * elems;
     float2 s = make_float2(0.0f, 0.0f);
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < elems;
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < elems / V;
          i += (int64_t)gridDim.x * kThreads) {
-        float v[1];
-        Pack<T, 1>::load(m + i, v);
-        s.x = fmaf(v[0], v[0], s.x);
-        s.y = fmaf(v[0] * kDown, v[0] * kDown, s.y);
+        float v[V];
+        Pack<T, V>::load(m + i * V, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s.x = fmaf(v[j], v[j], s.x);
+            s.y = fmaf(v[j] * kDown, v[j] * kDown, s.y);
+        }
     }
     s = block_sum(s);
     if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
@@ -114,9 +118,9 @@ __device__ __forceinline__ void halves(const float (&v)[8], uint4 (&h)[kParts]) 
 }
 
 // X_0 in panels, g [m, n] transposed where it is tall; the padding is zero.
-// A thread takes eight columns of a row; consecutive threads lie along what
-// is contiguous in g.
-template <typename T, int kParts>
+// A thread takes eight columns of a row (V at a time); consecutive threads
+// lie along what is contiguous in g.
+template <typename T, int kParts, int V>
 __global__ void __launch_bounds__(kThreads)
 k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t cp, bool tall,
              const float2* __restrict__ part, int parts, float eps, __half* __restrict__ x,
@@ -131,11 +135,12 @@ k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t 
         const int64_t row = tall ? i % rp : i / chunks, c0 = (tall ? i / rp : i % chunks) * 8;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float u[1] = {0.0f};
+        for (int j = 0; j < 8; j += V) {
+            float u[V] = {};
             if (row < r && c0 + j < c)
-                Pack<T, 1>::load(m + (tall ? (c0 + j) * r + row : row * c + c0 + j), u);
-            v[j] = u[0] * inv * kScaleX;
+                Pack<T, V>::load(m + (tall ? (c0 + j) * r + row : row * c + c0 + j), u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
         }
         uint4 h[kParts];
         halves<kParts>(v, h);
@@ -164,16 +169,26 @@ k_orth_scale(const T* __restrict__ g, int64_t elems, const float2* __restrict__ 
 // -------------------------------------------------------------- products --
 // One kernel for the three products, a persistent CTA per SM.  Roles: one
 // thread keeps a ring of operand stages filled with bulk copies, one issues
-// the MMAs into one of two accumulators in tensor memory, and four warps
-// drain the other: scale, round, and write the tile back in panels through
-// shared memory (bulk stores), or in the last step as the result.
+// the MMAs into one of two accumulators in tensor memory, and eight warps
+// drain the other (four per half of the tile's columns, a thread per row):
+// sum, scale, round, and store, into panels or, in the last step, as the
+// result.
+//
+// In 32 bits the tensor cores' accumulation, which truncates, would be what
+// limits the result: hi hi and the cross terms have accumulators of their
+// own, and both are drained and summed in registers every kChunk panels.
+//
+// Where a product has too few tiles for the SMs (the symmetric ones of a
+// small or oblong matrix), a cluster of kCluster CTAs shares a tile: each
+// takes a part of K, leaves its sums in shared memory, and finishes a part of
+// the columns from all of them, in the order of the CTAs.
 struct Product {
     const __half *l, *r;      // left and right operands, hi parts
     size_t l_lo, r_lo;        // halves from a hi part to its lo part
     size_t l_size, r_size;    // halves per matrix of the batch
     int64_t l_rows, r_rows;   // padded rows
     int k_panels;
-    int tiles_m, tiles_n;     // of the product (kGram: tiles_m^2 / 2 are computed)
+    int tiles_m;              // row blocks of the product
     int tiles;                // per matrix
     int batch;
     // D = alpha (accumulator) + beta C + gamma I, C and D in panels
@@ -189,20 +204,22 @@ struct Product {
     int dtype;
 };
 
-constexpr int kProductThreads = 192;   // warps: copies, MMAs, four of the epilogue
-constexpr int kEpilogue = 128;
-constexpr int kStaging = kBlock * kPanel * 2;   // one panel of a tile: 16 KB
+constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epilogue
+constexpr int kChunk = 4;              // panels of K per drained sum (32 bits)
+constexpr int kRowPitch = 33;          // words of a row of a warp's 32 x 32 exchange
 
 template <bool kSplit, int kN>
 struct ProductSmem {
     static constexpr int parts = kSplit ? 2 : 1;
     static constexpr int a = kBlock * kPanel * 2, b = kN * kPanel * 2;
     static constexpr int stage = parts * (a + b);
-    static constexpr int stages = (227 * 1024 - 1024 - 2 * kStaging - 256) / stage;
-    static constexpr int staging = stages * stage;
-    static constexpr int bars = staging + 2 * kStaging;
+    static constexpr int exchange_bytes = 8 * 32 * kRowPitch * 4;
+    static constexpr int stages = (227 * 1024 - 1024 - exchange_bytes - 256) / stage;
+    static constexpr int exchange = stages * stage;
+    static constexpr int bars = exchange + exchange_bytes;
     static constexpr int bytes = bars + 256 + 1024;   // and the alignment to 1024
     static_assert(stages >= 2 && (2 * stages + 5) * 8 + 8 <= 256, "shared memory of a product");
+    static_assert(stages * stage >= kBlock * kBlock * 4, "a tile of sums fits the stages");
 };
 
 // Descriptor of a 128-byte-swizzled operand: `lbo` is the stride between
@@ -226,34 +243,38 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
         "l"(src), "r"(bytes), "r"(smem_u32(mbar))
         : "memory");
 }
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(smem_u32(src)), "r"(bytes)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-template <int kLeft>
-__device__ __forceinline__ void bulk_store_read() {   // all but kLeft stores have been read
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
-}
-__device__ __forceinline__ void epilogue_sync() {
-    __syncwarp();
-    asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory");
-}
-// The same, and whether any thread has `v`: one decision for all.
+// Whether any of the epilogue's threads has `v`: one decision for all.
 __device__ __forceinline__ bool epilogue_any(bool v) {
     uint32_t any;
     __syncwarp();
     asm volatile(
-        "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred r, 1, %2, p;\n"
+        "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred r, 1, 256, p;\n"
         "selp.u32 %0, 1, 0, r;\n}\n"
         : "=r"(any)
-        : "r"((uint32_t)v), "n"(kEpilogue)
+        : "r"((uint32_t)v)
         : "memory");
     return any != 0;
 }
+__device__ __forceinline__ void mbar_init_n(uint64_t* mbar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(mbar)), "r"(n));
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // Tile t of a symmetric product, row blocks i >= j.
@@ -265,13 +286,29 @@ __device__ __forceinline__ void lower_tile(int t, int* i, int* j) {
     *j = t - row * (row + 1) / 2;
 }
 
-template <bool kSplit, int kN, bool kGram>
-__global__ void __launch_bounds__(kProductThreads)
+// C's halves of eight columns added to v.
+__device__ __forceinline__ void add_halves(float (&v)[8], const uint4& w, float beta) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+        v[2 * e] = fmaf(beta, f.x, v[2 * e]);
+        v[2 * e + 1] = fmaf(beta, f.y, v[2 * e + 1]);
+    }
+}
+
+template <bool kSplit, int kN, bool kGram, int kCluster>
+__global__ void __launch_bounds__(kProductThreads) __cluster_dims__(kCluster, 1, 1)
 k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     using L = ProductSmem<kSplit, kN>;
     constexpr int kParts = L::parts;
-    constexpr int kPanels = kN / kPanel;   // of a tile
+    constexpr int kPanels = kN / kPanel;          // of a tile
+    constexpr int kMine = kPanels / 2;            // panels of an epilogue thread
+    constexpr int kCols = kPanel / kCluster;      // columns of a panel it finishes
+    constexpr int kAcc = kSplit ? 2 * kN : kN;    // columns of an accumulator
     static_assert(!kGram || kN == kBlock, "symmetric products have square tiles");
+    static_assert(kCluster == 1 || kMine == 1, "a shared tile is one panel per thread");
+    static_assert(2 * kAcc <= 512, "tensor memory");
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
@@ -281,7 +318,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     uint64_t* drain = acc_empty + 2;
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* s_fail = s_taddr + 1;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < L::stages; ++s) {
             mbar_init(full + s);
@@ -289,19 +326,24 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s);
-            mbar_init(acc_empty + s);
+            mbar_init_n(acc_empty + s, 8);
         }
         mbar_init(drain);
         *s_fail = 0u;
         fence_async_smem();
     }
-    if (warp == 1) tmem_alloc(s_taddr, 2 * kN);
+    if (warp == 1) tmem_alloc(s_taddr, 2 * kAcc);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
     pdl_begin();
     const int total = q.tiles * q.batch;
+    const uint32_t rank = kCluster > 1 ? cluster_rank() : 0u;
+    const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
+    const int k0 = (int)(rank * (uint32_t)q.k_panels / kCluster);
+    const int k1 = (int)((rank + 1) * (uint32_t)q.k_panels / kCluster);
+    const int chunk = kSplit ? kChunk : k1 - k0;
     auto place = [&](int t, int* z, int* i, int* j) {
         *z = t / q.tiles;
         t -= *z * q.tiles;
@@ -312,19 +354,60 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
             *j = t / q.tiles_m;
         }
     };
+    bool met = false;   // this thread was at the cluster's first meeting: all sums are written
+    // ---- what an epilogue thread owns: a row of the tile, the columns of its panels
+    const int group = (warp - 2) >> 2, quarter = warp & 3;   // (epilogue warps are 2 .. 9)
+    const int row = quarter * 32 + lane;
+    // columns col .. col + kCols - 1 of the tile from their finished sums
+    auto finish = [&](int z, int i, int j, int col, const uint4 (&c)[kCols / 8][kParts],
+                      float (&v)[kCols]) {
+        const int64_t grow = (int64_t)i * kBlock + row, gcol = (int64_t)j * kN + col;
+        __half* d = q.d + z * q.d_size;
+        // col begins a run of kCols inside one panel: its row of 64 halves, and mirrored
+        // the run's rows in the panel of this thread's column (the warp's are adjacent)
+        __half* line = d + ((gcol / kPanel) * q.d_rows + grow) * kPanel;
+        __half* column = d + ((grow / kPanel) * q.d_rows + gcol) * kPanel + (row & 7);
+        const int chunk0 = (int)(gcol & (kPanel - 1)) >> 3, rchunk = (row & (kPanel - 1)) >> 3;
+        const int on = i == j ? row - col : -1;   // the diagonal's place among the columns
+#pragma unroll
+        for (int b = 0; b < kCols / 8; ++b) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = q.alpha * v[8 * b + e];
+            if (kGram && q.c) {
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) add_halves(w, c[b][p], q.beta);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] += 8 * b + e == on ? q.gamma : 0.0f;
+            }
+            uint4 h[kParts];
+            halves<kParts>(w, h);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                *reinterpret_cast<uint4*>(line + p * q.d_lo + (((chunk0 + b) ^ (row & 7)) << 3)) =
+                    h[p];
+                if (kGram && i != j) {
+                    const __half* e16 = reinterpret_cast<const __half*>(&h[p]);
+                    __half* m = column + p * q.d_lo + 8 * b * kPanel;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m[e * kPanel + ((rchunk ^ e) << 3)] = e16[e];
+                }
+            }
+        }
+    };
 
     if (warp == 0) {
-        if (tid == 0) {   // ---- copies
+        if (lane == 0) {   // ---- copies
             int n = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first; t < total && ok; t += step) {
                 int z, i, j;
                 place(t, &z, &i, &j);
                 const __half* l = q.l + z * q.l_size + (size_t)i * kBlock * kPanel;
                 const __half* r = q.r + z * q.r_size +
                                   (kGram ? (size_t)j * kN * kPanel
                                          : (size_t)j * kPanels * q.r_rows * kPanel);
-                for (int k = 0; k < q.k_panels; ++k, ++n) {
+                for (int k = k0; k < k1; ++k, ++n) {
                     const int s = n % L::stages;
                     ok = mbar_wait(empty + s, ((n / L::stages) & 1) ^ 1) && !*s_fail;
                     if (!ok) break;
@@ -358,45 +441,48 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
             }
         }
     } else if (warp == 1) {
-        if (tid == 32) {   // ---- MMAs
+        if (lane == 0) {   // ---- MMAs
             constexpr uint32_t idesc = (1u << 4) | (kGram ? 0u : 1u << 16) |
                                        ((uint32_t)(kN >> 3) << 17) |
                                        ((uint32_t)(kBlock >> 4) << 24);
             const uint32_t base = smem_u32(smem);
             int n = 0, it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
-                const int buf = it & 1;
-                const uint32_t d = tmem + buf * kN;
-                ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
-                if (!ok) break;
-                tc_fence_after();
-                for (int k = 0; k < q.k_panels; ++k, ++n) {
-                    const int s = n % L::stages;
-                    ok = mbar_wait(full + s, (n / L::stages) & 1) && !*s_fail;
+            for (int t = first; t < total && ok; t += step) {
+                for (int kc = k0; kc < k1 && ok; kc += chunk, ++it) {
+                    const int buf = it & 1, ke = min(kc + chunk, k1);
+                    const uint32_t d = tmem + buf * kAcc;
+                    ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = base + s * L::stage;
-                    uint64_t a[kParts], b[kParts];
+                    for (int k = kc; k < ke; ++k, ++n) {
+                        const int s = n % L::stages;
+                        ok = mbar_wait(full + s, (n / L::stages) & 1) && !*s_fail;
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t at = base + s * L::stage;
+                        uint64_t a[kParts], b[kParts];
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        a[p] = desc_sw128(at + p * L::a, 16);
-                        b[p] = desc_sw128(at + kParts * L::a + p * L::b,
-                                          kGram ? 16 : kPanel * kPanel * 2);
-                    }
-#pragma unroll
-                    for (int e = 0; e < kPanel / 16; ++e) {
-                        // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major operand
-                        const uint32_t ea = 32u * e >> 4, eb = kGram ? ea : (2048u * e >> 4);
-                        mma_f16(d, a[0] + ea, b[0] + eb, idesc, (k | e) != 0);
-                        if (kSplit) {
-                            mma_f16(d, a[0] + ea, b[kParts - 1] + eb, idesc, 1);
-                            mma_f16(d, a[kParts - 1] + ea, b[0] + eb, idesc, 1);
+                        for (int p = 0; p < kParts; ++p) {
+                            a[p] = desc_sw128(at + p * L::a, 16);
+                            b[p] = desc_sw128(at + kParts * L::a + p * L::b,
+                                              kGram ? 16 : kPanel * kPanel * 2);
                         }
+#pragma unroll
+                        for (int e = 0; e < kPanel / 16; ++e) {
+                            // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major operand
+                            const uint32_t ea = 32u * e >> 4, eb = kGram ? ea : (2048u * e >> 4);
+                            const uint32_t more = k > kc || e > 0;
+                            mma_f16(d, a[0] + ea, b[0] + eb, idesc, more);
+                            if (kSplit) {
+                                mma_f16(d + kN, a[0] + ea, b[kParts - 1] + eb, idesc, more);
+                                mma_f16(d + kN, a[kParts - 1] + ea, b[0] + eb, idesc, 1);
+                            }
+                        }
+                        mma_commit(empty + s);
                     }
-                    mma_commit(empty + s);
+                    if (ok) mma_commit(acc_full + buf);
                 }
-                if (ok) mma_commit(acc_full + buf);
             }
             if (!ok) {
                 *s_fail = 1u;
@@ -405,146 +491,153 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
             }
         }
     } else {   // ---- epilogue
-        const int quarter = warp & 3, lane = tid & 31;
-        const int row = quarter * 32 + lane;   // of the tile: its lane in tensor memory
-        const bool lead = tid == 64;
-        unsigned char* stage = smem + L::staging;
         int it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-            const int buf = it & 1;
+        for (int t = first; t < total; t += step) {   // (once, where a cluster shares the tile)
             int z, i, j;
             place(t, &z, &i, &j);
-            const bool ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
-            if (epilogue_any(!ok)) {
+            uint4 c[kCols / 8][kParts];   // C of the columns this thread finishes, loaded early
+            if (kGram && q.c) {
+                const __half* cz = q.c + z * q.d_size;
+#pragma unroll
+                for (int b = 0; b < kCols / 8; ++b)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+                        c[b][p] = *reinterpret_cast<const uint4*>(
+                            cz + p * q.d_lo +
+                            panel_at((int64_t)i * kBlock + row,
+                                     (int64_t)j * kN + group * kPanel + rank * kCols + 8 * b,
+                                     q.d_rows));
+            }
+            float v[kPanel];
+            bool ok = true;
+            if (kSplit) {
+#pragma unroll
+                for (int e = 0; e < kPanel; ++e) v[e] = 0.0f;
+                for (int kc = k0; kc < k1; kc += chunk, ++it) {
+                    const int buf = it & 1;
+                    ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
+                    ok = !epilogue_any(!ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * kAcc + ((uint32_t)(quarter * 32) << 16) +
+                                         group * kPanel;
+#pragma unroll
+                    for (int h = 0; h < kPanel; h += 16) {
+                        uint32_t u[16], w[16];
+                        tmem_ld16(acc + h, u);
+                        tmem_ld16(acc + kN + h, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[h + e] += __uint_as_float(u[e]) + __uint_as_float(w[e]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                }
+            } else {
+                ok = mbar_wait(acc_full + (it & 1), (it >> 1) & 1) && !*s_fail;
+                ok = !epilogue_any(!ok);
+                tc_fence_after();
+            }
+            if (!ok) {
                 *s_fail = 1u;
                 break;
             }
-            tc_fence_after();
-            const uint32_t acc = tmem + buf * kN + ((uint32_t)(quarter * 32) << 16);
-            const int64_t grow = (int64_t)i * kBlock + row;
-            // 32 columns of this row of D
-            auto values = [&](int col, float (&v)[32]) {
-                uint32_t u[32];
-                __syncwarp();
-                tmem_ld32(acc + col, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = q.alpha * __uint_as_float(u[e]);
-                if (q.c) {
-                    const __half* c = q.c + z * q.d_size;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int64_t gcol = (int64_t)j * kN + col + 8 * h;
-                        const size_t at = panel_at(grow, gcol, q.d_rows);
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(c + p * q.d_lo + at);
-                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f =
-                                    __half22float2(*reinterpret_cast<const __half2*>(&ws[e]));
-                                v[8 * h + 2 * e] = fmaf(q.beta, f.x, v[8 * h + 2 * e]);
-                                v[8 * h + 2 * e + 1] = fmaf(q.beta, f.y, v[8 * h + 2 * e + 1]);
-                            }
-                        }
-                    }
-                    const int64_t on = grow - ((int64_t)j * kN + col);   // the diagonal
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] += e == on ? q.gamma : 0.0f;
-                }
-            };
-            if (q.out) {
-                for (int col = 0; col < kN; col += 32) {
-                    float v[32];
-                    values(col, v);
-                    const int64_t gcol = (int64_t)j * kN + col;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (grow >= q.out_r || gcol + e >= q.out_c) continue;
-                        const size_t at = (size_t)z * q.out_r * q.out_c +
-                                          (q.tall ? (gcol + e) * q.out_r + grow
-                                                  : grow * q.out_c + gcol + e);
-                        if (q.dtype == kF32)
-                            static_cast<float*>(q.out)[at] = v[e];
-                        else
-                            static_cast<__nv_bfloat16*>(q.out)[at] = __float2bfloat16_rn(v[e]);
-                    }
-                }
-            } else {
-                __half* d = q.d + z * q.d_size;
-                for (int c = 0; c < kPanels; ++c) {
-                    uint4 h[8][kParts];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float v[32];
-                        values(c * kPanel + 32 * half, v);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float w[8];
-#pragma unroll
-                            for (int b = 0; b < 8; ++b) w[b] = v[8 * e + b];
-                            halves<kParts>(w, h[4 * half + e]);
-                        }
-                    }
-                    __half* dst = d + ((size_t)(j * kPanels + c) * q.d_rows + (size_t)i * kBlock) *
-                                          kPanel;
-#pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        unsigned char* b = stage + ((c * kParts + p) & 1) * kStaging;
-                        if (lead) bulk_store_read<1>();
-                        epilogue_sync();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(b + row * 128 + ((e ^ (row & 7)) << 4)) =
-                                h[e][p];
-                        fence_async_smem();
-                        epilogue_sync();
-                        if (lead) bulk_store(dst + p * q.d_lo, b, kStaging);
-                    }
-                }
-                if (kGram && i != j) {   // the mirrored tile: its panels are halves of our rows
 #pragma unroll 1
-                    for (int p = 0; p < kParts; ++p) {
-                        if (lead) bulk_store_read<0>();
-                        epilogue_sync();
-                        unsigned char* b = stage + (row >> 6) * kStaging + (row & 7) * 2;
-                        const int chunk = (row & 63) >> 3;
-                        for (int col = 0; col < kN; col += 32) {
-                            float v[32];
-                            values(col, v);
+            for (int m = 0; m < kMine; ++m) {
+                const int col = (group * kMine + m) * kPanel;
+                if (!kSplit) {
+                    const uint32_t acc = tmem + (it & 1) * kAcc +
+                                         ((uint32_t)(quarter * 32) << 16) + col;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                __half h = __float2half_rn(v[e]);
-                                if (p == 1) h = __float2half_rn(v[e] - __half2float(h));
-                                *reinterpret_cast<__half*>(b + (col + e) * 128 +
-                                                           ((chunk ^ (e & 7)) << 4)) = h;
-                            }
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t u[32];
+                        __syncwarp();
+                        tmem_ld32(acc + 32 * h, u);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[32 * h + e] = __uint_as_float(u[e]);
+                    }
+                    if (m + 1 == kMine) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(acc_empty + (it & 1));
+                        ++it;
+                    }
+                }
+                if (kCluster > 1) {   // the stages are free: every MMA of this CTA is complete
+                    float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+                    for (int e = 0; e < kPanel; ++e) sums[(col + e) * kBlock + row] = v[e];
+                } else if (kGram || !q.out) {
+                    float w[kCols];
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) w[e] = v[e % kPanel];
+                    finish(z, i, j, col, c, w);
+                } else {   // the result: through a 32 x 32 exchange of the warp, row by row
+                    float* x = reinterpret_cast<float*>(smem + L::exchange) +
+                               (warp - 2) * 32 * kRowPitch;
+                    const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
+                    const size_t base = (size_t)z * q.out_r * q.out_c;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int64_t c0 = (int64_t)j * kN + col + 32 * h;
+                        if (!q.tall) {
+                            __syncwarp();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[lane * kRowPitch + e] = v[32 * h + e];
+                            __syncwarp();
                         }
-                        fence_async_smem();
-                        epilogue_sync();
-                        if (lead) {
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                bulk_store(d + p * q.d_lo + ((size_t)(2 * i + c) * q.d_rows +
-                                                             (size_t)j * kBlock) * kPanel,
-                                           stage + c * kStaging, kStaging);
+                        for (int e = 0; e < 32; ++e) {
+                            // e: a row of the exchange, or (tall) a column of the tile
+                            const int64_t orow = q.tall ? r0 + lane : r0 + e;
+                            const int64_t ocol = q.tall ? c0 + e : c0 + lane;
+                            const float y = q.alpha * (q.tall ? v[32 * h + e]
+                                                              : x[e * kRowPitch + lane]);
+                            if (orow < q.out_r && ocol < q.out_c) {
+                                const size_t at = base + (q.tall ? ocol * q.out_r + orow
+                                                                 : orow * q.out_c + ocol);
+                                if (q.dtype == kF32)
+                                    static_cast<float*>(q.out)[at] = y;
+                                else
+                                    static_cast<__nv_bfloat16*>(q.out)[at] = __float2bfloat16_rn(y);
+                            }
                         }
                     }
                 }
             }
-            tc_fence_before();
-            epilogue_sync();
-            if (lead) mbar_arrive(acc_empty + buf);
+            if (kCluster > 1) {
+                __syncwarp();
+                cluster_sync();
+                met = true;
+                float w[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) w[e] = 0.0f;
+                const int col = group * kPanel + (int)rank * kCols;
+                const uint32_t at = smem_u32(smem) + (uint32_t)((col * kBlock + row) * 4);
+#pragma unroll
+                for (int s = 0; s < kCluster; ++s)
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        w[e] += ld_cluster(at + e * kBlock * 4, s);
+                finish(z, i, j, col, c, w);
+            }
         }
-        if (lead) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
+    // the other CTAs of the cluster still read this one's sums
+    if (kCluster > 1) {
+        if (!met) cluster_sync();
+        __syncwarp();
+        cluster_sync();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (tid == 0 && *s_fail) atomicOr(&st->error, kErrTimeout);
-    if (warp == 1) tmem_dealloc(tmem, 2 * kN);
+    if (warp == 1) tmem_dealloc(tmem, 2 * kAcc);
 }
 
 // ----------------------------------------------------------------- plans --
@@ -581,12 +674,24 @@ Space carve(Carve& w, int64_t batch, const Plan& p) {
     return s;
 }
 
-template <bool kSplit, int kN, bool kGram>
+template <bool kSplit, int kN, bool kGram, int kCluster = 1>
 cudaError_t product(const Product& q, LearnState* st, int n_sms, cudaStream_t s) {
+    const int64_t total = (int64_t)q.tiles * q.batch * kCluster;
+    return launch_pdl(k_orth_product<kSplit, kN, kGram, kCluster>,
+                      dim3((unsigned)(total < n_sms || kCluster > 1 ? total : n_sms)),
+                      dim3(kProductThreads), ProductSmem<kSplit, kN>::bytes, s, q, st);
+}
+
+// A symmetric product: as many CTAs share a tile as there are SMs (and panels)
+// for; clusters do not fill every SM of a GPC, hence seven eighths of them.
+template <bool kSplit>
+cudaError_t symmetric(const Product& q, LearnState* st, int n_sms, cudaStream_t s) {
     const int64_t total = (int64_t)q.tiles * q.batch;
-    return launch_pdl(k_orth_product<kSplit, kN, kGram>,
-                      dim3((unsigned)(total < n_sms ? total : n_sms)), dim3(kProductThreads),
-                      ProductSmem<kSplit, kN>::bytes, s, q, st);
+    const auto fits = [&](int n) { return total * n * 8 <= n_sms * 7 && q.k_panels >= n; };
+    if (fits(8)) return product<kSplit, kBlock, true, 8>(q, st, n_sms, s);
+    if (fits(4)) return product<kSplit, kBlock, true, 4>(q, st, n_sms, s);
+    if (fits(2)) return product<kSplit, kBlock, true, 2>(q, st, n_sms, s);
+    return product<kSplit, kBlock, true>(q, st, n_sms, s);
 }
 
 template <typename T, bool kSplit>
@@ -603,15 +708,20 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         const int64_t b = ceil_div(items, kThreads);
         return dim3((unsigned)(b < 2048 ? b : 2048), B);
     };
-    cudaError_t e = launch_pdl(k_orth_norm<T>, dim3(parts, B), dim3(kThreads), 0, s,
-                               (const T*)o.grad, elems, w.part);
+    constexpr int V = VecOf<T>::n;
+    const bool vec = aligned16(o.grad) && elems % V == 0;   // every matrix of the batch
+    cudaError_t e = vec ? launch_pdl(k_orth_norm<T, V>, dim3(parts, B), dim3(kThreads), 0, s,
+                                     (const T*)o.grad, elems, w.part)
+                        : launch_pdl(k_orth_norm<T, 1>, dim3(parts, B), dim3(kThreads), 0, s,
+                                     (const T*)o.grad, elems, w.part);
     if (e != cudaSuccess) return e;
     if (o.steps == 0)
         return launch_pdl(k_orth_scale<T>, flat(elems), dim3(kThreads), 0, s, (const T*)o.grad,
                           elems, (const float2*)w.part, parts, o.eps, (T*)o.out);
-    e = launch_pdl(k_orth_start<T, kParts>, flat(p.rp * p.cp / 8), dim3(kThreads), 0, s,
-                   (const T*)o.grad, p.r, p.c, p.rp, p.cp, p.tall, (const float2*)w.part, parts,
-                   o.eps, w.x[0], w.x_lo);
+    const auto start = !p.tall && vec && p.c % V == 0 ? k_orth_start<T, kParts, V>
+                                                      : k_orth_start<T, kParts, 1>;
+    e = launch_pdl(start, flat(p.rp * p.cp / 8), dim3(kThreads), 0, s, (const T*)o.grad, p.r, p.c,
+                   p.rp, p.cp, p.tall, (const float2*)w.part, parts, o.eps, w.x[0], w.x_lo);
     const int tm = (int)(p.rp / kBlock);
     for (int k = 0; k < o.steps && e == cudaSuccess; ++k) {
         const __half* x = w.x[k & 1];
@@ -621,7 +731,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         g.l_size = g.r_size = (size_t)p.rp * p.cp;
         g.l_rows = g.r_rows = p.rp;
         g.k_panels = (int)(p.cp / kPanel);
-        g.tiles_m = g.tiles_n = tm;
+        g.tiles_m = tm;
         g.tiles = tm * (tm + 1) / 2;
         g.batch = (int)o.batch;
         g.d = w.a;
@@ -629,7 +739,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         g.d_size = (size_t)p.rp * p.rp;
         g.d_rows = p.rp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
-        e = product<kSplit, kBlock, true>(g, st, n_sms, s);
+        e = symmetric<kSplit>(g, st, n_sms, s);
         if (e != cudaSuccess) return e;
         Product h = g;   // P = a I + b A + c A A
         h.l = h.r = h.c = w.a;
@@ -640,7 +750,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         h.alpha = o.c * (kScaleP / (kScaleA * kScaleA));
         h.beta = o.b * (kScaleP / kScaleA);
         h.gamma = o.a * kScaleP;
-        e = product<kSplit, kBlock, true>(h, st, n_sms, s);
+        e = symmetric<kSplit>(h, st, n_sms, s);
         if (e != cudaSuccess) return e;
         Product f = g;   // X' = P X
         f.l = w.p;
@@ -662,8 +772,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         // 256 columns a tile move fewer operand bytes per product; 128 give twice the tiles
         const bool wide = !kSplit && p.cp % 256 == 0 &&
                           (int64_t)tm * (p.cp / 256) * o.batch >= n_sms;
-        f.tiles_n = (int)(p.cp / (wide ? 256 : 128));
-        f.tiles = tm * f.tiles_n;
+        f.tiles = tm * (int)(p.cp / (wide ? 256 : 128));
         if (wide)
             e = product<kSplit, kSplit ? 128 : 256, false>(f, st, n_sms, s);
         else
@@ -672,11 +781,20 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
     return e;
 }
 
-template <bool kSplit, int kN, bool kGram>
+template <bool kSplit, int kN, bool kGram, int kCluster = 1>
 cudaError_t prepare_one() {
-    return cudaFuncSetAttribute(k_orth_product<kSplit, kN, kGram>,
+    return cudaFuncSetAttribute(k_orth_product<kSplit, kN, kGram, kCluster>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 ProductSmem<kSplit, kN>::bytes);
+}
+template <bool kSplit>
+cudaError_t prepare_type() {
+    cudaError_t e = prepare_one<kSplit, 128, true>();
+    if (e == cudaSuccess) e = prepare_one<kSplit, 128, true, 2>();
+    if (e == cudaSuccess) e = prepare_one<kSplit, 128, true, 4>();
+    if (e == cudaSuccess) e = prepare_one<kSplit, 128, true, 8>();
+    if (e == cudaSuccess) e = prepare_one<kSplit, 128, false>();
+    return e;
 }
 
 }  // namespace
@@ -689,11 +807,9 @@ size_t orth_workspace(int64_t batch, int64_t m, int64_t n, int dtype) {
 }
 
 cudaError_t prepare_orth() {
-    cudaError_t e = prepare_one<false, 128, true>();
-    if (e == cudaSuccess) e = prepare_one<false, 128, false>();
+    cudaError_t e = prepare_type<false>();
+    if (e == cudaSuccess) e = prepare_type<true>();
     if (e == cudaSuccess) e = prepare_one<false, 256, false>();
-    if (e == cudaSuccess) e = prepare_one<true, 128, true>();
-    if (e == cudaSuccess) e = prepare_one<true, 128, false>();
     return e;
 }
 
