@@ -27,6 +27,13 @@
 namespace pulsar {
 namespace {
 
+// The calls' launches form a chain in which each needs all of the one before:
+// a kernel lets the next one's blocks take free SMs and set up at once, and
+// that waits in pdl_begin() for this one's results.
+__device__ __forceinline__ void pdl_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 constexpr int kThreads = 256;
 constexpr int kPanel = 64;      // columns of a panel: 128 bytes of halves
 constexpr int kBlock = 128;     // rows are padded to it
@@ -87,16 +94,20 @@ k_orth_norm(const T* __restrict__ g, int64_t elems, float2* __restrict__ part) {
     if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// 1 / (|G|_F + eps) from a matrix's parts (every thread of the block calls).
+// 1 / (|G|_F + eps) from the sums
+__device__ __forceinline__ float norm_inverse(float2 s, float eps) {
+    const float norm = isinf(s.x) ? sqrtf(s.y) * 18446744073709551616.0f : sqrtf(s.x);
+    return 1.0f / (norm + eps);
+}
+
+// The same from a matrix's parts (every thread of the block calls).
 __device__ __forceinline__ float inv_norm(const float2* part, int blocks, float eps) {
     float2 s = make_float2(0.0f, 0.0f);
     for (int i = threadIdx.x; i < blocks; i += kThreads) {
         s.x += part[i].x;
         s.y += part[i].y;
     }
-    s = block_sum(s);
-    const float norm = isinf(s.x) ? sqrtf(s.y) * 18446744073709551616.0f : sqrtf(s.x);
-    return 1.0f / (norm + eps);
+    return norm_inverse(block_sum(s), eps);
 }
 
 // Eight values as halves, and what their rounding left (kParts 2).
@@ -269,11 +280,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
     uint32_t at;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
@@ -337,6 +351,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
+    pdl_next();
     pdl_begin();
     const int total = q.tiles * q.batch;
     const uint32_t rank = kCluster > 1 ? cluster_rank() : 0u;
@@ -567,9 +582,11 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                     }
                 }
                 if (kCluster > 1) {   // the stages are free: every MMA of this CTA is complete
-                    float* sums = reinterpret_cast<float*>(smem);
+                    float4* sums = reinterpret_cast<float4*>(smem);   // [column / 4][row]
 #pragma unroll
-                    for (int e = 0; e < kPanel; ++e) sums[(col + e) * kBlock + row] = v[e];
+                    for (int e = 0; e < kPanel; e += 4)
+                        sums[(col + e) / 4 * kBlock + row] =
+                            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                 } else if (kGram || !q.out) {
                     float w[kCols];
 #pragma unroll
@@ -616,12 +633,17 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) w[e] = 0.0f;
                 const int col = group * kPanel + (int)rank * kCols;
-                const uint32_t at = smem_u32(smem) + (uint32_t)((col * kBlock + row) * 4);
+                const uint32_t at = smem_u32(smem) + (uint32_t)((col / 4 * kBlock + row) * 16);
 #pragma unroll
                 for (int s = 0; s < kCluster; ++s)
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e)
-                        w[e] += ld_cluster(at + e * kBlock * 4, s);
+                    for (int e = 0; e < kCols; e += 4) {
+                        const float4 u = ld_cluster(at + e / 4 * kBlock * 16, s);
+                        w[e] += u.x;
+                        w[e + 1] += u.y;
+                        w[e + 2] += u.z;
+                        w[e + 3] += u.w;
+                    }
                 finish(z, i, j, col, c, w);
             }
         }
@@ -640,11 +662,269 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     if (warp == 1) tmem_dealloc(tmem, 2 * kAcc);
 }
 
+// ----------------------------------------------------------- small matrices --
+// A matrix whose X and A fit one SM's shared memory: one CTA takes it through
+// all steps in one launch, X, A and P never leaving the SM (P overwrites A,
+// X' overwrites X: a product is complete before its epilogue writes, and an
+// epilogue thread reads no row but its own).  Panels hold rn rows; an MMA's
+// 128 rows reach past them into what follows, which only makes rows of the
+// product that nobody reads.  Eight warps share an epilogue: a thread has a
+// row and half of the columns.
+struct Small {
+    int r, c, rn, cn;      // rn, cn: padded to 16
+    int xp, ap;            // panels of X and of A
+    bool tall;
+    int steps;
+    float a, b, c2, eps;
+};
+constexpr int kSmallChunk = 256;   // K of a sum in tensor memory (as kChunk)
+
+template <bool kSplit>
+size_t small_bytes(int rn, int xp, int ap) {
+    return (size_t)(kSplit ? 2 : 1) * (xp + ap) * rn * 128 + (kBlock - 16) * 128 + 64 + 1024;
+}
+
+template <typename T, bool kSplit>
+__global__ void __launch_bounds__(kThreads)
+k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out, LearnState* st) {
+    constexpr int kParts = kSplit ? 2 : 1;
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t pb = (uint32_t)q.rn * 128u;                 // bytes of a panel
+    const uint32_t x_part = q.xp * pb, a_part = q.ap * pb;     // from hi to lo
+    unsigned char* xs = smem;
+    unsigned char* as = smem + kParts * x_part;
+    uint64_t* mbar = reinterpret_cast<uint64_t*>(as + kParts * a_part + (kBlock - 16) * 128);
+    uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quarter = warp & 3, half = warp >> 2;
+    const int row = quarter * 32 + lane;
+    if (tid == 0) {
+        mbar_init(mbar);
+        mbar_init(mbar + 1);
+        fence_async_smem();
+    }
+    if (warp == 0) tmem_alloc(s_taddr, 512);
+    pdl_begin();
+    const size_t elems = (size_t)q.r * q.c;
+    const T* g = grad + blockIdx.x * elems;
+    float2 sq = make_float2(0.0f, 0.0f);
+    for (int i = tid; i < (int)elems; i += kThreads) {
+        float v[1];
+        Pack<T, 1>::load(g + i, v);
+        sq.x = fmaf(v[0], v[0], sq.x);
+        sq.y = fmaf(v[0] * kDown, v[0] * kDown, sq.y);
+    }
+    const float inv = norm_inverse(block_sum(sq), q.eps);
+    for (int i = tid; i < q.rn * q.xp * 8; i += kThreads) {
+        const int xr = q.tall ? i % q.rn : i / (q.xp * 8);
+        const int c0 = (q.tall ? i / q.rn : i % (q.xp * 8)) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float u[1] = {0.0f};
+            if (xr < q.r && c0 + j < q.c)
+                Pack<T, 1>::load(g + (q.tall ? (c0 + j) * q.r + xr : xr * q.c + c0 + j), u);
+            v[j] = u[0] * inv * kScaleX;
+        }
+        uint4 h[kParts];
+        halves<kParts>(v, h);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+            *reinterpret_cast<uint4*>(xs + p * x_part + panel_at(xr, c0, q.rn) * 2) = h[p];
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_taddr;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t x0 = smem_u32(xs), a0 = smem_u32(as);
+    const bool busy = quarter * 32 < q.rn;   // this warp has rows
+    uint32_t ph[2] = {0u, 0u};
+    bool ok = true;
+    // D (columns d, cross terms at d + 256) = the rows at l times the operand at r, K = 16 ks
+    auto issue = [&](int buf, uint32_t d, uint32_t l, uint32_t l_part, uint32_t r, uint32_t r_part,
+                     int n, int k_begin, int k_end, bool mn) {
+        const uint32_t idesc = (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+                               ((uint32_t)(kBlock >> 4) << 24);
+        for (int k = k_begin; k < k_end; ++k) {
+            const uint32_t ka = (uint32_t)(k >> 2) * pb + (uint32_t)(k & 3) * 32u;
+            const uint32_t kb = mn ? (uint32_t)k * 2048u : ka;
+            const uint64_t dl = desc_sw128(l + ka, 16), dr = desc_sw128(r + kb, mn ? pb : 16);
+            const uint32_t more = k > k_begin;
+            mma_f16(tmem + d, dl, dr, idesc, more);
+            if (kSplit) {
+                mma_f16(tmem + d + 256, dl, desc_sw128(r + r_part + kb, mn ? pb : 16), idesc, more);
+                mma_f16(tmem + d + 256, desc_sw128(l + l_part + ka, 16), dr, idesc, 1);
+            }
+        }
+        mma_commit(mbar + buf);
+    };
+    auto await = [&](int buf) {   // one decision for all
+        ok = __syncthreads_and(mbar_wait(mbar + buf, ph[buf] & 1));
+        ++ph[buf];
+        tc_fence_after();
+        return ok;
+    };
+    // sixteen columns of this row of D
+    auto sums = [&](uint32_t d, float (&v)[16]) {
+        uint32_t u[16], w[16];
+        __syncwarp();
+        tmem_ld16(trow + d, u);
+        if (kSplit) tmem_ld16(trow + d + 256, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            v[e] = kSplit ? __uint_as_float(u[e]) + __uint_as_float(w[e]) : __uint_as_float(u[e]);
+    };
+    auto put = [&](unsigned char* m, uint32_t part, int col, const float (&v)[16]) {
+        if (row >= q.rn) return;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = v[8 * b + e];
+            uint4 h[kParts];
+            halves<kParts>(w, h);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+                *reinterpret_cast<uint4*>(m + p * part + panel_at(row, col + 8 * b, q.rn) * 2) = h[p];
+        }
+    };
+    auto ready = [&]() {   // what the threads wrote is ready for the next product
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    const int r_units = q.rn / 16, r_mine = (r_units + 1 - half) / 2;   // units half, half + 2, ..
+    for (int step = 0; step < q.steps && ok; ++step) {
+        // ---- A = X X^T, in chunks of K through two accumulators
+        {
+            float acc[4][16];
+            const int ks = q.cn / 16, per = kSmallChunk / 16, chunks = (ks + per - 1) / per;
+            if (tid == 0) issue(0, 0, x0, x_part, x0, x_part, q.rn, 0, min(per, ks), false);
+            for (int ch = 0; ch < chunks; ++ch) {
+                if (tid == 0 && ch + 1 < chunks)
+                    issue((ch + 1) & 1, 128 * ((ch + 1) & 1), x0, x_part, x0, x_part, q.rn,
+                          (ch + 1) * per, min((ch + 2) * per, ks), false);
+                if (!await(ch & 1)) break;
+                if (busy) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        if (m < r_mine) {
+                            float v[16];
+                            sums(128 * (ch & 1) + 16 * (half + 2 * m), v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) acc[m][e] = ch ? acc[m][e] + v[e] : v[e];
+                        }
+                    }
+                }
+                tc_fence_before();
+                if (ch + 2 < chunks) __syncthreads();   // its accumulator is refilled next
+                tc_fence_after();
+            }
+            if (!ok) break;
+            if (busy) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    if (m < r_mine) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
+                        put(as, a_part, 16 * (half + 2 * m), acc[m]);
+                    }
+                }
+            }
+        }
+        ready();
+        // ---- P = a I + b A + c A A
+        if (tid == 0) issue(0, 0, a0, a_part, a0, a_part, q.rn, 0, r_units, false);
+        if (!await(0)) break;
+        if (busy) {
+            for (int m = 0; m < r_mine; ++m) {
+                const int col = 16 * (half + 2 * m);
+                float v[16];
+                sums(col, v);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    v[e] *= q.c2 * (kScaleP / (kScaleA * kScaleA));
+                    if (col + e == row) v[e] += q.a * kScaleP;
+                }
+                if (row < q.rn) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) {
+                            float w[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = v[8 * b + e];
+                            add_halves(w, *reinterpret_cast<const uint4*>(
+                                              as + p * a_part + panel_at(row, col + 8 * b, q.rn) * 2),
+                                       q.b * (kScaleP / kScaleA));
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[8 * b + e] = w[e];
+                        }
+                }
+                put(as, a_part, col, v);
+            }
+        }
+        ready();
+        // ---- X' = P X, 256 columns at a time; the last one is the result
+        for (int c0 = 0; c0 < q.cn; c0 += 256) {
+            const int n = min(256, q.cn - c0);
+            if (tid == 0)
+                issue(0, 0, a0, a_part, x0 + (uint32_t)(c0 / kPanel) * pb, x_part, n, 0, r_units,
+                      true);
+            if (!await(0)) break;
+            if (busy) {
+                for (int u = half; u < n / 16; u += 2) {
+                    float v[16];
+                    sums(16 * u, v);
+                    const int col = c0 + 16 * u;
+                    if (step + 1 < q.steps) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleP;
+                        put(xs, x_part, col, v);
+                    } else if (row < q.r) {
+                        T* o = out + blockIdx.x * elems;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float y[1] = {v[e] * (1.0f / (kScaleP * kScaleX))};
+                            if (col + e < q.c)
+                                Pack<T, 1>::store(o + (q.tall ? (col + e) * q.r + row
+                                                              : row * q.c + col + e), y);
+                        }
+                    }
+                }
+            }
+            ready();
+        }
+    }
+    if (!ok) {
+        // an MMA did not complete in time: report it, give what was awaited and
+        // what may still be in flight one more bounded wait each, then release
+        // the tensor memory
+        if (tid == 0) atomicOr(&st->error, kErrTimeout);
+        for (int k = 0; k < 2; ++k) {
+            mbar_wait(mbar + k, (ph[k] - 1) & 1);
+            mbar_wait(mbar + k, ph[k] & 1);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 // ----------------------------------------------------------------- plans --
+constexpr size_t kSmemMax = 227 * 1024 - 128;   // (the norm has a little of its own)
+
 struct Plan {
     int64_t r, c, rp, cp;   // padded
     bool tall;
     int parts;
+    bool small;             // one CTA takes a matrix through all steps
 };
 Plan plan_of(int64_t m, int64_t n, int dtype) {
     Plan p;
@@ -655,6 +935,10 @@ Plan plan_of(int64_t m, int64_t n, int dtype) {
     const int64_t to = p.c > 1024 ? 256 : 128;   // two widths of a tile of the last product
     p.cp = ceil_div(p.c, to) * to;
     p.parts = dtype == kF32 ? 2 : 1;
+    const int rn = (int)ceil_div(p.r, 16) * 16, xp = (int)ceil_div(p.c, kPanel),
+              ap = (int)ceil_div(p.r, kPanel);
+    p.small = rn <= kBlock && (dtype == kF32 ? small_bytes<true>(rn, xp, ap)
+                                             : small_bytes<false>(rn, xp, ap)) <= kSmemMax;
     return p;
 }
 
@@ -698,6 +982,14 @@ template <typename T, bool kSplit>
 cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
     constexpr int kParts = kSplit ? 2 : 1;
     const Plan p = plan_of(o.m, o.n, o.dtype);
+    if (o.steps > 0 && p.small) {
+        const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16, (int)ceil_div(p.c, 16) * 16,
+                      (int)ceil_div(p.c, kPanel), (int)ceil_div(p.r, kPanel), p.tall, o.steps,
+                      o.a, o.b, o.c, o.eps};
+        return launch_pdl(k_orth_small<T, kSplit>, dim3((unsigned)o.batch), dim3(kThreads),
+                          small_bytes<kSplit>(q.rn, q.xp, q.ap), s, (const T*)o.grad, q, (T*)o.out,
+                          st);
+    }
     Carve cv{static_cast<unsigned char*>(ws)};
     const Space w = carve(cv, o.batch, p);
     const unsigned B = (unsigned)o.batch;
@@ -810,6 +1102,12 @@ cudaError_t prepare_orth() {
     cudaError_t e = prepare_type<false>();
     if (e == cudaSuccess) e = prepare_type<true>();
     if (e == cudaSuccess) e = prepare_one<false, 256, false>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_orth_small<float, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_orth_small<__nv_bfloat16, false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     return e;
 }
 
