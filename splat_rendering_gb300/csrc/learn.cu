@@ -22,6 +22,7 @@ struct pulsar_learn {
 namespace {
 
 constexpr int64_t kMaxIndex = 0x7fff0000LL;   // positions and rows are 32-bit on the device
+constexpr int kMaxSms = 160;                  // of an sm_103a part (launches size workspace by it)
 constexpr int64_t kMaxDim = 65536;
 constexpr int64_t kMaxSide = 65536;           // of a matrix
 constexpr int64_t kMaxBatch = 65535;          // a launch's grid
@@ -78,7 +79,8 @@ int pulsar_learn_create(pulsar_learn_t* out, int device, int64_t workspace_bytes
     if (ok)
         ok = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, device) ==
                  cudaSuccess &&
-             prepare_orth() == cudaSuccess &&
+             h->n_sms <= kMaxSms && prepare_orth() == cudaSuccess &&
+             prepare_group_norm() == cudaSuccess &&
              cudaMemset(h->state, 0, sizeof(LearnState)) == cudaSuccess &&
              cudaDeviceSynchronize() == cudaSuccess;
     if (!ok) {

@@ -22,6 +22,13 @@ enum ElemType { kF32 = 0, kBf16 = 1 };
 enum IndexType { kI32 = 0, kI64 = 1 };
 enum Activation { kActNone = 0, kActSilu = 1, kActRelu = 2 };
 
+// The launches of a call form a chain in which each needs all of the one
+// before: a kernel of long-lived blocks lets the next one's blocks take SMs
+// as they fall free and set up, and those wait in pdl_begin() for its results.
+__device__ __forceinline__ void pdl_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Piece by piece carve-up of the workspace, every piece 256-byte aligned; run
 // over a null base it counts the bytes a call needs.
 struct Carve {
@@ -41,6 +48,13 @@ template <typename T, int V>
 struct Pack;
 template <>
 struct Pack<float, 4> {
+    using Raw = float4;   // as it was loaded
+    static __device__ __forceinline__ Raw raw(const float* p) {
+        return *reinterpret_cast<const float4*>(p);
+    }
+    static __device__ __forceinline__ void open(const Raw& u, float (&v)[4]) {
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    }
     static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
         const float4 u = *reinterpret_cast<const float4*>(p);
         v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
@@ -48,11 +62,33 @@ struct Pack<float, 4> {
     static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
         *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     }
+    // read for the last time; written, not to be read soon
+    static __device__ __forceinline__ Raw raw_last(const float* p) {
+        return __ldcs(reinterpret_cast<const float4*>(p));
+    }
+    static __device__ __forceinline__ void store_through(float* p, const float (&v)[4]) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    }
 };
 template <>
 struct Pack<__nv_bfloat16, 8> {
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw raw(const __nv_bfloat16* p) {
+        return *reinterpret_cast<const uint4*>(p);
+    }
     static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        open(*reinterpret_cast<const uint4*>(p), v);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+        *reinterpret_cast<uint4*>(p) = round8(v);
+    }
+    static __device__ __forceinline__ Raw raw_last(const __nv_bfloat16* p) {
+        return __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    static __device__ __forceinline__ void store_through(__nv_bfloat16* p, const float (&v)[8]) {
+        __stcs(reinterpret_cast<uint4*>(p), round8(v));
+    }
+    static __device__ __forceinline__ void open(const uint4& u, float (&v)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -60,28 +96,44 @@ struct Pack<__nv_bfloat16, 8> {
             v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+    static __device__ __forceinline__ uint4 round8(const float (&v)[8]) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
             w[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 template <>
 struct Pack<float, 1> {
+    using Raw = float;
+    static __device__ __forceinline__ Raw raw(const float* p) { return *p; }
+    static __device__ __forceinline__ void open(const Raw& u, float (&v)[1]) { v[0] = u; }
     static __device__ __forceinline__ void load(const float* p, float (&v)[1]) { v[0] = *p; }
     static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { *p = v[0]; }
+    static __device__ __forceinline__ Raw raw_last(const float* p) { return *p; }
+    static __device__ __forceinline__ void store_through(float* p, const float (&v)[1]) {
+        store(p, v);
+    }
 };
 template <>
 struct Pack<__nv_bfloat16, 1> {
+    using Raw = __nv_bfloat16;
+    static __device__ __forceinline__ Raw raw(const __nv_bfloat16* p) { return *p; }
+    static __device__ __forceinline__ void open(const Raw& u, float (&v)[1]) {
+        v[0] = __bfloat162float(u);
+    }
     static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[1]) {
         v[0] = __bfloat162float(*p);
     }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[1]) {
         *p = __float2bfloat16_rn(v[0]);
+    }
+    static __device__ __forceinline__ Raw raw_last(const __nv_bfloat16* p) { return *p; }
+    static __device__ __forceinline__ void store_through(__nv_bfloat16* p, const float (&v)[1]) {
+        store(p, v);
     }
 };
 
@@ -124,6 +176,7 @@ struct NormCall {
     float* grad_bias;         // may be NULL
 };
 size_t group_norm_workspace(int64_t images, int64_t pixels, int32_t channels, int32_t groups);
+cudaError_t prepare_group_norm();
 cudaError_t launch_group_norm_forward(const NormCall& c, void* ws, int n_sms, cudaStream_t stream);
 cudaError_t launch_group_norm_backward(const NormCall& c, void* ws, int n_sms,
                                        cudaStream_t stream);

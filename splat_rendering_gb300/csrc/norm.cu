@@ -10,18 +10,31 @@
 // channels in 16-byte vectors and walk the pixels, so every access is
 // coalesced and a thread's channels (its weights, its sums) never change.
 //
-// Statistics: a thread sums x - k and (x - k)^2 with k its own first value,
-// which bounds the cancellation of the second moment by the number of its
-// pixels whatever the mean, and turns them into (mean, M2); parts are joined
-// by sum(M2) + sum(n (mean - common mean)^2), in 32 bits and a fixed order.
+// A small image is one cluster's: its blocks keep their pixels in registers
+// between the reduction and its use and join through distributed shared
+// memory, one launch that reads and writes everything once.  A larger one
+// takes two launches, each one wave of resident blocks: the second joins the
+// parts of the first and reads the image again, from the end, where the L2
+// still holds it; of a batch that the L2 does not hold, as many images at a
+// time as it does.
+//
+// Statistics: a thread sums x - k and (x - k)^2 over up to 64 pixels with k
+// the first of them, which bounds the cancellation of the second moment by
+// that number whatever the mean, and turns them into (mean, M2); parts are
+// joined by sum(M2) + sum(n (mean - common mean)^2), in 32 bits and a fixed
+// order.
 #include "learn_internal.cuh"
 
 namespace pulsar {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxNormChannels = 4096;
-constexpr int kMaxChunks = 1024;   // pixel chunks per image
+constexpr int kSegment = 64;   // pixels a thread sums about one value
+constexpr int kAhead = 8;      // 16-byte loads a thread has in flight
+
+// Resident blocks per SM: what the registers of each form allow.
+constexpr int blocks_per_sm(int v, bool back) { return back ? (v == 8 ? 2 : 3) : (v == 8 ? 3 : 4); }
+constexpr int kMostBlocks = 4 * 160;   // of a wave, on the largest part
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -29,13 +42,13 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// How the threads lie on an image's rows of C channels.
+// How an image lies on its blocks.
 struct Shape {
     int64_t pixels;
     int channels, groups, cpg;   // cpg = channels / groups
     int cols;                    // vectors per pixel
     int rpb;                     // pixels a block covers at once (cols <= kThreads), else 1
-    int chunks;                  // blocks per image
+    int blocks;                  // per image
     int64_t chunk;               // pixels per block
 };
 
@@ -43,81 +56,127 @@ __device__ __forceinline__ int rows_of(int64_t len, int row, int rpb) {
     return len > row ? (int)((len - row + rpb - 1) / rpb) : 0;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
-
-__device__ __forceinline__ float activate(float z, int act) {
-    if (act == kActSilu) return z * sigmoid(z);
-    if (act == kActRelu) return z > 0.0f || z != z ? z : 0.0f;   // NaN stays NaN
+// ------------------------------------------------------------- activation --
+template <int kAct>
+__device__ __forceinline__ float activate(float z) {
+    if (kAct == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
+    if (kAct == kActRelu) return z > 0.0f || z != z ? z : 0.0f;   // NaN stays NaN
     return z;
 }
-__device__ __forceinline__ float activate_grad(float z, float dy, int act) {
-    if (act == kActSilu) {
-        const float s = sigmoid(z);
+template <int kAct>
+__device__ __forceinline__ float activate_grad(float z, float dy) {
+    if (kAct == kActSilu) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
         return dy * (s * fmaf(z, 1.0f - s, 1.0f));
     }
-    if (act == kActRelu) return z > 0.0f ? dy : 0.0f;
+    if (kAct == kActRelu) return z > 0.0f ? dy : 0.0f;
     return dy;
 }
 
-// ------------------------------------------------------------ statistics --
-// part[image][chunk][group] = (mean, M2) of the chunk's values.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
-k_norm_stats(const T* __restrict__ x, Shape sh, float2* __restrict__ part) {
-    pdl_begin();
-    // one entry per thread and channel (or per vector, where a vector stays in a group)
-    __shared__ float s_mean[kMaxNormChannels], s_m2[kMaxNormChannels];
-    const bool whole = sh.cpg % V == 0;
-    const int sub = whole ? 1 : V;               // entries per vector
-    const int epr = sh.cols * sub, eg = epr / sh.groups;
-    const int64_t p0 = blockIdx.x * sh.chunk;
-    const int64_t len = min(sh.chunk, sh.pixels - p0);
-    const T* base = x + ((int64_t)blockIdx.y * sh.pixels + p0) * sh.channels;
-    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
-    const int cnt = rows_of(len, row, sh.rpb);
-    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
-        float k[V], s[V], q[V];
-        if (cnt > 0) Pack<T, V>::load(base + (int64_t)row * sh.channels + col * V, k);
-#pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = q[j] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            float v[V];
-            Pack<T, V>::load(base + (row + (int64_t)i * sh.rpb) * sh.channels + col * V, v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = v[j] - k[j];
-                s[j] += d;
-                q[j] = fmaf(d, d, q[j]);
-            }
-        }
-        const float inv = cnt > 0 ? 1.0f / (float)cnt : 0.0f;
-        float mean[V], m2[V];
+// What a thread's V channels need: the mean, rstd, w and b.
+template <int V>
+struct Affine {
+    float mean[V], rstd[V], w[V], b[V];
+    __device__ __forceinline__ void load(const float2* stats, const float* weight,
+                                         const float* bias, int c0, int cpg) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            mean[j] = cnt > 0 ? fmaf(s[j], inv, k[j]) : 0.0f;
-            m2[j] = fmaxf(fmaf(-s[j] * inv, s[j], q[j]), 0.0f);
-            if (q[j] != q[j]) m2[j] = q[j];   // fmaxf drops a NaN
+            const float2 s = stats[(c0 + j) / cpg];
+            mean[j] = s.x;
+            rstd[j] = s.y;
+            w[j] = weight ? weight[c0 + j] : 1.0f;
+            b[j] = bias ? bias[c0 + j] : 0.0f;
         }
-        const int e = row * epr + col * sub;
-        if (whole) {
-            float m = 0.0f, t = 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) m += mean[j];
-            m *= 1.0f / V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) t += fmaf((float)cnt * (mean[j] - m), mean[j] - m, m2[j]);
-            s_mean[e] = m;
-            s_m2[e] = t;
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                s_mean[e + j] = mean[j];
-                s_m2[e + j] = m2[j];
-            }
+    }
+};
+
+// ------------------------------------------------------------------ joins --
+// The image's statistics from its blocks' parts, S1 = sum n (m - k) and
+// S2 = sum n (m - k)^2 about the first part's mean k, a warp per group.
+template <typename Part>
+__device__ __forceinline__ void join_stats(const Part& part, const Shape& sh, float eps,
+                                           float2* s_stats) {
+    const int lane = threadIdx.x & 31;
+    const float inv_pix = 1.0f / (float)sh.pixels;
+    for (int g = threadIdx.x >> 5; g < sh.groups; g += kThreads / 32) {
+        const float k = part(0, g).x;
+        float s1 = 0.0f, s2 = 0.0f, t = 0.0f;
+        for (int b = lane; b < sh.blocks; b += 32) {
+            const float share = (float)min(sh.chunk, sh.pixels - b * sh.chunk) * inv_pix;
+            const float2 u = part(b, g);
+            const float d = u.x - k;
+            s1 = fmaf(share, d, s1);
+            s2 = fmaf(share * d, d, s2);
+            t += u.y;
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        t = warp_sum(t);
+        if (lane == 0) {
+            float between = fmaxf(fmaf(-s1, s1, s2), 0.0f);
+            if (s2 != s2) between = s2;   // fmaxf drops a NaN
+            const float var = t / ((float)sh.pixels * (float)sh.cpg) + between;
+            s_stats[g] = make_float2(k + s1, 1.0f / sqrtf(var + eps));
         }
     }
     __syncthreads();
+}
+
+// s_means[g] = (mean dh, mean dh h) from the blocks' parts.
+template <typename Part>
+__device__ __forceinline__ void join_means(const Part& part, const Shape& sh, float2* s_means) {
+    const int lane = threadIdx.x & 31;
+    const float inv = 1.0f / ((float)sh.pixels * (float)sh.cpg);
+    for (int g = threadIdx.x >> 5; g < sh.groups; g += kThreads / 32) {
+        float a = 0.0f, q = 0.0f;
+        for (int b = lane; b < sh.blocks; b += 32) {
+            const float2 u = part(b, g);
+            a += u.x;
+            q += u.y;
+        }
+        a = warp_sum(a);
+        q = warp_sum(q);
+        if (lane == 0) s_means[g] = make_float2(a * inv, q * inv);
+    }
+    __syncthreads();
+}
+
+// -------------------------------------------------- reductions over a run --
+// s_mean, s_m2 hold one entry per thread and channel (or per vector, where a
+// vector stays in a group).
+__device__ __forceinline__ bool whole_vectors(const Shape& sh, int v) { return sh.cpg % v == 0; }
+
+// A thread's (mean, M2) of cnt pixels of its V channels, as its entries.
+template <int V>
+__device__ __forceinline__ void put_entries(const Shape& sh, int row, int col, int cnt,
+                                            const float (&mean)[V], const float (&m2)[V],
+                                            float* s_mean, float* s_m2) {
+    if (whole_vectors(sh, V)) {
+        const int e = row * sh.cols + col;
+        float m = 0.0f, t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m += mean[j];
+        m *= 1.0f / V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) t += fmaf((float)cnt * (mean[j] - m), mean[j] - m, m2[j]);
+        s_mean[e] = m;
+        s_m2[e] = t;
+    } else {
+        const int e = (row * sh.cols + col) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s_mean[e + j] = mean[j];
+            s_m2[e + j] = m2[j];
+        }
+    }
+}
+
+// (mean, M2) of the run per group from the entries: a warp per group.
+template <int V>
+__device__ __forceinline__ void group_entries(const Shape& sh, int64_t len, const float* s_mean,
+                                              const float* s_m2, float2* part) {
+    const int sub = whole_vectors(sh, V) ? 1 : V;
+    const int epr = sh.cols * sub, eg = epr / sh.groups;
     const int lane = threadIdx.x & 31;
     const float per = (float)(V / sub);   // channels per entry
     const float inv_all = 1.0f / ((float)len * (float)sh.cpg);
@@ -138,349 +197,788 @@ k_norm_stats(const T* __restrict__ x, Shape sh, float2* __restrict__ part) {
             if (c > 0) t += fmaf((float)c * per * d, d, s_m2[at]);
         }
         t = warp_sum(t);
-        if (lane == 0)
-            part[((size_t)blockIdx.y * sh.chunks + blockIdx.x) * sh.groups + g] = make_float2(m, t);
+        if (lane == 0) part[g] = make_float2(m, t);
     }
 }
 
-// stats[image][group] = (mean, rstd) from the chunks: a warp per group.
-__global__ void __launch_bounds__(kThreads)
-k_norm_finish(const float2* __restrict__ part, Shape sh, float eps, float2* __restrict__ stats) {
-    pdl_begin();
-    const int lane = threadIdx.x & 31;
-    const int g = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (g >= sh.groups) return;
-    const float2* p = part + (size_t)blockIdx.y * sh.chunks * sh.groups + g;
-    const float inv_pix = 1.0f / (float)sh.pixels;   // (no chunk reads it where there is no pixel)
-    float m = 0.0f;
-    for (int c = lane; c < sh.chunks; c += 32) {
-        const float len = (float)min(sh.chunk, sh.pixels - c * sh.chunk);
-        m = fmaf(len * inv_pix, p[(size_t)c * sh.groups].x, m);
-    }
-    m = warp_sum(m);
-    float t = 0.0f;
-    for (int c = lane; c < sh.chunks; c += 32) {
-        const float len = (float)min(sh.chunk, sh.pixels - c * sh.chunk);
-        const float2 u = p[(size_t)c * sh.groups];
-        const float d = u.x - m;
-        t += fmaf(len * (float)sh.cpg * d, d, u.y);
-    }
-    t = warp_sum(t);
-    if (lane == 0) {
-        const float var = sh.pixels > 0 ? t / ((float)sh.pixels * (float)sh.cpg) : 0.0f;
-        stats[(size_t)blockIdx.y * sh.groups + g] = make_float2(m, 1.0f / sqrtf(var + eps));
-    }
+// (mean, M2) of n values about k, one of them, from s = sum(x - k), q = sum(x - k)^2.
+__device__ __forceinline__ void settle(float k, float s, float q, float inv_n, float* mean,
+                                       float* m2) {
+    *mean = fmaf(s, inv_n, k);
+    const float t = fmaxf(fmaf(-s * inv_n, s, q), 0.0f);
+    *m2 = q != q ? q : t;
 }
-
-// ----------------------------------------------------------------- apply --
-// What a thread's V channels need: the mean, rstd w and b.
-template <int V>
-struct Affine {
-    float mean[V], rstd[V], w[V], b[V];
-    __device__ __forceinline__ void load(const float2* stats, const float* weight,
-                                         const float* bias, int c0, int cpg) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float2 s = stats[(c0 + j) / cpg];
-            mean[j] = s.x;
-            rstd[j] = s.y;
-            w[j] = weight ? weight[c0 + j] : 1.0f;
-            b[j] = bias ? bias[c0 + j] : 0.0f;
-        }
-    }
-};
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
-k_norm_apply(const T* __restrict__ x, Shape sh, const float2* __restrict__ stats,
-             const float* __restrict__ weight, const float* __restrict__ bias, int act,
-             T* __restrict__ y) {
-    pdl_begin();
-    const int64_t p0 = blockIdx.x * sh.chunk;
-    const int64_t len = min(sh.chunk, sh.pixels - p0);
-    const int64_t off = ((int64_t)blockIdx.y * sh.pixels + p0) * sh.channels;
+__device__ __forceinline__ void run_stats(const T* __restrict__ base, int64_t len, const Shape& sh,
+                                          float* s_mean, float* s_m2, float2* __restrict__ part) {
     const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
     const int cnt = rows_of(len, row, sh.rpb);
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
     for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
-        Affine<V> f;
-        f.load(stats + (size_t)blockIdx.y * sh.groups, weight, bias, col * V, sh.cpg);
+        const T* at = base + (int64_t)row * sh.channels + col * V;
+        float mean[V], m2[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f.rstd[j] *= f.w[j];
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            const int64_t at = off + (row + (int64_t)i * sh.rpb) * sh.channels + col * V;
-            float v[V];
-            Pack<T, V>::load(x + at, v);
+        for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.0f;
+        for (int i0 = 0; i0 < cnt; i0 += kSegment) {
+            const int n = min(kSegment, cnt - i0);
+            float k[V], s[V], q[V];
+            Pack<T, V>::load(at, k);   // (kAhead divides kSegment: `at` is at pixel i0)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] = activate(fmaf(v[j] - f.mean[j], f.rstd[j], f.b[j]), act);
-            Pack<T, V>::store(y + at, v);
+            for (int j = 0; j < V; ++j) s[j] = q[j] = 0.0f;
+            for (int i = 0; i < n; i += kAhead, at += kAhead * pitch) {
+                typename Pack<T, V>::Raw r[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (i + u < n) r[u] = Pack<T, V>::raw(at + u * pitch);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    float v[V];
+                    Pack<T, V>::open(r[u], v);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float d = i + u < n ? v[j] - k[j] : 0.0f;
+                        s[j] += d;
+                        q[j] = fmaf(d, d, q[j]);
+                    }
+                }
+            }
+            // this segment joins the ones before
+            const float f = (float)n / (float)(i0 + n);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float m, t;
+                settle(k[j], s[j], q[j], 1.0f / (float)n, &m, &t);
+                const float d = m - mean[j];
+                m2[j] = i0 ? m2[j] + fmaf(d * d, f * (float)i0, t) : t;
+                mean[j] = i0 ? fmaf(d, f, mean[j]) : m;
+            }
         }
+        put_entries<V>(sh, row, col, cnt, mean, m2, s_mean, s_m2);
     }
+    __syncthreads();
+    group_entries<V>(sh, len, s_mean, s_m2, part);
 }
 
-// -------------------------------------------------------------- backward --
-// part[image][chunk][channel] = (sum dz, sum dz h) over the chunk's pixels.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
-k_norm_back_sums(const T* __restrict__ x, const T* __restrict__ dy, Shape sh,
-                 const float2* __restrict__ stats, const float* __restrict__ weight,
-                 const float* __restrict__ bias, int act, float2* __restrict__ part) {
-    pdl_begin();
-    __shared__ float s1[kThreads * V], s2[kThreads * V];
-    const int64_t p0 = blockIdx.x * sh.chunk;
-    const int64_t len = min(sh.chunk, sh.pixels - p0);
-    const int64_t off = ((int64_t)blockIdx.y * sh.pixels + p0) * sh.channels;
-    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
-    const int cnt = rows_of(len, row, sh.rpb);
-    float2* out = part + ((size_t)blockIdx.y * sh.chunks + blockIdx.x) * sh.channels;
-    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
-        Affine<V> f;
-        f.load(stats + (size_t)blockIdx.y * sh.groups, weight, bias, col * V, sh.cpg);
-        float a[V], q[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) a[j] = q[j] = 0.0f;
-#pragma unroll 2
-        for (int i = 0; i < cnt; ++i) {
-            const int64_t at = off + (row + (int64_t)i * sh.rpb) * sh.channels + col * V;
-            float v[V], g[V];
-            Pack<T, V>::load(x + at, v);
-            Pack<T, V>::load(dy + at, g);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float h = (v[j] - f.mean[j]) * f.rstd[j];
-                const float dz = activate_grad(fmaf(h, f.w[j], f.b[j]), g[j], act);
-                a[j] += dz;
-                q[j] = fmaf(dz, h, q[j]);
-            }
-        }
-        if (sh.rpb == 1) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) out[col * V + j] = make_float2(a[j], q[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                s1[row * sh.channels + col * V + j] = a[j];
-                s2[row * sh.channels + col * V + j] = q[j];
-            }
-        }
-    }
-    if (sh.rpb == 1) return;
+// s_sum holds (sum dz, sum dz h) per thread and channel: per channel into row
+// 0 (and `total`), and per group, weighted by w, into `part`.
+__device__ __forceinline__ void channel_sums(const Shape& sh, const float* __restrict__ weight,
+                                             float2* s_sum, float2* total, float2* part) {
     __syncthreads();
     for (int c = threadIdx.x; c < sh.channels; c += kThreads) {
         float a = 0.0f, q = 0.0f;
+#pragma unroll 4
         for (int r = 0; r < sh.rpb; ++r) {
-            a += s1[r * sh.channels + c];
-            q += s2[r * sh.channels + c];
+            const float2 u = s_sum[r * sh.channels + c];
+            a += u.x;
+            q += u.y;
         }
-        out[c] = make_float2(a, q);
+        s_sum[c] = make_float2(a, q);   // (row 0's own entry: nobody else reads it)
+        if (total) total[c] = make_float2(a, q);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < sh.groups; g += kThreads / 32) {
+        float a = 0.0f, q = 0.0f;
+        for (int c = g * sh.cpg + lane; c < (g + 1) * sh.cpg; c += 32) {
+            const float wc = weight ? weight[c] : 1.0f;
+            a = fmaf(wc, s_sum[c].x, a);
+            q = fmaf(wc, s_sum[c].y, q);
+        }
+        a = warp_sum(a);
+        q = warp_sum(q);
+        if (lane == 0) part[g] = make_float2(a, q);
     }
 }
 
-// sums[image][channel] over the chunks: a warp per channel.
-__global__ void __launch_bounds__(kThreads)
-k_norm_back_chunks(const float2* __restrict__ part, Shape sh, float2* __restrict__ sums) {
+// One value's share of the sums, and its gradient.
+template <int kAct>
+__device__ __forceinline__ float grad_h(float x, float dy, float mean, float rstd, float w, float b,
+                                        float* h) {
+    *h = (x - mean) * rstd;
+    return activate_grad<kAct>(fmaf(*h, w, b), dy);
+}
+
+// ----------------------------------------------------------- two launches --
+template <typename T, int V, int kAct>
+__device__ __forceinline__ void run_apply(const T* __restrict__ x, T* __restrict__ y, int64_t off,
+                                          int64_t len, const Shape& sh, const float2* stats,
+                                          const float* __restrict__ weight,
+                                          const float* __restrict__ bias) {
+    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
+    const int cnt = rows_of(len, row, sh.rpb);
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
+    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
+        Affine<V> f;
+        f.load(stats, weight, bias, col * V, sh.cpg);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f.rstd[j] *= f.w[j];
+        // from the end: what was read last is nearest
+        int64_t at = off + (row + (int64_t)(cnt - 1) * sh.rpb) * sh.channels + col * V;
+        for (int i = 0; i < cnt; i += kAhead / 2, at -= kAhead / 2 * pitch) {
+            typename Pack<T, V>::Raw r[kAhead / 2];
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u)
+                if (i + u < cnt) r[u] = Pack<T, V>::raw_last(x + at - u * pitch);
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u) {
+                if (i + u >= cnt) break;
+                float v[V];
+                Pack<T, V>::open(r[u], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = activate<kAct>(fmaf(v[j] - f.mean[j], f.rstd[j], f.b[j]));
+                Pack<T, V>::store_through(y + at - u * pitch, v);
+            }
+        }
+    }
+}
+
+struct Place {
+    int64_t off, len;   // first element of the block's run, pixels
+};
+__device__ __forceinline__ Place place(const Shape& sh, int64_t image) {
+    const int64_t p0 = (int64_t)blockIdx.x * sh.chunk;
+    return {(image * sh.pixels + p0) * sh.channels, min(sh.chunk, sh.pixels - p0)};
+}
+
+// part[image of the launch][block][group] = (mean, M2).
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, false))
+k_norm_stats(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t image0,
+             float2* __restrict__ part) {
     pdl_begin();
+    extern __shared__ float smem[];
+    const Place p = place(sh, image0 + blockIdx.y);
+    const int entries = sh.rpb * sh.cols * V;
+    run_stats<T, V>(x + p.off, p.len, sh, smem, smem + entries,
+                    part + ((size_t)blockIdx.y * sh.blocks + blockIdx.x) * sh.groups);
+}
+
+template <typename T, int V, int kAct>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, false))
+k_norm_apply(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t image0,
+             const float2* __restrict__ part, const float* __restrict__ weight,
+             const float* __restrict__ bias, float eps, T* __restrict__ y,
+             float2* __restrict__ stats) {
+    pdl_begin();
+    extern __shared__ float smem[];
+    float2* s_stats = reinterpret_cast<float2*>(smem);
+    const int64_t image = image0 + blockIdx.y;
+    const Place p = place(sh, image);
+    const float2* mine = part + (size_t)blockIdx.y * sh.blocks * sh.groups;
+    join_stats([&](int b, int g) { return mine[(size_t)b * sh.groups + g]; }, sh, eps, s_stats);
+    if (blockIdx.x == 0)
+        for (int g = threadIdx.x; g < sh.groups; g += kThreads)
+            stats[(size_t)image * sh.groups + g] = s_stats[g];
+    run_apply<T, V, kAct>(x, y, p.off, p.len, sh, s_stats, weight, bias);
+}
+
+// part[image of the launch][block][group], total[..][block][channel].
+template <typename T, int V, int kAct>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, true))
+k_norm_back_sums(const T* __restrict__ x, const T* __restrict__ dy, const __grid_constant__ Shape sh,
+                 int64_t image0, const float2* __restrict__ stats,
+                 const float* __restrict__ weight, const float* __restrict__ bias,
+                 float2* __restrict__ part, float2* __restrict__ total) {
+    pdl_begin();
+    extern __shared__ float smem[];
+    float2* s_sum = reinterpret_cast<float2*>(smem);
+    const int64_t image = image0 + blockIdx.y;
+    const Place p = place(sh, image);
+    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
+    const int cnt = rows_of(p.len, row, sh.rpb);
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
+    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
+        Affine<V> f;
+        f.load(stats + (size_t)image * sh.groups, weight, bias, col * V, sh.cpg);
+        float a[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = q[j] = 0.0f;
+        int64_t at = p.off + (int64_t)row * sh.channels + col * V;
+        for (int i = 0; i < cnt; i += kAhead / 2, at += kAhead / 2 * pitch) {
+            typename Pack<T, V>::Raw rx[kAhead / 2], ry[kAhead / 2];
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u) {
+                if (i + u < cnt) {
+                    rx[u] = Pack<T, V>::raw(x + at + u * pitch);
+                    ry[u] = Pack<T, V>::raw(dy + at + u * pitch);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u) {
+                if (i + u >= cnt) break;
+                float v[V], g[V];
+                Pack<T, V>::open(rx[u], v);
+                Pack<T, V>::open(ry[u], g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float h;
+                    const float dz =
+                        grad_h<kAct>(v[j], g[j], f.mean[j], f.rstd[j], f.w[j], f.b[j], &h);
+                    a[j] += dz;
+                    q[j] = fmaf(dz, h, q[j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            s_sum[row * sh.channels + col * V + j] = make_float2(a[j], q[j]);
+    }
+    const size_t blk = (size_t)blockIdx.y * sh.blocks + blockIdx.x;
+    channel_sums(sh, weight, s_sum,
+                 total + blk * sh.channels,
+                 part + blk * sh.groups);
+}
+
+template <typename T, int V, int kAct>
+__device__ __forceinline__ void run_back(const T* __restrict__ x, const T* __restrict__ dy,
+                                         T* __restrict__ dx, int64_t off, int64_t len,
+                                         const Shape& sh, const float2* __restrict__ stats,
+                                         const float2* means, const float* __restrict__ weight,
+                                         const float* __restrict__ bias) {
+    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
+    const int cnt = rows_of(len, row, sh.rpb);
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
+    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
+        Affine<V> f;
+        f.load(stats, weight, bias, col * V, sh.cpg);
+        float m1[V], m2[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 u = means[(col * V + j) / sh.cpg];
+            m1[j] = u.x;
+            m2[j] = u.y;
+        }
+        int64_t at = off + (row + (int64_t)(cnt - 1) * sh.rpb) * sh.channels + col * V;
+        for (int i = 0; i < cnt; i += kAhead / 2, at -= kAhead / 2 * pitch) {
+            typename Pack<T, V>::Raw rx[kAhead / 2], ry[kAhead / 2];
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u) {
+                if (i + u < cnt) {
+                    rx[u] = Pack<T, V>::raw_last(x + at - u * pitch);
+                    ry[u] = Pack<T, V>::raw_last(dy + at - u * pitch);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead / 2; ++u) {
+                if (i + u >= cnt) break;
+                float v[V], g[V];
+                Pack<T, V>::open(rx[u], v);
+                Pack<T, V>::open(ry[u], g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float h;
+                    const float dz =
+                        grad_h<kAct>(v[j], g[j], f.mean[j], f.rstd[j], f.w[j], f.b[j], &h);
+                    v[j] = f.rstd[j] * (fmaf(dz, f.w[j], -m1[j]) - h * m2[j]);
+                }
+                Pack<T, V>::store_through(dx + at - u * pitch, v);
+            }
+        }
+    }
+}
+
+template <typename T, int V, int kAct>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, true))
+k_norm_back_apply(const T* __restrict__ x, const T* __restrict__ dy,
+                  const __grid_constant__ Shape sh, int64_t image0,
+                  const float2* __restrict__ stats, const float2* __restrict__ part,
+                  const float* __restrict__ weight, const float* __restrict__ bias,
+                  T* __restrict__ dx, const float2* __restrict__ total, int images,
+                  float2* __restrict__ image_total, float* __restrict__ grad_weight,
+                  float* __restrict__ grad_bias) {
+    pdl_begin();
+    extern __shared__ float smem[];
+    float2* s_means = reinterpret_cast<float2*>(smem);
+    const int64_t image = image0 + blockIdx.y;
+    const Place p = place(sh, image);
+    if (dx) {
+        const float2* mine = part + (size_t)blockIdx.y * sh.blocks * sh.groups;
+        join_means([&](int b, int g) { return mine[(size_t)b * sh.groups + g]; }, sh, s_means);
+        run_back<T, V, kAct>(x, dy, dx, p.off, p.len, sh, stats + (size_t)image * sh.groups,
+                             s_means, weight, bias);
+    }
+    // the image's channel sums, a warp per channel; of one image, the gradients themselves
+    const float2* t = total + (size_t)blockIdx.y * sh.blocks * sh.channels;
     const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (c >= sh.channels) return;
-    const float2* p = part + (size_t)blockIdx.y * sh.chunks * sh.channels + c;
+    for (int c = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); c < sh.channels;
+         c += gridDim.x * (kThreads / 32)) {
+        float a = 0.0f, q = 0.0f;
+#pragma unroll 4
+        for (int b = lane; b < sh.blocks; b += 32) {
+            const float2 u = t[(size_t)b * sh.channels + c];
+            a += u.x;
+            q += u.y;
+        }
+        a = warp_sum(a);
+        q = warp_sum(q);
+        if (lane == 0) {
+            if (images > 1) {
+                image_total[(size_t)image * sh.channels + c] = make_float2(a, q);
+            } else {
+                if (grad_bias) grad_bias[c] = a;
+                if (grad_weight) grad_weight[c] = q;
+            }
+        }
+    }
+}
+
+// The parameters' gradients from the images' totals [n][channels].
+__global__ void __launch_bounds__(kThreads)
+k_norm_back_params(const float2* __restrict__ total, int64_t n, int channels,
+                   float* __restrict__ grad_weight, float* __restrict__ grad_bias) {
+    pdl_begin();
+    const int lane = threadIdx.x & 31, c = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (c >= channels) return;
     float a = 0.0f, q = 0.0f;
-    for (int k = lane; k < sh.chunks; k += 32) {
-        const float2 u = p[(size_t)k * sh.channels];
+#pragma unroll 4
+    for (int64_t r = lane; r < n; r += 32) {
+        const float2 u = total[r * channels + c];
         a += u.x;
         q += u.y;
     }
     a = warp_sum(a);
     q = warp_sum(q);
-    if (lane == 0) sums[(size_t)blockIdx.y * sh.channels + c] = make_float2(a, q);
-}
-
-// The parameters' gradients (sums over the images), and
-// means[image][group] = (mean dh, mean dh h).
-__global__ void __launch_bounds__(kThreads)
-k_norm_back_finish(const float2* __restrict__ sums, Shape sh, int images,
-                   const float* __restrict__ weight, float* __restrict__ grad_weight,
-                   float* __restrict__ grad_bias, float2* __restrict__ means) {
-    pdl_begin();
-    const int64_t stride = (int64_t)gridDim.x * kThreads;
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-         e < sh.channels + (int64_t)images * sh.groups; e += stride) {
-        if (e < sh.channels) {
-            float a = 0.0f, q = 0.0f;
-            for (int i = 0; i < images; ++i) {
-                const float2 u = sums[(size_t)i * sh.channels + e];
-                a += u.x;
-                q += u.y;
-            }
-            if (grad_bias) grad_bias[e] = a;
-            if (grad_weight) grad_weight[e] = q;
-        } else {
-            const int64_t ig = e - sh.channels;
-            const int64_t image = ig / sh.groups;
-            const int c0 = (int)(ig % sh.groups) * sh.cpg;
-            float a = 0.0f, q = 0.0f;
-            for (int c = c0; c < c0 + sh.cpg; ++c) {
-                const float2 u = sums[(size_t)image * sh.channels + c];
-                const float wc = weight ? weight[c] : 1.0f;
-                a = fmaf(wc, u.x, a);
-                q = fmaf(wc, u.y, q);
-            }
-            const float inv = 1.0f / ((float)sh.pixels * (float)sh.cpg);
-            means[ig] = make_float2(a * inv, q * inv);
-        }
+    if (lane == 0) {
+        if (grad_bias) grad_bias[c] = a;
+        if (grad_weight) grad_weight[c] = q;
     }
 }
 
-template <typename T, int V>
+// The statistics of nothing: mean 0, variance 0.
+__global__ void k_norm_empty(float2* stats, int64_t n, float eps) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) stats[i] = make_float2(0.0f, 1.0f / sqrtf(eps));
+}
+
+// ---------------------------------------------------------- small images --
+// A cluster of sh.blocks blocks (1 to 8) has an image; a thread keeps its
+// pixels, at most kHeld, as they were loaded.
+constexpr int kHeld = 8;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// *p in the shared memory of the cluster's block `rank`
+__device__ __forceinline__ float2 of_block(const float2* p, int rank) {
+    uint32_t at;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(kThreads)
-k_norm_back_apply(const T* __restrict__ x, const T* __restrict__ dy, Shape sh,
-                  const float2* __restrict__ stats, const float2* __restrict__ means,
-                  const float* __restrict__ weight, const float* __restrict__ bias, int act,
-                  T* __restrict__ dx) {
+k_norm_small(const T* __restrict__ x, const __grid_constant__ Shape sh,
+             const float* __restrict__ weight, const float* __restrict__ bias, float eps,
+             T* __restrict__ y, float2* __restrict__ stats) {
+    using P = Pack<T, V>;
     pdl_begin();
-    const int64_t p0 = blockIdx.x * sh.chunk;
-    const int64_t len = min(sh.chunk, sh.pixels - p0);
-    const int64_t off = ((int64_t)blockIdx.y * sh.pixels + p0) * sh.channels;
-    const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
-    const int cnt = rows_of(len, row, sh.rpb);
-    for (int col = threadIdx.x - row * sh.cols; col < sh.cols && row < sh.rpb; col += kThreads) {
+    extern __shared__ float smem[];
+    const int entries = sh.rpb * sh.cols * V;
+    float* s_mean = smem;
+    float* s_m2 = smem + entries;
+    float2* s_part = reinterpret_cast<float2*>(smem + 2 * entries);
+    float2* s_stats = s_part + sh.groups;
+    const Place p = place(sh, blockIdx.y);
+    const int row = (int)threadIdx.x / sh.cols, col = (int)threadIdx.x - row * sh.cols;
+    const int cnt = row < sh.rpb ? rows_of(p.len, row, sh.rpb) : 0;
+    const int64_t at = p.off + (int64_t)row * sh.channels + col * V;
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
+    typename P::Raw held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (i < cnt) held[i] = P::raw(x + at + i * pitch);
+    if (row < sh.rpb) {
+        float k[V], mean[V], m2[V], s[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) k[j] = mean[j] = m2[j] = s[j] = q[j] = 0.0f;
+        if (cnt > 0) P::open(held[0], k);
+#pragma unroll
+        for (int i = 1; i < kHeld; ++i) {
+            if (i < cnt) {
+                float v[V];
+                P::open(held[i], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = v[j] - k[j];
+                    s[j] += d;
+                    q[j] = fmaf(d, d, q[j]);
+                }
+            }
+        }
+        if (cnt > 0) {
+            const float inv = 1.0f / (float)cnt;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                // (an infinite k leaves no difference to itself where it is alone)
+                if (!(k[j] - k[j] == 0.0f)) q[j] = k[j] - k[j];
+                settle(k[j], s[j], q[j], inv, &mean[j], &m2[j]);
+            }
+        }
+        put_entries<V>(sh, row, col, cnt, mean, m2, s_mean, s_m2);
+    }
+    __syncthreads();
+    group_entries<V>(sh, p.len, s_mean, s_m2, s_part);
+    cluster_meet();
+    join_stats([&](int b, int g) { return of_block(s_part + g, b); }, sh, eps, s_stats);
+    if (blockIdx.x == 0)
+        for (int g = threadIdx.x; g < sh.groups; g += kThreads)
+            stats[(size_t)blockIdx.y * sh.groups + g] = s_stats[g];
+    if (row < sh.rpb) {
         Affine<V> f;
+        f.load(s_stats, weight, bias, col * V, sh.cpg);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f.rstd[j] *= f.w[j];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (i < cnt) {
+                float v[V];
+                P::open(held[i], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = activate<kAct>(fmaf(v[j] - f.mean[j], f.rstd[j], f.b[j]));
+                P::store(y + at + i * pitch, v);
+            }
+        }
+    }
+    cluster_meet();   // the others may still read this block's parts
+}
+
+// total[image][channel]; where there is one image, its gradients themselves.
+template <typename T, int V, int kAct>
+__global__ void __launch_bounds__(kThreads)
+k_norm_small_back(const T* __restrict__ x, const T* __restrict__ dy,
+                  const __grid_constant__ Shape sh, const float2* __restrict__ stats,
+                  const float* __restrict__ weight, const float* __restrict__ bias,
+                  T* __restrict__ dx, float* __restrict__ grad_weight,
+                  float* __restrict__ grad_bias, float2* __restrict__ total) {
+    using P = Pack<T, V>;
+    pdl_begin();
+    extern __shared__ float smem[];
+    float2* s_sum = reinterpret_cast<float2*>(smem);
+    float2* s_part = s_sum + sh.rpb * sh.cols * V;
+    float2* s_means = s_part + sh.groups;
+    const Place p = place(sh, blockIdx.y);
+    const int row = (int)threadIdx.x / sh.cols, col = (int)threadIdx.x - row * sh.cols;
+    const int cnt = row < sh.rpb ? rows_of(p.len, row, sh.rpb) : 0;
+    const int64_t at = p.off + (int64_t)row * sh.channels + col * V;
+    const int64_t pitch = (int64_t)sh.rpb * sh.channels;
+    typename P::Raw hx[kHeld], hy[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        if (i < cnt) {
+            hx[i] = P::raw(x + at + i * pitch);
+            hy[i] = P::raw(dy + at + i * pitch);
+        }
+    }
+    Affine<V> f;
+    if (row < sh.rpb) {
         f.load(stats + (size_t)blockIdx.y * sh.groups, weight, bias, col * V, sh.cpg);
+        float a[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = q[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            if (i < cnt) {
+                float v[V], g[V];
+                P::open(hx[i], v);
+                P::open(hy[i], g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float h;
+                    const float dz =
+                        grad_h<kAct>(v[j], g[j], f.mean[j], f.rstd[j], f.w[j], f.b[j], &h);
+                    a[j] += dz;
+                    q[j] = fmaf(dz, h, q[j]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            s_sum[row * sh.channels + col * V + j] = make_float2(a[j], q[j]);
+    }
+    channel_sums(sh, weight, s_sum, nullptr, s_part);
+    cluster_meet();
+    join_means([&](int b, int g) { return of_block(s_part + g, b); }, sh, s_means);
+    // the channels' sums over the cluster: each block takes a share of them
+    for (int c = blockIdx.x * kThreads + threadIdx.x; c < sh.channels; c += sh.blocks * kThreads) {
+        float a = 0.0f, q = 0.0f;
+        for (int b = 0; b < sh.blocks; ++b) {
+            const float2 u = of_block(s_sum + c, b);
+            a += u.x;
+            q += u.y;
+        }
+        if (gridDim.y > 1) {
+            total[(size_t)blockIdx.y * sh.channels + c] = make_float2(a, q);
+        } else {
+            if (grad_bias) grad_bias[c] = a;
+            if (grad_weight) grad_weight[c] = q;
+        }
+    }
+    if (row < sh.rpb && dx) {
         float m1[V], m2[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float2 u = means[(size_t)blockIdx.y * sh.groups + (col * V + j) / sh.cpg];
+            const float2 u = s_means[(col * V + j) / sh.cpg];
             m1[j] = u.x;
             m2[j] = u.y;
         }
-#pragma unroll 2
-        for (int i = 0; i < cnt; ++i) {
-            const int64_t at = off + (row + (int64_t)i * sh.rpb) * sh.channels + col * V;
-            float v[V], g[V];
-            Pack<T, V>::load(x + at, v);
-            Pack<T, V>::load(dy + at, g);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float h = (v[j] - f.mean[j]) * f.rstd[j];
-                const float dz = activate_grad(fmaf(h, f.w[j], f.b[j]), g[j], act);
-                v[j] = f.rstd[j] * (fmaf(dz, f.w[j], -m1[j]) - h * m2[j]);
+        for (int i = 0; i < kHeld; ++i) {
+            if (i < cnt) {
+                float v[V], g[V];
+                P::open(hx[i], v);
+                P::open(hy[i], g);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float h;
+                    const float dz =
+                        grad_h<kAct>(v[j], g[j], f.mean[j], f.rstd[j], f.w[j], f.b[j], &h);
+                    v[j] = f.rstd[j] * (fmaf(dz, f.w[j], -m1[j]) - h * m2[j]);
+                }
+                P::store(dx + at + i * pitch, v);
             }
-            Pack<T, V>::store(dx + at, v);
         }
     }
+    cluster_meet();
 }
 
 // ----------------------------------------------------------------- plans --
-Shape shape_of(int64_t images, int64_t pixels, int channels, int groups, int v) {
-    Shape s;
+// Shared memory of the reductions: an entry of two floats per thread and
+// channel of a vector, and the per-group values.
+size_t smem_bytes(const Shape& s, int v) { return (size_t)8 * (s.rpb * s.cols * v + 2 * s.groups); }
+constexpr size_t kSmemMost = 8 * 3 * 4096;   // 4096 channels in as many groups
+constexpr int64_t kL2Share = 128 << 20;      // bytes of images in flight that the L2 keeps (in part)
+
+Shape shape_of(int64_t pixels, int channels, int groups, int v) {
+    Shape s{};
     s.pixels = pixels;
     s.channels = channels;
     s.groups = groups;
     s.cpg = channels / groups;
     s.cols = channels / v;
     s.rpb = s.cols < kThreads ? kThreads / s.cols : 1;
-    // about 1216 blocks (eight per SM) over the images, none with less than
-    // eight pixels per thread
-    int64_t per = ceil_div(images * pixels, 1216);
-    const int64_t least = (int64_t)s.rpb * 8;
-    per = ceil_div(per < least ? least : per, s.rpb) * s.rpb;
-    if (ceil_div(pixels, per) > kMaxChunks) per = ceil_div(ceil_div(pixels, kMaxChunks), s.rpb) * s.rpb;
-    s.chunk = per;
-    s.chunks = (int)ceil_div(pixels, per);
     return s;
+}
+
+// Whether a cluster holds an image, and its blocks: the fewest pixels per
+// thread that eight blocks give.
+bool small_shape(Shape* s) {
+    if (s->cols > kThreads || s->pixels > (int64_t)kMaxCluster * s->rpb * kHeld) return false;
+    int n = 1;
+    while (n < kMaxCluster && (int64_t)n * s->rpb < s->pixels) n *= 2;
+    while ((n - 1) * ceil_div(s->pixels, n) >= s->pixels) n /= 2;   // no block without a pixel
+    s->blocks = n;
+    s->chunk = ceil_div(s->pixels, n);
+    return s->chunk <= (int64_t)s->rpb * kHeld;
+}
+
+// Two launches: as many images a round as the L2 keeps, in equal rounds ...
+int64_t images_at_once(int64_t images, int64_t pixels, int channels, int elem, bool back) {
+    const int64_t fit = kL2Share / (pixels * channels * elem * (back ? 2 : 1));
+    return ceil_div(images, ceil_div(images, fit < 1 ? 1 : fit < images ? fit : images));
+}
+// ... over which one wave of resident blocks lies, none with less than four
+// pixels per thread.
+void large_shape(Shape* s, int64_t at_once, int v, bool back, int n_sms) {
+    int per_sm = (int)(220 * 1024 / (smem_bytes(*s, v) + 1024));
+    per_sm = per_sm < blocks_per_sm(v, back) ? per_sm : blocks_per_sm(v, back);
+    const int64_t blocks = (int64_t)n_sms * per_sm;
+    const int64_t each = blocks / at_once > 0 ? blocks / at_once : 1;
+    int64_t per = ceil_div(s->pixels, each);
+    const int64_t least = (int64_t)s->rpb * 4;
+    per = ceil_div(per < least ? least : per, s->rpb) * s->rpb;
+    s->chunk = per;
+    s->blocks = (int)ceil_div(s->pixels, per);
 }
 
 struct Space {
-    float2 *part, *sums, *means;
+    float2 *part, *total, *image_total;
 };
-Space carve(Carve& w, int64_t images, int chunks, int channels, int groups) {
-    Space s;
-    s.part = w.take<float2>((size_t)images * chunks * channels);
-    s.sums = w.take<float2>((size_t)images * channels);
-    s.means = w.take<float2>((size_t)images * groups);
-    return s;
+// `at_once` images of `blocks` blocks each
+Space carve(Carve& w, int64_t images, int64_t at_once, int64_t blocks, int channels, int groups) {
+    Space p;
+    p.part = w.take<float2>((size_t)at_once * blocks * groups);
+    p.total = w.take<float2>((size_t)at_once * blocks * channels);
+    p.image_total = w.take<float2>((size_t)images * channels);
+    return p;
 }
 
-template <typename T, int V>
-cudaError_t forward(const NormCall& c, const Shape& sh, const Space& w, cudaStream_t s) {
-    const dim3 grid(sh.chunks, (unsigned)c.images);
-    cudaError_t e = launch_pdl(k_norm_stats<T, V>, grid, dim3(kThreads), 0, s, (const T*)c.x, sh,
-                               w.part);
-    if (e == cudaSuccess)
-        e = launch_pdl(k_norm_finish, dim3((unsigned)ceil_div(sh.groups, kThreads / 32),
-                                           (unsigned)c.images),
-                       dim3(kThreads), 0, s, (const float2*)w.part, sh, c.eps, (float2*)c.stats);
-    if (e == cudaSuccess)
-        e = launch_pdl(k_norm_apply<T, V>, grid, dim3(kThreads), 0, s, (const T*)c.x, sh,
-                       (const float2*)c.stats, c.weight, c.bias, c.act, (T*)c.out);
-    return e;
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), const Shape& sh, int64_t images, size_t smem,
+                           cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sh.blocks, (unsigned)images);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)sh.blocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-template <typename T, int V>
-cudaError_t backward(const NormCall& c, const Shape& sh, const Space& w, cudaStream_t s) {
-    const dim3 grid(sh.chunks, (unsigned)c.images);
-    cudaError_t e = launch_pdl(k_norm_back_sums<T, V>, grid, dim3(kThreads), 0, s, (const T*)c.x,
-                               (const T*)c.grad_y, sh, (const float2*)c.stats, c.weight, c.bias,
-                               c.act, w.part);
-    if (e == cudaSuccess)
-        e = launch_pdl(k_norm_back_chunks, dim3((unsigned)ceil_div(sh.channels, kThreads / 32),
-                                                (unsigned)c.images),
-                       dim3(kThreads), 0, s, (const float2*)w.part, sh, w.sums);
-    if (e == cudaSuccess) {
-        const int64_t work = sh.channels + c.images * sh.groups;
-        e = launch_pdl(k_norm_back_finish, dim3((unsigned)ceil_div(work, kThreads)), dim3(kThreads),
-                       0, s, (const float2*)w.sums, sh, (int)c.images, c.weight, c.grad_weight,
-                       c.grad_bias, w.means);
-    }
-    if (e == cudaSuccess && c.out)
-        e = launch_pdl(k_norm_back_apply<T, V>, grid, dim3(kThreads), 0, s, (const T*)c.x,
-                       (const T*)c.grad_y, sh, (const float2*)c.stats, (const float2*)w.means,
-                       c.weight, c.bias, c.act, (T*)c.out);
-    return e;
-}
-
-template <typename T>
-cudaError_t run(const NormCall& c, void* ws, bool back, cudaStream_t s) {
-    constexpr int V = VecOf<T>::n;
-    const bool wide = c.channels % V == 0 && aligned16(c.x) && aligned16(c.out) &&
-                      aligned16(c.grad_y);
-    const Shape sh = shape_of(c.images, c.pixels, c.channels, c.groups, wide ? V : 1);
+template <typename T, int V, int kAct>
+cudaError_t forward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
+    Shape sh = shape_of(c.pixels, c.channels, c.groups, V);
+    if (small_shape(&sh))
+        return launch_cluster(k_norm_small<T, V, kAct>, sh, c.images, smem_bytes(sh, V), s,
+                              (const T*)c.x, sh, c.weight, c.bias, c.eps, (T*)c.out,
+                              (float2*)c.stats);
+    const int64_t at_once = images_at_once(c.images, c.pixels, c.channels, sizeof(T), false);
+    large_shape(&sh, at_once, V, false, n_sms);
     Carve cv{static_cast<unsigned char*>(ws)};
-    const Space w = carve(cv, c.images, sh.chunks, c.channels, c.groups);
-    if (wide) return back ? backward<T, V>(c, sh, w, s) : forward<T, V>(c, sh, w, s);
-    return back ? backward<T, 1>(c, sh, w, s) : forward<T, 1>(c, sh, w, s);
+    const Space w = carve(cv, c.images, at_once, sh.blocks, c.channels, c.groups);
+    cudaError_t e = cudaSuccess;
+    for (int64_t i = 0; i < c.images && e == cudaSuccess; i += at_once) {
+        const int64_t n = c.images - i < at_once ? c.images - i : at_once;
+        const dim3 grid((unsigned)sh.blocks, (unsigned)n);
+        e = launch_pdl(k_norm_stats<T, V>, grid, dim3(kThreads), smem_bytes(sh, V), s,
+                       (const T*)c.x, sh, i, w.part);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_norm_apply<T, V, kAct>, grid, dim3(kThreads), (size_t)8 * sh.groups,
+                           s, (const T*)c.x, sh, i, (const float2*)w.part, c.weight, c.bias, c.eps,
+                           (T*)c.out, (float2*)c.stats);
+    }
+    return e;
+}
+
+cudaError_t params(const NormCall& c, const float2* total, int64_t rows, cudaStream_t s) {
+    if (!c.grad_weight && !c.grad_bias) return cudaSuccess;
+    return launch_pdl(k_norm_back_params, dim3((unsigned)ceil_div(c.channels, kThreads / 32)),
+                      dim3(kThreads), 0, s, total, rows, c.channels, c.grad_weight, c.grad_bias);
+}
+
+template <typename T, int V, int kAct>
+cudaError_t backward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
+    Shape sh = shape_of(c.pixels, c.channels, c.groups, V);
+    Carve cv{static_cast<unsigned char*>(ws)};
+    if (small_shape(&sh)) {
+        const Space w = carve(cv, c.images, 0, 0, c.channels, c.groups);
+        const cudaError_t e = launch_cluster(
+            k_norm_small_back<T, V, kAct>, sh, c.images, smem_bytes(sh, V), s, (const T*)c.x,
+            (const T*)c.grad_y, sh, (const float2*)c.stats, c.weight, c.bias, (T*)c.out,
+            c.grad_weight, c.grad_bias, w.image_total);
+        return e != cudaSuccess || c.images == 1 ? e : params(c, w.image_total, c.images, s);
+    }
+    const int64_t at_once = images_at_once(c.images, c.pixels, c.channels, sizeof(T), true);
+    large_shape(&sh, at_once, V, true, n_sms);
+    const Space w = carve(cv, c.images, at_once, sh.blocks, c.channels, c.groups);
+    cudaError_t e = cudaSuccess;
+    for (int64_t i = 0; i < c.images && e == cudaSuccess; i += at_once) {
+        const int64_t n = c.images - i < at_once ? c.images - i : at_once;
+        const dim3 grid((unsigned)sh.blocks, (unsigned)n);
+        e = launch_pdl(k_norm_back_sums<T, V, kAct>, grid, dim3(kThreads), smem_bytes(sh, V), s,
+                       (const T*)c.x, (const T*)c.grad_y, sh, i, (const float2*)c.stats, c.weight,
+                       c.bias, w.part, w.total);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_norm_back_apply<T, V, kAct>, grid, dim3(kThreads),
+                           (size_t)8 * sh.groups, s, (const T*)c.x, (const T*)c.grad_y, sh, i,
+                           (const float2*)c.stats, (const float2*)w.part, c.weight, c.bias,
+                           (T*)c.out, (const float2*)w.total, (int)c.images, w.image_total,
+                           c.grad_weight, c.grad_bias);
+    }
+    return e != cudaSuccess || c.images == 1 ? e : params(c, w.image_total, c.images, s);
+}
+
+template <typename T, int V>
+cudaError_t by_act(const NormCall& c, bool back, void* ws, int n_sms, cudaStream_t s) {
+    switch (c.act) {
+        case kActSilu:
+            return back ? backward<T, V, kActSilu>(c, ws, n_sms, s)
+                        : forward<T, V, kActSilu>(c, ws, n_sms, s);
+        case kActRelu:
+            return back ? backward<T, V, kActRelu>(c, ws, n_sms, s)
+                        : forward<T, V, kActRelu>(c, ws, n_sms, s);
+        default:
+            return back ? backward<T, V, kActNone>(c, ws, n_sms, s)
+                        : forward<T, V, kActNone>(c, ws, n_sms, s);
+    }
+}
+
+cudaError_t run(const NormCall& c, bool back, void* ws, int n_sms, cudaStream_t s) {
+    const int v = c.dtype == kF32 ? 4 : 8;
+    const bool wide = c.channels % v == 0 && aligned16(c.x) && aligned16(c.out) &&
+                      aligned16(c.grad_y);
+    if (c.dtype == kF32)
+        return wide ? by_act<float, 4>(c, back, ws, n_sms, s)
+                    : by_act<float, 1>(c, back, ws, n_sms, s);
+    return wide ? by_act<__nv_bfloat16, 8>(c, back, ws, n_sms, s)
+                : by_act<__nv_bfloat16, 1>(c, back, ws, n_sms, s);
+}
+
+template <typename T, int V, int kAct>
+cudaError_t prepare_one() {
+    const auto most = [](const void* k) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    };
+    cudaError_t e = most((const void*)k_norm_stats<T, V>);
+    if (e == cudaSuccess) e = most((const void*)k_norm_apply<T, V, kAct>);
+    if (e == cudaSuccess) e = most((const void*)k_norm_back_sums<T, V, kAct>);
+    if (e == cudaSuccess) e = most((const void*)k_norm_back_apply<T, V, kAct>);
+    if (e == cudaSuccess) e = most((const void*)k_norm_small<T, V, kAct>);
+    if (e == cudaSuccess) e = most((const void*)k_norm_small_back<T, V, kAct>);
+    return e;
+}
+template <typename T, int V>
+cudaError_t prepare_acts() {
+    cudaError_t e = prepare_one<T, V, kActNone>();
+    if (e == cudaSuccess) e = prepare_one<T, V, kActSilu>();
+    if (e == cudaSuccess) e = prepare_one<T, V, kActRelu>();
+    return e;
 }
 
 }  // namespace
 
 size_t group_norm_workspace(int64_t images, int64_t pixels, int32_t channels, int32_t groups) {
     if (images == 0 || pixels == 0) return 0;
-    int chunks = 0;
-    for (int v : {1, 4, 8})
-        if (channels % v == 0) {
-            const int k = shape_of(images, pixels, channels, groups, v).chunks;
-            chunks = k > chunks ? k : chunks;
+    // the most blocks of a round in any form: one wave of the largest part, or
+    // one per image; and no more than the pixels
+    int64_t blocks = 0;
+    for (int elem : {2, 4})
+        for (bool back : {false, true}) {
+            const int64_t n = images_at_once(images, pixels, channels, elem, back);
+            const int64_t each = kMostBlocks / n > 0 ? kMostBlocks / n : 1;
+            const int64_t all = n * (each < pixels ? each : pixels);
+            blocks = all > blocks ? all : blocks;
         }
     Carve cv{nullptr};
-    carve(cv, images, chunks, channels, groups);
+    carve(cv, images, 1, blocks, channels, groups);
     return cv.used;
 }
 
-cudaError_t launch_group_norm_forward(const NormCall& c, void* ws, int, cudaStream_t s) {
-    if (c.images == 0) return cudaSuccess;
-    if (c.pixels == 0) {   // the statistics of nothing: mean 0, variance 0
-        Shape sh = shape_of(1, 1, c.channels, c.groups, 1);
-        sh.pixels = sh.chunks = 0;
-        return launch_pdl(k_norm_finish, dim3((unsigned)ceil_div(sh.groups, kThreads / 32),
-                                              (unsigned)c.images),
-                          dim3(kThreads), 0, s, (const float2*)nullptr, sh, c.eps,
-                          (float2*)c.stats);
-    }
-    return c.dtype == kF32 ? run<float>(c, ws, false, s) : run<__nv_bfloat16>(c, ws, false, s);
+cudaError_t prepare_group_norm() {
+    cudaError_t e = prepare_acts<float, 4>();
+    if (e == cudaSuccess) e = prepare_acts<float, 1>();
+    if (e == cudaSuccess) e = prepare_acts<__nv_bfloat16, 8>();
+    if (e == cudaSuccess) e = prepare_acts<__nv_bfloat16, 1>();
+    return e;
 }
 
-cudaError_t launch_group_norm_backward(const NormCall& c, void* ws, int, cudaStream_t s) {
+cudaError_t launch_group_norm_forward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
+    const int64_t n = c.images * c.groups;
+    if (c.images == 0) return cudaSuccess;
+    if (c.pixels == 0) {
+        k_norm_empty<<<(unsigned)ceil_div(n, kThreads), kThreads, 0, s>>>((float2*)c.stats, n, c.eps);
+        return cudaGetLastError();
+    }
+    return run(c, false, ws, n_sms, s);
+}
+
+cudaError_t launch_group_norm_backward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
     if (c.images == 0 || c.pixels == 0) {
         for (float* g : {c.grad_weight, c.grad_bias})
             if (g) {
@@ -489,7 +987,7 @@ cudaError_t launch_group_norm_backward(const NormCall& c, void* ws, int, cudaStr
             }
         return cudaSuccess;
     }
-    return c.dtype == kF32 ? run<float>(c, ws, true, s) : run<__nv_bfloat16>(c, ws, true, s);
+    return run(c, true, ws, n_sms, s);
 }
 
 }  // namespace pulsar

@@ -27,13 +27,6 @@
 namespace pulsar {
 namespace {
 
-// The calls' launches form a chain in which each needs all of the one before:
-// a kernel lets the next one's blocks take free SMs and set up at once, and
-// that waits in pdl_begin() for this one's results.
-__device__ __forceinline__ void pdl_next() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 constexpr int kThreads = 256;
 constexpr int kPanel = 64;      // columns of a panel: 128 bytes of halves
 constexpr int kBlock = 128;     // rows are padded to it
