@@ -71,17 +71,9 @@ k_embed_rows(const T* __restrict__ table, const I* __restrict__ tokens, int64_t 
 }
 
 // ------------------------------------------------------------------ sort --
-// Stable LSD radix sort of (key, position) pairs.  A pass is two launches:
-// every block counts the digits of its contiguous chunk; then every block
-// sums the count matrix to its own offsets and scatters its chunk in order.
-// Keys are the tokens, `rows` standing for a token that contributes nothing.
-constexpr int kSortThreads = 512;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 16;                              // per thread and sub-tile
-constexpr int kSortTile = kSortThreads * kSortItems;        // 8192
-constexpr int kMaxDigit = 8;                                // bits
-constexpr int kMaxBins = 1 << kMaxDigit;
-
+// (key, position) pairs in the order of the keys, equal keys in the order of
+// the positions.  Keys are the tokens, `rows` standing for a token that
+// contributes nothing.
 template <typename I>
 __device__ __forceinline__ uint32_t token_key(I t, uint32_t rows, bool* bad) {
     const int64_t v = (int64_t)t;
@@ -89,12 +81,71 @@ __device__ __forceinline__ uint32_t token_key(I t, uint32_t rows, bool* bad) {
     return v >= 0 && v < (int64_t)rows ? (uint32_t)v : rows;
 }
 
+// The table rows' marks (set by the reduction where a row is written) start
+// at zero: the grid's threads clear them.
+__device__ __forceinline__ void clear_marks(unsigned char* __restrict__ marks, uint32_t rows) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(marks);   // (padded to whole words)
+    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < (rows + 3) / 4;
+         i += gridDim.x * blockDim.x)
+        w[i] = 0u;
+}
+
+// Few tokens: one launch, a token's place is the number of keys before it,
+// counted against all of them in shared memory.
+constexpr int kRankMost = 4096;
+
+template <typename I>
+__global__ void __launch_bounds__(kThreads)
+k_sort_rank(const I* __restrict__ tokens, uint32_t n, uint32_t rows,
+            uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+            unsigned char* __restrict__ marks, LearnState* st) {
+    pdl_begin();
+    __shared__ __align__(16) uint32_t key[kRankMost];
+    bool bad = false;
+    const uint32_t padded = (n + 3) / 4 * 4;
+    for (uint32_t i = threadIdx.x; i < padded; i += kThreads)
+        key[i] = i < n ? token_key(tokens[i], rows, &bad) : 0xffffffffu;
+    if (bad) atomicOr(&st->error, kErrIndex);
+    clear_marks(marks, rows);
+    __syncthreads();
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= n) return;
+    const uint32_t k = key[i];
+    uint32_t at = 0;
+    // keys at or below its own before it, keys below its own after it
+    uint32_t j = 0;
+#pragma unroll 4
+    for (; j + 4 <= i; j += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(key + j);
+        at += (u.x <= k) + (u.y <= k) + (u.z <= k) + (u.w <= k);
+    }
+    for (uint32_t e = j; e < min(j + 4, n); ++e) at += e < i ? key[e] <= k : key[e] < k;
+#pragma unroll 4
+    for (j += 4; j < padded; j += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(key + j);
+        at += (u.x < k) + (u.y < k) + (u.z < k) + (u.w < k);
+    }
+    keys_out[at] = k;
+    pos_out[at] = i;
+}
+
+// More: a stable LSD radix sort.  A pass is two launches: every block counts
+// the digits of its contiguous chunk; then every block sums the count matrix
+// to its own offsets and scatters its chunk in order.
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortItems = 16;                              // most per thread at a time
+constexpr int kSortTile = kSortThreads * kSortItems;        // 8192
+constexpr int kMaxDigit = 8;                                // bits
+constexpr int kMaxBins = 1 << kMaxDigit;
+constexpr int kWarpBins = kMaxBins / kSortWarps;            // digits a warp sums
+
 // counts[digit][block] of one pass; `keys` NULL: from the tokens.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
 k_sort_count(const I* __restrict__ tokens, const uint32_t* __restrict__ keys, uint32_t n,
              uint32_t rows, uint32_t chunk, int shift, int bits, uint32_t* __restrict__ counts,
-             LearnState* st) {
+             unsigned char* __restrict__ marks, LearnState* st) {
     pdl_begin();
     __shared__ uint32_t h[kSortWarps][kMaxBins];
     const int bins = 1 << bits, warp = threadIdx.x >> 5;
@@ -102,11 +153,13 @@ k_sort_count(const I* __restrict__ tokens, const uint32_t* __restrict__ keys, ui
     __syncthreads();
     const uint32_t lo = blockIdx.x * chunk, hi = min(n, lo + chunk);
     bool bad = false;
+#pragma unroll 4
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kSortThreads) {
         const uint32_t k = keys ? keys[i] : token_key(tokens[i], rows, &bad);
         atomicAdd(&h[warp][(k >> shift) & (bins - 1)], 1u);
     }
     if (bad) atomicOr(&st->error, kErrIndex);
+    if (!keys) clear_marks(marks, rows);
     __syncthreads();
     for (int d = threadIdx.x; d < bins; d += kSortThreads) {
         uint32_t s = 0;
@@ -128,68 +181,81 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
     __shared__ uint32_t wh[kSortWarps][kMaxBins];     // per warp: count, then offset
     const int bins = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t nb = gridDim.x, b = blockIdx.x;
-    for (int d = warp; d < bins; d += kSortWarps) {
-        uint32_t all = 0, before = 0;
+    {   // a warp's digits together, so that their counts load together
+        uint32_t all[kWarpBins], before[kWarpBins];
+#pragma unroll
+        for (int e = 0; e < kWarpBins; ++e) all[e] = before[e] = 0u;
         for (uint32_t q = lane; q < nb; q += 32) {
-            const uint32_t c = counts[(size_t)d * nb + q];
-            all += c;
-            before += q < b ? c : 0u;
+#pragma unroll
+            for (int e = 0; e < kWarpBins; ++e) {
+                const int d = warp + e * kSortWarps;
+                const uint32_t c = d < bins ? counts[(size_t)d * nb + q] : 0u;
+                all[e] += c;
+                before[e] += q < b ? c : 0u;
+            }
         }
-        all = __reduce_add_sync(0xffffffffu, all);
-        before = __reduce_add_sync(0xffffffffu, before);
-        if (lane == 0) {
-            total[d] = all;
-            base[d] = before;
+#pragma unroll
+        for (int e = 0; e < kWarpBins; ++e) {
+            const int d = warp + e * kSortWarps;
+            const uint32_t s = __reduce_add_sync(0xffffffffu, all[e]);
+            const uint32_t f = __reduce_add_sync(0xffffffffu, before[e]);
+            if (lane == 0) {
+                total[d] = s;
+                base[d] = f;
+            }
         }
     }
     __syncthreads();
     if (warp == 0) {   // exclusive scan of the digit totals
-        uint32_t run = 0;
-        for (int d0 = 0; d0 < bins; d0 += 32) {
-            const uint32_t c = d0 + lane < bins ? total[d0 + lane] : 0u;
-            uint32_t s = c;
+        uint32_t c[kMaxBins / 32], sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t up = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += up;
-            }
-            if (d0 + lane < bins) base[d0 + lane] += run + s - c;
-            run += __shfl_sync(0xffffffffu, s, 31);
+        for (int e = 0; e < kMaxBins / 32; ++e) sum += c[e] = total[lane * (kMaxBins / 32) + e];
+        uint32_t s = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += up;
+        }
+        s -= sum;
+#pragma unroll
+        for (int e = 0; e < kMaxBins / 32; ++e) {
+            base[lane * (kMaxBins / 32) + e] += s;
+            s += c[e];
         }
     }
     const uint32_t lo = b * chunk, hi = min(n, lo + chunk);
     bool bad = false;
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
+        // the warps share the tile's items evenly, each a contiguous run of 32 x rounds
+        const int rounds = (int)((min(hi - t0, (uint32_t)kSortTile) + kSortThreads - 1) / kSortThreads);
         for (int e = threadIdx.x; e < kSortWarps * kMaxBins; e += kSortThreads)
             (&wh[0][0])[e] = 0u;
-        __syncthreads();
         uint32_t key[kSortItems], val[kSortItems], rank[kSortItems];
-        const uint32_t i0 = t0 + warp * (32 * kSortItems) + lane;
+        const uint32_t i0 = t0 + warp * (32 * rounds) + lane;
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
             const uint32_t i = i0 + 32 * j;
             key[j] = 0;
             val[j] = i;
-            if (i < hi) {
+            if (j < rounds && i < hi) {
                 key[j] = keys ? keys[i] : token_key(tokens[i], rows, &bad);
                 if (pos) val[j] = pos[i];
             }
         }
-        // rank inside the warp's 512 items, in their order
+        __syncthreads();
+        // rank inside the warp's items, in their order
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
-            const bool on = i0 + 32 * j < hi;
-            const uint32_t d = (key[j] >> shift) & (bins - 1);
-            uint32_t same = __ballot_sync(0xffffffffu, on);
-            for (int q = 0; q < bits; ++q) {
-                const uint32_t m = __ballot_sync(0xffffffffu, (d >> q) & 1u);
-                same &= (d >> q) & 1u ? m : ~m;
+            if (j < rounds) {
+                const bool on = i0 + 32 * j < hi;
+                const uint32_t d = (key[j] >> shift) & (bins - 1);
+                const uint32_t same = __match_any_sync(0xffffffffu, on ? d : kMaxBins);
+                const uint32_t before = __popc(same & ((1u << lane) - 1u));
+                rank[j] = on ? wh[warp][d] + before : 0u;
+                __syncwarp();
+                if (on && before == 0) wh[warp][d] += __popc(same);
+                __syncwarp();
             }
-            const uint32_t before = __popc(same & ((1u << lane) - 1u));
-            rank[j] = on ? wh[warp][d] + before : 0u;
-            __syncwarp();
-            if (on && before == 0) wh[warp][d] += __popc(same);
-            __syncwarp();
         }
         __syncthreads();
         for (int d = threadIdx.x; d < bins; d += kSortThreads) {
@@ -205,7 +271,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
-            if (i0 + 32 * j < hi) {
+            if (j < rounds && i0 + 32 * j < hi) {
                 const uint32_t at = wh[warp][(key[j] >> shift) & (bins - 1)] + rank[j];
                 keys_out[at] = key[j];
                 pos_out[at] = val[j];
@@ -216,23 +282,8 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
 }
 
 // ------------------------------------------------------------- reduction --
-// First sorted position whose key is at least `key`.
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ keys, uint32_t n,
-                                                uint32_t key) {
-    uint32_t lo = 0, len = n;
-    while (len > 0) {
-        const uint32_t half = len >> 1;
-        if (keys[lo + half] < key) {
-            lo += half + 1;
-            len -= half + 1;
-        } else {
-            len = half;
-        }
-    }
-    return lo;
-}
-
-constexpr int kAhead = 8;   // gathered rows in flight per thread
+constexpr int kAhead = 8;        // gathered rows in flight per thread
+constexpr int kMostQ = 32;       // positions per slot
 
 // A block's tile is S slots x q sorted positions, S = kThreads / L; the L
 // lanes of a slot own columns (vectors of V) and walk the slot's positions.
@@ -240,73 +291,65 @@ constexpr int kAhead = 8;   // gathered rows in flight per thread
 // parts of runs that do not: `head`, of a run that began before the slot (and
 // may pass through it), and `tail`, of a run that begins in it and goes on.
 // The slot where a run begins joins its parts in order; what leaves the tile
-// goes to tile_head / tile_tail for k_embed_join.
+// goes to tile_head / tile_tail for k_embed_join.  Where a row is written its
+// mark is set.
 enum : int { kHasHead = 1, kThrough = 2, kHasTail = 4 };
 
+constexpr int reduce_blocks_per_sm(int v) { return v == 8 ? 3 : 4; }
+
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, reduce_blocks_per_sm(V))
 k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
                const uint32_t* __restrict__ pos, uint32_t n, uint32_t rows, int nv, int lshift,
-               int q, uint32_t tiles, float scale, T* __restrict__ out, float* __restrict__ tile_head,
-               float* __restrict__ tile_tail, int* __restrict__ tile_flag) {
+               int q, float scale, T* __restrict__ out, float* __restrict__ tile_head,
+               float* __restrict__ tile_tail, int* __restrict__ tile_flag,
+               unsigned char* __restrict__ marks) {
     pdl_begin();
+    extern __shared__ __align__(16) unsigned char smem[];
     const int L = 1 << lshift, S = kThreads >> lshift;
     const int lane = threadIdx.x & (L - 1), slot = threadIdx.x >> lshift;
     const int v = blockIdx.y * L + lane;
-    if (blockIdx.x >= tiles) {
-        // ---- the rows without a token: 32 rows per warp, one search per lane
-        const int wl = threadIdx.x & 31;
-        const uint32_t r0 = ((blockIdx.x - tiles) * (kThreads / 32) + (threadIdx.x >> 5)) * 32u;
-        if (r0 >= rows) return;
-        bool empty = false;
-        if (r0 + wl < rows) {
-            const uint32_t at = lower_bound(keys, n, r0 + wl);
-            empty = at >= n || keys[at] != r0 + wl;
-        }
-        uint32_t todo = __ballot_sync(0xffffffffu, empty);
-        const float zero[V] = {};
-        const int c1 = min(nv, (int)(blockIdx.y + 1) * L);
-        while (todo) {
-            const uint32_t r = r0 + __ffs(todo) - 1;
-            todo &= todo - 1;
-            for (int c = blockIdx.y * L + wl; c < c1; c += 32)
-                Pack<T, V>::store(out + ((size_t)r * nv + c) * V, zero);
-        }
-        return;
+    float* s_head = reinterpret_cast<float*>(smem);   // [kThreads][V]
+    float* s_tail = s_head + kThreads * V;
+    int* s_flag = reinterpret_cast<int*>(s_tail + kThreads * V);   // [S]
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(s_flag + S);     // [S q + 2]: with both neighbours
+    uint32_t* s_pos = s_key + S * q + 2;                           // [S q]
+    const uint32_t t0 = blockIdx.x * (uint32_t)(S * q), len = min((uint32_t)(S * q), n - t0);
+    for (uint32_t i = threadIdx.x; i < len + 2; i += kThreads) {
+        // (a key that is no token's beyond both ends)
+        s_key[i] = t0 + i == 0 || t0 + i - 1 >= n ? 0xffffffffu : keys[t0 + i - 1];
+        if (i < len) s_pos[i] = pos[t0 + i];
     }
-    __shared__ float s_head[kThreads * V], s_tail[kThreads * V];
-    __shared__ int s_flag[kThreads];
-    __shared__ uint32_t s_key[kThreads];   // key of the slot's last position
-    const uint32_t p0 = min(n, (blockIdx.x * S + slot) * (uint32_t)q), p1 = min(n, p0 + q);
+    __syncthreads();
+    const uint32_t* key = s_key + 1;   // key[-1], key[len]: the neighbours'
+    const int p0 = min((int)len, slot * q), p1 = min((int)len, p0 + q);
     const bool col = v < nv;
     int flag = 0;
-    uint32_t cur = rows;
     auto emit = [&](uint32_t row, const float (&a)[V]) {
-        if (!col || row >= rows) return;
+        if (row >= rows) return;
+        if (v == 0) marks[row] = 1;
+        if (!col) return;
         float y[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) y[j] = a[j] * scale;
         Pack<T, V>::store(out + ((size_t)row * nv + v) * V, y);
     };
+    uint32_t cur = rows;
     if (p0 < p1) {
-        cur = keys[p0];
-        bool head = p0 > 0 && keys[p0 - 1] == cur;   // the current run began before the slot
+        cur = key[p0];
+        bool head = key[p0 - 1] == cur;   // the current run began before the slot
         float acc[V] = {};
-        for (uint32_t p = p0; p < p1; p += kAhead) {
-            uint32_t k[kAhead];
-            float x[kAhead][V];
+        for (int p = p0; p < p1; p += kAhead) {
+            typename Pack<T, V>::Raw x[kAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                k[u] = p + u < p1 ? keys[p + u] : rows;
-#pragma unroll
-                for (int j = 0; j < V; ++j) x[u][j] = 0.0f;
-                if (k[u] < rows && col)
-                    Pack<T, V>::load(grad + ((size_t)pos[p + u] * nv + v) * V, x[u]);
-            }
+            for (int u = 0; u < kAhead; ++u)
+                if (p + u < p1 && key[p + u] < rows && col)
+                    x[u] = Pack<T, V>::raw(grad + ((size_t)s_pos[p + u] * nv + v) * V);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (p + u >= p1) break;
-                if (k[u] != cur) {
+                const uint32_t k = key[p + u];
+                if (k != cur) {
                     if (head) {
                         flag |= kHasHead;
 #pragma unroll
@@ -317,13 +360,17 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
                     }
 #pragma unroll
                     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-                    cur = k[u];
+                    cur = k;
                 }
+                if (k < rows && col) {
+                    float f[V];
+                    Pack<T, V>::open(x[u], f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] += x[u][j];
+                    for (int j = 0; j < V; ++j) acc[j] += f[j];
+                }
             }
         }
-        const bool goes_on = p1 < n && keys[p1] == cur;
+        const bool goes_on = key[p1] == cur;
         if (head) {
             flag |= kHasHead | (goes_on ? kThrough : 0);
 #pragma unroll
@@ -336,10 +383,7 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
             emit(cur, acc);
         }
     }
-    if (lane == 0) {
-        s_flag[slot] = flag;
-        s_key[slot] = cur;
-    }
+    if (lane == 0) s_flag[slot] = flag;
     __syncthreads();
     // ---- join the parts of the runs that begin in this slot, and (slot 0)
     // of the run that began before the tile
@@ -369,13 +413,11 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
         float a[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) a[j] = s_tail[threadIdx.x * V + j];
-        const uint32_t key = s_key[slot];
-        leaves = follow(a, slot + 1);
         // at the tile's end the run goes on if the next tile begins with its key
-        const uint32_t end = min(n, (blockIdx.x + 1) * (uint32_t)(S * q));
-        if (leaves) leaves = end < n && keys[end] == key;
+        leaves = follow(a, slot + 1) && key[len] == cur;
+        if (leaves && v == 0 && cur < rows) marks[cur] = 1;   // k_embed_join writes it
         if (!leaves) {
-            emit(key, a);
+            emit(cur, a);
         } else if (col) {
 #pragma unroll
             for (int j = 0; j < V; ++j) tile_tail[at + j] = a[j];
@@ -387,25 +429,59 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
 }
 
 // The runs that leave the tile they begin in: one block per tile (and column
-// block), its slots striding over the tiles the run covers, joined in order
-// of the slots.
+// block), its slots striding over the tiles the run covers, joined in the
+// order of the slots.  Behind them, blocks that clear the rows without a mark,
+// kZeroRows rows each.
+constexpr int kZeroRows = 64;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
 k_embed_join(const uint32_t* __restrict__ keys, uint32_t n, uint32_t rows, int nv, int lshift, int q,
-             float scale, T* __restrict__ out, const float* __restrict__ tile_head,
-             const float* __restrict__ tile_tail, const int* __restrict__ tile_flag) {
+             uint32_t tiles, float scale, T* __restrict__ out, const float* __restrict__ tile_head,
+             const float* __restrict__ tile_tail, const int* __restrict__ tile_flag,
+             const unsigned char* __restrict__ marks) {
     pdl_begin();
+    if (blockIdx.x >= tiles - 1) {
+        const uint32_t r0 = (blockIdx.x - (tiles - 1)) * kZeroRows;
+        const int count = (int)min((uint32_t)kZeroRows, rows - r0);
+        const int c0 = (blockIdx.y << lshift), width = min(nv - c0, 1 << lshift);
+        const float zero[V] = {};
+        for (int e = threadIdx.x; e < count * width; e += kThreads) {
+            const int r = e / width;
+            if (!marks[r0 + r])
+                Pack<T, V>::store(out + ((size_t)(r0 + r) * nv + c0 + (e - r * width)) * V, zero);
+        }
+        return;
+    }
     if (!(tile_flag[blockIdx.x] & kHasTail)) return;
     const int L = 1 << lshift, S = kThreads >> lshift;
     const int lane = threadIdx.x & (L - 1), slot = threadIdx.x >> lshift;
     const int v = blockIdx.y * L + lane;
-    const uint32_t tile = S * q;
-    const uint32_t key = keys[(blockIdx.x + 1) * tile - 1];
+    const uint32_t key = keys[(blockIdx.x + 1) * (uint32_t)(S * q) - 1];
     if (key >= rows) return;
-    const uint32_t last = (lower_bound(keys, n, key + 1) - 1) / tile;   // the run's last tile
+    // the run's last tile: the first that it does not pass through
+    uint32_t last = blockIdx.x + 1;
+    for (;; last += kThreads) {
+        const uint32_t t = last + threadIdx.x;
+        const bool passes = t < tiles && (tile_flag[t] & kThrough);
+        const uint32_t stop = __ballot_sync(0xffffffffu, !passes);
+        __shared__ uint32_t first[kThreads / 32];
+        if ((threadIdx.x & 31) == 0) first[threadIdx.x >> 5] = stop ? __ffs(stop) - 1 : 32u;
+        __syncthreads();
+        uint32_t found = kThreads;
+#pragma unroll
+        for (int w = kThreads / 32 - 1; w >= 0; --w)
+            if (first[w] < 32u) found = 32u * w + first[w];
+        __syncthreads();
+        if (found < kThreads) {
+            last += found;
+            break;
+        }
+    }
     __shared__ float part[kThreads * V];
     float a[V] = {};
     if (v < nv) {
+#pragma unroll 4
         for (uint32_t t = blockIdx.x + 1 + slot; t <= last; t += S) {
             const float* h = tile_head + ((size_t)t * nv + v) * V;
 #pragma unroll
@@ -447,27 +523,29 @@ SortPlan sort_plan(int64_t n, int64_t rows) {
     p.passes = (kb + kMaxDigit - 1) / kMaxDigit;
     p.bits = (kb + p.passes - 1) / p.passes;
     const int64_t per = ceil_div(n, kSortBlocks);
-    p.chunk = (uint32_t)(ceil_div(per < 2048 ? 2048 : per, 32) * 32);
+    p.chunk = (uint32_t)(ceil_div(per < 1024 ? 1024 : per, kSortThreads) * kSortThreads);
     p.blocks = (uint32_t)ceil_div(n, p.chunk);
     return p;
 }
 
-// Tile shape of the reduction for rows of nv vectors.
+// Tile shape of the reduction for rows of nv vectors: as many positions per
+// slot as give one wave of resident blocks, kAhead to kMostQ.
 struct ReducePlan {
     int lshift, q;
     uint32_t tiles;
     unsigned cols;
+    size_t smem;
 };
-ReducePlan reduce_plan(int64_t n, int64_t nv) {
+ReducePlan reduce_plan(int64_t n, int64_t nv, int v) {
     ReducePlan r;
     r.lshift = log2_up(nv);
     r.lshift = r.lshift < 2 ? 2 : r.lshift > 8 ? 8 : r.lshift;
     const int64_t S = kThreads >> r.lshift;
-    // as many positions per slot as leave two blocks per SM, 8 to 32
-    r.q = 32;
-    while (r.q > kAhead && S * r.q * 304 > n) r.q >>= 1;
+    const int64_t q = ceil_div(n, S * 152 * reduce_blocks_per_sm(v));
+    r.q = (int)(q < kAhead ? kAhead : q > kMostQ ? kMostQ : q);
     r.tiles = (uint32_t)ceil_div(n, S * r.q);
     r.cols = (unsigned)ceil_div(nv, 1 << r.lshift);
+    r.smem = 4 * (2 * (size_t)kThreads * v + S + 2 * S * r.q + 2);
     return r;
 }
 
@@ -475,9 +553,10 @@ struct BackwardSpace {
     uint32_t *keys[2], *pos[2], *counts;
     float *head, *tail;
     int* flag;
+    unsigned char* marks;
 };
 // V only splits a row: nv * V is dim, so the pieces have one size for both.
-BackwardSpace carve(Carve& w, int64_t n, int64_t dim, uint32_t tiles) {
+BackwardSpace carve(Carve& w, int64_t n, int64_t rows, int64_t dim, uint32_t tiles) {
     BackwardSpace s;
     for (int k = 0; k < 2; ++k) {
         s.keys[k] = w.take<uint32_t>(n);
@@ -487,6 +566,7 @@ BackwardSpace carve(Carve& w, int64_t n, int64_t dim, uint32_t tiles) {
     s.head = w.take<float>((size_t)tiles * dim);
     s.tail = w.take<float>((size_t)tiles * dim);
     s.flag = w.take<int>(tiles);
+    s.marks = w.take<unsigned char>(rows);
     return s;
 }
 
@@ -506,38 +586,47 @@ cudaError_t reduce(const EmbedCall& c, const BackwardSpace& w, int from, const R
                    cudaStream_t s) {
     const int nv = (int)(c.dim / V);
     const uint32_t n = (uint32_t)c.n, rows = (uint32_t)c.rows;
-    const unsigned zero_blocks = (unsigned)ceil_div(rows, kThreads);
-    cudaError_t e = launch_pdl(k_embed_reduce<T, V>, dim3(r.tiles + zero_blocks, r.cols),
-                               dim3(kThreads), 0, s, (const T*)c.src, (const uint32_t*)w.keys[from],
-                               (const uint32_t*)w.pos[from], n, rows, nv, r.lshift, r.q, r.tiles,
-                               c.scale, (T*)c.dst, w.head, w.tail, w.flag);
-    if (e != cudaSuccess || r.tiles < 2) return e;
-    return launch_pdl(k_embed_join<T, V>, dim3(r.tiles - 1, r.cols), dim3(kThreads), 0, s,
-                      (const uint32_t*)w.keys[from], n, rows, nv, r.lshift, r.q, c.scale,
-                      (T*)c.dst, (const float*)w.head, (const float*)w.tail, (const int*)w.flag);
+    cudaError_t e = launch_pdl(k_embed_reduce<T, V>, dim3(r.tiles, r.cols), dim3(kThreads), r.smem,
+                               s, (const T*)c.src, (const uint32_t*)w.keys[from],
+                               (const uint32_t*)w.pos[from], n, rows, nv, r.lshift, r.q, c.scale,
+                               (T*)c.dst, w.head, w.tail, w.flag, w.marks);
+    if (e != cudaSuccess) return e;
+    const unsigned zero_blocks = (unsigned)ceil_div(rows, kZeroRows);
+    return launch_pdl(k_embed_join<T, V>, dim3(r.tiles - 1 + zero_blocks, r.cols), dim3(kThreads),
+                      0, s, (const uint32_t*)w.keys[from], n, rows, nv, r.lshift, r.q, r.tiles,
+                      c.scale, (T*)c.dst, (const float*)w.head, (const float*)w.tail,
+                      (const int*)w.flag, (const unsigned char*)w.marks);
 }
 
 template <typename T, typename I>
 cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t s) {
     const bool wide = c.dim % VecOf<T>::n == 0 && aligned16(c.src) && aligned16(c.dst);
-    const ReducePlan r = reduce_plan(c.n, wide ? c.dim / VecOf<T>::n : c.dim);
+    const int v = wide ? VecOf<T>::n : 1;
+    const ReducePlan r = reduce_plan(c.n, c.dim / v, v);
     Carve cv{static_cast<unsigned char*>(ws)};
-    const BackwardSpace w = carve(cv, c.n, c.dim, r.tiles);
-    const SortPlan p = sort_plan(c.n, c.rows);
+    const BackwardSpace w = carve(cv, c.n, c.rows, c.dim, r.tiles);
     const uint32_t n = (uint32_t)c.n, rows = (uint32_t)c.rows;
-    for (int k = 0; k < p.passes; ++k) {
-        const uint32_t* ki = k ? w.keys[(k - 1) & 1] : nullptr;
-        const uint32_t* pi = k ? w.pos[(k - 1) & 1] : nullptr;
-        cudaError_t e = launch_pdl(k_sort_count<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
-                                   (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits, p.bits,
-                                   w.counts, st);
-        if (e == cudaSuccess)
-            e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
-                           (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
-                           (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
-        if (e != cudaSuccess) return e;
+    int from = 0;
+    cudaError_t e = cudaSuccess;
+    if (n <= kRankMost) {
+        e = launch_pdl(k_sort_rank<I>, dim3((unsigned)ceil_div(n, kThreads)), dim3(kThreads), 0, s,
+                       (const I*)c.tokens, n, rows, w.keys[0], w.pos[0], w.marks, st);
+    } else {
+        const SortPlan p = sort_plan(c.n, c.rows);
+        for (int k = 0; k < p.passes && e == cudaSuccess; ++k) {
+            const uint32_t* ki = k ? w.keys[(k - 1) & 1] : nullptr;
+            const uint32_t* pi = k ? w.pos[(k - 1) & 1] : nullptr;
+            e = launch_pdl(k_sort_count<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                           (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits, p.bits, w.counts,
+                           w.marks, st);
+            if (e == cudaSuccess)
+                e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                               (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
+                               (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
+        }
+        from = (p.passes - 1) & 1;
     }
-    const int from = (p.passes - 1) & 1;
+    if (e != cudaSuccess) return e;
     return wide ? reduce<T, VecOf<T>::n>(c, w, from, r, s) : reduce<T, 1>(c, w, from, r, s);
 }
 
@@ -545,12 +634,15 @@ cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t 
 
 size_t embed_workspace(int64_t n, int64_t rows, int64_t dim) {
     if (n == 0) return 0;
-    // the larger of the plans of the vector and the element form
-    uint32_t tiles = reduce_plan(n, dim).tiles;
-    for (int v = 4; v <= 8; v += 4)
-        if (dim % v == 0 && reduce_plan(n, dim / v).tiles > tiles) tiles = reduce_plan(n, dim / v).tiles;
+    // the largest of the plans of the vector and the element forms
+    uint32_t tiles = 0;
+    for (int v : {1, 4, 8})
+        if (dim % v == 0) {
+            const uint32_t t = reduce_plan(n, dim / v, v).tiles;
+            tiles = t > tiles ? t : tiles;
+        }
     Carve cv{nullptr};
-    carve(cv, n, dim, tiles);
+    carve(cv, n, rows, dim, tiles);
     return cv.used;
 }
 

@@ -32,9 +32,10 @@ constexpr int kThreads = 256;
 constexpr int kSegment = 64;   // pixels a thread sums about one value
 constexpr int kAhead = 8;      // 16-byte loads a thread has in flight
 
-// Resident blocks per SM: what the registers of each form allow.
-constexpr int blocks_per_sm(int v, bool back) { return back ? (v == 8 ? 2 : 3) : (v == 8 ? 3 : 4); }
-constexpr int kMostBlocks = 4 * 160;   // of a wave, on the largest part
+// Resident blocks per SM: registers for kAhead loads in flight come first (one
+// more block with spilled ones is 5 to 40 percent slower).
+constexpr int blocks_per_sm(int v) { return v == 8 ? 2 : 3; }
+constexpr int kMostBlocks = 3 * 160;   // of a wave, on the largest part
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -344,7 +345,7 @@ __device__ __forceinline__ Place place(const Shape& sh, int64_t image) {
 
 // part[image of the launch][block][group] = (mean, M2).
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, false))
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
 k_norm_stats(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t image0,
              float2* __restrict__ part) {
     pdl_begin();
@@ -356,7 +357,7 @@ k_norm_stats(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t 
 }
 
 template <typename T, int V, int kAct>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, false))
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
 k_norm_apply(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t image0,
              const float2* __restrict__ part, const float* __restrict__ weight,
              const float* __restrict__ bias, float eps, T* __restrict__ y,
@@ -376,7 +377,7 @@ k_norm_apply(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t 
 
 // part[image of the launch][block][group], total[..][block][channel].
 template <typename T, int V, int kAct>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, true))
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
 k_norm_back_sums(const T* __restrict__ x, const T* __restrict__ dy, const __grid_constant__ Shape sh,
                  int64_t image0, const float2* __restrict__ stats,
                  const float* __restrict__ weight, const float* __restrict__ bias,
@@ -480,7 +481,7 @@ __device__ __forceinline__ void run_back(const T* __restrict__ x, const T* __res
 }
 
 template <typename T, int V, int kAct>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, true))
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
 k_norm_back_apply(const T* __restrict__ x, const T* __restrict__ dy,
                   const __grid_constant__ Shape sh, int64_t image0,
                   const float2* __restrict__ stats, const float2* __restrict__ part,
@@ -787,9 +788,9 @@ int64_t images_at_once(int64_t images, int64_t pixels, int channels, int elem, b
 }
 // ... over which one wave of resident blocks lies, none with less than four
 // pixels per thread.
-void large_shape(Shape* s, int64_t at_once, int v, bool back, int n_sms) {
+void large_shape(Shape* s, int64_t at_once, int v, int n_sms) {
     int per_sm = (int)(220 * 1024 / (smem_bytes(*s, v) + 1024));
-    per_sm = per_sm < blocks_per_sm(v, back) ? per_sm : blocks_per_sm(v, back);
+    per_sm = per_sm < blocks_per_sm(v) ? per_sm : blocks_per_sm(v);
     const int64_t blocks = (int64_t)n_sms * per_sm;
     const int64_t each = blocks / at_once > 0 ? blocks / at_once : 1;
     int64_t per = ceil_div(s->pixels, each);
@@ -839,7 +840,7 @@ cudaError_t forward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
                               (const T*)c.x, sh, c.weight, c.bias, c.eps, (T*)c.out,
                               (float2*)c.stats);
     const int64_t at_once = images_at_once(c.images, c.pixels, c.channels, sizeof(T), false);
-    large_shape(&sh, at_once, V, false, n_sms);
+    large_shape(&sh, at_once, V, n_sms);
     Carve cv{static_cast<unsigned char*>(ws)};
     const Space w = carve(cv, c.images, at_once, sh.blocks, c.channels, c.groups);
     cudaError_t e = cudaSuccess;
@@ -875,7 +876,7 @@ cudaError_t backward(const NormCall& c, void* ws, int n_sms, cudaStream_t s) {
         return e != cudaSuccess || c.images == 1 ? e : params(c, w.image_total, c.images, s);
     }
     const int64_t at_once = images_at_once(c.images, c.pixels, c.channels, sizeof(T), true);
-    large_shape(&sh, at_once, V, true, n_sms);
+    large_shape(&sh, at_once, V, n_sms);
     const Space w = carve(cv, c.images, at_once, sh.blocks, c.channels, c.groups);
     cudaError_t e = cudaSuccess;
     for (int64_t i = 0; i < c.images && e == cudaSuccess; i += at_once) {

@@ -348,20 +348,27 @@ __device__ __forceinline__ void mbar_init(uint64_t* mbar) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(mbar)));
 }
 
+// Whether the mbarrier phase of the given parity is complete, after at most
+// the hardware's own short wait.
+__device__ __forceinline__ bool mbar_try(uint64_t* mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(mbar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Wait for the mbarrier phase of the given parity, at most kWaitNs of wall
 // time (try_wait itself may suspend for an unspecified while, so the bound is
 // on the global timer, not on the number of polls); false on timeout.
 __device__ __forceinline__ bool mbar_wait(uint64_t* mbar, uint32_t parity) {
+    if (mbar_try(mbar, parity)) return true;   // (the timer is slow to read)
     const unsigned long long t0 = global_ns();
     for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(done)
-            : "r"(smem_u32(mbar)), "r"(parity)
-            : "memory");
-        if (done) return true;
+        if (mbar_try(mbar, parity)) return true;
         if (global_ns() - t0 > kWaitNs) return false;
     }
 }
