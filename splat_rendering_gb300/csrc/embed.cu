@@ -65,7 +65,7 @@ k_embed_rows(const T* __restrict__ table, const I* __restrict__ tokens, int64_t 
 #pragma unroll
                 for (int j = 0; j < V; ++j) x[u][j] *= scale;
             }
-            Pack<T, V>::store(out + (i * nv + v) * V, x[u]);
+            Pack<T, V>::store_through(out + (i * nv + v) * V, x[u]);
         }
     }
 }
@@ -131,13 +131,16 @@ k_sort_rank(const I* __restrict__ tokens, uint32_t n, uint32_t rows,
 
 // More: a stable LSD radix sort.  A pass is two launches: every block counts
 // the digits of its contiguous chunk; then every block sums the count matrix
-// to its own offsets and scatters its chunk in order.
-constexpr int kSortThreads = 512;
+// to its own offsets, orders its chunk by the digit in shared memory and
+// writes it out from there, so that stores of a digit lie side by side.
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 16;                              // most per thread at a time
+constexpr int kSortItems = 8;                               // most per thread at a time
 constexpr int kSortTile = kSortThreads * kSortItems;        // 8192
 constexpr int kMaxDigit = 8;                                // bits
 constexpr int kMaxBins = 1 << kMaxDigit;
+constexpr size_t kSortSmem = kSortTile * 8;
+constexpr uint32_t kSortBlocks = 152;                       // at most, one per SM
 constexpr int kWarpBins = kMaxBins / kSortWarps;            // digits a warp sums
 
 // counts[digit][block] of one pass; `keys` NULL: from the tokens.
@@ -176,9 +179,11 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
                int shift, int bits, const uint32_t* __restrict__ counts,
                uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
     pdl_begin();
+    extern __shared__ uint2 s_pair[];                 // [kSortTile] the tile in order
     __shared__ uint32_t base[kMaxBins];               // next output position of each digit
-    __shared__ uint32_t total[kMaxBins];
-    __shared__ uint32_t wh[kSortWarps][kMaxBins];     // per warp: count, then offset
+    __shared__ uint32_t total[kMaxBins];              // of the sort; then of the tile
+    __shared__ uint32_t start[kMaxBins];              // where a digit begins in the tile
+    __shared__ uint32_t wh[kSortWarps][kMaxBins];     // per warp: count, then offset in the tile
     const int bins = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t nb = gridDim.x, b = blockIdx.x;
     {   // a warp's digits together, so that their counts load together
@@ -206,7 +211,8 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
         }
     }
     __syncthreads();
-    if (warp == 0) {   // exclusive scan of the digit totals
+    // exclusive scan of the totals, by one warp: digit d's sum to f(d, sum)
+    const auto scan_totals = [&](auto&& f) {
         uint32_t c[kMaxBins / 32], sum = 0;
 #pragma unroll
         for (int e = 0; e < kMaxBins / 32; ++e) sum += c[e] = total[lane * (kMaxBins / 32) + e];
@@ -219,10 +225,11 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
         s -= sum;
 #pragma unroll
         for (int e = 0; e < kMaxBins / 32; ++e) {
-            base[lane * (kMaxBins / 32) + e] += s;
+            f(lane * (kMaxBins / 32) + e, s);
             s += c[e];
         }
-    }
+    };
+    if (warp == 0) scan_totals([&](int d, uint32_t s) { base[d] += s; });
     const uint32_t lo = b * chunk, hi = min(n, lo + chunk);
     bool bad = false;
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
@@ -249,7 +256,12 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
             if (j < rounds) {
                 const bool on = i0 + 32 * j < hi;
                 const uint32_t d = (key[j] >> shift) & (bins - 1);
-                const uint32_t same = __match_any_sync(0xffffffffu, on ? d : kMaxBins);
+                uint32_t same = __ballot_sync(0xffffffffu, on);   // (faster than a match)
+#pragma unroll
+                for (int q = 0; q < kMaxDigit; ++q) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, (d >> q) & 1u);
+                    same &= (d >> q) & 1u ? m : ~m;
+                }
                 const uint32_t before = __popc(same & ((1u << lane) - 1u));
                 rank[j] = on ? wh[warp][d] + before : 0u;
                 __syncwarp();
@@ -258,25 +270,37 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
             }
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-            uint32_t run = base[d];
+        for (int d = threadIdx.x; d < kMaxBins; d += kSortThreads) {
+            uint32_t run = 0;
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
                 const uint32_t c = wh[w][d];
                 wh[w][d] = run;
                 run += c;
             }
-            base[d] = run;
+            total[d] = run;
         }
+        __syncthreads();
+        if (warp == 0) scan_totals([&](int d, uint32_t s) { start[d] = s; });
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kSortItems; ++j) {
             if (j < rounds && i0 + 32 * j < hi) {
-                const uint32_t at = wh[warp][(key[j] >> shift) & (bins - 1)] + rank[j];
-                keys_out[at] = key[j];
-                pos_out[at] = val[j];
+                const uint32_t d = (key[j] >> shift) & (bins - 1);
+                s_pair[start[d] + wh[warp][d] + rank[j]] = make_uint2(key[j], val[j]);
             }
         }
+        __syncthreads();
+        const uint32_t count = min(hi - t0, (uint32_t)kSortTile);
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < count; i += kSortThreads) {
+            const uint2 u = s_pair[i];
+            const uint32_t d = (u.x >> shift) & (bins - 1), at = base[d] + i - start[d];
+            keys_out[at] = u.x;
+            pos_out[at] = u.y;
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < kMaxBins; d += kSortThreads) base[d] += total[d];
         __syncthreads();
     }
 }
@@ -344,7 +368,7 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (p + u < p1 && key[p + u] < rows && col)
-                    x[u] = Pack<T, V>::raw(grad + ((size_t)s_pos[p + u] * nv + v) * V);
+                    x[u] = Pack<T, V>::raw_last(grad + ((size_t)s_pos[p + u] * nv + v) * V);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (p + u >= p1) break;
@@ -516,14 +540,13 @@ struct SortPlan {
     int passes, bits;
     uint32_t blocks, chunk;
 };
-constexpr uint32_t kSortBlocks = 152;   // one per SM: the count matrix stays small
 SortPlan sort_plan(int64_t n, int64_t rows) {
     SortPlan p;
     const int kb = log2_up(rows + 1) > 0 ? log2_up(rows + 1) : 1;   // keys 0 .. rows
     p.passes = (kb + kMaxDigit - 1) / kMaxDigit;
     p.bits = (kb + p.passes - 1) / p.passes;
     const int64_t per = ceil_div(n, kSortBlocks);
-    p.chunk = (uint32_t)(ceil_div(per < 1024 ? 1024 : per, kSortThreads) * kSortThreads);
+    p.chunk = (uint32_t)(ceil_div(per, kSortThreads) * kSortThreads);
     p.blocks = (uint32_t)ceil_div(n, p.chunk);
     return p;
 }
@@ -620,7 +643,7 @@ cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t 
                            (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits, p.bits, w.counts,
                            w.marks, st);
             if (e == cudaSuccess)
-                e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), kSortSmem, s,
                                (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
                                (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
         }
@@ -644,6 +667,15 @@ size_t embed_workspace(int64_t n, int64_t rows, int64_t dim) {
     Carve cv{nullptr};
     carve(cv, n, rows, dim, tiles);
     return cv.used;
+}
+
+cudaError_t prepare_embed() {
+    cudaError_t e = cudaFuncSetAttribute(
+        k_sort_scatter<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_sort_scatter<int64_t>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+    return e;
 }
 
 cudaError_t launch_embed_forward(const EmbedCall& c, LearnState* st, cudaStream_t s) {

@@ -80,7 +80,7 @@ int pulsar_learn_create(pulsar_learn_t* out, int device, int64_t workspace_bytes
         ok = cudaDeviceGetAttribute(&h->n_sms, cudaDevAttrMultiProcessorCount, device) ==
                  cudaSuccess &&
              h->n_sms <= kMaxSms && prepare_orth() == cudaSuccess &&
-             prepare_group_norm() == cudaSuccess &&
+             prepare_group_norm() == cudaSuccess && prepare_embed() == cudaSuccess &&
              cudaMemset(h->state, 0, sizeof(LearnState)) == cudaSuccess &&
              cudaDeviceSynchronize() == cudaSuccess;
     if (!ok) {

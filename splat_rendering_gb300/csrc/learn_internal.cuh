@@ -157,6 +157,7 @@ struct EmbedCall {
     void* dst;            // out (forward) or grad_table (backward)
 };
 size_t embed_workspace(int64_t n, int64_t rows, int64_t dim);
+cudaError_t prepare_embed();
 cudaError_t launch_embed_forward(const EmbedCall& c, LearnState* st, cudaStream_t stream);
 cudaError_t launch_embed_backward(const EmbedCall& c, LearnState* st, void* ws, int n_sms,
                                   cudaStream_t stream);

@@ -380,22 +380,26 @@ def debug_inject(ctx, what: int, stream=None):
 ACT = dict(none=0, silu=1, relu=2)
 
 
+_CODES = {}   # torch's types by what they can be: filled on first use (torch is imported late)
+
+
+def _code(dtype, kind: str) -> int:
+    if not _CODES:
+        import torch
+        _CODES.update(value={torch.float32: 0, torch.bfloat16: 1},
+                      index={torch.int32: 0, torch.int64: 1})
+    code = _CODES[kind].get(dtype)
+    if code is None:
+        raise TypeError(f"{' or '.join(str(t) for t in _CODES[kind])} is wanted, got {dtype}")
+    return code
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    if dtype == torch.float32:
-        return 0
-    if dtype == torch.bfloat16:
-        return 1
-    raise TypeError(f"float32 or bfloat16 is wanted, got {dtype}")
+    return _code(dtype, "value")
 
 
 def _index_code(dtype) -> int:
-    import torch
-    if dtype == torch.int32:
-        return 0
-    if dtype == torch.int64:
-        return 1
-    raise TypeError(f"tokens are int32 or int64, got {dtype}")
+    return _code(dtype, "index")
 
 
 def _bytes(code: int, what: str) -> int:
@@ -436,10 +440,16 @@ class Learner:
     before a kernel is launched.  Outputs are allocated unless given."""
 
     def __init__(self, workspace_bytes: int, device: int = 0):
+        import torch
         self.device, self.workspace_bytes = int(device), int(workspace_bytes)
         self.handle = 0
+        self._lib = load()
+        # a call costs a few microseconds of host time: keep what it looks up
+        self._torch, self._dev = torch, torch.device("cuda", self.device)
+        self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
         h = ctypes.c_void_p()
-        _check(load().pulsar_learn_create(ctypes.byref(h), self.device, self.workspace_bytes),
+        _check(self._lib.pulsar_learn_create(ctypes.byref(h), self.device, self.workspace_bytes),
                "pulsar_learn_create")
         self.handle = h.value
 
@@ -456,45 +466,41 @@ class Learner:
 
     def status(self, stream=None, raise_on_error: bool = True) -> int:
         """Synchronise the stream and report the latched device error."""
-        code = load().pulsar_learn_status(self.handle, self._stream(stream))
+        code = self._lib.pulsar_learn_status(self.handle, self._stream(stream))
         if raise_on_error:
             _check(code, "pulsar_learn_status")
         return code
 
     def _stream(self, s):
-        if s is None:
-            import torch
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return _stream(s)
+        return self._current_stream(self.device) if s is None else _stream(s)
 
     def _tensor(self, t, what: str, shape=None, dtype=None):
         """Checks a tensor argument and returns its pointer (None stays None)."""
         if t is None:
             return None
-        if not t.is_cuda or t.get_device() != self.device:
+        if t.get_device() != self.device:   # (-1 on the host)
             raise ValueError(f"{what} is not on cuda:{self.device}")
         if not t.is_contiguous():
             raise ValueError(f"{what} is not contiguous")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{what} has shape {tuple(t.shape)}, wanted {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{what} is {t.dtype}, wanted {dtype}")
         return t.data_ptr()
 
     def _empty(self, shape, dtype):
-        import torch
-        return torch.empty(shape, device=f"cuda:{self.device}", dtype=dtype)
+        return self._torch.empty(shape, device=self._dev, dtype=dtype)
 
     def embed(self, table, tokens, scale: float = 1.0, out=None, stream=None):
         """scale * table[tokens] ([*tokens.shape, dim]); zeros where a token is negative."""
         if table.dim() != 2:
             raise ValueError(f"table has shape {tuple(table.shape)}, wanted [rows, dim]")
         rows, dim = table.shape
-        shape = tuple(tokens.shape) + (dim,)
+        shape = (*tokens.shape, dim)
         dt, ix = _dtype_code(table.dtype), _index_code(tokens.dtype)
         if out is None:
             out = self._empty(shape, table.dtype)
-        _check(load().pulsar_embed_forward(
+        _check(self._lib.pulsar_embed_forward(
             self.handle, self._tensor(table, "table"), self._tensor(tokens, "tokens"),
             tokens.numel(), rows, dim, scale, dt, ix,
             self._tensor(out, "out", shape, table.dtype), self._stream(stream)),
@@ -504,14 +510,14 @@ class Learner:
     def embed_backward(self, grad_out, tokens, rows: int, scale: float = 1.0, grad_table=None,
                        stream=None):
         """Gradient [rows, dim] of `embed` for grad_out [*tokens.shape, dim]."""
-        if tuple(grad_out.shape[:-1]) != tuple(tokens.shape):
+        if grad_out.shape[:-1] != tokens.shape:
             raise ValueError(f"grad_out has shape {tuple(grad_out.shape)}, wanted "
                              f"{tuple(tokens.shape) + ('dim',)}")
         dim = grad_out.shape[-1]
         dt, ix = _dtype_code(grad_out.dtype), _index_code(tokens.dtype)
         if grad_table is None:
             grad_table = self._empty((rows, dim), grad_out.dtype)
-        _check(load().pulsar_embed_backward(
+        _check(self._lib.pulsar_embed_backward(
             self.handle, self._tensor(grad_out, "grad_out"), self._tensor(tokens, "tokens"),
             tokens.numel(), rows, dim, scale, dt, ix,
             self._tensor(grad_table, "grad_table", (rows, dim), grad_out.dtype),
@@ -533,14 +539,13 @@ class Learner:
                    act: str = "none", out=None, stats=None, stream=None):
         """(y, stats): act(group norm) of x [images, ..., channels], channels
         last, and the (mean, 1/std) [images, groups, 2] its backward needs."""
-        import torch
         images, pixels, C, a = self._image_shape(x, act)
-        dt, f32 = _dtype_code(x.dtype), torch.float32
+        dt, f32 = _dtype_code(x.dtype), self._torch.float32
         if out is None:
             out = self._empty(x.shape, x.dtype)
         if stats is None:
             stats = self._empty((images, groups, 2), f32)
-        _check(load().pulsar_group_norm_forward(
+        _check(self._lib.pulsar_group_norm_forward(
             self.handle, self._tensor(x, "x"), images, pixels, C, groups,
             self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32),
             eps, a, dt, self._tensor(out, "out", x.shape, x.dtype),
@@ -553,16 +558,15 @@ class Learner:
                             want=("x", "weight", "bias"), stream=None):
         """(grad_x, grad_weight, grad_bias) of `group_norm`; those not in
         `want` (and not given) are None and not computed."""
-        import torch
         images, pixels, C, a = self._image_shape(x, act)
-        dt, f32 = _dtype_code(x.dtype), torch.float32
+        dt, f32 = _dtype_code(x.dtype), self._torch.float32
         if grad_x is None and "x" in want:
             grad_x = self._empty(x.shape, x.dtype)
         if grad_weight is None and "weight" in want:
             grad_weight = self._empty((C,), f32)
         if grad_bias is None and "bias" in want:
             grad_bias = self._empty((C,), f32)
-        _check(load().pulsar_group_norm_backward(
+        _check(self._lib.pulsar_group_norm_backward(
             self.handle, self._tensor(grad_y, "grad_y", x.shape, x.dtype), self._tensor(x, "x"),
             self._tensor(stats, "stats", (images, groups, 2), f32), images, pixels, C, groups,
             self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32), a, dt,
@@ -585,7 +589,7 @@ class Learner:
         if out is None:
             out = self._empty(grad.shape, grad.dtype)
         abc = (ctypes.c_float * 3)(*[float(v) for v in coeffs])
-        _check(load().pulsar_orthogonalize(
+        _check(self._lib.pulsar_orthogonalize(
             self.handle, self._tensor(grad, "grad"), batch, m, n, steps, abc, eps, dt,
             self._tensor(out, "out", grad.shape, grad.dtype), self._stream(stream)),
             "pulsar_orthogonalize")
