@@ -210,7 +210,7 @@ struct Product {
 
 constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epilogue
 constexpr int kChunk = 4;              // panels of K per drained sum (32 bits)
-constexpr int kRowPitch = 33;          // words of a row of a warp's 32 x 32 exchange
+constexpr int kRowPitch = 33;          // words of a row of a warp's 32 x 32 word exchange
 
 template <bool kSplit, int kN>
 struct ProductSmem {
@@ -223,7 +223,7 @@ struct ProductSmem {
     static constexpr int bars = exchange + exchange_bytes;
     static constexpr int bytes = bars + 256 + 1024;   // and the alignment to 1024
     static_assert(stages >= 2 && (2 * stages + 5) * 8 + 8 <= 256, "shared memory of a product");
-    static_assert(stages * stage >= kBlock * kBlock * 4, "a tile of sums fits the stages");
+    static_assert(stages * stage >= kBlock * kN * 4, "a tile of sums fits the stages");
 };
 
 // Descriptor of a 128-byte-swizzled operand: `lbo` is the stride between
@@ -284,6 +284,18 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
     return v;
 }
 
+// Tile t of a symmetric product in tiles of 128 x 256: row blocks of 128, the
+// column blocks up to the diagonal, i / 2 + 1 of them in row block i.
+__device__ __forceinline__ void lower_wide(int t, int* i, int* j) {
+    // rows 2 a and 2 a + 1 have a + 1 tiles each; a (a + 1) lie before row 2 a
+    int a = (int)((sqrtf(4.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while ((a + 1) * (a + 2) <= t) ++a;
+    while (a * (a + 1) > t) --a;
+    const int rest = t - a * (a + 1);
+    *i = 2 * a + (rest > a ? 1 : 0);
+    *j = rest > a ? rest - a - 1 : rest;
+}
+
 // Tile t of a symmetric product, row blocks i >= j.
 __device__ __forceinline__ void lower_tile(int t, int* i, int* j) {
     int row = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
@@ -313,8 +325,6 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     constexpr int kMine = kPanels / 2;            // panels of an epilogue thread
     constexpr int kCols = kPanel / kCluster;      // columns of a panel it finishes
     constexpr int kAcc = kSplit ? 2 * kN : kN;    // columns of an accumulator
-    static_assert(!kGram || kN == kBlock, "symmetric products have square tiles");
-    static_assert(kCluster == 1 || kMine == 1, "a shared tile is one panel per thread");
     static_assert(2 * kAcc <= 512, "tensor memory");
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -356,7 +366,10 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         *z = t / q.tiles;
         t -= *z * q.tiles;
         if (kGram) {
-            lower_tile(t, i, j);
+            if (kN == kBlock)
+                lower_tile(t, i, j);
+            else
+                lower_wide(t, i, j);
         } else {
             *i = t % q.tiles_m;   // neighbours share the columns of X
             *j = t / q.tiles_m;
@@ -367,16 +380,18 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     const int group = (warp - 2) >> 2, quarter = warp & 3;   // (epilogue warps are 2 .. 9)
     const int row = quarter * 32 + lane;
     // columns col .. col + kCols - 1 of the tile from their finished sums
-    auto finish = [&](int z, int i, int j, int col, const uint4 (&c)[kCols / 8][kParts],
-                      float (&v)[kCols]) {
+    using CHalves = uint4[kCols / 8][kParts];
+    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float (&v)[kCols]) {
         const int64_t grow = (int64_t)i * kBlock + row, gcol = (int64_t)j * kN + col;
+        const int jb = j * (kN / kBlock) + col / kBlock;   // the columns' block of 128
+        if (kGram && jb > i) return;   // above the diagonal: the mirrored block's
         __half* d = q.d + z * q.d_size;
         // col begins a run of kCols inside one panel: its row of 64 halves, and mirrored
         // the run's rows in the panel of this thread's column (the warp's are adjacent)
         __half* line = d + ((gcol / kPanel) * q.d_rows + grow) * kPanel;
         __half* column = d + ((grow / kPanel) * q.d_rows + gcol) * kPanel + (row & 7);
         const int chunk0 = (int)(gcol & (kPanel - 1)) >> 3, rchunk = (row & (kPanel - 1)) >> 3;
-        const int on = i == j ? row - col : -1;   // the diagonal's place among the columns
+        const int on = i == jb ? row - col % kBlock : -1;   // the diagonal's place in them
 #pragma unroll
         for (int b = 0; b < kCols / 8; ++b) {
             float w[8];
@@ -394,11 +409,72 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
             for (int p = 0; p < kParts; ++p) {
                 *reinterpret_cast<uint4*>(line + p * q.d_lo + (((chunk0 + b) ^ (row & 7)) << 3)) =
                     h[p];
-                if (kGram && i != j) {
+                if (kGram && i != jb) {
                     const __half* e16 = reinterpret_cast<const __half*>(&h[p]);
                     __half* m = column + p * q.d_lo + 8 * b * kPanel;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) m[e * kPanel + ((rchunk ^ e) << 3)] = e16[e];
+                }
+            }
+        }
+    };
+
+    // a panel of the result from its sums: through the warp's exchange, so that
+    // a warp writes whole rows (of the transpose, whole columns as they are)
+    auto store_result = [&](int z, int i, int j, int col, const float (&v)[kPanel]) {
+        const int64_t r0 = (int64_t)i * kBlock + quarter * 32, c0 = (int64_t)j * kN + col;
+        const size_t base = (size_t)z * q.out_r * q.out_c;
+        if (q.tall) {
+            if (r0 + lane >= q.out_r) return;
+            const size_t at = base + c0 * q.out_r + r0 + lane;
+            const int n = (int)min((int64_t)kPanel, q.out_c - c0);
+#pragma unroll
+            for (int e = 0; e < kPanel; ++e) {
+                if (e >= n) continue;
+                const float y = q.alpha * v[e];
+                if (q.dtype == kF32)
+                    static_cast<float*>(q.out)[at + e * q.out_r] = y;
+                else
+                    static_cast<__nv_bfloat16*>(q.out)[at + e * q.out_r] = __float2bfloat16_rn(y);
+            }
+            return;
+        }
+        uint32_t* x = reinterpret_cast<uint32_t*>(smem + L::exchange) + (warp - 2) * 32 * kRowPitch;
+        const int rows = (int)min((int64_t)32, q.out_r - r0);
+        if (q.dtype == kF32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    x[lane * kRowPitch + e] = __float_as_uint(q.alpha * v[32 * h + e]);
+                __syncwarp();
+                if (c0 + 32 * h + lane < q.out_c) {
+                    float* o = static_cast<float*>(q.out) + base + r0 * q.out_c + c0 + 32 * h + lane;
+                    for (int e = 0; e < rows; ++e, o += q.out_c)
+                        *o = __uint_as_float(x[e * kRowPitch + lane]);
+                }
+            }
+        } else {   // two columns a word
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const __nv_bfloat162 h =
+                    __floats2bfloat162_rn(q.alpha * v[2 * e], q.alpha * v[2 * e + 1]);
+                x[lane * kRowPitch + e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            __syncwarp();
+            const int64_t c = c0 + 2 * lane;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(q.out) + base + r0 * q.out_c + c;
+            const bool words = q.out_c % 2 == 0 && (reinterpret_cast<uintptr_t>(q.out) & 3u) == 0;
+            for (int e = 0; e < rows; ++e, o += q.out_c) {
+                const uint32_t u = x[e * kRowPitch + lane];
+                const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&u);
+                if (words) {
+                    if (c < q.out_c) *reinterpret_cast<uint32_t*>(o) = u;
+                } else {
+                    if (c < q.out_c) o[0] = h.x;
+                    if (c + 1 < q.out_c) o[1] = h.y;
                 }
             }
         }
@@ -503,18 +579,21 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         for (int t = first; t < total; t += step) {   // (once, where a cluster shares the tile)
             int z, i, j;
             place(t, &z, &i, &j);
-            uint4 c[kCols / 8][kParts];   // C of the columns this thread finishes, loaded early
+            CHalves c[kGram ? kMine : 1];   // C of the columns this thread finishes, loaded early
             if (kGram && q.c) {
                 const __half* cz = q.c + z * q.d_size;
 #pragma unroll
-                for (int b = 0; b < kCols / 8; ++b)
+                for (int m = 0; m < kMine; ++m)
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
-                        c[b][p] = *reinterpret_cast<const uint4*>(
-                            cz + p * q.d_lo +
-                            panel_at((int64_t)i * kBlock + row,
-                                     (int64_t)j * kN + group * kPanel + rank * kCols + 8 * b,
-                                     q.d_rows));
+                    for (int b = 0; b < kCols / 8; ++b)
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p)
+                            c[kGram ? m : 0][b][p] = *reinterpret_cast<const uint4*>(
+                                cz + p * q.d_lo +
+                                panel_at((int64_t)i * kBlock + row,
+                                         (int64_t)j * kN + (group * kMine + m) * kPanel +
+                                             rank * kCols + 8 * b,
+                                         q.d_rows));
             }
             float v[kPanel];
             bool ok = true;
@@ -584,60 +663,34 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                     float w[kCols];
 #pragma unroll
                     for (int e = 0; e < kCols; ++e) w[e] = v[e % kPanel];
-                    finish(z, i, j, col, c, w);
-                } else {   // the result: through a 32 x 32 exchange of the warp, row by row
-                    float* x = reinterpret_cast<float*>(smem + L::exchange) +
-                               (warp - 2) * 32 * kRowPitch;
-                    const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
-                    const size_t base = (size_t)z * q.out_r * q.out_c;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int64_t c0 = (int64_t)j * kN + col + 32 * h;
-                        if (!q.tall) {
-                            __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[lane * kRowPitch + e] = v[32 * h + e];
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            // e: a row of the exchange, or (tall) a column of the tile
-                            const int64_t orow = q.tall ? r0 + lane : r0 + e;
-                            const int64_t ocol = q.tall ? c0 + e : c0 + lane;
-                            const float y = q.alpha * (q.tall ? v[32 * h + e]
-                                                              : x[e * kRowPitch + lane]);
-                            if (orow < q.out_r && ocol < q.out_c) {
-                                const size_t at = base + (q.tall ? ocol * q.out_r + orow
-                                                                 : orow * q.out_c + ocol);
-                                if (q.dtype == kF32)
-                                    static_cast<float*>(q.out)[at] = y;
-                                else
-                                    static_cast<__nv_bfloat16*>(q.out)[at] = __float2bfloat16_rn(y);
-                            }
-                        }
-                    }
+                    finish(z, i, j, col, c[0], w);   // (one panel where there is a C)
+                } else {   // the result
+                    store_result(z, i, j, col, v);
                 }
             }
             if (kCluster > 1) {
                 __syncwarp();
                 cluster_sync();
                 met = true;
-                float w[kCols];
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) w[e] = 0.0f;
-                const int col = group * kPanel + (int)rank * kCols;
-                const uint32_t at = smem_u32(smem) + (uint32_t)((col / 4 * kBlock + row) * 16);
+                for (int m = 0; m < kMine; ++m) {
+                    float w[kCols];
 #pragma unroll
-                for (int s = 0; s < kCluster; ++s)
+                    for (int e = 0; e < kCols; ++e) w[e] = 0.0f;
+                    const int col = (group * kMine + m) * kPanel + (int)rank * kCols;
+                    const uint32_t at = smem_u32(smem) + (uint32_t)((col / 4 * kBlock + row) * 16);
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 4) {
-                        const float4 u = ld_cluster(at + e / 4 * kBlock * 16, s);
-                        w[e] += u.x;
-                        w[e + 1] += u.y;
-                        w[e + 2] += u.z;
-                        w[e + 3] += u.w;
-                    }
-                finish(z, i, j, col, c, w);
+                    for (int s = 0; s < kCluster; ++s)
+#pragma unroll
+                        for (int e = 0; e < kCols; e += 4) {
+                            const float4 u = ld_cluster(at + e / 4 * kBlock * 16, s);
+                            w[e] += u.x;
+                            w[e + 1] += u.y;
+                            w[e + 2] += u.z;
+                            w[e + 3] += u.w;
+                        }
+                    finish(z, i, j, col, c[kGram ? m : 0], w);
+                }
             }
         }
     }
@@ -924,7 +977,8 @@ Plan plan_of(int64_t m, int64_t n, int dtype) {
     p.tall = m > n;
     p.r = p.tall ? n : m;
     p.c = p.tall ? m : n;
-    p.rp = ceil_div(p.r, kBlock) * kBlock;
+    // (of 1024 rows and more in pairs of blocks, for the wide symmetric tiles)
+    p.rp = p.r > 1024 ? ceil_div(p.r, 2 * kBlock) * 2 * kBlock : ceil_div(p.r, kBlock) * kBlock;
     const int64_t to = p.c > 1024 ? 256 : 128;   // two widths of a tile of the last product
     p.cp = ceil_div(p.c, to) * to;
     p.parts = dtype == kF32 ? 2 : 1;
@@ -968,6 +1022,17 @@ cudaError_t symmetric(const Product& q, LearnState* st, int n_sms, cudaStream_t 
     if (fits(8)) return product<kSplit, kBlock, true, 8>(q, st, n_sms, s);
     if (fits(4)) return product<kSplit, kBlock, true, 4>(q, st, n_sms, s);
     if (fits(2)) return product<kSplit, kBlock, true, 2>(q, st, n_sms, s);
+    if constexpr (!kSplit) {
+        // An MMA of N = 256 takes little longer than one of 128: tiles twice as wide, shared by
+        // two CTAs, take two thirds of the time (2048 rows: 72 tiles instead of 136).
+        const int64_t half = (q.tiles_m + 1) / 2, wide = half * (half + 1) * q.batch;
+        if (q.tiles_m % 2 == 0 && q.k_panels >= 2 &&
+            ceil_div(wide * 2, n_sms) * 13 <= ceil_div(total, n_sms) * 20 && wide * 2 <= n_sms) {
+            Product w = q;
+            w.tiles = (int)(half * (half + 1));
+            return product<kSplit, 256, true, 2>(w, st, n_sms, s);
+        }
+    }
     return product<kSplit, kBlock, true>(q, st, n_sms, s);
 }
 
@@ -1095,6 +1160,7 @@ cudaError_t prepare_orth() {
     cudaError_t e = prepare_type<false>();
     if (e == cudaSuccess) e = prepare_type<true>();
     if (e == cudaSuccess) e = prepare_one<false, 256, false>();
+    if (e == cudaSuccess) e = prepare_one<false, 256, true, 2>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_orth_small<float, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
