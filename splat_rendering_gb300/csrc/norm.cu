@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSegment = 64;   // pixels a thread sums about one value
 constexpr int kAhead = 8;      // 16-byte loads a thread has in flight
+constexpr int kAheadApply = 6; // (beside what the forward's output needs in registers)
 
 // Resident blocks per SM: registers for kAhead loads in flight come first (one
 // more block with spilled ones is 5 to 40 percent slower).
@@ -316,13 +317,13 @@ __device__ __forceinline__ void run_apply(const T* __restrict__ x, T* __restrict
         for (int j = 0; j < V; ++j) f.rstd[j] *= f.w[j];
         // from the end: what was read last is nearest
         int64_t at = off + (row + (int64_t)(cnt - 1) * sh.rpb) * sh.channels + col * V;
-        for (int i = 0; i < cnt; i += kAhead / 2, at -= kAhead / 2 * pitch) {
-            typename Pack<T, V>::Raw r[kAhead / 2];
+        for (int i = 0; i < cnt; i += kAheadApply, at -= kAheadApply * pitch) {
+            typename Pack<T, V>::Raw r[kAheadApply];
 #pragma unroll
-            for (int u = 0; u < kAhead / 2; ++u)
+            for (int u = 0; u < kAheadApply; ++u)
                 if (i + u < cnt) r[u] = Pack<T, V>::raw_last(x + at - u * pitch);
 #pragma unroll
-            for (int u = 0; u < kAhead / 2; ++u) {
+            for (int u = 0; u < kAheadApply; ++u) {
                 if (i + u >= cnt) break;
                 float v[V];
                 Pack<T, V>::open(r[u], v);

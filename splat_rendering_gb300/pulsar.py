@@ -488,8 +488,19 @@ class Learner:
             raise TypeError(f"{what} is {t.dtype}, wanted {dtype}")
         return t.data_ptr()
 
-    def _empty(self, shape, dtype):
-        return self._torch.empty(shape, device=self._dev, dtype=dtype)
+    def _out(self, t, what: str, shape, dtype):
+        """An output and its pointer: `t` checked, or where it is None a new one."""
+        if t is None:
+            t = self._torch.empty(shape, device=self._dev, dtype=dtype)
+            return t, t.data_ptr()
+        return t, self._tensor(t, what, shape, dtype)
+
+    @staticmethod
+    def _product(shape):
+        n = 1
+        for d in shape:
+            n *= d
+        return n
 
     def embed(self, table, tokens, scale: float = 1.0, out=None, stream=None):
         """scale * table[tokens] ([*tokens.shape, dim]); zeros where a token is negative."""
@@ -498,12 +509,10 @@ class Learner:
         rows, dim = table.shape
         shape = (*tokens.shape, dim)
         dt, ix = _dtype_code(table.dtype), _index_code(tokens.dtype)
-        if out is None:
-            out = self._empty(shape, table.dtype)
+        out, p_out = self._out(out, "out", shape, table.dtype)
         _check(self._lib.pulsar_embed_forward(
             self.handle, self._tensor(table, "table"), self._tensor(tokens, "tokens"),
-            tokens.numel(), rows, dim, scale, dt, ix,
-            self._tensor(out, "out", shape, table.dtype), self._stream(stream)),
+            tokens.numel(), rows, dim, scale, dt, ix, p_out, self._stream(stream)),
             "pulsar_embed_forward")
         return out
 
@@ -515,42 +524,34 @@ class Learner:
                              f"{tuple(tokens.shape) + ('dim',)}")
         dim = grad_out.shape[-1]
         dt, ix = _dtype_code(grad_out.dtype), _index_code(tokens.dtype)
-        if grad_table is None:
-            grad_table = self._empty((rows, dim), grad_out.dtype)
+        grad_table, p_table = self._out(grad_table, "grad_table", (rows, dim), grad_out.dtype)
         _check(self._lib.pulsar_embed_backward(
             self.handle, self._tensor(grad_out, "grad_out"), self._tensor(tokens, "tokens"),
-            tokens.numel(), rows, dim, scale, dt, ix,
-            self._tensor(grad_table, "grad_table", (rows, dim), grad_out.dtype),
-            self._stream(stream)), "pulsar_embed_backward")
+            tokens.numel(), rows, dim, scale, dt, ix, p_table, self._stream(stream)),
+            "pulsar_embed_backward")
         return grad_table
 
-    @staticmethod
-    def _image_shape(x, act):
-        if x.dim() < 2:
-            raise ValueError(f"x has shape {tuple(x.shape)}, wanted [images, ..., channels]")
-        if act not in ACT:
+    def _image_shape(self, x, act):
+        shape = x.shape
+        if len(shape) < 2:
+            raise ValueError(f"x has shape {tuple(shape)}, wanted [images, ..., channels]")
+        a = ACT.get(act)
+        if a is None:
             raise ValueError(f"act is one of {sorted(ACT)}, got {act!r}")
-        pixels = 1
-        for d in x.shape[1:-1]:
-            pixels *= int(d)
-        return int(x.shape[0]), pixels, int(x.shape[-1]), ACT[act]
+        return shape, shape[0], self._product(shape[1:-1]), shape[-1], a
 
     def group_norm(self, x, groups: int, weight=None, bias=None, eps: float = 1e-5,
                    act: str = "none", out=None, stats=None, stream=None):
         """(y, stats): act(group norm) of x [images, ..., channels], channels
         last, and the (mean, 1/std) [images, groups, 2] its backward needs."""
-        images, pixels, C, a = self._image_shape(x, act)
+        shape, images, pixels, C, a = self._image_shape(x, act)
         dt, f32 = _dtype_code(x.dtype), self._torch.float32
-        if out is None:
-            out = self._empty(x.shape, x.dtype)
-        if stats is None:
-            stats = self._empty((images, groups, 2), f32)
+        out, p_out = self._out(out, "out", shape, x.dtype)
+        stats, p_stats = self._out(stats, "stats", (images, groups, 2), f32)
         _check(self._lib.pulsar_group_norm_forward(
             self.handle, self._tensor(x, "x"), images, pixels, C, groups,
             self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32),
-            eps, a, dt, self._tensor(out, "out", x.shape, x.dtype),
-            self._tensor(stats, "stats", (images, groups, 2), f32), self._stream(stream)),
-            "pulsar_group_norm_forward")
+            eps, a, dt, p_out, p_stats, self._stream(stream)), "pulsar_group_norm_forward")
         return out, stats
 
     def group_norm_backward(self, grad_y, x, stats, groups: int, weight=None, bias=None,
@@ -558,39 +559,32 @@ class Learner:
                             want=("x", "weight", "bias"), stream=None):
         """(grad_x, grad_weight, grad_bias) of `group_norm`; those not in
         `want` (and not given) are None and not computed."""
-        images, pixels, C, a = self._image_shape(x, act)
+        shape, images, pixels, C, a = self._image_shape(x, act)
         dt, f32 = _dtype_code(x.dtype), self._torch.float32
-        if grad_x is None and "x" in want:
-            grad_x = self._empty(x.shape, x.dtype)
-        if grad_weight is None and "weight" in want:
-            grad_weight = self._empty((C,), f32)
-        if grad_bias is None and "bias" in want:
-            grad_bias = self._empty((C,), f32)
+        p_x = p_weight = p_bias = None
+        if grad_x is not None or "x" in want:
+            grad_x, p_x = self._out(grad_x, "grad_x", shape, x.dtype)
+        if grad_weight is not None or "weight" in want:
+            grad_weight, p_weight = self._out(grad_weight, "grad_weight", (C,), f32)
+        if grad_bias is not None or "bias" in want:
+            grad_bias, p_bias = self._out(grad_bias, "grad_bias", (C,), f32)
         _check(self._lib.pulsar_group_norm_backward(
-            self.handle, self._tensor(grad_y, "grad_y", x.shape, x.dtype), self._tensor(x, "x"),
+            self.handle, self._tensor(grad_y, "grad_y", shape, x.dtype), self._tensor(x, "x"),
             self._tensor(stats, "stats", (images, groups, 2), f32), images, pixels, C, groups,
             self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32), a, dt,
-            self._tensor(grad_x, "grad_x", x.shape, x.dtype),
-            self._tensor(grad_weight, "grad_weight", (C,), f32),
-            self._tensor(grad_bias, "grad_bias", (C,), f32), self._stream(stream)),
-            "pulsar_group_norm_backward")
+            p_x, p_weight, p_bias, self._stream(stream)), "pulsar_group_norm_backward")
         return grad_x, grad_weight, grad_bias
 
     def orthogonalize(self, grad, steps: int = 5, coeffs=(3.4445, -4.775, 2.0315),
                       eps: float = 1e-7, out=None, stream=None):
         """`steps` Newton-Schulz products on each matrix of grad [..., m, n]."""
-        if grad.dim() < 2:
-            raise ValueError(f"grad has shape {tuple(grad.shape)}, wanted [..., m, n]")
-        m, n = grad.shape[-2:]
-        batch = 1
-        for d in grad.shape[:-2]:
-            batch *= int(d)
+        shape = grad.shape
+        if len(shape) < 2:
+            raise ValueError(f"grad has shape {tuple(shape)}, wanted [..., m, n]")
         dt = _dtype_code(grad.dtype)
-        if out is None:
-            out = self._empty(grad.shape, grad.dtype)
+        out, p_out = self._out(out, "out", shape, grad.dtype)
         abc = (ctypes.c_float * 3)(*[float(v) for v in coeffs])
         _check(self._lib.pulsar_orthogonalize(
-            self.handle, self._tensor(grad, "grad"), batch, m, n, steps, abc, eps, dt,
-            self._tensor(out, "out", grad.shape, grad.dtype), self._stream(stream)),
-            "pulsar_orthogonalize")
+            self.handle, self._tensor(grad, "grad"), self._product(shape[:-2]), shape[-2], shape[-1],
+            steps, abc, eps, dt, p_out, self._stream(stream)), "pulsar_orthogonalize")
         return out
