@@ -47,8 +47,9 @@ __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, in
 constexpr float kDown = 5.421010862427522e-20f;   // 2^-64
 constexpr int kNormBlocks = 304;                  // at most, per matrix
 
+template <int kN = kThreads>
 __device__ __forceinline__ float2 block_sum(float2 v) {
-    __shared__ float2 s[kThreads / 32];
+    __shared__ float2 s[kN / 32];
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
@@ -58,7 +59,7 @@ __device__ __forceinline__ float2 block_sum(float2 v) {
     __syncthreads();
     float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kN / 32; ++w) {
         t.x += s[w].x;
         t.y += s[w].y;
     }
@@ -279,6 +280,24 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, const float4& v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t saddr, uint32_t rank) {
+    uint32_t at;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
                  : "r"(at)
                  : "memory");
     return v;
@@ -709,42 +728,62 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 }
 
 // ----------------------------------------------------------- small matrices --
-// A matrix whose X and A fit one SM's shared memory: one CTA takes it through
-// all steps in one launch, X, A and P never leaving the SM (P overwrites A,
-// X' overwrites X: a product is complete before its epilogue writes, and an
-// epilogue thread reads no row but its own).  Panels hold rn rows; an MMA's
-// 128 rows reach past them into what follows, which only makes rows of the
-// product that nobody reads.  Eight warps share an epilogue: a thread has a
-// row and half of the columns.
+// A matrix of up to 128 rows whose X and A fit the shared memory of one SM, or
+// of the SMs of a cluster: one launch takes it through all steps, X, A and P
+// never leaving the SMs (P overwrites A, X' overwrites X: a product is
+// complete before its epilogue writes, and an epilogue thread reads no row but
+// its own).  The CTAs of a cluster have the columns of X in equal shares of
+// whole panels; each makes its share of A = X X^T, adds up all shares, in the
+// order of the CTAs, and goes on with the same A and its own columns.
+//
+// Panels hold rn rows, a panel's lo part behind its hi part: as a K-major right
+// operand the two are one of 2 rn rows, and the product of a hi panel with
+// both is one MMA (an MMA takes 50 ns here whatever its N).  An MMA's 128 rows
+// reach past a panel into what follows, which only makes rows of the product
+// that nobody reads.  Sixteen warps share an epilogue: a thread has a row and
+// every fourth 16 of the columns.
+constexpr int kSmallThreads = 512;
+constexpr int kSmallGroups = kSmallThreads / 128;
+
 struct Small {
-    int r, c, rn, cn;      // rn, cn: padded to 16
-    int xp, ap;            // panels of X and of A
+    int r, c, rn;          // rn: padded to 16
+    int xp, ap;            // panels of a CTA's share of X, and of A
+    int ctas;              // of the cluster
     bool tall;
     int steps;
     float a, b, c2, eps;
 };
+constexpr int kMaxShares = 8;
 constexpr int kSmallChunk = 256;   // K of a sum in tensor memory (as kChunk)
 
-template <bool kSplit>
-size_t small_bytes(int rn, int xp, int ap) {
-    return (size_t)(kSplit ? 2 : 1) * (xp + ap) * rn * 128 + (kBlock - 16) * 128 + 64 + 1024;
+// A and P; before them, where there is a cluster, a CTA's share of A in 32 bits.
+__host__ __device__ inline uint32_t small_a_bytes(int parts, int rn, int ap, int ctas) {
+    const uint32_t a = (uint32_t)(parts * ap * rn * 128), sums = (uint32_t)(rn * rn * 4);
+    return ctas > 1 && sums > a ? (sums + 1023) / 1024 * 1024 : a;
+}
+size_t small_bytes(int parts, int rn, int xp, int ap, int ctas) {
+    return (size_t)parts * xp * rn * 128 + small_a_bytes(parts, rn, ap, ctas) +
+           (kBlock - 16) * 128 + 64 + 1024;
 }
 
-template <typename T, bool kSplit>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool kSplit, int V>
+__global__ void __launch_bounds__(kSmallThreads, 1)
 k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out, LearnState* st) {
     constexpr int kParts = kSplit ? 2 : 1;
     extern __shared__ unsigned char raw[];
+    __shared__ float2 s_norm;
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const uint32_t pb = (uint32_t)q.rn * 128u;                 // bytes of a panel
-    const uint32_t x_part = q.xp * pb, a_part = q.ap * pb;     // from hi to lo
+    const uint32_t pb = (uint32_t)q.rn * 128u;   // bytes of a part of a panel
     unsigned char* xs = smem;
-    unsigned char* as = smem + kParts * x_part;
-    uint64_t* mbar = reinterpret_cast<uint64_t*>(as + kParts * a_part + (kBlock - 16) * 128);
+    unsigned char* as = smem + kParts * q.xp * pb;
+    uint64_t* mbar = reinterpret_cast<uint64_t*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas) +
+                                                 (kBlock - 16) * 128);
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, group = warp >> 2;
     const int row = quarter * 32 + lane;
+    const bool shared = q.ctas > 1;
+    const int rank = (int)blockIdx.x % q.ctas;
     if (tid == 0) {
         mbar_init(mbar);
         mbar_init(mbar + 1);
@@ -753,31 +792,60 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     if (warp == 0) tmem_alloc(s_taddr, 512);
     pdl_begin();
     const size_t elems = (size_t)q.r * q.c;
-    const T* g = grad + blockIdx.x * elems;
-    float2 sq = make_float2(0.0f, 0.0f);
-    for (int i = tid; i < (int)elems; i += kThreads) {
-        float v[1];
-        Pack<T, 1>::load(g + i, v);
-        sq.x = fmaf(v[0], v[0], sq.x);
-        sq.y = fmaf(v[0] * kDown, v[0] * kDown, sq.y);
+    const T* g = grad + blockIdx.x / q.ctas * elems;
+    // this CTA's columns of X, and of those that the matrix has, padded to 16
+    const int col0 = rank * q.xp * kPanel;
+    const int mine = max(0, min(q.xp * kPanel, q.c - col0)), cn = (mine + 15) / 16 * 16;
+    {   // (any share of the elements serves the norm)
+        float2 sq = make_float2(0.0f, 0.0f);
+        const int n = (int)(elems / V), step = kSmallThreads * q.ctas;
+#pragma unroll 4
+        for (int i = rank * kSmallThreads + tid; i < n; i += step) {
+            float v[V];
+            Pack<T, V>::load(g + (size_t)i * V, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                sq.x = fmaf(v[j], v[j], sq.x);
+                sq.y = fmaf(v[j] * kDown, v[j] * kDown, sq.y);
+            }
+        }
+        sq = block_sum<kSmallThreads>(sq);
+        if (tid == 0) s_norm = sq;
     }
-    const float inv = norm_inverse(block_sum(sq), q.eps);
-    for (int i = tid; i < q.rn * q.xp * 8; i += kThreads) {
+    float2 sq = make_float2(0.0f, 0.0f);
+    if (shared) {
+        __syncwarp();
+        cluster_sync();
+        for (int k = 0; k < q.ctas; ++k) {
+            const float2 u = ld_cluster2(smem_u32(&s_norm), k);
+            sq.x += u.x;
+            sq.y += u.y;
+        }
+    } else {
+        __syncthreads();
+        sq = s_norm;
+    }
+    const float inv = norm_inverse(sq, q.eps);
+#pragma unroll 2
+    for (int i = tid; i < q.rn * q.xp * 8; i += kSmallThreads) {
         const int xr = q.tall ? i % q.rn : i / (q.xp * 8);
-        const int c0 = (q.tall ? i / q.rn : i % (q.xp * 8)) * 8;
+        const int l0 = (q.tall ? i / q.rn : i % (q.xp * 8)) * 8, c0 = col0 + l0;
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float u[1] = {0.0f};
+        for (int j = 0; j < 8; j += V) {
+            float u[V] = {};
             if (xr < q.r && c0 + j < q.c)
-                Pack<T, 1>::load(g + (q.tall ? (c0 + j) * q.r + xr : xr * q.c + c0 + j), u);
-            v[j] = u[0] * inv * kScaleX;
+                Pack<T, V>::load(g + (q.tall ? (size_t)(c0 + j) * q.r + xr
+                                             : (size_t)xr * q.c + c0 + j), u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
         }
         uint4 h[kParts];
         halves<kParts>(v, h);
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
-            *reinterpret_cast<uint4*>(xs + p * x_part + panel_at(xr, c0, q.rn) * 2) = h[p];
+            *reinterpret_cast<uint4*>(xs + l0 / kPanel * kParts * pb + p * pb +
+                                      panel_at(xr, l0 % kPanel, q.rn) * 2) = h[p];
     }
     fence_async_smem();
     tc_fence_before();
@@ -789,21 +857,31 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     const bool busy = quarter * 32 < q.rn;   // this warp has rows
     uint32_t ph[2] = {0u, 0u};
     bool ok = true;
-    // D (columns d, cross terms at d + 256) = the rows at l times the operand at r, K = 16 ks
-    auto issue = [&](int buf, uint32_t d, uint32_t l, uint32_t l_part, uint32_t r, uint32_t r_part,
-                     int n, int k_begin, int k_end, bool mn) {
-        const uint32_t idesc = (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
-                               ((uint32_t)(kBlock >> 4) << 24);
+    // D = the rows of the panels at l times the operand at r, K = 16 ks: hi times hi in the
+    // columns at d, the cross terms in those at x.  mn: r's rows are K (X), not columns of D.
+    auto issue = [&](int buf, uint32_t d, uint32_t x, uint32_t l, uint32_t r, int n, int k_begin,
+                     int k_end, bool mn) {
+        const auto idesc = [&](int columns) {
+            return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(columns >> 3) << 17) |
+                   ((uint32_t)(kBlock >> 4) << 24);
+        };
+        const uint32_t lbo = mn ? kParts * pb : 16;
         for (int k = k_begin; k < k_end; ++k) {
-            const uint32_t ka = (uint32_t)(k >> 2) * pb + (uint32_t)(k & 3) * 32u;
+            const uint32_t ka = (uint32_t)(k >> 2) * kParts * pb + (uint32_t)(k & 3) * 32u;
             const uint32_t kb = mn ? (uint32_t)k * 2048u : ka;
-            const uint64_t dl = desc_sw128(l + ka, 16), dr = desc_sw128(r + kb, mn ? pb : 16);
+            const uint64_t hi = desc_sw128(l + ka, 16), rhi = desc_sw128(r + kb, lbo);
             const uint32_t more = k > k_begin;
-            mma_f16(tmem + d, dl, dr, idesc, more);
-            if (kSplit) {
-                mma_f16(tmem + d + 256, dl, desc_sw128(r + r_part + kb, mn ? pb : 16), idesc, more);
-                mma_f16(tmem + d + 256, desc_sw128(l + l_part + ka, 16), dr, idesc, 1);
+            if (!kSplit) {
+                mma_f16(tmem + d, hi, rhi, idesc(n), more);
+                continue;
             }
+            if (mn) {
+                mma_f16(tmem + d, hi, rhi, idesc(n), more);
+                mma_f16(tmem + x, hi, desc_sw128(r + pb + kb, lbo), idesc(n), more);
+            } else {   // (x is d + n)
+                mma_f16(tmem + d, hi, rhi, idesc(2 * n), more);
+            }
+            mma_f16(tmem + x, desc_sw128(l + pb + ka, 16), rhi, idesc(n), 1);
         }
         mma_commit(mbar + buf);
     };
@@ -814,18 +892,19 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         return ok;
     };
     // sixteen columns of this row of D
-    auto sums = [&](uint32_t d, float (&v)[16]) {
+    auto sums = [&](uint32_t d, uint32_t x, float (&v)[16]) {
         uint32_t u[16], w[16];
         __syncwarp();
         tmem_ld16(trow + d, u);
-        if (kSplit) tmem_ld16(trow + d + 256, w);
+        if (kSplit) tmem_ld16(trow + x, w);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             v[e] = kSplit ? __uint_as_float(u[e]) + __uint_as_float(w[e]) : __uint_as_float(u[e]);
     };
-    auto put = [&](unsigned char* m, uint32_t part, int col, const float (&v)[16]) {
+    auto put = [&](unsigned char* m, int col, const float (&v)[16]) {
         if (row >= q.rn) return;
+        m += col / kPanel * kParts * pb;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             float w[8];
@@ -835,7 +914,8 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             halves<kParts>(w, h);
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
-                *reinterpret_cast<uint4*>(m + p * part + panel_at(row, col + 8 * b, q.rn) * 2) = h[p];
+                *reinterpret_cast<uint4*>(m + p * pb + panel_at(row, col % kPanel + 8 * b, q.rn) * 2) =
+                    h[p];
         }
     };
     auto ready = [&]() {   // what the threads wrote is ready for the next product
@@ -844,54 +924,105 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         __syncthreads();
         tc_fence_after();
     };
-    const int r_units = q.rn / 16, r_mine = (r_units + 1 - half) / 2;   // units half, half + 2, ..
-    for (int step = 0; step < q.steps && ok; ++step) {
+    // a thread's units of 16 columns of A: group, group + 4
+    const int r_units = q.rn / 16, r_mine = (r_units + kSmallGroups - 1 - group) / kSmallGroups;
+    constexpr int kMost = 128 / 16 / kSmallGroups;
+    // (a CTA that gave up skips the work but not the cluster's meetings)
+    for (int step = 0; step < q.steps && (ok || shared); ++step) {
         // ---- A = X X^T, in chunks of K through two accumulators
-        {
-            float acc[4][16];
-            const int ks = q.cn / 16, per = kSmallChunk / 16, chunks = (ks + per - 1) / per;
-            if (tid == 0) issue(0, 0, x0, x_part, x0, x_part, q.rn, 0, min(per, ks), false);
-            for (int ch = 0; ch < chunks; ++ch) {
-                if (tid == 0 && ch + 1 < chunks)
-                    issue((ch + 1) & 1, 128 * ((ch + 1) & 1), x0, x_part, x0, x_part, q.rn,
-                          (ch + 1) * per, min((ch + 2) * per, ks), false);
-                if (!await(ch & 1)) break;
-                if (busy) {
+        float acc[kMost][16];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        if (m < r_mine) {
-                            float v[16];
-                            sums(128 * (ch & 1) + 16 * (half + 2 * m), v);
+        for (int m = 0; m < kMost; ++m)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) acc[m][e] = ch ? acc[m][e] + v[e] : v[e];
-                        }
-                    }
-                }
-                tc_fence_before();
-                if (ch + 2 < chunks) __syncthreads();   // its accumulator is refilled next
-                tc_fence_after();
-            }
-            if (!ok) break;
+            for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
+        const int ks = cn / 16, per = kSmallChunk / 16, chunks = (ks + per - 1) / per;
+        if (ok && tid == 0 && chunks > 0)
+            issue(0, 0, q.rn, x0, x0, q.rn, 0, min(per, ks), false);
+        for (int ch = 0; ch < chunks && ok; ++ch) {
+            if (tid == 0 && ch + 1 < chunks)
+                issue((ch + 1) & 1, 256 * ((ch + 1) & 1), 256 * ((ch + 1) & 1) + q.rn, x0, x0, q.rn,
+                      (ch + 1) * per, min((ch + 2) * per, ks), false);
+            if (!await(ch & 1)) break;
             if (busy) {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < kMost; ++m) {
                     if (m < r_mine) {
+                        float v[16];
+                        const uint32_t at = 256 * (ch & 1) + 16 * (group + kSmallGroups * m);
+                        sums(at, at + q.rn, v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
-                        put(as, a_part, 16 * (half + 2 * m), acc[m]);
+                        for (int e = 0; e < 16; ++e) acc[m][e] += v[e];
                     }
+                }
+            }
+            tc_fence_before();
+            if (ch + 2 < chunks) __syncthreads();   // its accumulator is refilled next
+            tc_fence_after();
+        }
+        if (shared) {   // the sum of the cluster's shares: [column / 4][row]
+            float4* mine4 = reinterpret_cast<float4*>(as);
+            if (row < q.rn) {
+#pragma unroll
+                for (int m = 0; m < kMost; ++m)
+                    if (m < r_mine)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            mine4[(4 * (group + kSmallGroups * m) + e / 4) * q.rn + row] = make_float4(
+                                acc[m][e], acc[m][e + 1], acc[m][e + 2], acc[m][e + 3]);
+            }
+            __syncwarp();
+            cluster_sync();
+            // each CTA adds up a part of them and leaves the sum with all
+            for (int i = rank * kSmallThreads + tid; i < q.rn * q.rn / 4;
+                 i += q.ctas * kSmallThreads) {
+                float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                for (int k = 0; k < q.ctas; ++k) {
+                    const float4 u = ld_cluster(a0 + (uint32_t)i * 16, k);
+                    t.x += u.x;
+                    t.y += u.y;
+                    t.z += u.z;
+                    t.w += u.w;
+                }
+                for (int k = 0; k < q.ctas; ++k) st_cluster(a0 + (uint32_t)i * 16, k, t);
+            }
+            __syncwarp();
+            cluster_sync();
+            if (row < q.rn) {
+#pragma unroll
+                for (int m = 0; m < kMost; ++m)
+                    if (m < r_mine)
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 u = mine4[(4 * (group + kSmallGroups * m) + e / 4) * q.rn + row];
+                            acc[m][e] = u.x;
+                            acc[m][e + 1] = u.y;
+                            acc[m][e + 2] = u.z;
+                            acc[m][e + 3] = u.w;
+                        }
+            }
+            __syncthreads();   // A takes the place of the shares
+        }
+        if (!ok) continue;
+        if (busy) {
+#pragma unroll
+            for (int m = 0; m < kMost; ++m) {
+                if (m < r_mine) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
+                    put(as, 16 * (group + kSmallGroups * m), acc[m]);
                 }
             }
         }
         ready();
         // ---- P = a I + b A + c A A
-        if (tid == 0) issue(0, 0, a0, a_part, a0, a_part, q.rn, 0, r_units, false);
-        if (!await(0)) break;
+        if (tid == 0) issue(0, 0, q.rn, a0, a0, q.rn, 0, r_units, false);
+        if (!await(0)) continue;
         if (busy) {
             for (int m = 0; m < r_mine; ++m) {
-                const int col = 16 * (half + 2 * m);
+                const int col = 16 * (group + kSmallGroups * m);
                 float v[16];
-                sums(col, v);
+                sums(col, col + q.rn, v);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     v[e] *= q.c2 * (kScaleP / (kScaleA * kScaleA));
@@ -906,40 +1037,41 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
 #pragma unroll
                             for (int e = 0; e < 8; ++e) w[e] = v[8 * b + e];
                             add_halves(w, *reinterpret_cast<const uint4*>(
-                                              as + p * a_part + panel_at(row, col + 8 * b, q.rn) * 2),
+                                              as + (col / kPanel * kParts + p) * pb +
+                                              panel_at(row, col % kPanel + 8 * b, q.rn) * 2),
                                        q.b * (kScaleP / kScaleA));
 #pragma unroll
                             for (int e = 0; e < 8; ++e) v[8 * b + e] = w[e];
                         }
                 }
-                put(as, a_part, col, v);
+                put(as, col, v);
             }
         }
         ready();
         // ---- X' = P X, 256 columns at a time; the last one is the result
-        for (int c0 = 0; c0 < q.cn; c0 += 256) {
-            const int n = min(256, q.cn - c0);
+        for (int c0 = 0; c0 < cn; c0 += 256) {
+            const int n = min(256, cn - c0);
             if (tid == 0)
-                issue(0, 0, a0, a_part, x0 + (uint32_t)(c0 / kPanel) * pb, x_part, n, 0, r_units,
-                      true);
+                issue(0, 0, 256, a0, x0 + (uint32_t)(c0 / kPanel) * kParts * pb, n, 0, r_units, true);
             if (!await(0)) break;
             if (busy) {
-                for (int u = half; u < n / 16; u += 2) {
+                for (int u = group; u < n / 16; u += kSmallGroups) {
                     float v[16];
-                    sums(16 * u, v);
+                    sums(16 * u, 256 + 16 * u, v);
                     const int col = c0 + 16 * u;
                     if (step + 1 < q.steps) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleP;
-                        put(xs, x_part, col, v);
+                        put(xs, col, v);
                     } else if (row < q.r) {
-                        T* o = out + blockIdx.x * elems;
+                        T* o = out + blockIdx.x / q.ctas * elems;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float y[1] = {v[e] * (1.0f / (kScaleP * kScaleX))};
-                            if (col + e < q.c)
-                                Pack<T, 1>::store(o + (q.tall ? (col + e) * q.r + row
-                                                              : row * q.c + col + e), y);
+                            const int oc = col0 + col + e;
+                            if (oc < q.c)
+                                Pack<T, 1>::store(o + (q.tall ? (size_t)oc * q.r + row
+                                                              : (size_t)row * q.c + oc), y);
                         }
                     }
                 }
@@ -961,18 +1093,24 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+    if (shared) {   // (the others may still read this CTA's norm where there was no step)
+        __syncwarp();
+        cluster_sync();
+    }
 }
 
 // ----------------------------------------------------------------- plans --
-constexpr size_t kSmemMax = 227 * 1024 - 128;   // (the norm has a little of its own)
+constexpr size_t kSmemMax = 227 * 1024 - 256;   // (the norm has a little of its own)
+
+constexpr size_t kSmemHalf = 120 * 1024;
 
 struct Plan {
     int64_t r, c, rp, cp;   // padded
     bool tall;
     int parts;
-    bool small;             // one CTA takes a matrix through all steps
+    int ctas;               // on chip: a cluster of them takes a matrix through all steps; else 0
 };
-Plan plan_of(int64_t m, int64_t n, int dtype) {
+Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
     Plan p;
     p.tall = m > n;
     p.r = p.tall ? n : m;
@@ -982,10 +1120,19 @@ Plan plan_of(int64_t m, int64_t n, int dtype) {
     const int64_t to = p.c > 1024 ? 256 : 128;   // two widths of a tile of the last product
     p.cp = ceil_div(p.c, to) * to;
     p.parts = dtype == kF32 ? 2 : 1;
-    const int rn = (int)ceil_div(p.r, 16) * 16, xp = (int)ceil_div(p.c, kPanel),
-              ap = (int)ceil_div(p.r, kPanel);
-    p.small = rn <= kBlock && (dtype == kF32 ? small_bytes<true>(rn, xp, ap)
-                                             : small_bytes<false>(rn, xp, ap)) <= kSmemMax;
+    // on chip: shares of about 256 columns, more where memory or the SMs ask for it
+    p.ctas = 0;
+    const int rn = (int)ceil_div(p.r, 16) * 16, ap = (int)ceil_div(p.r, kPanel);
+    if (rn <= kBlock && p.c <= 65536) {
+        const auto fits = [&](int n) {
+            return small_bytes(p.parts, rn, (int)ceil_div(ceil_div(p.c, kPanel), n), ap, n) <= kSmemMax;
+        };
+        int n = 1;
+        while (n < kMaxShares && (!fits(n) || (n * 256 < p.c && batch * n * 2 <= 152))) n *= 2;
+        // (of many rows and columns the separate products are faster: 100 x 4000 in 16 bits 96
+        // against 129 us; 128 x 2000 in 32 bits 117 against 104)
+        if (fits(n) && (rn <= 64 || p.c <= n * 256)) p.ctas = n;
+    }
     return p;
 }
 
@@ -1039,14 +1186,31 @@ cudaError_t symmetric(const Product& q, LearnState* st, int n_sms, cudaStream_t 
 template <typename T, bool kSplit>
 cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
     constexpr int kParts = kSplit ? 2 : 1;
-    const Plan p = plan_of(o.m, o.n, o.dtype);
-    if (o.steps > 0 && p.small) {
-        const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16, (int)ceil_div(p.c, 16) * 16,
-                      (int)ceil_div(p.c, kPanel), (int)ceil_div(p.r, kPanel), p.tall, o.steps,
-                      o.a, o.b, o.c, o.eps};
-        return launch_pdl(k_orth_small<T, kSplit>, dim3((unsigned)o.batch), dim3(kThreads),
-                          small_bytes<kSplit>(q.rn, q.xp, q.ap), s, (const T*)o.grad, q, (T*)o.out,
-                          st);
+    const Plan p = plan_of(o.batch, o.m, o.n, o.dtype);
+    if (o.steps > 0 && p.ctas > 0) {
+        constexpr int V = VecOf<T>::n;
+        const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16,
+                      (int)ceil_div(ceil_div(p.c, kPanel), p.ctas), (int)ceil_div(p.r, kPanel),
+                      p.ctas, p.tall, o.steps, o.a, o.b, o.c, o.eps};
+        const bool vec = !p.tall && p.c % V == 0 && aligned16(o.grad);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(o.batch * p.ctas));
+        cfg.blockDim = dim3(kSmallThreads);
+        cfg.dynamicSmemBytes = small_bytes(kParts, q.rn, q.xp, q.ap, q.ctas);
+        // CTAs of a cluster wait for one another holding all of their SM's tensor memory: more
+        // than half of its shared memory keeps a second one from waiting for that
+        if (p.ctas > 1 && cfg.dynamicSmemBytes < kSmemHalf) cfg.dynamicSmemBytes = kSmemHalf;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)p.ctas;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, vec ? k_orth_small<T, kSplit, V> : k_orth_small<T, kSplit, 1>,
+                                  (const T*)o.grad, q, (T*)o.out, st);
     }
     Carve cv{static_cast<unsigned char*>(ws)};
     const Space w = carve(cv, o.batch, p);
@@ -1152,7 +1316,7 @@ cudaError_t prepare_type() {
 size_t orth_workspace(int64_t batch, int64_t m, int64_t n, int dtype) {
     if (batch == 0 || m == 0 || n == 0) return 0;
     Carve cv{nullptr};
-    carve(cv, batch, plan_of(m, n, dtype));
+    carve(cv, batch, plan_of(batch, m, n, dtype));
     return cv.used;
 }
 
@@ -1161,12 +1325,12 @@ cudaError_t prepare_orth() {
     if (e == cudaSuccess) e = prepare_type<true>();
     if (e == cudaSuccess) e = prepare_one<false, 256, false>();
     if (e == cudaSuccess) e = prepare_one<false, 256, true, 2>();
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_orth_small<float, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_orth_small<__nv_bfloat16, false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    for (const void* k : {(const void*)k_orth_small<float, true, 1>,
+                          (const void*)k_orth_small<float, true, 4>,
+                          (const void*)k_orth_small<__nv_bfloat16, false, 1>,
+                          (const void*)k_orth_small<__nv_bfloat16, false, 8>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     return e;
 }
 

@@ -34,7 +34,8 @@ CASES = [
     (1, 1, 1), (3, 1, 7), (2, 9, 1), (8, 64, 64), (4, 64, 19), (5, 3, 64), (1, 16, 700),
     (1, 2000, 16), (2, 65, 64), (1, 127, 129), (1, 128, 128), (1, 200, 100), (2, 150, 300),
     (1, 513, 257), (1, 300, 1025), (33, 20, 31), (1, 128, 3000), (1, 640, 512), (1, 512, 768),
-    (1, 1301, 1154),
+    (1, 1301, 1154), (1, 10, 3000), (2, 100, 900), (1, 5000, 30), (3, 128, 1024), (1, 7, 2100),
+    (40, 50, 600), (1, 128, 2000), (1, 2, 40000),
 ]
 
 
