@@ -924,6 +924,14 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         __syncthreads();
         tc_fence_after();
     };
+    // the result's element (r, c) of the block of up to 256 columns at c0, of the type's size in
+    // 16-byte chunks, in the bytes of X's panels there
+    const auto staged = [&](int c0, int r, int c) {
+        constexpr int kChunk16 = VecOf<T>::n;
+        const int pitch = min(256, q.xp * kPanel - c0);
+        return reinterpret_cast<T*>(xs + c0 / kPanel * kParts * pb) + (size_t)r * pitch +
+               (((c / kChunk16) ^ (r & 7)) * kChunk16 + c % kChunk16);
+    };
     // a thread's units of 16 columns of A: group, group + 4
     const int r_units = q.rn / 16, r_mine = (r_units + kSmallGroups - 1 - group) / kSmallGroups;
     constexpr int kMost = 128 / 16 / kSmallGroups;
@@ -973,18 +981,28 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             __syncwarp();
             cluster_sync();
             // each CTA adds up a part of them and leaves the sum with all
-            for (int i = rank * kSmallThreads + tid; i < q.rn * q.rn / 4;
-                 i += q.ctas * kSmallThreads) {
-                float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            // (at most four places a thread: 128 x 128 over two CTAs; all loads before the stores)
+            constexpr int kPlaces = 128 * 128 / 4 / (2 * kSmallThreads);
+            float4 t[kPlaces];
+            const auto at_of = [&](int j) { return (j * q.ctas + rank) * kSmallThreads + tid; };
+#pragma unroll
+            for (int j = 0; j < kPlaces; ++j) {
+                t[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (at_of(j) >= q.rn * q.rn / 4) continue;
 #pragma unroll 8
                 for (int k = 0; k < q.ctas; ++k) {
-                    const float4 u = ld_cluster(a0 + (uint32_t)i * 16, k);
-                    t.x += u.x;
-                    t.y += u.y;
-                    t.z += u.z;
-                    t.w += u.w;
+                    const float4 u = ld_cluster(a0 + (uint32_t)at_of(j) * 16, k);
+                    t[j].x += u.x;
+                    t[j].y += u.y;
+                    t[j].z += u.z;
+                    t[j].w += u.w;
                 }
-                for (int k = 0; k < q.ctas; ++k) st_cluster(a0 + (uint32_t)i * 16, k, t);
+            }
+#pragma unroll
+            for (int j = 0; j < kPlaces; ++j) {
+                if (at_of(j) >= q.rn * q.rn / 4) continue;
+                for (int k = 0; k < q.ctas; ++k)
+                    st_cluster(a0 + (uint32_t)at_of(j) * 16, k, t[j]);
             }
             __syncwarp();
             cluster_sync();
@@ -1063,17 +1081,37 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleP;
                         put(xs, col, v);
-                    } else if (row < q.r) {
+                    } else if (q.tall) {   // (the warp's rows are adjacent there)
                         T* o = out + blockIdx.x / q.ctas * elems;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float y[1] = {v[e] * (1.0f / (kScaleP * kScaleX))};
                             const int oc = col0 + col + e;
-                            if (oc < q.c)
-                                Pack<T, 1>::store(o + (q.tall ? (size_t)oc * q.r + row
-                                                              : (size_t)row * q.c + oc), y);
+                            if (row < q.r && oc < q.c)
+                                Pack<T, 1>::store(o + (size_t)oc * q.r + row, y);
+                        }
+                    } else if (row < q.r) {   // staged where these columns of X were
+                        constexpr int kChunk16 = VecOf<T>::n;
+#pragma unroll
+                        for (int e = 0; e < 16; e += kChunk16) {
+                            float y[kChunk16];
+#pragma unroll
+                            for (int b = 0; b < kChunk16; ++b)
+                                y[b] = v[e + b] * (1.0f / (kScaleP * kScaleX));
+                            Pack<T, kChunk16>::store(staged(c0, row, 16 * u + e), y);
                         }
                     }
+                }
+            }
+            if (step + 1 == q.steps && !q.tall) {   // whole rows of the block's columns
+                __syncthreads();
+                T* o = out + blockIdx.x / q.ctas * elems + col0 + c0;
+                const int width = min(n, mine - c0) / V;
+                for (int e = tid; e < q.r * width; e += kSmallThreads) {
+                    const int orow = e / width, oc = (e - orow * width) * V;
+                    float y[V];
+                    Pack<T, V>::load(staged(c0, orow, oc), y);
+                    Pack<T, V>::store(o + (size_t)orow * q.c + oc, y);
                 }
             }
             ready();
