@@ -799,7 +799,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     {   // (any share of the elements serves the norm)
         float2 sq = make_float2(0.0f, 0.0f);
         const int n = (int)(elems / V), step = kSmallThreads * q.ctas;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = rank * kSmallThreads + tid; i < n; i += step) {
             float v[V];
             Pack<T, V>::load(g + (size_t)i * V, v);
@@ -826,7 +826,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         sq = s_norm;
     }
     const float inv = norm_inverse(sq, q.eps);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = tid; i < q.rn * q.xp * 8; i += kSmallThreads) {
         const int xr = q.tall ? i % q.rn : i / (q.xp * 8);
         const int l0 = (q.tall ? i / q.rn : i % (q.xp * 8)) * 8, c0 = col0 + l0;
@@ -1167,9 +1167,7 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
         };
         int n = 1;
         while (n < kMaxShares && (!fits(n) || (n * 256 < p.c && batch * n * 2 <= 152))) n *= 2;
-        // (of many rows and columns the separate products are faster: 100 x 4000 in 16 bits 96
-        // against 129 us; 128 x 2000 in 32 bits 117 against 104)
-        if (fits(n) && (rn <= 64 || p.c <= n * 256)) p.ctas = n;
+        if (fits(n)) p.ctas = n;
     }
     return p;
 }
