@@ -91,11 +91,13 @@ __device__ __forceinline__ void clear_marks(unsigned char* __restrict__ marks, u
 }
 
 // Few tokens: one launch, a token's place is the number of keys before it,
-// counted against all of them in shared memory.
+// counted against all of them in shared memory by sixteen threads.
 constexpr int kRankMost = 4096;
+constexpr int kRankThreads = 512, kRankLanes = 16;
+constexpr int kRankTokens = kRankThreads / kRankLanes;   // of a block
 
 template <typename I>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kRankThreads)
 k_sort_rank(const I* __restrict__ tokens, uint32_t n, uint32_t rows,
             uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
             unsigned char* __restrict__ marks, LearnState* st) {
@@ -103,30 +105,36 @@ k_sort_rank(const I* __restrict__ tokens, uint32_t n, uint32_t rows,
     __shared__ __align__(16) uint32_t key[kRankMost];
     bool bad = false;
     const uint32_t padded = (n + 3) / 4 * 4;
-    for (uint32_t i = threadIdx.x; i < padded; i += kThreads)
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < padded; i += kRankThreads)
         key[i] = i < n ? token_key(tokens[i], rows, &bad) : 0xffffffffu;
     if (bad) atomicOr(&st->error, kErrIndex);
     clear_marks(marks, rows);
     __syncthreads();
-    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t k = key[i];
-    uint32_t at = 0;
-    // keys at or below its own before it, keys below its own after it
-    uint32_t j = 0;
+    const uint32_t i = blockIdx.x * kRankTokens + threadIdx.x / kRankLanes;
+    const uint32_t lane = threadIdx.x % kRankLanes;
+    const uint32_t k = i < n ? key[i] : 0u, own = i / 4;
+    uint32_t at[4] = {0u, 0u, 0u, 0u};
+    // keys at or below its own in the vectors before its own, keys below it from there on ...
 #pragma unroll 4
-    for (; j + 4 <= i; j += 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(key + j);
-        at += (u.x <= k) + (u.y <= k) + (u.z <= k) + (u.w <= k);
+    for (uint32_t v = lane; v < padded / 4; v += kRankLanes) {
+        const uint4 u = reinterpret_cast<const uint4*>(key)[v];
+        const uint32_t t = k + (v < own ? 1u : 0u);
+        at[0] += u.x < t;
+        at[1] += u.y < t;
+        at[2] += u.z < t;
+        at[3] += u.w < t;
     }
-    for (uint32_t e = j; e < min(j + 4, n); ++e) at += e < i ? key[e] <= k : key[e] < k;
-#pragma unroll 4
-    for (j += 4; j < padded; j += 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(key + j);
-        at += (u.x < k) + (u.y < k) + (u.z < k) + (u.w < k);
+    // ... and those equal to it that stand before it in its own vector
+    if (lane == 0)
+        for (uint32_t e = own * 4; e < i; ++e) at[0] += key[e] == k;
+    uint32_t sum = at[0] + at[1] + at[2] + at[3];
+#pragma unroll
+    for (int o = kRankLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0 && i < n) {
+        keys_out[sum] = k;
+        pos_out[sum] = i;
     }
-    keys_out[at] = k;
-    pos_out[at] = i;
 }
 
 // More: a stable LSD radix sort.  A pass is two launches: every block counts
@@ -632,8 +640,8 @@ cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t 
     int from = 0;
     cudaError_t e = cudaSuccess;
     if (n <= kRankMost) {
-        e = launch_pdl(k_sort_rank<I>, dim3((unsigned)ceil_div(n, kThreads)), dim3(kThreads), 0, s,
-                       (const I*)c.tokens, n, rows, w.keys[0], w.pos[0], w.marks, st);
+        e = launch_pdl(k_sort_rank<I>, dim3((unsigned)ceil_div(n, kRankTokens)),
+                       dim3(kRankThreads), 0, s, (const I*)c.tokens, n, rows, w.keys[0], w.pos[0], w.marks, st);
     } else {
         const SortPlan p = sort_plan(c.n, c.rows);
         for (int k = 0; k < p.passes && e == cudaSuccess; ++k) {
