@@ -4,7 +4,9 @@
 //   dtable_v = s sum_{i: t_i = v} dout_i    (in the order of i)
 //
 // Forward: one pass, bound by the bytes of `out`.  Lanes take 16-byte vectors
-// of a row; four rows per thread are in flight.
+// of a row; four rows per thread are in flight (eight: 21.5 us against 16.0),
+// and the output goes past the caches (16.0 -> 11.7 us at 1M x 16 floats from
+// 8192 rows, 5.8 TB/s).
 //
 // Backward: the tokens are sorted (a stable radix sort of (token, i) pairs),
 // so that a table row's terms lie in a run of sorted positions and are summed
@@ -91,7 +93,9 @@ __device__ __forceinline__ void clear_marks(unsigned char* __restrict__ marks, u
 }
 
 // Few tokens: one launch, a token's place is the number of keys before it,
-// counted against all of them in shared memory by sixteen threads.
+// counted against all of them in shared memory by sixteen threads (one thread
+// a token, bound by its own chain of additions, took 43 us at 4000 tokens; now
+// 7, and the radix sort's four launches 18 at 6000).
 constexpr int kRankMost = 4096;
 constexpr int kRankThreads = 512, kRankLanes = 16;
 constexpr int kRankTokens = kRankThreads / kRankLanes;   // of a block
@@ -141,6 +145,9 @@ k_sort_rank(const I* __restrict__ tokens, uint32_t n, uint32_t rows,
 // the digits of its contiguous chunk; then every block sums the count matrix
 // to its own offsets, orders its chunk by the digit in shared memory and
 // writes it out from there, so that stores of a digit lie side by side.
+// 1M tokens of 14 bits: count 2 us, scatter 12.5 us a pass -- offsets 2.5,
+// items 2.2, ranking 3.8 (ballots: the integer pipe), ordering 2.5, writing
+// 1.5 -- of which every part is latency or issue, not bytes (16 MB, 2.4 us).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortItems = 8;                               // most per thread at a time
@@ -319,6 +326,9 @@ constexpr int kMostQ = 32;       // positions per slot
 
 // A block's tile is S slots x q sorted positions, S = kThreads / L; the L
 // lanes of a slot own columns (vectors of V) and walk the slot's positions.
+// Equal tiles, whatever rows they hold, are one wave of blocks; the gather of
+// rows in sorted order is what bounds it: 64 MB of 64-byte rows in 16 us (4
+// TB/s), 33 MB of 2 KB rows and 22 MB of results in 12 us.
 // A run that lies inside a slot goes straight to the table.  A slot keeps two
 // parts of runs that do not: `head`, of a run that began before the slot (and
 // may pass through it), and `tail`, of a run that begins in it and goes on.
@@ -463,7 +473,8 @@ k_embed_reduce(const T* __restrict__ grad, const uint32_t* __restrict__ keys,
 // The runs that leave the tile they begin in: one block per tile (and column
 // block), its slots striding over the tiles the run covers, joined in the
 // order of the slots.  Behind them, blocks that clear the rows without a mark,
-// kZeroRows rows each.
+// kZeroRows rows each (80 MB of them in 10 to 15 us, DRAM writes; marks, not a
+// search of the sorted keys per row, which took 12 us before the first store).
 constexpr int kZeroRows = 64;
 
 template <typename T, int V>
