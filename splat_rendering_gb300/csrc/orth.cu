@@ -45,7 +45,7 @@ __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, in
 // Sums of squares, a block per chunk of a matrix.  The second sum is of the
 // values times 2^-64, and is taken where the first overflows.
 constexpr float kDown = 5.421010862427522e-20f;   // 2^-64
-constexpr int kNormBlocks = 304;                  // at most, per matrix
+constexpr int kNormBlocks = 608;                  // at most, per matrix
 
 template <int kN = kThreads>
 __device__ __forceinline__ float2 block_sum(float2 v) {
@@ -135,24 +135,32 @@ k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t 
     const float inv = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
     const T* m = g + (size_t)blockIdx.y * r * c;
     __half* o = x + (size_t)blockIdx.y * rp * cp;
-    const int64_t chunks = cp / 8;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rp * chunks;
-         i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = tall ? i % rp : i / chunks, c0 = (tall ? i / rp : i % chunks) * 8;
-        float v[8];
+    // a block takes 128 of what is contiguous in g, four a thread, of eight lines of it
+    const int inner = (int)(tall ? rp : cp / 8), lines = (int)(tall ? cp / 8 : rp);
+    const int across = (inner + 127) / 128, pieces = across * ((lines + 7) / 8);
+    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        const int line = piece / across * 8 + (threadIdx.x >> 5);
+        const int i0 = piece % across * 128 + (threadIdx.x & 31);
 #pragma unroll
-        for (int j = 0; j < 8; j += V) {
-            float u[V] = {};
-            if (row < r && c0 + j < c)
-                Pack<T, V>::load(m + (tall ? (c0 + j) * r + row : row * c + c0 + j), u);
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + 32 * q;
+            if (i >= inner || line >= lines) continue;
+            const int64_t row = tall ? i : line, c0 = 8 * (int64_t)(tall ? line : i);
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
+            for (int j = 0; j < 8; j += V) {
+                float u[V] = {};
+                if (row < r && c0 + j < c)
+                    Pack<T, V>::load(m + (tall ? (c0 + j) * r + row : row * c + c0 + j), u);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
+            }
+            uint4 h[kParts];
+            halves<kParts>(v, h);
+            const size_t at = panel_at(row, c0, rp);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) *reinterpret_cast<uint4*>(o + k * lo + at) = h[k];
         }
-        uint4 h[kParts];
-        halves<kParts>(v, h);
-        const size_t at = panel_at(row, c0, rp);
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) *reinterpret_cast<uint4*>(o + k * lo + at) = h[k];
     }
 }
 
@@ -1282,7 +1290,10 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
                           elems, (const float2*)w.part, parts, o.eps, (T*)o.out);
     const auto start = !p.tall && vec && p.c % V == 0 ? k_orth_start<T, kParts, V>
                                                       : k_orth_start<T, kParts, 1>;
-    e = launch_pdl(start, flat(p.rp * p.cp / 8), dim3(kThreads), 0, s, (const T*)o.grad, p.r, p.c,
+    const int64_t inner = p.tall ? p.rp : p.cp / 8, lines = p.tall ? p.cp / 8 : p.rp;
+    const int64_t pieces = ceil_div(inner, 128) * ceil_div(lines, 8);
+    const dim3 grid((unsigned)(pieces < 2432 ? pieces : 2432), B);
+    e = launch_pdl(start, grid, dim3(kThreads), 0, s, (const T*)o.grad, p.r, p.c,
                    p.rp, p.cp, p.tall, (const float2*)w.part, parts, o.eps, w.x[0], w.x_lo);
     const int tm = (int)(p.rp / kBlock);
     for (int k = 0; k < o.steps && e == cudaSuccess; ++k) {
