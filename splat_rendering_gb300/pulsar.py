@@ -17,6 +17,7 @@ None for the current torch stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -408,17 +409,20 @@ def _bytes(code: int, what: str) -> int:
     return int(code)
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def embed_workspace(n: int, rows: int, dim: int) -> int:
     """Bytes of workspace of Learner.embed_backward for n tokens."""
     return _bytes(load().pulsar_embed_workspace(n, rows, dim), "pulsar_embed_workspace")
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def group_norm_workspace(images: int, pixels: int, channels: int, groups: int) -> int:
     """Bytes of workspace of Learner.group_norm and group_norm_backward."""
     return _bytes(load().pulsar_group_norm_workspace(images, pixels, channels, groups),
                   "pulsar_group_norm_workspace")
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def orthogonalize_workspace(batch: int, m: int, n: int, dtype) -> int:
     """Bytes of workspace of Learner.orthogonalize for `batch` m x n matrices."""
     return _bytes(load().pulsar_orthogonalize_workspace(batch, m, n, _dtype_code(dtype)),
