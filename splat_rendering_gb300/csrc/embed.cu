@@ -156,18 +156,18 @@ constexpr int kMaxDigit = 8;                                // bits
 constexpr int kMaxBins = 1 << kMaxDigit;
 constexpr size_t kSortSmem = kSortTile * 8;
 constexpr uint32_t kSortBlocks = 152;                       // at most, one per SM
-constexpr int kWarpBins = kMaxBins / kSortWarps;            // digits a warp sums
 
 // counts[digit][block] of one pass; `keys` NULL: from the tokens.
-template <typename I>
+template <typename I, int kDigit>
 __global__ void __launch_bounds__(kSortThreads)
 k_sort_count(const I* __restrict__ tokens, const uint32_t* __restrict__ keys, uint32_t n,
              uint32_t rows, uint32_t chunk, int shift, int bits, uint32_t* __restrict__ counts,
              unsigned char* __restrict__ marks, LearnState* st) {
     pdl_begin();
-    __shared__ uint32_t h[kSortWarps][kMaxBins];
+    constexpr int kBins = 1 << kDigit;
+    __shared__ uint32_t h[kSortWarps][kBins];
     const int bins = 1 << bits, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < kSortWarps * kMaxBins; e += kSortThreads) (&h[0][0])[e] = 0u;
+    for (int e = threadIdx.x; e < kSortWarps * kBins; e += kSortThreads) (&h[0][0])[e] = 0u;
     __syncthreads();
     const uint32_t lo = blockIdx.x * chunk, hi = min(n, lo + chunk);
     bool bad = false;
@@ -187,27 +187,29 @@ k_sort_count(const I* __restrict__ tokens, const uint32_t* __restrict__ keys, ui
     }
 }
 
-template <typename I>
+template <typename I, int kDigit>
 __global__ void __launch_bounds__(kSortThreads)
 k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
                const uint32_t* __restrict__ pos, uint32_t n, uint32_t rows, uint32_t chunk,
                int shift, int bits, const uint32_t* __restrict__ counts,
                uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
     pdl_begin();
+    constexpr int kBins = 1 << kDigit, kPerWarp = kBins / kSortWarps;   // digits a warp sums
+    static_assert(kBins % 32 == 0 && kPerWarp >= 1, "digits");
     extern __shared__ uint2 s_pair[];                 // [kSortTile] the tile in order
-    __shared__ uint32_t base[kMaxBins];               // next output position of each digit
-    __shared__ uint32_t total[kMaxBins];              // of the sort; then of the tile
-    __shared__ uint32_t start[kMaxBins];              // where a digit begins in the tile
-    __shared__ uint32_t wh[kSortWarps][kMaxBins];     // per warp: count, then offset in the tile
+    __shared__ uint32_t base[kBins];               // next output position of each digit
+    __shared__ uint32_t total[kBins];              // of the sort; then of the tile
+    __shared__ uint32_t start[kBins];              // where a digit begins in the tile
+    __shared__ uint32_t wh[kSortWarps][kBins];     // per warp: count, then offset in the tile
     const int bins = 1 << bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t nb = gridDim.x, b = blockIdx.x;
     {   // a warp's digits together, so that their counts load together
-        uint32_t all[kWarpBins], before[kWarpBins];
+        uint32_t all[kPerWarp], before[kPerWarp];
 #pragma unroll
-        for (int e = 0; e < kWarpBins; ++e) all[e] = before[e] = 0u;
+        for (int e = 0; e < kPerWarp; ++e) all[e] = before[e] = 0u;
         for (uint32_t q = lane; q < nb; q += 32) {
 #pragma unroll
-            for (int e = 0; e < kWarpBins; ++e) {
+            for (int e = 0; e < kPerWarp; ++e) {
                 const int d = warp + e * kSortWarps;
                 const uint32_t c = d < bins ? counts[(size_t)d * nb + q] : 0u;
                 all[e] += c;
@@ -215,7 +217,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
             }
         }
 #pragma unroll
-        for (int e = 0; e < kWarpBins; ++e) {
+        for (int e = 0; e < kPerWarp; ++e) {
             const int d = warp + e * kSortWarps;
             const uint32_t s = __reduce_add_sync(0xffffffffu, all[e]);
             const uint32_t f = __reduce_add_sync(0xffffffffu, before[e]);
@@ -228,9 +230,9 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
     __syncthreads();
     // exclusive scan of the totals, by one warp: digit d's sum to f(d, sum)
     const auto scan_totals = [&](auto&& f) {
-        uint32_t c[kMaxBins / 32], sum = 0;
+        uint32_t c[kBins / 32], sum = 0;
 #pragma unroll
-        for (int e = 0; e < kMaxBins / 32; ++e) sum += c[e] = total[lane * (kMaxBins / 32) + e];
+        for (int e = 0; e < kBins / 32; ++e) sum += c[e] = total[lane * (kBins / 32) + e];
         uint32_t s = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -239,8 +241,8 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
         }
         s -= sum;
 #pragma unroll
-        for (int e = 0; e < kMaxBins / 32; ++e) {
-            f(lane * (kMaxBins / 32) + e, s);
+        for (int e = 0; e < kBins / 32; ++e) {
+            f(lane * (kBins / 32) + e, s);
             s += c[e];
         }
     };
@@ -250,7 +252,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
     for (uint32_t t0 = lo; t0 < hi; t0 += kSortTile) {
         // the warps share the tile's items evenly, each a contiguous run of 32 x rounds
         const int rounds = (int)((min(hi - t0, (uint32_t)kSortTile) + kSortThreads - 1) / kSortThreads);
-        for (int e = threadIdx.x; e < kSortWarps * kMaxBins; e += kSortThreads)
+        for (int e = threadIdx.x; e < kSortWarps * kBins; e += kSortThreads)
             (&wh[0][0])[e] = 0u;
         uint32_t key[kSortItems], val[kSortItems], rank[kSortItems];
         const uint32_t i0 = t0 + warp * (32 * rounds) + lane;
@@ -273,7 +275,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
                 const uint32_t d = (key[j] >> shift) & (bins - 1);
                 uint32_t same = __ballot_sync(0xffffffffu, on);   // (faster than a match)
 #pragma unroll
-                for (int q = 0; q < kMaxDigit; ++q) {
+                for (int q = 0; q < kDigit; ++q) {
                     const uint32_t m = __ballot_sync(0xffffffffu, (d >> q) & 1u);
                     same &= (d >> q) & 1u ? m : ~m;
                 }
@@ -285,7 +287,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
             }
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < kMaxBins; d += kSortThreads) {
+        for (int d = threadIdx.x; d < kBins; d += kSortThreads) {
             uint32_t run = 0;
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
@@ -315,7 +317,7 @@ k_sort_scatter(const I* __restrict__ tokens, const uint32_t* __restrict__ keys,
             pos_out[at] = u.y;
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < kMaxBins; d += kSortThreads) base[d] += total[d];
+        for (int d = threadIdx.x; d < kBins; d += kSortThreads) base[d] += total[d];
         __syncthreads();
     }
 }
@@ -658,13 +660,21 @@ cudaError_t backward(const EmbedCall& c, LearnState* st, void* ws, cudaStream_t 
         for (int k = 0; k < p.passes && e == cudaSuccess; ++k) {
             const uint32_t* ki = k ? w.keys[(k - 1) & 1] : nullptr;
             const uint32_t* pi = k ? w.pos[(k - 1) & 1] : nullptr;
-            e = launch_pdl(k_sort_count<I>, dim3(p.blocks), dim3(kSortThreads), 0, s,
-                           (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits, p.bits, w.counts,
-                           w.marks, st);
-            if (e == cudaSuccess)
-                e = launch_pdl(k_sort_scatter<I>, dim3(p.blocks), dim3(kSortThreads), kSortSmem, s,
-                               (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
-                               (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
+            // (the forms differ in the bins they have room for: 14 bits in two passes of 128
+            // bins take 3.3 us less than with room for 256)
+            const auto pass = [&](auto count, auto scatter) {
+                cudaError_t f = launch_pdl(count, dim3(p.blocks), dim3(kSortThreads), 0, s,
+                                           (const I*)c.tokens, ki, n, rows, p.chunk, k * p.bits,
+                                           p.bits, w.counts, w.marks, st);
+                if (f == cudaSuccess)
+                    f = launch_pdl(scatter, dim3(p.blocks), dim3(kSortThreads), kSortSmem, s,
+                                   (const I*)c.tokens, ki, pi, n, rows, p.chunk, k * p.bits, p.bits,
+                                   (const uint32_t*)w.counts, w.keys[k & 1], w.pos[k & 1]);
+                return f;
+            };
+            e = p.bits <= 6   ? pass(k_sort_count<I, 6>, k_sort_scatter<I, 6>)
+                : p.bits == 7 ? pass(k_sort_count<I, 7>, k_sort_scatter<I, 7>)
+                              : pass(k_sort_count<I, 8>, k_sort_scatter<I, 8>);
         }
         from = (p.passes - 1) & 1;
     }
@@ -689,11 +699,12 @@ size_t embed_workspace(int64_t n, int64_t rows, int64_t dim) {
 }
 
 cudaError_t prepare_embed() {
-    cudaError_t e = cudaFuncSetAttribute(
-        k_sort_scatter<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_sort_scatter<int64_t>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+    cudaError_t e = cudaSuccess;
+    for (const void* k : {(const void*)k_sort_scatter<int32_t, 6>, (const void*)k_sort_scatter<int32_t, 7>,
+                          (const void*)k_sort_scatter<int32_t, 8>, (const void*)k_sort_scatter<int64_t, 6>,
+                          (const void*)k_sort_scatter<int64_t, 7>, (const void*)k_sort_scatter<int64_t, 8>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
     return e;
 }
 
