@@ -199,6 +199,16 @@ k_orth_scale(const T* __restrict__ g, int64_t elems, const float2* __restrict__ 
 // limits the result: hi hi and the cross terms have accumulators of their
 // own, and both are drained and summed in registers every kChunk panels.
 //
+// Diagonals.  In single halves the roundings of A and P average out but for
+// those of their diagonals: where the rows are nearly orthogonal, as they are in
+// an oblong matrix, each diagonal's elements are nearly equal, are rounded alike,
+// and move every singular value the same way (35 x 1330: the result 2.0 times as
+// far off as its own rounding to 16 bits, now 1.06).  So A's diagonal keeps what
+// its rounding left (`rest`) for P's, and P's is made exact by a factor per row
+// of X' (`rows`, within 2^-11 of 1), for which a row of P counts as scaled: its
+// other elements move by less than their own rounding.  It costs 3 of 351 us at
+// 2048 x 4096, 2 to 3 of 52 at 128 x 512 on chip.
+//
 // Where a product has too few tiles for the SMs (the symmetric ones of a
 // small or oblong matrix), a cluster of kCluster CTAs shares a tile: each
 // takes a part of K, leaves its sums in shared memory, and finishes a part of
@@ -218,6 +228,7 @@ struct Product {
     size_t d_lo, d_size;      // also C's
     int64_t d_rows;
     float alpha, beta, gamma;
+    float *rest, *rows;       // [batch][rows], single halves (see Diagonals)
     // the result, where `out` is given: [r, c] or its transpose, unpadded
     void* out;
     int64_t out_r, out_c;
@@ -340,6 +351,13 @@ __device__ __forceinline__ void lower_tile(int t, int* i, int* j) {
     *j = t - row * (row + 1) / 2;
 }
 
+// What a row of X' is scaled with for P's diagonal: its value over its rounded one.
+// (Not where that is subnormal, whose rounding may be large, or infinite.)
+__device__ __forceinline__ float row_factor(float v, float rounded) {
+    const float m = fabsf(rounded);
+    return m >= 6.103515625e-5f && m <= 65504.0f ? __fdividef(v, rounded) : 1.0f;
+}
+
 // C's halves of eight columns added to v.
 __device__ __forceinline__ void add_halves(float (&v)[8], const uint4& w, float beta) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -416,7 +434,8 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     const int row = quarter * 32 + lane;
     // columns col .. col + kCols - 1 of the tile from their finished sums
     using CHalves = uint4[kCols / 8][kParts];
-    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float (&v)[kCols]) {
+    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float alpha,
+                      float rest, float (&v)[kCols]) {
         const int64_t grow = (int64_t)i * kBlock + row, gcol = (int64_t)j * kN + col;
         const int jb = j * (kN / kBlock) + col / kBlock;   // the columns' block of 128
         if (kGram && jb > i) return;   // above the diagonal: the mirrored block's
@@ -427,19 +446,36 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         __half* column = d + ((grow / kPanel) * q.d_rows + gcol) * kPanel + (row & 7);
         const int chunk0 = (int)(gcol & (kPanel - 1)) >> 3, rchunk = (row & (kPanel - 1)) >> 3;
         const int on = i == jb ? row - col % kBlock : -1;   // the diagonal's place in them
+        float exact = 0.0f, rounded = 0.0f;                 // its value, where it is here
 #pragma unroll
         for (int b = 0; b < kCols / 8; ++b) {
             float w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = q.alpha * v[8 * b + e];
+            for (int e = 0; e < 8; ++e) w[e] = alpha * v[8 * b + e];
             if (kGram && q.c) {
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) add_halves(w, c[b][p], q.beta);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] += 8 * b + e == on ? q.gamma : 0.0f;
+                if (!kSplit && i == jb) {
+                    const __half* e16 = reinterpret_cast<const __half*>(&c[b][0]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] += 8 * b + e == on
+                                    ? rest * (q.beta + 2.0f * alpha * __half2float(e16[e]))
+                                    : 0.0f;
+                }
             }
             uint4 h[kParts];
             halves<kParts>(w, h);
+            if (kGram && !kSplit && i == jb) {
+                const __half* e16 = reinterpret_cast<const __half*>(&h[0]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    exact = 8 * b + e == on ? w[e] : exact;
+                    rounded = 8 * b + e == on ? __half2float(e16[e]) : rounded;
+                }
+            }
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 *reinterpret_cast<uint4*>(line + p * q.d_lo + (((chunk0 + b) ^ (row & 7)) << 3)) =
@@ -452,11 +488,14 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                 }
             }
         }
+        if (kGram && !kSplit && on >= 0 && on < kCols)
+            (q.c ? q.rows : q.rest)[z * q.d_rows + grow] =
+                q.c ? row_factor(exact, rounded) : exact - rounded;
     };
 
     // a panel of the result from its sums: through the warp's exchange, so that
     // a warp writes whole rows (of the transpose, whole columns as they are)
-    auto store_result = [&](int z, int i, int j, int col, const float (&v)[kPanel]) {
+    auto store_result = [&](int z, int i, int j, int col, float alpha, const float (&v)[kPanel]) {
         const int64_t r0 = (int64_t)i * kBlock + quarter * 32, c0 = (int64_t)j * kN + col;
         const size_t base = (size_t)z * q.out_r * q.out_c;
         if (q.tall) {
@@ -466,7 +505,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 #pragma unroll
             for (int e = 0; e < kPanel; ++e) {
                 if (e >= n) continue;
-                const float y = q.alpha * v[e];
+                const float y = alpha * v[e];
                 if (q.dtype == kF32)
                     static_cast<float*>(q.out)[at + e * q.out_r] = y;
                 else
@@ -482,7 +521,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                 __syncwarp();
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    x[lane * kRowPitch + e] = __float_as_uint(q.alpha * v[32 * h + e]);
+                    x[lane * kRowPitch + e] = __float_as_uint(alpha * v[32 * h + e]);
                 __syncwarp();
                 if (c0 + 32 * h + lane < q.out_c) {
                     float* o = static_cast<float*>(q.out) + base + r0 * q.out_c + c0 + 32 * h + lane;
@@ -495,7 +534,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const __nv_bfloat162 h =
-                    __floats2bfloat162_rn(q.alpha * v[2 * e], q.alpha * v[2 * e + 1]);
+                    __floats2bfloat162_rn(alpha * v[2 * e], alpha * v[2 * e + 1]);
                 x[lane * kRowPitch + e] = *reinterpret_cast<const uint32_t*>(&h);
             }
             __syncwarp();
@@ -630,6 +669,10 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                                              rank * kCols + 8 * b,
                                          q.d_rows));
             }
+            float alpha = q.alpha;
+            if (!kSplit && !kGram) alpha *= q.rows[z * q.d_rows + (int64_t)i * kBlock + row];
+            const float rest = kGram && !kSplit && q.c
+                                   ? q.rest[z * q.d_rows + (int64_t)i * kBlock + row] : 0.0f;
             float v[kPanel];
             bool ok = true;
             if (kSplit) {
@@ -698,9 +741,9 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                     float w[kCols];
 #pragma unroll
                     for (int e = 0; e < kCols; ++e) w[e] = v[e % kPanel];
-                    finish(z, i, j, col, c[0], w);   // (one panel where there is a C)
+                    finish(z, i, j, col, c[0], alpha, rest, w);   // (one panel where there is a C)
                 } else {   // the result
-                    store_result(z, i, j, col, v);
+                    store_result(z, i, j, col, alpha, v);
                 }
             }
             if (kCluster > 1) {
@@ -724,7 +767,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                             w[e + 2] += u.z;
                             w[e + 3] += u.w;
                         }
-                    finish(z, i, j, col, c[kGram ? m : 0], w);
+                    finish(z, i, j, col, c[kGram ? m : 0], alpha, rest, w);
                 }
             }
         }
@@ -796,6 +839,8 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     const uint32_t pb = (uint32_t)q.rn * 128u;   // bytes of a part of a panel
     unsigned char* xs = smem;
     unsigned char* as = smem + kParts * q.xp * pb;
+    // row factors, in the room that the MMAs' unused rows reach into
+    float* s_rows = reinterpret_cast<float*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas));
     uint64_t* mbar = reinterpret_cast<uint64_t*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas) +
                                                  (kBlock - 16) * 128);
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
@@ -1042,13 +1087,19 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             __syncthreads();   // A takes the place of the shares
         }
         if (!ok) continue;
+        float exact = 0.0f;   // A's diagonal in this row, where this thread has it
         if (busy) {
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
                 if (m < r_mine) {
+                    const int col = 16 * (group + kSmallGroups * m);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
-                    put(as, 16 * (group + kSmallGroups * m), acc[m]);
+                    if (!kSplit && col / 32 == quarter) {   // (one for the warp)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) exact = col + e == row ? acc[m][e] : exact;
+                    }
+                    put(as, col, acc[m]);
                 }
             }
         }
@@ -1082,10 +1133,25 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                             for (int e = 0; e < 8; ++e) v[8 * b + e] = w[e];
                         }
                 }
+                if (!kSplit && col / 32 == quarter) {
+                    const float rounded = __half2float(__float2half_rn(exact));
+                    const float more = (exact - rounded) *
+                                       (q.b * (kScaleP / kScaleA) +
+                                        2.0f * q.c2 * (kScaleP / (kScaleA * kScaleA)) * rounded);
+                    float d = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        v[e] += col + e == row ? more : 0.0f;
+                        d = col + e == row ? v[e] : d;
+                    }
+                    if (row >= col && row < min(col + 16, q.rn))
+                        s_rows[row] = row_factor(d, __half2float(__float2half_rn(d)));
+                }
                 put(as, col, v);
             }
         }
         ready();
+        const float scale = kSplit || !busy ? 1.0f : s_rows[row];
         // ---- X' = P X, 256 columns at a time; the last one is the result
         for (int c0 = 0; c0 < cn; c0 += 256) {
             const int n = min(256, cn - c0);
@@ -1099,13 +1165,13 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                     const int col = c0 + 16 * u;
                     if (step + 1 < q.steps) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= 1.0f / kScaleP;
+                        for (int e = 0; e < 16; ++e) v[e] *= scale / kScaleP;
                         put(xs, col, v);
                     } else if (q.tall) {   // (the warp's rows are adjacent there)
                         T* o = out + blockIdx.x / q.ctas * elems;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float y[1] = {v[e] * (1.0f / (kScaleP * kScaleX))};
+                            const float y[1] = {v[e] * (scale / (kScaleP * kScaleX))};
                             const int oc = col0 + col + e;
                             if (row < q.r && oc < q.c)
                                 Pack<T, 1>::store(o + (size_t)oc * q.r + row, y);
@@ -1117,7 +1183,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                             float y[kChunk16];
 #pragma unroll
                             for (int b = 0; b < kChunk16; ++b)
-                                y[b] = v[e + b] * (1.0f / (kScaleP * kScaleX));
+                                y[b] = v[e + b] * (scale / (kScaleP * kScaleX));
                             Pack<T, kChunk16>::store(staged(c0, row, 16 * u + e), y);
                         }
                     }
@@ -1177,7 +1243,10 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
     p.rp = p.r > 1024 ? ceil_div(p.r, 2 * kBlock) * 2 * kBlock : ceil_div(p.r, kBlock) * kBlock;
     const int64_t to = p.c > 1024 ? 256 : 128;   // two widths of a tile of the last product
     p.cp = ceil_div(p.c, to) * to;
-    p.parts = dtype == kF32 ? 2 : 1;
+    // pairs in 16 bits too where there are too few elements for the roundings of single halves to
+    // average out (5 x 6: the result up to 2.4 times as far off as its own rounding; with pairs 1.0;
+    // 16 x 16: 14.7 us instead of 13)
+    p.parts = dtype == kF32 || (p.r <= 32 && p.c <= 256) ? 2 : 1;
     // on chip: shares of about 256 columns, more where memory or the SMs ask for it
     p.ctas = 0;
     const int rn = (int)ceil_div(p.r, 16) * 16, ap = (int)ceil_div(p.r, kPanel);
@@ -1196,6 +1265,7 @@ struct Space {
     __half *x[2], *a, *p;
     size_t x_lo, a_lo;
     float2* part;
+    float *rest, *rows;
 };
 Space carve(Carve& w, int64_t batch, const Plan& p) {
     Space s;
@@ -1205,6 +1275,8 @@ Space carve(Carve& w, int64_t batch, const Plan& p) {
     s.a = w.take<__half>(s.a_lo * p.parts);
     s.p = w.take<__half>(s.a_lo * p.parts);
     s.part = w.take<float2>((size_t)batch * kNormBlocks);
+    s.rest = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
+    s.rows = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
     return s;
 }
 
@@ -1312,6 +1384,8 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         g.d_size = (size_t)p.rp * p.rp;
         g.d_rows = p.rp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
+        g.rest = w.rest;
+        g.rows = w.rows;
         e = symmetric<kSplit>(g, st, n_sms, s);
         if (e != cudaSuccess) return e;
         Product h = g;   // P = a I + b A + c A A
@@ -1386,6 +1460,8 @@ cudaError_t prepare_orth() {
     if (e == cudaSuccess) e = prepare_one<false, 256, true, 2>();
     for (const void* k : {(const void*)k_orth_small<float, true, 1>,
                           (const void*)k_orth_small<float, true, 4>,
+                          (const void*)k_orth_small<__nv_bfloat16, true, 1>,
+                          (const void*)k_orth_small<__nv_bfloat16, true, 8>,
                           (const void*)k_orth_small<__nv_bfloat16, false, 1>,
                           (const void*)k_orth_small<__nv_bfloat16, false, 8>})
         if (e == cudaSuccess)
@@ -1395,8 +1471,10 @@ cudaError_t prepare_orth() {
 
 cudaError_t launch_orth(const OrthCall& q, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
     if (q.batch == 0 || q.m == 0 || q.n == 0) return cudaSuccess;
-    return q.dtype == kF32 ? run<float, true>(q, st, ws, n_sms, s)
-                           : run<__nv_bfloat16, false>(q, st, ws, n_sms, s);
+    if (q.dtype == kF32) return run<float, true>(q, st, ws, n_sms, s);
+    return plan_of(q.batch, q.m, q.n, q.dtype).parts == 2
+               ? run<__nv_bfloat16, true>(q, st, ws, n_sms, s)
+               : run<__nv_bfloat16, false>(q, st, ws, n_sms, s);
 }
 
 }  // namespace pulsar

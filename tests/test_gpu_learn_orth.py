@@ -50,6 +50,29 @@ def test_orthogonalize(ops, case, dtype):
     _check(ops.orthogonalize(g.cuda()), g)
 
 
+@pytest.mark.parametrize("shape", [(1, 35, 1330), (2, 4, 318), (1, 436, 3), (8, 5, 6), (16, 2, 10),
+                                   (2, 39, 513), (8, 64, 64), (1, 128, 512), (1, 100, 4000),
+                                   (2, 300, 400), (1, 4096, 350), (1, 512, 8192)],
+                         ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("same", [False, True], ids=["normal", "orthogonal"])
+def test_sixteen_bits_lose_no_more_than_their_result(ops, shape, same):
+    """In 16 bits the arithmetic may add as much error as the rounding of the
+    result has by itself: sqrt(2) of it together.  Roundings that are alike in
+    every row (nearly orthogonal rows have nearly equal diagonals) would not
+    average out and break this."""
+    for seed in range(3):
+        gen = torch.Generator().manual_seed(seed)
+        g = torch.randn(*shape, generator=gen)
+        if same:
+            g = torch.linalg.svd(g.double(), full_matrices=False)
+            g = (g.U @ g.Vh).float()
+        g = g.bfloat16()
+        want, _ = ref.orthogonalize(g, 5, COEFFS, EPS)
+        err = (ops.orthogonalize(g.cuda()).cpu().double() - want).norm()
+        own = (want.float().bfloat16().double() - want).norm()
+        assert err <= 2 ** 0.5 * own, float(err / own)
+
+
 def test_singular_values_go_to_one(ops):
     """The polynomial takes singular values of a well-conditioned matrix into
     [0.65, 1.25] and keeps the singular vectors: U^T out V is diagonal."""
