@@ -202,12 +202,12 @@ k_orth_scale(const T* __restrict__ g, int64_t elems, const float2* __restrict__ 
 // Diagonals.  In single halves the roundings of A and P average out but for
 // those of their diagonals: where the rows are nearly orthogonal, as they are in
 // an oblong matrix, each diagonal's elements are nearly equal, are rounded alike,
-// and move every singular value the same way (35 x 1330: the result 2.0 times as
+// and move every singular value the same way (512 x 8192: the result 1.5 times as
 // far off as its own rounding to 16 bits, now 1.06).  So A's diagonal keeps what
 // its rounding left (`rest`) for P's, and P's is made exact by a factor per row
 // of X' (`rows`, within 2^-11 of 1), for which a row of P counts as scaled: its
 // other elements move by less than their own rounding.  It costs 3 of 351 us at
-// 2048 x 4096, 2 to 3 of 52 at 128 x 512 on chip.
+// 2048 x 4096.
 //
 // Where a product has too few tiles for the SMs (the symmetric ones of a
 // small or oblong matrix), a cluster of kCluster CTAs shares a tile: each
@@ -794,10 +794,16 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 // its own).  The CTAs of a cluster have the columns of X in equal shares of
 // whole panels; each makes its share of A = X X^T, adds up a part of all
 // shares, in the order of the CTAs, for everybody, and goes on with the same A
-// and its own columns.  Bound by latency: a step of a 64 x 64 matrix takes 3.8
-// us (MMAs 1.7, epilogues and their barriers 2.1), eight of them 22 us in 32
-// bits; 10 x 3000 on eight CTAs 46 us (on one: 324), 128 x 2000 80 us (by
-// separate products: 117).
+// and its own columns.  Bound by latency: a step of a 64 x 64 matrix takes 4.2
+// us (MMAs 1.7, epilogues and their barriers 2.5), eight of them 24 us in 32
+// bits; 10 x 3000 on eight CTAs 55 us, 128 x 2000 85 us (by separate products:
+// 117).
+//
+// The diagonals D_A of A and D_P of P stay in 32 bits and out of the operands:
+// with O = A - D_A, A^2 = O^2 + D_A O + O D_A + D_A^2, and X' = D_P X + (P - D_P) X.
+// What the tensor cores truncate and the operands round is then relative to the
+// rest: 35 x 1330 in 32 bits 4.9e-6 -> 1.0e-6 from the exact result, 64 x 64
+// 1.9e-6 -> 0.5e-6 (32-bit library products: 1.8e-6 and 1.2e-6), for 22 -> 24 us.
 //
 // Panels hold rn rows, a panel's lo part behind its hi part: as a K-major right
 // operand the two are one of 2 rn rows, and the product of a hi panel with
@@ -839,8 +845,9 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     const uint32_t pb = (uint32_t)q.rn * 128u;   // bytes of a part of a panel
     unsigned char* xs = smem;
     unsigned char* as = smem + kParts * q.xp * pb;
-    // row factors, in the room that the MMAs' unused rows reach into
-    float* s_rows = reinterpret_cast<float*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas));
+    // the diagonals of A and P, in the room that the MMAs' unused rows reach into
+    float* a_diag = reinterpret_cast<float*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas));
+    float* p_diag = a_diag + kBlock;
     uint64_t* mbar = reinterpret_cast<uint64_t*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas) +
                                                  (kBlock - 16) * 128);
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
@@ -983,19 +990,27 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                     h[p];
         }
     };
+    // sixteen columns of this row without the diagonal's element, which goes to `diag`
+    auto off_diagonal = [&](float* diag, int col, float (&v)[16]) {
+        float d = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            d = col + e == row ? v[e] : d;
+            v[e] = col + e == row ? 0.0f : v[e];
+        }
+        if (row >= col && row < min(col + 16, q.rn)) diag[row] = d;
+    };
     auto ready = [&]() {   // what the threads wrote is ready for the next product
         fence_async_smem();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     };
-    // the result's element (r, c) of the block of up to 256 columns at c0, of the type's size in
-    // 16-byte chunks, in the bytes of X's panels there
-    const auto staged = [&](int c0, int r, int c) {
-        constexpr int kChunk16 = VecOf<T>::n;
-        const int pitch = min(256, q.xp * kPanel - c0);
-        return reinterpret_cast<T*>(xs + c0 / kPanel * kParts * pb) + (size_t)r * pitch +
-               (((c / kChunk16) ^ (r & 7)) * kChunk16 + c % kChunk16);
+    // the result's element (r, c): in the bytes that were X's there, a float in those of a pair
+    const auto staged = [&](int r, int c) {
+        const int part = sizeof(T) == 4 ? c >> 2 & 1 : 0, in = sizeof(T) == 4 ? c & 3 : c & 7;
+        return reinterpret_cast<T*>(xs + (c / kPanel * kParts + part) * pb +
+                                    panel_at(r, c % kPanel & ~7, q.rn) * 2) + in;
     };
     // a thread's units of 16 columns of A: group, group + 4
     const int r_units = q.rn / 16, r_mine = (r_units + kSmallGroups - 1 - group) / kSmallGroups;
@@ -1087,7 +1102,6 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             __syncthreads();   // A takes the place of the shares
         }
         if (!ok) continue;
-        float exact = 0.0f;   // A's diagonal in this row, where this thread has it
         if (busy) {
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
@@ -1095,10 +1109,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                     const int col = 16 * (group + kSmallGroups * m);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
-                    if (!kSplit && col / 32 == quarter) {   // (one for the warp)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) exact = col + e == row ? acc[m][e] : exact;
-                    }
+                    if (col / 32 == quarter) off_diagonal(a_diag, col, acc[m]);
                     put(as, col, acc[m]);
                 }
             }
@@ -1108,95 +1119,105 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         if (tid == 0) issue(0, 0, q.rn, a0, a0, q.rn, 0, r_units, false);
         if (!await(0)) continue;
         if (busy) {
-            for (int m = 0; m < r_mine; ++m) {
+            constexpr float k2 = kScaleP / (kScaleA * kScaleA);
+            const float d = a_diag[row];
+#pragma unroll
+            for (int m = 0; m < kMost; ++m) {
+                if (m >= r_mine) continue;
                 const int col = 16 * (group + kSmallGroups * m);
                 float v[16];
                 sums(col, col + q.rn, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    v[e] *= q.c2 * (kScaleP / (kScaleA * kScaleA));
-                    if (col + e == row) v[e] += q.a * kScaleP;
-                }
                 if (row < q.rn) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int p = 0; p < kParts; ++p) {
-                            float w[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = v[8 * b + e];
-                            add_halves(w, *reinterpret_cast<const uint4*>(
-                                              as + (col / kPanel * kParts + p) * pb +
-                                              panel_at(row, col % kPanel + 8 * b, q.rn) * 2),
-                                       q.b * (kScaleP / kScaleA));
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[8 * b + e] = w[e];
-                        }
-                }
-                if (!kSplit && col / 32 == quarter) {
-                    const float rounded = __half2float(__float2half_rn(exact));
-                    const float more = (exact - rounded) *
-                                       (q.b * (kScaleP / kScaleA) +
-                                        2.0f * q.c2 * (kScaleP / (kScaleA * kScaleA)) * rounded);
-                    float d = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        v[e] += col + e == row ? more : 0.0f;
-                        d = col + e == row ? v[e] : d;
+                    for (int e = 0; e < 16; ++e) {   // (acc is O here)
+                        const float beta =
+                            q.b * (kScaleP / kScaleA) + q.c2 * k2 * (d + a_diag[col + e]);
+                        v[e] = fmaf(beta, acc[m][e], v[e] * (q.c2 * k2));
                     }
-                    if (row >= col && row < min(col + 16, q.rn))
-                        s_rows[row] = row_factor(d, __half2float(__float2half_rn(d)));
+                    if (col / 32 == quarter) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)   // (O is zero there)
+                            v[e] += col + e == row ? q.a * kScaleP + d * (q.b * (kScaleP / kScaleA) +
+                                                                          q.c2 * k2 * d)
+                                                   : 0.0f;
+                    }
                 }
+                if (col / 32 == quarter) off_diagonal(p_diag, col, v);
                 put(as, col, v);
             }
         }
         ready();
-        const float scale = kSplit || !busy ? 1.0f : s_rows[row];
+        const float d = busy ? p_diag[row] : 0.0f;
+        const bool last = step + 1 == q.steps;
         // ---- X' = P X, 256 columns at a time; the last one is the result
         for (int c0 = 0; c0 < cn; c0 += 256) {
             const int n = min(256, cn - c0);
             if (tid == 0)
                 issue(0, 0, 256, a0, x0 + (uint32_t)(c0 / kPanel) * kParts * pb, n, 0, r_units, true);
+            uint4 x[2][kParts];   // this row's halves of X in the next unit
+            const auto fetch = [&](int u) {
+                if (row >= q.rn || u >= n / 16) return;
+                const int col = c0 + 16 * u;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+                        x[b][p] = *reinterpret_cast<const uint4*>(
+                            xs + (col / kPanel * kParts + p) * pb +
+                            panel_at(row, col % kPanel + 8 * b, q.rn) * 2);
+            };
+            fetch(group);
             if (!await(0)) break;
             if (busy) {
+#pragma unroll 1
                 for (int u = group; u < n / 16; u += kSmallGroups) {
                     float v[16];
                     sums(16 * u, 256 + 16 * u, v);
+                    if (row >= q.rn) continue;
                     const int col = c0 + 16 * u;
-                    if (step + 1 < q.steps) {
+                    const float unit = last ? 1.0f / (kScaleP * kScaleX) : 1.0f / kScaleP;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] *= scale / kScaleP;
+                    for (int b = 0; b < 2; ++b) {
+                        float w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = v[8 * b + e];
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) add_halves(w, x[b][p], d);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[8 * b + e] = w[e] * unit;
+                    }
+                    fetch(u + kSmallGroups);
+                    if (!last) {
                         put(xs, col, v);
                     } else if (q.tall) {   // (the warp's rows are adjacent there)
                         T* o = out + blockIdx.x / q.ctas * elems;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float y[1] = {v[e] * (scale / (kScaleP * kScaleX))};
+                            const float y[1] = {v[e]};
                             const int oc = col0 + col + e;
                             if (row < q.r && oc < q.c)
                                 Pack<T, 1>::store(o + (size_t)oc * q.r + row, y);
                         }
-                    } else if (row < q.r) {   // staged where these columns of X were
+                    } else {
                         constexpr int kChunk16 = VecOf<T>::n;
 #pragma unroll
                         for (int e = 0; e < 16; e += kChunk16) {
                             float y[kChunk16];
 #pragma unroll
-                            for (int b = 0; b < kChunk16; ++b)
-                                y[b] = v[e + b] * (scale / (kScaleP * kScaleX));
-                            Pack<T, kChunk16>::store(staged(c0, row, 16 * u + e), y);
+                            for (int b = 0; b < kChunk16; ++b) y[b] = v[e + b];
+                            Pack<T, kChunk16>::store(staged(row, col + e), y);
                         }
                     }
                 }
             }
-            if (step + 1 == q.steps && !q.tall) {   // whole rows of the block's columns
+            if (last && !q.tall) {   // whole rows of the block's columns
                 __syncthreads();
                 T* o = out + blockIdx.x / q.ctas * elems + col0 + c0;
                 const int width = min(n, mine - c0) / V;
                 for (int e = tid; e < q.r * width; e += kSmallThreads) {
                     const int orow = e / width, oc = (e - orow * width) * V;
                     float y[V];
-                    Pack<T, V>::load(staged(c0, orow, oc), y);
+                    Pack<T, V>::load(staged(orow, c0 + oc), y);
                     Pack<T, V>::store(o + (size_t)orow * q.c + oc, y);
                 }
             }
