@@ -197,7 +197,9 @@ k_orth_scale(const T* __restrict__ g, int64_t elems, const float2* __restrict__ 
 //
 // In 32 bits the tensor cores' accumulation, which truncates, would be what
 // limits the result: hi hi and the cross terms have accumulators of their
-// own, and both are drained and summed in registers every kChunk panels.
+// own, and both are drained and summed in registers every kChunk panels (two;
+// of four, 683 x 2967 was 2.0 times as far off as plain 32-bit products, now 1.3
+// times, and 1024 x 1024 1.65, now 0.9; 1500 x 509: 142 us, now 147; of one: 152).
 //
 // Diagonals.  In single halves the roundings of A and P average out but for
 // those of their diagonals: where the rows are nearly orthogonal, as they are in
@@ -237,7 +239,7 @@ struct Product {
 };
 
 constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epilogue
-constexpr int kChunk = 4;              // panels of K per drained sum (32 bits)
+constexpr int kChunk = 2;              // panels of K per drained sum (32 bits)
 constexpr int kRowPitch = 33;          // words of a row of a warp's 32 x 32 word exchange
 
 template <bool kSplit, int kN>
