@@ -10,8 +10,8 @@
 // bfloat16 at the same rate, and its narrow range is no limit because the
 // iterates are bounded: |X_0|_F <= 1 and the polynomial keeps the singular
 // values near 1, so powers of two (kScale*) place X, A and P inside it.  For
-// float32 tensors every operand is a pair hi + lo of halves (22 bits) and a
-// product is hi hi + hi lo + lo hi.  aI is folded into P, so that the last
+// float32 tensors, and tiny ones in 16 bits, every operand is a pair hi + lo of
+// halves (22 bits) and a product is hi hi + hi lo + lo hi.  aI is folded into P, so that the last
 // product needs nothing but P and X.  A and P are symmetric: only the 128 x
 // 128 tiles on and below the diagonal are computed, each written twice.
 //
@@ -798,13 +798,13 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 // shares, in the order of the CTAs, for everybody, and goes on with the same A
 // and its own columns.  Bound by latency: a step of a 64 x 64 matrix takes 4.2
 // us (MMAs 1.7, epilogues and their barriers 2.5), eight of them 24 us in 32
-// bits; 10 x 3000 on eight CTAs 55 us, 128 x 2000 85 us (by separate products:
+// bits; 10 x 3000 on eight CTAs 58 us, 128 x 2000 87 us (by separate products:
 // 117).
 //
 // The diagonals D_A of A and D_P of P stay in 32 bits and out of the operands:
 // with O = A - D_A, A^2 = O^2 + D_A O + O D_A + D_A^2, and X' = D_P X + (P - D_P) X.
 // What the tensor cores truncate and the operands round is then relative to the
-// rest: 35 x 1330 in 32 bits 4.9e-6 -> 1.0e-6 from the exact result, 64 x 64
+// rest: 35 x 1330 in 32 bits 4.9e-6 -> 0.7e-6 from the exact result, 64 x 64
 // 1.9e-6 -> 0.5e-6 (32-bit library products: 1.8e-6 and 1.2e-6), for 22 -> 24 us.
 //
 // Panels hold rn rows, a panel's lo part behind its hi part: as a K-major right
@@ -825,7 +825,9 @@ struct Small {
     float a, b, c2, eps;
 };
 constexpr int kMaxShares = 8;
-constexpr int kSmallChunk = 256;   // K of a sum in tensor memory (as kChunk)
+// K of a sum in tensor memory (as kChunk).  Pairs: of 256, 128 x 2000 was 1.25
+// times as far off as plain 32-bit products, now 0.5 (85 us, now 87).
+constexpr int small_chunk(bool split) { return split ? 128 : 256; }
 
 // A and P; before them, where there is a cluster, a CTA's share of A in 32 bits.
 __host__ __device__ inline uint32_t small_a_bytes(int parts, int rn, int ap, int ctas) {
@@ -1025,7 +1027,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         for (int m = 0; m < kMost; ++m)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
-        const int ks = cn / 16, per = kSmallChunk / 16, chunks = (ks + per - 1) / per;
+        const int ks = cn / 16, per = small_chunk(kSplit) / 16, chunks = (ks + per - 1) / per;
         if (ok && tid == 0 && chunks > 0)
             issue(0, 0, q.rn, x0, x0, q.rn, 0, min(per, ks), false);
         for (int ch = 0; ch < chunks && ok; ++ch) {
