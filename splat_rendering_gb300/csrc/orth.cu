@@ -1345,7 +1345,8 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16,
                       (int)ceil_div(ceil_div(p.c, kPanel), p.ctas), (int)ceil_div(p.r, kPanel),
                       p.ctas, p.tall, o.steps, o.a, o.b, o.c, o.eps};
-        const bool vec = !p.tall && p.c % V == 0 && aligned16(o.grad);
+        // (the loads of `grad` and the stores to `out` are of one width)
+        const bool vec = !p.tall && p.c % V == 0 && aligned16(o.grad) && aligned16(o.out);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(o.batch * p.ctas));
         cfg.blockDim = dim3(kSmallThreads);
