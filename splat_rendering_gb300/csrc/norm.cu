@@ -570,7 +570,10 @@ __global__ void k_norm_empty(float2* stats, int64_t n, float eps) {
 constexpr int kHeld = 8;
 constexpr int kMaxCluster = 8;
 
+// (every thread of the block calls; the barrier wants each warp whole, and the work before it
+// may have split one)
 __device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // *p in the shared memory of the cluster's block `rank`
