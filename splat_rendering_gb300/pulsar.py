@@ -148,6 +148,20 @@ def _stream(s):
     return s.cuda_stream
 
 
+def _empty(shape, device: int, dtype, stream):
+    """A new tensor for a call on `stream` (None: the current one).  It comes
+    from that stream's own memory: a block of another stream may still be in
+    use there, and would be handed out again without waiting for this call."""
+    import torch
+    if stream is None or _stream(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, device=f"cuda:{device}", dtype=dtype)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=f"cuda:{device}", dtype=dtype)
+
+
 def _check(code: int, what: str):
     if code != OK:
         raise PulsarError(code, what)
@@ -316,7 +330,7 @@ class Renderer:
         first = cam[0] if batch else cam
         shape = ((len(cam),) if batch else ()) + (first.height, first.width, C)
         if image is None:
-            image = torch.empty(shape, device=f"cuda:{self.device}", dtype=torch.float32)
+            image = _empty(shape, self.device, torch.float32, stream)
         if batch:
             project_cams(self.ctx, pos, radius, opacity, n, list(cam), prm, stream)
         else:
@@ -330,13 +344,12 @@ class Renderer:
                  out=None, stream=None):
         import torch
         pos, features, bg, image, n, C, K = self._frame
-        dev = image.device
         if out is None:
             out = {}
             shapes = dict(pos=(n, 3), radius=(n,), opacity=(n,), features=(n, C),
                           cam=(K, 16) if K else (16,))
             for k in want:
-                out[k] = torch.empty(shapes[k], device=dev, dtype=torch.float32)
+                out[k] = _empty(shapes[k], self.device, torch.float32, stream)
         backward(self.ctx, features, bg, image, grad_image, out.get("pos"), out.get("radius"),
                  out.get("opacity"), out.get("features"), out.get("cam"), stream)
         return out
@@ -346,19 +359,17 @@ class Renderer:
         of the current frame's camera(s)."""
         import torch
         if rgb is None:
-            rgb = torch.empty(tuple(features.shape[:-1]) + (3,), device=features.device,
-                              dtype=torch.float32)
+            rgb = _empty(tuple(features.shape[:-1]) + (3,), self.device, torch.float32, stream)
         shade_forward(self.ctx, features, params, rgb, stream)
         return rgb
 
     def shade_backward(self, features, params, grad_rgb, grad_features=None, grad_params=None,
                        stream=None):
         """(dL/dfeatures, dL/dparams) of the shading for dL/drgb."""
-        import torch
         if grad_features is None:
-            grad_features = torch.empty_like(features)
+            grad_features = _empty(features.shape, self.device, features.dtype, stream)
         if grad_params is None:
-            grad_params = torch.empty_like(params)
+            grad_params = _empty(params.shape, self.device, params.dtype, stream)
         shade_backward(self.ctx, features, params, grad_rgb, grad_features, grad_params, stream)
         return grad_features, grad_params
 
@@ -441,7 +452,8 @@ class Learner:
         update = ops.orthogonalize(grad_matrix)
 
     Tensors are contiguous and on the handle's device; anything else raises
-    before a kernel is launched.  Outputs are allocated unless given."""
+    before a kernel is launched.  Outputs are allocated unless given, from the
+    memory of the stream that the call runs on."""
 
     def __init__(self, workspace_bytes: int, device: int = 0):
         import torch
@@ -492,10 +504,11 @@ class Learner:
             raise TypeError(f"{what} is {t.dtype}, wanted {dtype}")
         return t.data_ptr()
 
-    def _out(self, t, what: str, shape, dtype):
+    def _out(self, t, what: str, shape, dtype, stream):
         """An output and its pointer: `t` checked, or where it is None a new one."""
         if t is None:
-            t = self._torch.empty(shape, device=self._dev, dtype=dtype)
+            t = self._torch.empty(shape, device=self._dev, dtype=dtype) if stream is None else \
+                _empty(shape, self.device, dtype, stream)
             return t, t.data_ptr()
         return t, self._tensor(t, what, shape, dtype)
 
@@ -513,7 +526,7 @@ class Learner:
         rows, dim = table.shape
         shape = (*tokens.shape, dim)
         dt, ix = _dtype_code(table.dtype), _index_code(tokens.dtype)
-        out, p_out = self._out(out, "out", shape, table.dtype)
+        out, p_out = self._out(out, "out", shape, table.dtype, stream)
         _check(self._lib.pulsar_embed_forward(
             self.handle, self._tensor(table, "table"), self._tensor(tokens, "tokens"),
             tokens.numel(), rows, dim, scale, dt, ix, p_out, self._stream(stream)),
@@ -528,7 +541,7 @@ class Learner:
                              f"{tuple(tokens.shape) + ('dim',)}")
         dim = grad_out.shape[-1]
         dt, ix = _dtype_code(grad_out.dtype), _index_code(tokens.dtype)
-        grad_table, p_table = self._out(grad_table, "grad_table", (rows, dim), grad_out.dtype)
+        grad_table, p_table = self._out(grad_table, "grad_table", (rows, dim), grad_out.dtype, stream)
         _check(self._lib.pulsar_embed_backward(
             self.handle, self._tensor(grad_out, "grad_out"), self._tensor(tokens, "tokens"),
             tokens.numel(), rows, dim, scale, dt, ix, p_table, self._stream(stream)),
@@ -550,8 +563,8 @@ class Learner:
         last, and the (mean, 1/std) [images, groups, 2] its backward needs."""
         shape, images, pixels, C, a = self._image_shape(x, act)
         dt, f32 = _dtype_code(x.dtype), self._torch.float32
-        out, p_out = self._out(out, "out", shape, x.dtype)
-        stats, p_stats = self._out(stats, "stats", (images, groups, 2), f32)
+        out, p_out = self._out(out, "out", shape, x.dtype, stream)
+        stats, p_stats = self._out(stats, "stats", (images, groups, 2), f32, stream)
         _check(self._lib.pulsar_group_norm_forward(
             self.handle, self._tensor(x, "x"), images, pixels, C, groups,
             self._tensor(weight, "weight", (C,), f32), self._tensor(bias, "bias", (C,), f32),
@@ -567,11 +580,11 @@ class Learner:
         dt, f32 = _dtype_code(x.dtype), self._torch.float32
         p_x = p_weight = p_bias = None
         if grad_x is not None or "x" in want:
-            grad_x, p_x = self._out(grad_x, "grad_x", shape, x.dtype)
+            grad_x, p_x = self._out(grad_x, "grad_x", shape, x.dtype, stream)
         if grad_weight is not None or "weight" in want:
-            grad_weight, p_weight = self._out(grad_weight, "grad_weight", (C,), f32)
+            grad_weight, p_weight = self._out(grad_weight, "grad_weight", (C,), f32, stream)
         if grad_bias is not None or "bias" in want:
-            grad_bias, p_bias = self._out(grad_bias, "grad_bias", (C,), f32)
+            grad_bias, p_bias = self._out(grad_bias, "grad_bias", (C,), f32, stream)
         _check(self._lib.pulsar_group_norm_backward(
             self.handle, self._tensor(grad_y, "grad_y", shape, x.dtype), self._tensor(x, "x"),
             self._tensor(stats, "stats", (images, groups, 2), f32), images, pixels, C, groups,
@@ -586,7 +599,7 @@ class Learner:
         if len(shape) < 2:
             raise ValueError(f"grad has shape {tuple(shape)}, wanted [..., m, n]")
         dt = _dtype_code(grad.dtype)
-        out, p_out = self._out(out, "out", shape, grad.dtype)
+        out, p_out = self._out(out, "out", shape, grad.dtype, stream)
         abc = (ctypes.c_float * 3)(*[float(v) for v in coeffs])
         _check(self._lib.pulsar_orthogonalize(
             self.handle, self._tensor(grad, "grad"), self._product(shape[:-2]), shape[-2], shape[-1],
