@@ -42,65 +42,106 @@ __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, in
 }
 
 // ------------------------------------------------------------------ norm --
-// Sums of squares, a block per chunk of a matrix.  The second sum is of the
-// values times 2^-64, and is taken where the first overflows.
-constexpr float kDown = 5.421010862427522e-20f;   // 2^-64
+// Sums of squares, a block per chunk of a matrix: of the values, and of the
+// values times 2^-80 and 2^80, which are taken where the first overflows or
+// is so small that squares were lost below float32's range.
+constexpr float kDown = 8.271806125530277e-25f;   // 2^-80
+constexpr float kUp = 1.2089258196146292e24f;     // 2^80
 constexpr int kNormBlocks = 608;                  // at most, per matrix
+constexpr int kNormAhead = 4;                     // vectors a thread has in flight
+
+struct __align__(16) Squares {
+    float plain, down, up, pad;
+    __device__ __forceinline__ void add(const Squares& s) {
+        plain += s.plain;
+        down += s.down;
+        up += s.up;
+    }
+    // The scaled sums count where the total is beyond 2^128 or below 2^-80: a term between 2^-60
+    // and 2^60 is nothing to the first and cannot be in the second.
+    template <int V>
+    __device__ __forceinline__ void add(const float (&v)[V]) {
+        float p = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) p = fmaf(v[j], v[j], p);
+        plain += p;
+        if (p >= 0x1p-60f && p <= 0x1p60f) return;
+        float d = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            d = fmaf(v[j] * kDown, v[j] * kDown, d);
+            u = fmaf(v[j] * kUp, v[j] * kUp, u);
+        }
+        down += d;
+        up += u;
+    }
+};
 
 template <int kN = kThreads>
-__device__ __forceinline__ float2 block_sum(float2 v) {
-    __shared__ float2 s[kN / 32];
+__device__ __forceinline__ Squares block_sum(Squares v) {
+    __shared__ Squares s[kN / 32];
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.plain += __shfl_xor_sync(0xffffffffu, v.plain, o);
+        v.down += __shfl_xor_sync(0xffffffffu, v.down, o);
+        v.up += __shfl_xor_sync(0xffffffffu, v.up, o);
     }
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    float2 t = make_float2(0.0f, 0.0f);
+    Squares t{};
 #pragma unroll
-    for (int w = 0; w < kN / 32; ++w) {
-        t.x += s[w].x;
-        t.y += s[w].y;
-    }
+    for (int w = 0; w < kN / 32; ++w) t.add(s[w]);
     __syncthreads();
     return t;
 }
 
+// The squares of a matrix's vectors i0, i0 + step, ...
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
-k_orth_norm(const T* __restrict__ g, int64_t elems, float2* __restrict__ part) {
-    pdl_begin();
-    const T* m = g + (size_t)blockIdx.y * elems;
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < elems / V;
-         i += (int64_t)gridDim.x * kThreads) {
-        float v[V];
-        Pack<T, V>::load(m + i * V, v);
+__device__ __forceinline__ Squares sum_squares(const T* __restrict__ m, int64_t vectors, int64_t i0,
+                                               int64_t step) {
+    Squares s{};
+    for (int64_t i = i0; i < vectors; i += kNormAhead * step) {
+        typename Pack<T, V>::Raw r[kNormAhead];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s.x = fmaf(v[j], v[j], s.x);
-            s.y = fmaf(v[j] * kDown, v[j] * kDown, s.y);
+        for (int k = 0; k < kNormAhead; ++k)
+            if (i + k * step < vectors) r[k] = Pack<T, V>::raw(m + (i + k * step) * V);
+#pragma unroll
+        for (int k = 0; k < kNormAhead; ++k) {
+            if (i + k * step >= vectors) break;
+            float v[V];
+            Pack<T, V>::open(r[k], v);
+            s.add(v);
         }
     }
-    s = block_sum(s);
+    return s;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads)
+k_orth_norm(const T* __restrict__ g, int64_t elems, Squares* __restrict__ part) {
+    pdl_begin();
+    const Squares s = block_sum(
+        sum_squares<T, V>(g + (size_t)blockIdx.y * elems, elems / V,
+                          (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads));
     if (threadIdx.x == 0) part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// 1 / (|G|_F + eps) from the sums
-__device__ __forceinline__ float norm_inverse(float2 s, float eps) {
-    const float norm = isinf(s.x) ? sqrtf(s.y) * 18446744073709551616.0f : sqrtf(s.x);
-    return 1.0f / (norm + eps);
+// g / (|G|_F + eps) is (g * pre) * inv: pre, a power of two, keeps the norm inside float32's range.
+struct Inverse {
+    float pre, inv;
+};
+__device__ __forceinline__ Inverse norm_inverse(const Squares& s, float eps) {
+    // (beside an eps of 1 a norm below 2^-40 is nothing; times 2^80 it could leave the range)
+    const bool down = isinf(s.plain), up = s.plain < kDown && eps < 1.0f;
+    const float pre = down ? kDown : up ? kUp : 1.0f;
+    const float sum = sqrtf(down ? s.down : up ? s.up : s.plain) + eps * pre;
+    return {pre, sum == 0.0f ? 0.0f : 1.0f / sum};   // (zero stays zero without an eps)
 }
 
 // The same from a matrix's parts (every thread of the block calls).
-__device__ __forceinline__ float inv_norm(const float2* part, int blocks, float eps) {
-    float2 s = make_float2(0.0f, 0.0f);
-    for (int i = threadIdx.x; i < blocks; i += kThreads) {
-        s.x += part[i].x;
-        s.y += part[i].y;
-    }
+__device__ __forceinline__ Inverse inv_norm(const Squares* part, int blocks, float eps) {
+    Squares s{};
+    for (int i = threadIdx.x; i < blocks; i += kThreads) s.add(part[i]);
     return norm_inverse(block_sum(s), eps);
 }
 
@@ -129,10 +170,11 @@ __device__ __forceinline__ void halves(const float (&v)[8], uint4 (&h)[kParts]) 
 template <typename T, int kParts, int V>
 __global__ void __launch_bounds__(kThreads)
 k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t cp, bool tall,
-             const float2* __restrict__ part, int parts, float eps, __half* __restrict__ x,
+             const Squares* __restrict__ part, int parts, float eps, __half* __restrict__ x,
              size_t lo) {
     pdl_begin();
-    const float inv = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
+    const Inverse by = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
+    const float inv = by.inv * kScaleX;
     const T* m = g + (size_t)blockIdx.y * r * c;
     __half* o = x + (size_t)blockIdx.y * rp * cp;
     // a block takes 128 of what is contiguous in g, four a thread, of eight lines of it
@@ -153,7 +195,7 @@ k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t 
                 if (row < r && c0 + j < c)
                     Pack<T, V>::load(m + (tall ? (c0 + j) * r + row : row * c + c0 + j), u);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
+                for (int e = 0; e < V; ++e) v[j + e] = u[e] * by.pre * inv;
             }
             uint4 h[kParts];
             halves<kParts>(v, h);
@@ -167,15 +209,15 @@ k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t 
 // No step at all: out = g / (|g| + eps).
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-k_orth_scale(const T* __restrict__ g, int64_t elems, const float2* __restrict__ part, int parts,
+k_orth_scale(const T* __restrict__ g, int64_t elems, const Squares* __restrict__ part, int parts,
              float eps, T* __restrict__ out) {
     pdl_begin();
-    const float inv = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
+    const Inverse by = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < elems;
          i += (int64_t)gridDim.x * kThreads) {
         float v[1];
         Pack<T, 1>::load(g + (size_t)blockIdx.y * elems + i, v);
-        v[0] *= inv;
+        v[0] = v[0] * by.pre * by.inv;
         Pack<T, 1>::store(out + (size_t)blockIdx.y * elems + i, v);
     }
 }
@@ -321,17 +363,6 @@ __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, const 
                  "f"(v.z), "f"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t saddr, uint32_t rank) {
-    uint32_t at;
-    float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(saddr), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                 : "=f"(v.x), "=f"(v.y)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
-
 // Tile t of a symmetric product in tiles of 128 x 256: row blocks of 128, the
 // column blocks up to the diagonal, i / 2 + 1 of them in row block i.
 __device__ __forceinline__ void lower_wide(int t, int* i, int* j) {
@@ -844,7 +875,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out, LearnState* st) {
     constexpr int kParts = kSplit ? 2 : 1;
     extern __shared__ unsigned char raw[];
-    __shared__ float2 s_norm;
+    __shared__ Squares s_norm;
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t pb = (uint32_t)q.rn * 128u;   // bytes of a part of a panel
     unsigned char* xs = smem;
@@ -873,35 +904,25 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     const int col0 = rank * q.xp * kPanel;
     const int mine = max(0, min(q.xp * kPanel, q.c - col0)), cn = (mine + 15) / 16 * 16;
     {   // (any share of the elements serves the norm)
-        float2 sq = make_float2(0.0f, 0.0f);
-        const int n = (int)(elems / V), step = kSmallThreads * q.ctas;
-#pragma unroll 8
-        for (int i = rank * kSmallThreads + tid; i < n; i += step) {
-            float v[V];
-            Pack<T, V>::load(g + (size_t)i * V, v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                sq.x = fmaf(v[j], v[j], sq.x);
-                sq.y = fmaf(v[j] * kDown, v[j] * kDown, sq.y);
-            }
-        }
-        sq = block_sum<kSmallThreads>(sq);
+        const Squares sq = block_sum<kSmallThreads>(
+            sum_squares<T, V>(g, (int64_t)(elems / V), rank * kSmallThreads + tid,
+                              kSmallThreads * q.ctas));
         if (tid == 0) s_norm = sq;
     }
-    float2 sq = make_float2(0.0f, 0.0f);
+    Squares sq{};
     if (shared) {
         __syncwarp();
         cluster_sync();
         for (int k = 0; k < q.ctas; ++k) {
-            const float2 u = ld_cluster2(smem_u32(&s_norm), k);
-            sq.x += u.x;
-            sq.y += u.y;
+            const float4 u = ld_cluster(smem_u32(&s_norm), k);
+            sq.add(Squares{u.x, u.y, u.z, 0.0f});
         }
     } else {
         __syncthreads();
         sq = s_norm;
     }
-    const float inv = norm_inverse(sq, q.eps);
+    const Inverse by = norm_inverse(sq, q.eps);
+    const float inv = by.inv * kScaleX;
 #pragma unroll 4
     for (int i = tid; i < q.rn * q.xp * 8; i += kSmallThreads) {
         const int xr = q.tall ? i % q.rn : i / (q.xp * 8);
@@ -914,7 +935,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                 Pack<T, V>::load(g + (q.tall ? (size_t)(c0 + j) * q.r + xr
                                              : (size_t)xr * q.c + c0 + j), u);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[j + e] = u[e] * inv * kScaleX;
+            for (int e = 0; e < V; ++e) v[j + e] = u[e] * by.pre * inv;
         }
         uint4 h[kParts];
         halves<kParts>(v, h);
@@ -1249,7 +1270,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
 }
 
 // ----------------------------------------------------------------- plans --
-constexpr size_t kSmemMax = 227 * 1024 - 256;   // (the norm has a little of its own)
+constexpr size_t kSmemMax = 227 * 1024 - 512;   // (the norm has a little of its own)
 
 constexpr size_t kSmemHalf = 120 * 1024;
 
@@ -1289,7 +1310,7 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
 struct Space {
     __half *x[2], *a, *p;
     size_t x_lo, a_lo;
-    float2* part;
+    Squares* part;
     float *rest, *rows;
 };
 Space carve(Carve& w, int64_t batch, const Plan& p) {
@@ -1299,7 +1320,7 @@ Space carve(Carve& w, int64_t batch, const Plan& p) {
     for (int k = 0; k < 2; ++k) s.x[k] = w.take<__half>(s.x_lo * p.parts);
     s.a = w.take<__half>(s.a_lo * p.parts);
     s.p = w.take<__half>(s.a_lo * p.parts);
-    s.part = w.take<float2>((size_t)batch * kNormBlocks);
+    s.part = w.take<Squares>((size_t)batch * kNormBlocks);
     s.rest = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
     s.rows = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
     return s;
@@ -1385,14 +1406,14 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
     if (e != cudaSuccess) return e;
     if (o.steps == 0)
         return launch_pdl(k_orth_scale<T>, flat(elems), dim3(kThreads), 0, s, (const T*)o.grad,
-                          elems, (const float2*)w.part, parts, o.eps, (T*)o.out);
+                          elems, (const Squares*)w.part, parts, o.eps, (T*)o.out);
     const auto start = !p.tall && vec && p.c % V == 0 ? k_orth_start<T, kParts, V>
                                                       : k_orth_start<T, kParts, 1>;
     const int64_t inner = p.tall ? p.rp : p.cp / 8, lines = p.tall ? p.cp / 8 : p.rp;
     const int64_t pieces = ceil_div(inner, 128) * ceil_div(lines, 8);
     const dim3 grid((unsigned)(pieces < 2432 ? pieces : 2432), B);
     e = launch_pdl(start, grid, dim3(kThreads), 0, s, (const T*)o.grad, p.r, p.c,
-                   p.rp, p.cp, p.tall, (const float2*)w.part, parts, o.eps, w.x[0], w.x_lo);
+                   p.rp, p.cp, p.tall, (const Squares*)w.part, parts, o.eps, w.x[0], w.x_lo);
     const int tm = (int)(p.rp / kBlock);
     for (int k = 0; k < o.steps && e == cudaSuccess; ++k) {
         const __half* x = w.x[k & 1];
