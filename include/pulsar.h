@@ -410,7 +410,11 @@ int pulsar_group_norm_backward(pulsar_learn_t h, const void* grad_y, const void*
  * on the orientation with the fewer rows.  It drives the singular values
  * towards 1 and keeps the singular vectors; a zero matrix stays zero.
  *   grad, out [batch,m,n] dtype, out overwritten; out may be grad
- * 0 <= batch <= 65535, 0 <= m, n <= 65536, 0 <= steps <= 100, eps >= 0. */
+ * 0 <= batch <= 65535, 0 <= m, n <= 65536, 0 <= steps <= 100, eps >= 0.
+ * With q(u) = a + b u + c u^2 and m_0 = 1, m_k+1 = max |s q(s^2)| over
+ * 0 <= s <= m_k bounds the singular values of X_k+1: coefficients for which an
+ * m_k before the last step's result reaches 2^30, or |q| 2^96 on the way, are
+ * refused (PULSAR_ERR_ARG). */
 int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int64_t m, int64_t n,
                          int steps, const float* coeffs, float eps, int dtype, void* out,
                          void* stream);

@@ -218,7 +218,7 @@ int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int6
     if (!h || !orth_sizes(batch, m, n) || !valid_type(dtype) || !coeffs || steps < 0 ||
         steps > 100 || !(eps >= 0.0f) || !finite(eps) || !finite(coeffs[0]) ||
         !finite(coeffs[1]) || !finite(coeffs[2]) || !aligned_to(grad, dtype) ||
-        !aligned_to(out, dtype))
+        !aligned_to(out, dtype) || !orth_in_range(steps, coeffs[0], coeffs[1], coeffs[2]))
         return PULSAR_ERR_ARG;
     if (batch > 0 && m > 0 && n > 0 && (!grad || !out)) return PULSAR_ERR_ARG;
     if ((int64_t)orth_workspace(batch, m, n, dtype) > h->bytes) return PULSAR_ERR_WORKSPACE;

@@ -190,6 +190,8 @@ struct OrthCall {
     int dtype;
     void* out;
 };
+// Whether the iterates and the polynomial's values stay inside what the products can hold.
+bool orth_in_range(int steps, float a, float b, float c);
 size_t orth_workspace(int64_t batch, int64_t m, int64_t n, int dtype);
 cudaError_t prepare_orth();
 cudaError_t launch_orth(const OrthCall& c, LearnState* st, void* ws, int n_sms,

@@ -7,9 +7,9 @@
 //
 // The products run on the tensor cores (tcgen05, fp32 accumulation) on
 // operands in half precision: 11 significant bits, eight times closer than
-// bfloat16 at the same rate, and its narrow range is no limit because the
-// iterates are bounded: |X_0|_F <= 1 and the polynomial keeps the singular
-// values near 1, so powers of two (kScale*) place X, A and P inside it.  For
+// bfloat16 at the same rate, and powers of two place X, A and P inside its
+// narrow range: what the polynomial can make of the largest singular value at
+// most is known from step to step (see Scales).  For
 // float32 tensors, and tiny ones in 16 bits, every operand is a pair hi + lo of
 // halves (22 bits) and a product is hi hi + hi lo + lo hi.  aI is folded into P, so that the last
 // product needs nothing but P and X.  A and P are symmetric: only the 128 x
@@ -24,16 +24,114 @@
 
 #include <cuda_fp16.h>
 
+#include <cmath>
+
 namespace pulsar {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPanel = 64;      // columns of a panel: 128 bytes of halves
 constexpr int kBlock = 128;     // rows are padded to it
-// stored value = value times this: |X|, |A| < 1.6 and |P| < 4 for the usual
-// coefficients, far inside 65504; typical entries (1/sqrt(rc) and above) stay
-// above the smallest normal half
-constexpr float kScaleX = 1024.0f, kScaleA = 4096.0f, kScaleP = 1024.0f;
+
+// ---------------------------------------------------------------- scales --
+// No element of a matrix is larger than its largest singular value.  X_0's are at most |X_0|_F;
+// from the bound m of X's, A's are at most m^2, P's the largest |q(u)| over 0 <= u <= m^2,
+// q(u) = a + b u + c u^2, and those of X' the largest |s q(s^2)| over 0 <= s <= m.  A polynomial
+// that grows or shrinks by orders of magnitude would lose sight of the matrix in a few steps: for
+// such a one m is lowered to |X|_F, the root of A's trace, once A is known.
+// Stored value = value times a power of two that puts its bound into [2^12, 2^13) (X: twice
+// that), four times below half's largest and 2^36 above its smallest.
+constexpr int kMaxSteps = 100;
+constexpr int kMostX = 30, kMostP = 96;   // log2 of the largest bounds that are taken
+
+struct Polynomial {
+    float a, b, c;
+    // where |q| and |s q(s^2)| have extrema (u; beyond every bound where they have none) and
+    // their values
+    float u_q, q, u_s[2], s[2];
+    bool wild;   // A's traces are needed (0.5 of 24 us at eight 64 x 64)
+    __host__ __device__ float at(float u) const { return fabsf(a + u * (b + u * c)); }
+    // for the bound u of A's singular values
+    __host__ __device__ float most_q(float u) const {
+        const float v = fmaxf(fabsf(a), at(u));
+        return u_q < u ? fmaxf(v, q) : v;
+    }
+    __host__ __device__ float most_s(float u) const {
+        float v = sqrtf(u) * at(u);
+        if (u_s[0] < u) v = fmaxf(v, s[0]);
+        return u_s[1] < u ? fmaxf(v, s[1]) : v;
+    }
+};
+
+Polynomial polynomial(float fa, float fb, float fc, int steps) {
+    const double a = fa, b = fb, c = fc;
+    const auto value = [&](double u) { return fabs(a + u * (b + u * c)); };
+    const auto place = [](double u) { return u > 0.0 && u < 0x1p62 ? (float)u : INFINITY; };
+    Polynomial p{fa, fb, fc};
+    const double u = -b / (2.0 * c);
+    // 5 c u^2 + 3 b u + a = 0 by the form that does not cancel
+    const double t = -0.5 * (3.0 * b + copysign(sqrt(9.0 * b * b - 20.0 * a * c), b));
+    const double us[2] = {t / (5.0 * c), a / t};
+    p.u_q = place(u);
+    p.q = p.u_q < INFINITY ? (float)value(u) : 0.0f;
+    for (int k = 0; k < 2; ++k) {
+        p.u_s[k] = place(us[k]);
+        p.s[k] = p.u_s[k] < INFINITY ? (float)(sqrt(us[k]) * value(us[k])) : 0.0f;
+    }
+    // (where |a| >= 1, small singular values do not shrink)
+    p.wild = !(fabs(a) >= 1.0);
+    float m = 1.0f;
+    for (int k = 0; k < steps && !p.wild; ++k) {
+        m = p.most_s(m * m);
+        p.wild = !(m <= 2.0f);
+    }
+    return p;
+}
+
+// The smallest e, within the limits, with v < 2^e.
+__device__ __forceinline__ int above(float v, int lo, int hi) {
+    const int e = (__float_as_int(v) >> 23 & 255) - 126;   // (below the limits where v is subnormal)
+    return min(max(e, lo), hi);
+}
+__device__ __forceinline__ float pow2(int e) {   // zero below the normal ones
+    return __int_as_float(min(max(e + 127, 0), 254) << 23);
+}
+__device__ __forceinline__ float times_pow2(float v, int e) {   // (|e| below 252)
+    return v * pow2(e >> 1) * pow2(e - (e >> 1));
+}
+// log2 of the scales for the bounds of X, of X in A = X X^T, and of P
+__device__ __forceinline__ int scale_x(float m) { return 14 - above(m, -100, kMostX + 1); }
+__device__ __forceinline__ int scale_a(float m) { return 13 - above(m * m, -126, 2 * kMostX + 2); }
+__device__ __forceinline__ int scale_p(float q) { return 13 - above(q, -60, kMostP + 1); }
+
+// A trace's part in whole numbers of 2^-10 stored units, rounded up: their sum has no order (and
+// that of 128 rows, each below 2^13, no overflow).
+__device__ __forceinline__ uint32_t trace_units(float stored) {
+    return stored > 0.0f ? __float2uint_ru(stored * 1024.0f) : 0u;
+}
+// The bound of A, where X's was `m` before A was known, with A's trace.
+__device__ __forceinline__ float known_bound(const Polynomial& p, float m, float trace) {
+    if (!p.wild || !(m > 0x1p-30f)) return m * m;   // (tiny ones are far from any overflow)
+    return fminf(m * m, trace * (1.001f / 1024.0f) * pow2(-scale_a(m)));
+}
+// The factors of P = p2 (A A) + p1 A + p0 I of stored values, for X's bound m and A's bound u.
+struct Factors {
+    float p2, p1, p0;
+};
+__device__ __forceinline__ Factors factors_p(const Polynomial& p, float m, float u) {
+    const int sa = scale_a(m), sp = scale_p(p.most_q(u));
+    return {times_pow2(p.c, max(sp - 2 * sa, -250)), times_pow2(p.b, sp - sa), times_pow2(p.a, sp)};
+}
+// X's next bound.  (sqrt(u) loses a bound below 2^-63, whose steps are all a X)
+__device__ __forceinline__ float next_bound(const Polynomial& p, float m, float u) {
+    return m > 0x1p-30f ? p.most_s(u) : fmaxf(p.most_s(u), m * fabsf(p.a));
+}
+// The factor of X' = x (P X), whose bound is `next`; the last X' is the result itself.
+__device__ __forceinline__ float factor_x(const Polynomial& p, float m, float u, float next, bool last) {
+    return times_pow2(1.0f, (last ? 0 : scale_x(next)) - scale_p(p.most_q(u)) - scale_x(m));
+}
+// The factor of A = X X^T
+__device__ __forceinline__ float factor_a(float m) { return pow2(scale_a(m) - 2 * scale_x(m)); }
 
 // Element (row, col) of a matrix of `rows` padded rows, in halves.
 __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, int64_t rows) {
@@ -57,24 +155,6 @@ struct __align__(16) Squares {
         down += s.down;
         up += s.up;
     }
-    // The scaled sums count where the total is beyond 2^128 or below 2^-80: a term between 2^-60
-    // and 2^60 is nothing to the first and cannot be in the second.
-    template <int V>
-    __device__ __forceinline__ void add(const float (&v)[V]) {
-        float p = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) p = fmaf(v[j], v[j], p);
-        plain += p;
-        if (p >= 0x1p-60f && p <= 0x1p60f) return;
-        float d = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            d = fmaf(v[j] * kDown, v[j] * kDown, d);
-            u = fmaf(v[j] * kUp, v[j] * kUp, u);
-        }
-        down += d;
-        up += u;
-    }
 };
 
 template <int kN = kThreads>
@@ -95,7 +175,10 @@ __device__ __forceinline__ Squares block_sum(Squares v) {
     return t;
 }
 
-// The squares of a matrix's vectors i0, i0 + step, ...
+// The squares of a matrix's vectors i0, i0 + step, ...  The scaled sums count where the total is
+// beyond 2^128 or below 2^-80: a vector of 2^-60 to 2^60 is nothing to the first and cannot be in
+// the second, so that theirs are seldom taken (and by a loop that is short in code: a launch on
+// chip waits for its instructions).
 template <typename T, int V>
 __device__ __forceinline__ Squares sum_squares(const T* __restrict__ m, int64_t vectors, int64_t i0,
                                                int64_t step) {
@@ -105,12 +188,29 @@ __device__ __forceinline__ Squares sum_squares(const T* __restrict__ m, int64_t 
 #pragma unroll
         for (int k = 0; k < kNormAhead; ++k)
             if (i + k * step < vectors) r[k] = Pack<T, V>::raw(m + (i + k * step) * V);
+        bool ends = false;
 #pragma unroll
         for (int k = 0; k < kNormAhead; ++k) {
             if (i + k * step >= vectors) break;
-            float v[V];
+            float v[V], p = 0.0f;
             Pack<T, V>::open(r[k], v);
-            s.add(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) p = fmaf(v[j], v[j], p);
+            s.plain += p;
+            ends |= !(p >= 0x1p-60f && p <= 0x1p60f);
+        }
+        if (!ends) continue;
+#pragma unroll 1
+        for (int k = 0; k < kNormAhead && i + k * step < vectors; ++k) {
+            float v[V], d = 0.0f, u = 0.0f;
+            Pack<T, V>::load(m + (i + k * step) * V, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d = fmaf(v[j] * kDown, v[j] * kDown, d);
+                u = fmaf(v[j] * kUp, v[j] * kUp, u);
+            }
+            s.down += d;
+            s.up += u;
         }
     }
     return s;
@@ -128,14 +228,15 @@ k_orth_norm(const T* __restrict__ g, int64_t elems, Squares* __restrict__ part) 
 
 // g / (|G|_F + eps) is (g * pre) * inv: pre, a power of two, keeps the norm inside float32's range.
 struct Inverse {
-    float pre, inv;
+    float pre, inv, norm;   // norm: |X_0|_F, or 1 where that is zero or no number
 };
 __device__ __forceinline__ Inverse norm_inverse(const Squares& s, float eps) {
     // (beside an eps of 1 a norm below 2^-40 is nothing; times 2^80 it could leave the range)
     const bool down = isinf(s.plain), up = s.plain < kDown && eps < 1.0f;
     const float pre = down ? kDown : up ? kUp : 1.0f;
-    const float sum = sqrtf(down ? s.down : up ? s.up : s.plain) + eps * pre;
-    return {pre, sum == 0.0f ? 0.0f : 1.0f / sum};   // (zero stays zero without an eps)
+    const float norm = sqrtf(down ? s.down : up ? s.up : s.plain), sum = norm + eps * pre;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // (zero stays zero without an eps)
+    return {pre, inv, norm * inv > 0.0f ? norm * inv : 1.0f};
 }
 
 // The same from a matrix's parts (every thread of the block calls).
@@ -170,11 +271,15 @@ __device__ __forceinline__ void halves(const float (&v)[8], uint4 (&h)[kParts]) 
 template <typename T, int kParts, int V>
 __global__ void __launch_bounds__(kThreads)
 k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t cp, bool tall,
-             const Squares* __restrict__ part, int parts, float eps, __half* __restrict__ x,
-             size_t lo) {
+             const Squares* __restrict__ part, int parts, float eps, float* __restrict__ bound,
+             unsigned long long* __restrict__ trace, __half* __restrict__ x, size_t lo) {
     pdl_begin();
     const Inverse by = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
-    const float inv = by.inv * kScaleX;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) bound[(size_t)blockIdx.y * kMaxSteps] = by.norm;
+        if (threadIdx.x < kMaxSteps) trace[(size_t)blockIdx.y * kMaxSteps + threadIdx.x] = 0;
+    }
+    const float inv = by.inv * pow2(scale_x(by.norm));
     const T* m = g + (size_t)blockIdx.y * r * c;
     __half* o = x + (size_t)blockIdx.y * rp * cp;
     // a block takes 128 of what is contiguous in g, four a thread, of eight lines of it
@@ -266,12 +371,15 @@ struct Product {
     int tiles_m;              // row blocks of the product
     int tiles;                // per matrix
     int batch;
-    // D = alpha (accumulator) + beta C + gamma I, C and D in panels
+    Polynomial poly;
+    float* bound;             // X's, of this step and (written with X') the next: [batch][kMaxSteps]
+    unsigned long long* trace;   // A's, of this step (written with A): [batch][kMaxSteps]
+    bool last;
+    // A, P (where there is a C, which is A) or X', C and D in panels
     const __half* c;
     __half* d;
     size_t d_lo, d_size;      // also C's
     int64_t d_rows;
-    float alpha, beta, gamma;
     float *rest, *rows;       // [batch][rows], single halves (see Diagonals)
     // the result, where `out` is given: [r, c] or its transpose, unpadded
     void* out;
@@ -467,7 +575,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     const int row = quarter * 32 + lane;
     // columns col .. col + kCols - 1 of the tile from their finished sums
     using CHalves = uint4[kCols / 8][kParts];
-    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float alpha,
+    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float alpha, float beta, float gamma,
                       float rest, float (&v)[kCols]) {
         const int64_t grow = (int64_t)i * kBlock + row, gcol = (int64_t)j * kN + col;
         const int jb = j * (kN / kBlock) + col / kBlock;   // the columns' block of 128
@@ -487,26 +595,26 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
             for (int e = 0; e < 8; ++e) w[e] = alpha * v[8 * b + e];
             if (kGram && q.c) {
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) add_halves(w, c[b][p], q.beta);
+                for (int p = 0; p < kParts; ++p) add_halves(w, c[b][p], beta);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] += 8 * b + e == on ? q.gamma : 0.0f;
+                for (int e = 0; e < 8; ++e) w[e] += 8 * b + e == on ? gamma : 0.0f;
                 if (!kSplit && i == jb) {
                     const __half* e16 = reinterpret_cast<const __half*>(&c[b][0]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         w[e] += 8 * b + e == on
-                                    ? rest * (q.beta + 2.0f * alpha * __half2float(e16[e]))
+                                    ? rest * (beta + 2.0f * alpha * __half2float(e16[e]))
                                     : 0.0f;
                 }
             }
             uint4 h[kParts];
             halves<kParts>(w, h);
-            if (kGram && !kSplit && i == jb) {
+            if (kGram && i == jb) {
                 const __half* e16 = reinterpret_cast<const __half*>(&h[0]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     exact = 8 * b + e == on ? w[e] : exact;
-                    rounded = 8 * b + e == on ? __half2float(e16[e]) : rounded;
+                    if (!kSplit) rounded = 8 * b + e == on ? __half2float(e16[e]) : rounded;
                 }
             }
 #pragma unroll
@@ -524,6 +632,10 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         if (kGram && !kSplit && on >= 0 && on < kCols)
             (q.c ? q.rows : q.rest)[z * q.d_rows + grow] =
                 q.c ? row_factor(exact, rounded) : exact - rounded;
+        if (kGram && !q.c && q.poly.wild && i == jb) {   // (`exact` is zero where the diagonal is not here)
+            const uint32_t t = __reduce_add_sync(0xffffffffu, trace_units(exact));
+            if (lane == 0 && t) atomicAdd(q.trace + (size_t)z * kMaxSteps, (unsigned long long)t);
+        }
     };
 
     // a panel of the result from its sums: through the warp's exchange, so that
@@ -702,7 +814,25 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                                              rank * kCols + 8 * b,
                                          q.d_rows));
             }
-            float alpha = q.alpha;
+            float* const bound = q.bound + (size_t)z * kMaxSteps;
+            float alpha, beta = 0.0f, gamma = 0.0f;
+            if (kGram && !q.c) {
+                alpha = factor_a(*bound);
+            } else {
+                const float m = *bound;
+                const float u =
+                    known_bound(q.poly, m, __ull2float_ru(q.trace[(size_t)z * kMaxSteps]));
+                if (kGram) {
+                    const Factors f = factors_p(q.poly, m, u);
+                    alpha = f.p2;
+                    beta = f.p1;
+                    gamma = f.p0;
+                } else {
+                    const float next = next_bound(q.poly, m, u);
+                    alpha = factor_x(q.poly, m, u, next, q.last);
+                    if (!q.last && i == 0 && j == 0 && tid == 64) bound[1] = next;
+                }
+            }
             if (!kSplit && !kGram) alpha *= q.rows[z * q.d_rows + (int64_t)i * kBlock + row];
             const float rest = kGram && !kSplit && q.c
                                    ? q.rest[z * q.d_rows + (int64_t)i * kBlock + row] : 0.0f;
@@ -774,7 +904,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                     float w[kCols];
 #pragma unroll
                     for (int e = 0; e < kCols; ++e) w[e] = v[e % kPanel];
-                    finish(z, i, j, col, c[0], alpha, rest, w);   // (one panel where there is a C)
+                    finish(z, i, j, col, c[0], alpha, beta, gamma, rest, w);   // (one panel where there is a C)
                 } else {   // the result
                     store_result(z, i, j, col, alpha, v);
                 }
@@ -800,7 +930,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                             w[e + 2] += u.z;
                             w[e + 3] += u.w;
                         }
-                    finish(z, i, j, col, c[kGram ? m : 0], alpha, rest, w);
+                    finish(z, i, j, col, c[kGram ? m : 0], alpha, beta, gamma, rest, w);
                 }
             }
         }
@@ -853,7 +983,8 @@ struct Small {
     int ctas;              // of the cluster
     bool tall;
     int steps;
-    float a, b, c2, eps;
+    Polynomial poly;
+    float eps;
 };
 constexpr int kMaxShares = 8;
 // K of a sum in tensor memory (as kChunk).  Pairs: of 256, 128 x 2000 was 1.25
@@ -883,6 +1014,12 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     // the diagonals of A and P, in the room that the MMAs' unused rows reach into
     float* a_diag = reinterpret_cast<float*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas));
     float* p_diag = a_diag + kBlock;
+    // this step's factors (read where they are used: registers are short) and bounds of X and A
+    struct Held {
+        Factors p;
+        float a, x, m, u;
+    };
+    Held* held = reinterpret_cast<Held*>(p_diag + kBlock);
     uint64_t* mbar = reinterpret_cast<uint64_t*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas) +
                                                  (kBlock - 16) * 128);
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
@@ -922,7 +1059,11 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         sq = s_norm;
     }
     const Inverse by = norm_inverse(sq, q.eps);
-    const float inv = by.inv * kScaleX;
+    const float inv = by.inv * pow2(scale_x(by.norm));
+    if (tid == kSmallThreads - 1) {
+        held->m = by.norm;
+        held->a = factor_a(by.norm);
+    }
 #pragma unroll 4
     for (int i = tid; i < q.rn * q.xp * 8; i += kSmallThreads) {
         const int xr = q.tall ? i % q.rn : i / (q.xp * 8);
@@ -1128,12 +1269,13 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         }
         if (!ok) continue;
         if (busy) {
+            const float fa = held->a;
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
                 if (m < r_mine) {
                     const int col = 16 * (group + kSmallGroups * m);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[m][e] *= kScaleA / (kScaleX * kScaleX);
+                    for (int e = 0; e < 16; ++e) acc[m][e] *= fa;
                     if (col / 32 == quarter) off_diagonal(a_diag, col, acc[m]);
                     put(as, col, acc[m]);
                 }
@@ -1142,10 +1284,23 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         ready();
         // ---- P = a I + b A + c A A
         if (tid == 0) issue(0, 0, q.rn, a0, a0, q.rn, 0, r_units, false);
+        const bool last = step + 1 == q.steps;
+        constexpr int kScaler = kSmallThreads / 32 - 1;   // a warp sees to the scales meanwhile
+        if (warp == kScaler) {
+            uint32_t t = 0u;
+            if (q.poly.wild) {
+                for (int i = lane; i < q.rn; i += 32) t += trace_units(a_diag[i]);
+                t = __reduce_add_sync(0xffffffffu, t);
+            }
+            const float m = held->m, u = known_bound(q.poly, m, (float)t);
+            if (lane == 0) {
+                held->p = factors_p(q.poly, m, u);
+                held->u = u;
+            }
+        }
         if (!await(0)) continue;
         if (busy) {
-            constexpr float k2 = kScaleP / (kScaleA * kScaleA);
-            const float d = a_diag[row];
+            const float d = a_diag[row], p2 = held->p.p2, p1 = held->p.p1, p0 = held->p.p0;
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
                 if (m >= r_mine) continue;
@@ -1155,16 +1310,13 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                 if (row < q.rn) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {   // (acc is O here)
-                        const float beta =
-                            q.b * (kScaleP / kScaleA) + q.c2 * k2 * (d + a_diag[col + e]);
-                        v[e] = fmaf(beta, acc[m][e], v[e] * (q.c2 * k2));
+                        const float beta = fmaf(p2, d + a_diag[col + e], p1);
+                        v[e] = fmaf(beta, acc[m][e], v[e] * p2);
                     }
                     if (col / 32 == quarter) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)   // (O is zero there)
-                            v[e] += col + e == row ? q.a * kScaleP + d * (q.b * (kScaleP / kScaleA) +
-                                                                          q.c2 * k2 * d)
-                                                   : 0.0f;
+                            v[e] += col + e == row ? fmaf(d, fmaf(p2, d, p1), p0) : 0.0f;
                     }
                 }
                 if (col / 32 == quarter) off_diagonal(p_diag, col, v);
@@ -1173,12 +1325,17 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         }
         ready();
         const float d = busy ? p_diag[row] : 0.0f;
-        const bool last = step + 1 == q.steps;
         // ---- X' = P X, 256 columns at a time; the last one is the result
         for (int c0 = 0; c0 < cn; c0 += 256) {
             const int n = min(256, cn - c0);
             if (tid == 0)
                 issue(0, 0, 256, a0, x0 + (uint32_t)(c0 / kPanel) * kParts * pb, n, 0, r_units, true);
+            if (c0 == 0 && tid == kScaler * 32) {
+                const float m = held->m, next = next_bound(q.poly, m, held->u);
+                held->x = factor_x(q.poly, m, held->u, next, last);
+                held->a = factor_a(next);
+                held->m = next;
+            }
             uint4 x[2][kParts];   // this row's halves of X in the next unit
             const auto fetch = [&](int u) {
                 if (row >= q.rn || u >= n / 16) return;
@@ -1194,13 +1351,13 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             fetch(group);
             if (!await(0)) break;
             if (busy) {
+                const float unit = held->x;
 #pragma unroll 1
                 for (int u = group; u < n / 16; u += kSmallGroups) {
                     float v[16];
                     sums(16 * u, 256 + 16 * u, v);
                     if (row >= q.rn) continue;
                     const int col = c0 + 16 * u;
-                    const float unit = last ? 1.0f / (kScaleP * kScaleX) : 1.0f / kScaleP;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         float w[8];
@@ -1311,6 +1468,8 @@ struct Space {
     __half *x[2], *a, *p;
     size_t x_lo, a_lo;
     Squares* part;
+    float* bound;
+    unsigned long long* trace;
     float *rest, *rows;
 };
 Space carve(Carve& w, int64_t batch, const Plan& p) {
@@ -1321,6 +1480,8 @@ Space carve(Carve& w, int64_t batch, const Plan& p) {
     s.a = w.take<__half>(s.a_lo * p.parts);
     s.p = w.take<__half>(s.a_lo * p.parts);
     s.part = w.take<Squares>((size_t)batch * kNormBlocks);
+    s.bound = w.take<float>((size_t)batch * kMaxSteps);
+    s.trace = w.take<unsigned long long>((size_t)batch * kMaxSteps);
     s.rest = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
     s.rows = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
     return s;
@@ -1365,7 +1526,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         constexpr int V = VecOf<T>::n;
         const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16,
                       (int)ceil_div(ceil_div(p.c, kPanel), p.ctas), (int)ceil_div(p.r, kPanel),
-                      p.ctas, p.tall, o.steps, o.a, o.b, o.c, o.eps};
+                      p.ctas, p.tall, o.steps, polynomial(o.a, o.b, o.c, o.steps), o.eps};
         // (the loads of `grad` and the stores to `out` are of one width)
         const bool vec = !p.tall && p.c % V == 0 && aligned16(o.grad) && aligned16(o.out);
         cudaLaunchConfig_t cfg = {};
@@ -1413,8 +1574,10 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
     const int64_t pieces = ceil_div(inner, 128) * ceil_div(lines, 8);
     const dim3 grid((unsigned)(pieces < 2432 ? pieces : 2432), B);
     e = launch_pdl(start, grid, dim3(kThreads), 0, s, (const T*)o.grad, p.r, p.c,
-                   p.rp, p.cp, p.tall, (const Squares*)w.part, parts, o.eps, w.x[0], w.x_lo);
+                   p.rp, p.cp, p.tall, (const Squares*)w.part, parts, o.eps, w.bound, w.trace, w.x[0],
+                   w.x_lo);
     const int tm = (int)(p.rp / kBlock);
+    const Polynomial poly = polynomial(o.a, o.b, o.c, o.steps);
     for (int k = 0; k < o.steps && e == cudaSuccess; ++k) {
         const __half* x = w.x[k & 1];
         Product g{};   // A = X X^T
@@ -1430,7 +1593,10 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         g.d_lo = w.a_lo;
         g.d_size = (size_t)p.rp * p.rp;
         g.d_rows = p.rp;
-        g.alpha = kScaleA / (kScaleX * kScaleX);
+        g.poly = poly;
+        g.bound = w.bound + k;
+        g.trace = w.trace + k;
+        g.last = k + 1 == o.steps;
         g.rest = w.rest;
         g.rows = w.rows;
         e = symmetric<kSplit>(g, st, n_sms, s);
@@ -1441,9 +1607,6 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         h.l_size = h.r_size = (size_t)p.rp * p.rp;
         h.k_panels = (int)(p.rp / kPanel);
         h.d = w.p;
-        h.alpha = o.c * (kScaleP / (kScaleA * kScaleA));
-        h.beta = o.b * (kScaleP / kScaleA);
-        h.gamma = o.a * kScaleP;
         e = symmetric<kSplit>(h, st, n_sms, s);
         if (e != cudaSuccess) return e;
         Product f = g;   // X' = P X
@@ -1454,14 +1617,12 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         f.d = w.x[(k + 1) & 1];
         f.d_lo = w.x_lo;
         f.d_size = (size_t)p.rp * p.cp;
-        f.alpha = 1.0f / kScaleP;
         if (k + 1 == o.steps) {
             f.out = o.out;
             f.out_r = p.r;
             f.out_c = p.c;
             f.tall = p.tall;
             f.dtype = o.dtype;
-            f.alpha = 1.0f / (kScaleP * kScaleX);
         }
         // 256 columns a tile move fewer operand bytes per product; 128 give twice the tiles
         const bool wide = !kSplit && p.cp % 256 == 0 &&
@@ -1498,6 +1659,19 @@ size_t orth_workspace(int64_t batch, int64_t m, int64_t n, int dtype) {
     Carve cv{nullptr};
     carve(cv, batch, plan_of(batch, m, n, dtype));
     return cv.used;
+}
+
+bool orth_in_range(int steps, float a, float b, float c) {
+    const Polynomial p = polynomial(a, b, c, 0);
+    float m = 1.0f;
+    for (int k = 0; k < steps; ++k) {
+        // (in this form a NaN is refused too)
+        if (!(m < ldexpf(1.0f, kMostX) && p.at(m * m) < ldexpf(1.0f, kMostP) &&
+              p.most_q(m * m) < ldexpf(1.0f, kMostP)))
+            return false;
+        m = p.most_s(m * m);
+    }
+    return true;
 }
 
 cudaError_t prepare_orth() {
