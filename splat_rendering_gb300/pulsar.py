@@ -600,6 +600,8 @@ class Learner:
             raise ValueError(f"grad has shape {tuple(shape)}, wanted [..., m, n]")
         dt = _dtype_code(grad.dtype)
         out, p_out = self._out(out, "out", shape, grad.dtype, stream)
+        if len(coeffs) != 3:
+            raise ValueError(f"coeffs are (a, b, c), got {len(coeffs)} values")
         abc = (ctypes.c_float * 3)(*[float(v) for v in coeffs])
         _check(self._lib.pulsar_orthogonalize(
             self.handle, self._tensor(grad, "grad"), self._product(shape[:-2]), shape[-2], shape[-1],
