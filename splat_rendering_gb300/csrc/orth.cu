@@ -1436,6 +1436,7 @@ struct Plan {
     bool tall;
     int parts;
     int ctas;               // on chip: a cluster of them takes a matrix through all steps; else 0
+    int norm_blocks;        // per matrix, of the norm by a launch of its own
 };
 Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
     Plan p;
@@ -1446,6 +1447,8 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
     p.rp = p.r > 1024 ? ceil_div(p.r, 2 * kBlock) * 2 * kBlock : ceil_div(p.r, kBlock) * kBlock;
     const int64_t to = p.c > 1024 ? 256 : 128;   // two widths of a tile of the last product
     p.cp = ceil_div(p.c, to) * to;
+    const int64_t chunks = ceil_div(p.r * p.c, kThreads * 16);
+    p.norm_blocks = (int)(chunks < kNormBlocks ? chunks : kNormBlocks);
     // pairs in 16 bits too where there are too few elements for the roundings of single halves to
     // average out (5 x 6: the result up to 2.4 times as far off as its own rounding; with pairs 1.0;
     // 16 x 16: 14.7 us instead of 13)
@@ -1473,13 +1476,14 @@ struct Space {
     float *rest, *rows;
 };
 Space carve(Carve& w, int64_t batch, const Plan& p) {
-    Space s;
+    Space s{};
+    s.part = w.take<Squares>((size_t)batch * p.norm_blocks);
+    if (p.ctas > 0) return s;   // on chip, all but the norm where no step follows it
     s.x_lo = (size_t)batch * p.rp * p.cp;
     s.a_lo = (size_t)batch * p.rp * p.rp;
     for (int k = 0; k < 2; ++k) s.x[k] = w.take<__half>(s.x_lo * p.parts);
     s.a = w.take<__half>(s.a_lo * p.parts);
     s.p = w.take<__half>(s.a_lo * p.parts);
-    s.part = w.take<Squares>((size_t)batch * kNormBlocks);
     s.bound = w.take<float>((size_t)batch * kMaxSteps);
     s.trace = w.take<unsigned long long>((size_t)batch * kMaxSteps);
     s.rest = w.take<float>(p.parts == 1 ? (size_t)batch * p.rp : 0);
@@ -1552,8 +1556,7 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
     const Space w = carve(cv, o.batch, p);
     const unsigned B = (unsigned)o.batch;
     const int64_t elems = p.r * p.c;
-    const int64_t want = ceil_div(elems, kThreads * 16);
-    const int parts = (int)(want < kNormBlocks ? want : kNormBlocks);
+    const int parts = p.norm_blocks;
     const auto flat = [&](int64_t items) {
         const int64_t b = ceil_div(items, kThreads);
         return dim3((unsigned)(b < 2048 ? b : 2048), B);
