@@ -325,7 +325,8 @@ int pulsar_render_noalloc(const float* pos, const float* radius, const float* op
  * asynchronous on the caller's stream and issued in order on one stream per
  * handle, argument errors found on the host before anything is enqueued.
  * `dtype` is the type of the tensors given as void*; every sum, statistic and
- * norm is held in 32 bits or more, and a bfloat16 result is rounded once.
+ * norm is held in 32 bits or more, and a bfloat16 result is rounded once
+ * (the orthogonalisation rounds its operands too, as said there).
  * Tensors need their element's alignment; where they (and their rows) are
  * 16-byte aligned the kernels move 16 bytes at a time.  Results do not depend
  * on the launch: the same inputs give the same bits. */
@@ -411,6 +412,15 @@ int pulsar_group_norm_backward(pulsar_learn_t h, const void* grad_y, const void*
  * towards 1 and keeps the singular vectors; a zero matrix stays zero.
  *   grad, out [batch,m,n] dtype, out overwritten; out may be grad
  * 0 <= batch <= 65535, 0 <= m, n <= 65536, 0 <= steps <= 100, eps >= 0.
+ * X, A and P are rounded to the tensor cores' operands in every step: in
+ * float32, and in bfloat16 where the smaller side is at most 32 and the larger
+ * at most 256, to pairs of halves (22 bits), in bfloat16 otherwise to single
+ * halves (11 bits; A's and P's diagonals are kept exact).  Sums have 32 bits.
+ * The usual coefficients' result is then about as near as that of 32-bit
+ * products in float32 (at most twice as far off), and in bfloat16 at most
+ * sqrt(2) times as far off as its own rounding (2048 x 4096: 1.2 times).  The
+ * halves are scaled to the largest value that the iterates can take, and their
+ * roundings are relative to that, down to 2^-36 of it.
  * With q(u) = a + b u + c u^2 and m_0 = 1, m_k+1 = max |s q(s^2)| over
  * 0 <= s <= m_k bounds the singular values of X_k+1: coefficients for which an
  * m_k before the last step's result reaches 2^30, or |q| 2^96 on the way, are

@@ -594,7 +594,10 @@ class Learner:
 
     def orthogonalize(self, grad, steps: int = 5, coeffs=(3.4445, -4.775, 2.0315),
                       eps: float = 1e-7, out=None, stream=None):
-        """`steps` Newton-Schulz products on each matrix of grad [..., m, n]."""
+        """`steps` Newton-Schulz products on each matrix of grad [..., m, n].
+        In bfloat16 the iterates are rounded to 11 bits in every step, in
+        float32 to 22 (include/pulsar.h says how far off that leaves the
+        result); convert the matrix first where 16 bits want more."""
         shape = grad.shape
         if len(shape) < 2:
             raise ValueError(f"grad has shape {tuple(shape)}, wanted [..., m, n]")
