@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <cstring>
 
 namespace pulsar {
 namespace {
@@ -89,20 +90,25 @@ Polynomial polynomial(float fa, float fb, float fc, int steps) {
 }
 
 // The smallest e, within the limits, with v < 2^e.
-__device__ __forceinline__ int above(float v, int lo, int hi) {
-    const int e = (__float_as_int(v) >> 23 & 255) - 126;   // (below the limits where v is subnormal)
-    return min(max(e, lo), hi);
+__host__ __device__ __forceinline__ int above(float v, int lo, int hi) {
+    int bits;
+    memcpy(&bits, &v, 4);
+    const int e = (bits >> 23 & 255) - 126;   // (below the limits where v is subnormal)
+    return e < lo ? lo : e > hi ? hi : e;
 }
-__device__ __forceinline__ float pow2(int e) {   // zero below the normal ones
-    return __int_as_float(min(max(e + 127, 0), 254) << 23);
+__host__ __device__ __forceinline__ float pow2(int e) {   // zero below the normal ones
+    const int b = e + 127, bits = (b < 0 ? 0 : b > 254 ? 254 : b) << 23;
+    float v;
+    memcpy(&v, &bits, 4);
+    return v;
 }
-__device__ __forceinline__ float times_pow2(float v, int e) {   // (|e| below 252)
+__host__ __device__ __forceinline__ float times_pow2(float v, int e) {   // (|e| below 252)
     return v * pow2(e >> 1) * pow2(e - (e >> 1));
 }
 // log2 of the scales for the bounds of X, of X in A = X X^T, and of P
-__device__ __forceinline__ int scale_x(float m) { return 14 - above(m, -100, kMostX + 1); }
-__device__ __forceinline__ int scale_a(float m) { return 13 - above(m * m, -126, 2 * kMostX + 2); }
-__device__ __forceinline__ int scale_p(float q) { return 13 - above(q, -60, kMostP + 1); }
+__host__ __device__ __forceinline__ int scale_x(float m) { return 14 - above(m, -100, kMostX + 1); }
+__host__ __device__ __forceinline__ int scale_a(float m) { return 13 - above(m * m, -126, 2 * kMostX + 2); }
+__host__ __device__ __forceinline__ int scale_p(float q) { return 13 - above(q, -60, kMostP + 1); }
 
 // A trace's part in whole numbers of 2^-10 stored units, rounded up: their sum has no order (and
 // that of 128 rows, each below 2^13, no overflow).
@@ -118,20 +124,20 @@ __device__ __forceinline__ float known_bound(const Polynomial& p, float m, float
 struct Factors {
     float p2, p1, p0;
 };
-__device__ __forceinline__ Factors factors_p(const Polynomial& p, float m, float u) {
+__host__ __device__ __forceinline__ Factors factors_p(const Polynomial& p, float m, float u) {
     const int sa = scale_a(m), sp = scale_p(p.most_q(u));
-    return {times_pow2(p.c, max(sp - 2 * sa, -250)), times_pow2(p.b, sp - sa), times_pow2(p.a, sp)};
+    return {times_pow2(p.c, sp - 2 * sa < -250 ? -250 : sp - 2 * sa), times_pow2(p.b, sp - sa), times_pow2(p.a, sp)};
 }
 // X's next bound.  (sqrt(u) loses a bound below 2^-63, whose steps are all a X)
-__device__ __forceinline__ float next_bound(const Polynomial& p, float m, float u) {
+__host__ __device__ __forceinline__ float next_bound(const Polynomial& p, float m, float u) {
     return m > 0x1p-30f ? p.most_s(u) : fmaxf(p.most_s(u), m * fabsf(p.a));
 }
 // The factor of X' = x (P X), whose bound is `next`; the last X' is the result itself.
-__device__ __forceinline__ float factor_x(const Polynomial& p, float m, float u, float next, bool last) {
+__host__ __device__ __forceinline__ float factor_x(const Polynomial& p, float m, float u, float next, bool last) {
     return times_pow2(1.0f, (last ? 0 : scale_x(next)) - scale_p(p.most_q(u)) - scale_x(m));
 }
 // The factor of A = X X^T
-__device__ __forceinline__ float factor_a(float m) { return pow2(scale_a(m) - 2 * scale_x(m)); }
+__host__ __device__ __forceinline__ float factor_a(float m) { return pow2(scale_a(m) - 2 * scale_x(m)); }
 
 // Element (row, col) of a matrix of `rows` padded rows, in halves.
 __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, int64_t rows) {
@@ -157,28 +163,69 @@ struct __align__(16) Squares {
     }
 };
 
+// What is seldom needed is kept out of line: a launch on chip waits for its instructions, and
+// those that it does not run cost it up to 2 us of 16 where they stand between the others.
+template <int kN>
+__device__ __forceinline__ float sum_of_warps(float v, float* s) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    return v;
+}
+template <int kN>
+__device__ __forceinline__ float sum_of_block(const float* s) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kN / 32; ++w) t += s[w];
+    return t;
+}
+template <int kN>
+__device__ __noinline__ void sum_ends(Squares* v, float* s) {
+    for (float* f : {&v->down, &v->up}) {
+        sum_of_warps<kN>(*f, s);
+        __syncthreads();
+        *f = sum_of_block<kN>(s);
+        __syncthreads();
+    }
+}
 template <int kN = kThreads>
 __device__ __forceinline__ Squares block_sum(Squares v) {
-    __shared__ Squares s[kN / 32];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        v.plain += __shfl_xor_sync(0xffffffffu, v.plain, o);
-        v.down += __shfl_xor_sync(0xffffffffu, v.down, o);
-        v.up += __shfl_xor_sync(0xffffffffu, v.up, o);
-    }
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
+    __shared__ float s[kN / 32];
+    sum_of_warps<kN>(v.plain, s);
+    const bool ends = __syncthreads_or(v.down != 0.0f || v.up != 0.0f);
     Squares t{};
-#pragma unroll
-    for (int w = 0; w < kN / 32; ++w) t.add(s[w]);
+    t.plain = sum_of_block<kN>(s);
     __syncthreads();
+    if (ends) {
+        t.down = v.down;
+        t.up = v.up;
+        sum_ends<kN>(&t, s);
+    }
     return t;
+}
+
+// The scaled sums of a thread's next kNormAhead vectors.
+template <typename T, int V>
+__device__ __noinline__ Squares squares_ends(const T* __restrict__ m, int64_t vectors, int64_t i,
+                                             int64_t step) {
+    Squares s{};
+    for (int k = 0; k < kNormAhead && i < vectors; ++k, i += step) {
+        float v[V], d = 0.0f, u = 0.0f;
+        Pack<T, V>::load(m + i * V, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            d = fmaf(v[j] * kDown, v[j] * kDown, d);
+            u = fmaf(v[j] * kUp, v[j] * kUp, u);
+        }
+        s.down += d;
+        s.up += u;
+    }
+    return s;
 }
 
 // The squares of a matrix's vectors i0, i0 + step, ...  The scaled sums count where the total is
 // beyond 2^128 or below 2^-80: a vector of 2^-60 to 2^60 is nothing to the first and cannot be in
-// the second, so that theirs are seldom taken (and by a loop that is short in code: a launch on
-// chip waits for its instructions).
+// the second, so that theirs are seldom taken.
 template <typename T, int V>
 __device__ __forceinline__ Squares sum_squares(const T* __restrict__ m, int64_t vectors, int64_t i0,
                                                int64_t step) {
@@ -199,19 +246,7 @@ __device__ __forceinline__ Squares sum_squares(const T* __restrict__ m, int64_t 
             s.plain += p;
             ends |= !(p >= 0x1p-60f && p <= 0x1p60f);
         }
-        if (!ends) continue;
-#pragma unroll 1
-        for (int k = 0; k < kNormAhead && i + k * step < vectors; ++k) {
-            float v[V], d = 0.0f, u = 0.0f;
-            Pack<T, V>::load(m + (i + k * step) * V, v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                d = fmaf(v[j] * kDown, v[j] * kDown, d);
-                u = fmaf(v[j] * kUp, v[j] * kUp, u);
-            }
-            s.down += d;
-            s.up += u;
-        }
+        if (ends) s.add(squares_ends<T, V>(m, vectors, i, step));
     }
     return s;
 }
@@ -976,6 +1011,16 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 // every fourth 16 of the columns.
 constexpr int kSmallThreads = 512;
 constexpr int kSmallGroups = kSmallThreads / 128;
+constexpr int kKnownSteps = 16;
+
+struct StepFactors {
+    Factors p;
+    float a, x;   // of A and of X'
+};
+struct Held {   // in shared memory
+    float m, u;   // bounds of X and A, where they have to be worked out
+    StepFactors of[kMaxSteps];
+};
 
 struct Small {
     int r, c, rn;          // rn: padded to 16
@@ -985,6 +1030,9 @@ struct Small {
     int steps;
     Polynomial poly;
     float eps;
+    // the factors where |X_0|_F is 1 or little less and the traces are not needed, as nearly always
+    bool known;
+    StepFactors of[kKnownSteps];
 };
 constexpr int kMaxShares = 8;
 // K of a sum in tensor memory (as kChunk).  Pairs: of 256, 128 x 2000 was 1.25
@@ -1001,7 +1049,37 @@ size_t small_bytes(int parts, int rn, int xp, int ap, int ctas) {
            (kBlock - 16) * 128 + 64 + 1024;
 }
 
-template <typename T, bool kSplit, int V>
+constexpr int kScaler = kSmallThreads / 32 - 1;   // the warp that works out factors
+// Those of every step, a lane a step, where no trace is needed but |X_0|_F is small.
+__device__ __noinline__ void scale_steps(const Polynomial& p, float m, int steps, StepFactors* of) {
+    for (int at = 0, k = threadIdx.x & 31; k < steps; k += 32) {
+        for (; at < k; ++at) m = next_bound(p, m, m * m);
+        const float u = m * m;
+        of[k] = {factors_p(p, m, u), factor_a(m),
+                 factor_x(p, m, u, next_bound(p, m, u), k + 1 == steps)};
+    }
+}
+// A step's of P, by a warp while the others wait for A A, and of X' and the next A, by a thread
+// while they wait for P X.
+__device__ __noinline__ void scale_p_step(const Polynomial& p, const float* a_diag, int rn, int step,
+                                          Held* held) {
+    uint32_t t = 0u;
+    for (int i = threadIdx.x & 31; i < rn; i += 32) t += trace_units(a_diag[i]);
+    const float m = held->m, u = known_bound(p, m, (float)__reduce_add_sync(0xffffffffu, t));
+    if ((threadIdx.x & 31) == 0) {
+        held->of[step].p = factors_p(p, m, u);
+        held->u = u;
+    }
+}
+__device__ __noinline__ void scale_x_step(const Polynomial& p, int step, int steps, Held* held) {
+    const float m = held->m, u = held->u, next = next_bound(p, m, u);
+    held->of[step].x = factor_x(p, m, u, next, step + 1 == steps);
+    if (step + 1 < steps) held->of[step + 1].a = factor_a(next);
+    held->m = next;
+}
+
+// kWild: poly.wild.
+template <typename T, bool kSplit, int V, bool kWild>
 __global__ void __launch_bounds__(kSmallThreads, 1)
 k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out, LearnState* st) {
     constexpr int kParts = kSplit ? 2 : 1;
@@ -1014,12 +1092,8 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
     // the diagonals of A and P, in the room that the MMAs' unused rows reach into
     float* a_diag = reinterpret_cast<float*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas));
     float* p_diag = a_diag + kBlock;
-    // this step's factors (read where they are used: registers are short) and bounds of X and A
-    struct Held {
-        Factors p;
-        float a, x, m, u;
-    };
     Held* held = reinterpret_cast<Held*>(p_diag + kBlock);
+    static_assert(2 * kBlock * 4 + sizeof(Held) <= (kBlock - 16) * 128, "room for the factors");
     uint64_t* mbar = reinterpret_cast<uint64_t*>(as + small_a_bytes(kParts, q.rn, q.ap, q.ctas) +
                                                  (kBlock - 16) * 128);
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(mbar + 2);
@@ -1059,10 +1133,17 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         sq = s_norm;
     }
     const Inverse by = norm_inverse(sq, q.eps);
-    const float inv = by.inv * pow2(scale_x(by.norm));
-    if (tid == kSmallThreads - 1) {
+    const bool known = !kWild && q.known && by.norm >= 0.5f;
+    const float inv = by.inv * pow2(scale_x(known ? 1.0f : by.norm));
+    if (known) {
+        constexpr int kEach = sizeof(StepFactors) / 4;
+        if (tid < q.steps * kEach)
+            reinterpret_cast<float*>(held->of)[tid] = reinterpret_cast<const float*>(q.of)[tid];
+    } else if (kWild && tid == 0) {
         held->m = by.norm;
-        held->a = factor_a(by.norm);
+        held->of[0].a = factor_a(by.norm);
+    } else if (!kWild && warp == kScaler) {
+        scale_steps(q.poly, by.norm, q.steps, held->of);
     }
 #pragma unroll 4
     for (int i = tid; i < q.rn * q.xp * 8; i += kSmallThreads) {
@@ -1269,7 +1350,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         }
         if (!ok) continue;
         if (busy) {
-            const float fa = held->a;
+            const float fa = held->of[step].a;
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
                 if (m < r_mine) {
@@ -1285,22 +1366,11 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
         // ---- P = a I + b A + c A A
         if (tid == 0) issue(0, 0, q.rn, a0, a0, q.rn, 0, r_units, false);
         const bool last = step + 1 == q.steps;
-        constexpr int kScaler = kSmallThreads / 32 - 1;   // a warp sees to the scales meanwhile
-        if (warp == kScaler) {
-            uint32_t t = 0u;
-            if (q.poly.wild) {
-                for (int i = lane; i < q.rn; i += 32) t += trace_units(a_diag[i]);
-                t = __reduce_add_sync(0xffffffffu, t);
-            }
-            const float m = held->m, u = known_bound(q.poly, m, (float)t);
-            if (lane == 0) {
-                held->p = factors_p(q.poly, m, u);
-                held->u = u;
-            }
-        }
+        if (kWild && warp == kScaler) scale_p_step(q.poly, a_diag, q.rn, step, held);
         if (!await(0)) continue;
         if (busy) {
-            const float d = a_diag[row], p2 = held->p.p2, p1 = held->p.p1, p0 = held->p.p0;
+            const float d = a_diag[row];
+            const Factors f = held->of[step].p;
 #pragma unroll
             for (int m = 0; m < kMost; ++m) {
                 if (m >= r_mine) continue;
@@ -1310,13 +1380,13 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
                 if (row < q.rn) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {   // (acc is O here)
-                        const float beta = fmaf(p2, d + a_diag[col + e], p1);
-                        v[e] = fmaf(beta, acc[m][e], v[e] * p2);
+                        const float beta = fmaf(f.p2, d + a_diag[col + e], f.p1);
+                        v[e] = fmaf(beta, acc[m][e], v[e] * f.p2);
                     }
                     if (col / 32 == quarter) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)   // (O is zero there)
-                            v[e] += col + e == row ? fmaf(d, fmaf(p2, d, p1), p0) : 0.0f;
+                            v[e] += col + e == row ? fmaf(d, fmaf(f.p2, d, f.p1), f.p0) : 0.0f;
                     }
                 }
                 if (col / 32 == quarter) off_diagonal(p_diag, col, v);
@@ -1330,12 +1400,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             const int n = min(256, cn - c0);
             if (tid == 0)
                 issue(0, 0, 256, a0, x0 + (uint32_t)(c0 / kPanel) * kParts * pb, n, 0, r_units, true);
-            if (c0 == 0 && tid == kScaler * 32) {
-                const float m = held->m, next = next_bound(q.poly, m, held->u);
-                held->x = factor_x(q.poly, m, held->u, next, last);
-                held->a = factor_a(next);
-                held->m = next;
-            }
+            if (kWild && c0 == 0 && tid == kScaler * 32) scale_x_step(q.poly, step, q.steps, held);
             uint4 x[2][kParts];   // this row's halves of X in the next unit
             const auto fetch = [&](int u) {
                 if (row >= q.rn || u >= n / 16) return;
@@ -1351,7 +1416,7 @@ k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out
             fetch(group);
             if (!await(0)) break;
             if (busy) {
-                const float unit = held->x;
+                const float unit = held->of[step].x;
 #pragma unroll 1
                 for (int u = group; u < n / 16; u += kSmallGroups) {
                     float v[16];
@@ -1528,9 +1593,17 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
     const Plan p = plan_of(o.batch, o.m, o.n, o.dtype);
     if (o.steps > 0 && p.ctas > 0) {
         constexpr int V = VecOf<T>::n;
-        const Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16,
-                      (int)ceil_div(ceil_div(p.c, kPanel), p.ctas), (int)ceil_div(p.r, kPanel),
-                      p.ctas, p.tall, o.steps, polynomial(o.a, o.b, o.c, o.steps), o.eps};
+        Small q{(int)p.r, (int)p.c, (int)ceil_div(p.r, 16) * 16,
+                (int)ceil_div(ceil_div(p.c, kPanel), p.ctas), (int)ceil_div(p.r, kPanel),
+                p.ctas, p.tall, o.steps, polynomial(o.a, o.b, o.c, o.steps), o.eps};
+        q.known = !q.poly.wild && o.steps <= kKnownSteps;
+        float m = 1.0f;
+        for (int k = 0; q.known && k < o.steps; ++k) {
+            const float u = m * m, next = next_bound(q.poly, m, u);
+            q.of[k] = {factors_p(q.poly, m, u), factor_a(m),
+                       factor_x(q.poly, m, u, next, k + 1 == o.steps)};
+            m = next;
+        }
         // (the loads of `grad` and the stores to `out` are of one width)
         const bool vec = !p.tall && p.c % V == 0 && aligned16(o.grad) && aligned16(o.out);
         cudaLaunchConfig_t cfg = {};
@@ -1549,7 +1622,10 @@ cudaError_t run(const OrthCall& o, LearnState* st, void* ws, int n_sms, cudaStre
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, vec ? k_orth_small<T, kSplit, V> : k_orth_small<T, kSplit, 1>,
+        // (a wild polynomial has one form: nothing waits for it)
+        return cudaLaunchKernelEx(&cfg, q.poly.wild ? k_orth_small<T, kSplit, 1, true>
+                                        : vec       ? k_orth_small<T, kSplit, V, false>
+                                                    : k_orth_small<T, kSplit, 1, false>,
                                   (const T*)o.grad, q, (T*)o.out, st);
     }
     Carve cv{static_cast<unsigned char*>(ws)};
@@ -1682,12 +1758,16 @@ cudaError_t prepare_orth() {
     if (e == cudaSuccess) e = prepare_type<true>();
     if (e == cudaSuccess) e = prepare_one<false, 256, false>();
     if (e == cudaSuccess) e = prepare_one<false, 256, true, 2>();
-    for (const void* k : {(const void*)k_orth_small<float, true, 1>,
-                          (const void*)k_orth_small<float, true, 4>,
-                          (const void*)k_orth_small<__nv_bfloat16, true, 1>,
-                          (const void*)k_orth_small<__nv_bfloat16, true, 8>,
-                          (const void*)k_orth_small<__nv_bfloat16, false, 1>,
-                          (const void*)k_orth_small<__nv_bfloat16, false, 8>})
+    using B = __nv_bfloat16;
+    for (const void* k : {(const void*)k_orth_small<float, true, 1, false>,
+                          (const void*)k_orth_small<float, true, 4, false>,
+                          (const void*)k_orth_small<float, true, 1, true>,
+                          (const void*)k_orth_small<B, true, 1, false>,
+                          (const void*)k_orth_small<B, true, 8, false>,
+                          (const void*)k_orth_small<B, true, 1, true>,
+                          (const void*)k_orth_small<B, false, 1, false>,
+                          (const void*)k_orth_small<B, false, 8, false>,
+                          (const void*)k_orth_small<B, false, 1, true>})
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     return e;

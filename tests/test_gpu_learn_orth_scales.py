@@ -68,3 +68,21 @@ def test_coefficients_that_leave_the_range_are_refused(ops):
         with pytest.raises(pl.PulsarError):
             ops.orthogonalize(g, steps=steps, coeffs=coeffs)
     ops.orthogonalize(g, steps=100, coeffs=(1.5, -0.5, 0.0))
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-9, 1e-14])
+@pytest.mark.parametrize("steps", [60, 100])
+def test_many_steps_end_at_the_polar_factor(ops, steps, scale):
+    """(1.5, -0.5, 0) takes every singular value to 1, where its slope is zero:
+    what is left is the last step's own rounding, (|a| + 3 |b|) 2^-20 |X|_F,
+    and as much again for what the one before moved.  Matrices far below eps
+    spend their first steps on growing (1.5^60 = 4e10)."""
+    for shape in SHAPES:
+        g = torch.randn(*shape, generator=torch.Generator().manual_seed(5)).double()
+        u, _, vh = torch.linalg.svd(g, full_matrices=False)
+        s = torch.linspace(1.0, 0.2, u.shape[-1], dtype=torch.float64)
+        g = (scale * (u * s) @ vh).float()
+        got = ops.orthogonalize(g.cuda(), steps=steps, coeffs=(1.5, -0.5, 0.0)).cpu().double()
+        want = u @ vh   # (the polar factor; the rounding of g to 32 bits moves it by 2^-24 / 0.2)
+        err = (got - want).flatten(-2).norm(dim=-1)
+        assert (err <= 8 * 2.0 ** -20 * want.flatten(-2).norm(dim=-1)).all(), (shape, err)
