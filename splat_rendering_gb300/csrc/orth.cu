@@ -994,14 +994,14 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
 // shares, in the order of the CTAs, for everybody, and goes on with the same A
 // and its own columns.  Bound by latency: a step of a 64 x 64 matrix takes 4.2
 // us (MMAs 1.7, epilogues and their barriers 2.5), eight of them 24 us in 32
-// bits; 10 x 3000 on eight CTAs 58 us, 128 x 2000 87 us (by separate products:
+// bits; 10 x 3000 on eight CTAs 59 us, 128 x 2000 88 us (by separate products:
 // 117).
 //
 // The diagonals D_A of A and D_P of P stay in 32 bits and out of the operands:
 // with O = A - D_A, A^2 = O^2 + D_A O + O D_A + D_A^2, and X' = D_P X + (P - D_P) X.
 // What the tensor cores truncate and the operands round is then relative to the
 // rest: 35 x 1330 in 32 bits 4.9e-6 -> 0.7e-6 from the exact result, 64 x 64
-// 1.9e-6 -> 0.5e-6 (32-bit library products: 1.8e-6 and 1.2e-6), for 22 -> 24 us.
+// 1.9e-6 -> 0.5e-6 (32-bit library products: 1.8e-6 and 1.2e-6), for 2 of 24 us.
 //
 // Panels hold rn rows, a panel's lo part behind its hi part: as a K-major right
 // operand the two are one of 2 rn rows, and the product of a hi panel with
@@ -1516,7 +1516,7 @@ Plan plan_of(int64_t batch, int64_t m, int64_t n, int dtype) {
     p.norm_blocks = (int)(chunks < kNormBlocks ? chunks : kNormBlocks);
     // pairs in 16 bits too where there are too few elements for the roundings of single halves to
     // average out (5 x 6: the result up to 2.4 times as far off as its own rounding; with pairs 1.0;
-    // 16 x 16: 14.7 us instead of 13)
+    // 16 x 16: 1.7 us more)
     p.parts = dtype == kF32 || (p.r <= 32 && p.c <= 256) ? 2 : 1;
     // on chip: shares of about 256 columns, more where memory or the SMs ask for it
     p.ctas = 0;
@@ -1575,10 +1575,11 @@ cudaError_t symmetric(const Product& q, LearnState* st, int n_sms, cudaStream_t 
     if (fits(2)) return product<kSplit, kBlock, true, 2>(q, st, n_sms, s);
     if constexpr (!kSplit) {
         // An MMA of N = 256 takes little longer than one of 128: tiles twice as wide, shared by
-        // two CTAs, take two thirds of the time (2048 rows: 72 tiles instead of 136).
+        // two CTAs, take two thirds of the time (2048 rows: 72 tiles instead of 136).  A cluster
+        // takes one tile, so that this is for calls of up to 76 of them (one matrix of 1281 to
+        // 2048 rows, two of 1025 to 1280); larger ones have tiles of 128 x 128 again.
         const int64_t half = (q.tiles_m + 1) / 2, wide = half * (half + 1) * q.batch;
-        if (q.tiles_m % 2 == 0 && q.k_panels >= 2 &&
-            ceil_div(wide * 2, n_sms) * 13 <= ceil_div(total, n_sms) * 20 && wide * 2 <= n_sms) {
+        if (q.tiles_m % 2 == 0 && q.k_panels >= 2 && wide * 2 <= n_sms) {
             Product w = q;
             w.tiles = (int)(half * (half + 1));
             return product<kSplit, 256, true, 2>(w, st, n_sms, s);
