@@ -325,9 +325,10 @@ __device__ __forceinline__ float grad_h(float x, float dy, float mean, float rst
 }
 
 // ----------------------------------------------------------- two launches --
+// (y may be x, dx may be dy or x: they are not restrict)
 template <typename T, int V, int kAct>
-__device__ __forceinline__ void run_apply(const T* __restrict__ x, T* __restrict__ y, int64_t off,
-                                          int64_t len, const Shape& sh, const float2* stats,
+__device__ __forceinline__ void run_apply(const T* x, T* y, int64_t off, int64_t len,
+                                          const Shape& sh, const float2* stats,
                                           const float* __restrict__ weight,
                                           const float* __restrict__ bias) {
     const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
@@ -387,9 +388,9 @@ k_norm_stats(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t 
 // image coming from DRAM again, 34 us for 100 MB in 16 bits.
 template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
-k_norm_apply(const T* __restrict__ x, const __grid_constant__ Shape sh, int64_t image0,
+k_norm_apply(const T* x, const __grid_constant__ Shape sh, int64_t image0,
              const float2* __restrict__ part, const float* __restrict__ weight,
-             const float* __restrict__ bias, float eps, T* __restrict__ y,
+             const float* __restrict__ bias, float eps, T* y,
              float2* __restrict__ stats) {
     pdl_begin();
     extern __shared__ float smem[];
@@ -464,9 +465,8 @@ k_norm_back_sums(const T* __restrict__ x, const T* __restrict__ dy, const __grid
 }
 
 template <typename T, int V, int kAct>
-__device__ __forceinline__ void run_back(const T* __restrict__ x, const T* __restrict__ dy,
-                                         T* __restrict__ dx, int64_t off, int64_t len,
-                                         const Shape& sh, const float2* __restrict__ stats,
+__device__ __forceinline__ void run_back(const T* x, const T* dy, T* dx, int64_t off,
+                                         int64_t len, const Shape& sh, const float2* __restrict__ stats,
                                          const float2* means, const float* __restrict__ weight,
                                          const float* __restrict__ bias) {
     const int row = sh.rpb > 1 ? (int)threadIdx.x / sh.cols : 0;
@@ -514,11 +514,10 @@ __device__ __forceinline__ void run_back(const T* __restrict__ x, const T* __res
 // 25 us for the same, 59 MB of 128 coming from DRAM again.
 template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(V))
-k_norm_back_apply(const T* __restrict__ x, const T* __restrict__ dy,
-                  const __grid_constant__ Shape sh, int64_t image0,
+k_norm_back_apply(const T* x, const T* dy, const __grid_constant__ Shape sh, int64_t image0,
                   const float2* __restrict__ stats, const float2* __restrict__ part,
                   const float* __restrict__ weight, const float* __restrict__ bias,
-                  T* __restrict__ dx, const float2* __restrict__ total, int images,
+                  T* dx, const float2* __restrict__ total, int images,
                   float2* __restrict__ image_total, float* __restrict__ grad_weight,
                   float* __restrict__ grad_bias) {
     pdl_begin();
@@ -613,9 +612,9 @@ __device__ __forceinline__ float2 of_block(const float2* p, int rank) {
 
 template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(kThreads)
-k_norm_small(const T* __restrict__ x, const __grid_constant__ Shape sh,
+k_norm_small(const T* x, const __grid_constant__ Shape sh,
              const float* __restrict__ weight, const float* __restrict__ bias, float eps,
-             T* __restrict__ y, float2* __restrict__ stats) {
+             T* y, float2* __restrict__ stats) {
     using P = Pack<T, V>;
     pdl_begin();
     extern __shared__ float smem[];
@@ -692,10 +691,10 @@ k_norm_small(const T* __restrict__ x, const __grid_constant__ Shape sh,
 // total[image][channel]; where there is one image, its gradients themselves.
 template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(kThreads)
-k_norm_small_back(const T* __restrict__ x, const T* __restrict__ dy,
+k_norm_small_back(const T* x, const T* dy,
                   const __grid_constant__ Shape sh, const float2* __restrict__ stats,
                   const float* __restrict__ weight, const float* __restrict__ bias,
-                  T* __restrict__ dx, float* __restrict__ grad_weight,
+                  T* dx, float* __restrict__ grad_weight,
                   float* __restrict__ grad_bias, float2* __restrict__ total) {
     using P = Pack<T, V>;
     pdl_begin();

@@ -346,11 +346,11 @@ k_orth_start(const T* __restrict__ g, int64_t r, int64_t c, int64_t rp, int64_t 
     }
 }
 
-// No step at all: out = g / (|g| + eps).
+// No step at all: out = g / (|g| + eps).  (`out` may be g.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-k_orth_scale(const T* __restrict__ g, int64_t elems, const Squares* __restrict__ part, int parts,
-             float eps, T* __restrict__ out) {
+k_orth_scale(const T* g, int64_t elems, const Squares* __restrict__ part, int parts, float eps,
+             T* out) {
     pdl_begin();
     const Inverse by = inv_norm(part + (size_t)blockIdx.y * parts, parts, eps);
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < elems;
@@ -1081,7 +1081,7 @@ __device__ __noinline__ void scale_x_step(const Polynomial& p, int step, int ste
 // kWild: poly.wild.
 template <typename T, bool kSplit, int V, bool kWild>
 __global__ void __launch_bounds__(kSmallThreads, 1)
-k_orth_small(const T* __restrict__ grad, const __grid_constant__ Small q, T* out, LearnState* st) {
+k_orth_small(const T* grad, const __grid_constant__ Small q, T* out, LearnState* st) {
     constexpr int kParts = kSplit ? 2 : 1;
     extern __shared__ unsigned char raw[];
     __shared__ Squares s_norm;
