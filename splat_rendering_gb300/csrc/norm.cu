@@ -398,7 +398,8 @@ k_norm_apply(const T* x, const __grid_constant__ Shape sh, int64_t image0,
     const int64_t image = image0 + blockIdx.y;
     const Place p = place(sh, image);
     const float2* mine = part + (size_t)blockIdx.y * sh.blocks * sh.groups;
-    join_stats<kMostBlocks>([&](int b, int g) { return mine[(size_t)b * sh.groups + g]; }, sh, eps, s_stats);
+    join_stats<kMostBlocks>([&](int b, int g) { return mine[(size_t)b * sh.groups + g]; }, sh, eps,
+                            s_stats);
     if (blockIdx.x == 0)
         for (int g = threadIdx.x; g < sh.groups; g += kThreads)
             stats[(size_t)image * sh.groups + g] = s_stats[g];

@@ -106,8 +106,10 @@ __host__ __device__ __forceinline__ float times_pow2(float v, int e) {   // (|e|
     return v * pow2(e >> 1) * pow2(e - (e >> 1));
 }
 // log2 of the scales for the bounds of X, of X in A = X X^T, and of P
-__host__ __device__ __forceinline__ int scale_x(float m) { return 14 - above(m, -100, kMostX + 1); }
-__host__ __device__ __forceinline__ int scale_a(float m) { return 13 - above(m * m, -126, 2 * kMostX + 2); }
+__host__ __device__ __forceinline__ int scale_x(float m) { return 14 - above(m, -112, kMostX + 1); }
+__host__ __device__ __forceinline__ int scale_a(float m) {
+    return 13 - above(m * m, -126, 2 * kMostX + 2);
+}
 __host__ __device__ __forceinline__ int scale_p(float q) { return 13 - above(q, -60, kMostP + 1); }
 
 // A trace's part in whole numbers of 2^-10 stored units, rounded up: their sum has no order (and
@@ -126,18 +128,22 @@ struct Factors {
 };
 __host__ __device__ __forceinline__ Factors factors_p(const Polynomial& p, float m, float u) {
     const int sa = scale_a(m), sp = scale_p(p.most_q(u));
-    return {times_pow2(p.c, sp - 2 * sa < -250 ? -250 : sp - 2 * sa), times_pow2(p.b, sp - sa), times_pow2(p.a, sp)};
+    const int sc = sp - 2 * sa;
+    return {times_pow2(p.c, sc < -250 ? -250 : sc), times_pow2(p.b, sp - sa), times_pow2(p.a, sp)};
 }
 // X's next bound.  (sqrt(u) loses a bound below 2^-63, whose steps are all a X)
 __host__ __device__ __forceinline__ float next_bound(const Polynomial& p, float m, float u) {
     return m > 0x1p-30f ? p.most_s(u) : fmaxf(p.most_s(u), m * fabsf(p.a));
 }
 // The factor of X' = x (P X), whose bound is `next`; the last X' is the result itself.
-__host__ __device__ __forceinline__ float factor_x(const Polynomial& p, float m, float u, float next, bool last) {
+__host__ __device__ __forceinline__ float factor_x(const Polynomial& p, float m, float u, float next,
+                                                   bool last) {
     return times_pow2(1.0f, (last ? 0 : scale_x(next)) - scale_p(p.most_q(u)) - scale_x(m));
 }
 // The factor of A = X X^T
-__host__ __device__ __forceinline__ float factor_a(float m) { return pow2(scale_a(m) - 2 * scale_x(m)); }
+__host__ __device__ __forceinline__ float factor_a(float m) {
+    return pow2(scale_a(m) - 2 * scale_x(m));
+}
 
 // Element (row, col) of a matrix of `rows` padded rows, in halves.
 __host__ __device__ __forceinline__ size_t panel_at(int64_t row, int64_t col, int64_t rows) {
@@ -266,12 +272,14 @@ struct Inverse {
     float pre, inv, norm;   // norm: |X_0|_F, or 1 where that is zero or no number
 };
 __device__ __forceinline__ Inverse norm_inverse(const Squares& s, float eps) {
-    // (beside an eps of 1 a norm below 2^-40 is nothing; times 2^80 it could leave the range)
-    const bool down = isinf(s.plain), up = s.plain < kDown && eps < 1.0f;
-    const float pre = down ? kDown : up ? kUp : 1.0f;
-    const float norm = sqrtf(down ? s.down : up ? s.up : s.plain), sum = norm + eps * pre;
+    const bool down = isinf(s.plain), up = s.plain < kDown;
+    // (an eps that would leave the range times 2^80 is all there is beside a norm below 2^-40)
+    const float pre = down ? kDown : up && eps < 0x1p40f ? kUp : 1.0f;
+    const float unit = up && pre == 1.0f ? kDown : 1.0f;
+    const float norm = sqrtf(down ? s.down : up ? s.up : s.plain), sum = norm * unit + eps * pre;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;   // (zero stays zero without an eps)
-    return {pre, inv, norm * inv > 0.0f ? norm * inv : 1.0f};
+    const float bound = norm * inv * unit;
+    return {pre, inv, bound > 0.0f ? bound : 1.0f};
 }
 
 // The same from a matrix's parts (every thread of the block calls).
@@ -407,8 +415,8 @@ struct Product {
     int tiles;                // per matrix
     int batch;
     Polynomial poly;
-    float* bound;             // X's, of this step and (written with X') the next: [batch][kMaxSteps]
-    unsigned long long* trace;   // A's, of this step (written with A): [batch][kMaxSteps]
+    float* bound;             // [batch][kMaxSteps] X's, of this step and (from X') the next
+    unsigned long long* trace;   // [batch][kMaxSteps] A's, of this step (from A)
     bool last;
     // A, P (where there is a C, which is A) or X', C and D in panels
     const __half* c;
@@ -610,8 +618,8 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
     const int row = quarter * 32 + lane;
     // columns col .. col + kCols - 1 of the tile from their finished sums
     using CHalves = uint4[kCols / 8][kParts];
-    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float alpha, float beta, float gamma,
-                      float rest, float (&v)[kCols]) {
+    auto finish = [&](int z, int i, int j, int col, const CHalves& c, float alpha, float beta,
+                      float gamma, float rest, float (&v)[kCols]) {
         const int64_t grow = (int64_t)i * kBlock + row, gcol = (int64_t)j * kN + col;
         const int jb = j * (kN / kBlock) + col / kBlock;   // the columns' block of 128
         if (kGram && jb > i) return;   // above the diagonal: the mirrored block's
@@ -667,7 +675,7 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
         if (kGram && !kSplit && on >= 0 && on < kCols)
             (q.c ? q.rows : q.rest)[z * q.d_rows + grow] =
                 q.c ? row_factor(exact, rounded) : exact - rounded;
-        if (kGram && !q.c && q.poly.wild && i == jb) {   // (`exact` is zero where the diagonal is not here)
+        if (kGram && !q.c && q.poly.wild && i == jb) {   // (`exact` is zero off the diagonal)
             const uint32_t t = __reduce_add_sync(0xffffffffu, trace_units(exact));
             if (lane == 0 && t) atomicAdd(q.trace + (size_t)z * kMaxSteps, (unsigned long long)t);
         }
@@ -939,7 +947,8 @@ k_orth_product(const __grid_constant__ Product q, LearnState* st) {
                     float w[kCols];
 #pragma unroll
                     for (int e = 0; e < kCols; ++e) w[e] = v[e % kPanel];
-                    finish(z, i, j, col, c[0], alpha, beta, gamma, rest, w);   // (one panel where there is a C)
+                    // (one panel where there is a C)
+                    finish(z, i, j, col, c[0], alpha, beta, gamma, rest, w);
                 } else {   // the result
                     store_result(z, i, j, col, alpha, v);
                 }

@@ -7,8 +7,8 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-CASES = [(2, 200, 20, 4, torch.float32), (1, 30_000, 16, 4, torch.float32), (1, 30_000, 3, 1, torch.bfloat16),
-         (3, 400_000, 16, 4, torch.float32), (5, 300_001, 64, 8, torch.bfloat16)]
+CASES = [(2, 200, 20, 4, torch.float32), (1, 30_000, 16, 4, torch.float32),
+         (1, 30_000, 3, 1, torch.bfloat16), (3, 400_000, 16, 4, torch.float32), (5, 300_001, 64, 8, torch.bfloat16)]
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:4])))

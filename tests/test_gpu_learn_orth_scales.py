@@ -86,3 +86,17 @@ def test_many_steps_end_at_the_polar_factor(ops, steps, scale):
         want = u @ vh   # (the polar factor; the rounding of g to 32 bits moves it by 2^-24 / 0.2)
         err = (got - want).flatten(-2).norm(dim=-1)
         assert (err <= 8 * 2.0 ** -20 * want.flatten(-2).norm(dim=-1)).all(), (shape, err)
+
+
+@pytest.mark.parametrize("eps", [1.0, 3e4, 1e13, 1e20])
+def test_a_large_eps(ops, eps):
+    """X_0 is G / eps whatever the norm, whose square is below float32's range."""
+    for shape in SHAPES:
+        for scale in (1e-3, 1e-13, 1e-17):
+            g = torch.randn(*shape, generator=torch.Generator().manual_seed(6)) * scale
+            got = ops.orthogonalize(g.cuda(), eps=eps).cpu().double()
+            want, bound = ref.orthogonalize(g, 5, COEFFS, _f32(eps))
+            err = (got - want).flatten(-2).norm(dim=-1)
+            # (below 2^-126 a result has the spacing of float32's subnormals)
+            floor = 2.0 ** -150 * (shape[-1] * shape[-2]) ** 0.5
+            assert (err <= bound + floor).all(), (shape, scale, float((err / bound).max()))
