@@ -61,8 +61,7 @@ __device__ __forceinline__ int rows_of(int64_t len, int row, int rpb) {
 // ------------------------------------------------------------- activation --
 // The fast exponential and division: with the exact ones the gradients of a 1024 x 1024 x 16 image
 // take 60 us instead of 53, and are no nearer (dx 7.1e-8 of its norm off either way, plain 32-bit
-// operations 7.6e-8; dw and db by their sums' roundings, 1.4e-7 and 2.3e-7 instead of 1.7e-7 and
-// 2.5e-7, plain 1.9e-7 and 2.3e-7).
+// operations 7.6e-8; dw and db are as far off as their sums' roundings).
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
     if (kAct == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
