@@ -317,8 +317,9 @@ int pulsar_render_noalloc(const float* pos, const float* radius, const float* op
 /* ------------------------------------------------------- learned parts --
  * What a model trained through the renderer needs next to it: a codebook from
  * which spheres (or any tokens) read their features, with its gradient; the
- * normalisation and activation of a feature image, with its gradients; and
- * the orthogonalisation of a matrix's update.  No camera or frame is
+ * normalisation and activation of a feature image, with its gradients; linear
+ * layers with theirs, and dropout, for the networks that read feature images
+ * (or tokens); and the orthogonalisation of a matrix's update.  No camera or frame is
  * involved: the calls work on a handle that owns one block of workspace.
  *
  * Conventions as above: caller-owned, C-contiguous device tensors, calls
@@ -355,11 +356,12 @@ int pulsar_learn_destroy(pulsar_learn_t h);
  * result is invalid and the handle should be destroyed). */
 int pulsar_learn_status(pulsar_learn_t h, void* stream);
 
-/* Bytes of workspace a call of these sizes needs (the forward embedding needs
- * none), or PULSAR_ERR_ARG. */
+/* Bytes of workspace a call of these sizes needs (the forward embedding and
+ * dropout need none), or PULSAR_ERR_ARG. */
 int64_t pulsar_embed_workspace(int64_t n, int64_t rows, int64_t dim);
 int64_t pulsar_group_norm_workspace(int64_t images, int64_t pixels, int32_t channels,
                                     int32_t groups);
+int64_t pulsar_linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype);
 int64_t pulsar_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n, int dtype);
 
 /* Codebook embedding: out_i = scale * table[tokens_i], a row of zeros where
@@ -428,6 +430,57 @@ int pulsar_group_norm_backward(pulsar_learn_t h, const void* grad_y, const void*
 int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int64_t m, int64_t n,
                          int steps, const float* coeffs, float eps, int dtype, void* out,
                          void* stream);
+
+/* A linear layer, its bias, activation and residual in one call:
+ *   z = x W^T + bias,   y = act(z) + residual.
+ *   x        [rows,inputs] dtype     weight [outputs,inputs] dtype
+ *   bias     [outputs] float32; NULL: zeros
+ *   residual [rows,outputs] dtype; NULL: none
+ *   y        [rows,outputs] dtype, overwritten; may be residual
+ *   pre      [rows,outputs] dtype, overwritten with z for the backward call;
+ *            NULL: not wanted.  pre and y may not be x or weight.
+ * 0 <= rows <= 0x7fff0000, 1 <= inputs, outputs <= 65536, and rows * inputs
+ * and rows * outputs at most 2^38.
+ * Products are exact and sums have 32 bits: in bfloat16 a result is rounded
+ * once, in float32 it is about as near as that of 32-bit products (operands
+ * beyond bfloat16's largest value, 3.39e38, count as infinite).  A row of x,
+ * or of the weight, with an infinity or a NaN gives infinities or NaNs in its
+ * row, or column, of z, and nowhere else. */
+int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, int64_t rows,
+                          int64_t inputs, int64_t outputs, const float* bias,
+                          const void* residual, int act, int dtype, void* y, void* pre,
+                          void* stream);
+
+/* Its gradients for dL/dy = grad_y (which is the residual's gradient as it
+ * is), with x, weight and pre of the forward call:
+ *   dz = grad_y act'(pre),   grad_x = dz W,   grad_weight = dz^T x,
+ *   grad_bias = the sum of dz's rows.
+ *   pre    may be NULL where act is PULSAR_ACT_NONE
+ *   grad_x [rows,inputs] dtype; grad_weight [outputs,inputs] dtype; grad_bias
+ *          [outputs] float32; each overwritten, each may be NULL (not
+ *          requested), none may be an input.
+ * In bfloat16 dz is rounded to 16 bits as an operand of the products (not for
+ * the bias), which leaves grad_x and grad_weight at most sqrt(2) times as far
+ * off as their own rounding; without an activation it is grad_y, exactly. */
+int pulsar_linear_backward(pulsar_learn_t h, const void* grad_y, const void* x,
+                           const void* weight, const void* pre, int64_t rows, int64_t inputs,
+                           int64_t outputs, int act, int dtype, void* grad_x, void* grad_weight,
+                           float* grad_bias, void* stream);
+
+/* Dropout with a mask that is never stored:
+ *   out_i = [w_i >= p 2^32] x_i / (1 - p) + residual_i,
+ * w_i word i mod 4 of Philox4x32 with seven rounds, its key `seed`, its
+ * counter offset + *counter + i / 4 (the upper 64 bits of the 128 zero).  The
+ * gradient of x is the same call on dL/dout without a residual.
+ *   x, residual, out [n] dtype; residual NULL: none; out may be either
+ *   offset   the first of ceil(n / 4) counters that the call uses, >= 0
+ *   counter  a device int64 that is added to it when the call runs (a call in
+ *            a CUDA graph draws new numbers where a replay counts it up);
+ *            NULL: nothing
+ * 0 <= n <= 2^38, 0 <= p < 1 - 2^-33 (p is rounded to a multiple of 2^-32). */
+int pulsar_dropout(pulsar_learn_t h, const void* x, const void* residual, int64_t n, double p,
+                   uint64_t seed, int64_t offset, const int64_t* counter, int dtype, void* out,
+                   void* stream);
 
 #ifdef __cplusplus
 }

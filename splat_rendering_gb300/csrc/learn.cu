@@ -1,8 +1,9 @@
 // C ABI of the learned parts around the renderer: a handle with one block of
-// workspace and a latched device error, and the embedding, group-norm and
-// orthogonalisation calls on it.  As with the renderer's calls, arguments are
+// workspace and a latched device error, and the embedding, group-norm, linear,
+// dropout and orthogonalisation calls on it.  As with the renderer's calls, arguments are
 // checked on the host before anything is enqueued, and nothing synchronises
 // but pulsar_learn_status.
+#include <cmath>
 #include <new>
 
 #include "../../include/pulsar.h"
@@ -25,6 +26,7 @@ constexpr int64_t kMaxIndex = 0x7fff0000LL;   // positions and rows are 32-bit o
 constexpr int kMaxSms = 160;                  // of an sm_103a part (launches size workspace by it)
 constexpr int64_t kMaxDim = 65536;
 constexpr int64_t kMaxSide = 65536;           // of a matrix
+constexpr int64_t kMaxElements = 1LL << 38;   // of a matrix of rows: strides of its maps, tiles
 constexpr int64_t kMaxBatch = 65535;          // a launch's grid
 
 bool valid_type(int t) { return t == PULSAR_F32 || t == PULSAR_BF16; }
@@ -44,6 +46,11 @@ bool norm_sizes(int64_t images, int64_t pixels, int32_t channels, int32_t groups
 bool orth_sizes(int64_t batch, int64_t m, int64_t n) {
     return batch >= 0 && batch <= kMaxBatch && m >= 0 && m <= kMaxSide && n >= 0 && n <= kMaxSide;
 }
+bool linear_sizes(int64_t rows, int64_t inputs, int64_t outputs) {
+    return rows >= 0 && rows <= kMaxIndex && inputs >= 1 && inputs <= kMaxSide && outputs >= 1 &&
+           outputs <= kMaxSide && rows * inputs <= kMaxElements && rows * outputs <= kMaxElements;
+}
+bool valid_act(int a) { return a == PULSAR_ACT_NONE || a == PULSAR_ACT_SILU || a == PULSAR_ACT_RELU; }
 bool embed_args(const void* src, const void* tokens, int64_t n, float scale, int dtype, int index,
                 const void* dst) {
     if (!valid_type(dtype) || (index != PULSAR_I32 && index != PULSAR_I64) || !finite(scale))
@@ -81,7 +88,7 @@ int pulsar_learn_create(pulsar_learn_t* out, int device, int64_t workspace_bytes
                  cudaSuccess &&
              h->n_sms <= kMaxSms && prepare_orth() == cudaSuccess &&
              prepare_group_norm() == cudaSuccess && prepare_embed() == cudaSuccess &&
-             cudaMemset(h->state, 0, sizeof(LearnState)) == cudaSuccess &&
+             prepare_linear() == cudaSuccess && cudaMemset(h->state, 0, sizeof(LearnState)) == cudaSuccess &&
              cudaDeviceSynchronize() == cudaSuccess;
     if (!ok) {
         cudaFree(h->ws);
@@ -225,6 +232,71 @@ int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int6
     DeviceGuard guard(h->device);
     const OrthCall c{grad, batch, m, n, steps, coeffs[0], coeffs[1], coeffs[2], eps, dtype, out};
     return cuda_err(launch_orth(c, h->state, h->ws, h->n_sms, as_stream(stream)));
+}
+
+// ------------------------------------------------------------ linear layer --
+int64_t pulsar_linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
+    if (!linear_sizes(rows, inputs, outputs) || !valid_type(dtype)) return PULSAR_ERR_ARG;
+    return (int64_t)linear_workspace(rows, inputs, outputs, dtype);
+}
+
+static bool linear_args(const LinearCall& c) {
+    if (!linear_sizes(c.rows, c.inputs, c.outputs) || !valid_type(c.dtype) || !valid_act(c.act))
+        return false;
+    for (const void* p : {c.x, c.weight, (const void*)c.pre, (const void*)c.out, c.residual,
+                          c.grad_y, (const void*)c.grad_x, (const void*)c.grad_weight})
+        if (!aligned_to(p, c.dtype)) return false;
+    return aligned4(c.bias) && aligned4(c.grad_bias);
+}
+
+int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, int64_t rows,
+                          int64_t inputs, int64_t outputs, const float* bias,
+                          const void* residual, int act, int dtype, void* y, void* pre,
+                          void* stream) {
+    PULSAR_TRACE("pulsar_linear_forward");
+    const LinearCall c{x, weight, rows, inputs, outputs, act, dtype, pre, y, bias, residual,
+                       nullptr, nullptr, nullptr, nullptr};
+    if (!h || !linear_args(c) || (rows > 0 && (!x || !weight || !y))) return PULSAR_ERR_ARG;
+    if ((int64_t)linear_workspace(rows, inputs, outputs, dtype) > h->bytes)
+        return PULSAR_ERR_WORKSPACE;
+    DeviceGuard guard(h->device);
+    return cuda_err(launch_linear_forward(c, h->state, h->ws, h->n_sms, as_stream(stream)));
+}
+
+int pulsar_linear_backward(pulsar_learn_t h, const void* grad_y, const void* x,
+                           const void* weight, const void* pre, int64_t rows, int64_t inputs,
+                           int64_t outputs, int act, int dtype, void* grad_x, void* grad_weight,
+                           float* grad_bias, void* stream) {
+    PULSAR_TRACE("pulsar_linear_backward");
+    const LinearCall c{x, weight, rows, inputs, outputs, act, dtype, const_cast<void*>(pre),
+                       nullptr, nullptr, nullptr, grad_y, grad_x, grad_weight, grad_bias};
+    if (!h || !linear_args(c)) return PULSAR_ERR_ARG;
+    if (!grad_x && !grad_weight && !grad_bias) return PULSAR_OK;   // nothing requested
+    if (rows > 0 && (!grad_y || (act != PULSAR_ACT_NONE && !pre) || (grad_x && !weight) ||
+                     (grad_weight && !x)))
+        return PULSAR_ERR_ARG;
+    if ((int64_t)linear_workspace(rows, inputs, outputs, dtype) > h->bytes)
+        return PULSAR_ERR_WORKSPACE;
+    DeviceGuard guard(h->device);
+    return cuda_err(launch_linear_backward(c, h->state, h->ws, h->n_sms, as_stream(stream)));
+}
+
+// ---------------------------------------------------------------- dropout --
+int pulsar_dropout(pulsar_learn_t h, const void* x, const void* residual, int64_t n, double p,
+                   uint64_t seed, int64_t offset, const int64_t* counter, int dtype, void* out,
+                   void* stream) {
+    PULSAR_TRACE("pulsar_dropout");
+    if (!h || n < 0 || n > kMaxElements || !valid_type(dtype) || !(p >= 0.0 && p < 1.0) ||
+        offset < 0 || !aligned_to(x, dtype) || !aligned_to(residual, dtype) ||
+        !aligned_to(out, dtype) || (reinterpret_cast<uintptr_t>(counter) & 7u) != 0 ||
+        (n > 0 && (!x || !out)))
+        return PULSAR_ERR_ARG;
+    const double least = std::nearbyint(p * 4294967296.0);
+    if (least > 4294967295.0) return PULSAR_ERR_ARG;   // nothing would be kept
+    DeviceGuard guard(h->device);
+    const DropoutCall c{x, residual, n, seed, offset, counter, (uint32_t)least,
+                        (float)(1.0 / (1.0 - p)), dtype, out};
+    return cuda_err(launch_dropout(c, h->n_sms, as_stream(stream)));
 }
 
 }  // extern "C"

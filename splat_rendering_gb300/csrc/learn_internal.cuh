@@ -1,6 +1,6 @@
 // Internal definitions shared by the kernels of the learned parts around the
-// renderer: the codebook embedding, the group normalisation of feature images
-// and the orthogonalisation of an update.  Their entry points work on a
+// renderer: the codebook embedding, the group normalisation of feature images,
+// linear layers, dropout and the orthogonalisation of an update.  Their entry points work on a
 // handle that owns one block of device workspace and a latched error word;
 // every launcher below carves what it needs out of that block.
 #pragma once
@@ -196,5 +196,40 @@ size_t orth_workspace(int64_t batch, int64_t m, int64_t n, int dtype);
 cudaError_t prepare_orth();
 cudaError_t launch_orth(const OrthCall& c, LearnState* st, void* ws, int n_sms,
                         cudaStream_t stream);
+
+struct LinearCall {
+    const void* x;            // [rows, inputs]
+    const void* weight;       // [outputs, inputs]
+    int64_t rows, inputs, outputs;
+    int act, dtype;
+    void* pre;                // z: written by the forward where given, read by the backward
+    void* out;                // y (forward)
+    const float* bias;        // forward; may be NULL: zeros
+    const void* residual;     // forward; may be NULL
+    const void* grad_y;       // backward
+    void* grad_x;             // may be NULL, as the other gradients
+    void* grad_weight;
+    float* grad_bias;
+};
+size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype);
+cudaError_t prepare_linear();
+cudaError_t launch_linear_forward(const LinearCall& c, LearnState* st, void* ws, int n_sms,
+                                  cudaStream_t stream);
+cudaError_t launch_linear_backward(const LinearCall& c, LearnState* st, void* ws, int n_sms,
+                                   cudaStream_t stream);
+
+struct DropoutCall {
+    const void* x;
+    const void* residual;     // may be NULL
+    int64_t n;
+    uint64_t seed;
+    int64_t offset;
+    const int64_t* counter;   // device; may be NULL
+    uint32_t least;           // the smallest word that keeps an element
+    float scale;
+    int dtype;
+    void* out;
+};
+cudaError_t launch_dropout(const DropoutCall& c, int n_sms, cudaStream_t stream);
 
 }  // namespace pulsar

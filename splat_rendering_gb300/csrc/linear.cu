@@ -1,0 +1,944 @@
+// A linear layer with its bias, activation and residual, and its gradients:
+//
+//   z = x W^T + b,   y = act(z) + residual            x [m, k], W [n, k]
+//   dz = dy act'(z),   dx = dz W,   dW = dz^T x,   db = sum of dz's rows
+//
+// The three products run on the tensor cores (tcgen05, fp32 accumulation).  A
+// product is D(i, j) = sum over c of A(i, c) B(j, c); an operand's matrix in
+// memory has either its i (j) or its c as rows: x, W and dz are read as they
+// lie by all three products (K-major or MN-major operands).
+//
+// bfloat16 operands are used as they are.  A float32 value is the sum of three
+// bfloat16 ones, hi + mid + lo (8 + 8 + 8 bits, the whole float32 range up to
+// bfloat16's largest value, and so no scales), and a product is the sum of six
+// of theirs: hi hi, hi mid, mid hi, mid mid, hi lo, lo hi.  The other three are
+// at most 2^-23 of it and, their signs being random, far below the rounding of
+// a sum in 32 bits.
+#include <cuda.h>
+
+#include "learn_internal.cuh"
+#include "tensor_core.cuh"
+
+namespace pulsar {
+namespace {
+
+constexpr int kPanel = 64;       // of the contraction, per stage: 128 bytes of a swizzled row
+constexpr int kBlock = 128;      // rows of a tile
+constexpr int kMaxPlanes = 3;
+
+// ------------------------------------------------------------ activation --
+template <int kAct>
+__device__ __forceinline__ float act_of(float z) {
+    if (kAct == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
+    if (kAct == kActRelu) return z > 0.0f ? z : 0.0f;
+    return z;
+}
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+    if (kAct == kActSilu) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+        return s * (1.0f + z * (1.0f - s));
+    }
+    if (kAct == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+    return 1.0f;
+}
+__device__ __forceinline__ float act_any(int act, float z) {
+    if (act == kActSilu) return act_of<kActSilu>(z);
+    if (act == kActRelu) return act_of<kActRelu>(z);
+    return z;
+}
+
+// ---------------------------------------------------------------- planes --
+// Two floats as three words of two bfloat16 each, whose sums they are (but for an infinity, which
+// leaves nothing over).
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float rest_of(float v, float part) {
+    return fabsf(part) <= 3.3895314e38f ? v - part : 0.0f;
+}
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&w)[3]) {
+    w[0] = pair_bf16(a, b);
+    a = rest_of(a, low_of(w[0]));
+    b = rest_of(b, high_of(w[0]));
+    w[1] = pair_bf16(a, b);
+    w[2] = pair_bf16(a - low_of(w[1]), b - high_of(w[1]));
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+    constexpr int V = VecOf<T>::n;
+    if (vec) {
+#pragma unroll
+        for (int h = 0; h < 8; h += V) {
+            float u[V];
+            Pack<T, V>::load(p + h, u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[h + e] = u[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float u[1] = {0.0f};
+            if (e < n) Pack<T, 1>::load(p + e, u);
+            v[e] = u[0];
+        }
+    }
+}
+
+// A matrix [rows, cols] made into an operand: times the activation's slope at `pre` (the gradient
+// dz from dy), split into planes [planes][rows][pitch] of bfloat16, and its column sums taken, a
+// partial sum [cols] per block of rows.  A thread has eight columns of every (256 / tx)-th row.
+struct Operand {
+    const void* src;
+    const void* pre;        // NULL: no activation
+    int act;
+    int64_t rows, cols;
+    int64_t pitch;          // a multiple of 8
+    __nv_bfloat16* planes;  // NULL: none are wanted
+    size_t plane;           // elements from one plane to the next
+    float* sums;            // NULL: none are wanted
+    int tx;                 // threads along the columns: a power of two up to 32
+    int64_t block_rows;
+    bool vec;
+};
+
+template <typename T, int kPlanes, int kAct>
+__global__ void __launch_bounds__(256)
+k_linear_operand(const Operand q) {
+    __shared__ float s_sums[256 * 8];
+    pdl_next();
+    pdl_begin();
+    const int tx = threadIdx.x & (q.tx - 1), ty = threadIdx.x / q.tx, step = 256 / q.tx;
+    const int64_t c = ((int64_t)blockIdx.y * q.tx + tx) * 8;
+    const int n = (int)(q.cols - c < 8 ? q.cols - c : 8);
+    const int64_t r0 = blockIdx.x * q.block_rows;
+    const int64_t r1 = r0 + q.block_rows < q.rows ? r0 + q.block_rows : q.rows;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    if (c < q.cols) {
+        const bool vec = q.vec && n == 8;
+#pragma unroll 4
+        for (int64_t r = r0 + ty; r < r1; r += step) {
+            float v[8];
+            load8(static_cast<const T*>(q.src) + r * q.cols + c, n, vec, v);
+            if (kAct != kActNone) {
+                float z[8];
+                load8(static_cast<const T*>(q.pre) + r * q.cols + c, n, vec, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = kAct == kActRelu ? (z[e] > 0.0f ? v[e] : 0.0f)
+                                            : v[e] * act_slope<kAct>(z[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += e < n ? v[e] : 0.0f;
+            if (q.planes) {
+                uint32_t w[4][3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (kPlanes == 3)
+                        split3(v[2 * e], v[2 * e + 1], w[e]);
+                    else
+                        w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
+                }
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p)
+                    *reinterpret_cast<uint4*>(q.planes + p * q.plane + r * q.pitch + c) =
+                        make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+            }
+        }
+    }
+    if (!q.sums) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_sums[(ty * q.tx + tx) * 8 + e] = sum[e];
+    __syncthreads();
+    for (int half = step / 2; half > 0; half /= 2) {   // [step][8 tx] by halves
+        for (int i = threadIdx.x; i < half * q.tx * 8; i += 256)
+            s_sums[i] += s_sums[i + half * q.tx * 8];
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < q.tx * 8; i += 256) {
+        const int64_t col = (int64_t)blockIdx.y * q.tx * 8 + i;
+        if (col < q.cols) q.sums[(int64_t)blockIdx.x * q.cols + col] = s_sums[i];
+    }
+}
+
+// The sums of `blocks` partial rows of `cols`: 32 columns a block, 32 rows of threads.
+__global__ void __launch_bounds__(1024)
+k_linear_sums(const float* __restrict__ part, int64_t blocks, int64_t cols,
+              float* __restrict__ out) {
+    __shared__ float s[32][33];
+    pdl_begin();
+    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float v = 0.0f;
+    if (col < cols)
+        for (int64_t b = threadIdx.y; b < blocks; b += 32) v += part[b * cols + col];
+    s[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    v = s[threadIdx.x][threadIdx.y];   // a warp per column
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    const int64_t mine = (int64_t)blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && mine < cols) out[mine] = v;
+}
+
+// -------------------------------------------------------------- products --
+// One kernel for the three products, a persistent CTA per SM.  Roles: one
+// thread keeps a ring of operand stages filled by TMA (out of range: zeros), one
+// issues the MMAs into one of two accumulators in tensor memory, and eight
+// warps finish the other (four per half of the tile's columns, a thread per
+// row): bias, activation, residual, rounding; through a swizzled exchange in
+// shared memory, so that a warp stores whole sectors.
+//
+// In 32 bits the tensor cores' accumulation, which truncates, would be what
+// limits the result (of K = 2048, some 2^-18.5 of it): hi hi and the other
+// five products have accumulators of their own, and both are drained and
+// summed in registers every kChunk panels (128 of K).
+//
+// Where a product has few tiles for the SMs and a long contraction (dW: one
+// tile and a million rows), its parts are separate work items, whose sums
+// k_linear_join adds up in their order.
+struct Product {
+    CUtensorMap a, b;
+    int tiles_m, tiles_n, splits, panels;   // panels of the contraction
+    int64_t m, n;
+    // the finished result, or, where there are parts, their sums [splits][m][n]
+    const float* bias;
+    const void* residual;
+    void* pre;
+    void* out;
+    int act;
+    bool vec;   // four columns at a time
+};
+
+constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epilogue
+constexpr int kChunk = 2;              // panels per drained sum (32 bits)
+constexpr int kGroup = 16;             // row blocks whose tiles lie side by side in time
+
+template <int kPlanes, int kN>
+struct ProductSmem {
+    static constexpr int a = kBlock * kPanel * 2, b = kN * kPanel * 2;
+    static constexpr int stage = kPlanes * (a + b);
+    static constexpr int exchange_bytes = 8 * 32 * 32 * 4;
+    static constexpr int stages = (227 * 1024 - 1024 - exchange_bytes - 256) / stage;
+    static constexpr int exchange = stages * stage;
+    static constexpr int bars = exchange + exchange_bytes;
+    static constexpr int bytes = bars + 256 + 1024;   // and the alignment to 1024
+    static_assert(stages >= 2 && (2 * stages + 5) * 8 + 8 <= 256, "shared memory of a product");
+};
+
+// Descriptor of a 128-byte-swizzled operand: `lbo` is the stride between
+// 64-element groups along M/N of an MN-major operand (unused when K-major);
+// groups of eight rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void expect_bytes(uint64_t* mbar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_init_n(uint64_t* mbar, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(mbar)), "r"(n));
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* mbar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
+}
+// A box of a tensor map [planes][rows][cols] at (plane, row, col): col a multiple of 64.
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int col, int row,
+                                         int plane, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(col), "r"(row), "r"(plane), "r"(smem_u32(mbar))
+        : "memory");
+}
+// Whether any of the epilogue's threads has `v`: one decision for all.
+__device__ __forceinline__ bool epilogue_any(bool v) {
+    uint32_t any;
+    __syncwarp();
+    asm volatile(
+        "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred r, 1, 256, p;\n"
+        "selp.u32 %0, 1, 0, r;\n}\n"
+        : "=r"(any)
+        : "r"((uint32_t)v)
+        : "memory");
+    return any != 0;
+}
+
+// Four columns of a row: bias, pre-activation, activation, residual, and the result.
+template <typename T>
+__device__ __forceinline__ void finish4(const Product& q, float (&z)[4], int64_t at, int n) {
+    const T* residual = static_cast<const T*>(q.residual);
+    T* pre = static_cast<T*>(q.pre);
+    T* out = static_cast<T*>(q.out);
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = act_any(q.act, z[e]);
+    if (q.vec) {
+        if constexpr (sizeof(T) == 4) {
+            if (pre) *reinterpret_cast<float4*>(pre + at) = make_float4(z[0], z[1], z[2], z[3]);
+            if (residual) {
+                const float4 r = *reinterpret_cast<const float4*>(residual + at);
+                y[0] += r.x; y[1] += r.y; y[2] += r.z; y[3] += r.w;
+            }
+            *reinterpret_cast<float4*>(out + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            if (pre)
+                *reinterpret_cast<uint2*>(pre + at) =
+                    make_uint2(pair_bf16(z[0], z[1]), pair_bf16(z[2], z[3]));
+            if (residual) {
+                const uint2 r = *reinterpret_cast<const uint2*>(residual + at);
+                y[0] += low_of(r.x); y[1] += high_of(r.x);
+                y[2] += low_of(r.y); y[3] += high_of(r.y);
+            }
+            *reinterpret_cast<uint2*>(out + at) =
+                make_uint2(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e >= n) continue;
+            float u[1] = {z[e]};
+            if (pre) Pack<T, 1>::store(pre + at + e, u);
+            if (residual) {
+                Pack<T, 1>::load(residual + at + e, u);
+                y[e] += u[0];
+            }
+            u[0] = y[e];
+            Pack<T, 1>::store(out + at + e, u);
+        }
+    }
+}
+
+// T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
+// as its rows.
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
+__global__ void __launch_bounds__(kProductThreads)
+k_linear_product(const __grid_constant__ Product q, LearnState* st) {
+    using L = ProductSmem<kPlanes, kN>;
+    constexpr int kAcc = kPlanes == 3 ? 2 * kN : kN;   // columns of an accumulator
+    constexpr int kHalf = kN / 2;                      // columns of an epilogue thread
+    static_assert(2 * kAcc <= 512, "tensor memory");
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint64_t* empty = full + L::stages;
+    uint64_t* acc_full = empty + L::stages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile uint32_t* s_fail = s_taddr + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < L::stages; ++s) {
+            mbar_init(full + s);
+            mbar_init(empty + s);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s);
+            mbar_init_n(acc_empty + s, 8);
+        }
+        mbar_init(drain);
+        *s_fail = 0u;
+        fence_async_smem();
+    }
+    if (warp == 1) tmem_alloc(s_taddr, 2 * kAcc);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_taddr;
+    pdl_next();
+    pdl_begin();
+    const int tiles = q.tiles_m * q.tiles_n, total = tiles * q.splits;
+    auto place = [&](int t, int* i, int* j, int* k0, int* k1, int* part) {
+        *part = t / tiles;
+        t -= *part * tiles;
+        const int g = t / (kGroup * q.tiles_n), rows = min(kGroup, q.tiles_m - g * kGroup);
+        t -= g * kGroup * q.tiles_n;
+        *i = g * kGroup + t % rows;
+        *j = t / rows;
+        *k0 = (int)((int64_t)*part * q.panels / q.splits);
+        *k1 = (int)((int64_t)(*part + 1) * q.panels / q.splits);
+    };
+    if (warp == 0) {
+        if (lane == 0) {   // ---- copies
+            int n = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                int i, j, k0, k1, part;
+                place(t, &i, &j, &k0, &k1, &part);
+                for (int k = k0; k < k1; ++k, ++n) {
+                    const int s = n % L::stages;
+                    ok = mbar_wait(empty + s, ((n / L::stages) & 1) ^ 1) && !*s_fail;
+                    if (!ok) break;
+                    unsigned char* dst = smem + s * L::stage;
+                    expect_bytes(full + s, L::stage);
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p) {
+                        if (kAMn) {
+#pragma unroll
+                            for (int c = 0; c < kBlock / kPanel; ++c)
+                                tma_load(dst + p * L::a + c * kPanel * kPanel * 2, &q.a,
+                                         i * kBlock + c * kPanel, k * kPanel, p, full + s);
+                        } else {
+                            tma_load(dst + p * L::a, &q.a, k * kPanel, i * kBlock, p, full + s);
+                        }
+                    }
+                    dst += kPlanes * L::a;
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p) {
+                        if (kBMn) {
+#pragma unroll
+                            for (int c = 0; c < kN / kPanel; ++c)
+                                tma_load(dst + p * L::b + c * kPanel * kPanel * 2, &q.b,
+                                         j * kN + c * kPanel, k * kPanel, p, full + s);
+                        } else {
+                            tma_load(dst + p * L::b, &q.b, k * kPanel, j * kN, p, full + s);
+                        }
+                    }
+                }
+            }
+            if (!ok) {   // give the copies in flight one more bounded wait
+                *s_fail = 1u;
+                for (int k = n > L::stages ? n - L::stages : 0; k < n; ++k)
+                    mbar_wait(full + k % L::stages, (k / L::stages) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {   // ---- MMAs
+            constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                                       (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
+                                       ((uint32_t)(kN >> 3) << 17) |
+                                       ((uint32_t)(kBlock >> 4) << 24);
+            const uint32_t base = smem_u32(smem);
+            int n = 0, it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                int i, j, k0, k1, part;
+                place(t, &i, &j, &k0, &k1, &part);
+                const int chunk = kPlanes == 3 ? kChunk : k1 - k0;
+                for (int kc = k0; kc < k1 && ok; kc += chunk, ++it) {
+                    const int buf = it & 1, ke = min(kc + chunk, k1);
+                    const uint32_t d = tmem + buf * kAcc;
+                    ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int k = kc; k < ke; ++k, ++n) {
+                        const int s = n % L::stages;
+                        ok = mbar_wait(full + s, (n / L::stages) & 1) && !*s_fail;
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t at = base + s * L::stage;
+                        uint64_t a[kPlanes], b[kPlanes];
+#pragma unroll
+                        for (int p = 0; p < kPlanes; ++p) {
+                            a[p] = desc_sw128(at + p * L::a, kAMn ? kPanel * kPanel * 2 : 16);
+                            b[p] = desc_sw128(at + kPlanes * L::a + p * L::b,
+                                              kBMn ? kPanel * kPanel * 2 : 16);
+                        }
+#pragma unroll
+                        for (int e = 0; e < kPanel / 16; ++e) {
+                            // 16 of K: 32 bytes along a K-major row, 16 rows of an MN-major operand
+                            const uint32_t ea = (kAMn ? 2048u : 32u) * e >> 4;
+                            const uint32_t eb = (kBMn ? 2048u : 32u) * e >> 4;
+                            const uint32_t more = k > kc || e > 0;
+                            mma_f16(d, a[0] + ea, b[0] + eb, idesc, more);
+                            if constexpr (kPlanes == 3) {
+                                mma_f16(d + kN, a[0] + ea, b[2] + eb, idesc, more);
+                                mma_f16(d + kN, a[1] + ea, b[1] + eb, idesc, 1);
+                                mma_f16(d + kN, a[2] + ea, b[0] + eb, idesc, 1);
+                                mma_f16(d + kN, a[0] + ea, b[1] + eb, idesc, 1);
+                                mma_f16(d + kN, a[1] + ea, b[0] + eb, idesc, 1);
+                            }
+                        }
+                        mma_commit(empty + s);
+                    }
+                    if (ok) mma_commit(acc_full + buf);
+                }
+            }
+            if (!ok) {
+                *s_fail = 1u;
+                mma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+        }
+    } else {   // ---- epilogue
+        const int group = (warp - 2) >> 2, quarter = warp & 3;   // (warps 2 .. 9)
+        float4* x = reinterpret_cast<float4*>(smem + L::exchange) + (warp - 2) * 256;
+        const int cq = lane & 7, rq = lane >> 3;
+        int it = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            int i, j, k0, k1, part;
+            place(t, &i, &j, &k0, &k1, &part);
+            // 32 columns from `col` of the tile, a row in each lane
+            auto emit = [&](const float* v, int col) {
+                const int64_t c = (int64_t)j * kN + col + 4 * cq;
+                const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
+                const int n = (int)(q.n - c < 4 ? q.n - c : 4);
+                float bias[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bias[e] = q.bias && e < n ? q.bias[c + e] : 0.0f;
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[lane * 8 + (e ^ (lane & 7))] =
+                        make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                __syncwarp();
+                if (n <= 0) return;
+                int64_t at = (int64_t)part * q.m * q.n + (r0 + rq) * q.n + c;
+#pragma unroll
+                for (int h = 0; h < 8; ++h, at += 4 * q.n) {
+                    const int r = 4 * h + rq;
+                    if (r0 + r >= q.m) break;
+                    const float4 u = x[r * 8 + (cq ^ (r & 7))];
+                    float z[4] = {u.x + bias[0], u.y + bias[1], u.z + bias[2], u.w + bias[3]};
+                    finish4<T>(q, z, at, n);
+                }
+            };
+            bool ok = true;
+            if constexpr (kPlanes == 3) {
+                float v[kHalf];
+#pragma unroll
+                for (int e = 0; e < kHalf; ++e) v[e] = 0.0f;
+                for (int kc = k0; kc < k1; kc += kChunk, ++it) {
+                    const int buf = it & 1;
+                    ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
+                    ok = !epilogue_any(!ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * kAcc + ((uint32_t)(quarter * 32) << 16) +
+                                         group * kHalf;
+#pragma unroll
+                    for (int h = 0; h < kHalf; h += 16) {
+                        uint32_t u[16], w[16];
+                        tmem_ld16(acc + h, u);
+                        tmem_ld16(acc + kN + h, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[h + e] += __uint_as_float(u[e]) + __uint_as_float(w[e]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                }
+                if (ok) {
+#pragma unroll
+                    for (int h = 0; h < kHalf; h += 32) emit(v + h, group * kHalf + h);
+                }
+            } else {
+                const int buf = it & 1;
+                ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
+                ok = !epilogue_any(!ok);
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * kAcc + ((uint32_t)(quarter * 32) << 16) +
+                                         group * kHalf;
+#pragma unroll 1
+                    for (int h = 0; h < kHalf; h += 32) {
+                        uint32_t u[32];
+                        float v[32];
+                        __syncwarp();
+                        tmem_ld32(acc + h, u);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(u[e]);
+                        if (h + 32 == kHalf) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(acc_empty + buf);
+                        }
+                        emit(v, group * kHalf + h);
+                    }
+                    ++it;
+                }
+            }
+            if (!ok) {
+                *s_fail = 1u;
+                break;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && *s_fail) atomicOr(&st->error, kErrTimeout);
+    if (warp == 1) tmem_dealloc(tmem, 2 * kAcc);
+}
+
+// The parts of a product added in their order, and finished.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part) {
+    pdl_begin();
+    const int64_t size = q.m * q.n, groups = (q.n + 3) / 4, total = q.m * groups;
+    for (int64_t g = blockIdx.x * 256ll + threadIdx.x; g < total; g += gridDim.x * 256ll) {
+        const int64_t r = g / groups, c = (g - r * groups) * 4, at = r * q.n + c;
+        const int n = (int)(q.n - c < 4 ? q.n - c : 4);
+        float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if ((q.n & 3) == 0) {   // (the workspace is aligned)
+#pragma unroll 8
+            for (int s = 0; s < q.splits; ++s) {
+                const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * size + at));
+                z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
+            }
+        } else {
+#pragma unroll 4
+            for (int s = 0; s < q.splits; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) z[e] += part[s * size + at + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] += q.bias && e < n ? q.bias[c + e] : 0.0f;
+        finish4<T>(q, z, at, n);
+    }
+}
+
+// -------------------------------------------------------------- few rows --
+// Up to kFewRows rows are bound by reading the weights once: a warp per output
+// takes the products in 32 bits, its lanes along the inputs.
+constexpr int kFewRows = 4;
+
+template <typename T, int V, int kRows>
+__global__ void __launch_bounds__(256)
+k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k,
+              const Product q) {
+    pdl_begin();
+    const int lane = threadIdx.x & 31;
+    const int64_t j = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    if (j >= q.n) return;
+    const T* w = weight + j * k;
+    float sum[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) sum[r] = 0.0f;
+#pragma unroll 8
+    for (int64_t c = lane * V; c < k; c += 32 * V) {
+        float u[V];
+        Pack<T, V>::load(w + c, u);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float v[V];
+            Pack<T, V>::load(x + r * k + c, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[r] = fmaf(u[e], v[e], sum[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
+        if (lane == r) {
+            float z[4] = {sum[r] + (q.bias ? q.bias[j] : 0.0f), 0.0f, 0.0f, 0.0f};
+            finish4<T>(q, z, r * q.n + j, 1);   // (q.vec is false)
+        }
+    }
+}
+
+// ------------------------------------------------------------------ plans --
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+
+// An operand as the products read it: a bfloat16 matrix [planes][rows][pitch].
+struct Matrix {
+    const __nv_bfloat16* at;
+    int64_t rows, cols, pitch;
+    size_t plane;
+    int planes;
+};
+
+// A map whose boxes are 64 columns of `box_rows` rows.
+bool encode(CUtensorMap* map, const Matrix& m, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)m.pitch * 2,
+                                   (cuuint64_t)(m.planes > 1 ? m.plane : m.pitch) * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kPanel, (cuuint32_t)box_rows, 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return g_encode &&
+           g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                    const_cast<__nv_bfloat16*>(m.at), dims, strides, box, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t plane_size(int64_t rows, int64_t cols) { return (size_t)rows * round8(cols); }
+
+// The sums' workspace of a product in parts: as many as fill the SMs once, of kLeast panels.
+constexpr int kMostSms = 160;
+constexpr int kLeast = 4;
+int splits_of(int64_t tiles, int64_t panels, int n_sms) {
+    const int64_t fit = n_sms / tiles, most = panels / kLeast;
+    const int64_t s = fit < most ? fit : most;
+    return s > 1 ? (int)s : 1;
+}
+// Columns of a tile: an MMA of N = 256 takes little longer than one of 128.
+int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
+size_t part_floats(int planes, int64_t m, int64_t n, int64_t k) {
+    const int64_t tiles = ceil_div(m, kBlock) * ceil_div(n, tile_n(planes, n));
+    if (tiles == 0 || tiles > kMostSms) return 0;
+    const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms);
+    return s > 1 ? (size_t)s * m * n : 0;
+}
+
+// Blocks of rows of k_linear_operand: about eight blocks per SM over the whole matrix.
+struct OperandGrid {
+    int tx;
+    int64_t block_rows, blocks, col_blocks;
+};
+OperandGrid operand_grid(int64_t rows, int64_t cols) {
+    OperandGrid g;
+    const int64_t groups = ceil_div(cols, 8);
+    g.tx = 1;
+    while (g.tx < 32 && g.tx < groups) g.tx *= 2;
+    g.col_blocks = ceil_div(groups, g.tx);
+    const int64_t least = 256 / g.tx;   // a row per thread
+    int64_t want = kMostSms * 8 / g.col_blocks;
+    if (want < 1) want = 1;
+    g.block_rows = ceil_div(ceil_div(rows, want), least) * least;
+    if (g.block_rows < least) g.block_rows = least;
+    g.blocks = ceil_div(rows, g.block_rows);
+    return g;
+}
+
+struct Space {
+    __nv_bfloat16 *x, *w, *dz;
+    float *sums, *parts;
+    size_t bytes;
+};
+Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
+    const int planes = dtype == kF32 ? kMaxPlanes : 1;
+    Carve c{static_cast<unsigned char*>(ws)};
+    Space s;
+    s.x = c.take<__nv_bfloat16>(planes * plane_size(m, k));
+    s.w = c.take<__nv_bfloat16>(planes * plane_size(n, k));
+    s.dz = c.take<__nv_bfloat16>(planes * plane_size(m, n));
+    s.sums = c.take<float>((size_t)operand_grid(m, n).blocks * n);
+    size_t parts = part_floats(planes, m, n, k);
+    const size_t dx = part_floats(planes, m, k, n), dw = part_floats(planes, n, k, m);
+    if (dx > parts) parts = dx;
+    if (dw > parts) parts = dw;
+    s.parts = c.take<float>(parts);
+    s.bytes = c.used;
+    return s;
+}
+
+template <typename T, int kPlanes, int kAct>
+cudaError_t operand_as(const Operand& o, const OperandGrid& g, cudaStream_t s) {
+    return launch_pdl(k_linear_operand<T, kPlanes, kAct>,
+                      dim3((unsigned)g.blocks, (unsigned)g.col_blocks), dim3(256), 0, s, o);
+}
+
+// `src` (times the activation's slope at `pre`) as an operand: its planes in `planes`, where it is
+// not one as it lies, and its column sums.
+template <typename T>
+cudaError_t operand(Matrix* out, const void* src, const void* pre, int act, int64_t rows,
+                    int64_t cols, __nv_bfloat16* planes, float* sums, cudaStream_t s) {
+    constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    if (!pre) act = kActNone;
+    const bool as_is = kPlanes == 1 && act == kActNone && cols % 8 == 0 && aligned16(src);
+    const int64_t pitch = round8(cols);
+    *out = as_is ? Matrix{static_cast<const __nv_bfloat16*>(src), rows, cols, cols, 0, 1}
+                 : Matrix{planes, rows, cols, pitch, (size_t)rows * pitch, kPlanes};
+    if ((as_is || !planes) && !sums) return cudaSuccess;
+    const OperandGrid g = operand_grid(rows, cols);
+    const Operand o{src, pre, act, rows, cols, pitch, as_is ? nullptr : planes,
+                    (size_t)rows * pitch, sums, g.tx, g.block_rows,
+                    cols % VecOf<T>::n == 0 && aligned16(src) && aligned16(pre)};
+    switch (act) {
+        case kActSilu: return operand_as<T, kPlanes, kActSilu>(o, g, s);
+        case kActRelu: return operand_as<T, kPlanes, kActRelu>(o, g, s);
+        default: return operand_as<T, kPlanes, kActNone>(o, g, s);
+    }
+}
+
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
+cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
+                       LearnState* st, int n_sms, cudaStream_t s) {
+    q.tiles_m = (int)ceil_div(q.m, kBlock);
+    q.tiles_n = (int)ceil_div(q.n, kN);
+    q.panels = (int)ceil_div(k, kPanel);
+    const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
+    q.splits = tiles <= n_sms ? splits_of(tiles, q.panels, n_sms) : 1;
+    if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : kN))
+        return cudaErrorInvalidValue;
+    const auto launch = [&](auto kernel, const Product& p) {
+        const int64_t total = tiles * p.splits;
+        return launch_pdl(kernel, dim3((unsigned)(total < n_sms ? total : n_sms)),
+                          dim3(kProductThreads), ProductSmem<kPlanes, kN>::bytes, s, p, st);
+    };
+    if (q.splits == 1) return launch(k_linear_product<T, kPlanes, kN, kAMn, kBMn>, q);
+    Product p = q;
+    p.bias = nullptr;
+    p.residual = p.pre = nullptr;
+    p.out = parts;
+    p.act = kActNone;
+    p.vec = q.n % 4 == 0;
+    cudaError_t e = launch(k_linear_product<float, kPlanes, kN, kAMn, kBMn>, p);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = ceil_div(q.m * ceil_div(q.n, 4), 256);
+    return launch_pdl(k_linear_join<T>, dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8)),
+                      dim3(256), 0, s, q, (const float*)parts);
+}
+
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t product(const Product& q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
+                    LearnState* st, int n_sms, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4)
+        return product_as<T, 3, 128, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+    else if (tile_n(1, q.n) == 128)
+        return product_as<T, 1, 128, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+    else
+        return product_as<T, 1, 256, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+}
+
+bool aligned_to4(const void* p, int size) {
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(4 * size - 1)) == 0;
+}
+template <typename T>
+bool vec4(const Product& q) {
+    return q.n % 4 == 0 && aligned_to4(q.out, sizeof(T)) && aligned_to4(q.pre, sizeof(T)) &&
+           aligned_to4(q.residual, sizeof(T));
+}
+
+template <typename T, int V>
+cudaError_t few_rows(const LinearCall& c, const Product& q, cudaStream_t s) {
+    const dim3 grid((unsigned)ceil_div(c.outputs, 8)), block(256);
+    const T *x = static_cast<const T*>(c.x), *w = static_cast<const T*>(c.weight);
+    switch (c.rows) {
+        case 1: return launch_pdl(k_linear_rows<T, V, 1>, grid, block, 0, s, x, w, c.inputs, q);
+        case 2: return launch_pdl(k_linear_rows<T, V, 2>, grid, block, 0, s, x, w, c.inputs, q);
+        case 3: return launch_pdl(k_linear_rows<T, V, 3>, grid, block, 0, s, x, w, c.inputs, q);
+        default: return launch_pdl(k_linear_rows<T, V, 4>, grid, block, 0, s, x, w, c.inputs, q);
+    }
+}
+
+template <typename T>
+cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
+    const int64_t m = c.rows, k = c.inputs, n = c.outputs;
+    if (m == 0) return cudaSuccess;
+    Product q{};
+    q.m = m;
+    q.n = n;
+    q.bias = c.bias;
+    q.residual = c.residual;
+    q.pre = c.pre;
+    q.out = c.out;
+    q.act = c.act;
+    if (m <= kFewRows) {
+        constexpr int V = VecOf<T>::n;
+        return k % V == 0 && aligned16(c.x) && aligned16(c.weight) ? few_rows<T, V>(c, q, s)
+                                                                   : few_rows<T, 1>(c, q, s);
+    }
+    q.vec = vec4<T>(q);
+    const Space sp = carve(ws, m, k, n, c.dtype);
+    Matrix x, w;
+    cudaError_t e = operand<T>(&x, c.x, nullptr, kActNone, m, k, sp.x, nullptr, s);
+    if (e == cudaSuccess) e = operand<T>(&w, c.weight, nullptr, kActNone, n, k, sp.w, nullptr, s);
+    if (e != cudaSuccess) return e;
+    return product<T, false, false>(q, x, w, k, sp.parts, st, n_sms, s);
+}
+
+template <typename T>
+cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
+    const int64_t m = c.rows, k = c.inputs, n = c.outputs;
+    if (m == 0) {
+        cudaError_t e = cudaSuccess;
+        if (c.grad_weight) e = cudaMemsetAsync(c.grad_weight, 0, sizeof(T) * n * k, s);
+        if (e == cudaSuccess && c.grad_bias) e = cudaMemsetAsync(c.grad_bias, 0, 4 * n, s);
+        return e;
+    }
+    const Space sp = carve(ws, m, k, n, c.dtype);
+    Matrix dz, w, x;
+    cudaError_t e = cudaSuccess;
+    if (c.grad_x || c.grad_weight || c.grad_bias)
+        e = operand<T>(&dz, c.grad_y, c.act == kActNone ? nullptr : c.pre, c.act, m, n,
+                       c.grad_x || c.grad_weight ? sp.dz : nullptr,
+                       c.grad_bias ? sp.sums : nullptr, s);
+    if (e == cudaSuccess && c.grad_bias)
+        e = launch_pdl(k_linear_sums, dim3((unsigned)ceil_div(n, 32)), dim3(32, 32), 0, s,
+                       (const float*)sp.sums, operand_grid(m, n).blocks, n, c.grad_bias);
+    if (e == cudaSuccess && c.grad_x) {
+        e = operand<T>(&w, c.weight, nullptr, kActNone, n, k, sp.w, nullptr, s);
+        Product q{};
+        q.m = m;
+        q.n = k;
+        q.out = c.grad_x;
+        q.vec = vec4<T>(q);
+        if (e == cudaSuccess)
+            e = product<T, false, true>(q, dz, w, n, sp.parts, st, n_sms, s);
+    }
+    if (e == cudaSuccess && c.grad_weight) {
+        e = operand<T>(&x, c.x, nullptr, kActNone, m, k, sp.x, nullptr, s);
+        Product q{};
+        q.m = n;
+        q.n = k;
+        q.out = c.grad_weight;
+        q.vec = vec4<T>(q);
+        if (e == cudaSuccess)
+            e = product<T, true, true>(q, dz, x, m, sp.parts, st, n_sms, s);
+    }
+    return e;
+}
+
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
+cudaError_t prepare_one() {
+    constexpr int bytes = ProductSmem<kPlanes, kN>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(k_linear_product<T, kPlanes, kN, kAMn, kBMn>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && sizeof(T) == 2)
+        e = cudaFuncSetAttribute(k_linear_product<float, kPlanes, kN, kAMn, kBMn>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e;
+}
+template <typename T, int kPlanes, int kN>
+cudaError_t prepare_three() {
+    cudaError_t e = prepare_one<T, kPlanes, kN, false, false>();
+    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, false, true>();
+    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, true, true>();
+    return e;
+}
+
+}  // namespace
+
+size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
+    return carve(nullptr, rows, inputs, outputs, dtype).bytes;
+}
+
+cudaError_t prepare_linear() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                     cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeTiled>(f);
+    e = prepare_three<float, 3, 128>();
+    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128>();
+    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256>();
+    return e;
+}
+
+cudaError_t launch_linear_forward(const LinearCall& c, LearnState* st, void* ws, int n_sms,
+                                  cudaStream_t stream) {
+    return c.dtype == kF32 ? forward<float>(c, st, ws, n_sms, stream)
+                           : forward<__nv_bfloat16>(c, st, ws, n_sms, stream);
+}
+cudaError_t launch_linear_backward(const LinearCall& c, LearnState* st, void* ws, int n_sms,
+                                   cudaStream_t stream) {
+    return c.dtype == kF32 ? backward<float>(c, st, ws, n_sms, stream)
+                           : backward<__nv_bfloat16>(c, st, ws, n_sms, stream);
+}
+
+}  // namespace pulsar

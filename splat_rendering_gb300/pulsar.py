@@ -8,8 +8,8 @@ Functions mirror the C entry points:
     create, destroy, project, bin, forward, backward, status, strerror,
     debug_copy
 and, for the learned parts around the renderer (codebook embedding, group
-norm, orthogonalised updates), the Learner class and the *_workspace
-functions.
+norm, linear layers, dropout, orthogonalised updates), the Learner class and
+the *_workspace functions.
 Tensor arguments are CUDA torch tensors (float32, contiguous) or raw device
 pointers (int); streams are torch.cuda.Stream objects, raw handles (int) or
 None for the current torch stream.
@@ -65,7 +65,9 @@ EXPORTS = ("pulsar_create", "pulsar_create_cams", "pulsar_destroy", "pulsar_proj
            "pulsar_learn_create", "pulsar_learn_destroy", "pulsar_learn_status",
            "pulsar_embed_workspace", "pulsar_group_norm_workspace",
            "pulsar_orthogonalize_workspace", "pulsar_embed_forward", "pulsar_embed_backward",
-           "pulsar_group_norm_forward", "pulsar_group_norm_backward", "pulsar_orthogonalize")
+           "pulsar_group_norm_forward", "pulsar_group_norm_backward", "pulsar_orthogonalize",
+           "pulsar_linear_workspace", "pulsar_linear_forward", "pulsar_linear_backward",
+           "pulsar_dropout")
 
 
 def load(path: str = LIB_PATH):
@@ -106,8 +108,9 @@ def load(path: str = LIB_PATH):
     lib.pulsar_embed_workspace.argtypes = [I64, I64, I64]
     lib.pulsar_group_norm_workspace.argtypes = [I64, I64, I32, I32]
     lib.pulsar_orthogonalize_workspace.argtypes = [I64, I64, I64, I]
+    lib.pulsar_linear_workspace.argtypes = [I64, I64, I64, I]
     workspaces = ("pulsar_embed_workspace", "pulsar_group_norm_workspace",
-                  "pulsar_orthogonalize_workspace")
+                  "pulsar_orthogonalize_workspace", "pulsar_linear_workspace")
     for name in workspaces:
         getattr(lib, name).restype = I64
     lib.pulsar_embed_forward.argtypes = [P, P, P, I64, I64, I64, F, I, I, P, P]
@@ -116,6 +119,9 @@ def load(path: str = LIB_PATH):
     lib.pulsar_group_norm_backward.argtypes = [P, P, P, P, I64, I64, I32, I32, P, P, I, I, P, P, P,
                                                P]
     lib.pulsar_orthogonalize.argtypes = [P, P, I64, I64, I64, I, P, F, I, P, P]
+    lib.pulsar_linear_forward.argtypes = [P, P, P, I64, I64, I64, P, P, I, I, P, P, P]
+    lib.pulsar_linear_backward.argtypes = [P, P, P, P, P, I64, I64, I64, I, I, P, P, P, P]
+    lib.pulsar_dropout.argtypes = [P, P, P, I64, ctypes.c_double, ctypes.c_uint64, I64, P, I, P, P]
     for name in EXPORTS:
         if name not in ("pulsar_strerror", "pulsar_debug_copy") + workspaces:
             getattr(lib, name).restype = ctypes.c_int
@@ -440,6 +446,13 @@ def orthogonalize_workspace(batch: int, m: int, n: int, dtype) -> int:
                   "pulsar_orthogonalize_workspace")
 
 
+@functools.lru_cache(maxsize=1024)   # a function of the sizes alone
+def linear_workspace(rows: int, inputs: int, outputs: int, dtype) -> int:
+    """Bytes of workspace of Learner.linear and linear_backward."""
+    return _bytes(load().pulsar_linear_workspace(rows, inputs, outputs, _dtype_code(dtype)),
+                  "pulsar_linear_workspace")
+
+
 class Learner:
     """A handle for the learned parts around the renderer, and its calls on
     torch tensors of one device (see include/pulsar.h for what they compute).
@@ -449,6 +462,9 @@ class Learner:
         y, stats = ops.group_norm(image, groups, weight, bias, act="silu")
         grad_image, gw, gb = ops.group_norm_backward(grad_y, image, stats, groups, weight, bias)
         grad_codebook = ops.embed_backward(grad_features, tokens, rows)
+        h, z = ops.linear(y, weight, bias, act="silu", want_pre=True)
+        h = ops.dropout(h, 0.1, seed, offset)           # gradient: the same call
+        grad_y, gw, gb = ops.linear_backward(grad_h, y, weight, z, act="silu")
         update = ops.orthogonalize(grad_matrix)
 
     Tensors are contiguous and on the handle's device; anything else raises
@@ -609,4 +625,84 @@ class Learner:
         _check(self._lib.pulsar_orthogonalize(
             self.handle, self._tensor(grad, "grad"), self._product(shape[:-2]), shape[-2], shape[-1],
             steps, abc, eps, dt, p_out, self._stream(stream)), "pulsar_orthogonalize")
+        return out
+
+    def _layer_shape(self, x, weight, act):
+        """(rows, inputs, outputs, activation) of a linear layer's call."""
+        if weight.dim() != 2:
+            raise ValueError(f"weight has shape {tuple(weight.shape)}, wanted [outputs, inputs]")
+        outputs, inputs = weight.shape
+        shape = x.shape
+        if len(shape) < 1 or shape[-1] != inputs:
+            raise ValueError(f"x has shape {tuple(shape)}, wanted [..., {inputs}]")
+        a = ACT.get(act)
+        if a is None:
+            raise ValueError(f"act is one of {sorted(ACT)}, got {act!r}")
+        return self._product(shape[:-1]), inputs, outputs, a
+
+    def linear(self, x, weight, bias=None, residual=None, act: str = "none", out=None, pre=None,
+               want_pre: bool = False, stream=None):
+        """(y, z): z = x weight^T + bias and y = act(z) + residual of x [..., inputs], weight
+        [outputs, inputs], bias [outputs] (float32) and residual [..., outputs].  z, which
+        linear_backward reads where there is an activation, is None unless wanted (or given)."""
+        rows, inputs, outputs, a = self._layer_shape(x, weight, act)
+        dtype = x.dtype
+        dt = _dtype_code(dtype)
+        shape = (*x.shape[:-1], outputs)
+        out, p_out = self._out(out, "out", shape, dtype, stream)
+        p_pre = None
+        if want_pre or pre is not None:
+            pre, p_pre = self._out(pre, "pre", shape, dtype, stream)
+        _check(self._lib.pulsar_linear_forward(
+            self.handle, self._tensor(x, "x"), self._tensor(weight, "weight", None, dtype), rows,
+            inputs, outputs, self._tensor(bias, "bias", (outputs,), self._torch.float32),
+            self._tensor(residual, "residual", shape, dtype), a, dt, p_out, p_pre,
+            self._stream(stream)), "pulsar_linear_forward")
+        return out, pre
+
+    def linear_backward(self, grad_y, x, weight, pre=None, act: str = "none", grad_x=None,
+                        grad_weight=None, grad_bias=None, want=("x", "weight", "bias"),
+                        stream=None):
+        """(grad_x, grad_weight, grad_bias) of `linear` for its x, weight and z (`pre`, needed
+        where there is an activation); those not in `want` (and not given) are None and not
+        computed.  The residual's gradient is grad_y."""
+        rows, inputs, outputs, a = self._layer_shape(x, weight, act)
+        dtype, f32 = x.dtype, self._torch.float32
+        dt = _dtype_code(dtype)
+        shape = (*x.shape[:-1], outputs)
+        if a and pre is None:
+            raise ValueError(f"pre is needed for act={act!r}")
+        p_x = p_weight = p_bias = None
+        if grad_x is not None or "x" in want:
+            grad_x, p_x = self._out(grad_x, "grad_x", x.shape, dtype, stream)
+        if grad_weight is not None or "weight" in want:
+            grad_weight, p_weight = self._out(grad_weight, "grad_weight", weight.shape, dtype,
+                                              stream)
+        if grad_bias is not None or "bias" in want:
+            grad_bias, p_bias = self._out(grad_bias, "grad_bias", (outputs,), f32, stream)
+        _check(self._lib.pulsar_linear_backward(
+            self.handle, self._tensor(grad_y, "grad_y", shape, dtype), self._tensor(x, "x"),
+            self._tensor(weight, "weight", None, dtype), self._tensor(pre, "pre", shape, dtype),
+            rows, inputs, outputs, a, dt, p_x, p_weight, p_bias, self._stream(stream)),
+            "pulsar_linear_backward")
+        return grad_x, grad_weight, grad_bias
+
+    def dropout(self, x, p: float, seed: int, offset: int = 0, counter=None, residual=None,
+                out=None, stream=None):
+        """x / (1 - p) where its random number is at least p, else 0, + residual.  The numbers
+        are Philox4x32-7 of the key `seed` (64 bits) and the ceil(numel / 4) counters from
+        `offset` on, plus what `counter`, an int64 tensor of one element, holds when the call
+        runs.  The gradient of x is the same call on the output's."""
+        dtype = x.dtype
+        dt = _dtype_code(dtype)
+        if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 63:   # (ctypes would cut them)
+            raise ValueError(f"seed and offset are whole numbers of 64 bits, got {seed}, {offset}")
+        if counter is not None and counter.numel() != 1:
+            raise ValueError(f"counter has {counter.numel()} elements, wanted 1")
+        out, p_out = self._out(out, "out", x.shape, dtype, stream)
+        _check(self._lib.pulsar_dropout(
+            self.handle, self._tensor(x, "x"), self._tensor(residual, "residual", x.shape, dtype),
+            x.numel(), p, seed, offset,
+            self._tensor(counter, "counter", None, self._torch.int64), dt, p_out,
+            self._stream(stream)), "pulsar_dropout")
         return out
