@@ -271,49 +271,139 @@ __device__ __forceinline__ bool epilogue_any(bool v) {
     return any != 0;
 }
 
-// Four columns of a row: bias, pre-activation, activation, residual, and the result.
+// What the epilogue does with 32 columns of a warp's 32 rows, a row in each lane: through the
+// warp's exchange in shared memory (float4 chunks, swizzled), after which a lane has four columns
+// of every fourth row, and a warp reads the residual and writes whole sectors of eight rows' 32
+// columns at a time.
+// (The residual's sum is kept apart from the activation's last product: whether z is wanted too
+// changes no bits.)
+__device__ __forceinline__ float plus(float a, float b) { return __fadd_rn(a, b); }
+
 template <typename T>
-__device__ __forceinline__ void finish4(const Product& q, float (&z)[4], int64_t at, int n) {
-    const T* residual = static_cast<const T*>(q.residual);
-    T* pre = static_cast<T*>(q.pre);
-    T* out = static_cast<T*>(q.out);
-    float y[4];
+struct Four;
+template <>
+struct Four<float> {
+    using Raw = float4;
+    static __device__ __forceinline__ void add(const Raw& r, float (&y)[4]) {
+        y[0] = plus(y[0], r.x); y[1] = plus(y[1], r.y);
+        y[2] = plus(y[2], r.z); y[3] = plus(y[3], r.w);
+    }
+    static __device__ __forceinline__ Raw pack(const float (&y)[4]) {
+        return make_float4(y[0], y[1], y[2], y[3]);
+    }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void add(const Raw& r, float (&y)[4]) {
+        y[0] = plus(y[0], low_of(r.x)); y[1] = plus(y[1], high_of(r.x));
+        y[2] = plus(y[2], low_of(r.y)); y[3] = plus(y[3], high_of(r.y));
+    }
+    static __device__ __forceinline__ Raw pack(const float (&y)[4]) {
+        return make_uint2(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]));
+    }
+};
+
+// A lane's share of the block of 32 rows from r0 and 32 columns from c0.
+template <typename T>
+struct Share {
+    using Raw = typename Four<T>::Raw;
+    int64_t c, at;   // its first column, and its first element
+    int n, rows;     // columns (of four), rows that there are from its first on
+    Raw residual[8];
+
+    // (at: of the element (r0, c0) in a matrix of q.n columns)
+    __device__ __forceinline__ void begin(const Product& q, int64_t r0, int64_t c0, int64_t base,
+                                          int lane) {
+        c = c0 + 4 * (lane & 7);
+        n = (int)(q.n - c < 4 ? q.n - c : 4);
+        at = base + (r0 + (lane >> 3)) * q.n + c;
+        const int64_t left = q.m - r0 - (lane >> 3);
+        rows = n <= 0 ? 0 : (int)(left < 32 ? left : 32);
+        if (q.residual && q.vec) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = act_any(q.act, z[e]);
-    if (q.vec) {
-        if constexpr (sizeof(T) == 4) {
-            if (pre) *reinterpret_cast<float4*>(pre + at) = make_float4(z[0], z[1], z[2], z[3]);
-            if (residual) {
-                const float4 r = *reinterpret_cast<const float4*>(residual + at);
-                y[0] += r.x; y[1] += r.y; y[2] += r.z; y[3] += r.w;
-            }
-            *reinterpret_cast<float4*>(out + at) = make_float4(y[0], y[1], y[2], y[3]);
-        } else {
-            if (pre)
-                *reinterpret_cast<uint2*>(pre + at) =
-                    make_uint2(pair_bf16(z[0], z[1]), pair_bf16(z[2], z[3]));
-            if (residual) {
-                const uint2 r = *reinterpret_cast<const uint2*>(residual + at);
-                y[0] += low_of(r.x); y[1] += high_of(r.x);
-                y[2] += low_of(r.y); y[3] += high_of(r.y);
-            }
-            *reinterpret_cast<uint2*>(out + at) =
-                make_uint2(pair_bf16(y[0], y[1]), pair_bf16(y[2], y[3]));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (e >= n) continue;
-            float u[1] = {z[e]};
-            if (pre) Pack<T, 1>::store(pre + at + e, u);
-            if (residual) {
-                Pack<T, 1>::load(residual + at + e, u);
-                y[e] += u[0];
-            }
-            u[0] = y[e];
-            Pack<T, 1>::store(out + at + e, u);
+            for (int h = 0; h < 8; ++h)
+                if (4 * h < rows)
+                    residual[h] = __ldcs(reinterpret_cast<const Raw*>(
+                        static_cast<const T*>(q.residual) + at + (int64_t)4 * h * q.n));
         }
     }
+
+    template <int kAct>
+    __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
+                                        int lane) {
+        float bias[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = q.bias && e < n ? q.bias[c + e] : 0.0f;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[lane * 8 + (e ^ (lane & 7))] =
+                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        __syncwarp();
+        T* out = static_cast<T*>(q.out) + at;
+        T* pre = q.pre ? static_cast<T*>(q.pre) + at : nullptr;
+        const int cq = lane & 7, rq = lane >> 3;
+        const int64_t step = 4 * q.n;
+        if (q.vec) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const int r = 4 * h + rq;
+                const float4 u = x[r * 8 + (cq ^ (r & 7))];
+                const float z[4] = {plus(u.x, bias[0]), plus(u.y, bias[1]), plus(u.z, bias[2]),
+                                    plus(u.w, bias[3])};
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = act_of<kAct>(z[e]);
+                if (4 * h < rows) {
+                    if (pre) *reinterpret_cast<Raw*>(pre + h * step) = Four<T>::pack(z);
+                    if (q.residual) Four<T>::add(residual[h], y);
+                    *reinterpret_cast<Raw*>(out + h * step) = Four<T>::pack(y);
+                }
+            }
+            return;
+        }
+        const T* skip = q.residual ? static_cast<const T*>(q.residual) + at : nullptr;
+#pragma unroll 1
+        for (int h = 0; 4 * h < rows; ++h) {
+            const int r = 4 * h + rq;
+            const float4 u = x[r * 8 + (cq ^ (r & 7))];
+            const float w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e >= n) continue;
+                const float z[1] = {plus(w[e], bias[e])};
+                float y[1] = {act_of<kAct>(z[0])};
+                if (pre) Pack<T, 1>::store(pre + h * step + e, z);
+                if (skip) {
+                    float f[1];
+                    Pack<T, 1>::load(skip + h * step + e, f);
+                    y[0] = plus(y[0], f[0]);
+                }
+                Pack<T, 1>::store(out + h * step + e, y);
+            }
+        }
+    }
+    __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
+                                        int lane) {
+        if (q.act == kActSilu) end<kActSilu>(q, x, v, lane);
+        else if (q.act == kActRelu) end<kActRelu>(q, x, v, lane);
+        else end<kActNone>(q, x, v, lane);
+    }
+};
+
+// One element of a result: bias (already in z), pre-activation, activation, residual.
+template <typename T>
+__device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
+    const float one[1] = {z};
+    if (q.pre) Pack<T, 1>::store(static_cast<T*>(q.pre) + at, one);
+    float y[1] = {act_any(q.act, z)};
+    if (q.residual) {
+        float f[1];
+        Pack<T, 1>::load(static_cast<const T*>(q.residual) + at, f);
+        y[0] = plus(y[0], f[0]);
+    }
+    Pack<T, 1>::store(static_cast<T*>(q.out) + at, y);
 }
 
 // T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
@@ -471,35 +561,18 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     } else {   // ---- epilogue
         const int group = (warp - 2) >> 2, quarter = warp & 3;   // (warps 2 .. 9)
         float4* x = reinterpret_cast<float4*>(smem + L::exchange) + (warp - 2) * 256;
-        const int cq = lane & 7, rq = lane >> 3;
         int it = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             int i, j, k0, k1, part;
             place(t, &i, &j, &k0, &k1, &part);
+            const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
+            const int64_t base = (int64_t)part * q.m * q.n;
             // 32 columns from `col` of the tile, a row in each lane
-            auto emit = [&](const float* v, int col) {
-                const int64_t c = (int64_t)j * kN + col + 4 * cq;
-                const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
-                const int n = (int)(q.n - c < 4 ? q.n - c : 4);
-                float bias[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bias[e] = q.bias && e < n ? q.bias[c + e] : 0.0f;
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[lane * 8 + (e ^ (lane & 7))] =
-                        make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                __syncwarp();
-                if (n <= 0) return;
-                int64_t at = (int64_t)part * q.m * q.n + (r0 + rq) * q.n + c;
-#pragma unroll
-                for (int h = 0; h < 8; ++h, at += 4 * q.n) {
-                    const int r = 4 * h + rq;
-                    if (r0 + r >= q.m) break;
-                    const float4 u = x[r * 8 + (cq ^ (r & 7))];
-                    float z[4] = {u.x + bias[0], u.y + bias[1], u.z + bias[2], u.w + bias[3]};
-                    finish4<T>(q, z, at, n);
-                }
+            auto emit = [&](const float (&v)[32], int col) {
+                Share<T> share;
+                share.begin(q, r0, (int64_t)j * kN + col, base, lane);
+                if (kAMn || kBMn) share.template end<kActNone>(q, x, v, lane);
+                else share.end(q, x, v, lane);
             };
             bool ok = true;
             if constexpr (kPlanes == 3) {
@@ -530,7 +603,12 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                 }
                 if (ok) {
 #pragma unroll
-                    for (int h = 0; h < kHalf; h += 32) emit(v + h, group * kHalf + h);
+                    for (int h = 0; h < kHalf; h += 32) {
+                        float w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = v[h + e];
+                        emit(w, group * kHalf + h);
+                    }
                 }
             } else {
                 const int buf = it & 1;
@@ -597,8 +675,8 @@ k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part)
                     if (e < n) z[e] += part[s * size + at + e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] += q.bias && e < n ? q.bias[c + e] : 0.0f;
-        finish4<T>(q, z, at, n);
+        for (int e = 0; e < 4; ++e)
+            if (e < n) finish1<T>(q, z[e] + (q.bias ? q.bias[c + e] : 0.0f), at + e);
     }
 }
 
@@ -635,11 +713,291 @@ k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k,
     for (int r = 0; r < kRows; ++r) {
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-        if (lane == r) {
-            float z[4] = {sum[r] + (q.bias ? q.bias[j] : 0.0f), 0.0f, 0.0f, 0.0f};
-            finish4<T>(q, z, r * q.n + j, 1);   // (q.vec is false)
+        if (lane == r) finish1<T>(q, sum[r] + (q.bias ? q.bias[j] : 0.0f), r * q.n + j);
+    }
+}
+
+// ---------------------------------------------------------- narrow layers --
+// A layer of few inputs and outputs over many rows (a network's hidden layer
+// over an image) is bound by its rows' way in and out.  One launch, a
+// persistent CTA per SM, tiles of 128 rows, each read and written once.  Roles:
+// one thread keeps a ring of raw tiles filled (128 rows are one contiguous bulk
+// copy, whatever their width), eight warps make a tile's operand from it, 64
+// columns of the contraction at a time (in 32 bits its three planes), one
+// thread issues the MMAs, and eight warps finish the tile from tensor memory.
+// The weights are made into operands by every CTA once, and stay.
+//
+// In 32 bits the weights' planes lie below one another, [hi; mid; lo], so that a
+// plane of the rows takes one MMA against those that count: hi against all
+// three, mid against hi and mid, lo against hi.  Their sums in three ranges of
+// columns are hi hi, (hi mid + mid hi), (hi lo + mid mid + lo hi), so that what
+// the tensor cores truncate is relative to each; at most 128 of K, as there.
+constexpr int kStreamThreads = 576;   // warps: copies, MMAs, eight of operands, eight of the epilogue
+constexpr int kStreamMaxK = 128;
+template <typename T>
+constexpr int kStreamN = sizeof(T) == 4 ? 64 : 128;   // outputs of a CTA
+
+struct Stream {
+    const void* x;         // [m, k]
+    const void* weight;    // [n, k]
+    int64_t tiles;
+    int k, panels;         // of the contraction
+    int np, blocks;        // outputs of a block (a multiple of 16), blocks
+    int raws, units;       // raw tiles, operand panels in flight
+    bool vec;              // a row of x, and of the weight, is whole 16-byte vectors
+    Product out;           // m, n, bias, ..., vec
+};
+struct StreamSmem {
+    int raw, raw_bytes, unit, unit_bytes, weight, weight_panel, exchange, bars, bytes;
+};
+__host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, int panels, int np,
+                                                  int raws, int units) {
+    StreamSmem s;
+    s.unit = 0;
+    s.unit_bytes = planes * kBlock * kPanel * 2;
+    s.weight = s.unit + units * s.unit_bytes;
+    s.weight_panel = planes * np * kPanel * 2;
+    s.exchange = s.weight + panels * s.weight_panel;
+    s.raw = s.exchange + 8 * 32 * 32 * 4;
+    s.raw_bytes = (kBlock * k * size + 127) / 128 * 128;
+    s.bars = s.raw + raws * s.raw_bytes;
+    s.bytes = s.bars + 256 + 1024;
+    return s;
+}
+constexpr int kStreamSmemMax = 227 * 1024;
+
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// Eight columns (16 bytes of bfloat16) of row `row`, the chunk'th of a 128-byte row, as planes.
+template <int kPlanes>
+__device__ __forceinline__ void put_chunk(unsigned char* at, uint32_t plane_bytes, int row,
+                                          int chunk, const float (&v)[8]) {
+    uint32_t w[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (kPlanes == 3)
+            split3(v[2 * e], v[2 * e + 1], w[e]);
+        else
+            w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
+    }
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p)
+        *reinterpret_cast<uint4*>(at + p * plane_bytes + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+            make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
+    constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    constexpr int kCols = sizeof(T) == 4 ? 512 : 256;   // tensor memory: two accumulators
+    extern __shared__ unsigned char raw_smem[];
+    unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    const StreamSmem L = stream_smem(kPlanes, sizeof(T), q.k, q.panels, q.np, q.raws, q.units);
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
+    uint64_t* raw_empty = raw_full + 4;
+    uint64_t* unit_full = raw_empty + 4;
+    uint64_t* unit_empty = unit_full + 4;
+    uint64_t* acc_full = unit_empty + 4;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile uint32_t* s_fail = s_taddr + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int block = blockIdx.x % q.blocks, first = blockIdx.x / q.blocks;
+    const int step = gridDim.x / q.blocks;
+    const int n0 = block * kStreamN<T>;
+    const int steps16 = (q.k + 15) / 16;
+    if (tid == 0) {
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(raw_full + s);
+            mbar_init_n(raw_empty + s, 8);
+            mbar_init_n(unit_full + s, 8);
+            mbar_init(unit_empty + s);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(acc_full + s);
+            mbar_init_n(acc_empty + s, 8);
+        }
+        mbar_init(drain);
+        *s_fail = 0u;
+    }
+    if (warp == 1) tmem_alloc(s_taddr, kCols);
+    pdl_next();
+    pdl_begin();
+    {   // the weights, zeros below and behind them
+        const int chunks = steps16 * 2, total = q.np * chunks;
+        for (int t = tid; t < total; t += kStreamThreads) {
+            const int r = t / chunks, c = t % chunks;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            const int n = q.k - c * 8 < 8 ? q.k - c * 8 : 8;
+            if (n0 + r < q.out.n && n > 0)
+                load8(static_cast<const T*>(q.weight) + (int64_t)(n0 + r) * q.k + c * 8, n,
+                      q.vec && n == 8, v);
+            put_chunk<kPlanes>(smem + L.weight + (c >> 3) * L.weight_panel, q.np * 128, r, c & 7, v);
         }
     }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_taddr;
+    if (warp == 0) {
+        if (lane == 0) {   // ---- raw tiles
+            int n = 0;
+            bool ok = true;
+            for (int64_t t = first; t < q.tiles; t += step, ++n) {
+                const int s = n % q.raws;
+                ok = mbar_wait(raw_empty + s, ((n / q.raws) & 1) ^ 1) && !*s_fail;
+                if (!ok) break;
+                const int64_t left = q.out.m - t * kBlock;
+                const uint32_t bytes =
+                    (uint32_t)((left < kBlock ? left : kBlock) * q.k * (int)sizeof(T));
+                const unsigned char* src =
+                    static_cast<const unsigned char*>(q.x) + t * kBlock * q.k * (int64_t)sizeof(T);
+                unsigned char* dst = smem + L.raw + s * L.raw_bytes;
+                const uint32_t bulk = bytes & ~15u;   // the last rows need not end on 16 bytes
+                for (uint32_t e = bulk / sizeof(T); e < bytes / sizeof(T); ++e)
+                    reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(src)[e];
+                if (bulk)
+                    bulk_load(dst, src, bulk, raw_full + s);
+                else
+                    mbar_arrive(raw_full + s);
+            }
+            if (!ok) {   // give the copies in flight one more bounded wait
+                *s_fail = 1u;
+                for (int k = n > q.raws ? n - q.raws : 0; k < n; ++k)
+                    mbar_wait(raw_full + k % q.raws, (k / q.raws) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {   // ---- MMAs
+            const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) |
+                                    ((uint32_t)(kBlock >> 4) << 24);
+            const uint32_t np = (uint32_t)q.np;
+            uint32_t idesc[kPlanes];   // of the weights' first kPlanes - p planes
+#pragma unroll
+            for (int p = 0; p < kPlanes; ++p)
+                idesc[p] = idesc0 | ((np * (uint32_t)(kPlanes - p) >> 3) << 17);
+            const uint32_t base = smem_u32(smem);
+            int u = 0, it = 0;
+            bool ok = true;
+            for (int64_t t = first; t < q.tiles && ok; t += step, ++it) {
+                const int buf = it & 1;
+                const uint32_t d = tmem + buf * (kCols / 2);
+                ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
+                if (!ok) break;
+                for (int h = 0; h < q.panels; ++h, ++u) {
+                    const int s = u % q.units;
+                    ok = mbar_wait(unit_full + s, (u / q.units) & 1) && !*s_fail;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = base + L.unit + s * L.unit_bytes;
+                    const uint64_t b = desc_sw128(base + L.weight + h * L.weight_panel, 16);
+                    uint64_t a[kPlanes];
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p)
+                        a[p] = desc_sw128(at + p * kBlock * kPanel * 2, 16);
+                    const int ends = min(4, steps16 - 4 * h);
+                    for (int e = 0; e < ends; ++e) {
+                        const uint32_t off = 32u * e >> 4;
+                        mma_f16(d, a[0] + off, b + off, idesc[0], h > 0 || e > 0);
+#pragma unroll
+                        for (int p = 1; p < kPlanes; ++p)
+                            mma_f16(d + p * np, a[p] + off, b + off, idesc[p], 1);
+                    }
+                    mma_commit(unit_empty + s);
+                }
+                if (ok) mma_commit(acc_full + buf);
+            }
+            if (!ok) {
+                *s_fail = 1u;
+                mma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+        }
+    } else if (warp < 10) {   // ---- operands
+        const int mine = tid - 64;
+        int n = 0, u = 0;
+        bool ok = true;
+        for (int64_t t = first; t < q.tiles && ok; t += step, ++n) {
+            const int s = n % q.raws;
+            ok = warp_all(mbar_wait(raw_full + s, (n / q.raws) & 1) && !*s_fail);
+            if (!ok) break;
+            const T* tile = reinterpret_cast<const T*>(smem + L.raw + s * L.raw_bytes);
+            const int64_t left = q.out.m - t * kBlock;
+            const int rows = (int)(left < kBlock ? left : kBlock);
+            for (int h = 0; h < q.panels; ++h, ++u) {
+                const int a = u % q.units;
+                ok = warp_all(mbar_wait(unit_empty + a, ((u / q.units) & 1) ^ 1) && !*s_fail);
+                if (!ok) break;
+                unsigned char* unit = smem + L.unit + a * L.unit_bytes;
+                const int chunks = min(8, 2 * steps16 - 8 * h);
+                // (rows behind the last keep what they held: their sums are not stored)
+#pragma unroll 4
+                for (int i = mine; i < kBlock * 8; i += 256) {
+                    const int r = i >> 3, c = i & 7;
+                    if (c >= chunks || r >= rows) continue;
+                    float v[8];
+                    const int col = h * kPanel + c * 8, k = q.k - col;
+                    load8(tile + r * q.k + col, k, q.vec && k >= 8, v);
+                    put_chunk<kPlanes>(unit, kBlock * kPanel * 2, r, c, v);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(unit_full + a);
+            }
+            if (lane == 0) mbar_arrive(raw_empty + s);   // (after the last __syncwarp)
+        }
+        if (!ok) *s_fail = 1u;
+    } else {   // ---- epilogue
+        const int e0 = warp - 10, quarter = warp & 3, group = e0 >> 2;
+        float4* x = reinterpret_cast<float4*>(smem + L.exchange) + e0 * 256;
+        int it = 0;
+        for (int64_t t = first; t < q.tiles; t += step, ++it) {
+            const int buf = it & 1;
+            const int64_t r0 = t * kBlock + quarter * 32;
+            Share<T> share;
+            if (group * 32 < q.np) share.begin(q.out, r0, n0 + group * 32, 0, lane);
+            const bool ok = warp_all(mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail);
+            if (!ok) {
+                *s_fail = 1u;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * (kCols / 2) + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+            for (int c = group * 32; c < q.np; c += 64) {
+                float v[32];
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) {
+                    uint32_t w[32];
+                    __syncwarp();
+                    tmem_ld32(acc + p * q.np + c, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = p ? v[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
+                }
+                if (c + 64 >= q.np) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                }
+                if (c != group * 32) share.begin(q.out, r0, n0 + c, 0, lane);
+                share.end(q.out, x, v, lane);
+            }
+            if (group * 32 >= q.np && lane == 0) mbar_arrive(acc_empty + buf);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && *s_fail) atomicOr(&st->error, kErrTimeout);
+    if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
 // ------------------------------------------------------------------ plans --
@@ -824,6 +1182,34 @@ cudaError_t few_rows(const LinearCall& c, const Product& q, cudaStream_t s) {
     }
 }
 
+// The plan of a narrow layer; false where it is none.
+template <typename T>
+bool stream_plan(const LinearCall& c, int n_sms, Stream* q, int* smem) {
+    constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    if (c.inputs > kStreamMaxK || c.outputs > 4 * kStreamN<T> || !aligned16(c.x)) return false;
+    q->x = c.x;
+    q->weight = c.weight;
+    q->tiles = ceil_div(c.rows, kBlock);
+    q->k = (int)c.inputs;
+    q->panels = (int)ceil_div(c.inputs, kPanel);
+    q->blocks = (int)ceil_div(c.outputs, kStreamN<T>);
+    q->np = q->blocks > 1 ? kStreamN<T> : (int)ceil_div(c.outputs, 16) * 16;
+    q->vec = c.inputs % VecOf<T>::n == 0 && aligned16(c.weight);
+    // as many operands, then raw tiles in flight as fit
+    const auto fits = [&](int raws, int units) {
+        *smem = stream_smem(kPlanes, sizeof(T), q->k, q->panels, q->np, raws, units).bytes;
+        return *smem <= kStreamSmemMax;
+    };
+    for (int raws = 4; raws >= 1; --raws)
+        for (int units = raws > 1 ? 2 : 3; units >= 1; --units)
+            if (fits(raws, units) && (units == 2 || raws == 1)) {
+                q->raws = raws;
+                q->units = units;
+                return true;
+            }
+    return false;
+}
+
 template <typename T>
 cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
     const int64_t m = c.rows, k = c.inputs, n = c.outputs;
@@ -842,6 +1228,15 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
                                                                    : few_rows<T, 1>(c, q, s);
     }
     q.vec = vec4<T>(q);
+    Stream narrow{};
+    int smem = 0;
+    if (stream_plan<T>(c, n_sms, &narrow, &smem)) {
+        narrow.out = q;
+        const int64_t per = n_sms / narrow.blocks;
+        const int64_t grid = narrow.blocks * (narrow.tiles < per ? narrow.tiles : per);
+        return launch_pdl(k_linear_stream<T>, dim3((unsigned)grid), dim3(kStreamThreads),
+                          (size_t)smem, s, narrow, st);
+    }
     const Space sp = carve(ws, m, k, n, c.dtype);
     Matrix x, w;
     cudaError_t e = operand<T>(&x, c.x, nullptr, kActNone, m, k, sp.x, nullptr, s);
@@ -927,6 +1322,12 @@ cudaError_t prepare_linear() {
     e = prepare_three<float, 3, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256>();
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_linear_stream<float>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_linear_stream<__nv_bfloat16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
     return e;
 }
 
