@@ -27,16 +27,25 @@ constexpr int kBlock = 128;      // rows of a tile
 constexpr int kMaxPlanes = 3;
 
 // ------------------------------------------------------------ activation --
+// 1 / (1 + exp(-z)) by the PTX ISA's approximate base-2 exponential and reciprocal, with
+// subnormals flushed: a few ulps, and below 2^-125 (z < -87) zero.  Five instructions; without the
+// flush, and as a division, eleven.
+__device__ __forceinline__ float sigmoid_of(float z) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
 template <int kAct>
 __device__ __forceinline__ float act_of(float z) {
-    if (kAct == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
+    if (kAct == kActSilu) return z * sigmoid_of(z);
     if (kAct == kActRelu) return z > 0.0f ? z : 0.0f;
     return z;
 }
 template <int kAct>
 __device__ __forceinline__ float act_slope(float z) {
     if (kAct == kActSilu) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+        const float s = sigmoid_of(z);
         return s * (1.0f + z * (1.0f - s));
     }
     if (kAct == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
@@ -49,21 +58,18 @@ __device__ __forceinline__ float act_any(int act, float z) {
 }
 
 // ---------------------------------------------------------------- planes --
-// Two floats as three words of two bfloat16 each, whose sums they are (but for an infinity, which
-// leaves nothing over).
+// Two floats as three words of two bfloat16 each, whose sums they are (an infinity, or what rounds
+// to one, leaves NaNs over).
 __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ float rest_of(float v, float part) {
-    return fabsf(part) <= 3.3895314e38f ? v - part : 0.0f;
-}
 __device__ __forceinline__ void split3(float a, float b, uint32_t (&w)[3]) {
     w[0] = pair_bf16(a, b);
-    a = rest_of(a, low_of(w[0]));
-    b = rest_of(b, high_of(w[0]));
+    a -= low_of(w[0]);
+    b -= high_of(w[0]);
     w[1] = pair_bf16(a, b);
     w[2] = pair_bf16(a - low_of(w[1]), b - high_of(w[1]));
 }
@@ -727,11 +733,9 @@ k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k,
 // thread issues the MMAs, and eight warps finish the tile from tensor memory.
 // The weights are made into operands by every CTA once, and stay.
 //
-// In 32 bits the weights' planes lie below one another, [hi; mid; lo], so that a
-// plane of the rows takes one MMA against those that count: hi against all
-// three, mid against hi and mid, lo against hi.  Their sums in three ranges of
-// columns are hi hi, (hi mid + mid hi), (hi lo + mid mid + lo hi), so that what
-// the tensor cores truncate is relative to each; at most 128 of K, as there.
+// In 32 bits all six products go into one accumulator, hi hi last: what the
+// tensor cores truncate of the others is relative to their small sums, and of
+// hi hi there are at most 128 of K, as there.
 constexpr int kStreamThreads = 576;   // warps: copies, MMAs, eight of operands, eight of the epilogue
 constexpr int kStreamMaxK = 128;
 template <typename T>
@@ -768,10 +772,10 @@ constexpr int kStreamSmemMax = 227 * 1024;
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// Eight columns (16 bytes of bfloat16) of row `row`, the chunk'th of a 128-byte row, as planes.
+// Eight columns, 16 bytes of bfloat16 in each plane.
 template <int kPlanes>
-__device__ __forceinline__ void put_chunk(unsigned char* at, uint32_t plane_bytes, int row,
-                                          int chunk, const float (&v)[8]) {
+__device__ __forceinline__ void put_chunk(unsigned char* at, uint32_t plane_bytes,
+                                          const float (&v)[8]) {
     uint32_t w[4][3];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -782,7 +786,7 @@ __device__ __forceinline__ void put_chunk(unsigned char* at, uint32_t plane_byte
     }
 #pragma unroll
     for (int p = 0; p < kPlanes; ++p)
-        *reinterpret_cast<uint4*>(at + p * plane_bytes + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(at + p * plane_bytes) =
             make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
 }
 
@@ -790,7 +794,7 @@ template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    constexpr int kCols = sizeof(T) == 4 ? 512 : 256;   // tensor memory: two accumulators
+    constexpr int kCols = sizeof(T) == 4 ? 128 : 256;   // tensor memory: two accumulators
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     const StreamSmem L = stream_smem(kPlanes, sizeof(T), q.k, q.panels, q.np, q.raws, q.units);
@@ -836,7 +840,9 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             if (n0 + r < q.out.n && n > 0)
                 load8(static_cast<const T*>(q.weight) + (int64_t)(n0 + r) * q.k + c * 8, n,
                       q.vec && n == 8, v);
-            put_chunk<kPlanes>(smem + L.weight + (c >> 3) * L.weight_panel, q.np * 128, r, c & 7, v);
+            put_chunk<kPlanes>(smem + L.weight + (c >> 3) * L.weight_panel + r * 128 +
+                                   (((c & 7) ^ (r & 7)) << 4),
+                               q.np * 128, v);
         }
     }
     fence_async_smem();
@@ -877,11 +883,32 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) |
                                     ((uint32_t)(kBlock >> 4) << 24);
             const uint32_t np = (uint32_t)q.np;
-            uint32_t idesc[kPlanes];   // of the weights' first kPlanes - p planes
-#pragma unroll
-            for (int p = 0; p < kPlanes; ++p)
-                idesc[p] = idesc0 | ((np * (uint32_t)(kPlanes - p) >> 3) << 17);
+            const uint32_t idesc = idesc0 | ((np >> 3) << 17);
             const uint32_t base = smem_u32(smem);
+            // a panel's products: in 32 bits all but hi hi (`small`), or hi hi
+            auto multiply = [&](uint32_t unit, uint32_t weight, uint32_t d, int ends, bool more,
+                                bool small) {
+                uint64_t a[kPlanes], b[kPlanes];
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) {
+                    a[p] = desc_sw128(unit + p * kBlock * kPanel * 2, 16);
+                    b[p] = desc_sw128(weight + p * np * kPanel * 2, 16);
+                }
+                for (int e = 0; e < ends; ++e) {
+                    const uint32_t off = 32u * e >> 4, acc = more || e > 0;
+                    if constexpr (kPlanes == 3) {
+                        if (small) {
+                            mma_f16(d, a[2] + off, b[0] + off, idesc, acc);
+                            mma_f16(d, a[1] + off, b[1] + off, idesc, 1);
+                            mma_f16(d, a[0] + off, b[2] + off, idesc, 1);
+                            mma_f16(d, a[1] + off, b[0] + off, idesc, 1);
+                            mma_f16(d, a[0] + off, b[1] + off, idesc, 1);
+                            continue;
+                        }
+                    }
+                    mma_f16(d, a[0] + off, b[0] + off, idesc, acc);
+                }
+            };
             int u = 0, it = 0;
             bool ok = true;
             for (int64_t t = first; t < q.tiles && ok; t += step, ++it) {
@@ -889,26 +916,25 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const uint32_t d = tmem + buf * (kCols / 2);
                 ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
                 if (!ok) break;
+                // (in 32 bits every panel of the tile has its unit)
                 for (int h = 0; h < q.panels; ++h, ++u) {
                     const int s = u % q.units;
                     ok = mbar_wait(unit_full + s, (u / q.units) & 1) && !*s_fail;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = base + L.unit + s * L.unit_bytes;
-                    const uint64_t b = desc_sw128(base + L.weight + h * L.weight_panel, 16);
-                    uint64_t a[kPlanes];
-#pragma unroll
-                    for (int p = 0; p < kPlanes; ++p)
-                        a[p] = desc_sw128(at + p * kBlock * kPanel * 2, 16);
-                    const int ends = min(4, steps16 - 4 * h);
-                    for (int e = 0; e < ends; ++e) {
-                        const uint32_t off = 32u * e >> 4;
-                        mma_f16(d, a[0] + off, b + off, idesc[0], h > 0 || e > 0);
-#pragma unroll
-                        for (int p = 1; p < kPlanes; ++p)
-                            mma_f16(d + p * np, a[p] + off, b + off, idesc[p], 1);
+                    multiply(base + L.unit + s * L.unit_bytes, base + L.weight + h * L.weight_panel,
+                             d, min(4, steps16 - 4 * h), h > 0, kPlanes == 3);
+                    if (kPlanes == 1) mma_commit(unit_empty + s);
+                }
+                if (kPlanes == 3 && ok) {
+                    u -= q.panels;
+                    for (int h = 0; h < q.panels; ++h, ++u) {
+                        const int s = u % q.units;
+                        multiply(base + L.unit + s * L.unit_bytes,
+                                 base + L.weight + h * L.weight_panel, d, min(4, steps16 - 4 * h),
+                                 true, false);
+                        mma_commit(unit_empty + s);
                     }
-                    mma_commit(unit_empty + s);
                 }
                 if (ok) mma_commit(acc_full + buf);
             }
@@ -935,15 +961,27 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 if (!ok) break;
                 unsigned char* unit = smem + L.unit + a * L.unit_bytes;
                 const int chunks = min(8, 2 * steps16 - 8 * h);
-                // (rows behind the last keep what they held: their sums are not stored)
-#pragma unroll 4
-                for (int i = mine; i < kBlock * 8; i += 256) {
-                    const int r = i >> 3, c = i & 7;
-                    if (c >= chunks || r >= rows) continue;
-                    float v[8];
-                    const int col = h * kPanel + c * 8, k = q.k - col;
-                    load8(tile + r * q.k + col, k, q.vec && k >= 8, v);
-                    put_chunk<kPlanes>(unit, kBlock * kPanel * 2, r, c, v);
+                // a thread has a chunk of every 32nd row (rows behind the last keep what they
+                // held: their sums are not stored)
+                const int c = mine & 7, r0 = mine >> 3, col = h * kPanel + c * 8;
+                const T* src = tile + r0 * q.k + col;
+                unsigned char* dst = unit + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+                if (q.vec && q.k - col >= 8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (r0 + 32 * i < rows) {
+                            float v[8];
+                            load8(src + 32 * i * q.k, 8, true, v);
+                            put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v);
+                        }
+                } else if (c < chunks) {
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i)
+                        if (r0 + 32 * i < rows) {
+                            float v[8];
+                            load8(src + 32 * i * q.k, q.k - col, false, v);
+                            put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v);
+                        }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -971,15 +1009,13 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 #pragma unroll 1
             for (int c = group * 32; c < q.np; c += 64) {
                 float v[32];
-#pragma unroll
-                for (int p = 0; p < kPlanes; ++p) {
+                {
                     uint32_t w[32];
                     __syncwarp();
-                    tmem_ld32(acc + p * q.np + c, w);
+                    tmem_ld32(acc + c, w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        v[e] = p ? v[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(w[e]);
                 }
                 if (c + 64 >= q.np) {
                     tc_fence_before();
@@ -1200,9 +1236,11 @@ bool stream_plan(const LinearCall& c, int n_sms, Stream* q, int* smem) {
         *smem = stream_smem(kPlanes, sizeof(T), q->k, q->panels, q->np, raws, units).bytes;
         return *smem <= kStreamSmemMax;
     };
-    for (int raws = 4; raws >= 1; --raws)
-        for (int units = raws > 1 ? 2 : 3; units >= 1; --units)
-            if (fits(raws, units) && (units == 2 || raws == 1)) {
+    // (in 32 bits a tile's panels are in use together)
+    const int least = kPlanes == 3 ? q->panels : 1;
+    for (int units = 2; units >= least; --units)
+        for (int raws = 4; raws >= (units > least ? 2 : 1); --raws)
+            if (fits(raws, units)) {
                 q->raws = raws;
                 q->units = units;
                 return true;
