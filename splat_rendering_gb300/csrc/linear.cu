@@ -335,12 +335,10 @@ struct Share {
         }
     }
 
+    // `bias`: of its four columns
     template <int kAct>
     __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
-                                        int lane) {
-        float bias[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bias[e] = q.bias && e < n ? q.bias[c + e] : 0.0f;
+                                        const float (&bias)[4], int lane) {
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -352,21 +350,31 @@ struct Share {
         const int cq = lane & 7, rq = lane >> 3;
         const int64_t step = 4 * q.n;
         if (q.vec) {
+            // (all loads, then all stores: the compiler keeps a load behind a store before it)
+            float z[8][4];
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
                 const int r = 4 * h + rq;
                 const float4 u = x[r * 8 + (cq ^ (r & 7))];
-                const float z[4] = {plus(u.x, bias[0]), plus(u.y, bias[1]), plus(u.z, bias[2]),
-                                    plus(u.w, bias[3])};
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = act_of<kAct>(z[e]);
-                if (4 * h < rows) {
-                    if (pre) *reinterpret_cast<Raw*>(pre + h * step) = Four<T>::pack(z);
-                    if (q.residual) Four<T>::add(residual[h], y);
-                    *reinterpret_cast<Raw*>(out + h * step) = Four<T>::pack(y);
-                }
+                z[h][0] = plus(u.x, bias[0]);
+                z[h][1] = plus(u.y, bias[1]);
+                z[h][2] = plus(u.z, bias[2]);
+                z[h][3] = plus(u.w, bias[3]);
             }
+            if (pre) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    if (4 * h < rows) *reinterpret_cast<Raw*>(pre + h * step) = Four<T>::pack(z[h]);
+            }
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
+                if (q.residual) Four<T>::add(residual[h], z[h]);
+            }
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+                if (4 * h < rows) *reinterpret_cast<Raw*>(out + h * step) = Four<T>::pack(z[h]);
             return;
         }
         const T* skip = q.residual ? static_cast<const T*>(q.residual) + at : nullptr;
@@ -391,10 +399,10 @@ struct Share {
         }
     }
     __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
-                                        int lane) {
-        if (q.act == kActSilu) end<kActSilu>(q, x, v, lane);
-        else if (q.act == kActRelu) end<kActRelu>(q, x, v, lane);
-        else end<kActNone>(q, x, v, lane);
+                                        const float (&bias)[4], int lane) {
+        if (q.act == kActSilu) end<kActSilu>(q, x, v, bias, lane);
+        else if (q.act == kActRelu) end<kActRelu>(q, x, v, bias, lane);
+        else end<kActNone>(q, x, v, bias, lane);
     }
 };
 
@@ -577,8 +585,12 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             auto emit = [&](const float (&v)[32], int col) {
                 Share<T> share;
                 share.begin(q, r0, (int64_t)j * kN + col, base, lane);
-                if (kAMn || kBMn) share.template end<kActNone>(q, x, v, lane);
-                else share.end(q, x, v, lane);
+                float bias[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    bias[e] = q.bias && e < share.n ? q.bias[share.c + e] : 0.0f;
+                if (kAMn || kBMn) share.template end<kActNone>(q, x, v, bias, lane);
+                else share.end(q, x, v, bias, lane);
             };
             bool ok = true;
             if constexpr (kPlanes == 3) {
@@ -733,9 +745,13 @@ k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k,
 // thread issues the MMAs, and eight warps finish the tile from tensor memory.
 // The weights are made into operands by every CTA once, and stay.
 //
-// In 32 bits all six products go into one accumulator, hi hi last: what the
-// tensor cores truncate of the others is relative to their small sums, and of
-// hi hi there are at most 128 of K, as there.
+// In 32 bits the weights' planes lie below one another, [hi; mid; lo], so that a
+// plane of the rows takes one MMA against those that count: hi against all
+// three, mid against hi and mid, lo against hi.  Their sums in three ranges of
+// columns are hi hi, (hi mid + mid hi), (hi lo + mid mid + lo hi), so that what
+// the tensor cores truncate is relative to each, of at most 128 of K, as there.
+// (Six MMAs into one accumulator, hi hi last, are as exact; an MMA takes some
+// 140 cycles whatever its columns, and 24 of them were 80 % of a tile's time.)
 constexpr int kStreamThreads = 576;   // warps: copies, MMAs, eight of operands, eight of the epilogue
 constexpr int kStreamMaxK = 128;
 template <typename T>
@@ -749,6 +765,7 @@ struct Stream {
     int np, blocks;        // outputs of a block (a multiple of 16), blocks
     int raws, units;       // raw tiles, operand panels in flight
     bool vec;              // a row of x, and of the weight, is whole 16-byte vectors
+    bool skip;             // there is a residual, on 16 bytes, and one block of outputs
     Product out;           // m, n, bias, ..., vec
 };
 struct StreamSmem {
@@ -768,8 +785,12 @@ __host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, i
     s.bytes = s.bars + 256 + 1024;
     return s;
 }
-constexpr int kStreamSmemMax = 227 * 1024;
+constexpr int kStreamSmemMax = 227 * 1024 - 512;   // (and the bias)
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    if (bytes)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
 // Eight columns, 16 bytes of bfloat16 in each plane.
@@ -794,8 +815,9 @@ template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    constexpr int kCols = sizeof(T) == 4 ? 128 : 256;   // tensor memory: two accumulators
+    constexpr int kCols = sizeof(T) == 4 ? 512 : 256;   // tensor memory: two accumulators
     extern __shared__ unsigned char raw_smem[];
+    __shared__ __align__(16) float s_bias[128];
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     const StreamSmem L = stream_smem(kPlanes, sizeof(T), q.k, q.panels, q.np, q.raws, q.units);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
@@ -829,6 +851,8 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     if (warp == 1) tmem_alloc(s_taddr, kCols);
     pdl_next();
     pdl_begin();
+    if (tid < 128)
+        s_bias[tid] = q.out.bias && n0 + tid < q.out.n ? q.out.bias[n0 + tid] : 0.0f;
     {   // the weights, zeros below and behind them
         const int chunks = steps16 * 2, total = q.np * chunks;
         for (int t = tid; t < total; t += kStreamThreads) {
@@ -864,6 +888,12 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const unsigned char* src =
                     static_cast<const unsigned char*>(q.x) + t * kBlock * q.k * (int64_t)sizeof(T);
                 unsigned char* dst = smem + L.raw + s * L.raw_bytes;
+                if (q.skip) {   // its residual is on its way to the L2 before the epilogue asks
+                    const uint32_t row = (uint32_t)(q.out.n * (int)sizeof(T));
+                    prefetch_l2(static_cast<const unsigned char*>(q.out.residual) +
+                                    t * kBlock * (int64_t)row,
+                                (uint32_t)(left < kBlock ? left : kBlock) * row & ~15u);
+                }
                 const uint32_t bulk = bytes & ~15u;   // the last rows need not end on 16 bytes
                 for (uint32_t e = bulk / sizeof(T); e < bytes / sizeof(T); ++e)
                     reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(src)[e];
@@ -883,32 +913,11 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) |
                                     ((uint32_t)(kBlock >> 4) << 24);
             const uint32_t np = (uint32_t)q.np;
-            const uint32_t idesc = idesc0 | ((np >> 3) << 17);
-            const uint32_t base = smem_u32(smem);
-            // a panel's products: in 32 bits all but hi hi (`small`), or hi hi
-            auto multiply = [&](uint32_t unit, uint32_t weight, uint32_t d, int ends, bool more,
-                                bool small) {
-                uint64_t a[kPlanes], b[kPlanes];
+            uint32_t idesc[kPlanes];   // against the weights' first kPlanes - p planes
 #pragma unroll
-                for (int p = 0; p < kPlanes; ++p) {
-                    a[p] = desc_sw128(unit + p * kBlock * kPanel * 2, 16);
-                    b[p] = desc_sw128(weight + p * np * kPanel * 2, 16);
-                }
-                for (int e = 0; e < ends; ++e) {
-                    const uint32_t off = 32u * e >> 4, acc = more || e > 0;
-                    if constexpr (kPlanes == 3) {
-                        if (small) {
-                            mma_f16(d, a[2] + off, b[0] + off, idesc, acc);
-                            mma_f16(d, a[1] + off, b[1] + off, idesc, 1);
-                            mma_f16(d, a[0] + off, b[2] + off, idesc, 1);
-                            mma_f16(d, a[1] + off, b[0] + off, idesc, 1);
-                            mma_f16(d, a[0] + off, b[1] + off, idesc, 1);
-                            continue;
-                        }
-                    }
-                    mma_f16(d, a[0] + off, b[0] + off, idesc, acc);
-                }
-            };
+            for (int p = 0; p < kPlanes; ++p)
+                idesc[p] = idesc0 | ((np * (uint32_t)(kPlanes - p) >> 3) << 17);
+            const uint32_t base = smem_u32(smem);
             int u = 0, it = 0;
             bool ok = true;
             for (int64_t t = first; t < q.tiles && ok; t += step, ++it) {
@@ -916,25 +925,26 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const uint32_t d = tmem + buf * (kCols / 2);
                 ok = mbar_wait(acc_empty + buf, ((it >> 1) & 1) ^ 1) && !*s_fail;
                 if (!ok) break;
-                // (in 32 bits every panel of the tile has its unit)
                 for (int h = 0; h < q.panels; ++h, ++u) {
                     const int s = u % q.units;
                     ok = mbar_wait(unit_full + s, (u / q.units) & 1) && !*s_fail;
                     if (!ok) break;
                     tc_fence_after();
-                    multiply(base + L.unit + s * L.unit_bytes, base + L.weight + h * L.weight_panel,
-                             d, min(4, steps16 - 4 * h), h > 0, kPlanes == 3);
-                    if (kPlanes == 1) mma_commit(unit_empty + s);
-                }
-                if (kPlanes == 3 && ok) {
-                    u -= q.panels;
-                    for (int h = 0; h < q.panels; ++h, ++u) {
-                        const int s = u % q.units;
-                        multiply(base + L.unit + s * L.unit_bytes,
-                                 base + L.weight + h * L.weight_panel, d, min(4, steps16 - 4 * h),
-                                 true, false);
-                        mma_commit(unit_empty + s);
+                    const uint32_t at = base + L.unit + s * L.unit_bytes;
+                    const uint64_t b = desc_sw128(base + L.weight + h * L.weight_panel, 16);
+                    uint64_t a[kPlanes];
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p)
+                        a[p] = desc_sw128(at + p * kBlock * kPanel * 2, 16);
+                    const int ends = min(4, steps16 - 4 * h);
+                    for (int e = 0; e < ends; ++e) {
+                        const uint32_t off = 32u * e >> 4;
+                        mma_f16(d, a[0] + off, b + off, idesc[0], h > 0 || e > 0);
+#pragma unroll
+                        for (int p = 1; p < kPlanes; ++p)
+                            mma_f16(d + p * np, a[p] + off, b + off, idesc[p], 1);
                     }
+                    mma_commit(unit_empty + s);
                 }
                 if (ok) mma_commit(acc_full + buf);
             }
@@ -967,13 +977,12 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const T* src = tile + r0 * q.k + col;
                 unsigned char* dst = unit + r0 * 128 + ((c ^ (r0 & 7)) << 4);
                 if (q.vec && q.k - col >= 8) {
+                    float v[4][8];   // (all loads, then all stores, as there)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) load8(src + 32 * i * q.k, 8, true, v[i]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (r0 + 32 * i < rows) {
-                            float v[8];
-                            load8(src + 32 * i * q.k, 8, true, v);
-                            put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v);
-                        }
+                        put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v[i]);
                 } else if (c < chunks) {
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i)
@@ -1009,13 +1018,15 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 #pragma unroll 1
             for (int c = group * 32; c < q.np; c += 64) {
                 float v[32];
-                {
+#pragma unroll
+                for (int p = 0; p < kPlanes; ++p) {
                     uint32_t w[32];
                     __syncwarp();
-                    tmem_ld32(acc + c, w);
+                    tmem_ld32(acc + p * q.np + c, w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(w[e]);
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = p ? v[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
                 }
                 if (c + 64 >= q.np) {
                     tc_fence_before();
@@ -1023,7 +1034,9 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                     if (lane == 0) mbar_arrive(acc_empty + buf);
                 }
                 if (c != group * 32) share.begin(q.out, r0, n0 + c, 0, lane);
-                share.end(q.out, x, v, lane);
+                const float4 b = *reinterpret_cast<const float4*>(s_bias + c + 4 * (lane & 7));
+                const float bias[4] = {b.x, b.y, b.z, b.w};
+                share.end(q.out, x, v, bias, lane);
             }
             if (group * 32 >= q.np && lane == 0) mbar_arrive(acc_empty + buf);
         }
@@ -1236,10 +1249,8 @@ bool stream_plan(const LinearCall& c, int n_sms, Stream* q, int* smem) {
         *smem = stream_smem(kPlanes, sizeof(T), q->k, q->panels, q->np, raws, units).bytes;
         return *smem <= kStreamSmemMax;
     };
-    // (in 32 bits a tile's panels are in use together)
-    const int least = kPlanes == 3 ? q->panels : 1;
-    for (int units = 2; units >= least; --units)
-        for (int raws = 4; raws >= (units > least ? 2 : 1); --raws)
+    for (int units = 2; units >= 1; --units)
+        for (int raws = 4; raws >= units; --raws)
             if (fits(raws, units)) {
                 q->raws = raws;
                 q->units = units;
@@ -1270,6 +1281,7 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
     int smem = 0;
     if (stream_plan<T>(c, n_sms, &narrow, &smem)) {
         narrow.out = q;
+        narrow.skip = q.residual && aligned16(q.residual) && narrow.blocks == 1;
         const int64_t per = n_sms / narrow.blocks;
         const int64_t grid = narrow.blocks * (narrow.tiles < per ? narrow.tiles : per);
         return launch_pdl(k_linear_stream<T>, dim3((unsigned)grid), dim3(kStreamThreads),
