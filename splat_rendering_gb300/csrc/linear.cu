@@ -244,6 +244,15 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// One lane of a whole warp, the compiler knowing that it is one: MMAs issued by it follow each
+// other at their own rate, while those of a lane that a comparison chose take 105 cycles each
+// (measured: M = 128, N = 64: 76 cycles, with A in tensor memory 49; N = 16: 57 and 35).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void expect_bytes(uint64_t* mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(mbar)),
                  "r"(bytes)
@@ -829,7 +838,8 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     uint64_t* drain = acc_empty + 2;
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* s_fail = s_taddr + 1;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the same in a warp)
     const int block = blockIdx.x % q.blocks, first = blockIdx.x / q.blocks;
     const int step = gridDim.x / q.blocks;
     const int n0 = block * kStreamN<T>;
@@ -875,7 +885,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
     if (warp == 0) {
-        if (lane == 0) {   // ---- raw tiles
+        if (elect_one()) {   // ---- raw tiles
             int n = 0;
             bool ok = true;
             for (int64_t t = first; t < q.tiles; t += step, ++n) {
@@ -909,7 +919,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {   // ---- MMAs
+        if (elect_one()) {   // ---- MMAs
             const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) |
                                     ((uint32_t)(kBlock >> 4) << 24);
             const uint32_t np = (uint32_t)q.np;
