@@ -447,7 +447,8 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     uint64_t* drain = acc_empty + 2;
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* s_fail = s_taddr + 1;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the same in a warp)
     if (tid == 0) {
         for (int s = 0; s < L::stages; ++s) {
             mbar_init(full + s);
@@ -480,7 +481,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
         *k1 = (int)((int64_t)(*part + 1) * q.panels / q.splits);
     };
     if (warp == 0) {
-        if (lane == 0) {   // ---- copies
+        if (elect_one()) {   // ---- copies
             int n = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -524,7 +525,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {   // ---- MMAs
+        if (elect_one()) {   // ---- MMAs
             constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                        (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                                        ((uint32_t)(kN >> 3) << 17) |
