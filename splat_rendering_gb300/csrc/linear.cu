@@ -679,28 +679,49 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     if (warp == 1) tmem_dealloc(tmem, 2 * kAcc);
 }
 
-// The parts of a product added in their order, and finished.
-template <typename T>
+// The parts of a product added in a fixed order, and finished: a thread has four columns, of few
+// parts all of them, of many (kLanes = 64) every 64th, which the block then adds up.
+template <typename T, int kLanes>
 __global__ void __launch_bounds__(256)
 k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part) {
+    constexpr int kPer = 256 / kLanes;   // groups of four columns of a block
+    __shared__ float4 s_sum[8][kLanes > 1 ? kPer : 1];
     pdl_begin();
     const int64_t size = q.m * q.n, groups = (q.n + 3) / 4, total = q.m * groups;
-    for (int64_t g = blockIdx.x * 256ll + threadIdx.x; g < total; g += gridDim.x * 256ll) {
-        const int64_t r = g / groups, c = (g - r * groups) * 4, at = r * q.n + c;
-        const int n = (int)(q.n - c < 4 ? q.n - c : 4);
+    const int mine = threadIdx.x % kPer, from = threadIdx.x / kPer;
+    for (int64_t g0 = (int64_t)blockIdx.x * kPer; g0 < total; g0 += (int64_t)gridDim.x * kPer) {
+        const int64_t g = g0 + mine, r = g / groups, c = (g - r * groups) * 4, at = r * q.n + c;
+        const int n = g < total ? (int)(q.n - c < 4 ? q.n - c : 4) : 0;
         float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if ((q.n & 3) == 0) {   // (the workspace is aligned)
+        if ((q.n & 3) == 0 && n > 0) {   // (the workspace is aligned)
 #pragma unroll 8
-            for (int s = 0; s < q.splits; ++s) {
+            for (int s = from; s < q.splits; s += kLanes) {
                 const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * size + at));
                 z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
             }
         } else {
 #pragma unroll 4
-            for (int s = 0; s < q.splits; ++s)
+            for (int s = from; s < q.splits; s += kLanes)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (e < n) z[e] += part[s * size + at + e];
+        }
+        if (kLanes > 1) {   // the warp's (its lanes kPer apart), then the block's
+#pragma unroll
+            for (int d = kPer; d < 32; d *= 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] += __shfl_xor_sync(0xffffffffu, z[e], d);
+            __syncthreads();
+            if ((threadIdx.x & 31) < kPer)
+                s_sum[threadIdx.x >> 5][kLanes > 1 ? mine : 0] = make_float4(z[0], z[1], z[2], z[3]);
+            __syncthreads();
+            if (from > 0) continue;
+            for (int e = 0; e < 4; ++e) z[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float4 u = s_sum[w][kLanes > 1 ? mine : 0];
+                z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
+            }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -1060,6 +1081,427 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
+// --------------------------------------------- narrow layers, gradients --
+// All gradients of a narrow layer in one pass over dy, z and x: a persistent CTA
+// per SM, tiles of 128 rows.  Eight warps make dz and x into operands (and add
+// up dz's columns), one thread issues the MMAs, eight warps finish dx.  dz's
+// tile, 128 rows of 128 bytes a panel, is a K-major left operand of dx = dz W
+// (its rows are rows) and, the same bytes, an MN-major one of dW = dz^T x (its
+// rows are the contraction).  dW stays in the CTA; k_linear_join adds up the
+// CTAs' sums in their order.
+//
+// In 32 bits the planes of dz are two groups of one left operand [hi; mid] of
+// dW, those of x three of the right one, so that one MMA makes six products
+// (lo mid among them, in rows that are not read); lo hi is a second one, into
+// the columns of hi lo.  They are drained every tile (128 of K) into registers:
+// the rows of hi, and those of mid, are parts of their own.  dx as in the
+// forward kernel.
+constexpr int kBackThreads = 544;   // warps: MMAs, eight of operands, eight of the epilogue
+template <typename T>
+constexpr int kBackSide = sizeof(T) == 4 ? 64 : 128;   // inputs and outputs of a layer
+constexpr int kBackAhead = 3;                          // tiles that are on their way to the L2
+
+struct Narrow {
+    const void *grad_y, *pre, *x, *weight;
+    int64_t rows, tiles;
+    int k, n;              // inputs, outputs
+    bool vec_n, vec_k;     // rows of n (k) elements are whole 16-byte vectors
+    bool ahead;            // the tensors begin on 16 bytes
+    bool want_x, want_w;
+    float* parts;          // [parts of all CTAs][n][k]
+    float* sums;           // [CTA][n]; may be NULL
+    Product out;           // of dx
+};
+template <typename T>
+struct BackSmem {
+    static constexpr int planes = sizeof(T) == 4 ? 3 : 1;
+    static constexpr int panels = kBackSide<T> / kPanel;
+    static constexpr int panel = kBlock * kPanel * 2;          // of one plane
+    static constexpr int operand = planes * panels * panel;    // [panel][plane]
+    static constexpr int unit = 2 * operand;                   // dz, x
+    static constexpr int weight_panel = kBackSide<T> * kPanel * 2;
+    static constexpr int weight = 2 * unit;                    // [panel of inputs][plane]
+    static constexpr int exchange = weight + planes * panels * weight_panel;
+    // 32 bits: of four warps, which take turns with the other four
+    static constexpr int exchange_bytes = sizeof(T) == 4 ? 8 * 1024 : 8 * 4096;
+    static constexpr int bars = exchange + exchange_bytes;
+    static constexpr int bytes = bars + 256 + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory of a narrow layer's gradients");
+};
+
+// A tile's operand from its rows of `cols` elements: dz where kAct is an activation and `pre`
+// given, its columns added to `sum`.  A thread has a chunk of eight columns (c of 0 .. 7 in every
+// panel) of every 32nd row.  Rows behind the last, and columns up to the next 16, are zeros.
+template <typename T, int kAct, bool kSum>
+__device__ __forceinline__ void make_operand(unsigned char* unit, const T* src, const T* pre,
+                                             int rows, int cols, bool vec, int mine,
+                                             float (&sum)[kBackSide<T> / kPanel][8]) {
+    using L = BackSmem<T>;
+    constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight together
+    const int c = mine & 7, r0 = mine >> 3;
+#pragma unroll
+    for (int h = 0; h < L::panels; ++h) {
+        const int col = h * kPanel + c * 8;
+        if (col >= (cols + 15) / 16 * 16) break;
+        const int n = cols - col;
+        unsigned char* dst = unit + h * L::planes * L::panel + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+#pragma unroll
+        for (int i0 = 0; i0 < 4; i0 += kBatch) {
+            float v[kBatch][8], z[kBatch][8];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + 32 * (i0 + i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = z[i][e] = 0.0f;
+                if (r < rows && n > 0) {
+                    load8(src + (int64_t)r * cols + col, n, vec && n >= 8, v[i]);
+                    if (kAct != kActNone)
+                        load8(pre + (int64_t)r * cols + col, n, vec && n >= 8, z[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (kAct == kActRelu) v[i][e] = z[i][e] > 0.0f ? v[i][e] : 0.0f;
+                    if (kAct == kActSilu) v[i][e] *= act_slope<kActSilu>(z[i][e]);
+                    if (kSum) sum[h][e] += v[i][e];
+                }
+                put_chunk<L::planes>(dst + 32 * (i0 + i) * 128, L::panel, v[i]);
+            }
+        }
+    }
+}
+
+template <typename T, int kAct>
+__global__ void __launch_bounds__(kBackThreads, 1)
+k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
+    using L = BackSmem<T>;
+    constexpr int kPlanes = L::planes;
+    constexpr bool kSplit = kPlanes == 3;
+    constexpr uint32_t kDw = kSplit ? 192 : 256;   // columns: dx below, dW from here
+    extern __shared__ unsigned char raw_smem[];
+    unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+    uint64_t* unit_full = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint64_t* unit_empty = unit_full + 2;
+    uint64_t* dx_full = unit_empty + 2;
+    uint64_t* dx_empty = dx_full + 2;
+    uint64_t* dw_full = dx_empty + 2;
+    uint64_t* dw_empty = dw_full + 1;
+    uint64_t* drain = dw_empty + 1;
+    uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile uint32_t* s_fail = s_taddr + 1;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the same in a warp)
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init_n(unit_full + s, 8);
+            mbar_init(unit_empty + s);
+            mbar_init(dx_full + s);
+            mbar_init_n(dx_empty + s, 8);
+        }
+        mbar_init(dw_full);
+        mbar_init_n(dw_empty, 8);
+        mbar_init(drain);
+        *s_fail = 0u;
+    }
+    if (warp == 0) tmem_alloc(s_taddr, 512);
+    pdl_next();
+    pdl_begin();
+    if (q.want_x) {   // W, rows of outputs: an MN-major operand; zeros in the rows up to the next 16
+        const int rows = (q.n + 15) / 16 * 16, chunks = (q.k + 7) / 8;
+        for (int t = tid; t < rows * chunks; t += kBackThreads) {
+            const int r = t / chunks, c = t % chunks, n = q.k - c * 8;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            if (r < q.n)
+                load8(static_cast<const T*>(q.weight) + r * q.k + c * 8, n, q.vec_k && n >= 8, v);
+            put_chunk<kPlanes>(smem + L::weight + (c >> 3) * kPlanes * L::weight_panel + r * 128 +
+                                   (((c & 7) ^ (r & 7)) << 4),
+                               L::weight_panel, v);
+        }
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_taddr;
+    const int first = blockIdx.x, step = gridDim.x;
+    if (warp == 0) {
+        if (elect_one()) {   // ---- MMAs
+            constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                                       ((uint32_t)(kBlock >> 4) << 24);   // B MN-major
+            constexpr uint32_t kAMn = 1u << 15;
+            const uint32_t base = smem_u32(smem);
+            const uint32_t k16 = (uint32_t)(q.k + 15) / 16 * 16;
+            const int steps_n = (q.n + 15) / 16;
+            int u = 0;
+            bool ok = true;
+            for (int64_t t = first; t < q.tiles; t += step, ++u) {
+                const int s = u & 1;
+                ok = mbar_wait(unit_full + s, (u >> 1) & 1) && !*s_fail;
+                if (!ok) break;
+                const uint32_t dz = base + s * L::unit, x = dz + L::operand;
+                const uint32_t w = base + L::weight;
+                if (q.want_x) {
+                    // (one accumulator in 32 bits, two in 16)
+                    const int buf = kSplit ? 0 : s, turn = kSplit ? u : u >> 1;
+                    ok = mbar_wait(dx_empty + buf, (turn & 1) ^ 1) && !*s_fail;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * 128;
+                    const uint64_t b = desc_sw128(w, L::weight_panel);
+                    for (int e = 0; e < steps_n; ++e) {
+                        const uint32_t at = dz + (e >> 2) * kPlanes * L::panel + (e & 3) * 32;
+                        const uint64_t be = b + (2048u * e >> 4);
+                        if constexpr (kSplit) {
+                            mma_f16(d, desc_sw128(at, 16), be, kBase | (192u >> 3 << 17), e > 0);
+                            mma_f16(d + 64, desc_sw128(at + L::panel, 16), be,
+                                    kBase | (128u >> 3 << 17), 1);
+                            mma_f16(d + 128, desc_sw128(at + 2 * L::panel, 16), be,
+                                    kBase | (64u >> 3 << 17), 1);
+                        } else {
+                            mma_f16(d, desc_sw128(at, 16), be, kBase | (k16 >> 3 << 17), e > 0);
+                        }
+                    }
+                    mma_commit(dx_full + buf);
+                }
+                if (q.want_w) {
+                    if (kSplit) {
+                        ok = mbar_wait(dw_empty, (u & 1) ^ 1) && !*s_fail;
+                        if (!ok) break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + kDw;
+                    const uint64_t a = desc_sw128(dz, L::panel), b = desc_sw128(x, L::panel);
+                    const uint64_t lo = desc_sw128(dz + 2 * L::panel, L::panel);
+                    for (int e = 0; e < kBlock / 16; ++e) {
+                        const uint32_t off = 2048u * e >> 4;
+                        if constexpr (kSplit) {
+                            mma_f16(d, a + off, b + off, kBase | kAMn | (192u >> 3 << 17), e > 0);
+                            mma_f16(d + 128, lo + off, b + off, kBase | kAMn | (64u >> 3 << 17), 1);
+                        } else {
+                            mma_f16(d, a + off, b + off, kBase | kAMn | (k16 >> 3 << 17),
+                                    u > 0 || e > 0);
+                        }
+                    }
+                    if (kSplit || t + step >= q.tiles) mma_commit(dw_full);
+                }
+                mma_commit(unit_empty + s);
+            }
+            if (!ok) {
+                *s_fail = 1u;
+                mma_commit(drain);
+                mbar_wait(drain, 0);
+            }
+        }
+    } else if (warp < 9) {   // ---- operands
+        const int mine = tid - 32;
+        float sum[L::panels][8], none[L::panels][8];
+#pragma unroll
+        for (int h = 0; h < L::panels; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[h][e] = none[h][e] = 0.0f;
+        // a tile's tensors, on their way to the L2
+        auto fetch = [&](int64_t t) {
+            if (t >= q.tiles) return;
+            const int64_t left = q.rows - t * kBlock;
+            const uint32_t rows = (uint32_t)(left < kBlock ? left : kBlock);
+            const auto one = [&](const void* p, int cols) {
+                prefetch_l2(static_cast<const T*>(p) + t * kBlock * cols,
+                            rows * cols * (uint32_t)sizeof(T) & ~15u);
+            };
+            one(q.grad_y, q.n);
+            if (kAct != kActNone) one(q.pre, q.n);
+            if (q.want_w) one(q.x, q.k);
+        };
+        if (q.ahead && warp == 1 && elect_one())
+            for (int a = 1; a < kBackAhead; ++a) fetch(first + (int64_t)a * step);
+        int u = 0;
+        bool ok = true;
+        for (int64_t t = first; t < q.tiles; t += step, ++u) {
+            const int s = u & 1;
+            ok = warp_all(mbar_wait(unit_empty + s, ((u >> 1) & 1) ^ 1) && !*s_fail);
+            if (!ok) break;
+            const int64_t r0 = t * kBlock, left = q.rows - r0;
+            const int rows = (int)(left < kBlock ? left : kBlock);
+            unsigned char* unit = smem + s * L::unit;
+            if (q.ahead && warp == 1 && elect_one()) fetch(t + (int64_t)kBackAhead * step);
+            make_operand<T, kAct, true>(unit, static_cast<const T*>(q.grad_y) + r0 * q.n,
+                                        static_cast<const T*>(q.pre) + r0 * q.n, rows, q.n, q.vec_n,
+                                        mine, sum);
+            if (q.want_w)
+                make_operand<T, kActNone, false>(unit + L::operand,
+                                                 static_cast<const T*>(q.x) + r0 * q.k, nullptr,
+                                                 rows, q.k, q.vec_k, mine, none);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(unit_full + s);
+        }
+        if (ok && q.sums)   // the next unit is free once the MMAs of its last tile are done
+            ok = mbar_wait(unit_empty + (u & 1), ((u >> 1) & 1) ^ 1) && !*s_fail;
+        if (!ok) *s_fail = 1u;
+        if (q.sums) {   // 32 rows of threads by halves: in a warp, then between the warps
+#pragma unroll
+            for (int h = 0; h < L::panels; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], 8);
+                    sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], 16);
+                }
+            float* all = reinterpret_cast<float*>(smem + (u & 1) * L::unit);
+            if (lane < 8)
+#pragma unroll
+                for (int h = 0; h < L::panels; ++h)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        all[(warp - 1) * kBackSide<T> + h * kPanel + lane * 8 + e] = sum[h][e];
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (mine < q.n) {
+                float v[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) v[w] = all[w * kBackSide<T> + mine];
+                q.sums[(int64_t)blockIdx.x * q.n + mine] =
+                    ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            }
+        }
+    } else {   // ---- epilogue
+        const int e0 = warp - 9, quarter = warp & 3, group = e0 >> 2;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        float dw[kSplit ? 32 : 1];
+#pragma unroll
+        for (int e = 0; e < (kSplit ? 32 : 1); ++e) dw[e] = 0.0f;
+        float4* x = reinterpret_cast<float4*>(smem + L::exchange) + e0 * (kSplit ? 64 : 256);
+        // 32 columns of dx, a row in each lane
+        auto store_dx = [&](const float (&v)[32], int64_t t, int c0) {
+            const int64_t r0 = t * kBlock + quarter * 32;
+            if constexpr (!kSplit) {
+                Share<T> share;
+                const float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                share.begin(q.out, r0, c0, 0, lane);
+                share.template end<kActNone>(q.out, x, v, bias, lane);
+            } else {   // a smaller exchange: eight columns, a sector of each row, at a time
+                const int j = lane & 1, rows = (int)(q.out.m - r0 < 32 ? q.out.m - r0 : 32);
+                float* out = static_cast<float*>(q.out.out) + (r0 + (lane >> 1)) * q.k;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        x[lane * 2 + (i ^ (lane >> 2 & 1))] =
+                            make_float4(v[8 * m + 4 * i], v[8 * m + 4 * i + 1],
+                                        v[8 * m + 4 * i + 2], v[8 * m + 4 * i + 3]);
+                    __syncwarp();
+                    float4 f[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = 16 * h + (lane >> 1);
+                        f[h] = x[r * 2 + (j ^ (r >> 2 & 1))];
+                    }
+                    const int c = c0 + 8 * m + 4 * j;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (16 * h + (lane >> 1) >= rows || c >= q.k) continue;
+                        float* o = out + (int64_t)16 * h * q.k + c;
+                        if (q.out.vec) {
+                            *reinterpret_cast<float4*>(o) = f[h];
+                        } else {
+                            o[0] = f[h].x;
+                            if (c + 1 < q.k) o[1] = f[h].y;
+                            if (c + 2 < q.k) o[2] = f[h].z;
+                            if (c + 3 < q.k) o[3] = f[h].w;
+                        }
+                    }
+                }
+            }
+        };
+        bool ok = true;
+        int u = 0;
+        for (int64_t t = first; t < q.tiles; t += step, ++u) {
+            if (q.want_x) {
+                const int buf = kSplit ? 0 : u & 1, turn = kSplit ? u : u >> 1;
+                ok = warp_all(mbar_wait(dx_full + buf, turn & 1) && !*s_fail);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = group * 32; c < (kSplit ? 64 : q.k); c += 64) {
+                    float v[32];
+#pragma unroll
+                    for (int p = 0; p < kPlanes; ++p) {
+                        uint32_t w[32];
+                        __syncwarp();
+                        tmem_ld32(tmem + buf * 128 + lanes + p * 64 + c, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = p ? v[e] + __uint_as_float(w[e]) : __uint_as_float(w[e]);
+                    }
+                    if (c + 64 >= (kSplit ? 64 : q.k)) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(dx_empty + buf);
+                    }
+                    store_dx(v, t, c);
+                }
+                if (!kSplit && group * 32 >= q.k && lane == 0) mbar_arrive(dx_empty + buf);
+            }
+            if (kSplit && q.want_w) {
+                ok = warp_all(mbar_wait(dw_full, u & 1) && !*s_fail);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    if (p == 2 && quarter >= 2) continue;   // lo mid, or what lies behind lo
+                    uint32_t w[32];
+                    __syncwarp();
+                    tmem_ld32(tmem + kDw + lanes + p * 64 + group * 32, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) dw[kSplit ? e : 0] += __uint_as_float(w[e]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dw_empty);
+            }
+        }
+        if (ok && q.want_w) {
+            // a lane has a row of its part
+            const int row = kSplit ? (quarter & 1) * 32 + lane : quarter * 32 + lane;
+            float* part = q.parts + ((int64_t)blockIdx.x * (kSplit ? 2 : 1) +
+                                     (kSplit ? quarter >> 1 : 0)) * q.n * q.k +
+                          (int64_t)row * q.k;
+            if constexpr (kSplit) {
+                if (row < q.n)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (group * 32 + e < q.k) part[group * 32 + e] = dw[e];
+            } else {
+                ok = warp_all(mbar_wait(dw_full, 0) && !*s_fail);
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = group * 32; ok && c < q.k; c += 64) {
+                    uint32_t w[32];
+                    __syncwarp();
+                    tmem_ld32(tmem + kDw + lanes + c, w);
+                    tmem_wait_ld();
+                    if (row < q.n)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c + e < q.k) part[c + e] = __uint_as_float(w[e]);
+                }
+            }
+        }
+        if (!ok) *s_fail = 1u;
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && *s_fail) atomicOr(&st->error, kErrTimeout);
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------ plans --
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -1142,11 +1584,18 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
     s.x = c.take<__nv_bfloat16>(planes * plane_size(m, k));
     s.w = c.take<__nv_bfloat16>(planes * plane_size(n, k));
     s.dz = c.take<__nv_bfloat16>(planes * plane_size(m, n));
-    s.sums = c.take<float>((size_t)operand_grid(m, n).blocks * n);
+    const int64_t blocks = operand_grid(m, n).blocks;
+    s.sums = c.take<float>((size_t)(blocks > kMostSms ? blocks : kMostSms) * n);
     size_t parts = part_floats(planes, m, n, k);
     const size_t dx = part_floats(planes, m, k, n), dw = part_floats(planes, n, k, m);
     if (dx > parts) parts = dx;
     if (dw > parts) parts = dw;
+    const int64_t side = dtype == kF32 ? kBackSide<float> : kBackSide<__nv_bfloat16>;
+    if (k <= side && n <= side) {   // two parts of every CTA
+        const size_t tiles = (size_t)ceil_div(m, kBlock);
+        const size_t narrow = 2 * (tiles < kMostSms ? tiles : kMostSms) * (size_t)(n * k);
+        if (narrow > parts) parts = narrow;
+    }
     s.parts = c.take<float>(parts);
     s.bytes = c.used;
     return s;
@@ -1181,6 +1630,16 @@ cudaError_t operand(Matrix* out, const void* src, const void* pre, int act, int6
     }
 }
 
+// (16 parts or fewer: a thread per four columns, each part's load behind the one before)
+template <typename T>
+cudaError_t join(const Product& q, const float* parts, int n_sms, cudaStream_t s) {
+    const bool many = q.splits > 16;
+    const int64_t blocks = ceil_div(q.m * ceil_div(q.n, 4), many ? 4 : 256);
+    return launch_pdl(many ? k_linear_join<T, 64> : k_linear_join<T, 1>,
+                      dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8)), dim3(256), 0, s, q,
+                      parts);
+}
+
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
 cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                        LearnState* st, int n_sms, cudaStream_t s) {
@@ -1205,9 +1664,7 @@ cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, f
     p.vec = q.n % 4 == 0;
     cudaError_t e = launch(k_linear_product<float, kPlanes, kN, kAMn, kBMn>, p);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = ceil_div(q.m * ceil_div(q.n, 4), 256);
-    return launch_pdl(k_linear_join<T>, dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8)),
-                      dim3(256), 0, s, q, (const float*)parts);
+    return join<T>(q, parts, n_sms, s);
 }
 
 template <typename T, bool kAMn, bool kBMn>
@@ -1307,6 +1764,50 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
 }
 
 template <typename T>
+cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_sms,
+                   cudaStream_t s) {
+    const int64_t m = c.rows, k = c.inputs, n = c.outputs;
+    Narrow q{};
+    q.grad_y = c.grad_y;
+    q.pre = c.pre;
+    q.x = c.x;
+    q.weight = c.weight;
+    q.rows = m;
+    q.tiles = ceil_div(m, kBlock);
+    q.k = (int)k;
+    q.n = (int)n;
+    const bool act = c.act != kActNone;
+    q.vec_n = n % VecOf<T>::n == 0 && aligned16(c.grad_y) && (!act || aligned16(c.pre));
+    q.vec_k = k % VecOf<T>::n == 0 && aligned16(c.x) && aligned16(c.weight);
+    q.ahead = aligned16(c.grad_y) && (!act || aligned16(c.pre)) && aligned16(c.x);
+    q.want_x = c.grad_x != nullptr;
+    q.want_w = c.grad_weight != nullptr;
+    q.parts = sp.parts;
+    q.sums = c.grad_bias ? sp.sums : nullptr;
+    q.out.m = m;
+    q.out.n = k;
+    q.out.out = c.grad_x;
+    q.out.vec = vec4<T>(q.out);
+    const unsigned ctas = (unsigned)(q.tiles < n_sms ? q.tiles : n_sms);
+    auto* kernel = c.act == kActSilu   ? k_linear_narrow<T, kActSilu>
+                   : c.act == kActRelu ? k_linear_narrow<T, kActRelu>
+                                       : k_linear_narrow<T, kActNone>;
+    cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kBackThreads), BackSmem<T>::bytes, s, q, st);
+    if (e == cudaSuccess && c.grad_bias)
+        e = launch_pdl(k_linear_sums, dim3((unsigned)ceil_div(n, 32)), dim3(32, 32), 0, s,
+                       (const float*)sp.sums, (int64_t)ctas, n, c.grad_bias);
+    if (e == cudaSuccess && c.grad_weight) {
+        Product p{};
+        p.m = n;
+        p.n = k;
+        p.out = c.grad_weight;
+        p.splits = (int)ctas * (sizeof(T) == 4 ? 2 : 1);
+        e = join<T>(p, sp.parts, n_sms, s);
+    }
+    return e;
+}
+
+template <typename T>
 cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cudaStream_t s) {
     const int64_t m = c.rows, k = c.inputs, n = c.outputs;
     if (m == 0) {
@@ -1316,6 +1817,7 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
         return e;
     }
     const Space sp = carve(ws, m, k, n, c.dtype);
+    if (k <= kBackSide<T> && n <= kBackSide<T>) return narrow<T>(c, sp, st, n_sms, s);
     Matrix dz, w, x;
     cudaError_t e = cudaSuccess;
     if (c.grad_x || c.grad_weight || c.grad_bias)
@@ -1366,6 +1868,12 @@ cudaError_t prepare_three() {
     return e;
 }
 
+template <typename T, int kAct>
+cudaError_t prepare_narrow() {
+    return cudaFuncSetAttribute(k_linear_narrow<T, kAct>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, BackSmem<T>::bytes);
+}
+
 }  // namespace
 
 size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
@@ -1383,6 +1891,12 @@ cudaError_t prepare_linear() {
     e = prepare_three<float, 3, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256>();
+    if (e == cudaSuccess) e = prepare_narrow<float, kActNone>();
+    if (e == cudaSuccess) e = prepare_narrow<float, kActSilu>();
+    if (e == cudaSuccess) e = prepare_narrow<float, kActRelu>();
+    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActNone>();
+    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActSilu>();
+    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActRelu>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_linear_stream<float>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
