@@ -1105,7 +1105,8 @@ struct Narrow {
     const void *grad_y, *pre, *x, *weight;
     int64_t rows, tiles;
     int k, n;              // inputs, outputs
-    bool vec_n, vec_k;     // rows of n (k) elements are whole 16-byte vectors
+    bool fast;             // rows are whole chunks of eight, on 16 bytes
+    bool vec_w;            // so are the weight's
     bool ahead;            // the tensors begin on 16 bytes
     bool want_x, want_w;
     float* parts;          // [parts of all CTAs][n][k]
@@ -1129,45 +1130,122 @@ struct BackSmem {
     static_assert(bytes <= 227 * 1024, "shared memory of a narrow layer's gradients");
 };
 
-// A tile's operand from its rows of `cols` elements: dz where kAct is an activation and `pre`
-// given, its columns added to `sum`.  A thread has a chunk of eight columns (c of 0 .. 7 in every
-// panel) of every 32nd row.  Rows behind the last, and columns up to the next 16, are zeros.
-template <typename T, int kAct, bool kSum>
-__device__ __forceinline__ void make_operand(unsigned char* unit, const T* src, const T* pre,
-                                             int rows, int cols, bool vec, int mine,
-                                             float (&sum)[kBackSide<T> / kPanel][8]) {
+// Eight columns of a row as they were loaded: nothing waits for them before they are opened.
+template <typename T>
+struct Chunk {
+    typename Pack<T, VecOf<T>::n>::Raw raw[8 / VecOf<T>::n];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int h = 0; h < 8 / VecOf<T>::n; ++h)
+            raw[h] = Pack<T, VecOf<T>::n>::raw_last(p + h * VecOf<T>::n);
+    }
+    __device__ __forceinline__ void open(float (&v)[8]) const {
+#pragma unroll
+        for (int h = 0; h < 8 / VecOf<T>::n; ++h) {
+            float u[VecOf<T>::n];
+            Pack<T, VecOf<T>::n>::open(raw[h], u);
+#pragma unroll
+            for (int e = 0; e < VecOf<T>::n; ++e) v[h * VecOf<T>::n + e] = u[e];
+        }
+    }
+};
+
+template <typename T, int kAct>
+__device__ __forceinline__ void to_dz(float (&v)[8], const float (&z)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (kAct == kActRelu) v[e] = z[e] > 0.0f ? v[e] : 0.0f;
+        if (kAct == kActSilu) v[e] *= act_slope<kActSilu>(z[e]);
+    }
+}
+
+// A tile's operands, dz (its columns added to `sum`) and x, by a thread that has a chunk of eight
+// columns (c of 0 .. 7 in every panel) of every 32nd row.  Rows behind the last, and columns up to
+// the next 16, are zeros.
+template <typename T, int kAct>
+__device__ __forceinline__ void make_operands(const Narrow& q, unsigned char* unit, int64_t row0,
+                                              int rows, int mine,
+                                              float (&sum)[kBackSide<T> / kPanel][8]) {
     using L = BackSmem<T>;
     constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight together
     const int c = mine & 7, r0 = mine >> 3;
+    const T* dy = static_cast<const T*>(q.grad_y) + (row0 + r0) * q.n;
+    const T* pre = static_cast<const T*>(q.pre) + (row0 + r0) * q.n;
+    const T* x = static_cast<const T*>(q.x) + (row0 + r0) * q.k;
+    const int n16 = (q.n + 15) / 16 * 16, k16 = q.want_w ? (q.k + 15) / 16 * 16 : 0;
 #pragma unroll
     for (int h = 0; h < L::panels; ++h) {
         const int col = h * kPanel + c * 8;
-        if (col >= (cols + 15) / 16 * 16) break;
-        const int n = cols - col;
+        const bool in_n = col < n16, in_k = col < k16;
         unsigned char* dst = unit + h * L::planes * L::panel + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        if (q.fast && rows == kBlock) {   // whole chunks of whole vectors
+            const bool full_n = col < q.n, full_k = in_k && col < q.k;
 #pragma unroll
-        for (int i0 = 0; i0 < 4; i0 += kBatch) {
-            float v[kBatch][8], z[kBatch][8];
+            for (int i0 = 0; i0 < 4; i0 += kBatch) {
+                Chunk<T> a[kBatch], z[kBatch], b[kBatch];
+                if (full_n) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int r = r0 + 32 * (i0 + i);
+                    for (int i = 0; i < kBatch; ++i) {
+                        a[i].load(dy + 32 * (i0 + i) * q.n + col);
+                        if (kAct != kActNone) z[i].load(pre + 32 * (i0 + i) * q.n + col);
+                    }
+                }
+                if (full_k) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = z[i][e] = 0.0f;
-                if (r < rows && n > 0) {
-                    load8(src + (int64_t)r * cols + col, n, vec && n >= 8, v[i]);
-                    if (kAct != kActNone)
-                        load8(pre + (int64_t)r * cols + col, n, vec && n >= 8, z[i]);
+                    for (int i = 0; i < kBatch; ++i) b[i].load(x + 32 * (i0 + i) * q.k + col);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (!in_n) continue;
+                    float v[8], w[8];
+                    if (full_n) {
+                        a[i].open(v);
+                        if (kAct != kActNone) z[i].open(w);
+                        to_dz<T, kAct>(v, w);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sum[h][e] += v[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    }
+                    put_chunk<L::planes>(dst + 32 * (i0 + i) * 128, L::panel, v);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (!in_k) continue;
+                    float v[8];
+                    if (full_k) {
+                        b[i].open(v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    }
+                    put_chunk<L::planes>(dst + L::operand + 32 * (i0 + i) * 128, L::panel, v);
                 }
             }
+            continue;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const bool row = r0 + 32 * i < rows;
+            float v[8], w[8];
+            if (in_n) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+                for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.0f;
+                if (row && col < q.n) {
+                    load8(dy + 32 * i * q.n + col, q.n - col, false, v);
+                    if (kAct != kActNone) load8(pre + 32 * i * q.n + col, q.n - col, false, w);
+                    to_dz<T, kAct>(v, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (kAct == kActRelu) v[i][e] = z[i][e] > 0.0f ? v[i][e] : 0.0f;
-                    if (kAct == kActSilu) v[i][e] *= act_slope<kActSilu>(z[i][e]);
-                    if (kSum) sum[h][e] += v[i][e];
+                    for (int e = 0; e < 8; ++e) sum[h][e] += v[e];
                 }
-                put_chunk<L::planes>(dst + 32 * (i0 + i) * 128, L::panel, v[i]);
+                put_chunk<L::planes>(dst + 32 * i * 128, L::panel, v);
+            }
+            if (in_k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                if (row && col < q.k) load8(x + 32 * i * q.k + col, q.k - col, false, v);
+                put_chunk<L::planes>(dst + L::operand + 32 * i * 128, L::panel, v);
             }
         }
     }
@@ -1216,7 +1294,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.0f;
             if (r < q.n)
-                load8(static_cast<const T*>(q.weight) + r * q.k + c * 8, n, q.vec_k && n >= 8, v);
+                load8(static_cast<const T*>(q.weight) + r * q.k + c * 8, n, q.vec_w && n >= 8, v);
             put_chunk<kPlanes>(smem + L::weight + (c >> 3) * kPlanes * L::weight_panel + r * 128 +
                                    (((c & 7) ^ (r & 7)) << 4),
                                L::weight_panel, v);
@@ -1298,11 +1376,11 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         }
     } else if (warp < 9) {   // ---- operands
         const int mine = tid - 32;
-        float sum[L::panels][8], none[L::panels][8];
+        float sum[L::panels][8];
 #pragma unroll
         for (int h = 0; h < L::panels; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[h][e] = none[h][e] = 0.0f;
+            for (int e = 0; e < 8; ++e) sum[h][e] = 0.0f;
         // a tile's tensors, on their way to the L2
         auto fetch = [&](int64_t t) {
             if (t >= q.tiles) return;
@@ -1328,13 +1406,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             const int rows = (int)(left < kBlock ? left : kBlock);
             unsigned char* unit = smem + s * L::unit;
             if (q.ahead && warp == 1 && elect_one()) fetch(t + (int64_t)kBackAhead * step);
-            make_operand<T, kAct, true>(unit, static_cast<const T*>(q.grad_y) + r0 * q.n,
-                                        static_cast<const T*>(q.pre) + r0 * q.n, rows, q.n, q.vec_n,
-                                        mine, sum);
-            if (q.want_w)
-                make_operand<T, kActNone, false>(unit + L::operand,
-                                                 static_cast<const T*>(q.x) + r0 * q.k, nullptr,
-                                                 rows, q.k, q.vec_k, mine, none);
+            make_operands<T, kAct>(q, unit, r0, rows, mine, sum);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(unit_full + s);
@@ -1777,9 +1849,9 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
     q.k = (int)k;
     q.n = (int)n;
     const bool act = c.act != kActNone;
-    q.vec_n = n % VecOf<T>::n == 0 && aligned16(c.grad_y) && (!act || aligned16(c.pre));
-    q.vec_k = k % VecOf<T>::n == 0 && aligned16(c.x) && aligned16(c.weight);
     q.ahead = aligned16(c.grad_y) && (!act || aligned16(c.pre)) && aligned16(c.x);
+    q.fast = q.ahead && n % 8 == 0 && k % 8 == 0;
+    q.vec_w = aligned16(c.weight) && k % 8 == 0;
     q.want_x = c.grad_x != nullptr;
     q.want_w = c.grad_weight != nullptr;
     q.parts = sp.parts;
