@@ -16,6 +16,8 @@
 // a sum in 32 bits.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "learn_internal.cuh"
 #include "tensor_core.cuh"
 
@@ -263,6 +265,14 @@ __device__ __forceinline__ void mbar_init_n(uint64_t* mbar, uint32_t n) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* mbar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(mbar)) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(mbar))
+        : "memory");
 }
 // A box of a tensor map [planes][rows][cols] at (plane, row, col): col a multiple of 64.
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int col, int row,
@@ -1083,186 +1093,170 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 
 // --------------------------------------------- narrow layers, gradients --
 // All gradients of a narrow layer in one pass over dy, z and x: a persistent CTA
-// per SM, tiles of 128 rows.  Eight warps make dz and x into operands (and add
-// up dz's columns), one thread issues the MMAs, eight warps finish dx.  dz's
-// tile, 128 rows of 128 bytes a panel, is a K-major left operand of dx = dz W
-// (its rows are rows) and, the same bytes, an MN-major one of dW = dz^T x (its
-// rows are the contraction).  dW stays in the CTA; k_linear_join adds up the
-// CTAs' sums in their order.
+// per SM, tiles of 128 rows.  One thread keeps raw tiles coming (contiguous bulk
+// copies), eight warps make dz and x into operands (and add up dz's columns), one
+// thread issues the MMAs, eight warps finish dx.  dz's tile, 128 rows of 128
+// bytes a panel, is an MN-major left operand of dW = dz^T x (its rows are the
+// contraction) and, the same bytes, a K-major one of dx = dz W (its rows are
+// rows).  dW stays in the CTA; k_linear_join adds up the CTAs' sums in their
+// order.
 //
 // In 32 bits the planes of dz are two groups of one left operand [hi; mid] of
 // dW, those of x three of the right one, so that one MMA makes six products
-// (lo mid among them, in rows that are not read); lo hi is a second one, into
+// (mid lo among them, in columns that are not read); lo hi is a second one, into
 // the columns of hi lo.  They are drained every tile (128 of K) into registers:
 // the rows of hi, and those of mid, are parts of their own.  dx as in the
-// forward kernel.
-constexpr int kBackThreads = 544;   // warps: MMAs, eight of operands, eight of the epilogue
+// forward kernel.  There is room for one tile's operands and one raw tile: x's
+// are made while the MMAs of dx run, which do not need them.
+constexpr int kBackThreads = 576;   // warps: MMAs, eight of operands, eight of the epilogue, copies
 template <typename T>
 constexpr int kBackSide = sizeof(T) == 4 ? 64 : 128;   // inputs and outputs of a layer
-constexpr int kBackAhead = 3;                          // tiles that are on their way to the L2
 
 struct Narrow {
     const void *grad_y, *pre, *x, *weight;
     int64_t rows, tiles;
     int k, n;              // inputs, outputs
-    bool fast;             // rows are whole chunks of eight, on 16 bytes
-    bool vec_w;            // so are the weight's
-    bool ahead;            // the tensors begin on 16 bytes
+    bool raw;              // the tensors begin on 16 bytes: raw tiles by bulk copies
+    bool vec_n, vec_k;     // ... and rows of n (k) elements are whole 16-byte vectors
+    bool vec_w;            // rows of the weight are whole chunks of eight, on 16 bytes
     bool want_x, want_w;
     float* parts;          // [parts of all CTAs][n][k]
     float* sums;           // [CTA][n]; may be NULL
     Product out;           // of dx
 };
-template <typename T>
+template <typename T, int kPanels>
 struct BackSmem {
     static constexpr int planes = sizeof(T) == 4 ? 3 : 1;
-    static constexpr int panels = kBackSide<T> / kPanel;
+    static constexpr int side = kPanels * kPanel;
     static constexpr int panel = kBlock * kPanel * 2;          // of one plane
-    static constexpr int operand = planes * panels * panel;    // [panel][plane]
+    static constexpr int operand = planes * kPanels * panel;   // [panel][plane]
     static constexpr int unit = 2 * operand;                   // dz, x
-    static constexpr int weight_panel = kBackSide<T> * kPanel * 2;
-    static constexpr int weight = 2 * unit;                    // [panel of inputs][plane]
-    static constexpr int exchange = weight + planes * panels * weight_panel;
-    // 32 bits: of four warps, which take turns with the other four
-    static constexpr int exchange_bytes = sizeof(T) == 4 ? 8 * 1024 : 8 * 4096;
-    static constexpr int bars = exchange + exchange_bytes;
+    static constexpr int units = planes == 1 && kPanels == 1 ? 2 : 1;
+    static constexpr int weight_panel = side * kPanel * 2;
+    static constexpr int weight = units * unit;                // [panel of inputs][plane]
+    // a warp's exchange is 32 x 32 words; in 32 bits, for want of room, 32 x 8
+    static constexpr int exchange = weight + planes * kPanels * weight_panel;
+    static constexpr int exchange_bytes = planes == 3 ? 8 * 1024 : 8 * 4096;
+    static constexpr int raw = exchange + exchange_bytes;      // dy, z, x
+    static constexpr int raw_tensor = kBlock * side * (int)sizeof(T);
+    static constexpr int raws = units;
+    static constexpr int bars = raw + raws * 3 * raw_tensor;
     static constexpr int bytes = bars + 256 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of a narrow layer's gradients");
 };
 
-// Eight columns of a row as they were loaded: nothing waits for them before they are opened.
-template <typename T>
-struct Chunk {
-    typename Pack<T, VecOf<T>::n>::Raw raw[8 / VecOf<T>::n];
-    __device__ __forceinline__ void load(const T* p) {
+template <typename T, int kAct, int V>
+__device__ __forceinline__ void to_dz(float (&v)[V], const float (&z)[V]) {
 #pragma unroll
-        for (int h = 0; h < 8 / VecOf<T>::n; ++h)
-            raw[h] = Pack<T, VecOf<T>::n>::raw_last(p + h * VecOf<T>::n);
-    }
-    __device__ __forceinline__ void open(float (&v)[8]) const {
-#pragma unroll
-        for (int h = 0; h < 8 / VecOf<T>::n; ++h) {
-            float u[VecOf<T>::n];
-            Pack<T, VecOf<T>::n>::open(raw[h], u);
-#pragma unroll
-            for (int e = 0; e < VecOf<T>::n; ++e) v[h * VecOf<T>::n + e] = u[e];
-        }
-    }
-};
-
-template <typename T, int kAct>
-__device__ __forceinline__ void to_dz(float (&v)[8], const float (&z)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < V; ++e) {
         if (kAct == kActRelu) v[e] = z[e] > 0.0f ? v[e] : 0.0f;
         if (kAct == kActSilu) v[e] *= act_slope<kActSilu>(z[e]);
     }
 }
 
-// A tile's operands, dz (its columns added to `sum`) and x, by a thread that has a chunk of eight
-// columns (c of 0 .. 7 in every panel) of every 32nd row.  Rows behind the last, and columns up to
-// the next 16, are zeros.
-template <typename T, int kAct>
-__device__ __forceinline__ void make_operands(const Narrow& q, unsigned char* unit, int64_t row0,
-                                              int rows, int mine,
-                                              float (&sum)[kBackSide<T> / kPanel][8]) {
-    using L = BackSmem<T>;
-    constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight together
-    const int c = mine & 7, r0 = mine >> 3;
-    const T* dy = static_cast<const T*>(q.grad_y) + (row0 + r0) * q.n;
-    const T* pre = static_cast<const T*>(q.pre) + (row0 + r0) * q.n;
-    const T* x = static_cast<const T*>(q.x) + (row0 + r0) * q.k;
-    const int n16 = (q.n + 15) / 16 * 16, k16 = q.want_w ? (q.k + 15) / 16 * 16 : 0;
+// V columns (eight or sixteen bytes of bfloat16 in a plane).
+template <int kPlanes, int V>
+__device__ __forceinline__ void put_columns(unsigned char* at, uint32_t plane_bytes,
+                                            const float (&v)[V]) {
+    uint32_t w[V / 2][3];
 #pragma unroll
-    for (int h = 0; h < L::panels; ++h) {
-        const int col = h * kPanel + c * 8;
-        const bool in_n = col < n16, in_k = col < k16;
-        unsigned char* dst = unit + h * L::planes * L::panel + r0 * 128 + ((c ^ (r0 & 7)) << 4);
-        if (q.fast && rows == kBlock) {   // whole chunks of whole vectors
-            const bool full_n = col < q.n, full_k = in_k && col < q.k;
+    for (int e = 0; e < V / 2; ++e) {
+        if (kPlanes == 3)
+            split3(v[2 * e], v[2 * e + 1], w[e]);
+        else
+            w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
+    }
 #pragma unroll
-            for (int i0 = 0; i0 < 4; i0 += kBatch) {
-                Chunk<T> a[kBatch], z[kBatch], b[kBatch];
-                if (full_n) {
+    for (int p = 0; p < kPlanes; ++p) {
+        if constexpr (V == 8)
+            *reinterpret_cast<uint4*>(at + p * plane_bytes) =
+                make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+        else
+            *reinterpret_cast<uint2*>(at + p * plane_bytes) = make_uint2(w[0][p], w[1][p]);
+    }
+}
+
+// The operand of a tile, [rows, cols] at `src` (times the activation's slope at `pre`, its columns
+// added to `sum`, where kDz), by a thread that has 16 bytes' columns of every kStep-th row: rows
+// behind the last, and columns up to the next 16, are zeros.  `vec`: src is a raw tile in shared
+// memory of whole 16-byte vectors.
+template <typename T, int kAct, int kPanels, bool kDz>
+__device__ __forceinline__ void make_operand(unsigned char* operand, const T* src, const T* pre,
+                                             int rows, int cols, bool vec, int mine,
+                                             float (&sum)[kPanels][VecOf<T>::n]) {
+    using L = BackSmem<T, kPanels>;
+    constexpr int V = VecOf<T>::n, kLanes = kPanel / V, kStep = 256 / kLanes, kBatch = 4;
+    const int c = mine % kLanes * V, r0 = mine / kLanes, cols16 = (cols + 15) / 16 * 16;
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        a[i].load(dy + 32 * (i0 + i) * q.n + col);
-                        if (kAct != kActNone) z[i].load(pre + 32 * (i0 + i) * q.n + col);
+    for (int h = 0; h < kPanels; ++h) {
+        const int col = h * kPanel + c;
+        if (col >= cols16) break;
+        unsigned char* dst = operand + h * L::planes * L::panel + r0 * 128 +
+                             (((c >> 3) ^ (r0 & 7)) << 4) + (c & 7) * 2;
+        if (vec) {
+            const T* s = src + r0 * cols + col;
+            const T* z = pre + r0 * cols + col;
+#pragma unroll
+            for (int i0 = 0; i0 < kBlock / kStep; i0 += kBatch) {
+                float v[kBatch][V], w[kBatch][V];   // (all loads, then all stores)
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = (i0 + i) * kStep;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[i][e] = w[i][e] = 0.0f;
+                    if (r0 + r < rows && col < cols) {
+                        Pack<T, V>::load(s + r * cols, v[i]);
+                        if (kAct != kActNone) Pack<T, V>::load(z + r * cols, w[i]);
                     }
-                }
-                if (full_k) {
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) b[i].load(x + 32 * (i0 + i) * q.k + col);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    if (!in_n) continue;
-                    float v[8], w[8];
-                    if (full_n) {
-                        a[i].open(v);
-                        if (kAct != kActNone) z[i].open(w);
-                        to_dz<T, kAct>(v, w);
+                    to_dz<T, kAct>(v[i], w[i]);
+                    if (kDz)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) sum[h][e] += v[e];
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                    }
-                    put_chunk<L::planes>(dst + 32 * (i0 + i) * 128, L::panel, v);
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    if (!in_k) continue;
-                    float v[8];
-                    if (full_k) {
-                        b[i].open(v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                    }
-                    put_chunk<L::planes>(dst + L::operand + 32 * (i0 + i) * 128, L::panel, v);
+                        for (int e = 0; e < V; ++e) sum[h][e] += v[i][e];
+                    put_columns<L::planes>(dst + (i0 + i) * kStep * 128, L::panel, v[i]);
                 }
             }
-            continue;
-        }
+        } else {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const bool row = r0 + 32 * i < rows;
-            float v[8], w[8];
-            if (in_n) {
+            for (int r = r0; r < kBlock; r += kStep) {
+                float v[V], w[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.0f;
-                if (row && col < q.n) {
-                    load8(dy + 32 * i * q.n + col, q.n - col, false, v);
-                    if (kAct != kActNone) load8(pre + 32 * i * q.n + col, q.n - col, false, w);
-                    to_dz<T, kAct>(v, w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum[h][e] += v[e];
+                for (int e = 0; e < V; ++e) {
+                    float one[1] = {0.0f}, z[1] = {0.0f};
+                    if (r < rows && col + e < cols) {
+                        Pack<T, 1>::load(src + (int64_t)r * cols + col + e, one);
+                        if (kAct != kActNone) Pack<T, 1>::load(pre + (int64_t)r * cols + col + e, z);
+                    }
+                    v[e] = one[0];
+                    w[e] = z[0];
                 }
-                put_chunk<L::planes>(dst + 32 * i * 128, L::panel, v);
-            }
-            if (in_k) {
+                to_dz<T, kAct>(v, w);
+                if (kDz)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-                if (row && col < q.k) load8(x + 32 * i * q.k + col, q.k - col, false, v);
-                put_chunk<L::planes>(dst + L::operand + 32 * i * 128, L::panel, v);
+                    for (int e = 0; e < V; ++e) sum[h][e] += v[e];
+                put_columns<L::planes>(dst + (r - r0) * 128, L::panel, v);
             }
         }
     }
 }
 
-template <typename T, int kAct>
+template <typename T, int kAct, int kPanels>
 __global__ void __launch_bounds__(kBackThreads, 1)
 k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
-    using L = BackSmem<T>;
-    constexpr int kPlanes = L::planes;
+    using L = BackSmem<T, kPanels>;
+    constexpr int kPlanes = L::planes, V = VecOf<T>::n;
     constexpr bool kSplit = kPlanes == 3;
     constexpr uint32_t kDw = kSplit ? 192 : 256;   // columns: dx below, dW from here
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
-    uint64_t* unit_full = reinterpret_cast<uint64_t*>(smem + L::bars);
-    uint64_t* unit_empty = unit_full + 2;
-    uint64_t* dx_full = unit_empty + 2;
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::bars);
+    uint64_t* raw_empty = raw_full + 2;
+    uint64_t* unit_full = raw_empty + 2;
+    uint64_t* dz_empty = unit_full + 2;
+    uint64_t* x_empty = dz_empty + 2;
+    uint64_t* dx_full = x_empty + 2;
     uint64_t* dx_empty = dx_full + 2;
     uint64_t* dw_full = dx_empty + 2;
     uint64_t* dw_empty = dw_full + 1;
@@ -1273,8 +1267,11 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the same in a warp)
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
+            mbar_init(raw_full + s);
+            mbar_init_n(raw_empty + s, 8);
             mbar_init_n(unit_full + s, 8);
-            mbar_init(unit_empty + s);
+            mbar_init(dz_empty + s);
+            mbar_init(x_empty + s);
             mbar_init(dx_full + s);
             mbar_init_n(dx_empty + s, 8);
         }
@@ -1306,7 +1303,47 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
     const int first = blockIdx.x, step = gridDim.x;
-    if (warp == 0) {
+    if (warp == 17) {
+        if (q.raw && elect_one()) {   // ---- raw tiles
+            int u = 0;
+            bool ok = true;
+            for (int64_t t = first; t < q.tiles; t += step, ++u) {
+                const int s = u % L::raws;
+                ok = mbar_wait(raw_empty + s, ((u / L::raws) & 1) ^ 1) && !*s_fail;
+                if (!ok) break;
+                const int64_t left = q.rows - t * kBlock;
+                const uint32_t rows = (uint32_t)(left < kBlock ? left : kBlock);
+                unsigned char* dst = smem + L::raw + s * 3 * L::raw_tensor;
+                const uint32_t of_n = rows * q.n * (uint32_t)sizeof(T);
+                const uint32_t of_k = q.want_w ? rows * q.k * (uint32_t)sizeof(T) : 0u;
+                // (the last rows need not end on 16 bytes)
+                const auto one = [&](int i, const void* p, int cols, uint32_t bytes, bool rest) {
+                    const T* src = static_cast<const T*>(p) + t * kBlock * cols;
+                    unsigned char* at = dst + i * L::raw_tensor;
+                    if (rest) {
+                        for (uint32_t e = (bytes & ~15u) / sizeof(T); e < bytes / sizeof(T); ++e)
+                            reinterpret_cast<T*>(at)[e] = src[e];
+                    } else if (bytes & ~15u) {
+                        bulk_copy(at, src, bytes & ~15u, raw_full + s);
+                    }
+                };
+#pragma unroll
+                for (int rest = 1; rest >= 0; --rest) {
+                    if (!rest)
+                        expect_bytes(raw_full + s, (kAct != kActNone ? 2 : 1) * (of_n & ~15u) +
+                                                       (of_k & ~15u));
+                    one(0, q.grad_y, q.n, of_n, rest);
+                    if (kAct != kActNone) one(1, q.pre, q.n, of_n, rest);
+                    if (q.want_w) one(2, q.x, q.k, of_k, rest);
+                }
+            }
+            if (!ok) {   // give the copies in flight one more bounded wait
+                *s_fail = 1u;
+                for (int k = u > L::raws ? u - L::raws : 0; k < u; ++k)
+                    mbar_wait(raw_full + k % L::raws, (k / L::raws) & 1);
+            }
+        }
+    } else if (warp == 0) {
         if (elect_one()) {   // ---- MMAs
             constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
                                        ((uint32_t)(kBlock >> 4) << 24);   // B MN-major
@@ -1317,34 +1354,10 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             int u = 0;
             bool ok = true;
             for (int64_t t = first; t < q.tiles; t += step, ++u) {
-                const int s = u & 1;
-                ok = mbar_wait(unit_full + s, (u >> 1) & 1) && !*s_fail;
+                const int s = u % L::units;
+                ok = mbar_wait(unit_full + s, (u / L::units) & 1) && !*s_fail;
                 if (!ok) break;
                 const uint32_t dz = base + s * L::unit, x = dz + L::operand;
-                const uint32_t w = base + L::weight;
-                if (q.want_x) {
-                    // (one accumulator in 32 bits, two in 16)
-                    const int buf = kSplit ? 0 : s, turn = kSplit ? u : u >> 1;
-                    ok = mbar_wait(dx_empty + buf, (turn & 1) ^ 1) && !*s_fail;
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + buf * 128;
-                    const uint64_t b = desc_sw128(w, L::weight_panel);
-                    for (int e = 0; e < steps_n; ++e) {
-                        const uint32_t at = dz + (e >> 2) * kPlanes * L::panel + (e & 3) * 32;
-                        const uint64_t be = b + (2048u * e >> 4);
-                        if constexpr (kSplit) {
-                            mma_f16(d, desc_sw128(at, 16), be, kBase | (192u >> 3 << 17), e > 0);
-                            mma_f16(d + 64, desc_sw128(at + L::panel, 16), be,
-                                    kBase | (128u >> 3 << 17), 1);
-                            mma_f16(d + 128, desc_sw128(at + 2 * L::panel, 16), be,
-                                    kBase | (64u >> 3 << 17), 1);
-                        } else {
-                            mma_f16(d, desc_sw128(at, 16), be, kBase | (k16 >> 3 << 17), e > 0);
-                        }
-                    }
-                    mma_commit(dx_full + buf);
-                }
                 if (q.want_w) {
                     if (kSplit) {
                         ok = mbar_wait(dw_empty, (u & 1) ^ 1) && !*s_fail;
@@ -1366,7 +1379,31 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     }
                     if (kSplit || t + step >= q.tiles) mma_commit(dw_full);
                 }
-                mma_commit(unit_empty + s);
+                mma_commit(x_empty + s);
+                if (q.want_x) {
+                    // (one accumulator in 32 bits, two in 16)
+                    const int buf = kSplit ? 0 : u & 1, turn = kSplit ? u : u >> 1;
+                    ok = mbar_wait(dx_empty + buf, (turn & 1) ^ 1) && !*s_fail;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * 128;
+                    const uint64_t b = desc_sw128(base + L::weight, L::weight_panel);
+                    for (int e = 0; e < steps_n; ++e) {
+                        const uint32_t at = dz + (e >> 2) * kPlanes * L::panel + (e & 3) * 32;
+                        const uint64_t be = b + (2048u * e >> 4);
+                        if constexpr (kSplit) {
+                            mma_f16(d, desc_sw128(at, 16), be, kBase | (192u >> 3 << 17), e > 0);
+                            mma_f16(d + 64, desc_sw128(at + L::panel, 16), be,
+                                    kBase | (128u >> 3 << 17), 1);
+                            mma_f16(d + 128, desc_sw128(at + 2 * L::panel, 16), be,
+                                    kBase | (64u >> 3 << 17), 1);
+                        } else {
+                            mma_f16(d, desc_sw128(at, 16), be, kBase | (k16 >> 3 << 17), e > 0);
+                        }
+                    }
+                    mma_commit(dx_full + buf);
+                }
+                mma_commit(dz_empty + s);
             }
             if (!ok) {
                 *s_fail = 1u;
@@ -1376,64 +1413,75 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         }
     } else if (warp < 9) {   // ---- operands
         const int mine = tid - 32;
-        float sum[L::panels][8];
+        float sum[kPanels][V], none[kPanels][V];
 #pragma unroll
-        for (int h = 0; h < L::panels; ++h)
+        for (int h = 0; h < kPanels; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[h][e] = 0.0f;
-        // a tile's tensors, on their way to the L2
-        auto fetch = [&](int64_t t) {
-            if (t >= q.tiles) return;
-            const int64_t left = q.rows - t * kBlock;
-            const uint32_t rows = (uint32_t)(left < kBlock ? left : kBlock);
-            const auto one = [&](const void* p, int cols) {
-                prefetch_l2(static_cast<const T*>(p) + t * kBlock * cols,
-                            rows * cols * (uint32_t)sizeof(T) & ~15u);
-            };
-            one(q.grad_y, q.n);
-            if (kAct != kActNone) one(q.pre, q.n);
-            if (q.want_w) one(q.x, q.k);
-        };
-        if (q.ahead && warp == 1 && elect_one())
-            for (int a = 1; a < kBackAhead; ++a) fetch(first + (int64_t)a * step);
+            for (int e = 0; e < V; ++e) sum[h][e] = none[h][e] = 0.0f;
         int u = 0;
         bool ok = true;
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
-            const int s = u & 1;
-            ok = warp_all(mbar_wait(unit_empty + s, ((u >> 1) & 1) ^ 1) && !*s_fail);
-            if (!ok) break;
-            const int64_t r0 = t * kBlock, left = q.rows - r0;
+            const int s = u % L::units, turn = u / L::units;   // (raw tiles and units are as many)
+            const int64_t row0 = t * kBlock, left = q.rows - row0;
             const int rows = (int)(left < kBlock ? left : kBlock);
+            if (q.raw) ok = warp_all(mbar_wait(raw_full + s, turn & 1) && !*s_fail);
+            if (!ok) break;
+            const T* raw = reinterpret_cast<const T*>(smem + L::raw + s * 3 * L::raw_tensor);
+            constexpr int kNext = L::raw_tensor / (int)sizeof(T);
             unsigned char* unit = smem + s * L::unit;
-            if (q.ahead && warp == 1 && elect_one()) fetch(t + (int64_t)kBackAhead * step);
-            make_operands<T, kAct>(q, unit, r0, rows, mine, sum);
+            if (q.want_w) {
+                ok = warp_all(mbar_wait(x_empty + s, (turn & 1) ^ 1) && !*s_fail);
+                if (!ok) break;
+                if (q.vec_k)
+                    make_operand<T, kActNone, kPanels, false>(unit + L::operand, raw + 2 * kNext,
+                                                              nullptr, rows, q.k, true, mine, none);
+                else
+                    make_operand<T, kActNone, kPanels, false>(
+                        unit + L::operand,
+                        q.raw ? raw + 2 * kNext : static_cast<const T*>(q.x) + row0 * q.k, nullptr,
+                        rows, q.k, false, mine, none);
+            }
+            ok = warp_all(mbar_wait(dz_empty + s, (turn & 1) ^ 1) && !*s_fail);
+            if (!ok) break;
+            if (q.vec_n)
+                make_operand<T, kAct, kPanels, true>(unit, raw, raw + kNext, rows, q.n, true, mine,
+                                                     sum);
+            else
+                make_operand<T, kAct, kPanels, true>(
+                    unit, q.raw ? raw : static_cast<const T*>(q.grad_y) + row0 * q.n,
+                    q.raw ? raw + kNext : static_cast<const T*>(q.pre) + row0 * q.n, rows, q.n,
+                    false, mine, sum);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(unit_full + s);
+            if (lane == 0) {
+                mbar_arrive(unit_full + s);
+                mbar_arrive(raw_empty + s);
+            }
         }
-        if (ok && q.sums)   // the next unit is free once the MMAs of its last tile are done
-            ok = mbar_wait(unit_empty + (u & 1), ((u >> 1) & 1) ^ 1) && !*s_fail;
         if (!ok) *s_fail = 1u;
-        if (q.sums) {   // 32 rows of threads by halves: in a warp, then between the warps
+        if (q.sums) {   // the rows of threads: in a warp, then between the warps
+            constexpr int kLanes = kPanel / V;
 #pragma unroll
-            for (int h = 0; h < L::panels; ++h)
+            for (int h = 0; h < kPanels; ++h)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], 8);
-                    sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], 16);
-                }
-            float* all = reinterpret_cast<float*>(smem + (u & 1) * L::unit);
-            if (lane < 8)
+                for (int e = 0; e < V; ++e)
 #pragma unroll
-                for (int h = 0; h < L::panels; ++h)
+                    for (int d = kLanes; d < 32; d *= 2)
+                        sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], d);
+            // (every raw tile has been read by all of these warps)
+            float* all = reinterpret_cast<float*>(smem + L::raw);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (lane < kLanes)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        all[(warp - 1) * kBackSide<T> + h * kPanel + lane * 8 + e] = sum[h][e];
+                for (int h = 0; h < kPanels; ++h)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        all[(warp - 1) * L::side + h * kPanel + lane * V + e] = sum[h][e];
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (mine < q.n) {
                 float v[8];
 #pragma unroll
-                for (int w = 0; w < 8; ++w) v[w] = all[w * kBackSide<T> + mine];
+                for (int w = 0; w < 8; ++w) v[w] = all[w * L::side + mine];
                 q.sums[(int64_t)blockIdx.x * q.n + mine] =
                     ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
             }
@@ -1849,8 +1897,9 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
     q.k = (int)k;
     q.n = (int)n;
     const bool act = c.act != kActNone;
-    q.ahead = aligned16(c.grad_y) && (!act || aligned16(c.pre)) && aligned16(c.x);
-    q.fast = q.ahead && n % 8 == 0 && k % 8 == 0;
+    q.raw = aligned16(c.grad_y) && (!act || aligned16(c.pre)) && aligned16(c.x);
+    q.vec_n = q.raw && n % VecOf<T>::n == 0;
+    q.vec_k = q.raw && k % VecOf<T>::n == 0;
     q.vec_w = aligned16(c.weight) && k % 8 == 0;
     q.want_x = c.grad_x != nullptr;
     q.want_w = c.grad_weight != nullptr;
@@ -1861,10 +1910,17 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
     q.out.out = c.grad_x;
     q.out.vec = vec4<T>(q.out);
     const unsigned ctas = (unsigned)(q.tiles < n_sms ? q.tiles : n_sms);
-    auto* kernel = c.act == kActSilu   ? k_linear_narrow<T, kActSilu>
-                   : c.act == kActRelu ? k_linear_narrow<T, kActRelu>
-                                       : k_linear_narrow<T, kActNone>;
-    cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kBackThreads), BackSmem<T>::bytes, s, q, st);
+    const auto run = [&](auto panels) {
+        constexpr int kPanels = decltype(panels)::value;
+        auto* kernel = c.act == kActSilu   ? k_linear_narrow<T, kActSilu, kPanels>
+                       : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels>
+                                           : k_linear_narrow<T, kActNone, kPanels>;
+        return launch_pdl(kernel, dim3(ctas), dim3(kBackThreads), BackSmem<T, kPanels>::bytes, s, q,
+                          st);
+    };
+    cudaError_t e = k <= kPanel && n <= kPanel
+                        ? run(std::integral_constant<int, 1>())
+                        : run(std::integral_constant<int, kBackSide<T> / kPanel>());
     if (e == cudaSuccess && c.grad_bias)
         e = launch_pdl(k_linear_sums, dim3((unsigned)ceil_div(n, 32)), dim3(32, 32), 0, s,
                        (const float*)sp.sums, (int64_t)ctas, n, c.grad_bias);
@@ -1940,10 +1996,15 @@ cudaError_t prepare_three() {
     return e;
 }
 
-template <typename T, int kAct>
+template <typename T, int kPanels>
 cudaError_t prepare_narrow() {
-    return cudaFuncSetAttribute(k_linear_narrow<T, kAct>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, BackSmem<T>::bytes);
+    cudaError_t e = cudaSuccess;
+    for (auto* f : {k_linear_narrow<T, kActNone, kPanels>, k_linear_narrow<T, kActSilu, kPanels>,
+                    k_linear_narrow<T, kActRelu, kPanels>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     BackSmem<T, kPanels>::bytes);
+    return e;
 }
 
 }  // namespace
@@ -1963,12 +2024,9 @@ cudaError_t prepare_linear() {
     e = prepare_three<float, 3, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256>();
-    if (e == cudaSuccess) e = prepare_narrow<float, kActNone>();
-    if (e == cudaSuccess) e = prepare_narrow<float, kActSilu>();
-    if (e == cudaSuccess) e = prepare_narrow<float, kActRelu>();
-    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActNone>();
-    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActSilu>();
-    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, kActRelu>();
+    if (e == cudaSuccess) e = prepare_narrow<float, 1>();
+    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 1>();
+    if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 2>();
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_linear_stream<float>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
