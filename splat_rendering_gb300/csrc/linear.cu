@@ -1093,8 +1093,9 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 
 // --------------------------------------------- narrow layers, gradients --
 // All gradients of a narrow layer in one pass over dy, z and x: a persistent CTA
-// per SM, tiles of 128 rows.  One thread keeps raw tiles coming (contiguous bulk
-// copies), eight warps make dz and x into operands (and add up dz's columns), one
+// per SM, tiles of 128 rows.  One thread keeps raw rows coming (contiguous bulk
+// copies, in pieces of 16 KB: a whole tile at a time, its way in was 44 % of the
+// time), eight warps make dz and x into operands (and add up dz's columns), one
 // thread issues the MMAs, eight warps finish dx.  dz's tile, 128 rows of 128
 // bytes a panel, is an MN-major left operand of dW = dz^T x (its rows are the
 // contraction) and, the same bytes, a K-major one of dx = dz W (its rows are
@@ -1106,7 +1107,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 // (mid lo among them, in columns that are not read); lo hi is a second one, into
 // the columns of hi lo.  They are drained every tile (128 of K) into registers:
 // the rows of hi, and those of mid, are parts of their own.  dx as in the
-// forward kernel.  There is room for one tile's operands and one raw tile: x's
+// forward kernel.  There is room for one tile's operands and its raw rows: x's
 // are made while the MMAs of dx run, which do not need them.
 constexpr int kBackThreads = 576;   // warps: MMAs, eight of operands, eight of the epilogue, copies
 template <typename T>
@@ -1137,10 +1138,10 @@ struct BackSmem {
     // a warp's exchange is 32 x 32 words; in 32 bits, for want of room, 32 x 8
     static constexpr int exchange = weight + planes * kPanels * weight_panel;
     static constexpr int exchange_bytes = planes == 3 ? 8 * 1024 : 8 * 4096;
-    static constexpr int raw = exchange + exchange_bytes;      // dy, z, x
-    static constexpr int raw_tensor = kBlock * side * (int)sizeof(T);
-    static constexpr int raws = units;
-    static constexpr int bars = raw + raws * 3 * raw_tensor;
+    static constexpr int raw = exchange + exchange_bytes;
+    static constexpr int piece = 16 * 1024, pieces = 6;        // of x's rows, or of dy's and z's
+    static constexpr int rows_x = piece / (side * (int)sizeof(T));
+    static constexpr int bars = raw + pieces * piece;
     static constexpr int bytes = bars + 256 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory of a narrow layer's gradients");
 };
@@ -1176,16 +1177,17 @@ __device__ __forceinline__ void put_columns(unsigned char* at, uint32_t plane_by
     }
 }
 
-// The operand of a tile, [rows, cols] at `src` (times the activation's slope at `pre`, its columns
-// added to `sum`, where kDz), by a thread that has 16 bytes' columns of every kStep-th row: rows
-// behind the last, and columns up to the next 16, are zeros.  `vec`: src is a raw tile in shared
-// memory of whole 16-byte vectors.
-template <typename T, int kAct, int kPanels, bool kDz>
+// kRows rows of an operand, [rows, cols] at `src` (times the activation's slope at `pre`, its
+// columns added to `sum`, where kDz), by a thread that has 16 bytes' columns of every kStep-th row:
+// rows behind the last, and columns up to the next 16, are zeros.  `vec`: src is a raw piece in
+// shared memory of whole 16-byte vectors.
+template <typename T, int kAct, int kPanels, bool kDz, int kRows>
 __device__ __forceinline__ void make_operand(unsigned char* operand, const T* src, const T* pre,
                                              int rows, int cols, bool vec, int mine,
                                              float (&sum)[kPanels][VecOf<T>::n]) {
     using L = BackSmem<T, kPanels>;
-    constexpr int V = VecOf<T>::n, kLanes = kPanel / V, kStep = 256 / kLanes, kBatch = 4;
+    constexpr int V = VecOf<T>::n, kLanes = kPanel / V, kStep = 256 / kLanes;
+    constexpr int kBatch = kRows / kStep < 4 ? kRows / kStep : 4;
     const int c = mine % kLanes * V, r0 = mine / kLanes, cols16 = (cols + 15) / 16 * 16;
 #pragma unroll
     for (int h = 0; h < kPanels; ++h) {
@@ -1197,7 +1199,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
             const T* s = src + r0 * cols + col;
             const T* z = pre + r0 * cols + col;
 #pragma unroll
-            for (int i0 = 0; i0 < kBlock / kStep; i0 += kBatch) {
+            for (int i0 = 0; i0 < kRows / kStep; i0 += kBatch) {
                 float v[kBatch][V], w[kBatch][V];   // (all loads, then all stores)
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -1220,7 +1222,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
             }
         } else {
 #pragma unroll 1
-            for (int r = r0; r < kBlock; r += kStep) {
+            for (int r = r0; r < kRows; r += kStep) {
                 float v[V], w[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -1248,12 +1250,13 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     using L = BackSmem<T, kPanels>;
     constexpr int kPlanes = L::planes, V = VecOf<T>::n;
     constexpr bool kSplit = kPlanes == 3;
+    constexpr int kRowsX = L::rows_x, kRowsZ = kAct == kActNone ? L::rows_x : L::rows_x / 2;
     constexpr uint32_t kDw = kSplit ? 192 : 256;   // columns: dx below, dW from here
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::bars);
-    uint64_t* raw_empty = raw_full + 2;
-    uint64_t* unit_full = raw_empty + 2;
+    uint64_t* raw_empty = raw_full + L::pieces;
+    uint64_t* unit_full = raw_empty + L::pieces;
     uint64_t* dz_empty = unit_full + 2;
     uint64_t* x_empty = dz_empty + 2;
     uint64_t* dx_full = x_empty + 2;
@@ -1266,9 +1269,11 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (known to be the same in a warp)
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < L::pieces; ++s) {
             mbar_init(raw_full + s);
             mbar_init_n(raw_empty + s, 8);
+        }
+        for (int s = 0; s < 2; ++s) {
             mbar_init_n(unit_full + s, 8);
             mbar_init(dz_empty + s);
             mbar_init(x_empty + s);
@@ -1304,43 +1309,45 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     const uint32_t tmem = *s_taddr;
     const int first = blockIdx.x, step = gridDim.x;
     if (warp == 17) {
-        if (q.raw && elect_one()) {   // ---- raw tiles
-            int u = 0;
+        if (q.raw && elect_one()) {   // ---- raw pieces, in the order in which they are used
+            int f = 0;
             bool ok = true;
-            for (int64_t t = first; t < q.tiles; t += step, ++u) {
-                const int s = u % L::raws;
-                ok = mbar_wait(raw_empty + s, ((u / L::raws) & 1) ^ 1) && !*s_fail;
-                if (!ok) break;
-                const int64_t left = q.rows - t * kBlock;
-                const uint32_t rows = (uint32_t)(left < kBlock ? left : kBlock);
-                unsigned char* dst = smem + L::raw + s * 3 * L::raw_tensor;
-                const uint32_t of_n = rows * q.n * (uint32_t)sizeof(T);
-                const uint32_t of_k = q.want_w ? rows * q.k * (uint32_t)sizeof(T) : 0u;
-                // (the last rows need not end on 16 bytes)
-                const auto one = [&](int i, const void* p, int cols, uint32_t bytes, bool rest) {
-                    const T* src = static_cast<const T*>(p) + t * kBlock * cols;
-                    unsigned char* at = dst + i * L::raw_tensor;
-                    if (rest) {
-                        for (uint32_t e = (bytes & ~15u) / sizeof(T); e < bytes / sizeof(T); ++e)
-                            reinterpret_cast<T*>(at)[e] = src[e];
-                    } else if (bytes & ~15u) {
-                        bulk_copy(at, src, bytes & ~15u, raw_full + s);
-                    }
-                };
-#pragma unroll
-                for (int rest = 1; rest >= 0; --rest) {
-                    if (!rest)
-                        expect_bytes(raw_full + s, (kAct != kActNone ? 2 : 1) * (of_n & ~15u) +
-                                                       (of_k & ~15u));
-                    one(0, q.grad_y, q.n, of_n, rest);
-                    if (kAct != kActNone) one(1, q.pre, q.n, of_n, rest);
-                    if (q.want_w) one(2, q.x, q.k, of_k, rest);
+            // `rows` rows of one tensor or two from row r on
+            const auto piece = [&](const void* p, const void* p2, int64_t r, int rows, int cols) {
+                const int s = f % L::pieces;
+                ok = mbar_wait(raw_empty + s, ((f / L::pieces) & 1) ^ 1) && !*s_fail;
+                if (!ok) return;
+                ++f;
+                const int64_t left = q.rows - r;
+                if (left < rows) rows = left > 0 ? (int)left : 0;
+                const uint32_t bytes = (uint32_t)rows * cols * (uint32_t)sizeof(T);
+                const uint32_t bulk = bytes & ~15u;   // (the last rows need not end on 16 bytes)
+                T* dst = reinterpret_cast<T*>(smem + L::raw + s * L::piece);
+                T* dst2 = dst + L::piece / 2 / (int)sizeof(T);
+                const T* src = static_cast<const T*>(p) + r * cols;
+                const T* src2 = static_cast<const T*>(p2) + r * cols;
+                for (uint32_t e = bulk / sizeof(T); e < bytes / sizeof(T); ++e) {
+                    dst[e] = src[e];
+                    if (p2) dst2[e] = src2[e];
                 }
+                expect_bytes(raw_full + s, p2 ? 2 * bulk : bulk);
+                if (bulk) {
+                    bulk_copy(dst, src, bulk, raw_full + s);
+                    if (p2) bulk_copy(dst2, src2, bulk, raw_full + s);
+                }
+            };
+            for (int64_t t = first; t < q.tiles && ok; t += step) {
+                const int64_t r = t * kBlock;
+                if (q.want_w)
+                    for (int i = 0; i < kBlock && ok; i += kRowsX)
+                        piece(q.x, nullptr, r + i, kRowsX, q.k);
+                for (int i = 0; i < kBlock && ok; i += kRowsZ)
+                    piece(q.grad_y, kAct != kActNone ? q.pre : nullptr, r + i, kRowsZ, q.n);
             }
             if (!ok) {   // give the copies in flight one more bounded wait
                 *s_fail = 1u;
-                for (int k = u > L::raws ? u - L::raws : 0; k < u; ++k)
-                    mbar_wait(raw_full + k % L::raws, (k / L::raws) & 1);
+                for (int k = f > L::pieces ? f - L::pieces : 0; k < f; ++k)
+                    mbar_wait(raw_full + k % L::pieces, (k / L::pieces) & 1);
             }
         }
     } else if (warp == 0) {
@@ -1418,45 +1425,65 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         for (int h = 0; h < kPanels; ++h)
 #pragma unroll
             for (int e = 0; e < V; ++e) sum[h][e] = none[h][e] = 0.0f;
-        int u = 0;
+        int u = 0, f = 0;
         bool ok = true;
+        // the piece in turn, or the place of row r in the tensor
+        const auto wait_piece = [&]() {
+            if (q.raw)
+                ok = warp_all(mbar_wait(raw_full + f % L::pieces, (f / L::pieces) & 1) && !*s_fail);
+            return ok;
+        };
+        const auto done_piece = [&]() {
+            __syncwarp();
+            if (q.raw && lane == 0) mbar_arrive(raw_empty + f % L::pieces);
+            ++f;
+        };
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
-            const int s = u % L::units, turn = u / L::units;   // (raw tiles and units are as many)
+            const int s = u % L::units, turn = u / L::units;
             const int64_t row0 = t * kBlock, left = q.rows - row0;
             const int rows = (int)(left < kBlock ? left : kBlock);
-            if (q.raw) ok = warp_all(mbar_wait(raw_full + s, turn & 1) && !*s_fail);
-            if (!ok) break;
-            const T* raw = reinterpret_cast<const T*>(smem + L::raw + s * 3 * L::raw_tensor);
-            constexpr int kNext = L::raw_tensor / (int)sizeof(T);
             unsigned char* unit = smem + s * L::unit;
             if (q.want_w) {
                 ok = warp_all(mbar_wait(x_empty + s, (turn & 1) ^ 1) && !*s_fail);
-                if (!ok) break;
-                if (q.vec_k)
-                    make_operand<T, kActNone, kPanels, false>(unit + L::operand, raw + 2 * kNext,
-                                                              nullptr, rows, q.k, true, mine, none);
-                else
-                    make_operand<T, kActNone, kPanels, false>(
-                        unit + L::operand,
-                        q.raw ? raw + 2 * kNext : static_cast<const T*>(q.x) + row0 * q.k, nullptr,
-                        rows, q.k, false, mine, none);
+#pragma unroll 1
+                for (int i = 0; i < kBlock && ok; i += kRowsX) {
+                    if (!wait_piece()) break;
+                    const T* raw =
+                        reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
+                    unsigned char* to = unit + L::operand + i * 128;
+                    if (q.vec_k)
+                        make_operand<T, kActNone, kPanels, false, kRowsX>(to, raw, nullptr, rows - i,
+                                                                          q.k, true, mine, none);
+                    else
+                        make_operand<T, kActNone, kPanels, false, kRowsX>(
+                            to, q.raw ? raw : static_cast<const T*>(q.x) + (row0 + i) * q.k, nullptr,
+                            rows - i, q.k, false, mine, none);
+                    done_piece();
+                }
             }
-            ok = warp_all(mbar_wait(dz_empty + s, (turn & 1) ^ 1) && !*s_fail);
+            if (ok) ok = warp_all(mbar_wait(dz_empty + s, (turn & 1) ^ 1) && !*s_fail);
+#pragma unroll 1
+            for (int i = 0; i < kBlock && ok; i += kRowsZ) {
+                if (!wait_piece()) break;
+                const T* raw = reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
+                const T* z = raw + L::piece / 2 / (int)sizeof(T);
+                unsigned char* to = unit + i * 128;
+                if (q.vec_n) {
+                    make_operand<T, kAct, kPanels, true, kRowsZ>(to, raw, z, rows - i, q.n, true,
+                                                                 mine, sum);
+                } else {
+                    const int64_t at = (row0 + i) * q.n;
+                    make_operand<T, kAct, kPanels, true, kRowsZ>(
+                        to, q.raw ? raw : static_cast<const T*>(q.grad_y) + at,
+                        q.raw ? z : static_cast<const T*>(q.pre) + at, rows - i, q.n, false, mine,
+                        sum);
+                }
+                done_piece();
+            }
             if (!ok) break;
-            if (q.vec_n)
-                make_operand<T, kAct, kPanels, true>(unit, raw, raw + kNext, rows, q.n, true, mine,
-                                                     sum);
-            else
-                make_operand<T, kAct, kPanels, true>(
-                    unit, q.raw ? raw : static_cast<const T*>(q.grad_y) + row0 * q.n,
-                    q.raw ? raw + kNext : static_cast<const T*>(q.pre) + row0 * q.n, rows, q.n,
-                    false, mine, sum);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(unit_full + s);
-                mbar_arrive(raw_empty + s);
-            }
+            if (lane == 0) mbar_arrive(unit_full + s);
         }
         if (!ok) *s_fail = 1u;
         if (q.sums) {   // the rows of threads: in a warp, then between the warps
@@ -1468,7 +1495,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
 #pragma unroll
                     for (int d = kLanes; d < 32; d *= 2)
                         sum[h][e] += __shfl_xor_sync(0xffffffffu, sum[h][e], d);
-            // (every raw tile has been read by all of these warps)
+            // (every raw piece has been read by all of these warps)
             float* all = reinterpret_cast<float*>(smem + L::raw);
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (lane < kLanes)
