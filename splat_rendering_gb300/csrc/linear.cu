@@ -1177,6 +1177,20 @@ __device__ __forceinline__ void put_columns(unsigned char* at, uint32_t plane_by
     }
 }
 
+// 16 bytes of shared memory, said to be that: a pointer that may also be global costs a generic
+// load, whose latency is several times a shared one's.
+template <typename T>
+__device__ __forceinline__ typename Pack<T, VecOf<T>::n>::Raw lds16(uint32_t at) {
+    typename Pack<T, VecOf<T>::n>::Raw r;
+    if constexpr (sizeof(T) == 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(at));
+    else
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
+    return r;
+}
+
 // kRows rows of an operand, [rows, cols] at `src` (times the activation's slope at `pre`, its
 // columns added to `sum`, where kDz), by a thread that has 16 bytes' columns of every kStep-th row:
 // rows behind the last, and columns up to the next 16, are zeros.  `vec`: src is a raw piece in
@@ -1196,24 +1210,29 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
         unsigned char* dst = operand + h * L::planes * L::panel + r0 * 128 +
                              (((c >> 3) ^ (r0 & 7)) << 4) + (c & 7) * 2;
         if (vec) {
-            const T* s = src + r0 * cols + col;
-            const T* z = pre + r0 * cols + col;
+            const uint32_t s = smem_u32(src + r0 * cols + col);
+            const uint32_t z = smem_u32(pre + r0 * cols + col);
+            const uint32_t pitch = (uint32_t)(kStep * cols) * (uint32_t)sizeof(T);
 #pragma unroll
             for (int i0 = 0; i0 < kRows / kStep; i0 += kBatch) {
-                float v[kBatch][V], w[kBatch][V];   // (all loads, then all stores)
+                typename Pack<T, V>::Raw a[kBatch], b[kBatch];   // (all loads, then all stores)
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {   // (what lies behind the last row is shared too)
+                    a[i] = lds16<T>(s + (i0 + i) * pitch);
+                    if (kAct != kActNone) b[i] = lds16<T>(z + (i0 + i) * pitch);
+                }
+                float v[kBatch][V], w[kBatch][V];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int r = (i0 + i) * kStep;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[i][e] = w[i][e] = 0.0f;
-                    if (r0 + r < rows && col < cols) {
-                        Pack<T, V>::load(s + r * cols, v[i]);
-                        if (kAct != kActNone) Pack<T, V>::load(z + r * cols, w[i]);
-                    }
+                    Pack<T, V>::open(a[i], v[i]);
+                    if (kAct != kActNone) Pack<T, V>::open(b[i], w[i]);
+                    to_dz<T, kAct>(v[i], w[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    to_dz<T, kAct>(v[i], w[i]);
+                    const bool in = r0 + (i0 + i) * kStep < rows && col < cols;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[i][e] = in ? v[i][e] : 0.0f;
                     if (kDz)
 #pragma unroll
                         for (int e = 0; e < V; ++e) sum[h][e] += v[i][e];
