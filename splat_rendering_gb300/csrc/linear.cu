@@ -1094,8 +1094,8 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 // --------------------------------------------- narrow layers, gradients --
 // All gradients of a narrow layer in one pass over dy, z and x: a persistent CTA
 // per SM, tiles of 128 rows.  One thread keeps raw rows coming (contiguous bulk
-// copies, in pieces of 16 KB: a whole tile at a time, its way in was 44 % of the
-// time), eight warps make dz and x into operands (and add up dz's columns), one
+// copies, in pieces of 16 or 32 KB: a whole tile at a time, its way in was 44 %
+// of the time), eight warps make dz and x into operands (and add up dz's columns), one
 // thread issues the MMAs, eight warps finish dx.  dz's tile, 128 rows of 128
 // bytes a panel, is an MN-major left operand of dW = dz^T x (its rows are the
 // contraction) and, the same bytes, a K-major one of dx = dz W (its rows are
@@ -1139,7 +1139,9 @@ struct BackSmem {
     static constexpr int exchange = weight + planes * kPanels * weight_panel;
     static constexpr int exchange_bytes = planes == 3 ? 8 * 1024 : 8 * 4096;
     static constexpr int raw = exchange + exchange_bytes;
-    static constexpr int piece = 16 * 1024, pieces = 6;        // of x's rows, or of dy's and z's
+    // pieces of x's rows, or of dy's and z's: whole tiles of x in 32 bits
+    static constexpr int piece = planes == 3 ? 32 * 1024 : 16 * 1024;
+    static constexpr int pieces = 96 * 1024 / piece;
     static constexpr int rows_x = piece / (side * (int)sizeof(T));
     static constexpr int bars = raw + pieces * piece;
     static constexpr int bytes = bars + 256 + 1024;
