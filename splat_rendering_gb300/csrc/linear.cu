@@ -227,9 +227,10 @@ constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epil
 constexpr int kChunk = 2;              // panels per drained sum (32 bits)
 constexpr int kGroup = 16;             // row blocks whose tiles lie side by side in time
 
-template <int kPlanes, int kN>
+template <int kPlanes, int kN, int kCtas>
 struct ProductSmem {
-    static constexpr int a = kBlock * kPanel * 2, b = kN * kPanel * 2;
+    static constexpr int rows_b = kN / kCtas;   // of B, in each CTA of a pair
+    static constexpr int a = kBlock * kPanel * 2, b = rows_b * kPanel * 2;
     static constexpr int stage = kPlanes * (a + b);
     static constexpr int exchange_bytes = 8 * 32 * 32 * 4;
     static constexpr int stages = (227 * 1024 - 1024 - exchange_bytes - 256) / stage;
@@ -282,6 +283,58 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         "[%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(col), "r"(row), "r"(plane), "r"(smem_u32(mbar))
         : "memory");
+}
+// ---- pairs of CTAs (cta_group::2) on one tile
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// the place of this CTA's shared address in the pair's first CTA
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+    return at;
+}
+__device__ __forceinline__ void arrive_at(uint32_t mbar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
+                 : "memory");
+}
+// into this CTA's shared memory, counted on the first one's barrier
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int col, int row,
+                                              int plane, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(col), "r"(row), "r"(plane), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// arrives at the barrier's place in both CTAs
+__device__ __forceinline__ void mma_commit_pair(uint64_t* mbar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(mbar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* s_taddr, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(s_taddr)),
+                 "r"(cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
 }
 // Whether any of the epilogue's threads has `v`: one decision for all.
 __device__ __forceinline__ bool epilogue_any(bool v) {
@@ -440,11 +493,13 @@ __device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
 }
 
 // T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
-// as its rows.
-template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
-__global__ void __launch_bounds__(kProductThreads)
+// as its rows.  kCtas: 1, or a pair of CTAs on a tile of 256 rows, each with its 128 rows of A and
+// of the sums, and half of B's; the first one issues the MMAs of both.
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
+__global__ void __launch_bounds__(kProductThreads) __cluster_dims__(kCtas, 1, 1)
 k_linear_product(const __grid_constant__ Product q, LearnState* st) {
-    using L = ProductSmem<kPlanes, kN>;
+    using L = ProductSmem<kPlanes, kN, kCtas>;
+    constexpr bool kPair = kCtas == 2;
     constexpr int kAcc = kPlanes == 3 ? 2 * kN : kN;   // columns of an accumulator
     constexpr int kHalf = kN / 2;                      // columns of an epilogue thread
     static_assert(2 * kAcc <= 512, "tensor memory");
@@ -466,16 +521,22 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s);
-            mbar_init_n(acc_empty + s, 8);
+            mbar_init_n(acc_empty + s, 8 * kCtas);
         }
         mbar_init(drain);
         *s_fail = 0u;
         fence_async_smem();
     }
-    if (warp == 1) tmem_alloc(s_taddr, 2 * kAcc);
+    if (warp == 1) {
+        if constexpr (kPair) tmem_alloc_pair(s_taddr, 2 * kAcc);
+        else tmem_alloc(s_taddr, 2 * kAcc);
+    }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();   // the barriers are there
     tc_fence_after();
+    const uint32_t rank = kPair ? cluster_rank() : 0u;
+    const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
     const uint32_t tmem = *s_taddr;
     pdl_next();
     pdl_begin();
@@ -494,7 +555,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
         if (elect_one()) {   // ---- copies
             int n = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first; t < total && ok; t += step) {
                 int i, j, k0, k1, part;
                 place(t, &i, &j, &k0, &k1, &part);
                 for (int k = k0; k < k1; ++k, ++n) {
@@ -502,16 +563,23 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                     ok = mbar_wait(empty + s, ((n / L::stages) & 1) ^ 1) && !*s_fail;
                     if (!ok) break;
                     unsigned char* dst = smem + s * L::stage;
-                    expect_bytes(full + s, L::stage);
+                    const uint32_t bar = kPair ? in_first(full + s) : 0u;
+                    const auto load = [&](void* to, const CUtensorMap* map, int col, int row, int p) {
+                        if constexpr (kPair) tma_load_pair(to, map, col, row, p, bar);
+                        else tma_load(to, map, col, row, p, full + s);
+                    };
+                    if (rank == 0) expect_bytes(full + s, kCtas * L::stage);
+                    const int row_a = (i * kCtas + (int)rank) * kBlock;
+                    const int row_b = j * kN + (int)rank * L::rows_b;
 #pragma unroll
                     for (int p = 0; p < kPlanes; ++p) {
                         if (kAMn) {
 #pragma unroll
                             for (int c = 0; c < kBlock / kPanel; ++c)
-                                tma_load(dst + p * L::a + c * kPanel * kPanel * 2, &q.a,
-                                         i * kBlock + c * kPanel, k * kPanel, p, full + s);
+                                load(dst + p * L::a + c * kPanel * kPanel * 2, &q.a,
+                                     row_a + c * kPanel, k * kPanel, p);
                         } else {
-                            tma_load(dst + p * L::a, &q.a, k * kPanel, i * kBlock, p, full + s);
+                            load(dst + p * L::a, &q.a, k * kPanel, row_a, p);
                         }
                     }
                     dst += kPlanes * L::a;
@@ -519,31 +587,40 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                     for (int p = 0; p < kPlanes; ++p) {
                         if (kBMn) {
 #pragma unroll
-                            for (int c = 0; c < kN / kPanel; ++c)
-                                tma_load(dst + p * L::b + c * kPanel * kPanel * 2, &q.b,
-                                         j * kN + c * kPanel, k * kPanel, p, full + s);
+                            for (int c = 0; c < L::rows_b / kPanel; ++c)
+                                load(dst + p * L::b + c * kPanel * kPanel * 2, &q.b,
+                                     row_b + c * kPanel, k * kPanel, p);
                         } else {
-                            tma_load(dst + p * L::b, &q.b, k * kPanel, j * kN, p, full + s);
+                            load(dst + p * L::b, &q.b, k * kPanel, row_b, p);
                         }
                     }
                 }
             }
             if (!ok) {   // give the copies in flight one more bounded wait
+                // (the second CTA's are counted by the first, which it meets before it leaves)
                 *s_fail = 1u;
-                for (int k = n > L::stages ? n - L::stages : 0; k < n; ++k)
+                for (int k = n > L::stages ? n - L::stages : 0; k < n && rank == 0; ++k)
                     mbar_wait(full + k % L::stages, (k / L::stages) & 1);
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {   // ---- MMAs
+        if (rank == 0 && elect_one()) {   // ---- MMAs
             constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                        (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                                        ((uint32_t)(kN >> 3) << 17) |
-                                       ((uint32_t)(kBlock >> 4) << 24);
+                                       ((uint32_t)(kCtas * kBlock >> 4) << 24);
+            const auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t more) {
+                if constexpr (kPair) mma_f16_pair(d, a, b, idesc, more);
+                else mma_f16(d, a, b, idesc, more);
+            };
+            const auto commit = [&](uint64_t* bar) {
+                if constexpr (kPair) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
             const uint32_t base = smem_u32(smem);
             int n = 0, it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first; t < total && ok; t += step) {
                 int i, j, k0, k1, part;
                 place(t, &i, &j, &k0, &k1, &part);
                 const int chunk = kPlanes == 3 ? kChunk : k1 - k0;
@@ -572,34 +649,38 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                             const uint32_t ea = (kAMn ? 2048u : 32u) * e >> 4;
                             const uint32_t eb = (kBMn ? 2048u : 32u) * e >> 4;
                             const uint32_t more = k > kc || e > 0;
-                            mma_f16(d, a[0] + ea, b[0] + eb, idesc, more);
+                            mma(d, a[0] + ea, b[0] + eb, more);
                             if constexpr (kPlanes == 3) {
-                                mma_f16(d + kN, a[0] + ea, b[2] + eb, idesc, more);
-                                mma_f16(d + kN, a[1] + ea, b[1] + eb, idesc, 1);
-                                mma_f16(d + kN, a[2] + ea, b[0] + eb, idesc, 1);
-                                mma_f16(d + kN, a[0] + ea, b[1] + eb, idesc, 1);
-                                mma_f16(d + kN, a[1] + ea, b[0] + eb, idesc, 1);
+                                mma(d + kN, a[0] + ea, b[2] + eb, more);
+                                mma(d + kN, a[1] + ea, b[1] + eb, 1);
+                                mma(d + kN, a[2] + ea, b[0] + eb, 1);
+                                mma(d + kN, a[0] + ea, b[1] + eb, 1);
+                                mma(d + kN, a[1] + ea, b[0] + eb, 1);
                             }
                         }
-                        mma_commit(empty + s);
+                        commit(empty + s);
                     }
-                    if (ok) mma_commit(acc_full + buf);
+                    if (ok) commit(acc_full + buf);
                 }
             }
             if (!ok) {
                 *s_fail = 1u;
-                mma_commit(drain);
+                commit(drain);
                 mbar_wait(drain, 0);
             }
         }
     } else {   // ---- epilogue
         const int group = (warp - 2) >> 2, quarter = warp & 3;   // (warps 2 .. 9)
         float4* x = reinterpret_cast<float4*>(smem + L::exchange) + (warp - 2) * 256;
+        const auto release = [&](int buf) {
+            if constexpr (kPair) arrive_at(in_first(acc_empty + buf));
+            else mbar_arrive(acc_empty + buf);
+        };
         int it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        for (int t = first; t < total; t += step) {
             int i, j, k0, k1, part;
             place(t, &i, &j, &k0, &k1, &part);
-            const int64_t r0 = (int64_t)i * kBlock + quarter * 32;
+            const int64_t r0 = ((int64_t)i * kCtas + rank) * kBlock + quarter * 32;
             const int64_t base = (int64_t)part * q.m * q.n;
             // 32 columns from `col` of the tile, a row in each lane
             auto emit = [&](const float (&v)[32], int col) {
@@ -637,7 +718,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                    if (lane == 0) release(buf);
                 }
                 if (ok) {
 #pragma unroll
@@ -668,7 +749,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                         if (h + 32 == kHalf) {
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(acc_empty + buf);
+                            if (lane == 0) release(buf);
                         }
                         emit(v, group * kHalf + h);
                     }
@@ -684,9 +765,13 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();   // the pair's MMAs and arrivals reach into both
     tc_fence_after();
     if (tid == 0 && *s_fail) atomicOr(&st->error, kErrTimeout);
-    if (warp == 1) tmem_dealloc(tmem, 2 * kAcc);
+    if (warp == 1) {
+        if constexpr (kPair) tmem_dealloc_pair(tmem, 2 * kAcc);
+        else tmem_dealloc(tmem, 2 * kAcc);
+    }
 }
 
 // The parts of a product added in a fixed order, and finished: a thread has four columns, of few
@@ -1713,10 +1798,13 @@ int splits_of(int64_t tiles, int64_t panels, int n_sms) {
 }
 // Columns of a tile: an MMA of N = 256 takes little longer than one of 128.
 int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
+// Pairs of CTAs where tiles of 256 x 256 are not half empty.
+bool paired(int64_t m) { return m > kBlock; }
 size_t part_floats(int planes, int64_t m, int64_t n, int64_t k) {
-    const int64_t tiles = ceil_div(m, kBlock) * ceil_div(n, tile_n(planes, n));
-    if (tiles == 0 || tiles > kMostSms) return 0;
-    const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms);
+    const int kn = tile_n(planes, n), ctas = kn == 256 && paired(m) ? 2 : 1;
+    const int64_t tiles = ceil_div(m, kBlock * ctas) * ceil_div(n, kn);
+    if (tiles == 0 || tiles > kMostSms / ctas) return 0;
+    const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms / ctas);
     return s > 1 ? (size_t)s * m * n : 0;
 }
 
@@ -1808,29 +1896,31 @@ cudaError_t join(const Product& q, const float* parts, int n_sms, cudaStream_t s
                       parts);
 }
 
-template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
 cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                        LearnState* st, int n_sms, cudaStream_t s) {
-    q.tiles_m = (int)ceil_div(q.m, kBlock);
+    using L = ProductSmem<kPlanes, kN, kCtas>;
+    q.tiles_m = (int)ceil_div(q.m, kBlock * kCtas);
     q.tiles_n = (int)ceil_div(q.n, kN);
     q.panels = (int)ceil_div(k, kPanel);
     const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
-    q.splits = tiles <= n_sms ? splits_of(tiles, q.panels, n_sms) : 1;
-    if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : kN))
+    const int groups = n_sms / kCtas;   // of CTAs that share a tile
+    q.splits = tiles <= groups ? splits_of(tiles, q.panels, groups) : 1;
+    if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : L::rows_b))
         return cudaErrorInvalidValue;
     const auto launch = [&](auto kernel, const Product& p) {
         const int64_t total = tiles * p.splits;
-        return launch_pdl(kernel, dim3((unsigned)(total < n_sms ? total : n_sms)),
-                          dim3(kProductThreads), ProductSmem<kPlanes, kN>::bytes, s, p, st);
+        return launch_pdl(kernel, dim3((unsigned)((total < groups ? total : groups) * kCtas)),
+                          dim3(kProductThreads), L::bytes, s, p, st);
     };
-    if (q.splits == 1) return launch(k_linear_product<T, kPlanes, kN, kAMn, kBMn>, q);
+    if (q.splits == 1) return launch(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas>, q);
     Product p = q;
     p.bias = nullptr;
     p.residual = p.pre = nullptr;
     p.out = parts;
     p.act = kActNone;
     p.vec = q.n % 4 == 0;
-    cudaError_t e = launch(k_linear_product<float, kPlanes, kN, kAMn, kBMn>, p);
+    cudaError_t e = launch(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas>, p);
     if (e != cudaSuccess) return e;
     return join<T>(q, parts, n_sms, s);
 }
@@ -1839,11 +1929,13 @@ template <typename T, bool kAMn, bool kBMn>
 cudaError_t product(const Product& q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                     LearnState* st, int n_sms, cudaStream_t s) {
     if constexpr (sizeof(T) == 4)
-        return product_as<T, 3, 128, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
     else if (tile_n(1, q.n) == 128)
-        return product_as<T, 1, 128, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 1, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
+    else if (paired(q.m))
+        return product_as<T, 1, 256, kAMn, kBMn, 2>(q, a, b, k, parts, st, n_sms, s);
     else
-        return product_as<T, 1, 256, kAMn, kBMn>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 1, 256, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
 }
 
 bool aligned_to4(const void* p, int size) {
@@ -2026,21 +2118,21 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
     return e;
 }
 
-template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn>
+template <typename T, int kPlanes, int kN, int kCtas, bool kAMn, bool kBMn>
 cudaError_t prepare_one() {
-    constexpr int bytes = ProductSmem<kPlanes, kN>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(k_linear_product<T, kPlanes, kN, kAMn, kBMn>,
+    constexpr int bytes = ProductSmem<kPlanes, kN, kCtas>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && sizeof(T) == 2)
-        e = cudaFuncSetAttribute(k_linear_product<float, kPlanes, kN, kAMn, kBMn>,
+        e = cudaFuncSetAttribute(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e;
 }
-template <typename T, int kPlanes, int kN>
+template <typename T, int kPlanes, int kN, int kCtas>
 cudaError_t prepare_three() {
-    cudaError_t e = prepare_one<T, kPlanes, kN, false, false>();
-    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, false, true>();
-    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, true, true>();
+    cudaError_t e = prepare_one<T, kPlanes, kN, kCtas, false, false>();
+    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, kCtas, false, true>();
+    if (e == cudaSuccess) e = prepare_one<T, kPlanes, kN, kCtas, true, true>();
     return e;
 }
 
@@ -2069,9 +2161,10 @@ cudaError_t prepare_linear() {
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(f);
-    e = prepare_three<float, 3, 128>();
-    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128>();
-    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256>();
+    e = prepare_three<float, 3, 128, 1>();
+    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128, 1>();
+    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256, 1>();
+    if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256, 2>();
     if (e == cudaSuccess) e = prepare_narrow<float, 1>();
     if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 1>();
     if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 2>();
