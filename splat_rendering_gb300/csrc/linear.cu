@@ -197,9 +197,9 @@ k_linear_sums(const float* __restrict__ part, int64_t blocks, int64_t cols,
 // -------------------------------------------------------------- products --
 // One kernel for the three products, a persistent CTA per SM.  Roles: one
 // thread keeps a ring of operand stages filled by TMA (out of range: zeros), one
-// issues the MMAs into one of two accumulators in tensor memory, and eight
-// warps finish the other (four per half of the tile's columns, a thread per
-// row): bias, activation, residual, rounding; through a swizzled exchange in
+// issues the MMAs into one of two accumulators in tensor memory, and the other
+// warps finish the other (four per half or quarter of the tile's columns, a
+// thread per row): bias, activation, residual, rounding; through a swizzled exchange in
 // shared memory, so that a warp stores whole sectors.
 //
 // In 32 bits the tensor cores' accumulation, which truncates, would be what
@@ -223,7 +223,9 @@ struct Product {
     bool vec;   // four columns at a time
 };
 
-constexpr int kProductThreads = 320;   // warps: copies, MMAs, eight of the epilogue
+// warps: copies, MMAs, and of the epilogue eight, or in 16 bits, where it has every tile's
+// activation to do within the MMAs' time, sixteen
+constexpr int epilogue_warps(int planes) { return planes == 3 ? 8 : 16; }
 constexpr int kChunk = 2;              // panels per drained sum (32 bits)
 constexpr int kGroup = 16;             // row blocks whose tiles lie side by side in time
 
@@ -232,7 +234,8 @@ struct ProductSmem {
     static constexpr int rows_b = kN / kCtas;   // of B, in each CTA of a pair
     static constexpr int a = kBlock * kPanel * 2, b = rows_b * kPanel * 2;
     static constexpr int stage = kPlanes * (a + b);
-    static constexpr int exchange_bytes = 8 * 32 * 32 * 4;
+    static constexpr int epilogue = epilogue_warps(kPlanes), threads = 64 + 32 * epilogue;
+    static constexpr int exchange_bytes = epilogue * 32 * 32 * 4;
     static constexpr int stages = (227 * 1024 - 1024 - exchange_bytes - 256) / stage;
     static constexpr int exchange = stages * stage;
     static constexpr int bars = exchange + exchange_bytes;
@@ -336,15 +339,16 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* s_taddr, uint32_t cols
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols));
 }
-// Whether any of the epilogue's threads has `v`: one decision for all.
+// Whether any of the epilogue's kThreads has `v`: one decision for all.
+template <int kThreads>
 __device__ __forceinline__ bool epilogue_any(bool v) {
     uint32_t any;
     __syncwarp();
     asm volatile(
-        "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred r, 1, 256, p;\n"
+        "{\n.reg .pred p, r;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred r, 1, %2, p;\n"
         "selp.u32 %0, 1, 0, r;\n}\n"
         : "=r"(any)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(kThreads)
         : "memory");
     return any != 0;
 }
@@ -496,12 +500,12 @@ __device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
 // as its rows.  kCtas: 1, or a pair of CTAs on a tile of 256 rows, each with its 128 rows of A and
 // of the sums, and half of B's; the first one issues the MMAs of both.
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
-__global__ void __launch_bounds__(kProductThreads) __cluster_dims__(kCtas, 1, 1)
+__global__ void __launch_bounds__(64 + 32 * epilogue_warps(kPlanes)) __cluster_dims__(kCtas, 1, 1)
 k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     using L = ProductSmem<kPlanes, kN, kCtas>;
     constexpr bool kPair = kCtas == 2;
     constexpr int kAcc = kPlanes == 3 ? 2 * kN : kN;   // columns of an accumulator
-    constexpr int kHalf = kN / 2;                      // columns of an epilogue thread
+    constexpr int kHalf = kN / (L::epilogue / 4);      // columns of an epilogue thread
     static_assert(2 * kAcc <= 512, "tensor memory");
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -521,7 +525,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full + s);
-            mbar_init_n(acc_empty + s, 8 * kCtas);
+            mbar_init_n(acc_empty + s, L::epilogue * kCtas);
         }
         mbar_init(drain);
         *s_fail = 0u;
@@ -670,7 +674,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             }
         }
     } else {   // ---- epilogue
-        const int group = (warp - 2) >> 2, quarter = warp & 3;   // (warps 2 .. 9)
+        const int group = (warp - 2) >> 2, quarter = warp & 3;   // (from warp 2 on)
         float4* x = reinterpret_cast<float4*>(smem + L::exchange) + (warp - 2) * 256;
         const auto release = [&](int buf) {
             if constexpr (kPair) arrive_at(in_first(acc_empty + buf));
@@ -701,7 +705,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                 for (int kc = k0; kc < k1; kc += kChunk, ++it) {
                     const int buf = it & 1;
                     ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
-                    ok = !epilogue_any(!ok);
+                    ok = !epilogue_any<32 * L::epilogue>(!ok);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + buf * kAcc + ((uint32_t)(quarter * 32) << 16) +
@@ -732,7 +736,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             } else {
                 const int buf = it & 1;
                 ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
-                ok = !epilogue_any(!ok);
+                ok = !epilogue_any<32 * L::epilogue>(!ok);
                 if (ok) {
                     tc_fence_after();
                     const uint32_t acc = tmem + buf * kAcc + ((uint32_t)(quarter * 32) << 16) +
@@ -1911,7 +1915,7 @@ cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, f
     const auto launch = [&](auto kernel, const Product& p) {
         const int64_t total = tiles * p.splits;
         return launch_pdl(kernel, dim3((unsigned)((total < groups ? total : groups) * kCtas)),
-                          dim3(kProductThreads), L::bytes, s, p, st);
+                          dim3(L::threads), L::bytes, s, p, st);
     };
     if (q.splits == 1) return launch(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas>, q);
     Product p = q;
