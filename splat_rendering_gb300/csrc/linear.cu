@@ -97,6 +97,53 @@ __device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]
     }
 }
 
+// Eight columns of a row as they were loaded: nothing waits for them before they are opened.
+template <typename T>
+struct Chunk {
+    static constexpr int V = VecOf<T>::n;
+    typename Pack<T, V>::Raw raw[8 / V];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int h = 0; h < 8 / V; ++h) raw[h] = Pack<T, V>::raw_last(p + h * V);
+    }
+    __device__ __forceinline__ void open(float (&v)[8]) const {
+#pragma unroll
+        for (int h = 0; h < 8 / V; ++h) {
+            float u[V];
+            Pack<T, V>::open(raw[h], u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[h * V + e] = u[e];
+        }
+    }
+};
+
+// dy made dz = dy act'(z)
+template <int kAct, int V>
+__device__ __forceinline__ void to_dz(float (&v)[V], const float (&z)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if (kAct == kActRelu) v[e] = z[e] > 0.0f ? v[e] : 0.0f;
+        if (kAct == kActSilu) v[e] *= act_slope<kActSilu>(z[e]);
+    }
+}
+
+// Eight columns, 16 bytes of bfloat16 in each plane.
+template <int kPlanes>
+__device__ __forceinline__ void put_chunk(void* at, size_t plane_bytes, const float (&v)[8]) {
+    uint32_t w[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (kPlanes == 3)
+            split3(v[2 * e], v[2 * e + 1], w[e]);
+        else
+            w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
+    }
+#pragma unroll
+    for (int p = 0; p < kPlanes; ++p)
+        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(at) + p * plane_bytes) =
+            make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+}
+
 // A matrix [rows, cols] made into an operand: times the activation's slope at `pre` (the gradient
 // dz from dy), split into planes [planes][rows][pitch] of bfloat16, and its column sums taken, a
 // partial sum [cols] per block of rows.  A thread has eight columns of every (256 / tx)-th row.
@@ -128,36 +175,40 @@ k_linear_operand(const Operand q) {
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-    if (c < q.cols) {
-        const bool vec = q.vec && n == 8;
-#pragma unroll 4
-        for (int64_t r = r0 + ty; r < r1; r += step) {
-            float v[8];
-            load8(static_cast<const T*>(q.src) + r * q.cols + c, n, vec, v);
-            if (kAct != kActNone) {
-                float z[8];
-                load8(static_cast<const T*>(q.pre) + r * q.cols + c, n, vec, z);
+    const T* src = static_cast<const T*>(q.src) + c;
+    const T* pre = static_cast<const T*>(q.pre) + c;
+    const auto finish = [&](int64_t r, float (&v)[8], const float (&z)[8]) {
+        to_dz<kAct>(v, z);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = kAct == kActRelu ? (z[e] > 0.0f ? v[e] : 0.0f)
-                                            : v[e] * act_slope<kAct>(z[e]);
-            }
+        for (int e = 0; e < 8; ++e) sum[e] += e < n ? v[e] : 0.0f;
+        if (q.planes) put_chunk<kPlanes>(q.planes + r * q.pitch + c, q.plane * 2, v);
+    };
+    if (q.vec && n == 8) {
+        constexpr int kBatch = 4;   // rows whose loads are in flight together
+        for (int64_t r = r0 + ty; r < r1; r += kBatch * step) {
+            Chunk<T> a[kBatch], b[kBatch];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += e < n ? v[e] : 0.0f;
-            if (q.planes) {
-                uint32_t w[4][3];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (kPlanes == 3)
-                        split3(v[2 * e], v[2 * e + 1], w[e]);
-                    else
-                        w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t at = (r + i * step) * q.cols;
+                if (r + i * step < r1) {
+                    a[i].load(src + at);
+                    if (kAct != kActNone) b[i].load(pre + at);
                 }
-#pragma unroll
-                for (int p = 0; p < kPlanes; ++p)
-                    *reinterpret_cast<uint4*>(q.planes + p * q.plane + r * q.pitch + c) =
-                        make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float v[8], z[8];
+                a[i].open(v);
+                if (kAct != kActNone) b[i].open(z);
+                if (r + i * step < r1) finish(r + i * step, v, z);
+            }
+        }
+    } else if (n > 0) {
+        for (int64_t r = r0 + ty; r < r1; r += step) {
+            float v[8], z[8];
+            load8(src + r * q.cols, n, false, v);
+            if (kAct != kActNone) load8(pre + r * q.cols, n, false, z);
+            finish(r, v, z);
         }
     }
     if (!q.sums) return;
@@ -923,24 +974,6 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 }
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// Eight columns, 16 bytes of bfloat16 in each plane.
-template <int kPlanes>
-__device__ __forceinline__ void put_chunk(unsigned char* at, uint32_t plane_bytes,
-                                          const float (&v)[8]) {
-    uint32_t w[4][3];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (kPlanes == 3)
-            split3(v[2 * e], v[2 * e + 1], w[e]);
-        else
-            w[e][0] = pair_bf16(v[2 * e], v[2 * e + 1]);
-    }
-#pragma unroll
-    for (int p = 0; p < kPlanes; ++p)
-        *reinterpret_cast<uint4*>(at + p * plane_bytes) =
-            make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
@@ -1237,15 +1270,6 @@ struct BackSmem {
     static_assert(bytes <= 227 * 1024, "shared memory of a narrow layer's gradients");
 };
 
-template <typename T, int kAct, int V>
-__device__ __forceinline__ void to_dz(float (&v)[V], const float (&z)[V]) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        if (kAct == kActRelu) v[e] = z[e] > 0.0f ? v[e] : 0.0f;
-        if (kAct == kActSilu) v[e] *= act_slope<kActSilu>(z[e]);
-    }
-}
-
 // V columns (eight or sixteen bytes of bfloat16 in a plane).
 template <int kPlanes, int V>
 __device__ __forceinline__ void put_columns(unsigned char* at, uint32_t plane_bytes,
@@ -1317,7 +1341,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
                 for (int i = 0; i < kBatch; ++i) {
                     Pack<T, V>::open(a[i], v[i]);
                     if (kAct != kActNone) Pack<T, V>::open(b[i], w[i]);
-                    to_dz<T, kAct>(v[i], w[i]);
+                    to_dz<kAct>(v[i], w[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -1344,7 +1368,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
                     v[e] = one[0];
                     w[e] = z[0];
                 }
-                to_dz<T, kAct>(v, w);
+                to_dz<kAct>(v, w);
                 if (kDz)
 #pragma unroll
                     for (int e = 0; e < V; ++e) sum[h][e] += v[e];
