@@ -149,8 +149,7 @@ __device__ __forceinline__ void put_chunk(void* at, size_t plane_bytes, const fl
 // partial sum [cols] per block of rows.  A thread has eight columns of every (256 / tx)-th row.
 struct Operand {
     const void* src;
-    const void* pre;        // NULL: no activation
-    int act;
+    const void* pre;
     int64_t rows, cols;
     int64_t pitch;          // a multiple of 8
     __nv_bfloat16* planes;  // NULL: none are wanted
@@ -158,15 +157,15 @@ struct Operand {
     float* sums;            // NULL: none are wanted
     int tx;                 // threads along the columns: a power of two up to 32
     int64_t block_rows;
+    unsigned blocks, col_blocks;
     bool vec;
+};
+struct Operands {   // of one call: the first may be a gradient with its activation
+    Operand of[3];
 };
 
 template <typename T, int kPlanes, int kAct>
-__global__ void __launch_bounds__(256)
-k_linear_operand(const Operand q) {
-    __shared__ float s_sums[256 * 8];
-    pdl_next();
-    pdl_begin();
+__device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
     const int tx = threadIdx.x & (q.tx - 1), ty = threadIdx.x / q.tx, step = 256 / q.tx;
     const int64_t c = ((int64_t)blockIdx.y * q.tx + tx) * 8;
     const int n = (int)(q.cols - c < 8 ? q.cols - c : 8);
@@ -184,7 +183,7 @@ k_linear_operand(const Operand q) {
         if (q.planes) put_chunk<kPlanes>(q.planes + r * q.pitch + c, q.plane * 2, v);
     };
     if (q.vec && n == 8) {
-        constexpr int kBatch = 4;   // rows whose loads are in flight together
+        constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;   // rows whose loads are in flight together
         for (int64_t r = r0 + ty; r < r1; r += kBatch * step) {
             Chunk<T> a[kBatch], b[kBatch];
 #pragma unroll
@@ -224,6 +223,18 @@ k_linear_operand(const Operand q) {
         const int64_t col = (int64_t)blockIdx.y * q.tx * 8 + i;
         if (col < q.cols) q.sums[(int64_t)blockIdx.x * q.cols + col] = s_sums[i];
     }
+}
+
+template <typename T, int kPlanes, int kAct>
+__global__ void __launch_bounds__(256)
+k_linear_operands(const __grid_constant__ Operands all) {
+    __shared__ float s_sums[256 * 8];
+    pdl_next();
+    pdl_begin();
+    const Operand& q = all.of[blockIdx.z];
+    if (blockIdx.x >= q.blocks || blockIdx.y >= q.col_blocks) return;
+    if (blockIdx.z == 0) make_planes<T, kPlanes, kAct>(q, s_sums);
+    else make_planes<T, kPlanes, kActNone>(q, s_sums);
 }
 
 // The sums of `blocks` partial rows of `cols`: 32 columns a block, 32 rows of threads.
@@ -1826,10 +1837,10 @@ int splits_of(int64_t tiles, int64_t panels, int n_sms) {
 }
 // Columns of a tile: an MMA of N = 256 takes little longer than one of 128.
 int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
-// Pairs of CTAs where tiles of 256 x 256 are not half empty.
+// Pairs of CTAs where tiles of 256 rows are not half empty.
 bool paired(int64_t m) { return m > kBlock; }
 size_t part_floats(int planes, int64_t m, int64_t n, int64_t k) {
-    const int kn = tile_n(planes, n), ctas = kn == 256 && paired(m) ? 2 : 1;
+    const int kn = tile_n(planes, n), ctas = (planes == 3 || kn == 256) && paired(m) ? 2 : 1;
     const int64_t tiles = ceil_div(m, kBlock * ctas) * ceil_div(n, kn);
     if (tiles == 0 || tiles > kMostSms / ctas) return 0;
     const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms / ctas);
@@ -1885,34 +1896,45 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
     return s;
 }
 
-template <typename T, int kPlanes, int kAct>
-cudaError_t operand_as(const Operand& o, const OperandGrid& g, cudaStream_t s) {
-    return launch_pdl(k_linear_operand<T, kPlanes, kAct>,
-                      dim3((unsigned)g.blocks, (unsigned)g.col_blocks), dim3(256), 0, s, o);
-}
-
-// `src` (times the activation's slope at `pre`) as an operand: its planes in `planes`, where it is
-// not one as it lies, and its column sums.
+// A call's operands: those that have to be made are made by one launch.
 template <typename T>
-cudaError_t operand(Matrix* out, const void* src, const void* pre, int act, int64_t rows,
-                    int64_t cols, __nv_bfloat16* planes, float* sums, cudaStream_t s) {
-    constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    if (!pre) act = kActNone;
-    const bool as_is = kPlanes == 1 && act == kActNone && cols % 8 == 0 && aligned16(src);
-    const int64_t pitch = round8(cols);
-    *out = as_is ? Matrix{static_cast<const __nv_bfloat16*>(src), rows, cols, cols, 0, 1}
-                 : Matrix{planes, rows, cols, pitch, (size_t)rows * pitch, kPlanes};
-    if ((as_is || !planes) && !sums) return cudaSuccess;
-    const OperandGrid g = operand_grid(rows, cols);
-    const Operand o{src, pre, act, rows, cols, pitch, as_is ? nullptr : planes,
-                    (size_t)rows * pitch, sums, g.tx, g.block_rows,
-                    cols % VecOf<T>::n == 0 && aligned16(src) && aligned16(pre)};
-    switch (act) {
-        case kActSilu: return operand_as<T, kPlanes, kActSilu>(o, g, s);
-        case kActRelu: return operand_as<T, kPlanes, kActRelu>(o, g, s);
-        default: return operand_as<T, kPlanes, kActNone>(o, g, s);
+struct Maker {
+    static constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+    Operands all{};
+    int count = 0, act = kActNone;
+
+    // `src` (in the first one times the activation's slope at `pre`) as an operand: its planes in
+    // `planes` (NULL: not wanted), where it is not one as it lies, and its column sums
+    Matrix add(const void* src, const void* pre, int slope, int64_t rows, int64_t cols,
+               __nv_bfloat16* planes, float* sums) {
+        if (!pre) slope = kActNone;
+        const bool as_is =
+            kPlanes == 1 && slope == kActNone && cols % 8 == 0 && aligned16(src);
+        const int64_t pitch = round8(cols);
+        if (!((as_is || !planes) && !sums)) {
+            const OperandGrid g = operand_grid(rows, cols);
+            if (count == 0) act = slope;
+            all.of[count++] = Operand{src, pre, rows, cols, pitch, as_is ? nullptr : planes,
+                                      (size_t)rows * pitch, sums, g.tx, g.block_rows,
+                                      (unsigned)g.blocks, (unsigned)g.col_blocks,
+                                      cols % VecOf<T>::n == 0 && aligned16(src) && aligned16(pre)};
+        }
+        return as_is ? Matrix{static_cast<const __nv_bfloat16*>(src), rows, cols, cols, 0, 1}
+                     : Matrix{planes, rows, cols, pitch, (size_t)rows * pitch, kPlanes};
     }
-}
+    cudaError_t launch(cudaStream_t s) const {
+        if (count == 0) return cudaSuccess;
+        dim3 grid(1, 1, (unsigned)count);
+        for (int i = 0; i < count; ++i) {
+            if (all.of[i].blocks > grid.x) grid.x = all.of[i].blocks;
+            if (all.of[i].col_blocks > grid.y) grid.y = all.of[i].col_blocks;
+        }
+        return launch_pdl(act == kActSilu   ? k_linear_operands<T, kPlanes, kActSilu>
+                          : act == kActRelu ? k_linear_operands<T, kPlanes, kActRelu>
+                                            : k_linear_operands<T, kPlanes, kActNone>,
+                          grid, dim3(256), 0, s, all);
+    }
+};
 
 // (16 parts or fewer: a thread per four columns, each part's load behind the one before)
 template <typename T>
@@ -1957,7 +1979,8 @@ template <typename T, bool kAMn, bool kBMn>
 cudaError_t product(const Product& q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                     LearnState* st, int n_sms, cudaStream_t s) {
     if constexpr (sizeof(T) == 4)
-        return product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
+        return paired(q.m) ? product_as<T, 3, 128, kAMn, kBMn, 2>(q, a, b, k, parts, st, n_sms, s)
+                           : product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
     else if (tile_n(1, q.n) == 128)
         return product_as<T, 1, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
     else if (paired(q.m))
@@ -2044,9 +2067,10 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
                           (size_t)smem, s, narrow, st);
     }
     const Space sp = carve(ws, m, k, n, c.dtype);
-    Matrix x, w;
-    cudaError_t e = operand<T>(&x, c.x, nullptr, kActNone, m, k, sp.x, nullptr, s);
-    if (e == cudaSuccess) e = operand<T>(&w, c.weight, nullptr, kActNone, n, k, sp.w, nullptr, s);
+    Maker<T> make;
+    const Matrix x = make.add(c.x, nullptr, kActNone, m, k, sp.x, nullptr);
+    const Matrix w = make.add(c.weight, nullptr, kActNone, n, k, sp.w, nullptr);
+    const cudaError_t e = make.launch(s);
     if (e != cudaSuccess) return e;
     return product<T, false, false>(q, x, w, k, sp.parts, st, n_sms, s);
 }
@@ -2114,34 +2138,31 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
     }
     const Space sp = carve(ws, m, k, n, c.dtype);
     if (k <= kBackSide<T> && n <= kBackSide<T>) return narrow<T>(c, sp, st, n_sms, s);
-    Matrix dz, w, x;
-    cudaError_t e = cudaSuccess;
-    if (c.grad_x || c.grad_weight || c.grad_bias)
-        e = operand<T>(&dz, c.grad_y, c.act == kActNone ? nullptr : c.pre, c.act, m, n,
-                       c.grad_x || c.grad_weight ? sp.dz : nullptr,
-                       c.grad_bias ? sp.sums : nullptr, s);
+    Maker<T> make;
+    const Matrix dz = make.add(c.grad_y, c.act == kActNone ? nullptr : c.pre, c.act, m, n,
+                               c.grad_x || c.grad_weight ? sp.dz : nullptr,
+                               c.grad_bias ? sp.sums : nullptr);
+    const Matrix w = make.add(c.weight, nullptr, kActNone, n, k, c.grad_x ? sp.w : nullptr, nullptr);
+    const Matrix x = make.add(c.x, nullptr, kActNone, m, k, c.grad_weight ? sp.x : nullptr, nullptr);
+    cudaError_t e = make.launch(s);
     if (e == cudaSuccess && c.grad_bias)
         e = launch_pdl(k_linear_sums, dim3((unsigned)ceil_div(n, 32)), dim3(32, 32), 0, s,
                        (const float*)sp.sums, operand_grid(m, n).blocks, n, c.grad_bias);
     if (e == cudaSuccess && c.grad_x) {
-        e = operand<T>(&w, c.weight, nullptr, kActNone, n, k, sp.w, nullptr, s);
         Product q{};
         q.m = m;
         q.n = k;
         q.out = c.grad_x;
         q.vec = vec4<T>(q);
-        if (e == cudaSuccess)
-            e = product<T, false, true>(q, dz, w, n, sp.parts, st, n_sms, s);
+        e = product<T, false, true>(q, dz, w, n, sp.parts, st, n_sms, s);
     }
     if (e == cudaSuccess && c.grad_weight) {
-        e = operand<T>(&x, c.x, nullptr, kActNone, m, k, sp.x, nullptr, s);
         Product q{};
         q.m = n;
         q.n = k;
         q.out = c.grad_weight;
         q.vec = vec4<T>(q);
-        if (e == cudaSuccess)
-            e = product<T, true, true>(q, dz, x, m, sp.parts, st, n_sms, s);
+        e = product<T, true, true>(q, dz, x, m, sp.parts, st, n_sms, s);
     }
     return e;
 }
@@ -2190,6 +2211,7 @@ cudaError_t prepare_linear() {
     if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<EncodeTiled>(f);
     e = prepare_three<float, 3, 128, 1>();
+    if (e == cudaSuccess) e = prepare_three<float, 3, 128, 2>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 128, 1>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256, 1>();
     if (e == cudaSuccess) e = prepare_three<__nv_bfloat16, 1, 256, 2>();
