@@ -53,12 +53,6 @@ __device__ __forceinline__ float act_slope(float z) {
     if (kAct == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
     return 1.0f;
 }
-__device__ __forceinline__ float act_any(int act, float z) {
-    if (act == kActSilu) return act_of<kActSilu>(z);
-    if (act == kActRelu) return act_of<kActRelu>(z);
-    return z;
-}
-
 // ---------------------------------------------------------------- planes --
 // Two floats as three words of two bfloat16 each, whose sums they are (an infinity, or what rounds
 // to one, leaves NaNs over).
@@ -297,7 +291,9 @@ struct ProductSmem {
     static constexpr int a = kBlock * kPanel * 2, b = rows_b * kPanel * 2;
     static constexpr int stage = kPlanes * (a + b);
     static constexpr int epilogue = epilogue_warps(kPlanes), threads = 64 + 32 * epilogue;
-    static constexpr int exchange_bytes = epilogue * 32 * 32 * 4;
+    // a warp's exchange: 32 x 32 words, in 32 bits 32 x 8 for a third stage
+    static constexpr int warp_exchange = 32 * (kPlanes == 3 ? 8 : 32) * 4;
+    static constexpr int exchange_bytes = epilogue * warp_exchange;
     static constexpr int stages = (227 * 1024 - 1024 - exchange_bytes - 256) / stage;
     static constexpr int exchange = stages * stage;
     static constexpr int bars = exchange + exchange_bytes;
@@ -448,6 +444,26 @@ struct Four<__nv_bfloat16> {
     }
 };
 
+// One element of a result: bias (already in z), pre-activation, activation, residual.
+template <typename T, int kAct>
+__device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
+    const float one[1] = {z};
+    if (q.pre) Pack<T, 1>::store(static_cast<T*>(q.pre) + at, one);
+    float y[1] = {act_of<kAct>(z)};
+    if (q.residual) {
+        float f[1];
+        Pack<T, 1>::load(static_cast<const T*>(q.residual) + at, f);
+        y[0] = plus(y[0], f[0]);
+    }
+    Pack<T, 1>::store(static_cast<T*>(q.out) + at, y);
+}
+template <typename T>
+__device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
+    if (q.act == kActSilu) finish1<T, kActSilu>(q, z, at);
+    else if (q.act == kActRelu) finish1<T, kActRelu>(q, z, at);
+    else finish1<T, kActNone>(q, z, at);
+}
+
 // A lane's share of the block of 32 rows from r0 and 32 columns from c0.
 template <typename T>
 struct Share {
@@ -473,27 +489,33 @@ struct Share {
         }
     }
 
-    // `bias`: of its four columns
-    template <int kAct>
-    __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
-                                        const float (&bias)[4], int lane) {
+    __device__ __forceinline__ static void put(float4* x, const float (&v)[32], int lane) {
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             x[lane * 8 + (e ^ (lane & 7))] =
                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         __syncwarp();
+    }
+    __device__ __forceinline__ static float4 get(const float4* x, int r, int lane) {
+        return x[r * 8 + ((lane & 7) ^ (r & 7))];
+    }
+
+    // `bias`: of its four columns
+    template <int kAct>
+    __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
+                                        const float (&bias)[4], int lane) {
         T* out = static_cast<T*>(q.out) + at;
         T* pre = q.pre ? static_cast<T*>(q.pre) + at : nullptr;
-        const int cq = lane & 7, rq = lane >> 3;
+        const int rq = lane >> 3;
         const int64_t step = 4 * q.n;
         if (q.vec) {
             // (all loads, then all stores: the compiler keeps a load behind a store before it)
             float z[8][4];
+            put(x, v, lane);
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
-                const int r = 4 * h + rq;
-                const float4 u = x[r * 8 + (cq ^ (r & 7))];
+                const float4 u = get(x, 4 * h + rq, lane);
                 z[h][0] = plus(u.x, bias[0]);
                 z[h][1] = plus(u.y, bias[1]);
                 z[h][2] = plus(u.z, bias[2]);
@@ -516,10 +538,10 @@ struct Share {
             return;
         }
         const T* skip = q.residual ? static_cast<const T*>(q.residual) + at : nullptr;
+        put(x, v, lane);
 #pragma unroll 1
         for (int h = 0; 4 * h < rows; ++h) {
-            const int r = 4 * h + rq;
-            const float4 u = x[r * 8 + (cq ^ (r & 7))];
+            const float4 u = get(x, 4 * h + rq, lane);
             const float w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -544,18 +566,61 @@ struct Share {
     }
 };
 
-// One element of a result: bias (already in z), pre-activation, activation, residual.
-template <typename T>
-__device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
-    const float one[1] = {z};
-    if (q.pre) Pack<T, 1>::store(static_cast<T*>(q.pre) + at, one);
-    float y[1] = {act_any(q.act, z)};
-    if (q.residual) {
-        float f[1];
-        Pack<T, 1>::load(static_cast<const T*>(q.residual) + at, f);
-        y[0] = plus(y[0], f[0]);
+// The same where there is room for an exchange of 32 x 8 words only: eight columns at a time, of
+// which a lane has four of every 16th row; a warp stores sectors.
+template <typename T, int kAct>
+__device__ __forceinline__ void finish_small(const Product& q, float4* x, const float (&v)[32],
+                                             int64_t r0, int64_t c0, int64_t base, int lane) {
+    using Raw = typename Four<T>::Raw;
+    const int j = lane & 1, rq = lane >> 1;
+    const int64_t left = q.m - r0 - rq, at0 = base + (r0 + rq) * q.n + c0 + 4 * j;
+    const int rows = (int)(left < 32 ? left : 32);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            x[lane * 2 + (i ^ (lane >> 2 & 1))] =
+                make_float4(v[8 * m + 4 * i], v[8 * m + 4 * i + 1], v[8 * m + 4 * i + 2],
+                            v[8 * m + 4 * i + 3]);
+        __syncwarp();
+        const int64_t c = c0 + 8 * m + 4 * j;
+        const int n = (int)(q.n - c < 4 ? q.n - c : 4);
+        float z[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 16 * h + rq;
+            const float4 u = x[r * 2 + (j ^ (r >> 2 & 1))];
+            z[h][0] = u.x;
+            z[h][1] = u.y;
+            z[h][2] = u.z;
+            z[h][3] = u.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float bias = q.bias && e < n ? q.bias[c + e] : 0.0f;
+            z[0][e] = plus(z[0][e], bias);
+            z[1][e] = plus(z[1][e], bias);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (16 * h >= rows || n <= 0) continue;
+            const int64_t at = at0 + 16 * h * q.n + 8 * m;
+            if (q.vec) {
+                if (q.pre) *reinterpret_cast<Raw*>(static_cast<T*>(q.pre) + at) = Four<T>::pack(z[h]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
+                if (q.residual)
+                    Four<T>::add(*reinterpret_cast<const Raw*>(
+                                     static_cast<const T*>(q.residual) + at), z[h]);
+                *reinterpret_cast<Raw*>(static_cast<T*>(q.out) + at) = Four<T>::pack(z[h]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) finish1<T, kAct>(q, z[h][e], at + e);
+            }
+        }
     }
-    Pack<T, 1>::store(static_cast<T*>(q.out) + at, y);
 }
 
 // T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
@@ -737,7 +802,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
         }
     } else {   // ---- epilogue
         const int group = (warp - 2) >> 2, quarter = warp & 3;   // (from warp 2 on)
-        float4* x = reinterpret_cast<float4*>(smem + L::exchange) + (warp - 2) * 256;
+        float4* x = reinterpret_cast<float4*>(smem + L::exchange + (warp - 2) * L::warp_exchange);
         const auto release = [&](int buf) {
             if constexpr (kPair) arrive_at(in_first(acc_empty + buf));
             else mbar_arrive(acc_empty + buf);
@@ -750,14 +815,24 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             const int64_t base = (int64_t)part * q.m * q.n;
             // 32 columns from `col` of the tile, a row in each lane
             auto emit = [&](const float (&v)[32], int col) {
-                Share<T> share;
-                share.begin(q, r0, (int64_t)j * kN + col, base, lane);
-                float bias[4];
+                const int64_t c0 = (int64_t)j * kN + col;
+                if constexpr (kPlanes == 3) {
+                    if (kAMn || kBMn || q.act == kActNone)
+                        finish_small<T, kActNone>(q, x, v, r0, c0, base, lane);
+                    else if (q.act == kActSilu)
+                        finish_small<T, kActSilu>(q, x, v, r0, c0, base, lane);
+                    else
+                        finish_small<T, kActRelu>(q, x, v, r0, c0, base, lane);
+                } else {
+                    Share<T> share;
+                    share.begin(q, r0, c0, base, lane);
+                    float bias[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    bias[e] = q.bias && e < share.n ? q.bias[share.c + e] : 0.0f;
-                if (kAMn || kBMn) share.template end<kActNone>(q, x, v, bias, lane);
-                else share.end(q, x, v, bias, lane);
+                    for (int e = 0; e < 4; ++e)
+                        bias[e] = q.bias && e < share.n ? q.bias[share.c + e] : 0.0f;
+                    if (kAMn || kBMn) share.template end<kActNone>(q, x, v, bias, lane);
+                    else share.end(q, x, v, bias, lane);
+                }
             };
             bool ok = true;
             if constexpr (kPlanes == 3) {
@@ -1668,44 +1743,13 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         // 32 columns of dx, a row in each lane
         auto store_dx = [&](const float (&v)[32], int64_t t, int c0) {
             const int64_t r0 = t * kBlock + quarter * 32;
-            if constexpr (!kSplit) {
+            if constexpr (kSplit) {
+                finish_small<T, kActNone>(q.out, x, v, r0, c0, 0, lane);
+            } else {
                 Share<T> share;
                 const float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 share.begin(q.out, r0, c0, 0, lane);
                 share.template end<kActNone>(q.out, x, v, bias, lane);
-            } else {   // a smaller exchange: eight columns, a sector of each row, at a time
-                const int j = lane & 1, rows = (int)(q.out.m - r0 < 32 ? q.out.m - r0 : 32);
-                float* out = static_cast<float*>(q.out.out) + (r0 + (lane >> 1)) * q.k;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        x[lane * 2 + (i ^ (lane >> 2 & 1))] =
-                            make_float4(v[8 * m + 4 * i], v[8 * m + 4 * i + 1],
-                                        v[8 * m + 4 * i + 2], v[8 * m + 4 * i + 3]);
-                    __syncwarp();
-                    float4 f[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = 16 * h + (lane >> 1);
-                        f[h] = x[r * 2 + (j ^ (r >> 2 & 1))];
-                    }
-                    const int c = c0 + 8 * m + 4 * j;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (16 * h + (lane >> 1) >= rows || c >= q.k) continue;
-                        float* o = out + (int64_t)16 * h * q.k + c;
-                        if (q.out.vec) {
-                            *reinterpret_cast<float4*>(o) = f[h];
-                        } else {
-                            o[0] = f[h].x;
-                            if (c + 1 < q.k) o[1] = f[h].y;
-                            if (c + 2 < q.k) o[2] = f[h].z;
-                            if (c + 3 < q.k) o[3] = f[h].w;
-                        }
-                    }
-                }
             }
         };
         bool ok = true;
