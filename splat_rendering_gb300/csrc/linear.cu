@@ -567,8 +567,8 @@ struct Share {
 };
 
 // The same where there is room for an exchange of 32 x 8 words only: eight columns at a time, of
-// which a lane has four of every 16th row; a warp stores sectors.
-template <typename T, int kAct>
+// which a lane has four of every 16th row; a warp stores sectors.  (kPlain: the sums are the result.)
+template <typename T, int kAct, bool kPlain = false>
 __device__ __forceinline__ void finish_small(const Product& q, float4* x, const float (&v)[32],
                                              int64_t r0, int64_t c0, int64_t base, int lane) {
     using Raw = typename Four<T>::Raw;
@@ -598,6 +598,7 @@ __device__ __forceinline__ void finish_small(const Product& q, float4* x, const 
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+            if (kPlain) continue;
             const float bias = q.bias && e < n ? q.bias[c + e] : 0.0f;
             z[0][e] = plus(z[0][e], bias);
             z[1][e] = plus(z[1][e], bias);
@@ -607,10 +608,11 @@ __device__ __forceinline__ void finish_small(const Product& q, float4* x, const 
             if (16 * h >= rows || n <= 0) continue;
             const int64_t at = at0 + 16 * h * q.n + 8 * m;
             if (q.vec) {
-                if (q.pre) *reinterpret_cast<Raw*>(static_cast<T*>(q.pre) + at) = Four<T>::pack(z[h]);
+                if (!kPlain && q.pre)
+                    *reinterpret_cast<Raw*>(static_cast<T*>(q.pre) + at) = Four<T>::pack(z[h]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
-                if (q.residual)
+                if (!kPlain && q.residual)
                     Four<T>::add(*reinterpret_cast<const Raw*>(
                                      static_cast<const T*>(q.residual) + at), z[h]);
                 *reinterpret_cast<Raw*>(static_cast<T*>(q.out) + at) = Four<T>::pack(z[h]);
@@ -817,7 +819,9 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             auto emit = [&](const float (&v)[32], int col) {
                 const int64_t c0 = (int64_t)j * kN + col;
                 if constexpr (kPlanes == 3) {
-                    if (kAMn || kBMn || q.act == kActNone)
+                    if (kAMn || kBMn)
+                        finish_small<T, kActNone, true>(q, x, v, r0, c0, base, lane);
+                    else if (q.act == kActNone)
                         finish_small<T, kActNone>(q, x, v, r0, c0, base, lane);
                     else if (q.act == kActSilu)
                         finish_small<T, kActSilu>(q, x, v, r0, c0, base, lane);
@@ -1744,7 +1748,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         auto store_dx = [&](const float (&v)[32], int64_t t, int c0) {
             const int64_t r0 = t * kBlock + quarter * 32;
             if constexpr (kSplit) {
-                finish_small<T, kActNone>(q.out, x, v, r0, c0, 0, lane);
+                finish_small<T, kActNone, true>(q.out, x, v, r0, c0, 0, lane);
             } else {
                 Share<T> share;
                 const float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
