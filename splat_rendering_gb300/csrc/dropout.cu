@@ -15,36 +15,36 @@ namespace pulsar {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;   // vectors a thread has in flight
+constexpr int kAhead = 2;   // vectors a thread has in flight
 
-__device__ __forceinline__ uint4 philox(uint64_t counter, uint64_t key) {
+constexpr int kRounds = 7;
+
+struct Draw {
+    uint32_t key[kRounds][2];   // of each round
+    uint64_t offset;
+    const int64_t* counter;     // added to the offset; may be NULL
+    uint32_t least;             // the smallest word that keeps an element
+    float scale;
+};
+
+__device__ __forceinline__ uint4 philox(uint64_t counter, const Draw& d) {
     uint32_t c0 = (uint32_t)counter, c1 = (uint32_t)(counter >> 32), c2 = 0, c3 = 0;
-    uint32_t k0 = (uint32_t)key, k1 = (uint32_t)(key >> 32);
 #pragma unroll
-    for (int r = 0; r < 7; ++r) {
+    for (int r = 0; r < kRounds; ++r) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[r][0];
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[r][1];
         c1 = (uint32_t)b;
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     return make_uint4(c0, c1, c2, c3);
 }
-
-struct Draw {
-    uint64_t seed, offset;
-    const int64_t* counter;   // added to the offset; may be NULL
-    uint32_t least;           // the smallest word that keeps an element
-    float scale;
-};
 
 // Four elements from their words.
 template <bool kSkip>
 __device__ __forceinline__ void keep4(const Draw& d, uint64_t block, const float* x, const float* r,
                                       float* y) {
-    const uint4 u = philox(block, d.seed);
+    const uint4 u = philox(block, d);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -57,7 +57,7 @@ __device__ __forceinline__ void keep4(const Draw& d, uint64_t block, const float
 // residual: a thread writes what it alone has read.)
 template <typename T, int V, bool kSkip>
 __global__ void __launch_bounds__(kThreads)
-k_dropout(const T* x, const T* residual, int64_t n, Draw d, T* out) {
+k_dropout(const T* x, const T* residual, int64_t n, const __grid_constant__ Draw d, T* out) {
     pdl_begin();
     const uint64_t first = d.offset + (d.counter ? (uint64_t)*d.counter : 0u);
     const int64_t vectors = n / V, step = (int64_t)gridDim.x * kThreads;
@@ -109,7 +109,7 @@ k_dropout(const T* x, const T* residual, int64_t n, Draw d, T* out) {
 // Tensors at any element alignment: four elements a thread, one at a time.
 template <typename T, bool kSkip>
 __global__ void __launch_bounds__(kThreads)
-k_dropout_any(const T* x, const T* residual, int64_t n, Draw d, T* out) {
+k_dropout_any(const T* x, const T* residual, int64_t n, const __grid_constant__ Draw d, T* out) {
     pdl_begin();
     const uint64_t first = d.offset + (d.counter ? (uint64_t)*d.counter : 0u);
     const int64_t blocks = (n + 3) / 4, step = (int64_t)gridDim.x * kThreads;
@@ -137,13 +137,17 @@ k_dropout_any(const T* x, const T* residual, int64_t n, Draw d, T* out) {
 template <typename T, bool kSkip>
 cudaError_t run(const DropoutCall& c, int n_sms, cudaStream_t s) {
     constexpr int V = VecOf<T>::n;
-    const Draw d{c.seed, (uint64_t)c.offset, c.counter, c.least, c.scale};
+    Draw d{{}, (uint64_t)c.offset, c.counter, c.least, c.scale};
+    for (uint32_t r = 0; r < kRounds; ++r) {
+        d.key[r][0] = (uint32_t)c.seed + r * 0x9E3779B9u;
+        d.key[r][1] = (uint32_t)(c.seed >> 32) + r * 0xBB67AE85u;
+    }
     const T *x = static_cast<const T*>(c.x), *r = static_cast<const T*>(c.residual);
     T* out = static_cast<T*>(c.out);
     const bool vec = aligned16(x) && aligned16(r) && aligned16(out);
     const int64_t threads = vec ? ceil_div(c.n, (int64_t)V * kAhead) : ceil_div(c.n, 4);
     int64_t blocks = ceil_div(threads, kThreads);
-    if (blocks > n_sms * 8) blocks = n_sms * 8;
+    if (blocks > n_sms * 16) blocks = n_sms * 16;
     return launch_pdl(vec ? k_dropout<T, V, kSkip> : k_dropout_any<T, kSkip>,
                       dim3((unsigned)blocks), dim3(kThreads), 0, s, x, r, c.n, d, out);
 }

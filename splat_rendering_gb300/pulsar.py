@@ -412,8 +412,14 @@ def _code(dtype, kind: str) -> int:
     return code
 
 
+_VALUES = {}   # as _CODES' values: the calls that small work waits for ask for them directly
+
+
 def _dtype_code(dtype) -> int:
-    return _code(dtype, "value")
+    code = _VALUES.get(dtype)
+    if code is None:
+        code = _VALUES[dtype] = _code(dtype, "value")
+    return code
 
 
 def _index_code(dtype) -> int:
@@ -627,37 +633,56 @@ class Learner:
             steps, abc, eps, dt, p_out, self._stream(stream)), "pulsar_orthogonalize")
         return out
 
-    def _layer_shape(self, x, weight, act):
-        """(rows, inputs, outputs, activation) of a linear layer's call."""
-        if weight.dim() != 2:
-            raise ValueError(f"weight has shape {tuple(weight.shape)}, wanted [outputs, inputs]")
-        outputs, inputs = weight.shape
-        shape = x.shape
-        if len(shape) < 1 or shape[-1] != inputs:
+    def _alike(self, *ts):
+        """Whether the tensors are as a call wants its inputs: contiguous, on the handle's device,
+        of the first one's type.  (`_tensor` says of each what is wrong; a small call's time is
+        that of its checks.)"""
+        device, dtype = self.device, ts[0].dtype
+        for t in ts:
+            if t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+                return False
+        return True
+
+    def _layer(self, x, weight, act):
+        """(rows, inputs, outputs, activation, type, y's shape) of a linear layer's call."""
+        shape, wanted = x.shape, weight.shape
+        if len(wanted) != 2:
+            raise ValueError(f"weight has shape {tuple(wanted)}, wanted [outputs, inputs]")
+        outputs, inputs = wanted
+        if not shape or shape[-1] != inputs:
             raise ValueError(f"x has shape {tuple(shape)}, wanted [..., {inputs}]")
         a = ACT.get(act)
         if a is None:
             raise ValueError(f"act is one of {sorted(ACT)}, got {act!r}")
-        return self._product(shape[:-1]), inputs, outputs, a
+        dt = _dtype_code(x.dtype)
+        if not self._alike(x, weight):
+            self._tensor(x, "x")
+            self._tensor(weight, "weight", None, x.dtype)
+        if len(shape) == 2:
+            rows = shape[0]
+            return rows, inputs, outputs, a, dt, (rows, outputs)
+        return self._product(shape[:-1]), inputs, outputs, a, dt, (*shape[:-1], outputs)
 
     def linear(self, x, weight, bias=None, residual=None, act: str = "none", out=None, pre=None,
                want_pre: bool = False, stream=None):
         """(y, z): z = x weight^T + bias and y = act(z) + residual of x [..., inputs], weight
         [outputs, inputs], bias [outputs] (float32) and residual [..., outputs].  z, which
         linear_backward reads where there is an activation, is None unless wanted (or given)."""
-        rows, inputs, outputs, a = self._layer_shape(x, weight, act)
+        rows, inputs, outputs, a, dt, shape = self._layer(x, weight, act)
         dtype = x.dtype
-        dt = _dtype_code(dtype)
-        shape = (*x.shape[:-1], outputs)
+        p_bias = p_residual = p_pre = None
+        if bias is not None:
+            p_bias = self._tensor(bias, "bias", (outputs,), self._torch.float32)
+        if residual is not None:
+            p_residual = self._tensor(residual, "residual", shape, dtype)
         out, p_out = self._out(out, "out", shape, dtype, stream)
-        p_pre = None
         if want_pre or pre is not None:
             pre, p_pre = self._out(pre, "pre", shape, dtype, stream)
-        _check(self._lib.pulsar_linear_forward(
-            self.handle, self._tensor(x, "x"), self._tensor(weight, "weight", None, dtype), rows,
-            inputs, outputs, self._tensor(bias, "bias", (outputs,), self._torch.float32),
-            self._tensor(residual, "residual", shape, dtype), a, dt, p_out, p_pre,
-            self._stream(stream)), "pulsar_linear_forward")
+        code = self._lib.pulsar_linear_forward(
+            self.handle, x.data_ptr(), weight.data_ptr(), rows, inputs, outputs, p_bias, p_residual,
+            a, dt, p_out, p_pre, self._stream(stream))
+        if code:
+            raise PulsarError(code, "pulsar_linear_forward")
         return out, pre
 
     def linear_backward(self, grad_y, x, weight, pre=None, act: str = "none", grad_x=None,
@@ -666,12 +691,12 @@ class Learner:
         """(grad_x, grad_weight, grad_bias) of `linear` for its x, weight and z (`pre`, needed
         where there is an activation); those not in `want` (and not given) are None and not
         computed.  The residual's gradient is grad_y."""
-        rows, inputs, outputs, a = self._layer_shape(x, weight, act)
+        rows, inputs, outputs, a, dt, shape = self._layer(x, weight, act)
         dtype, f32 = x.dtype, self._torch.float32
-        dt = _dtype_code(dtype)
-        shape = (*x.shape[:-1], outputs)
         if a and pre is None:
             raise ValueError(f"pre is needed for act={act!r}")
+        p_y = self._tensor(grad_y, "grad_y", shape, dtype)
+        p_pre = None if pre is None else self._tensor(pre, "pre", shape, dtype)
         p_x = p_weight = p_bias = None
         if grad_x is not None or "x" in want:
             grad_x, p_x = self._out(grad_x, "grad_x", x.shape, dtype, stream)
@@ -680,11 +705,11 @@ class Learner:
                                               stream)
         if grad_bias is not None or "bias" in want:
             grad_bias, p_bias = self._out(grad_bias, "grad_bias", (outputs,), f32, stream)
-        _check(self._lib.pulsar_linear_backward(
-            self.handle, self._tensor(grad_y, "grad_y", shape, dtype), self._tensor(x, "x"),
-            self._tensor(weight, "weight", None, dtype), self._tensor(pre, "pre", shape, dtype),
-            rows, inputs, outputs, a, dt, p_x, p_weight, p_bias, self._stream(stream)),
-            "pulsar_linear_backward")
+        code = self._lib.pulsar_linear_backward(
+            self.handle, p_y, x.data_ptr(), weight.data_ptr(), p_pre, rows, inputs, outputs, a, dt,
+            p_x, p_weight, p_bias, self._stream(stream))
+        if code:
+            raise PulsarError(code, "pulsar_linear_backward")
         return grad_x, grad_weight, grad_bias
 
     def dropout(self, x, p: float, seed: int, offset: int = 0, counter=None, residual=None,
@@ -697,12 +722,16 @@ class Learner:
         dt = _dtype_code(dtype)
         if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 63:   # (ctypes would cut them)
             raise ValueError(f"seed and offset are whole numbers of 64 bits, got {seed}, {offset}")
-        if counter is not None and counter.numel() != 1:
-            raise ValueError(f"counter has {counter.numel()} elements, wanted 1")
+        p_x, p_residual, p_counter = self._tensor(x, "x"), None, None
+        if residual is not None:
+            p_residual = self._tensor(residual, "residual", x.shape, dtype)
+        if counter is not None:
+            if counter.numel() != 1:
+                raise ValueError(f"counter has {counter.numel()} elements, wanted 1")
+            p_counter = self._tensor(counter, "counter", None, self._torch.int64)
         out, p_out = self._out(out, "out", x.shape, dtype, stream)
-        _check(self._lib.pulsar_dropout(
-            self.handle, self._tensor(x, "x"), self._tensor(residual, "residual", x.shape, dtype),
-            x.numel(), p, seed, offset,
-            self._tensor(counter, "counter", None, self._torch.int64), dt, p_out,
-            self._stream(stream)), "pulsar_dropout")
+        code = self._lib.pulsar_dropout(self.handle, p_x, p_residual, x.numel(), p, seed, offset,
+                                        p_counter, dt, p_out, self._stream(stream))
+        if code:
+            raise PulsarError(code, "pulsar_dropout")
         return out
