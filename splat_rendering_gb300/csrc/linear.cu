@@ -970,39 +970,60 @@ k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part)
 }
 
 // -------------------------------------------------------------- few rows --
-// Up to kFewRows rows are bound by reading the weights once: a warp per output
-// takes the products in 32 bits, its lanes along the inputs.
-constexpr int kFewRows = 4;
+// Up to kFewRows rows are bound by reading the weights once: the products are
+// taken in 32 bits, `per` warps to an output, their lanes along the inputs: so
+// many that a lane has up to eight vectors of the weights to take, four of them
+// in flight (a row of 4096 into 2048 outputs in 16 bits: 5.1 us in a chain of
+// launches, 2.5 by the bytes; one warp to an output, which leaves the SMs one or
+// two blocks each, 5.8, and with four rows 10.3 instead of 6.9).
+constexpr int kFewRows = 8;
 
 template <typename T, int V, int kRows>
 __global__ void __launch_bounds__(256)
-k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k,
-              const Product q) {
+k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k, int per,
+              const __grid_constant__ Product q) {
+    __shared__ float s_sum[8][kRows];
     pdl_begin();
-    const int lane = threadIdx.x & 31;
-    const int64_t j = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    if (j >= q.n) return;
-    const T* w = weight + j * k;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & (per - 1);
+    const int64_t j = blockIdx.x * (int64_t)(8 / per) + warp / per;
     float sum[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) sum[r] = 0.0f;
-#pragma unroll 8
-    for (int64_t c = lane * V; c < k; c += 32 * V) {
-        float u[V];
-        Pack<T, V>::load(w + c, u);
+    if (j < q.n) {
+        const T* w = weight + j * k;
+        const int64_t step = (int64_t)per * 32 * V;
+        constexpr int kBatch = 4;
+        for (int64_t c0 = (part * 32 + lane) * V; c0 < k; c0 += kBatch * step) {
+            typename Pack<T, V>::Raw u[kBatch];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float v[V];
-            Pack<T, V>::load(x + r * k + c, v);
+            for (int i = 0; i < kBatch; ++i)
+                if (c0 + i * step < k) u[i] = Pack<T, V>::raw_last(w + c0 + i * step);
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[r] = fmaf(u[e], v[e], sum[r]);
+            for (int i = 0; i < kBatch; ++i) {
+                if (c0 + i * step >= k) continue;
+                float a[V];
+                Pack<T, V>::open(u[i], a);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float v[V];
+                    Pack<T, V>::load(x + r * k + c0 + i * step, v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum[r] = fmaf(a[e], v[e], sum[r]);
+                }
+            }
         }
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], d);
-        if (lane == r) finish1<T>(q, sum[r] + (q.bias ? q.bias[j] : 0.0f), r * q.n + j);
+        if (lane == 0) s_sum[warp][r] = sum[r];
+    }
+    __syncthreads();
+    if (part == 0 && lane < kRows && j < q.n) {
+        float z = s_sum[warp][lane];
+        for (int p = 1; p < per; ++p) z += s_sum[warp + p][lane];
+        finish1<T>(q, plus(z, q.bias ? q.bias[j] : 0.0f), lane * q.n + j);
     }
 }
 
@@ -2048,14 +2069,19 @@ bool vec4(const Product& q) {
 
 template <typename T, int V>
 cudaError_t few_rows(const LinearCall& c, const Product& q, cudaStream_t s) {
-    const dim3 grid((unsigned)ceil_div(c.outputs, 8)), block(256);
-    const T *x = static_cast<const T*>(c.x), *w = static_cast<const T*>(c.weight);
-    switch (c.rows) {
-        case 1: return launch_pdl(k_linear_rows<T, V, 1>, grid, block, 0, s, x, w, c.inputs, q);
-        case 2: return launch_pdl(k_linear_rows<T, V, 2>, grid, block, 0, s, x, w, c.inputs, q);
-        case 3: return launch_pdl(k_linear_rows<T, V, 3>, grid, block, 0, s, x, w, c.inputs, q);
-        default: return launch_pdl(k_linear_rows<T, V, 4>, grid, block, 0, s, x, w, c.inputs, q);
-    }
+    int per = 1;
+    while (per < 8 && (int64_t)per * 32 * V * 8 < c.inputs) per *= 2;
+    const dim3 grid((unsigned)ceil_div(c.outputs, 8 / per)), block(256);
+    auto* kernel = c.rows == 1   ? k_linear_rows<T, V, 1>
+                   : c.rows == 2 ? k_linear_rows<T, V, 2>
+                   : c.rows == 3 ? k_linear_rows<T, V, 3>
+                   : c.rows == 4 ? k_linear_rows<T, V, 4>
+                   : c.rows == 5 ? k_linear_rows<T, V, 5>
+                   : c.rows == 6 ? k_linear_rows<T, V, 6>
+                   : c.rows == 7 ? k_linear_rows<T, V, 7>
+                                 : k_linear_rows<T, V, 8>;
+    return launch_pdl(kernel, grid, block, 0, s, static_cast<const T*>(c.x),
+                      static_cast<const T*>(c.weight), c.inputs, per, q);
 }
 
 // The plan of a narrow layer; false where it is none.
