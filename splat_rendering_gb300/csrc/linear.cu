@@ -91,6 +91,65 @@ __device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]
     }
 }
 
+// kCount consecutive elements at any alignment, from the 16-byte vectors that they lie in.
+template <typename T, int kCount>
+struct Window {
+    static constexpr int kSize = (int)sizeof(T), kVectors = kCount * kSize / 16 + 1;
+    uint4 raw[kVectors];
+    int shift;   // elements from the first vector's beginning
+
+    __device__ __forceinline__ void load_shared(uint32_t at) {
+        shift = (int)(at & 15u) / kSize;
+        at &= ~15u;
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                         : "r"(at + 16 * i));
+    }
+    // whether the vectors lie within [begin, end)
+    __device__ __forceinline__ static bool within(const T* p, const T* begin, const T* end) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
+        return at >= reinterpret_cast<uintptr_t>(begin) &&
+               at + 16 * kVectors <= reinterpret_cast<uintptr_t>(end);
+    }
+    __device__ __forceinline__ void load(const T* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        shift = (int)(at & 15u) / kSize;
+        const uint4* v = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) raw[i] = v[i];
+    }
+    __device__ __forceinline__ void open(float (&v)[kCount]) const {
+        constexpr int kWords = 4 * kVectors;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) {
+            w[4 * i] = raw[i].x;
+            w[4 * i + 1] = raw[i].y;
+            w[4 * i + 2] = raw[i].z;
+            w[4 * i + 3] = raw[i].w;
+        }
+        if constexpr (kSize == 4) {
+#pragma unroll
+            for (int i = 0; i + 2 < kWords; ++i) w[i] = shift & 2 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) v[i] = __uint_as_float(shift & 1 ? w[i + 1] : w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i + 2 < kWords; ++i) w[i] = shift & 4 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i + 3 < kWords; ++i) w[i] = shift & 2 ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < kCount / 2; ++i) {
+                const uint32_t u = shift & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+                v[2 * i] = low_of(u);
+                v[2 * i + 1] = high_of(u);
+            }
+        }
+    }
+};
+
 // Eight columns of a row as they were loaded: nothing waits for them before they are opened.
 template <typename T>
 struct Chunk {
@@ -197,10 +256,25 @@ __device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
             }
         }
     } else if (n > 0) {
+        const T* end = static_cast<const T*>(q.src) + q.rows * q.cols;
+        const T* pre_end = static_cast<const T*>(q.pre) + q.rows * q.cols;
+        const auto load = [&](const T* p, const T* begin, const T* stop, float (&v)[8]) {
+            if (Window<T, 8>::within(p, begin, stop)) {
+                Window<T, 8> w;
+                w.load(p);
+                w.open(v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : 0.0f;
+            } else {
+                load8(p, n, false, v);
+            }
+        };
+#pragma unroll 2
         for (int64_t r = r0 + ty; r < r1; r += step) {
             float v[8], z[8];
-            load8(src + r * q.cols, n, false, v);
-            if (kAct != kActNone) load8(pre + r * q.cols, n, false, z);
+            load(src + r * q.cols, static_cast<const T*>(q.src), end, v);
+            if (kAct != kActNone)
+                load(pre + r * q.cols, static_cast<const T*>(q.pre), pre_end, z);
             finish(r, v, z);
         }
     }
@@ -270,6 +344,7 @@ struct Product {
     CUtensorMap a, b;
     int tiles_m, tiles_n, splits, panels;   // panels of the contraction
     int64_t m, n;
+    int64_t part;   // floats from one part's sums to the next
     // the finished result, or, where there are parts, their sums [splits][m][n]
     const float* bias;
     const void* residual;
@@ -464,13 +539,37 @@ __device__ __forceinline__ void finish1(const Product& q, float z, int64_t at) {
     else finish1<T, kActNone>(q, z, at);
 }
 
-// A lane's share of the block of 32 rows from r0 and 32 columns from c0.
-template <typename T>
+// A block of 32 rows and 32 (or, kSmall, eight) columns whose sums are in the exchange, where rows
+// are no whole vectors: as many lanes to a row as it has columns, so that a warp stores what is
+// contiguous.  `first`: its first element, col0: its column.
+template <typename T, int kAct, bool kSmall>
+__device__ __forceinline__ void finish_scalar(const Product& q, const float4* x, int64_t col0,
+                                           int64_t first, int64_t left_rows, int lane) {
+    const int rows = (int)(left_rows < 32 ? left_rows : 32);
+    const int64_t left = q.n - col0;
+    const int cols = (int)(left < (kSmall ? 8 : 32) ? left : (kSmall ? 8 : 32));
+    int log = 0;
+    while (1 << log < cols) ++log;
+    const int c = lane & ((1 << log) - 1);
+    const float* word = reinterpret_cast<const float*>(x) + (c & 3);
+    if (c >= cols) return;
+    const float b = q.bias ? q.bias[col0 + c] : 0.0f;
+#pragma unroll 1
+    for (int r = lane >> log; r < rows; r += 32 >> log) {
+        const int at = kSmall ? r * 2 + ((c >> 2) ^ (r >> 2 & 1)) : r * 8 + ((c >> 2) ^ (r & 7));
+        finish1<T, kAct>(q, plus(word[at * 4], b), first + r * q.n + c);
+    }
+}
+
+// A lane's share of the block of 32 rows from r0 and 32 columns from c0.  kVec: rows are whole
+// vectors (four columns at a time), known when compiled: kernels that have the other case's
+// instructions too were up to a tenth slower.  kSkip: there is a residual.
+template <typename T, bool kVec, bool kSkip>
 struct Share {
     using Raw = typename Four<T>::Raw;
     int64_t c, at;   // its first column, and its first element
     int n, rows;     // columns (of four), rows that there are from its first on
-    Raw residual[8];
+    Raw residual[kSkip ? 8 : 1];
 
     // (at: of the element (r0, c0) in a matrix of q.n columns)
     __device__ __forceinline__ void begin(const Product& q, int64_t r0, int64_t c0, int64_t base,
@@ -480,11 +579,11 @@ struct Share {
         at = base + (r0 + (lane >> 3)) * q.n + c;
         const int64_t left = q.m - r0 - (lane >> 3);
         rows = n <= 0 ? 0 : (int)(left < 32 ? left : 32);
-        if (q.residual && q.vec) {
+        if (kSkip && kVec) {
 #pragma unroll
             for (int h = 0; h < 8; ++h)
                 if (4 * h < rows)
-                    residual[h] = __ldcs(reinterpret_cast<const Raw*>(
+                    residual[kSkip ? h : 0] = __ldcs(reinterpret_cast<const Raw*>(
                         static_cast<const T*>(q.residual) + at + (int64_t)4 * h * q.n));
         }
     }
@@ -501,15 +600,16 @@ struct Share {
         return x[r * 8 + ((lane & 7) ^ (r & 7))];
     }
 
-    // `bias`: of its four columns
+    // `bias`: of its four columns; r0, c0, base as in begin()
     template <int kAct>
     __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
-                                        const float (&bias)[4], int lane) {
+                                        const float (&bias)[4], int64_t r0, int64_t c0,
+                                        int64_t base, int lane) {
         T* out = static_cast<T*>(q.out) + at;
         T* pre = q.pre ? static_cast<T*>(q.pre) + at : nullptr;
         const int rq = lane >> 3;
         const int64_t step = 4 * q.n;
-        if (q.vec) {
+        if constexpr (kVec) {
             // (all loads, then all stores: the compiler keeps a load behind a store before it)
             float z[8][4];
             put(x, v, lane);
@@ -530,45 +630,28 @@ struct Share {
             for (int h = 0; h < 8; ++h) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
-                if (q.residual) Four<T>::add(residual[h], z[h]);
+                if (kSkip) Four<T>::add(residual[kSkip ? h : 0], z[h]);
             }
 #pragma unroll
             for (int h = 0; h < 8; ++h)
                 if (4 * h < rows) *reinterpret_cast<Raw*>(out + h * step) = Four<T>::pack(z[h]);
-            return;
-        }
-        const T* skip = q.residual ? static_cast<const T*>(q.residual) + at : nullptr;
-        put(x, v, lane);
-#pragma unroll 1
-        for (int h = 0; 4 * h < rows; ++h) {
-            const float4 u = get(x, 4 * h + rq, lane);
-            const float w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (e >= n) continue;
-                const float z[1] = {plus(w[e], bias[e])};
-                float y[1] = {act_of<kAct>(z[0])};
-                if (pre) Pack<T, 1>::store(pre + h * step + e, z);
-                if (skip) {
-                    float f[1];
-                    Pack<T, 1>::load(skip + h * step + e, f);
-                    y[0] = plus(y[0], f[0]);
-                }
-                Pack<T, 1>::store(out + h * step + e, y);
-            }
+        } else {
+            put(x, v, lane);
+            finish_scalar<T, kAct, false>(q, x, c0, base + r0 * q.n + c0, q.m - r0, lane);
         }
     }
     __device__ __forceinline__ void end(const Product& q, float4* x, const float (&v)[32],
-                                        const float (&bias)[4], int lane) {
-        if (q.act == kActSilu) end<kActSilu>(q, x, v, bias, lane);
-        else if (q.act == kActRelu) end<kActRelu>(q, x, v, bias, lane);
-        else end<kActNone>(q, x, v, bias, lane);
+                                        const float (&bias)[4], int64_t r0, int64_t c0,
+                                        int64_t base, int lane) {
+        if (q.act == kActSilu) end<kActSilu>(q, x, v, bias, r0, c0, base, lane);
+        else if (q.act == kActRelu) end<kActRelu>(q, x, v, bias, r0, c0, base, lane);
+        else end<kActNone>(q, x, v, bias, r0, c0, base, lane);
     }
 };
 
 // The same where there is room for an exchange of 32 x 8 words only: eight columns at a time, of
 // which a lane has four of every 16th row; a warp stores sectors.  (kPlain: the sums are the result.)
-template <typename T, int kAct, bool kPlain = false>
+template <typename T, int kAct, bool kPlain, bool kVec>
 __device__ __forceinline__ void finish_small(const Product& q, float4* x, const float (&v)[32],
                                              int64_t r0, int64_t c0, int64_t base, int lane) {
     using Raw = typename Four<T>::Raw;
@@ -603,24 +686,23 @@ __device__ __forceinline__ void finish_small(const Product& q, float4* x, const 
             z[0][e] = plus(z[0][e], bias);
             z[1][e] = plus(z[1][e], bias);
         }
+        if constexpr (!kVec) {
+            finish_scalar<T, kAct, true>(q, x, c0 + 8 * m, base + r0 * q.n + c0 + 8 * m, q.m - r0,
+                                         lane);
+            continue;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (16 * h >= rows || n <= 0) continue;
             const int64_t at = at0 + 16 * h * q.n + 8 * m;
-            if (q.vec) {
-                if (!kPlain && q.pre)
-                    *reinterpret_cast<Raw*>(static_cast<T*>(q.pre) + at) = Four<T>::pack(z[h]);
+            if (!kPlain && q.pre)
+                *reinterpret_cast<Raw*>(static_cast<T*>(q.pre) + at) = Four<T>::pack(z[h]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
-                if (!kPlain && q.residual)
-                    Four<T>::add(*reinterpret_cast<const Raw*>(
-                                     static_cast<const T*>(q.residual) + at), z[h]);
-                *reinterpret_cast<Raw*>(static_cast<T*>(q.out) + at) = Four<T>::pack(z[h]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < n) finish1<T, kAct>(q, z[h][e], at + e);
-            }
+            for (int e = 0; e < 4; ++e) z[h][e] = act_of<kAct>(z[h][e]);
+            if (!kPlain && q.residual)
+                Four<T>::add(*reinterpret_cast<const Raw*>(static_cast<const T*>(q.residual) + at),
+                             z[h]);
+            *reinterpret_cast<Raw*>(static_cast<T*>(q.out) + at) = Four<T>::pack(z[h]);
         }
     }
 }
@@ -628,7 +710,7 @@ __device__ __forceinline__ void finish_small(const Product& q, float4* x, const 
 // T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
 // as its rows.  kCtas: 1, or a pair of CTAs on a tile of 256 rows, each with its 128 rows of A and
 // of the sums, and half of B's; the first one issues the MMAs of both.
-template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas, bool kVec>
 __global__ void __launch_bounds__(64 + 32 * epilogue_warps(kPlanes)) __cluster_dims__(kCtas, 1, 1)
 k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     using L = ProductSmem<kPlanes, kN, kCtas>;
@@ -814,28 +896,34 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             int i, j, k0, k1, part;
             place(t, &i, &j, &k0, &k1, &part);
             const int64_t r0 = ((int64_t)i * kCtas + rank) * kBlock + quarter * 32;
-            const int64_t base = (int64_t)part * q.m * q.n;
+            const int64_t base = part * q.part;
             // 32 columns from `col` of the tile, a row in each lane
             auto emit = [&](const float (&v)[32], int col) {
                 const int64_t c0 = (int64_t)j * kN + col;
                 if constexpr (kPlanes == 3) {
                     if (kAMn || kBMn)
-                        finish_small<T, kActNone, true>(q, x, v, r0, c0, base, lane);
+                        finish_small<T, kActNone, true, kVec>(q, x, v, r0, c0, base, lane);
                     else if (q.act == kActNone)
-                        finish_small<T, kActNone>(q, x, v, r0, c0, base, lane);
+                        finish_small<T, kActNone, false, kVec>(q, x, v, r0, c0, base, lane);
                     else if (q.act == kActSilu)
-                        finish_small<T, kActSilu>(q, x, v, r0, c0, base, lane);
+                        finish_small<T, kActSilu, false, kVec>(q, x, v, r0, c0, base, lane);
                     else
-                        finish_small<T, kActRelu>(q, x, v, r0, c0, base, lane);
+                        finish_small<T, kActRelu, false, kVec>(q, x, v, r0, c0, base, lane);
                 } else {
-                    Share<T> share;
-                    share.begin(q, r0, c0, base, lane);
-                    float bias[4];
+                    const auto finish = [&](auto skip) {
+                        Share<T, kVec, decltype(skip)::value> share;
+                        share.begin(q, r0, c0, base, lane);
+                        float bias[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        bias[e] = q.bias && e < share.n ? q.bias[share.c + e] : 0.0f;
-                    if (kAMn || kBMn) share.template end<kActNone>(q, x, v, bias, lane);
-                    else share.end(q, x, v, bias, lane);
+                        for (int e = 0; e < 4; ++e)
+                            bias[e] = q.bias && e < share.n ? q.bias[share.c + e] : 0.0f;
+                        if (kAMn || kBMn)
+                            share.template end<kActNone>(q, x, v, bias, r0, c0, base, lane);
+                        else
+                            share.end(q, x, v, bias, r0, c0, base, lane);
+                    };
+                    if (kAMn || kBMn || !q.residual) finish(std::false_type());
+                    else finish(std::true_type());
                 }
             };
             bool ok = true;
@@ -927,24 +1015,18 @@ k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part)
     constexpr int kPer = 256 / kLanes;   // groups of four columns of a block
     __shared__ float4 s_sum[8][kLanes > 1 ? kPer : 1];
     pdl_begin();
-    const int64_t size = q.m * q.n, groups = (q.n + 3) / 4, total = q.m * groups;
+    const int64_t size = q.m * q.n, total = (size + 3) / 4;
     const int mine = threadIdx.x % kPer, from = threadIdx.x / kPer;
     for (int64_t g0 = (int64_t)blockIdx.x * kPer; g0 < total; g0 += (int64_t)gridDim.x * kPer) {
-        const int64_t g = g0 + mine, r = g / groups, c = (g - r * groups) * 4, at = r * q.n + c;
-        const int n = g < total ? (int)(q.n - c < 4 ? q.n - c : 4) : 0;
+        const int64_t at = (g0 + mine) * 4;
+        const int n = (int)(size - at < 4 ? size - at : 4);   // (a part ends on a whole vector)
         float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if ((q.n & 3) == 0 && n > 0) {   // (the workspace is aligned)
+        if (n > 0) {
 #pragma unroll 8
             for (int s = from; s < q.splits; s += kLanes) {
-                const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * size + at));
+                const float4 u = __ldcs(reinterpret_cast<const float4*>(part + s * q.part + at));
                 z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
             }
-        } else {
-#pragma unroll 4
-            for (int s = from; s < q.splits; s += kLanes)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < n) z[e] += part[s * size + at + e];
         }
         if (kLanes > 1) {   // the warp's (its lanes kPer apart), then the block's
 #pragma unroll
@@ -965,7 +1047,7 @@ k_linear_join(const __grid_constant__ Product q, const float* __restrict__ part)
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (e < n) finish1<T>(q, z[e] + (q.bias ? q.bias[c + e] : 0.0f), at + e);
+            if (e < n) finish1<T>(q, plus(z[e], q.bias ? q.bias[(at + e) % q.n] : 0.0f), at + e);
     }
 }
 
@@ -1085,7 +1167,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
 }
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-template <typename T>
+// kVec: rows of x and of the result are whole vectors.  kSkip: there is a residual.
+template <typename T, bool kVec, bool kSkip>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
@@ -1251,21 +1334,27 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const int c = mine & 7, r0 = mine >> 3, col = h * kPanel + c * 8;
                 const T* src = tile + r0 * q.k + col;
                 unsigned char* dst = unit + r0 * 128 + ((c ^ (r0 & 7)) << 4);
-                if (q.vec && q.k - col >= 8) {
+                if ((kVec || q.vec) && q.k - col >= 8) {
                     float v[4][8];   // (all loads, then all stores, as there)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) load8(src + 32 * i * q.k, 8, true, v[i]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v[i]);
-                } else if (c < chunks) {
-#pragma unroll 1
+                } else if (c < chunks) {   // (what lies behind the last row is shared too)
+                    const uint32_t at = smem_u32(src);
+                    Window<T, 8> w[4];
+#pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (r0 + 32 * i < rows) {
-                            float v[8];
-                            load8(src + 32 * i * q.k, q.k - col, false, v);
-                            put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v);
-                        }
+                        w[i].load_shared(at + (uint32_t)(32 * i * q.k * (int)sizeof(T)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v[8];
+                        w[i].open(v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = col + e < q.k ? v[e] : 0.0f;
+                        put_chunk<kPlanes>(dst + 32 * i * 128, kBlock * kPanel * 2, v);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -1281,7 +1370,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
         for (int64_t t = first; t < q.tiles; t += step, ++it) {
             const int buf = it & 1;
             const int64_t r0 = t * kBlock + quarter * 32;
-            Share<T> share;
+            Share<T, kVec, kSkip> share;
             if (group * 32 < q.np) share.begin(q.out, r0, n0 + group * 32, 0, lane);
             const bool ok = warp_all(mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail);
             if (!ok) {
@@ -1311,7 +1400,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 if (c != group * 32) share.begin(q.out, r0, n0 + c, 0, lane);
                 const float4 b = *reinterpret_cast<const float4*>(s_bias + c + 4 * (lane & 7));
                 const float bias[4] = {b.x, b.y, b.z, b.w};
-                share.end(q.out, x, v, bias, lane);
+                share.end(q.out, x, v, bias, r0, n0 + c, 0, lane);
             }
             if (group * 32 >= q.np && lane == 0) mbar_arrive(acc_empty + buf);
         }
@@ -1354,7 +1443,8 @@ struct Narrow {
     bool vec_n, vec_k;     // ... and rows of n (k) elements are whole 16-byte vectors
     bool vec_w;            // rows of the weight are whole chunks of eight, on 16 bytes
     bool want_x, want_w;
-    float* parts;          // [parts of all CTAs][n][k]
+    float* parts;          // [parts of all CTAs][n][k], `part` floats each
+    int64_t part;
     float* sums;           // [CTA][n]; may be NULL
     Product out;           // of dx
 };
@@ -1419,11 +1509,11 @@ __device__ __forceinline__ typename Pack<T, VecOf<T>::n>::Raw lds16(uint32_t at)
 
 // kRows rows of an operand, [rows, cols] at `src` (times the activation's slope at `pre`, its
 // columns added to `sum`, where kDz), by a thread that has 16 bytes' columns of every kStep-th row:
-// rows behind the last, and columns up to the next 16, are zeros.  `vec`: src is a raw piece in
-// shared memory of whole 16-byte vectors.
+// rows behind the last, and columns up to the next 16, are zeros.  `shared`: src is a raw piece in
+// shared memory, `vec`: whose rows are whole 16-byte vectors.
 template <typename T, int kAct, int kPanels, bool kDz, int kRows>
 __device__ __forceinline__ void make_operand(unsigned char* operand, const T* src, const T* pre,
-                                             int rows, int cols, bool vec, int mine,
+                                             int rows, int cols, bool shared, bool vec, int mine,
                                              float (&sum)[kPanels][VecOf<T>::n]) {
     using L = BackSmem<T, kPanels>;
     constexpr int V = VecOf<T>::n, kLanes = kPanel / V, kStep = 256 / kLanes;
@@ -1465,6 +1555,26 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
                     put_columns<L::planes>(dst + (i0 + i) * kStep * 128, L::panel, v[i]);
                 }
             }
+        } else if (shared) {
+            const uint32_t s = smem_u32(src + r0 * cols + col), z = smem_u32(pre + r0 * cols + col);
+            const uint32_t pitch = (uint32_t)(kStep * cols) * (uint32_t)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < kRows / kStep; ++i) {   // (what lies behind the last is shared too)
+                Window<T, V> a, b;
+                a.load_shared(s + i * pitch);
+                if (kAct != kActNone) b.load_shared(z + i * pitch);
+                float v[V], w[V];
+                a.open(v);
+                if (kAct != kActNone) b.open(w);
+                to_dz<kAct>(v, w);
+                const bool row = r0 + i * kStep < rows;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    v[e] = row && col + e < cols ? v[e] : 0.0f;
+                    if (kDz) sum[h][e] += v[e];
+                }
+                put_columns<L::planes>(dst + i * kStep * 128, L::panel, v);
+            }
         } else {
 #pragma unroll 1
             for (int r = r0; r < kRows; r += kStep) {
@@ -1489,7 +1599,8 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
     }
 }
 
-template <typename T, int kAct, int kPanels>
+// kVec: rows of dy, z, x and dx are whole vectors, in raw pieces.
+template <typename T, int kAct, int kPanels, bool kVec>
 __global__ void __launch_bounds__(kBackThreads, 1)
 k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     using L = BackSmem<T, kPanels>;
@@ -1674,13 +1785,13 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         bool ok = true;
         // the piece in turn, or the place of row r in the tensor
         const auto wait_piece = [&]() {
-            if (q.raw)
+            if (kVec || q.raw)
                 ok = warp_all(mbar_wait(raw_full + f % L::pieces, (f / L::pieces) & 1) && !*s_fail);
             return ok;
         };
         const auto done_piece = [&]() {
             __syncwarp();
-            if (q.raw && lane == 0) mbar_arrive(raw_empty + f % L::pieces);
+            if ((kVec || q.raw) && lane == 0) mbar_arrive(raw_empty + f % L::pieces);
             ++f;
         };
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
@@ -1696,13 +1807,14 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     const T* raw =
                         reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
                     unsigned char* to = unit + L::operand + i * 128;
-                    if (q.vec_k)
+                    if (kVec || q.vec_k)
                         make_operand<T, kActNone, kPanels, false, kRowsX>(to, raw, nullptr, rows - i,
-                                                                          q.k, true, mine, none);
+                                                                          q.k, true, true, mine,
+                                                                          none);
                     else
                         make_operand<T, kActNone, kPanels, false, kRowsX>(
                             to, q.raw ? raw : static_cast<const T*>(q.x) + (row0 + i) * q.k, nullptr,
-                            rows - i, q.k, false, mine, none);
+                            rows - i, q.k, q.raw, false, mine, none);
                     done_piece();
                 }
             }
@@ -1713,15 +1825,15 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 const T* raw = reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
                 const T* z = raw + L::piece / 2 / (int)sizeof(T);
                 unsigned char* to = unit + i * 128;
-                if (q.vec_n) {
+                if (kVec || q.vec_n) {
                     make_operand<T, kAct, kPanels, true, kRowsZ>(to, raw, z, rows - i, q.n, true,
-                                                                 mine, sum);
+                                                                 true, mine, sum);
                 } else {
                     const int64_t at = (row0 + i) * q.n;
                     make_operand<T, kAct, kPanels, true, kRowsZ>(
                         to, q.raw ? raw : static_cast<const T*>(q.grad_y) + at,
-                        q.raw ? z : static_cast<const T*>(q.pre) + at, rows - i, q.n, false, mine,
-                        sum);
+                        q.raw ? z : static_cast<const T*>(q.pre) + at, rows - i, q.n, q.raw,
+                        false, mine, sum);
                 }
                 done_piece();
             }
@@ -1769,12 +1881,12 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         auto store_dx = [&](const float (&v)[32], int64_t t, int c0) {
             const int64_t r0 = t * kBlock + quarter * 32;
             if constexpr (kSplit) {
-                finish_small<T, kActNone, true>(q.out, x, v, r0, c0, 0, lane);
+                finish_small<T, kActNone, true, kVec>(q.out, x, v, r0, c0, 0, lane);
             } else {
-                Share<T> share;
+                Share<T, kVec, false> share;
                 const float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 share.begin(q.out, r0, c0, 0, lane);
-                share.template end<kActNone>(q.out, x, v, bias, lane);
+                share.template end<kActNone>(q.out, x, v, bias, r0, c0, 0, lane);
             }
         };
         bool ok = true;
@@ -1830,7 +1942,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             // a lane has a row of its part
             const int row = kSplit ? (quarter & 1) * 32 + lane : quarter * 32 + lane;
             float* part = q.parts + ((int64_t)blockIdx.x * (kSplit ? 2 : 1) +
-                                     (kSplit ? quarter >> 1 : 0)) * q.n * q.k +
+                                     (kSplit ? quarter >> 1 : 0)) * q.part +
                           (int64_t)row * q.k;
             if constexpr (kSplit) {
                 if (row < q.n)
@@ -1908,12 +2020,13 @@ int splits_of(int64_t tiles, int64_t panels, int n_sms) {
 int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
 // Pairs of CTAs where tiles of 256 rows are not half empty.
 bool paired(int64_t m) { return m > kBlock; }
+int64_t part_size(int64_t m, int64_t n) { return (m * n + 3) / 4 * 4; }
 size_t part_floats(int planes, int64_t m, int64_t n, int64_t k) {
     const int kn = tile_n(planes, n), ctas = (planes == 3 || kn == 256) && paired(m) ? 2 : 1;
     const int64_t tiles = ceil_div(m, kBlock * ctas) * ceil_div(n, kn);
     if (tiles == 0 || tiles > kMostSms / ctas) return 0;
     const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms / ctas);
-    return s > 1 ? (size_t)s * m * n : 0;
+    return s > 1 ? (size_t)s * part_size(m, n) : 0;
 }
 
 // Blocks of rows of k_linear_operand: about eight blocks per SM over the whole matrix.
@@ -1957,7 +2070,7 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
     const int64_t side = dtype == kF32 ? kBackSide<float> : kBackSide<__nv_bfloat16>;
     if (k <= side && n <= side) {   // two parts of every CTA
         const size_t tiles = (size_t)ceil_div(m, kBlock);
-        const size_t narrow = 2 * (tiles < kMostSms ? tiles : kMostSms) * (size_t)(n * k);
+        const size_t narrow = 2 * (tiles < kMostSms ? tiles : kMostSms) * (size_t)part_size(n, k);
         if (narrow > parts) parts = narrow;
     }
     s.parts = c.take<float>(parts);
@@ -2009,7 +2122,7 @@ struct Maker {
 template <typename T>
 cudaError_t join(const Product& q, const float* parts, int n_sms, cudaStream_t s) {
     const bool many = q.splits > 16;
-    const int64_t blocks = ceil_div(q.m * ceil_div(q.n, 4), many ? 4 : 256);
+    const int64_t blocks = ceil_div(ceil_div(q.m * q.n, 4), many ? 4 : 256);
     return launch_pdl(many ? k_linear_join<T, 64> : k_linear_join<T, 1>,
                       dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8)), dim3(256), 0, s, q,
                       parts);
@@ -2025,6 +2138,7 @@ cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, f
     const int64_t tiles = (int64_t)q.tiles_m * q.tiles_n;
     const int groups = n_sms / kCtas;   // of CTAs that share a tile
     q.splits = tiles <= groups ? splits_of(tiles, q.panels, groups) : 1;
+    q.part = part_size(q.m, q.n);
     if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : L::rows_b))
         return cudaErrorInvalidValue;
     const auto launch = [&](auto kernel, const Product& p) {
@@ -2032,14 +2146,18 @@ cudaError_t product_as(Product q, const Matrix& a, const Matrix& b, int64_t k, f
         return launch_pdl(kernel, dim3((unsigned)((total < groups ? total : groups) * kCtas)),
                           dim3(L::threads), L::bytes, s, p, st);
     };
-    if (q.splits == 1) return launch(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas>, q);
+    if (q.splits == 1)
+        return launch(q.vec ? k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>
+                            : k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>, q);
     Product p = q;
     p.bias = nullptr;
     p.residual = p.pre = nullptr;
     p.out = parts;
     p.act = kActNone;
     p.vec = q.n % 4 == 0;
-    cudaError_t e = launch(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas>, p);
+    cudaError_t e =
+        launch(p.vec ? k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>
+                     : k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>, p);
     if (e != cudaSuccess) return e;
     return join<T>(q, parts, n_sms, s);
 }
@@ -2137,7 +2255,10 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
         narrow.skip = q.residual && aligned16(q.residual) && narrow.blocks == 1;
         const int64_t per = n_sms / narrow.blocks;
         const int64_t grid = narrow.blocks * (narrow.tiles < per ? narrow.tiles : per);
-        return launch_pdl(k_linear_stream<T>, dim3((unsigned)grid), dim3(kStreamThreads),
+        auto* kernel = !(narrow.vec && q.vec) ? k_linear_stream<T, false, true>
+                       : q.residual           ? k_linear_stream<T, true, true>
+                                              : k_linear_stream<T, true, false>;
+        return launch_pdl(kernel, dim3((unsigned)grid), dim3(kStreamThreads),
                           (size_t)smem, s, narrow, st);
     }
     const Space sp = carve(ws, m, k, n, c.dtype);
@@ -2170,6 +2291,7 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
     q.want_x = c.grad_x != nullptr;
     q.want_w = c.grad_weight != nullptr;
     q.parts = sp.parts;
+    q.part = part_size(n, k);
     q.sums = c.grad_bias ? sp.sums : nullptr;
     q.out.m = m;
     q.out.n = k;
@@ -2178,9 +2300,13 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
     const unsigned ctas = (unsigned)(q.tiles < n_sms ? q.tiles : n_sms);
     const auto run = [&](auto panels) {
         constexpr int kPanels = decltype(panels)::value;
-        auto* kernel = c.act == kActSilu   ? k_linear_narrow<T, kActSilu, kPanels>
-                       : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels>
-                                           : k_linear_narrow<T, kActNone, kPanels>;
+        const auto pick = [&](auto vec) {
+            constexpr bool kVec = decltype(vec)::value;
+            return c.act == kActSilu   ? k_linear_narrow<T, kActSilu, kPanels, kVec>
+                   : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels, kVec>
+                                       : k_linear_narrow<T, kActNone, kPanels, kVec>;
+        };
+        auto* kernel = q.vec_n && q.vec_k && q.out.vec ? pick(std::true_type()) : pick(std::false_type());
         return launch_pdl(kernel, dim3(ctas), dim3(kBackThreads), BackSmem<T, kPanels>::bytes, s, q,
                           st);
     };
@@ -2196,6 +2322,7 @@ cudaError_t narrow(const LinearCall& c, const Space& sp, LearnState* st, int n_s
         p.n = k;
         p.out = c.grad_weight;
         p.splits = (int)ctas * (sizeof(T) == 4 ? 2 : 1);
+        p.part = q.part;
         e = join<T>(p, sp.parts, n_sms, s);
     }
     return e;
@@ -2243,12 +2370,18 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
 
 template <typename T, int kPlanes, int kN, int kCtas, bool kAMn, bool kBMn>
 cudaError_t prepare_one() {
-    constexpr int bytes = ProductSmem<kPlanes, kN, kCtas>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && sizeof(T) == 2)
-        e = cudaFuncSetAttribute(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaSuccess;
+    const auto prepare = [&](auto* f) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     ProductSmem<kPlanes, kN, kCtas>::bytes);
+    };
+    prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>);
+    prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>);
+    if constexpr (sizeof(T) == 2) {
+        prepare(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>);
+        prepare(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>);
+    }
     return e;
 }
 template <typename T, int kPlanes, int kN, int kCtas>
@@ -2262,8 +2395,12 @@ cudaError_t prepare_three() {
 template <typename T, int kPanels>
 cudaError_t prepare_narrow() {
     cudaError_t e = cudaSuccess;
-    for (auto* f : {k_linear_narrow<T, kActNone, kPanels>, k_linear_narrow<T, kActSilu, kPanels>,
-                    k_linear_narrow<T, kActRelu, kPanels>})
+    for (auto* f : {k_linear_narrow<T, kActNone, kPanels, true>,
+                    k_linear_narrow<T, kActSilu, kPanels, true>,
+                    k_linear_narrow<T, kActRelu, kPanels, true>,
+                    k_linear_narrow<T, kActNone, kPanels, false>,
+                    k_linear_narrow<T, kActSilu, kPanels, false>,
+                    k_linear_narrow<T, kActRelu, kPanels, false>})
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      BackSmem<T, kPanels>::bytes);
@@ -2292,12 +2429,13 @@ cudaError_t prepare_linear() {
     if (e == cudaSuccess) e = prepare_narrow<float, 1>();
     if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 1>();
     if (e == cudaSuccess) e = prepare_narrow<__nv_bfloat16, 2>();
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_linear_stream<float>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_linear_stream<__nv_bfloat16>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmemMax);
+    for (auto* f : {k_linear_stream<float, true, true>, k_linear_stream<float, true, false>,
+                    k_linear_stream<float, false, true>, k_linear_stream<__nv_bfloat16, true, true>,
+                    k_linear_stream<__nv_bfloat16, true, false>,
+                    k_linear_stream<__nv_bfloat16, false, true>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kStreamSmemMax);
     return e;
 }
 
