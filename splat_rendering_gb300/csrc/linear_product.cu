@@ -29,18 +29,19 @@ struct Product {
     Result out;
 };
 
-// warps: copies, MMAs, and of the epilogue eight, or in 16 bits, where it has every tile's
-// activation to do within the MMAs' time, sixteen
-constexpr int epilogue_warps(int planes) { return planes == 3 ? 8 : 16; }
+// warps: copies, MMAs, and of the epilogue eight, or for a layer's outputs in 16 bits, where it has
+// every tile's activation to do within the MMAs' time, sixteen (16381 x 1024 -> 4096: 90 us, with
+// eight 96; dx, which has none: 84 us with eight, with sixteen 88)
+constexpr int epilogue_warps(int planes, bool outputs) { return planes == 1 && outputs ? 16 : 8; }
 constexpr int kChunk = 2;              // panels per drained sum (32 bits)
-constexpr int kGroup = 16;             // row blocks whose tiles lie side by side in time
+constexpr int kGroup = 4;              // row blocks whose tiles lie side by side in time
 
-template <int kPlanes, int kN, int kCtas>
+template <int kPlanes, int kN, int kCtas, bool kOutputs>
 struct ProductSmem {
     static constexpr int rows_b = kN / kCtas;   // of B, in each CTA of a pair
     static constexpr int a = kBlock * kPanel * 2, b = rows_b * kPanel * 2;
     static constexpr int stage = kPlanes * (a + b);
-    static constexpr int epilogue = epilogue_warps(kPlanes), threads = 64 + 32 * epilogue;
+    static constexpr int epilogue = epilogue_warps(kPlanes, kOutputs), threads = 64 + 32 * epilogue;
     // a warp's exchange: 32 x 32 words, in 32 bits 32 x 8 for a third stage
     static constexpr int warp_exchange = 32 * (kPlanes == 3 ? 8 : 32) * 4;
     static constexpr int exchange_bytes = epilogue * warp_exchange;
@@ -130,9 +131,9 @@ __device__ __forceinline__ bool epilogue_any(bool v) {
 // as its rows.  kCtas: 1, or a pair of CTAs on a tile of 256 rows, each with its 128 rows of A and
 // of the sums, and half of B's; the first one issues the MMAs of both.
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas, bool kVec>
-__global__ void __launch_bounds__(64 + 32 * epilogue_warps(kPlanes)) __cluster_dims__(kCtas, 1, 1)
+__global__ void __launch_bounds__(64 + 32 * epilogue_warps(kPlanes, !kAMn && !kBMn)) __cluster_dims__(kCtas, 1, 1)
 k_linear_product(const __grid_constant__ Product q, LearnState* st) {
-    using L = ProductSmem<kPlanes, kN, kCtas>;
+    using L = ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>;
     constexpr bool kPair = kCtas == 2;
     constexpr int kAcc = kPlanes == 3 ? 2 * kN : kN;   // columns of an accumulator
     constexpr int kHalf = kN / (L::epilogue / 4);      // columns of an epilogue thread
@@ -462,7 +463,7 @@ bool paired(int64_t m) { return m > kBlock; }
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
 cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                        LearnState* st, int n_sms, cudaStream_t s) {
-    using L = ProductSmem<kPlanes, kN, kCtas>;
+    using L = ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>;
     Product q{};
     q.out = r;
     q.tiles_m = (int)ceil_div(r.m, kBlock * kCtas);
@@ -511,7 +512,7 @@ cudaError_t prepare_one() {
     const auto prepare = [&](auto* f) {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     ProductSmem<kPlanes, kN, kCtas>::bytes);
+                                     ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>::bytes);
     };
     prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>);
     prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>);
