@@ -341,23 +341,28 @@ struct Narrow {
     float* sums;           // [CTA][n]; may be NULL
     Result out;            // of dx
 };
-template <typename T, int kPanels>
+template <typename T, int kPanels, bool kAct>
 struct BackSmem {
     static constexpr int planes = sizeof(T) == 4 ? 3 : 1;
     static constexpr int side = kPanels * kPanel;
     static constexpr int panel = kBlock * kPanel * 2;          // of one plane
     static constexpr int operand = planes * kPanels * panel;   // [panel][plane]
-    static constexpr int unit = 2 * operand;                   // dz, x
-    static constexpr int units = planes == 1 && kPanels == 1 ? 2 : 1;
+    // dz's operands, x's: in 32 bits with an activation, whose raw rows are half as many again, the
+    // room is theirs (1M x 64 -> 64 with SiLU: 210 us, with two operands of dz and half the raw rows
+    // 230; without an activation 195 and 169)
+    static constexpr int dzs = planes == 3 && kAct ? 1 : 2;
+    static constexpr int xs = planes == 1 && kPanels == 1 ? 2 : 1;
+    static constexpr int x = dzs * operand;                    // dz's come first
     static constexpr int weight_panel = side * kPanel * 2;
-    static constexpr int weight = units * unit;                // [panel of inputs][plane]
+    static constexpr int weight = x + xs * operand;            // [panel of inputs][plane]
     // a warp's exchange is 32 x 32 words; in 32 bits, for want of room, 32 x 8
     static constexpr int exchange = weight + planes * kPanels * weight_panel;
     static constexpr int exchange_bytes = planes == 3 ? 8 * 1024 : 8 * 4096;
     static constexpr int raw = exchange + exchange_bytes;
-    // pieces of x's rows, or of dy's and z's: whole tiles of x in 32 bits
-    static constexpr int piece = planes == 3 ? 32 * 1024 : 16 * 1024;
-    static constexpr int pieces = 96 * 1024 / piece;
+    // pieces of x's rows, or of dy's and z's
+    static constexpr int piece = dzs == 1 ? 32 * 1024 : 16 * 1024;
+    static constexpr int room = (227 * 1024 - 1280 - raw) / piece;
+    static constexpr int pieces = room < 6 ? room : 6;
     static constexpr int rows_x = piece / (side * (int)sizeof(T));
     static constexpr int bars = raw + pieces * piece;
     static constexpr int bytes = bars + 256 + 1024;
@@ -408,7 +413,7 @@ template <typename T, int kAct, int kPanels, bool kDz, int kRows>
 __device__ __forceinline__ void make_operand(unsigned char* operand, const T* src, const T* pre,
                                              int rows, int cols, bool shared, bool vec, int mine,
                                              float (&sum)[kPanels][VecOf<T>::n]) {
-    using L = BackSmem<T, kPanels>;
+    using L = BackSmem<T, kPanels, false>;   // (its planes and panels)
     constexpr int V = VecOf<T>::n, kLanes = kPanel / V, kStep = 256 / kLanes;
     constexpr int kBatch = kRows / kStep < 4 ? kRows / kStep : 4;
     const int c = mine % kLanes * V, r0 = mine / kLanes, cols16 = (cols + 15) / 16 * 16;
@@ -496,7 +501,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
 template <typename T, int kAct, int kPanels, bool kVec>
 __global__ void __launch_bounds__(kBackThreads, 1)
 k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
-    using L = BackSmem<T, kPanels>;
+    using L = BackSmem<T, kPanels, kAct != kActNone>;
     constexpr int kPlanes = L::planes, V = VecOf<T>::n;
     constexpr bool kSplit = kPlanes == 3;
     constexpr int kRowsX = L::rows_x, kRowsZ = kAct == kActNone ? L::rows_x : L::rows_x / 2;
@@ -505,8 +510,9 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::bars);
     uint64_t* raw_empty = raw_full + L::pieces;
-    uint64_t* unit_full = raw_empty + L::pieces;
-    uint64_t* dz_empty = unit_full + 2;
+    uint64_t* dz_full = raw_empty + L::pieces;
+    uint64_t* x_full = dz_full + 2;
+    uint64_t* dz_empty = x_full + 2;
     uint64_t* x_empty = dz_empty + 2;
     uint64_t* dx_full = x_empty + 2;
     uint64_t* dx_empty = dx_full + 2;
@@ -523,7 +529,8 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             mbar_init_n(raw_empty + s, 8);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init_n(unit_full + s, 8);
+            mbar_init_n(dz_full + s, 8);
+            mbar_init_n(x_full + s, 8);
             mbar_init(dz_empty + s);
             mbar_init(x_empty + s);
             mbar_init(dx_full + s);
@@ -585,13 +592,29 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     if (p2) bulk_copy(dst2, src2, bulk, raw_full + s);
                 }
             };
+            // a tile's tensors, on their way to the L2: the pieces' own way in is short then
+            const auto ahead = [&](int64_t t) {
+                if (t >= q.tiles) return;
+                const int64_t left = q.rows - t * kBlock;
+                const uint32_t rows = (uint32_t)(left < kBlock ? left : kBlock);
+                const auto one = [&](const void* p, int cols) {
+                    prefetch_l2(static_cast<const T*>(p) + t * kBlock * cols,
+                                rows * cols * (uint32_t)sizeof(T) & ~15u);
+                };
+                one(q.grad_y, q.n);
+                if (kAct != kActNone) one(q.pre, q.n);
+                if (q.want_w) one(q.x, q.k);
+            };
+            constexpr bool kAhead = L::pieces * L::piece < 96 * 1024;   // (with these, no need)
+            if (kAhead) ahead(first + step);
             for (int64_t t = first; t < q.tiles && ok; t += step) {
                 const int64_t r = t * kBlock;
+                if (kAhead) ahead(t + 2 * step);
+                for (int i = 0; i < kBlock && ok; i += kRowsZ)
+                    piece(q.grad_y, kAct != kActNone ? q.pre : nullptr, r + i, kRowsZ, q.n);
                 if (q.want_w)
                     for (int i = 0; i < kBlock && ok; i += kRowsX)
                         piece(q.x, nullptr, r + i, kRowsX, q.k);
-                for (int i = 0; i < kBlock && ok; i += kRowsZ)
-                    piece(q.grad_y, kAct != kActNone ? q.pre : nullptr, r + i, kRowsZ, q.n);
             }
             if (!ok) {   // give the copies in flight one more bounded wait
                 *s_fail = 1u;
@@ -610,33 +633,11 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             int u = 0;
             bool ok = true;
             for (int64_t t = first; t < q.tiles; t += step, ++u) {
-                const int s = u % L::units;
-                ok = mbar_wait(unit_full + s, (u / L::units) & 1) && !*s_fail;
+                const int sz = u % L::dzs, sx = u % L::xs;
+                ok = mbar_wait(dz_full + sz, (u / L::dzs) & 1) && !*s_fail;
                 if (!ok) break;
-                const uint32_t dz = base + s * L::unit, x = dz + L::operand;
-                if (q.want_w) {
-                    if (kSplit) {
-                        ok = mbar_wait(dw_empty, (u & 1) ^ 1) && !*s_fail;
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + kDw;
-                    const uint64_t a = desc_sw128(dz, L::panel), b = desc_sw128(x, L::panel);
-                    const uint64_t lo = desc_sw128(dz + 2 * L::panel, L::panel);
-                    for (int e = 0; e < kBlock / 16; ++e) {
-                        const uint32_t off = 2048u * e >> 4;
-                        if constexpr (kSplit) {
-                            mma_f16(d, a + off, b + off, kBase | kAMn | (192u >> 3 << 17), e > 0);
-                            mma_f16(d + 128, lo + off, b + off, kBase | kAMn | (64u >> 3 << 17), 1);
-                        } else {
-                            mma_f16(d, a + off, b + off, kBase | kAMn | (k16 >> 3 << 17),
-                                    u > 0 || e > 0);
-                        }
-                    }
-                    if (kSplit || t + step >= q.tiles) mma_commit(dw_full);
-                }
-                mma_commit(x_empty + s);
-                if (q.want_x) {
+                const uint32_t dz = base + sz * L::operand, x = base + L::x + sx * L::operand;
+                if (q.want_x) {   // (while x's operand is made)
                     // (one accumulator in 32 bits, two in 16)
                     const int buf = kSplit ? 0 : u & 1, turn = kSplit ? u : u >> 1;
                     ok = mbar_wait(dx_empty + buf, (turn & 1) ^ 1) && !*s_fail;
@@ -659,7 +660,28 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     }
                     mma_commit(dx_full + buf);
                 }
-                mma_commit(dz_empty + s);
+                if (q.want_w) {
+                    ok = mbar_wait(x_full + sx, (u / L::xs) & 1) && !*s_fail;
+                    if (kSplit && ok) ok = mbar_wait(dw_empty, (u & 1) ^ 1) && !*s_fail;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + kDw;
+                    const uint64_t a = desc_sw128(dz, L::panel), b = desc_sw128(x, L::panel);
+                    const uint64_t lo = desc_sw128(dz + 2 * L::panel, L::panel);
+                    for (int e = 0; e < kBlock / 16; ++e) {
+                        const uint32_t off = 2048u * e >> 4;
+                        if constexpr (kSplit) {
+                            mma_f16(d, a + off, b + off, kBase | kAMn | (192u >> 3 << 17), e > 0);
+                            mma_f16(d + 128, lo + off, b + off, kBase | kAMn | (64u >> 3 << 17), 1);
+                        } else {
+                            mma_f16(d, a + off, b + off, kBase | kAMn | (k16 >> 3 << 17),
+                                    u > 0 || e > 0);
+                        }
+                    }
+                    if (kSplit || t + step >= q.tiles) mma_commit(dw_full);
+                    mma_commit(x_empty + sx);
+                }
+                mma_commit(dz_empty + sz);
             }
             if (!ok) {
                 *s_fail = 1u;
@@ -688,36 +710,21 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             ++f;
         };
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
-            const int s = u % L::units, turn = u / L::units;
+            const int sz = u % L::dzs, sx = u % L::xs;
             const int64_t row0 = t * kBlock, left = q.rows - row0;
             const int rows = (int)(left < kBlock ? left : kBlock);
-            unsigned char* unit = smem + s * L::unit;
-            if (q.want_w) {
-                ok = warp_all(mbar_wait(x_empty + s, (turn & 1) ^ 1) && !*s_fail);
-#pragma unroll 1
-                for (int i = 0; i < kBlock && ok; i += kRowsX) {
-                    if (!wait_piece()) break;
-                    const T* raw =
-                        reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
-                    unsigned char* to = unit + L::operand + i * 128;
-                    if (kVec || q.vec_k)
-                        make_operand<T, kActNone, kPanels, false, kRowsX>(to, raw, nullptr, rows - i,
-                                                                          q.k, true, true, mine,
-                                                                          none);
-                    else
-                        make_operand<T, kActNone, kPanels, false, kRowsX>(
-                            to, q.raw ? raw : static_cast<const T*>(q.x) + (row0 + i) * q.k, nullptr,
-                            rows - i, q.k, q.raw, false, mine, none);
-                    done_piece();
-                }
-            }
-            if (ok) ok = warp_all(mbar_wait(dz_empty + s, (turn & 1) ^ 1) && !*s_fail);
+            const auto given = [&](uint64_t* full) {   // an operand is complete
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            };
+            ok = warp_all(mbar_wait(dz_empty + sz, ((u / L::dzs) & 1) ^ 1) && !*s_fail);
 #pragma unroll 1
             for (int i = 0; i < kBlock && ok; i += kRowsZ) {
                 if (!wait_piece()) break;
                 const T* raw = reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
                 const T* z = raw + L::piece / 2 / (int)sizeof(T);
-                unsigned char* to = unit + i * 128;
+                unsigned char* to = smem + sz * L::operand + i * 128;
                 if (kVec || q.vec_n) {
                     make_operand<T, kAct, kPanels, true, kRowsZ>(to, raw, z, rows - i, q.n, true,
                                                                  true, mine, sum);
@@ -731,9 +738,28 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 done_piece();
             }
             if (!ok) break;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(unit_full + s);
+            given(dz_full + sz);
+            if (q.want_w) {
+                ok = warp_all(mbar_wait(x_empty + sx, ((u / L::xs) & 1) ^ 1) && !*s_fail);
+#pragma unroll 1
+                for (int i = 0; i < kBlock && ok; i += kRowsX) {
+                    if (!wait_piece()) break;
+                    const T* raw =
+                        reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
+                    unsigned char* to = smem + L::x + sx * L::operand + i * 128;
+                    if (kVec || q.vec_k)
+                        make_operand<T, kActNone, kPanels, false, kRowsX>(to, raw, nullptr, rows - i,
+                                                                          q.k, true, true, mine,
+                                                                          none);
+                    else
+                        make_operand<T, kActNone, kPanels, false, kRowsX>(
+                            to, q.raw ? raw : static_cast<const T*>(q.x) + (row0 + i) * q.k, nullptr,
+                            rows - i, q.k, q.raw, false, mine, none);
+                    done_piece();
+                }
+                if (!ok) break;
+                given(x_full + sx);
+            }
         }
         if (!ok) *s_fail = 1u;
         if (q.sums) {   // the rows of threads: in a warp, then between the warps
@@ -898,6 +924,11 @@ bool stream_plan(const LinearCall& c, Stream* q, int* smem) {
 }
 
 template <typename T, int kPanels>
+constexpr size_t back_smem(bool act) {
+    return act ? BackSmem<T, kPanels, true>::bytes : BackSmem<T, kPanels, false>::bytes;
+}
+
+template <typename T, int kPanels>
 cudaError_t prepare_back() {
     cudaError_t e = cudaSuccess;
     for (auto* f : {k_linear_narrow<T, kActNone, kPanels, true>,
@@ -908,7 +939,9 @@ cudaError_t prepare_back() {
                     k_linear_narrow<T, kActRelu, kPanels, false>})
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     BackSmem<T, kPanels>::bytes);
+                                     (int)(back_smem<T, kPanels>(true) > back_smem<T, kPanels>(false)
+                                               ? back_smem<T, kPanels>(true)
+                                               : back_smem<T, kPanels>(false)));
     return e;
 }
 
@@ -988,13 +1021,12 @@ cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnS
                    : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels, kVec>
                                        : k_linear_narrow<T, kActNone, kPanels, kVec>;
         };
-        auto* kernel = q.vec_n && q.vec_k && q.out.vec ? pick(std::true_type()) : pick(std::false_type());
-        return launch_pdl(kernel, dim3(ctas), dim3(kBackThreads), BackSmem<T, kPanels>::bytes, s, q,
-                          st);
+        return launch_pdl(q.vec_n && q.vec_k && q.out.vec ? pick(std::true_type())
+                                                          : pick(std::false_type()),
+                          dim3(ctas), dim3(kBackThreads), back_smem<T, kPanels>(act), s, q, st);
     };
-    return k <= kPanel && n <= kPanel
-                        ? run(std::integral_constant<int, 1>())
-                        : run(std::integral_constant<int, kBackSide<T> / kPanel>());
+    return k <= kPanel && n <= kPanel ? run(std::integral_constant<int, 1>())
+                                      : run(std::integral_constant<int, kBackSide<T> / kPanel>());
 }
 template cudaError_t launch_narrow<float>(const LinearCall&, float*, float*, LearnState*, int,
                                           cudaStream_t);
