@@ -24,7 +24,8 @@ namespace {
 
 // A matrix [rows, cols] made into an operand: times the activation's slope at `pre` (the gradient
 // dz from dy), split into planes [planes][rows][pitch] of bfloat16, and its column sums taken, a
-// partial sum [cols] per block of rows.  A thread has eight columns of every (256 / tx)-th row.
+// partial sum [cols] per block of rows.  A thread has eight columns of every (256 / tx)-th row, and
+// the loads of two or four rows in flight.  16381 x 4096 with SiLU in 16 bits: 72 us for 403 MB.
 struct Operand {
     const void* src;
     const void* pre;
@@ -254,7 +255,7 @@ k_linear_rows(const T* __restrict__ x, const T* __restrict__ weight, int64_t k, 
 // ------------------------------------------------------------------ plans --
 size_t plane_size(int64_t rows, int64_t cols) { return (size_t)rows * round8(cols); }
 
-// Blocks of rows of k_linear_operand: about eight blocks per SM over the whole matrix.
+// Blocks of rows of k_linear_operands: about eight blocks per SM over the whole matrix.
 struct OperandGrid {
     int tx;
     int64_t block_rows, blocks, col_blocks;
@@ -344,7 +345,8 @@ struct Maker {
     }
 };
 
-// (16 parts or fewer: a thread per four columns, each part's load behind the one before)
+// (Up to 16 parts a thread's loads follow one another; 304 parts of 64 x 64 would take some 20 us
+// so, and take 4 by 64 threads.)
 template <typename T>
 cudaError_t join(const Result& q, const float* parts, int n_sms, cudaStream_t s) {
     const bool many = q.splits > 16;

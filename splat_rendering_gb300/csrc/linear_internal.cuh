@@ -501,7 +501,7 @@ template <typename T>
 cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnState* st, int n_sms,
                           cudaStream_t s);
 
-// linear.cu: parts added in their order; partial column sums [blocks][cols] too.
+// linear.cu: parts added in their order.
 template <typename T>
 cudaError_t launch_join(const Result& q, const float* parts, int n_sms, cudaStream_t s);
 

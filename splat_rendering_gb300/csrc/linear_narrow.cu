@@ -22,12 +22,22 @@ namespace {
 // three, mid against hi and mid, lo against hi.  Their sums in three ranges of
 // columns are hi hi, (hi mid + mid hi), (hi lo + mid mid + lo hi), so that what
 // the tensor cores truncate is relative to each, of at most 128 of K, as there.
-// (Six MMAs into one accumulator, hi hi last, are as exact; an MMA takes some
-// 140 cycles whatever its columns, and 24 of them were 80 % of a tile's time.)
+// (Six MMAs of 64 columns into one accumulator, hi hi last, are as exact and take
+// half as long again: an MMA reads 128 rows of A whatever its columns.)
+//
+// 1M x 64 -> 64 with SiLU in 32 bits: 94 us, 5.7 TB/s of measured 6.8 (its bytes
+// take 79); 777600 x 64 -> 64 in 16 bits 50 us, with a residual 62 (29 and 44).
+// Bound by the warps' work on a tile, not by its bytes: operands (LDS, three
+// conversions, STS), the exchange and the activation, whose exponential and
+// reciprocal are half of the bfloat16 tile's time on their pipe.
 constexpr int kStreamThreads = 576;   // warps: copies, MMAs, eight of operands, eight of the epilogue
 constexpr int kStreamMaxK = 128;
 template <typename T>
 constexpr int kStreamN = sizeof(T) == 4 ? 64 : 128;   // outputs of a CTA
+// Up to eight blocks of them read the same rows side by side: 200000 x 64 -> 512 in 32 bits takes 125
+// us, by the wide products 262, 128 -> 512 291 and 300 (but 128 -> 1024 in sixteen blocks, per 100000
+// rows, 302 and 274); in 16 bits 200000 x 64 -> 64 17 and 28, 100000 x 128 -> 1024 92 and 104.
+constexpr int kStreamBlocks = 8;
 
 struct Stream {
     const void* x;         // [m, k]
@@ -58,7 +68,6 @@ __host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, i
     return s;
 }
 constexpr int kStreamSmemMax = 227 * 1024 - 512;   // (and the bias)
-
 
 // kVec: rows of x and of the result are whole vectors.  kSkip: there is a residual.
 template <typename T, bool kVec, bool kSkip>
@@ -309,24 +318,31 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 // --------------------------------------------- narrow layers, gradients --
 // All gradients of a narrow layer in one pass over dy, z and x: a persistent CTA
 // per SM, tiles of 128 rows.  One thread keeps raw rows coming (contiguous bulk
-// copies, in pieces of 16 or 32 KB: a whole tile at a time, its way in was 44 %
-// of the time), eight warps make dz and x into operands (and add up dz's columns), one
-// thread issues the MMAs, eight warps finish dx.  dz's tile, 128 rows of 128
-// bytes a panel, is an MN-major left operand of dW = dz^T x (its rows are the
-// contraction) and, the same bytes, a K-major one of dx = dz W (its rows are
-// rows).  dW stays in the CTA; k_linear_join adds up the CTAs' sums in their
-// order.
+// copies, in pieces of 16 or 32 KB: with a whole tile at a time their way in was
+// 44 % of the time), eight warps make dz and x into operands (and add up dz's
+// columns), one thread issues the MMAs, eight warps finish dx.  dz's tile, 128
+// rows of 128 bytes a panel, is a K-major left operand of dx = dz W (its rows are
+// rows) and, the same bytes, an MN-major one of dW = dz^T x (its rows are the
+// contraction).  dW stays in the CTA; k_linear_join adds up the CTAs' sums in
+// their order.
 //
 // In 32 bits the planes of dz are two groups of one left operand [hi; mid] of
 // dW, those of x three of the right one, so that one MMA makes six products
 // (mid lo among them, in columns that are not read); lo hi is a second one, into
 // the columns of hi lo.  They are drained every tile (128 of K) into registers:
 // the rows of hi, and those of mid, are parts of their own.  dx as in the
-// forward kernel.  There is room for one tile's operands and its raw rows: x's
-// are made while the MMAs of dx run, which do not need them.
+// forward kernel.  x's operand is made while the MMAs of dx run, which do not
+// need it, and where there is room dz's next one during those of dW.
+//
+// 1M x 64 -> 64 in 32 bits: 169 us, with SiLU 205 (118 and 158 by the bytes); 777600
+// x 64 -> 64 in 16 bits 62 us, with ReLU 74, with SiLU 82 (44 and 59).  Bound by the
+// eight warps that make operands; loads straight to registers, kept ahead of their
+// use, were slower (their fence awaits every load).
 constexpr int kBackThreads = 576;   // warps: MMAs, eight of operands, eight of the epilogue, copies
+// Inputs and outputs of a layer, as many as there is room for (200000 x 64 -> 64 with SiLU in 32
+// bits: 55 us, by the wide products 130; 128 -> 128 in 16 bits 66 and 81).
 template <typename T>
-constexpr int kBackSide = sizeof(T) == 4 ? 64 : 128;   // inputs and outputs of a layer
+constexpr int kBackSide = sizeof(T) == 4 ? 64 : 128;
 
 struct Narrow {
     const void *grad_y, *pre, *x, *weight;
@@ -698,7 +714,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             for (int e = 0; e < V; ++e) sum[h][e] = none[h][e] = 0.0f;
         int u = 0, f = 0;
         bool ok = true;
-        // the piece in turn, or the place of row r in the tensor
+        // the piece in turn (where the tensors do not begin on 16 bytes there are none)
         const auto wait_piece = [&]() {
             if (kVec || q.raw)
                 ok = warp_all(mbar_wait(raw_full + f % L::pieces, (f / L::pieces) & 1) && !*s_fail);
@@ -844,7 +860,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 tc_fence_after();
 #pragma unroll
                 for (int p = 0; p < 3; ++p) {
-                    if (p == 2 && quarter >= 2) continue;   // lo mid, or what lies behind lo
+                    if (p == 2 && quarter >= 2) continue;   // mid lo, and what lies behind lo
                     uint32_t w[32];
                     __syncwarp();
                     tmem_ld32(tmem + kDw + lanes + p * 64 + group * 32, w);
@@ -899,7 +915,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
 template <typename T>
 bool stream_plan(const LinearCall& c, Stream* q, int* smem) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    if (c.inputs > kStreamMaxK || c.outputs > 4 * kStreamN<T> || !aligned16(c.x)) return false;
+    if (c.inputs > kStreamMaxK || c.outputs > kStreamBlocks * kStreamN<T> || !aligned16(c.x)) return false;
     q->x = c.x;
     q->weight = c.weight;
     q->tiles = ceil_div(c.rows, kBlock);

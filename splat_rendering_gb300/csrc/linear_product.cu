@@ -8,17 +8,29 @@ namespace linear {
 namespace {
 
 // -------------------------------------------------------------- products --
-// One kernel for the three products, a persistent CTA per SM.  Roles: one
-// thread keeps a ring of operand stages filled by TMA (out of range: zeros), one
-// issues the MMAs into one of two accumulators in tensor memory, and the other
-// warps finish the other (four per half or quarter of the tile's columns, a
-// thread per row): bias, activation, residual, rounding; through a swizzled exchange in
-// shared memory, so that a warp stores whole sectors.
+// One kernel for the three products, a persistent CTA per SM, or a pair of them on
+// a tile of twice the rows.  Roles: one thread keeps a ring of operand stages
+// filled by TMA (out of range: zeros), one issues the MMAs into one of two
+// accumulators in tensor memory, and the other warps finish the other (four per
+// half or quarter of the tile's columns, a thread per row): bias, activation,
+// residual, rounding; through a swizzled exchange in shared memory, so that a
+// warp stores whole sectors.
+//
+// A stage of a 128 x 256 tile is 48 KB, and at the MMAs' rate the SMs would ask
+// the L2 for more than it gives (the MMAs waited for operands half of the time).
+// A pair of CTAs reads each half of B once for both: 32 KB a stage.  16381 x 1024
+// -> 4096 in 16 bits: 90 us (97 by single CTAs), dx 84 (95), dW 80 (89); by the
+// operations 73 at the rate of a library's product in a burst, 81 in a long run.
+// dx and dW have 256 and 64 tiles for 76 pairs, which is 84 % of them busy; the
+// MMAs of a 256 x 256 tile follow each other at 1.05 times their own time.
 //
 // In 32 bits the tensor cores' accumulation, which truncates, would be what
 // limits the result (of K = 2048, some 2^-18.5 of it): hi hi and the other
 // five products have accumulators of their own, and both are drained and
-// summed in registers every kChunk panels (128 of K).
+// summed in registers every kChunk panels (128 of K).  4001 x 1500 -> 509: 24
+// panels of 24 MMAs of 256 x 128 at 78 cycles, some 30 us, after 8 us for the
+// planes.  In 16 bits nothing is drained: what is truncated of K = 2^16 is still
+// below half a step of the result.
 //
 // Where a product has few tiles for the SMs and a long contraction (dW: one
 // tile and a million rows), its parts are separate work items, whose sums
@@ -449,17 +461,19 @@ bool encode(CUtensorMap* map, const Matrix& m, int box_rows) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The sums' workspace of a product in parts: as many as fill the SMs once, of kLeast panels.
+// The parts of a product: as many as fill the SMs once, of kLeast panels or more.
 constexpr int kLeast = 4;
 int splits_of(int64_t tiles, int64_t panels, int n_sms) {
     const int64_t fit = n_sms / tiles, most = panels / kLeast;
     const int64_t s = fit < most ? fit : most;
     return s > 1 ? (int)s : 1;
 }
-// Columns of a tile: an MMA of N = 256 takes little longer than one of 128.
+// Columns of a tile: an MMA of N = 256 takes 137 cycles, one of 128 114.  (In 32 bits the
+// accumulators of both kinds, twice, leave room for 128.)
 int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
 // Pairs of CTAs where tiles of 256 rows are not half empty.
 bool paired(int64_t m) { return m > kBlock; }
+
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
 cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_t k, float* parts,
                        LearnState* st, int n_sms, cudaStream_t s) {
