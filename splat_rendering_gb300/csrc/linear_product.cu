@@ -88,9 +88,10 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
     return at;
 }
+// (what it orders is the accumulator's loads, which are complete: a release to the whole cluster
+// would wait for the stores of the results too)
 __device__ __forceinline__ void arrive_at(uint32_t mbar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 // into this CTA's shared memory, counted on the first one's barrier
 __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int col, int row,
