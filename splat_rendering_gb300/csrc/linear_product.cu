@@ -19,7 +19,7 @@ namespace {
 // A stage of a 128 x 256 tile is 48 KB, and at the MMAs' rate the SMs would ask
 // the L2 for more than it gives (the MMAs waited for operands half of the time).
 // A pair of CTAs reads each half of B once for both: 32 KB a stage.  16381 x 1024
-// -> 4096 in 16 bits: 90 us (97 by single CTAs), dx 84 (95), dW 80 (89); by the
+// -> 4096 in 16 bits: 83 us (101 by single CTAs), dx 82 (95), dW 79 (89); by the
 // operations 73 at the rate of a library's product in a burst, 81 in a long run.
 // dx and dW have 256 and 64 tiles for 76 pairs, which is 84 % of them busy; the
 // MMAs of a 256 x 256 tile follow each other at 1.05 times their own time.
@@ -29,7 +29,8 @@ namespace {
 // five products have accumulators of their own, and both are drained and
 // summed in registers every kChunk panels (128 of K).  4001 x 1500 -> 509: 24
 // panels of 24 MMAs of 256 x 128 at 78 cycles, some 30 us, after 8 us for the
-// planes.  In 16 bits nothing is drained: what is truncated of K = 2^16 is still
+// planes (dx 42 us of 45 by single CTAs; drained every 256 of K: 39, and twice as far
+// off).  In 16 bits nothing is drained: what is truncated of K = 2^16 is still
 // below half a step of the result.
 //
 // Where a product has few tiles for the SMs and a long contraction (dW: one
@@ -42,11 +43,11 @@ struct Product {
 };
 
 // warps: copies, MMAs, and of the epilogue eight, or for a layer's outputs in 16 bits, where it has
-// every tile's activation to do within the MMAs' time, sixteen (16381 x 1024 -> 4096: 90 us, with
-// eight 96; dx, which has none: 84 us with eight, with sixteen 88)
+// every tile's activation to do within the MMAs' time, sixteen (16381 x 1024 -> 4096: 83 us, with
+// eight 85; dx, which has none: 82 us with eight, with sixteen 85)
 constexpr int epilogue_warps(int planes, bool outputs) { return planes == 1 && outputs ? 16 : 8; }
 constexpr int kChunk = 2;              // panels per drained sum (32 bits)
-constexpr int kGroup = 4;              // row blocks whose tiles lie side by side in time
+constexpr int kGroup = 4;              // row blocks whose tiles lie side by side in time (of 16: 1 us more)
 
 template <int kPlanes, int kN, int kCtas, bool kOutputs>
 struct ProductSmem {
