@@ -15,7 +15,7 @@
 // at most 2^-23 of it and, their signs being random, far below the rounding of
 // a sum in 32 bits.
 //
-// This file has the calls' plans and their small kernels: operands, column sums, parts, few rows.
+// This file has the calls' plans and their small kernels: operands, joins, few rows.
 #include "linear_internal.cuh"
 
 namespace pulsar {
@@ -131,33 +131,23 @@ k_linear_operands(const __grid_constant__ Operands all) {
     else make_planes<T, kPlanes, kActNone>(q, s_sums);
 }
 
-// The sums of `blocks` partial rows of `cols`: 32 columns a block, 32 rows of threads.
-__global__ void __launch_bounds__(1024)
-k_linear_sums(const float* __restrict__ part, int64_t blocks, int64_t cols,
-              float* __restrict__ out) {
-    __shared__ float s[32][33];
-    pdl_begin();
-    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    float v = 0.0f;
-    if (col < cols)
-        for (int64_t b = threadIdx.y; b < blocks; b += 32) v += part[b * cols + col];
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    v = s[threadIdx.x][threadIdx.y];   // a warp per column
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
-    const int64_t mine = (int64_t)blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && mine < cols) out[mine] = v;
-}
+// The last launch of a call: the parts of its products added in a fixed order, and finished, and
+// the partial column sums [blocks][cols] of a bias' gradient.
+struct Joins {
+    Result of[2];
+    const float* parts[2];   // NULL: there are none
+    const float* sums;       // NULL: none
+    int64_t sum_blocks, cols;
+    float* sum_out;
+};
 
-// The parts of a product added in a fixed order, and finished: a thread has four columns, of few
-// parts all of them, of many (kLanes = 64) every 64th, which the block then adds up.
+// A thread has four elements, of few parts all of them, of many (kLanes = 64) every 64th, which the
+// block then adds up.  (Of 16 parts a thread's loads may follow one another; 304 parts of 64 x 64
+// would take some 20 us so, and take 4 by 64 threads.)
 template <typename T, int kLanes>
-__global__ void __launch_bounds__(256)
-k_linear_join(const __grid_constant__ Result q, const float* __restrict__ part) {
-    constexpr int kPer = 256 / kLanes;   // groups of four columns of a block
-    __shared__ float4 s_sum[8][kLanes > 1 ? kPer : 1];
-    pdl_begin();
+__device__ __forceinline__ void join_parts(const Result& q, const float* __restrict__ part,
+                                           float4 (*s_sum)[4]) {
+    constexpr int kPer = 256 / kLanes;   // fours of elements of a block
     const int64_t size = q.m * q.n, total = (size + 3) / 4;
     const int mine = threadIdx.x % kPer, from = threadIdx.x / kPer;
     for (int64_t g0 = (int64_t)blockIdx.x * kPer; g0 < total; g0 += (int64_t)gridDim.x * kPer) {
@@ -178,19 +168,55 @@ k_linear_join(const __grid_constant__ Result q, const float* __restrict__ part) 
                 for (int e = 0; e < 4; ++e) z[e] += __shfl_xor_sync(0xffffffffu, z[e], d);
             __syncthreads();
             if ((threadIdx.x & 31) < kPer)
-                s_sum[threadIdx.x >> 5][kLanes > 1 ? mine : 0] = make_float4(z[0], z[1], z[2], z[3]);
+                s_sum[threadIdx.x >> 5][mine & 3] = make_float4(z[0], z[1], z[2], z[3]);
             __syncthreads();
             if (from > 0) continue;
             for (int e = 0; e < 4; ++e) z[e] = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) {
-                const float4 u = s_sum[w][kLanes > 1 ? mine : 0];
+                const float4 u = s_sum[w][mine & 3];
                 z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (e < n) finish1<T>(q, plus(z[e], q.bias ? q.bias[(at + e) % q.n] : 0.0f), at + e);
+    }
+}
+
+// Eight columns of sums a block, 32 threads to each.
+__device__ __forceinline__ void join_sums(const Joins& q, float (*s)[33]) {
+    const int c = threadIdx.x & 7, from = threadIdx.x >> 3;
+    for (int64_t c0 = (int64_t)blockIdx.x * 8; c0 < q.cols; c0 += (int64_t)gridDim.x * 8) {
+        float v = 0.0f;
+        if (c0 + c < q.cols)
+#pragma unroll 4
+            for (int64_t b = from; b < q.sum_blocks; b += 32) v += q.sums[b * q.cols + c0 + c];
+        __syncthreads();
+        s[c][from] = v;
+        __syncthreads();
+        v = s[threadIdx.x >> 5][threadIdx.x & 31];   // a warp per column
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+        const int64_t col = c0 + (threadIdx.x >> 5);
+        if ((threadIdx.x & 31) == 0 && col < q.cols) q.sum_out[col] = v;
+    }
+}
+
+constexpr int kFewParts = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_linear_joins(const __grid_constant__ Joins q) {
+    __shared__ float4 s_sum[8][4];
+    __shared__ float s_cols[8][33];
+    pdl_begin();
+    if (blockIdx.y == 2) {
+        if (q.sums) join_sums(q, s_cols);
+    } else if (q.parts[blockIdx.y]) {
+        const Result& r = q.of[blockIdx.y];
+        if (r.splits > kFewParts) join_parts<T, 64>(r, q.parts[blockIdx.y], s_sum);
+        else join_parts<T, 1>(r, q.parts[blockIdx.y], s_sum);
     }
 }
 
@@ -277,7 +303,7 @@ OperandGrid operand_grid(int64_t rows, int64_t cols) {
 
 struct Space {
     __nv_bfloat16 *x, *w, *dz;
-    float *sums, *parts;
+    float *sums, *parts, *parts_w;   // parts: of the outputs or dx, of dW
     size_t bytes;
 };
 Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
@@ -289,18 +315,17 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
     s.dz = c.take<__nv_bfloat16>(planes * plane_size(m, n));
     const int64_t blocks = operand_grid(m, n).blocks;
     s.sums = c.take<float>((size_t)(blocks > kMostSms ? blocks : kMostSms) * n);
-    size_t parts = product_parts(planes, m, n, k);
-    const size_t dx = product_parts(planes, m, k, n), dw = product_parts(planes, n, k, m);
-    if (dx > parts) parts = dx;
-    if (dw > parts) parts = dw;
+    const size_t y = product_parts(planes, m, n, k), dx = product_parts(planes, m, k, n);
+    size_t dw = product_parts(planes, n, k, m);
     const bool f32 = dtype == kF32;
     if (f32 ? is_narrow<float>(k, n) : is_narrow<__nv_bfloat16>(k, n)) {
         const size_t narrow = (size_t)(f32 ? narrow_parts<float>(m, kMostSms)
                                            : narrow_parts<__nv_bfloat16>(m, kMostSms)) *
                               part_size(n, k);
-        if (narrow > parts) parts = narrow;
+        if (narrow > dw) dw = narrow;
     }
-    s.parts = c.take<float>(parts);
+    s.parts = c.take<float>(y > dx ? y : dx);
+    s.parts_w = c.take<float>(dw);
     s.bytes = c.used;
     return s;
 }
@@ -345,15 +370,20 @@ struct Maker {
     }
 };
 
-// (Up to 16 parts a thread's loads follow one another; 304 parts of 64 x 64 would take some 20 us
-// so, and take 4 by 64 threads.)
 template <typename T>
-cudaError_t join(const Result& q, const float* parts, int n_sms, cudaStream_t s) {
-    const bool many = q.splits > 16;
-    const int64_t blocks = ceil_div(ceil_div(q.m * q.n, 4), many ? 4 : 256);
-    return launch_pdl(many ? k_linear_join<T, 64> : k_linear_join<T, 1>,
-                      dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8)), dim3(256), 0, s, q,
-                      parts);
+cudaError_t launch_joins(const Joins& q, int n_sms, cudaStream_t s) {
+    int64_t blocks = 0;
+    for (int i = 0; i < 2; ++i) {
+        if (!q.parts[i]) continue;
+        const Result& r = q.of[i];
+        const int64_t b = ceil_div(ceil_div(r.m * r.n, 4), r.splits > kFewParts ? 4 : 256);
+        if (b > blocks) blocks = b;
+    }
+    if (q.sums && ceil_div(q.cols, 8) > blocks) blocks = ceil_div(q.cols, 8);
+    if (blocks == 0) return cudaSuccess;
+    return launch_pdl(k_linear_joins<T>,
+                      dim3((unsigned)(blocks < n_sms * 8 ? blocks : n_sms * 8), q.sums ? 3 : 2),
+                      dim3(256), 0, s, q);
 }
 
 template <typename T, int V>
@@ -399,7 +429,11 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
     const Matrix w = make.add(c.weight, nullptr, kActNone, n, k, sp.w, nullptr);
     e = make.launch(s);
     if (e != cudaSuccess) return e;
-    return launch_product<T>(q, x, false, w, false, k, sp.parts, st, n_sms, s);
+    Joins joins{};
+    e = launch_product<T>(q, x, false, w, false, k, sp.parts, &joins.of[0], st, n_sms, s);
+    if (e != cudaSuccess || joins.of[0].splits <= 1) return e;
+    joins.parts[0] = sp.parts;
+    return launch_joins<T>(joins, n_sms, s);
 }
 
 template <typename T>
@@ -412,24 +446,32 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
         return e;
     }
     const Space sp = carve(ws, m, k, n, c.dtype);
-    const auto sum_bias = [&](int64_t blocks) {
-        return launch_pdl(k_linear_sums, dim3((unsigned)ceil_div(n, 32)), dim3(32, 32), 0, s,
-                          (const float*)sp.sums, blocks, n, c.grad_bias);
-    };
+    Joins joins{};
+    joins.sums = c.grad_bias ? sp.sums : nullptr;
+    joins.sum_blocks = operand_grid(m, n).blocks;
+    joins.cols = n;
+    joins.sum_out = c.grad_bias;
+    Result dx{}, dw{};
+    dx.m = m;
+    dw.m = n;
+    dx.n = dw.n = k;
+    dx.out = c.grad_x;
+    dw.out = c.grad_weight;
+    dx.vec = vec4<T>(dx);
+    dw.vec = vec4<T>(dw);
     if (is_narrow<T>(k, n)) {
-        cudaError_t e = launch_narrow<T>(c, sp.parts, c.grad_bias ? sp.sums : nullptr, st, n_sms, s);
+        const cudaError_t e = launch_narrow<T>(c, sp.parts_w, c.grad_bias ? sp.sums : nullptr, st,
+                                               n_sms, s);
+        if (e != cudaSuccess) return e;
         const int64_t tiles = ceil_div(m, kBlock);
-        if (e == cudaSuccess && c.grad_bias) e = sum_bias(tiles < n_sms ? tiles : n_sms);
-        if (e == cudaSuccess && c.grad_weight) {
-            Result q{};
-            q.m = n;
-            q.n = k;
-            q.out = c.grad_weight;
-            q.splits = narrow_parts<T>(m, n_sms);
-            q.part = part_size(n, k);
-            e = launch_join<T>(q, sp.parts, n_sms, s);
+        joins.sum_blocks = tiles < n_sms ? tiles : n_sms;
+        if (c.grad_weight) {
+            joins.of[1] = dw;
+            joins.of[1].splits = narrow_parts<T>(m, n_sms);
+            joins.of[1].part = part_size(n, k);
+            joins.parts[1] = sp.parts_w;
         }
-        return e;
+        return launch_joins<T>(joins, n_sms, s);
     }
     Maker<T> make;
     const Matrix dz = make.add(c.grad_y, c.act == kActNone ? nullptr : c.pre, c.act, m, n,
@@ -438,37 +480,17 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
     const Matrix w = make.add(c.weight, nullptr, kActNone, n, k, c.grad_x ? sp.w : nullptr, nullptr);
     const Matrix x = make.add(c.x, nullptr, kActNone, m, k, c.grad_weight ? sp.x : nullptr, nullptr);
     cudaError_t e = make.launch(s);
-    if (e == cudaSuccess && c.grad_bias)
-        e = sum_bias(operand_grid(m, n).blocks);
-    if (e == cudaSuccess && c.grad_x) {
-        Result q{};
-        q.m = m;
-        q.n = k;
-        q.out = c.grad_x;
-        q.vec = vec4<T>(q);
-        e = launch_product<T>(q, dz, false, w, true, n, sp.parts, st, n_sms, s);
-    }
-    if (e == cudaSuccess && c.grad_weight) {
-        Result q{};
-        q.m = n;
-        q.n = k;
-        q.out = c.grad_weight;
-        q.vec = vec4<T>(q);
-        e = launch_product<T>(q, dz, true, x, true, m, sp.parts, st, n_sms, s);
-    }
-    return e;
+    if (e == cudaSuccess && c.grad_x)
+        e = launch_product<T>(dx, dz, false, w, true, n, sp.parts, &joins.of[0], st, n_sms, s);
+    if (e == cudaSuccess && c.grad_weight)
+        e = launch_product<T>(dw, dz, true, x, true, m, sp.parts_w, &joins.of[1], st, n_sms, s);
+    if (e != cudaSuccess) return e;
+    joins.parts[0] = joins.of[0].splits > 1 ? sp.parts : nullptr;
+    joins.parts[1] = joins.of[1].splits > 1 ? sp.parts_w : nullptr;
+    return launch_joins<T>(joins, n_sms, s);
 }
 
 }  // namespace
-
-namespace linear {
-template <typename T>
-cudaError_t launch_join(const Result& q, const float* parts, int n_sms, cudaStream_t s) {
-    return join<T>(q, parts, n_sms, s);
-}
-template cudaError_t launch_join<float>(const Result&, const float*, int, cudaStream_t);
-template cudaError_t launch_join<__nv_bfloat16>(const Result&, const float*, int, cudaStream_t);
-}  // namespace linear
 
 size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
     return carve(nullptr, rows, inputs, outputs, dtype).bytes;

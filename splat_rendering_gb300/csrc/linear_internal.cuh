@@ -481,12 +481,14 @@ struct Matrix {
 };
 
 // Wide layers (linear_product.cu): a product of any size, q's sums of a(i, c) b(j, c) over k
-// values of c; x_mn: the operand's matrix has c as its rows.
+// values of c; x_mn: the operand's matrix has c as its rows.  Where *pending has more than one part
+// they are in `parts` and still to be joined.
 size_t product_parts(int planes, int64_t m, int64_t n, int64_t k);   // floats of workspace
 cudaError_t prepare_product();
 template <typename T>
 cudaError_t launch_product(const Result& q, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn,
-                           int64_t k, float* parts, LearnState* st, int n_sms, cudaStream_t s);
+                           int64_t k, float* parts, Result* pending, LearnState* st, int n_sms,
+                           cudaStream_t s);
 
 // Narrow layers (linear_narrow.cu).  The forward call: false where the layer is none.
 cudaError_t prepare_narrow();
@@ -500,10 +502,6 @@ int narrow_parts(int64_t rows, int n_sms);         // sums of dW, [outputs][inpu
 template <typename T>
 cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnState* st, int n_sms,
                           cudaStream_t s);
-
-// linear.cu: parts added in their order.
-template <typename T>
-cudaError_t launch_join(const Result& q, const float* parts, int n_sms, cudaStream_t s);
 
 }  // namespace linear
 }  // namespace pulsar

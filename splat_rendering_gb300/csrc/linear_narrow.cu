@@ -323,7 +323,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 // columns), one thread issues the MMAs, eight warps finish dx.  dz's tile, 128
 // rows of 128 bytes a panel, is a K-major left operand of dx = dz W (its rows are
 // rows) and, the same bytes, an MN-major one of dW = dz^T x (its rows are the
-// contraction).  dW stays in the CTA; k_linear_join adds up the CTAs' sums in
+// contraction).  dW stays in the CTA; k_linear_joins adds up the CTAs' sums in
 // their order.
 //
 // In 32 bits the planes of dz are two groups of one left operand [hi; mid] of

@@ -35,7 +35,7 @@ namespace {
 //
 // Where a product has few tiles for the SMs and a long contraction (dW: one
 // tile and a million rows), its parts are separate work items, whose sums
-// k_linear_join adds up in their order.
+// k_linear_joins adds up in their order.
 struct Product {
     CUtensorMap a, b;
     int tiles_m, tiles_n, panels;   // panels of the contraction
@@ -478,7 +478,7 @@ bool paired(int64_t m) { return m > kBlock; }
 
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
 cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_t k, float* parts,
-                       LearnState* st, int n_sms, cudaStream_t s) {
+                       Result* pending, LearnState* st, int n_sms, cudaStream_t s) {
     using L = ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>;
     Product q{};
     q.out = r;
@@ -489,6 +489,7 @@ cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_
     const int groups = n_sms / kCtas;   // of CTAs that share a tile
     q.out.splits = tiles <= groups ? splits_of(tiles, q.panels, groups) : 1;
     q.out.part = part_size(r.m, r.n);
+    *pending = q.out;
     if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : L::rows_b))
         return cudaErrorInvalidValue;
     const auto launch = [&](auto kernel) {
@@ -499,27 +500,24 @@ cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_
     if (q.out.splits == 1)
         return launch(r.vec ? k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>
                             : k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>);
-    Result whole = q.out;
     q.out = Result{r.m, r.n, nullptr, nullptr, nullptr, parts, kActNone, r.n % 4 == 0,
-                   whole.splits, whole.part};
-    const cudaError_t e =
-        launch(q.out.vec ? k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>
-                         : k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>);
-    return e != cudaSuccess ? e : launch_join<T>(whole, parts, n_sms, s);
+                   q.out.splits, q.out.part};
+    return launch(q.out.vec ? k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>
+                            : k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>);
 }
 
 template <typename T, bool kAMn, bool kBMn>
 cudaError_t product(const Result& q, const Matrix& a, const Matrix& b, int64_t k, float* parts,
-                    LearnState* st, int n_sms, cudaStream_t s) {
+                    Result* pending, LearnState* st, int n_sms, cudaStream_t s) {
     if constexpr (sizeof(T) == 4)
-        return paired(q.m) ? product_as<T, 3, 128, kAMn, kBMn, 2>(q, a, b, k, parts, st, n_sms, s)
-                           : product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
+        return paired(q.m) ? product_as<T, 3, 128, kAMn, kBMn, 2>(q, a, b, k, parts, pending, st, n_sms, s)
+                           : product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, pending, st, n_sms, s);
     else if (tile_n(1, q.n) == 128)
-        return product_as<T, 1, 128, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 1, 128, kAMn, kBMn, 1>(q, a, b, k, parts, pending, st, n_sms, s);
     else if (paired(q.m))
-        return product_as<T, 1, 256, kAMn, kBMn, 2>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 1, 256, kAMn, kBMn, 2>(q, a, b, k, parts, pending, st, n_sms, s);
     else
-        return product_as<T, 1, 256, kAMn, kBMn, 1>(q, a, b, k, parts, st, n_sms, s);
+        return product_as<T, 1, 256, kAMn, kBMn, 1>(q, a, b, k, parts, pending, st, n_sms, s);
 }
 
 template <typename T, int kPlanes, int kN, int kCtas, bool kAMn, bool kBMn>
@@ -558,15 +556,17 @@ size_t product_parts(int planes, int64_t m, int64_t n, int64_t k) {
 
 template <typename T>
 cudaError_t launch_product(const Result& q, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn,
-                           int64_t k, float* parts, LearnState* st, int n_sms, cudaStream_t s) {
-    if (a_mn) return product<T, true, true>(q, a, b, k, parts, st, n_sms, s);
-    return b_mn ? product<T, false, true>(q, a, b, k, parts, st, n_sms, s)
-                : product<T, false, false>(q, a, b, k, parts, st, n_sms, s);
+                           int64_t k, float* parts, Result* pending, LearnState* st, int n_sms,
+                           cudaStream_t s) {
+    if (a_mn) return product<T, true, true>(q, a, b, k, parts, pending, st, n_sms, s);
+    return b_mn ? product<T, false, true>(q, a, b, k, parts, pending, st, n_sms, s)
+                : product<T, false, false>(q, a, b, k, parts, pending, st, n_sms, s);
 }
 template cudaError_t launch_product<float>(const Result&, const Matrix&, bool, const Matrix&, bool,
-                                           int64_t, float*, LearnState*, int, cudaStream_t);
+                                           int64_t, float*, Result*, LearnState*, int,
+                                           cudaStream_t);
 template cudaError_t launch_product<__nv_bfloat16>(const Result&, const Matrix&, bool,
-                                                   const Matrix&, bool, int64_t, float*,
+                                                   const Matrix&, bool, int64_t, float*, Result*,
                                                    LearnState*, int, cudaStream_t);
 
 cudaError_t prepare_product() {
