@@ -43,7 +43,10 @@ struct Operands {   // of one call: the first may be a gradient with its activat
     Operand of[3];
 };
 
-template <typename T, int kPlanes, int kAct>
+// kWindows: rows may be no whole vectors, and are read by windows of whole ones.  (A kernel of its
+// own: its registers would cost the other a sixth, 60 us for 51 of a bias' gradient of 16381 x 4096
+// with SiLU.  Four windows in flight, not one by one: the gradients of 57072 x 27 -> 782 169 -> 146.)
+template <typename T, int kPlanes, int kAct, bool kWindows>
 __device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
     const int tx = threadIdx.x & (q.tx - 1), ty = threadIdx.x / q.tx, step = 256 / q.tx;
     const int64_t c = ((int64_t)blockIdx.y * q.tx + tx) * 8;
@@ -58,7 +61,10 @@ __device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
     const auto finish = [&](int64_t r, float (&v)[8], const float (&z)[8]) {
         to_dz<kAct>(v, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += e < n ? v[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            v[e] = e < n ? v[e] : 0.0f;   // (what a window has behind the row)
+            sum[e] += v[e];
+        }
         if (q.planes) put_chunk<kPlanes>(q.planes + r * q.pitch + c, q.plane * 2, v);
     };
     if (q.vec && n == 8) {
@@ -82,26 +88,40 @@ __device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
             }
         }
     } else if (n > 0) {
-        const T* end = static_cast<const T*>(q.src) + q.rows * q.cols;
-        const T* pre_end = static_cast<const T*>(q.pre) + q.rows * q.cols;
-        const auto load = [&](const T* p, const T* begin, const T* stop, float (&v)[8]) {
-            if (Window<T, 8>::within(p, begin, stop)) {
-                Window<T, 8> w;
-                w.load(p);
-                w.open(v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = e < n ? v[e] : 0.0f;
-            } else {
-                load8(p, n, false, v);
-            }
-        };
-#pragma unroll 2
-        for (int64_t r = r0 + ty; r < r1; r += step) {
+        const auto alone = [&](int64_t r) {
             float v[8], z[8];
-            load(src + r * q.cols, static_cast<const T*>(q.src), end, v);
-            if (kAct != kActNone)
-                load(pre + r * q.cols, static_cast<const T*>(q.pre), pre_end, z);
+            load8(src + r * q.cols, n, false, v);
+            if (kAct != kActNone) load8(pre + r * q.cols, n, false, z);
             finish(r, v, z);
+        };
+        if constexpr (!kWindows) {   // (of 32 bits: the last four columns)
+#pragma unroll 2
+            for (int64_t r = r0 + ty; r < r1; r += step) alone(r);
+        } else {
+            constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;
+            const int64_t total = q.rows * q.cols;
+            for (int64_t r = r0 + ty; r < r1; r += kBatch * step) {
+                const int64_t last = r + (kBatch - 1) * step;
+                // (a window may reach eight elements out of its own to the left, 16 to the right)
+                if (last < r1 && r * q.cols + c >= 8 && last * q.cols + c + 24 <= total) {
+                    Window<T, 8> a[kBatch], b[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        a[i].load(src + (r + i * step) * q.cols);
+                        if (kAct != kActNone) b[i].load(pre + (r + i * step) * q.cols);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        float v[8], z[8];
+                        a[i].open(v);
+                        if (kAct != kActNone) b[i].open(z);
+                        finish(r + i * step, v, z);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int64_t row = r; row <= last && row < r1; row += step) alone(row);
+                }
+            }
         }
     }
     if (!q.sums) return;
@@ -119,7 +139,7 @@ __device__ __forceinline__ void make_planes(const Operand& q, float* s_sums) {
     }
 }
 
-template <typename T, int kPlanes, int kAct>
+template <typename T, int kPlanes, int kAct, bool kWindows>
 __global__ void __launch_bounds__(256)
 k_linear_operands(const __grid_constant__ Operands all) {
     __shared__ float s_sums[256 * 8];
@@ -127,8 +147,8 @@ k_linear_operands(const __grid_constant__ Operands all) {
     pdl_begin();
     const Operand& q = all.of[blockIdx.z];
     if (blockIdx.x >= q.blocks || blockIdx.y >= q.col_blocks) return;
-    if (blockIdx.z == 0) make_planes<T, kPlanes, kAct>(q, s_sums);
-    else make_planes<T, kPlanes, kActNone>(q, s_sums);
+    if (blockIdx.z == 0) make_planes<T, kPlanes, kAct, kWindows>(q, s_sums);
+    else make_planes<T, kPlanes, kActNone, kWindows>(q, s_sums);
 }
 
 // The last launch of a call: the parts of its products added in a fixed order, and finished, and
@@ -363,10 +383,16 @@ struct Maker {
             if (all.of[i].blocks > grid.x) grid.x = all.of[i].blocks;
             if (all.of[i].col_blocks > grid.y) grid.y = all.of[i].col_blocks;
         }
-        return launch_pdl(act == kActSilu   ? k_linear_operands<T, kPlanes, kActSilu>
-                          : act == kActRelu ? k_linear_operands<T, kPlanes, kActRelu>
-                                            : k_linear_operands<T, kPlanes, kActNone>,
-                          grid, dim3(256), 0, s, all);
+        bool vec = true;
+        for (int i = 0; i < count; ++i) vec &= all.of[i].vec;
+        const auto pick = [&](auto windows) {
+            constexpr bool kWindows = decltype(windows)::value;
+            return act == kActSilu   ? k_linear_operands<T, kPlanes, kActSilu, kWindows>
+                   : act == kActRelu ? k_linear_operands<T, kPlanes, kActRelu, kWindows>
+                                     : k_linear_operands<T, kPlanes, kActNone, kWindows>;
+        };
+        return launch_pdl(vec ? pick(std::false_type()) : pick(std::true_type()), grid, dim3(256),
+                          0, s, all);
     }
 };
 

@@ -92,12 +92,7 @@ struct Window {
                          : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
                          : "r"(at + 16 * i));
     }
-    // whether the vectors lie within [begin, end)
-    __device__ __forceinline__ static bool within(const T* p, const T* begin, const T* end) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
-        return at >= reinterpret_cast<uintptr_t>(begin) &&
-               at + 16 * kVectors <= reinterpret_cast<uintptr_t>(end);
-    }
+    // (up to seven elements before p and 16 behind it are read)
     __device__ __forceinline__ void load(const T* p) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(p);
         shift = (int)(at & 15u) / kSize;

@@ -69,7 +69,7 @@ __host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, i
 }
 constexpr int kStreamSmemMax = 227 * 1024 - 512;   // (and the bias)
 
-// kVec: rows of x and of the result are whole vectors.  kSkip: there is a residual.
+// kVec: rows of the result are whole vectors.  kSkip: there is a residual.
 template <typename T, bool kVec, bool kSkip>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
@@ -236,7 +236,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                 const int c = mine & 7, r0 = mine >> 3, col = h * kPanel + c * 8;
                 const T* src = tile + r0 * q.k + col;
                 unsigned char* dst = unit + r0 * 128 + ((c ^ (r0 & 7)) << 4);
-                if ((kVec || q.vec) && q.k - col >= 8) {
+                if (q.vec && q.k - col >= 8) {
                     float v[4][8];   // (all loads, then all stores, as there)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) load8(src + 32 * i * q.k, 8, true, v[i]);
@@ -513,8 +513,10 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
     }
 }
 
-// kVec: rows of dy, z, x and dx are whole vectors, in raw pieces.
-template <typename T, int kAct, int kPanels, bool kVec>
+// kForm: 2, rows of dy, z, x and dx are whole vectors; 1, those of dx are; 0, none need be.  (One
+// kernel of forms 1 and 2 takes 67 us, not 62, of 777600 x 64 -> 64 in 16 bits; form 0 in place of 1
+// 143, not 112, of 590465 x 96 -> 1.)
+template <typename T, int kAct, int kPanels, int kForm>
 __global__ void __launch_bounds__(kBackThreads, 1)
 k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     using L = BackSmem<T, kPanels, kAct != kActNone>;
@@ -716,13 +718,13 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         bool ok = true;
         // the piece in turn (where the tensors do not begin on 16 bytes there are none)
         const auto wait_piece = [&]() {
-            if (kVec || q.raw)
+            if (kForm == 2 || q.raw)
                 ok = warp_all(mbar_wait(raw_full + f % L::pieces, (f / L::pieces) & 1) && !*s_fail);
             return ok;
         };
         const auto done_piece = [&]() {
             __syncwarp();
-            if ((kVec || q.raw) && lane == 0) mbar_arrive(raw_empty + f % L::pieces);
+            if ((kForm == 2 || q.raw) && lane == 0) mbar_arrive(raw_empty + f % L::pieces);
             ++f;
         };
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
@@ -741,7 +743,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 const T* raw = reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
                 const T* z = raw + L::piece / 2 / (int)sizeof(T);
                 unsigned char* to = smem + sz * L::operand + i * 128;
-                if (kVec || q.vec_n) {
+                if (kForm == 2 || q.vec_n) {
                     make_operand<T, kAct, kPanels, true, kRowsZ>(to, raw, z, rows - i, q.n, true,
                                                                  true, mine, sum);
                 } else {
@@ -763,7 +765,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     const T* raw =
                         reinterpret_cast<const T*>(smem + L::raw + f % L::pieces * L::piece);
                     unsigned char* to = smem + L::x + sx * L::operand + i * 128;
-                    if (kVec || q.vec_k)
+                    if (kForm == 2 || q.vec_k)
                         make_operand<T, kActNone, kPanels, false, kRowsX>(to, raw, nullptr, rows - i,
                                                                           q.k, true, true, mine,
                                                                           none);
@@ -816,9 +818,9 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         auto store_dx = [&](const float (&v)[32], int64_t t, int c0) {
             const int64_t r0 = t * kBlock + quarter * 32;
             if constexpr (kSplit) {
-                finish_small<T, kActNone, true, kVec>(q.out, x, v, r0, c0, 0, lane);
+                finish_small<T, kActNone, true, kForm >= 1>(q.out, x, v, r0, c0, 0, lane);
             } else {
-                Share<T, kVec, false> share;
+                Share<T, kForm >= 1, false> share;
                 const float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 share.begin(q.out, r0, c0, 0, lane);
                 share.template end<kActNone>(q.out, x, v, bias, r0, c0, 0, lane);
@@ -947,12 +949,11 @@ constexpr size_t back_smem(bool act) {
 template <typename T, int kPanels>
 cudaError_t prepare_back() {
     cudaError_t e = cudaSuccess;
-    for (auto* f : {k_linear_narrow<T, kActNone, kPanels, true>,
-                    k_linear_narrow<T, kActSilu, kPanels, true>,
-                    k_linear_narrow<T, kActRelu, kPanels, true>,
-                    k_linear_narrow<T, kActNone, kPanels, false>,
-                    k_linear_narrow<T, kActSilu, kPanels, false>,
-                    k_linear_narrow<T, kActRelu, kPanels, false>})
+    for (auto* f : {k_linear_narrow<T, kActNone, kPanels, 2>, k_linear_narrow<T, kActSilu, kPanels, 2>,
+                    k_linear_narrow<T, kActRelu, kPanels, 2>, k_linear_narrow<T, kActNone, kPanels, 1>,
+                    k_linear_narrow<T, kActSilu, kPanels, 1>, k_linear_narrow<T, kActRelu, kPanels, 1>,
+                    k_linear_narrow<T, kActNone, kPanels, 0>, k_linear_narrow<T, kActSilu, kPanels, 0>,
+                    k_linear_narrow<T, kActRelu, kPanels, 0>})
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)(back_smem<T, kPanels>(true) > back_smem<T, kPanels>(false)
@@ -973,9 +974,9 @@ bool launch_stream(const LinearCall& c, const Result& q, LearnState* st, int n_s
     narrow.skip = q.residual && aligned16(q.residual) && narrow.blocks == 1;
     const int64_t per = n_sms / narrow.blocks;
     const int64_t grid = narrow.blocks * (narrow.tiles < per ? narrow.tiles : per);
-    auto* kernel = !(narrow.vec && q.vec) ? k_linear_stream<T, false, true>
-                   : q.residual           ? k_linear_stream<T, true, true>
-                                          : k_linear_stream<T, true, false>;
+    auto* kernel = !q.vec       ? k_linear_stream<T, false, true>
+                   : q.residual ? k_linear_stream<T, true, true>
+                                : k_linear_stream<T, true, false>;
     *e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kStreamThreads),
                       (size_t)smem, s, narrow, st);
     return true;
@@ -1031,14 +1032,15 @@ cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnS
     const unsigned ctas = (unsigned)(q.tiles < n_sms ? q.tiles : n_sms);
     const auto run = [&](auto panels) {
         constexpr int kPanels = decltype(panels)::value;
-        const auto pick = [&](auto vec) {
-            constexpr bool kVec = decltype(vec)::value;
-            return c.act == kActSilu   ? k_linear_narrow<T, kActSilu, kPanels, kVec>
-                   : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels, kVec>
-                                       : k_linear_narrow<T, kActNone, kPanels, kVec>;
+        const auto pick = [&](auto form) {
+            constexpr int kForm = decltype(form)::value;
+            return c.act == kActSilu   ? k_linear_narrow<T, kActSilu, kPanels, kForm>
+                   : c.act == kActRelu ? k_linear_narrow<T, kActRelu, kPanels, kForm>
+                                       : k_linear_narrow<T, kActNone, kPanels, kForm>;
         };
-        return launch_pdl(q.vec_n && q.vec_k && q.out.vec ? pick(std::true_type())
-                                                          : pick(std::false_type()),
+        return launch_pdl(!q.out.vec             ? pick(std::integral_constant<int, 0>())
+                          : q.vec_n && q.vec_k ? pick(std::integral_constant<int, 2>())
+                                               : pick(std::integral_constant<int, 1>()),
                           dim3(ctas), dim3(kBackThreads), back_smem<T, kPanels>(act), s, q, st);
     };
     return k <= kPanel && n <= kPanel ? run(std::integral_constant<int, 1>())
