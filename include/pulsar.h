@@ -443,7 +443,8 @@ int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int6
  * and rows * outputs at most 2^38.
  * Products are exact and sums have 32 bits: in bfloat16 a result is rounded
  * once, in float32 it is about as near as that of 32-bit products (operands
- * beyond bfloat16's largest value, 3.39e38, count as infinite).  A row of x,
+ * beyond bfloat16's largest value, 3.39e38, count as infinite, and those below
+ * 2^-110 are off by up to 2^-134).  A row of x,
  * or of the weight, with an infinity or a NaN gives infinities or NaNs in its
  * row, or column, of z, and nowhere else. */
 int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, int64_t rows,
