@@ -161,12 +161,12 @@ struct Joins {
     float* sum_out;
 };
 
-// A thread has four elements, of few parts all of them, of many (kLanes = 64) every 64th, which the
-// block then adds up.  (Of 16 parts a thread's loads may follow one another; 304 parts of 64 x 64
-// would take some 20 us so, and take 4 by 64 threads.)
+// A thread has four elements, of up to 16 parts all of them, of more every kLanes-th (8, or of more
+// than 128 parts 64), which the block then adds up.  (Of 16 parts a thread's loads may follow one
+// another; 304 parts of 64 x 64 would take some 20 us so, and take 4 by 64 threads.)
 template <typename T, int kLanes>
 __device__ __forceinline__ void join_parts(const Result& q, const float* __restrict__ part,
-                                           float4 (*s_sum)[4]) {
+                                           float4* s_sum) {
     constexpr int kPer = 256 / kLanes;   // fours of elements of a block
     const int64_t size = q.m * q.n, total = (size + 3) / 4;
     const int mine = threadIdx.x % kPer, from = threadIdx.x / kPer;
@@ -188,13 +188,13 @@ __device__ __forceinline__ void join_parts(const Result& q, const float* __restr
                 for (int e = 0; e < 4; ++e) z[e] += __shfl_xor_sync(0xffffffffu, z[e], d);
             __syncthreads();
             if ((threadIdx.x & 31) < kPer)
-                s_sum[threadIdx.x >> 5][mine & 3] = make_float4(z[0], z[1], z[2], z[3]);
+                s_sum[(threadIdx.x >> 5) * kPer + mine] = make_float4(z[0], z[1], z[2], z[3]);
             __syncthreads();
             if (from > 0) continue;
             for (int e = 0; e < 4; ++e) z[e] = 0.0f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) {
-                const float4 u = s_sum[w][mine & 3];
+                const float4 u = s_sum[w * kPer + mine];
                 z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
             }
         }
@@ -223,19 +223,21 @@ __device__ __forceinline__ void join_sums(const Joins& q, float (*s)[33]) {
     }
 }
 
-constexpr int kFewParts = 16;
+__host__ __device__ inline int lanes_of(int splits) { return splits <= 16 ? 1 : splits <= 128 ? 8 : 64; }
 
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_linear_joins(const __grid_constant__ Joins q) {
-    __shared__ float4 s_sum[8][4];
+    __shared__ float4 s_sum[8 * 32];
     __shared__ float s_cols[8][33];
     pdl_begin();
     if (blockIdx.y == 2) {
         if (q.sums) join_sums(q, s_cols);
     } else if (q.parts[blockIdx.y]) {
         const Result& r = q.of[blockIdx.y];
-        if (r.splits > kFewParts) join_parts<T, 64>(r, q.parts[blockIdx.y], s_sum);
+        const int lanes = lanes_of(r.splits);
+        if (lanes == 64) join_parts<T, 64>(r, q.parts[blockIdx.y], s_sum);
+        else if (lanes == 8) join_parts<T, 8>(r, q.parts[blockIdx.y], s_sum);
         else join_parts<T, 1>(r, q.parts[blockIdx.y], s_sum);
     }
 }
@@ -402,7 +404,7 @@ cudaError_t launch_joins(const Joins& q, int n_sms, cudaStream_t s) {
     for (int i = 0; i < 2; ++i) {
         if (!q.parts[i]) continue;
         const Result& r = q.of[i];
-        const int64_t b = ceil_div(ceil_div(r.m * r.n, 4), r.splits > kFewParts ? 4 : 256);
+        const int64_t b = ceil_div(ceil_div(r.m * r.n, 4), 256 / lanes_of(r.splits));
         if (b > blocks) blocks = b;
     }
     if (q.sums && ceil_div(q.cols, 8) > blocks) blocks = ceil_div(q.cols, 8);

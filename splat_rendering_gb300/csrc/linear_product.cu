@@ -470,11 +470,24 @@ int splits_of(int64_t tiles, int64_t panels, int n_sms) {
     const int64_t s = fit < most ? fit : most;
     return s > 1 ? (int)s : 1;
 }
-// Columns of a tile: an MMA of N = 256 takes 137 cycles, one of 128 114.  (In 32 bits the
-// accumulators of both kinds, twice, leave room for 128.)
-int tile_n(int planes, int64_t n) { return planes == 3 || n <= 128 ? 128 : 256; }
 // Pairs of CTAs where tiles of 256 rows are not half empty.
 bool paired(int64_t m) { return m > kBlock; }
+// Columns of a tile.  In 32 bits the accumulators of both kinds, twice, leave room for 128.  In 16
+// bits tiles of 128 x 128 that fill the SMs once at most have the shorter way from the first operand
+// to the last result (some 6 us: 960 x 512 -> 512 8 us for 11, 2000 x 1000 -> 1000 11 for 17), while
+// a panel takes a CTA of them 0.24 us and a pair's, of four times the products, 0.36: dW of 20000 x
+// 1000 -> 1000 takes the pairs (with its dx 112 us, else 144), of 20000 x 512 -> 512 it does not.
+int tile_n(int planes, int64_t m, int64_t n, int64_t k) {
+    if (planes == 3 || n <= 128) return 128;
+    constexpr int kSms = 152;   // (a choice that does not depend on the device: it sizes workspace)
+    const int64_t small = ceil_div(m, 128) * ceil_div(n, 128), panels = ceil_div(k, kPanel);
+    if (small > kSms) return 256;
+    const int ctas = paired(m) ? 2 : 1;
+    const int64_t large = ceil_div(m, kBlock * ctas) * ceil_div(n, 256);
+    const int64_t by_small = ceil_div(panels, splits_of(small, panels, kSms));
+    const int64_t by_large = ceil_div(panels, splits_of(large, panels, kSms / ctas));
+    return 2 * by_small <= 3 * by_large + 40 ? 128 : 256;
+}
 
 template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas>
 cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_t k, float* parts,
@@ -512,7 +525,7 @@ cudaError_t product(const Result& q, const Matrix& a, const Matrix& b, int64_t k
     if constexpr (sizeof(T) == 4)
         return paired(q.m) ? product_as<T, 3, 128, kAMn, kBMn, 2>(q, a, b, k, parts, pending, st, n_sms, s)
                            : product_as<T, 3, 128, kAMn, kBMn, 1>(q, a, b, k, parts, pending, st, n_sms, s);
-    else if (tile_n(1, q.n) == 128)
+    else if (tile_n(1, q.m, q.n, k) == 128)
         return product_as<T, 1, 128, kAMn, kBMn, 1>(q, a, b, k, parts, pending, st, n_sms, s);
     else if (paired(q.m))
         return product_as<T, 1, 256, kAMn, kBMn, 2>(q, a, b, k, parts, pending, st, n_sms, s);
@@ -547,7 +560,7 @@ cudaError_t prepare_three() {
 }  // namespace
 
 size_t product_parts(int planes, int64_t m, int64_t n, int64_t k) {
-    const int kn = tile_n(planes, n), ctas = (planes == 3 || kn == 256) && paired(m) ? 2 : 1;
+    const int kn = tile_n(planes, m, n, k), ctas = (planes == 3 || kn == 256) && paired(m) ? 2 : 1;
     const int64_t tiles = ceil_div(m, kBlock * ctas) * ceil_div(n, kn);
     if (tiles == 0 || tiles > kMostSms / ctas) return 0;
     const int s = splits_of(tiles, ceil_div(k, kPanel), kMostSms / ctas);
