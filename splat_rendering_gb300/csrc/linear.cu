@@ -3,8 +3,8 @@
 //   z = x W^T + b,   y = act(z) + residual            x [m, k], W [n, k]
 //   dz = dy act'(z),   dx = dz W,   dW = dz^T x,   db = sum of dz's rows
 //
-// The three products run on the tensor cores (tcgen05, fp32 accumulation).  A
-// product is D(i, j) = sum over c of A(i, c) B(j, c); an operand's matrix in
+// The three products run on the tensor cores (tcgen05, fp32 accumulation), but
+// for few rows (below) or outputs (linear_few.cu).  A product is D(i, j) = sum over c of A(i, c) B(j, c); an operand's matrix in
 // memory has either its i (j) or its c as rows: x, W and dz are read as they
 // lie by all three products (K-major or MN-major operands).
 //
@@ -335,8 +335,11 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
     s.x = c.take<__nv_bfloat16>(planes * plane_size(m, k));
     s.w = c.take<__nv_bfloat16>(planes * plane_size(n, k));
     s.dz = c.take<__nv_bfloat16>(planes * plane_size(m, n));
-    const int64_t blocks = operand_grid(m, n).blocks;
-    s.sums = c.take<float>((size_t)(blocks > kMostSms ? blocks : kMostSms) * n);
+    const int64_t few = is_few(k, n) ? few_parts(m, kMostSms) : 0;
+    int64_t blocks = operand_grid(m, n).blocks;
+    if (blocks < kMostSms) blocks = kMostSms;
+    if (blocks < few) blocks = few;
+    s.sums = c.take<float>((size_t)blocks * n);
     const size_t y = product_parts(planes, m, n, k), dx = product_parts(planes, m, k, n);
     size_t dw = product_parts(planes, n, k, m);
     const bool f32 = dtype == kF32;
@@ -346,6 +349,7 @@ Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
                               part_size(n, k);
         if (narrow > dw) dw = narrow;
     }
+    if ((size_t)few * part_size(n, k) > dw) dw = (size_t)few * part_size(n, k);
     s.parts = c.take<float>(y > dx ? y : dx);
     s.parts_w = c.take<float>(dw);
     s.bytes = c.used;
@@ -450,6 +454,7 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
     }
     q.vec = vec4<T>(q);
     cudaError_t e = cudaSuccess;
+    if (launch_few<T>(c, q, n_sms, s, &e)) return e;
     if (launch_stream<T>(c, q, st, n_sms, s, &e)) return e;
     const Space sp = carve(ws, m, k, n, c.dtype);
     Maker<T> make;
@@ -487,6 +492,20 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
     dw.out = c.grad_weight;
     dx.vec = vec4<T>(dx);
     dw.vec = vec4<T>(dw);
+    if (is_few(k, n)) {
+        int64_t blocks = 0;
+        const cudaError_t e = launch_few_back<T>(c, c.grad_weight ? sp.parts_w : nullptr,
+                                                 c.grad_bias ? sp.sums : nullptr, n_sms, s, &blocks);
+        if (e != cudaSuccess) return e;
+        joins.sum_blocks = blocks;
+        if (c.grad_weight) {
+            joins.of[1] = dw;
+            joins.of[1].splits = (int)blocks;
+            joins.of[1].part = part_size(n, k);
+            joins.parts[1] = sp.parts_w;
+        }
+        return launch_joins<T>(joins, n_sms, s);
+    }
     if (is_narrow<T>(k, n)) {
         const cudaError_t e = launch_narrow<T>(c, sp.parts_w, c.grad_bias ? sp.sums : nullptr, st,
                                                n_sms, s);

@@ -536,5 +536,16 @@ template <typename T>
 cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnState* st, int n_sms,
                           cudaStream_t s);
 
+// Layers of a few outputs (linear_few.cu).  The forward call: false where another form is faster.
+constexpr int64_t kFewOutputs = 4, kFewInputs = 2048;
+bool is_few(int64_t inputs, int64_t outputs);   // of the backward call
+int64_t few_parts(int64_t rows, int n_sms);   // at most; sums of dW as above, and of the bias
+template <typename T>
+bool launch_few(const LinearCall& c, const Result& q, int n_sms, cudaStream_t s,
+                cudaError_t* result);
+template <typename T>
+cudaError_t launch_few_back(const LinearCall& c, float* parts, float* sums, int n_sms, cudaStream_t s,
+                            int64_t* blocks);   // how many there are
+
 }  // namespace linear
 }  // namespace pulsar
