@@ -44,12 +44,11 @@ struct Some<__nv_bfloat16, 4> {
 
 constexpr int kBatch = 4;    // rows of a thread in flight
 constexpr int kChunk = 1024;   // rows whose dz a block has at a time
-constexpr int kBlocks = 4;   // of an SM, of the backward call
+constexpr int kBlocks = 4;     // of an SM, of the backward call, at most
 
 // The outputs: 1 << log_g lanes to a row, each with every so many'th V of its inputs, the weights
-// in shared memory in 32 bits.  590465 x 96 -> 1 in 16 bits: 24 us for 115 MB (the narrow layers'
-// kernel 39), 874606 x 4 -> 1 4.8 (45).  It is bound by the instructions that open and sum 16 bits
-// (in 32 bits 590465 x 64 -> 4 takes 28 us for 161 MB, 85 % of the copy rate).
+// in shared memory in 32 bits.  590465 x 96 -> 1 in 16 bits: 20 us for 115 MB, 84 % of the copy rate
+// (the narrow layers' kernel 39), 874606 x 4 -> 1 4.8 (45); it waits for its loads.
 template <typename T, int V, int kN>
 __global__ void __launch_bounds__(256)
 k_linear_few(const T* __restrict__ x, const T* __restrict__ weight, int k, int log_g,
@@ -74,6 +73,7 @@ k_linear_few(const T* __restrict__ x, const T* __restrict__ weight, int k, int l
         for (int i = 0; i < kBatch; ++i)
 #pragma unroll
             for (int j = 0; j < kN; ++j) sum[i][j] = 0.0f;
+#pragma unroll 2
         for (int c = g * V; c < k; c += V << log_g) {
             typename Some<T, V>::Raw u[kBatch] = {};
 #pragma unroll
@@ -272,18 +272,20 @@ cudaError_t with_sizes(int width, int64_t n, F f) {
     return outputs(std::integral_constant<int, 1>());
 }
 
-// Blocks of rows: kBlocks for an SM over all columns, of kBatch rows for each thread or more.
+// Blocks of rows: as many for an SM, over all columns, as it holds at once by their registers (`held`
+// floats of a thread: 590465 x 64 -> 4 in 32 bits 70 us by two, 75 by four; 952959 x 52 -> 3 in 16
+// bits 80 and 60), of kBatch rows for each thread or more.
 struct FewGrid {
     int log_tx;
     int64_t block_rows, blocks, col_blocks;
 };
-FewGrid few_grid(int64_t rows, int64_t k, int width, int n_sms) {
+FewGrid few_grid(int64_t rows, int64_t k, int width, int held, int n_sms) {
     FewGrid g;
     const int64_t groups = ceil_div(k, width);
     g.log_tx = log2_up(groups, 5);
     g.col_blocks = ceil_div(groups, 1 << g.log_tx);
     const int64_t least = kBatch * (256 >> g.log_tx);
-    int64_t want = kBlocks * n_sms / g.col_blocks;
+    int64_t want = (held < 32 ? kBlocks : 2) * n_sms / g.col_blocks;
     if (want < 1) want = 1;
     g.block_rows = ceil_div(ceil_div(rows, want), least) * least;
     g.blocks = ceil_div(rows, g.block_rows);
@@ -302,7 +304,7 @@ int64_t few_parts(int64_t rows, int n_sms) {
 
 // The other forms keep what they are faster at: up to 128 inputs the narrow one, but for 32 inputs or
 // fewer and loads of 8 bytes or more (1176470 x 51 -> 4 in 16 bits 67 us, here 111; 967741 x 31 54,
-// here 42; 590465 x 96 42, here 31); above 128 the products of 16 bits, where they need no copy of x
+// here 42; 590465 x 96 42, here 30); above 128 the products of 16 bits, where they need no copy of x
 // (58593 x 1024 -> 4 32 us, here 55; to one output 32, here 25; 119521 x 502 -> 4 96, here 58).
 template <typename T>
 bool launch_few(const LinearCall& c, const Result& q, int n_sms, cudaStream_t s, cudaError_t* result) {
@@ -316,8 +318,9 @@ bool launch_few(const LinearCall& c, const Result& q, int n_sms, cudaStream_t s,
         constexpr int V = decltype(v)::value, kN = decltype(n)::value;
         const int log_g = log2_up(ceil_div(c.inputs / V, 4), 5);   // (up to four loads to a lane)
         const int64_t blocks = ceil_div(c.rows, 8 * kBatch * (32 >> log_g));
+        const int64_t most = n_sms * (sizeof(T) == 2 ? 6 : 4);   // (in 32 bits 4 are up to a tenth faster)
         return launch_pdl(k_linear_few<T, V, kN>,
-                          dim3((unsigned)(blocks < n_sms * 4 ? blocks : n_sms * 4)), dim3(256),
+                          dim3((unsigned)(blocks < most ? blocks : most)), dim3(256),
                           (size_t)(kN * c.inputs * 4), s, static_cast<const T*>(c.x),
                           static_cast<const T*>(c.weight), (int)c.inputs, log_g, q);
     });
@@ -331,7 +334,8 @@ template <typename T>
 cudaError_t launch_few_back(const LinearCall& c, float* parts, float* sums, int n_sms, cudaStream_t s,
                             int64_t* blocks) {
     const int width = width_of<T>(c.inputs, c.grad_weight ? c.x : nullptr, c.grad_x);
-    const FewGrid g = few_grid(c.rows, c.inputs, width, n_sms);
+    const int held = (int)c.outputs * width * (sizeof(T) == 4 ? 3 : 2);
+    const FewGrid g = few_grid(c.rows, c.inputs, width, held, n_sms);
     *blocks = g.blocks;
     const Few q{c.grad_y, c.pre, c.x, c.weight, c.grad_x, parts, sums, c.rows, g.block_rows,
                 part_size(c.outputs, c.inputs), (int)c.inputs, c.act, g.log_tx};

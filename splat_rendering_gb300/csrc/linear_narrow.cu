@@ -515,7 +515,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
 
 // kForm: 2, rows of dy, z, x and dx are whole vectors; 1, those of dx are; 0, none need be.  (One
 // kernel of forms 1 and 2 takes 67 us, not 62, of 777600 x 64 -> 64 in 16 bits; form 0 in place of 1
-// 143, not 112, of 590465 x 96 -> 1.)
+// 124, not 113, of 590465 x 96 -> 7 with SiLU.)
 template <typename T, int kAct, int kPanels, int kForm>
 __global__ void __launch_bounds__(kBackThreads, 1)
 k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
