@@ -81,3 +81,31 @@ def test_tensors_that_begin_anywhere(ops, case, off, dtype):
     for g, v, e, what in zip(got, want, bounds, ("dx", "dw", "db")):
         _inside(g, v, e, what)
     assert room[:off].isnan().all() and room[off + gx.numel():].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [(3000, 40, 3), (900, 512, 512), (2000, 100, 5)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_captured_and_replayed(ops, case, dtype):
+    """A captured step reads its tensors when it is replayed, and leaves what a call leaves."""
+    x, w, b, _, dy = _cuda(*_inputs(*case, TYPES[dtype], 900))
+    step = lambda: (ops.linear(x, w, b, act="relu", want_pre=True),  # noqa: E731
+                    ops.linear_backward(dy, x, w))
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        (y, z), grads = step()
+    x.mul_(-0.5)
+    dy.mul_(2)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    (y2, z2), grads2 = step()
+    assert torch.equal(y, y2) and torch.equal(z, z2)
+    assert all(torch.equal(p, q) for p, q in zip(grads, grads2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        (y3, _), grads3 = step()
+    side.synchronize()
+    assert torch.equal(y, y3) and all(torch.equal(p, q) for p, q in zip(grads, grads3))
