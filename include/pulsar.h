@@ -446,7 +446,7 @@ int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int6
  * beyond bfloat16's largest value, 3.39e38, count as infinite, and those below
  * 2^-110 are off by up to 2^-134).  A row of x,
  * or of the weight, with an infinity or a NaN gives infinities or NaNs in its
- * row, or column, of z, and nowhere else. */
+ * row, or column, of z, and nowhere else; ReLU keeps a NaN. */
 int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, int64_t rows,
                           int64_t inputs, int64_t outputs, const float* bias,
                           const void* residual, int act, int dtype, void* y, void* pre,
@@ -456,6 +456,7 @@ int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, i
  * is), with x, weight and pre of the forward call:
  *   dz = grad_y act'(pre),   grad_x = dz W,   grad_weight = dz^T x,
  *   grad_bias = the sum of dz's rows.
+ * (ReLU passes grad_y where pre is a NaN, as where it is positive.)
  *   pre    may be NULL where act is PULSAR_ACT_NONE
  *   grad_x [rows,inputs] dtype; grad_weight [outputs,inputs] dtype; grad_bias
  *          [outputs] float32; each overwritten, each may be NULL (not

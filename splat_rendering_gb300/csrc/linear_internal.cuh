@@ -28,17 +28,16 @@ __device__ __forceinline__ float sigmoid_of(float z) {
 template <int kAct>
 __device__ __forceinline__ float act_of(float z) {
     if (kAct == kActSilu) return z * sigmoid_of(z);
-    if (kAct == kActRelu) return z > 0.0f ? z : 0.0f;
+    if (kAct == kActRelu) {   // NaN stays NaN
+        float y;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(0.0f));
+        return y;
+    }
     return z;
 }
-template <int kAct>
-__device__ __forceinline__ float act_slope(float z) {
-    if (kAct == kActSilu) {
-        const float s = sigmoid_of(z);
-        return s * (1.0f + z * (1.0f - s));
-    }
-    if (kAct == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
-    return 1.0f;
+__device__ __forceinline__ float silu_slope(float z) {
+    const float s = sigmoid_of(z);
+    return s * (1.0f + z * (1.0f - s));
 }
 // ---------------------------------------------------------------- planes --
 // Two floats as three words of two bfloat16 each, whose sums they are (an infinity, or what rounds
@@ -152,13 +151,14 @@ struct Chunk {
     }
 };
 
-// dy made dz = dy act'(z)
+// dy made dz = dy act'(z).  (Through ReLU dy passes where z is a NaN: a float32 sum with an
+// infinity, whose parts cancel to one, may be that infinity.)
 template <int kAct, int V>
 __device__ __forceinline__ void to_dz(float (&v)[V], const float (&z)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        if (kAct == kActRelu) v[e] = z[e] > 0.0f ? v[e] : 0.0f;
-        if (kAct == kActSilu) v[e] *= act_slope<kActSilu>(z[e]);
+        if (kAct == kActRelu) v[e] = z[e] <= 0.0f ? 0.0f : v[e];
+        if (kAct == kActSilu) v[e] *= silu_slope(z[e]);
     }
 }
 
