@@ -30,8 +30,10 @@ namespace {
 // summed in registers every kChunk panels (128 of K).  4001 x 1500 -> 509: 24
 // panels of 24 MMAs of 256 x 128 at 78 cycles, some 30 us, after 8 us for the
 // planes (dx 42 us of 45 by single CTAs; drained every 256 of K: 39, and twice as far
-// off).  In 16 bits nothing is drained: what is truncated of K = 2^16 is still
-// below half a step of the result.
+// off).  In 16 bits an instruction's truncation, of 16 of K, is at most 2^-23 of the
+// sum: the outputs' and dx's K of 2^16 or less lose an eighth of half a step of the
+// result and are not drained, dW's, whose K is the rows, is every kDrain panels (2^14
+// rows: 2^-13, a thirtieth of half a step).
 //
 // Where a product has few tiles for the SMs and a long contraction (dW: one
 // tile and a million rows), its parts are separate work items, whose sums
@@ -47,6 +49,9 @@ struct Product {
 // eight 85; dx, which has none: 82 us with eight, with sixteen 85)
 constexpr int epilogue_warps(int planes, bool outputs) { return planes == 1 && outputs ? 16 : 8; }
 constexpr int kChunk = 2;              // panels per drained sum (32 bits)
+// the same in 16 bits, where a part has more than one of them (262144 x 1024 -> 4096: dW 1178 us,
+// undrained 1183; one of them has a kernel that keeps no sums: 16381 rows 77 us, else 79)
+constexpr int kDrain = 256;
 constexpr int kGroup = 4;              // row blocks whose tiles lie side by side in time (of 16: 1 us more)
 
 template <int kPlanes, int kN, int kCtas, bool kOutputs>
@@ -143,14 +148,17 @@ __device__ __forceinline__ bool epilogue_any(bool v) {
 
 // T: the result's type (float for parts).  kAMn, kBMn: the operand's matrix has the contraction
 // as its rows.  kCtas: 1, or a pair of CTAs on a tile of 256 rows, each with its 128 rows of A and
-// of the sums, and half of B's; the first one issues the MMAs of both.
-template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas, bool kVec>
+// of the sums, and half of B's; the first one issues the MMAs of both.  kLong: a part's contraction
+// is more than kDrain panels, in 16 bits.
+template <typename T, int kPlanes, int kN, bool kAMn, bool kBMn, int kCtas, bool kVec, bool kLong>
 __global__ void __launch_bounds__(64 + 32 * epilogue_warps(kPlanes, !kAMn && !kBMn)) __cluster_dims__(kCtas, 1, 1)
 k_linear_product(const __grid_constant__ Product q, LearnState* st) {
     using L = ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>;
     constexpr bool kPair = kCtas == 2;
     constexpr int kAcc = kPlanes == 3 ? 2 * kN : kN;   // columns of an accumulator
     constexpr int kHalf = kN / (L::epilogue / 4);      // columns of an epilogue thread
+    constexpr bool kDrained = kPlanes == 3 || kLong;
+    constexpr int kPiece = kPlanes == 3 ? kChunk : kDrain;   // panels of a drained sum
     static_assert(2 * kAcc <= 512, "tensor memory");
     extern __shared__ unsigned char raw[];
     unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -272,7 +280,7 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
             for (int t = first; t < total && ok; t += step) {
                 int i, j, k0, k1, part;
                 place(t, &i, &j, &k0, &k1, &part);
-                const int chunk = kPlanes == 3 ? kChunk : k1 - k0;
+                const int chunk = kDrained ? kPiece : k1 - k0;
                 for (int kc = k0; kc < k1 && ok; kc += chunk, ++it) {
                     const int buf = it & 1, ke = min(kc + chunk, k1);
                     const uint32_t d = tmem + buf * kAcc;
@@ -361,11 +369,11 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                 }
             };
             bool ok = true;
-            if constexpr (kPlanes == 3) {
+            if constexpr (kDrained) {
                 float v[kHalf];
 #pragma unroll
                 for (int e = 0; e < kHalf; ++e) v[e] = 0.0f;
-                for (int kc = k0; kc < k1; kc += kChunk, ++it) {
+                for (int kc = k0; kc < k1; kc += kPiece, ++it) {
                     const int buf = it & 1;
                     ok = mbar_wait(acc_full + buf, (it >> 1) & 1) && !*s_fail;
                     ok = !epilogue_any<32 * L::epilogue>(!ok);
@@ -377,11 +385,12 @@ k_linear_product(const __grid_constant__ Product q, LearnState* st) {
                     for (int h = 0; h < kHalf; h += 16) {
                         uint32_t u[16], w[16];
                         tmem_ld16(acc + h, u);
-                        tmem_ld16(acc + kN + h, w);
+                        if (kPlanes == 3) tmem_ld16(acc + kN + h, w);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            v[h + e] += __uint_as_float(u[e]) + __uint_as_float(w[e]);
+                            v[h + e] += kPlanes == 3 ? __uint_as_float(u[e]) + __uint_as_float(w[e])
+                                                     : __uint_as_float(u[e]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -505,18 +514,25 @@ cudaError_t product_as(const Result& r, const Matrix& a, const Matrix& b, int64_
     *pending = q.out;
     if (!encode(&q.a, a, kAMn ? kPanel : kBlock) || !encode(&q.b, b, kBMn ? kPanel : L::rows_b))
         return cudaErrorInvalidValue;
-    const auto launch = [&](auto kernel) {
+    if (q.out.splits > 1)
+        q.out = Result{r.m, r.n, nullptr, nullptr, nullptr, parts, kActNone, r.n % 4 == 0,
+                       q.out.splits, q.out.part};
+    const auto launch = [&](auto type, auto is_long) {
+        using R = decltype(type);
+        constexpr bool kLong = decltype(is_long)::value;
         const int64_t total = tiles * q.out.splits;
-        return launch_pdl(kernel, dim3((unsigned)((total < groups ? total : groups) * kCtas)),
+        return launch_pdl(q.out.vec ? k_linear_product<R, kPlanes, kN, kAMn, kBMn, kCtas, true, kLong>
+                                    : k_linear_product<R, kPlanes, kN, kAMn, kBMn, kCtas, false, kLong>,
+                          dim3((unsigned)((total < groups ? total : groups) * kCtas)),
                           dim3(L::threads), L::bytes, s, q, st);
     };
-    if (q.out.splits == 1)
-        return launch(r.vec ? k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>
-                            : k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>);
-    q.out = Result{r.m, r.n, nullptr, nullptr, nullptr, parts, kActNone, r.n % 4 == 0,
-                   q.out.splits, q.out.part};
-    return launch(q.out.vec ? k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>
-                            : k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>);
+    const auto typed = [&](auto is_long) {
+        return q.out.splits > 1 ? launch(float(), is_long) : launch(T(), is_long);
+    };
+    if constexpr (kPlanes == 1 && kAMn) {
+        if (ceil_div(q.panels, q.out.splits) > kDrain) return typed(std::true_type());
+    }
+    return typed(std::false_type());
 }
 
 template <typename T, bool kAMn, bool kBMn>
@@ -541,11 +557,19 @@ cudaError_t prepare_one() {
             e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      ProductSmem<kPlanes, kN, kCtas, !kAMn && !kBMn>::bytes);
     };
-    prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, true>);
-    prepare(k_linear_product<T, kPlanes, kN, kAMn, kBMn, kCtas, false>);
+    const auto both = [&](auto type, auto is_long) {
+        using R = decltype(type);
+        constexpr bool kLong = decltype(is_long)::value;
+        prepare(k_linear_product<R, kPlanes, kN, kAMn, kBMn, kCtas, true, kLong>);
+        prepare(k_linear_product<R, kPlanes, kN, kAMn, kBMn, kCtas, false, kLong>);
+    };
+    both(T(), std::false_type());
     if constexpr (sizeof(T) == 2) {
-        prepare(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, true>);
-        prepare(k_linear_product<float, kPlanes, kN, kAMn, kBMn, kCtas, false>);
+        both(float(), std::false_type());
+        if constexpr (kAMn) {
+            both(T(), std::true_type());
+            both(float(), std::true_type());
+        }
     }
     return e;
 }

@@ -1,0 +1,63 @@
+"""Gradients of a weight over many rows in 16 bits: sums that the tensor cores truncate are drained
+every 2^14 rows, so that what they lose does not grow with the rows."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import linear_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+DRAIN = 1 << 14   # rows
+
+
+def _one(n, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn((1, n), device="cuda", generator=g, dtype=BF16)
+
+
+def _alike(rows, inputs, outputs, want=("weight", "bias")):
+    """dW of rows that are all alike, so that all of a sum's terms have one sign, by the number of
+    rows: each of a piece's DRAIN / 16 instructions truncates at most 2 U32 of its sum, the pieces and
+    the parts are added in float32, and the result is rounded."""
+    from splat_rendering_gb300 import pulsar as pl
+    ops = pl.Learner(workspace_bytes=pl.linear_workspace(rows, inputs, outputs, BF16))
+    one, dy1 = _one(inputs, 3), _one(outputs, 4)
+    x, dy = one.expand(rows, inputs).contiguous(), dy1.expand(rows, outputs).contiguous()
+    w = _one(inputs, 5).expand(outputs, inputs).contiguous()
+    _, dw, _ = ops.linear_backward(dy, x, w, want=want)
+    exact = rows * dy1.double().T @ one.double()
+    e = (2 * DRAIN / 16 + rows / DRAIN + 304 + 4) * ref.U32 + ref.UB
+    bad = (dw.double() - exact).abs() > e * exact.abs()
+    assert not bad.any(), (int(bad.sum()), float(((dw.double() - exact) / exact).abs().max()), e)
+    ops.status()
+    ops.close()
+
+
+@pytest.mark.parametrize("rows,inputs,outputs", [(1 << 21, 2560, 1024), ((1 << 21) + 77, 256, 9728),
+                                                 (4_000_001, 520, 264)],
+                         ids=["one-part", "one-part-oblong", "parts"])
+def test_wide(rows, inputs, outputs):
+    _alike(rows, inputs, outputs)
+
+
+@pytest.mark.parametrize("rows,inputs,outputs", [(3_000_001, 300, 301), (700_003, 129, 1200), (200_000, 2560, 1024)])
+def test_wide_against_64_bits(rows, inputs, outputs):
+    """Pieces of rows that differ, and a last one that is not whole."""
+    from splat_rendering_gb300 import pulsar as pl
+    ops = pl.Learner(workspace_bytes=pl.linear_workspace(rows, inputs, outputs, BF16))
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, dy, w = (torch.randn(s, device="cuda", generator=g, dtype=BF16)
+                for s in ((rows, inputs), (rows, outputs), (outputs, inputs)))
+    _, dw, _ = ops.linear_backward(dy, x, w, want=("weight",))
+    want = torch.zeros(outputs, inputs, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for at in range(0, rows, 200_000):
+        a, b = dy[at:at + 200_000].double(), x[at:at + 200_000].double()
+        want += a.T @ b
+        size += a.abs().T @ b.abs()
+    bound = (2 * DRAIN / 16 + rows / DRAIN + 304 + 4) * ref.U32 * size
+    assert not ref.outside(dw, want.cpu(), bound.cpu()).any()
+    ops.status()
+    ops.close()
