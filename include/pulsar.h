@@ -466,9 +466,7 @@ int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, i
  * off as their own rounding; without an activation it is grad_y, exactly.  The
  * tensor cores truncate their sums, of 16 terms at a time, by at most 2^-23: of
  * grad_weight's, over rows, they are added up in float32 every 2^14 rows, so
- * that terms of one sign lose at most 2^-13 (of layers of up to 128 inputs and
- * outputs, which are not, 2^-23 for every 16 rows that one of some 152 parts
- * has), a 32nd of a result's own rounding. */
+ * that terms of one sign lose at most 2^-13, a 32nd of a result's own rounding. */
 int pulsar_linear_backward(pulsar_learn_t h, const void* grad_y, const void* x,
                            const void* weight, const void* pre, int64_t rows, int64_t inputs,
                            int64_t outputs, int act, int dtype, void* grad_x, void* grad_weight,

@@ -334,8 +334,14 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
 // forward kernel.  x's operand is made while the MMAs of dx run, which do not
 // need it, and where there is room dz's next one during those of dW.
 //
+// In 16 bits dW's accumulator, whose sums the tensor cores truncate, is added to
+// the CTA's part in memory every kPieceTiles tiles (2^14 rows), while the next
+// ones go to another: what is lost of terms of one sign is 2^-13 of a sum at
+// most, and no wait lasts for more than that many tiles.  (16M x 64 -> 64 takes
+// 1091 us, without it 1043.)
+//
 // 1M x 64 -> 64 in 32 bits: 169 us, with SiLU 205 (118 and 158 by the bytes); 777600
-// x 64 -> 64 in 16 bits 62 us, with ReLU 74, with SiLU 82 (44 and 59).  Bound by the
+// x 64 -> 64 in 16 bits 61 us, with ReLU 72, with SiLU 80 (44 and 59).  Bound by the
 // eight warps that make operands; loads straight to registers, kept ahead of their
 // use, were slower (their fence awaits every load).
 constexpr int kBackThreads = 576;   // warps: MMAs, eight of operands, eight of the epilogue, copies
@@ -343,6 +349,7 @@ constexpr int kBackThreads = 576;   // warps: MMAs, eight of operands, eight of 
 // bits: 55 us, by the wide products 130; 128 -> 128 in 16 bits 66 and 81).
 template <typename T>
 constexpr int kBackSide = sizeof(T) == 4 ? 64 : 128;
+constexpr int kPieceTiles = 128;   // (no layer of a million rows has more for a CTA)
 
 struct Narrow {
     const void *grad_y, *pre, *x, *weight;
@@ -513,6 +520,33 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
     }
 }
 
+// 32 sums of a row, or the `left` that there are, into a part of dW: added to what it has where
+// `more`.  (All loads, then all stores; by fours where rows begin on them: a lane has a row, and
+// one by one the sectors are asked for eight times.)
+__device__ __forceinline__ void add_part(float* part, uint32_t (&w)[32], int left, bool more) {
+    if ((reinterpret_cast<uintptr_t>(part) & 15u) == 0 && left % 4 == 0) {
+        float4* at = reinterpret_cast<float4*>(part);
+        float4 u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            u[e] = more && 4 * e < left ? at[e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (4 * e < left)
+                at[e] = make_float4(u[e].x + __uint_as_float(w[4 * e]),
+                                    u[e].y + __uint_as_float(w[4 * e + 1]),
+                                    u[e].z + __uint_as_float(w[4 * e + 2]),
+                                    u[e].w + __uint_as_float(w[4 * e + 3]));
+    } else {
+        float u[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) u[e] = more && e < left ? part[e] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (e < left) part[e] = u[e] + __uint_as_float(w[e]);
+    }
+}
+
 // kForm: 2, rows of dy, z, x and dx are whole vectors; 1, those of dx are; 0, none need be.  (One
 // kernel of forms 1 and 2 takes 67 us, not 62, of 777600 x 64 -> 64 in 16 bits; form 0 in place of 1
 // 124, not 113, of 590465 x 96 -> 7 with SiLU.)
@@ -535,8 +569,9 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     uint64_t* dx_full = x_empty + 2;
     uint64_t* dx_empty = dx_full + 2;
     uint64_t* dw_full = dx_empty + 2;
-    uint64_t* dw_empty = dw_full + 1;
-    uint64_t* drain = dw_empty + 1;
+    uint64_t* dw_empty = dw_full + 2;
+    uint64_t* drain = dw_empty + 2;
+    static_assert((2 * L::pieces + 17) * 8 + 8 <= 256, "barriers");
     uint32_t* s_taddr = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* s_fail = s_taddr + 1;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -553,9 +588,9 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
             mbar_init(x_empty + s);
             mbar_init(dx_full + s);
             mbar_init_n(dx_empty + s, 8);
+            mbar_init(dw_full + s);
+            mbar_init_n(dw_empty + s, 8);
         }
-        mbar_init(dw_full);
-        mbar_init_n(dw_empty, 8);
         mbar_init(drain);
         *s_fail = 0u;
     }
@@ -679,11 +714,17 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                     mma_commit(dx_full + buf);
                 }
                 if (q.want_w) {
+                    // (in 32 bits one accumulator, drained every tile; in 16 two, every piece)
+                    const int piece = kSplit ? u : u / kPieceTiles, buf = kSplit ? 0 : piece & 1;
+                    const bool begins = kSplit || u % kPieceTiles == 0;
+                    const bool ends = kSplit || u % kPieceTiles == kPieceTiles - 1;
                     ok = mbar_wait(x_full + sx, (u / L::xs) & 1) && !*s_fail;
-                    if (kSplit && ok) ok = mbar_wait(dw_empty, (u & 1) ^ 1) && !*s_fail;
+                    if (begins && ok)
+                        ok = mbar_wait(dw_empty + buf, ((kSplit ? piece : piece >> 1) & 1) ^ 1) &&
+                             !*s_fail;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + kDw;
+                    const uint32_t d = tmem + kDw + buf * 128;
                     const uint64_t a = desc_sw128(dz, L::panel), b = desc_sw128(x, L::panel);
                     const uint64_t lo = desc_sw128(dz + 2 * L::panel, L::panel);
                     for (int e = 0; e < kBlock / 16; ++e) {
@@ -693,10 +734,10 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                             mma_f16(d + 128, lo + off, b + off, kBase | kAMn | (64u >> 3 << 17), 1);
                         } else {
                             mma_f16(d, a + off, b + off, kBase | kAMn | (k16 >> 3 << 17),
-                                    u > 0 || e > 0);
+                                    !begins || e > 0);
                         }
                     }
-                    if (kSplit || t + step >= q.tiles) mma_commit(dw_full);
+                    if (ends || t + step >= q.tiles) mma_commit(dw_full + buf);
                     mma_commit(x_empty + sx);
                 }
                 mma_commit(dz_empty + sz);
@@ -826,6 +867,13 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 share.template end<kActNone>(q.out, x, v, bias, r0, c0, 0, lane);
             }
         };
+        // a lane has a row of its part of dW
+        const int row = kSplit ? (quarter & 1) * 32 + lane : quarter * 32 + lane;
+        const auto part_of = [&]() {
+            return q.parts + ((int64_t)blockIdx.x * (kSplit ? 2 : 1) +
+                              (kSplit ? quarter >> 1 : 0)) * q.part +
+                   (int64_t)row * q.k;
+        };
         bool ok = true;
         int u = 0;
         for (int64_t t = first; t < q.tiles; t += step, ++u) {
@@ -874,32 +922,33 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(dw_empty);
             }
-        }
-        if (ok && q.want_w) {
-            // a lane has a row of its part
-            const int row = kSplit ? (quarter & 1) * 32 + lane : quarter * 32 + lane;
-            float* part = q.parts + ((int64_t)blockIdx.x * (kSplit ? 2 : 1) +
-                                     (kSplit ? quarter >> 1 : 0)) * q.part +
-                          (int64_t)row * q.k;
-            if constexpr (kSplit) {
-                if (row < q.n)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (group * 32 + e < q.k) part[group * 32 + e] = dw[e];
-            } else {
-                ok = warp_all(mbar_wait(dw_full, 0) && !*s_fail);
+            if (!kSplit && q.want_w &&
+                (u % kPieceTiles == kPieceTiles - 1 || t + step >= q.tiles)) {
+                const int piece = u / kPieceTiles, buf = piece & 1;
+                ok = warp_all(mbar_wait(dw_full + buf, (piece >> 1) & 1) && !*s_fail);
+                if (!ok) break;
                 tc_fence_after();
+                float* part = part_of();
 #pragma unroll 1
-                for (int c = group * 32; ok && c < q.k; c += 64) {
+                for (int c = group * 32; c < q.k; c += 64) {
                     uint32_t w[32];
                     __syncwarp();
-                    tmem_ld32(tmem + kDw + lanes + c, w);
+                    tmem_ld32(tmem + kDw + buf * 128 + lanes + c, w);
                     tmem_wait_ld();
-                    if (row < q.n)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c + e < q.k) part[c + e] = __uint_as_float(w[e]);
+                    if (row >= q.n) continue;
+                    add_part(part + c, w, q.k - c, piece > 0);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dw_empty + buf);
+            }
+        }
+        if constexpr (kSplit) {
+            if (ok && q.want_w && row < q.n) {
+                float* part = part_of();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (group * 32 + e < q.k) part[group * 32 + e] = dw[e];
             }
         }
         if (!ok) *s_fail = 1u;

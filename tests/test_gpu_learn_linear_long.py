@@ -61,3 +61,38 @@ def test_wide_against_64_bits(rows, inputs, outputs):
     assert not ref.outside(dw, want.cpu(), bound.cpu()).any()
     ops.status()
     ops.close()
+
+
+@pytest.mark.parametrize("want", [("weight", "bias"), ("x", "weight", "bias")], ids=["first", "inner"])
+@pytest.mark.parametrize("rows,inputs,outputs", [(1 << 25, 64, 64), ((1 << 23) + 99, 128, 100)])
+def test_narrow(rows, inputs, outputs, want):
+    _alike(rows, inputs, outputs, want)
+
+
+@pytest.mark.parametrize("rows", [152 * 128 * 128, 152 * 128 * 128 + 1, 3 * 152 * 128 * 128 - 500])
+@pytest.mark.parametrize("inputs,outputs", [(40, 24), (33, 17), (100, 128), (16, 128)])
+def test_narrow_against_64_bits(rows, inputs, outputs):
+    """Whole pieces, one tile of another, and several."""
+    from splat_rendering_gb300 import pulsar as pl
+    ops = pl.Learner(workspace_bytes=pl.linear_workspace(rows, inputs, outputs, BF16))
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, dy, w = (torch.randn(s, device="cuda", generator=g, dtype=BF16)
+                for s in ((rows, inputs), (rows, outputs), (outputs, inputs)))
+    dx, dw, db = ops.linear_backward(dy, x, w)
+    alone = ops.linear_backward(dy, x, w, want=("weight",))[1]
+    assert torch.equal(dw, alone)
+    want = torch.zeros(outputs, inputs, dtype=torch.float64, device="cuda")
+    size, sums, sizes = torch.zeros_like(want), 0.0, 0.0
+    for at in range(0, rows, 500_000):
+        a, b = dy[at:at + 500_000].double(), x[at:at + 500_000].double()
+        want += a.T @ b
+        size += a.abs().T @ b.abs()
+        sums, sizes = sums + a.sum(0), sizes + a.abs().sum(0)
+    bound = (2 * DRAIN / 16 + rows / DRAIN + 304 + 4) * ref.U32 * size
+    assert not ref.outside(dw, want.cpu(), bound.cpu()).any()
+    assert not ref.outside(db, sums.cpu(), ((rows / 152 / 32 + 400) * ref.U32 * sizes).cpu()).any()
+    for part in (slice(0, 200), slice(rows - 200, rows)):
+        (v, _, _), (e, _, _) = ref.linear_backward(dy[part].cpu(), x[part].cpu(), w.cpu(), None, "none")
+        assert not ref.outside(dx[part], v, e).any()
+    ops.status()
+    ops.close()
