@@ -444,6 +444,10 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
     for (int h = 0; h < kPanels; ++h) {
         const int col = h * kPanel + c;
         if (col >= cols16) break;
+        float more[V];   // these rows' sum: a quarter as many roundings in a row
+        if (kDz)
+#pragma unroll
+            for (int e = 0; e < V; ++e) more[e] = 0.0f;
         unsigned char* dst = operand + h * L::planes * L::panel + r0 * 128 +
                              (((c >> 3) ^ (r0 & 7)) << 4) + (c & 7) * 2;
         if (vec) {
@@ -472,7 +476,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
                     for (int e = 0; e < V; ++e) v[i][e] = in ? v[i][e] : 0.0f;
                     if (kDz)
 #pragma unroll
-                        for (int e = 0; e < V; ++e) sum[h][e] += v[i][e];
+                        for (int e = 0; e < V; ++e) more[e] += v[i][e];
                     put_columns<L::planes>(dst + (i0 + i) * kStep * 128, L::panel, v[i]);
                 }
             }
@@ -492,7 +496,7 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     v[e] = row && col + e < cols ? v[e] : 0.0f;
-                    if (kDz) sum[h][e] += v[e];
+                    if (kDz) more[e] += v[e];
                 }
                 put_columns<L::planes>(dst + i * kStep * 128, L::panel, v);
             }
@@ -513,10 +517,13 @@ __device__ __forceinline__ void make_operand(unsigned char* operand, const T* sr
                 to_dz<kAct>(v, w);
                 if (kDz)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) sum[h][e] += v[e];
+                    for (int e = 0; e < V; ++e) more[e] += v[e];
                 put_columns<L::planes>(dst + (r - r0) * 128, L::panel, v);
             }
         }
+        if (kDz)
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[h][e] += more[e];
     }
 }
 
