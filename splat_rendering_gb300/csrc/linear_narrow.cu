@@ -109,7 +109,6 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
         *s_fail = 0u;
     }
     if (warp == 1) tmem_alloc(s_taddr, kCols);
-    pdl_next();
     pdl_begin();
     if (tid < 128)
         s_bias[tid] = q.out.bias && n0 + tid < q.out.n ? q.out.bias[n0 + tid] : 0.0f;
@@ -134,6 +133,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
+    pdl_next();   // (not before this block has its tensor memory: the next one's would wait with it)
     if (warp == 0) {
         if (elect_one()) {   // ---- raw tiles
             int n = 0;
@@ -602,7 +602,6 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
         *s_fail = 0u;
     }
     if (warp == 0) tmem_alloc(s_taddr, 512);
-    pdl_next();
     pdl_begin();
     if (q.want_x) {   // W, rows of outputs: an MN-major operand; zeros in the rows up to the next 16
         const int rows = (q.n + 15) / 16 * 16, chunks = (q.k + 7) / 8;
@@ -623,6 +622,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_taddr;
+    pdl_next();   // (not before this block has its tensor memory: the next one's would wait with it)
     const int first = blockIdx.x, step = gridDim.x;
     if (warp == 17) {
         if (q.raw && elect_one()) {   // ---- raw pieces, in the order in which they are used
