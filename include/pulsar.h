@@ -356,8 +356,10 @@ int pulsar_learn_destroy(pulsar_learn_t h);
  * result is invalid and the handle should be destroyed). */
 int pulsar_learn_status(pulsar_learn_t h, void* stream);
 
-/* Bytes of workspace a call of these sizes needs (the forward embedding and
- * dropout need none), or PULSAR_ERR_ARG. */
+/* Bytes of workspace a call of these sizes needs (the forward embedding,
+ * dropout and a linear layer's forward call of up to eight rows need none), or
+ * PULSAR_ERR_ARG.  A linear layer's is what its forward and its backward call
+ * need, tensors at any alignment. */
 int64_t pulsar_embed_workspace(int64_t n, int64_t rows, int64_t dim);
 int64_t pulsar_group_norm_workspace(int64_t images, int64_t pixels, int32_t channels,
                                     int32_t groups);

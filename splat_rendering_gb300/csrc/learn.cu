@@ -257,7 +257,7 @@ int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, i
     const LinearCall c{x, weight, rows, inputs, outputs, act, dtype, pre, y, bias, residual,
                        nullptr, nullptr, nullptr, nullptr};
     if (!h || !linear_args(c) || (rows > 0 && (!x || !weight || !y))) return PULSAR_ERR_ARG;
-    if ((int64_t)linear_workspace(rows, inputs, outputs, dtype) > h->bytes)
+    if ((int64_t)linear_forward_workspace(rows, inputs, outputs, dtype) > h->bytes)
         return PULSAR_ERR_WORKSPACE;
     DeviceGuard guard(h->device);
     return cuda_err(launch_linear_forward(c, h->state, h->ws, h->n_sms, as_stream(stream)));

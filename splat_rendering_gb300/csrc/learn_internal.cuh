@@ -212,6 +212,7 @@ struct LinearCall {
     float* grad_bias;
 };
 size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype);
+size_t linear_forward_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype);
 cudaError_t prepare_linear();
 cudaError_t launch_linear_forward(const LinearCall& c, LearnState* st, void* ws, int n_sms,
                                   cudaStream_t stream);

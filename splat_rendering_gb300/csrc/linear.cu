@@ -249,7 +249,6 @@ k_linear_joins(const __grid_constant__ Joins q) {
 // in flight (a row of 4096 into 2048 outputs in 16 bits: 5.1 us in a chain of
 // launches, 2.5 by the bytes; one warp to an output, which leaves the SMs one or
 // two blocks each, 5.8, and with four rows 10.3 instead of 6.9).
-constexpr int kFewRows = 8;
 
 template <typename T, int V, int kRows>
 __global__ void __launch_bounds__(256)
@@ -323,35 +322,42 @@ OperandGrid operand_grid(int64_t rows, int64_t cols) {
     return g;
 }
 
+// The workspace of both calls of a layer of these sizes, whatever its tensors' alignment: operands
+// only where a call may take the products, whose own matrices are operands as they lie in 16 bits
+// where that allows it.  (The forms for few rows and narrow layers, forward, have none, those for
+// few outputs and narrow layers, backward, the parts of their sums.)
 struct Space {
     __nv_bfloat16 *x, *w, *dz;
     float *sums, *parts, *parts_w;   // parts: of the outputs or dx, of dW
     size_t bytes;
 };
-Space carve(void* ws, int64_t m, int64_t k, int64_t n, int dtype) {
-    const int planes = dtype == kF32 ? kMaxPlanes : 1;
+template <typename T>
+Space carve(void* ws, int64_t m, int64_t k, int64_t n) {
+    constexpr int kPlanes = sizeof(T) == 4 ? kMaxPlanes : 1;
+    const bool few = is_few(k, n), narrow = is_narrow<T>(k, n);
+    const bool back = !few && !narrow;
+    // (of few outputs the products take x as it lies)
+    const bool products = m > kFewRows && !is_stream<T>(k, n);   // of the forward call
+    const bool wide_few = products && few && sizeof(T) == 2, wide = products && !few;
+    const auto larger = [](size_t a, size_t b) { return a > b ? a : b; };
     Carve c{static_cast<unsigned char*>(ws)};
     Space s;
-    s.x = c.take<__nv_bfloat16>(planes * plane_size(m, k));
-    s.w = c.take<__nv_bfloat16>(planes * plane_size(n, k));
-    s.dz = c.take<__nv_bfloat16>(planes * plane_size(m, n));
-    const int64_t few = is_few(k, n) ? few_parts(m, kMostSms) : 0;
-    int64_t blocks = operand_grid(m, n).blocks;
-    if (blocks < kMostSms) blocks = kMostSms;
-    if (blocks < few) blocks = few;
+    s.x = c.take<__nv_bfloat16>(back || wide ? kPlanes * plane_size(m, k) : 0);
+    s.w = c.take<__nv_bfloat16>(back || wide || wide_few ? kPlanes * plane_size(n, k) : 0);
+    s.dz = c.take<__nv_bfloat16>(back ? kPlanes * plane_size(m, n) : 0);
+    const int64_t blocks = few ? few_parts(m, kMostSms)
+                           : narrow ? kMostSms : operand_grid(m, n).blocks;
     s.sums = c.take<float>((size_t)blocks * n);
-    const size_t y = product_parts(planes, m, n, k), dx = product_parts(planes, m, k, n);
-    size_t dw = product_parts(planes, n, k, m);
-    const bool f32 = dtype == kF32;
-    if (f32 ? is_narrow<float>(k, n) : is_narrow<__nv_bfloat16>(k, n)) {
-        const size_t narrow = (size_t)(f32 ? narrow_parts<float>(m, kMostSms)
-                                           : narrow_parts<__nv_bfloat16>(m, kMostSms)) *
-                              part_size(n, k);
-        if (narrow > dw) dw = narrow;
+    size_t parts = wide || wide_few ? product_parts(kPlanes, m, n, k) : 0, parts_w;
+    if (back) {
+        parts = larger(parts, product_parts(kPlanes, m, k, n));
+        parts_w = product_parts(kPlanes, n, k, m);
+    } else {
+        parts_w = (size_t)(few ? few_parts(m, kMostSms) : narrow_parts<T>(m, kMostSms)) *
+                  part_size(n, k);
     }
-    if ((size_t)few * part_size(n, k) > dw) dw = (size_t)few * part_size(n, k);
-    s.parts = c.take<float>(y > dx ? y : dx);
-    s.parts_w = c.take<float>(dw);
+    s.parts = c.take<float>(parts);
+    s.parts_w = c.take<float>(parts_w);
     s.bytes = c.used;
     return s;
 }
@@ -456,7 +462,7 @@ cudaError_t forward(const LinearCall& c, LearnState* st, void* ws, int n_sms, cu
     cudaError_t e = cudaSuccess;
     if (launch_few<T>(c, q, n_sms, s, &e)) return e;
     if (launch_stream<T>(c, q, st, n_sms, s, &e)) return e;
-    const Space sp = carve(ws, m, k, n, c.dtype);
+    const Space sp = carve<T>(ws, m, k, n);
     Maker<T> make;
     const Matrix x = make.add(c.x, nullptr, kActNone, m, k, sp.x, nullptr);
     const Matrix w = make.add(c.weight, nullptr, kActNone, n, k, sp.w, nullptr);
@@ -478,7 +484,7 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
         if (e == cudaSuccess && c.grad_bias) e = cudaMemsetAsync(c.grad_bias, 0, 4 * n, s);
         return e;
     }
-    const Space sp = carve(ws, m, k, n, c.dtype);
+    const Space sp = carve<T>(ws, m, k, n);
     Joins joins{};
     joins.sums = c.grad_bias ? sp.sums : nullptr;
     joins.sum_blocks = operand_grid(m, n).blocks;
@@ -539,8 +545,12 @@ cudaError_t backward(const LinearCall& c, LearnState* st, void* ws, int n_sms, c
 
 }  // namespace
 
+size_t linear_forward_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
+    return rows <= linear::kFewRows ? 0 : linear_workspace(rows, inputs, outputs, dtype);
+}
 size_t linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, int dtype) {
-    return carve(nullptr, rows, inputs, outputs, dtype).bytes;
+    return dtype == kF32 ? carve<float>(nullptr, rows, inputs, outputs).bytes
+                         : carve<__nv_bfloat16>(nullptr, rows, inputs, outputs).bytes;
 }
 
 cudaError_t prepare_linear() {

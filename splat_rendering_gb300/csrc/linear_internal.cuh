@@ -530,6 +530,8 @@ cudaError_t launch_product(const Result& q, const Matrix& a, bool a_mn, const Ma
 // Narrow layers (linear_narrow.cu).  The forward call: false where the layer is none.
 cudaError_t prepare_narrow();
 template <typename T>
+bool is_stream(int64_t inputs, int64_t outputs);   // of the forward call
+template <typename T>
 bool launch_stream(const LinearCall& c, const Result& q, LearnState* st, int n_sms, cudaStream_t s,
                    cudaError_t* e);
 template <typename T>
@@ -539,6 +541,8 @@ int narrow_parts(int64_t rows, int n_sms);         // sums of dW, [outputs][inpu
 template <typename T>
 cudaError_t launch_narrow(const LinearCall& c, float* parts, float* sums, LearnState* st, int n_sms,
                           cudaStream_t s);
+
+constexpr int64_t kFewRows = 8;   // of the forward call that the products have no part in (linear.cu)
 
 // Layers of a few outputs (linear_few.cu).  The forward call: false where another form is faster.
 constexpr int64_t kFewOutputs = 4, kFewInputs = 2048;

@@ -12,7 +12,8 @@ namespace {
 // over an image) is bound by its rows' way in and out.  One launch, a
 // persistent CTA per SM, tiles of 128 rows, each read and written once.  Roles:
 // one thread keeps a ring of raw tiles filled (128 rows are one contiguous bulk
-// copy, whatever their width), eight warps make a tile's operand from it, 64
+// copy, whatever their width, but for what lies before x's first 16-byte boundary
+// in a tile and behind its last), eight warps make a tile's operand from it, 64
 // columns of the contraction at a time (in 32 bits its three planes), one
 // thread issues the MMAs, and eight warps finish the tile from tensor memory.
 // The weights are made into operands by every CTA once, and stay.
@@ -46,7 +47,8 @@ struct Stream {
     int k, panels;         // of the contraction
     int np, blocks;        // outputs of a block (a multiple of 16), blocks
     int raws, units;       // raw tiles, operand panels in flight
-    bool vec;              // a row of x, and of the weight, is whole 16-byte vectors
+    int shift;             // bytes from a 16-byte boundary to x, as to every tile of it
+    bool vec, vec_w;       // rows of x (the weight) are whole 16-byte vectors
     bool skip;             // there is a residual, on 16 bytes, and one block of outputs
     Result out;
 };
@@ -54,7 +56,7 @@ struct StreamSmem {
     int raw, raw_bytes, unit, unit_bytes, weight, weight_panel, exchange, bars, bytes;
 };
 __host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, int panels, int np,
-                                                  int raws, int units) {
+                                                  int raws, int units, int shift) {
     StreamSmem s;
     s.unit = 0;
     s.unit_bytes = planes * kBlock * kPanel * 2;
@@ -62,7 +64,7 @@ __host__ __device__ inline StreamSmem stream_smem(int planes, int size, int k, i
     s.weight_panel = planes * np * kPanel * 2;
     s.exchange = s.weight + panels * s.weight_panel;
     s.raw = s.exchange + 8 * 32 * 32 * 4;
-    s.raw_bytes = (kBlock * k * size + 127) / 128 * 128;
+    s.raw_bytes = (kBlock * k * size + shift + 127) / 128 * 128;
     s.bars = s.raw + raws * s.raw_bytes;
     s.bytes = s.bars + 256 + 1024;
     return s;
@@ -78,7 +80,8 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
     extern __shared__ unsigned char raw_smem[];
     __shared__ __align__(16) float s_bias[128];
     unsigned char* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
-    const StreamSmem L = stream_smem(kPlanes, sizeof(T), q.k, q.panels, q.np, q.raws, q.units);
+    const StreamSmem L = stream_smem(kPlanes, sizeof(T), q.k, q.panels, q.np, q.raws, q.units,
+                                     q.shift);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L.bars);
     uint64_t* raw_empty = raw_full + 4;
     uint64_t* unit_full = raw_empty + 4;
@@ -122,7 +125,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             const int n = q.k - c * 8 < 8 ? q.k - c * 8 : 8;
             if (n0 + r < q.out.n && n > 0)
                 load8(static_cast<const T*>(q.weight) + (int64_t)(n0 + r) * q.k + c * 8, n,
-                      q.vec && n == 8, v);
+                      q.vec_w && n == 8, v);
             put_chunk<kPlanes>(smem + L.weight + (c >> 3) * L.weight_panel + r * 128 +
                                    (((c & 7) ^ (r & 7)) << 4),
                                q.np * 128, v);
@@ -147,18 +150,23 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
                     (uint32_t)((left < kBlock ? left : kBlock) * q.k * (int)sizeof(T));
                 const unsigned char* src =
                     static_cast<const unsigned char*>(q.x) + t * kBlock * q.k * (int64_t)sizeof(T);
-                unsigned char* dst = smem + L.raw + s * L.raw_bytes;
+                unsigned char* dst = smem + L.raw + s * L.raw_bytes + q.shift;
                 if (q.skip) {   // its residual is on its way to the L2 before the epilogue asks
                     const uint32_t row = (uint32_t)(q.out.n * (int)sizeof(T));
                     prefetch_l2(static_cast<const unsigned char*>(q.out.residual) +
                                     t * kBlock * (int64_t)row,
                                 (uint32_t)(left < kBlock ? left : kBlock) * row & ~15u);
                 }
-                const uint32_t bulk = bytes & ~15u;   // the last rows need not end on 16 bytes
-                for (uint32_t e = bulk / sizeof(T); e < bytes / sizeof(T); ++e)
-                    reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(src)[e];
+                // (neither the first rows need begin on 16 bytes nor the last ones end there)
+                const auto alone = [&](uint32_t from, uint32_t to) {
+                    for (uint32_t e = from / sizeof(T); e < to / sizeof(T); ++e)
+                        reinterpret_cast<T*>(dst)[e] = reinterpret_cast<const T*>(src)[e];
+                };
+                const uint32_t head = min((16u - q.shift) & 15u, bytes), bulk = (bytes - head) & ~15u;
+                alone(0, head);
+                alone(head + bulk, bytes);
                 if (bulk)
-                    bulk_load(dst, src, bulk, raw_full + s);
+                    bulk_load(dst + head, src + head, bulk, raw_full + s);
                 else
                     mbar_arrive(raw_full + s);
             }
@@ -222,7 +230,7 @@ k_linear_stream(const __grid_constant__ Stream q, LearnState* st) {
             const int s = n % q.raws;
             ok = warp_all(mbar_wait(raw_full + s, (n / q.raws) & 1) && !*s_fail);
             if (!ok) break;
-            const T* tile = reinterpret_cast<const T*>(smem + L.raw + s * L.raw_bytes);
+            const T* tile = reinterpret_cast<const T*>(smem + L.raw + s * L.raw_bytes + q.shift);
             const int64_t left = q.out.m - t * kBlock;
             const int rows = (int)(left < kBlock ? left : kBlock);
             for (int h = 0; h < q.panels; ++h, ++u) {
@@ -973,7 +981,7 @@ k_linear_narrow(const __grid_constant__ Narrow q, LearnState* st) {
 template <typename T>
 bool stream_plan(const LinearCall& c, Stream* q, int* smem) {
     constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-    if (c.inputs > kStreamMaxK || c.outputs > kStreamBlocks * kStreamN<T> || !aligned16(c.x)) return false;
+    if (!is_stream<T>(c.inputs, c.outputs)) return false;
     q->x = c.x;
     q->weight = c.weight;
     q->tiles = ceil_div(c.rows, kBlock);
@@ -981,10 +989,13 @@ bool stream_plan(const LinearCall& c, Stream* q, int* smem) {
     q->panels = (int)ceil_div(c.inputs, kPanel);
     q->blocks = (int)ceil_div(c.outputs, kStreamN<T>);
     q->np = q->blocks > 1 ? kStreamN<T> : (int)ceil_div(c.outputs, 16) * 16;
-    q->vec = c.inputs % VecOf<T>::n == 0 && aligned16(c.weight);
+    q->shift = (int)(reinterpret_cast<uintptr_t>(c.x) & 15u);
+    q->vec = c.inputs % VecOf<T>::n == 0 && q->shift == 0;
+    q->vec_w = c.inputs % VecOf<T>::n == 0 && aligned16(c.weight);
     // as many operands, then raw tiles in flight as fit
     const auto fits = [&](int raws, int units) {
-        *smem = stream_smem(kPlanes, sizeof(T), q->k, q->panels, q->np, raws, units).bytes;
+        *smem = stream_smem(kPlanes, sizeof(T), q->k, q->panels, q->np, raws, units, q->shift)
+                    .bytes;
         return *smem <= kStreamSmemMax;
     };
     for (int units = 2; units >= 1; --units)
@@ -1019,6 +1030,13 @@ cudaError_t prepare_back() {
 }
 
 }  // namespace
+
+template <typename T>
+bool is_stream(int64_t inputs, int64_t outputs) {
+    return inputs <= kStreamMaxK && outputs <= kStreamBlocks * kStreamN<T>;
+}
+template bool is_stream<float>(int64_t, int64_t);
+template bool is_stream<__nv_bfloat16>(int64_t, int64_t);
 
 template <typename T>
 bool launch_stream(const LinearCall& c, const Result& q, LearnState* st, int n_sms, cudaStream_t s,
