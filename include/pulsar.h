@@ -440,7 +440,9 @@ int pulsar_orthogonalize(pulsar_learn_t h, const void* grad, int64_t batch, int6
  *   residual [rows,outputs] dtype; NULL: none
  *   y        [rows,outputs] dtype, overwritten; may be residual
  *   pre      [rows,outputs] dtype, overwritten with z for the backward call;
- *            NULL: not wanted.  pre and y may not be x, weight or each other.
+ *            NULL: not wanted
+ * y and pre share no memory with x, weight, bias, each other or (but for a y
+ * that is the residual) the residual: PULSAR_ERR_ARG.
  * 0 <= rows <= 0x7fff0000, 1 <= inputs, outputs <= 65536, and rows * inputs
  * and rows * outputs at most 2^38.
  * Products are exact and sums have 32 bits: in bfloat16 a result is rounded
@@ -462,7 +464,8 @@ int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, i
  *   pre    may be NULL where act is PULSAR_ACT_NONE
  *   grad_x [rows,inputs] dtype; grad_weight [outputs,inputs] dtype; grad_bias
  *          [outputs] float32; each overwritten, each may be NULL (not
- *          requested), none may be an input.
+ *          requested); none shares memory with an input or another:
+ *          PULSAR_ERR_ARG
  * In bfloat16 dz is rounded to 16 bits as an operand of the products (not for
  * the bias), which leaves grad_x and grad_weight at most sqrt(2) times as far
  * off as their own rounding; without an activation it is grad_y, exactly.  The
@@ -479,7 +482,8 @@ int pulsar_linear_backward(pulsar_learn_t h, const void* grad_y, const void* x,
  * w_i word i mod 4 of Philox4x32 with seven rounds, its key `seed`, its
  * counter offset + *counter + i / 4 (the upper 64 bits of the 128 zero).  The
  * gradient of x is the same call on dL/dout without a residual.
- *   x, residual, out [n] dtype; residual NULL: none; out may be either
+ *   x, residual, out [n] dtype; residual NULL: none; out may be either, and
+ *            shares no memory with them otherwise
  *   offset   the first of ceil(n / 4) counters that the call uses, >= 0
  *   counter  a device int64 that is added to it when the call runs (a call in
  *            a CUDA graph draws new numbers where a replay counts it up);

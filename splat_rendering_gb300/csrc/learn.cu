@@ -51,6 +51,18 @@ bool linear_sizes(int64_t rows, int64_t inputs, int64_t outputs) {
            outputs <= kMaxSide && rows * inputs <= kMaxElements && rows * outputs <= kMaxElements;
 }
 bool valid_act(int a) { return a == PULSAR_ACT_NONE || a == PULSAR_ACT_SILU || a == PULSAR_ACT_RELU; }
+// Tensors as ranges of bytes, and whether two of them share some.
+struct Range {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+           y < x + (uintptr_t)a.bytes;
+}
+int64_t bytes_of(int64_t count, int dtype) { return count * (dtype == PULSAR_BF16 ? 2 : 4); }
+
 bool embed_args(const void* src, const void* tokens, int64_t n, float scale, int dtype, int index,
                 const void* dst) {
     if (!valid_type(dtype) || (index != PULSAR_I32 && index != PULSAR_I64) || !finite(scale))
@@ -243,6 +255,21 @@ int64_t pulsar_linear_workspace(int64_t rows, int64_t inputs, int64_t outputs, i
 static bool linear_args(const LinearCall& c) {
     if (!linear_sizes(c.rows, c.inputs, c.outputs) || !valid_type(c.dtype) || !valid_act(c.act))
         return false;
+    // no output may share memory with an input that is still read, or with another output
+    const int64_t x_bytes = bytes_of(c.rows * c.inputs, c.dtype);
+    const int64_t y_bytes = bytes_of(c.rows * c.outputs, c.dtype);
+    const int64_t w_bytes = bytes_of(c.outputs * c.inputs, c.dtype), b_bytes = 4 * c.outputs;
+    const Range in[] = {{c.x, x_bytes},        {c.weight, w_bytes}, {c.bias, b_bytes},
+                        {c.residual, y_bytes}, {c.grad_y, y_bytes}, {c.grad_y ? c.pre : nullptr, y_bytes}};
+    const Range out[] = {{c.out, y_bytes},    {c.grad_y ? nullptr : c.pre, y_bytes},
+                         {c.grad_x, x_bytes}, {c.grad_weight, w_bytes},
+                         {c.grad_bias, b_bytes}};
+    for (const Range& o : out) {
+        for (const Range& i : in)
+            if (overlap(o, i) && !(&o == &out[0] && &i == &in[3] && o.p == i.p)) return false;
+        for (const Range& other : out)
+            if (&other != &o && overlap(o, other)) return false;
+    }
     for (const void* p : {c.x, c.weight, (const void*)c.pre, (const void*)c.out, c.residual,
                           c.grad_y, (const void*)c.grad_x, (const void*)c.grad_weight})
         if (!aligned_to(p, c.dtype)) return false;
@@ -290,6 +317,11 @@ int pulsar_dropout(pulsar_learn_t h, const void* x, const void* residual, int64_
         offset < 0 || !aligned_to(x, dtype) || !aligned_to(residual, dtype) ||
         !aligned_to(out, dtype) || (reinterpret_cast<uintptr_t>(counter) & 7u) != 0 ||
         (n > 0 && (!x || !out)))
+        return PULSAR_ERR_ARG;
+    const Range result{out, bytes_of(n, dtype)};
+    if ((out != x && overlap(result, Range{x, result.bytes})) ||
+        (out != residual && overlap(result, Range{residual, result.bytes})) ||
+        overlap(result, Range{counter, 8}))
         return PULSAR_ERR_ARG;
     const double least = std::nearbyint(p * 4294967296.0);
     if (least > 4294967295.0) return PULSAR_ERR_ARG;   // nothing would be kept
