@@ -466,12 +466,13 @@ int pulsar_linear_forward(pulsar_learn_t h, const void* x, const void* weight, i
  *          [outputs] float32; each overwritten, each may be NULL (not
  *          requested); none shares memory with an input or another:
  *          PULSAR_ERR_ARG
- * In bfloat16 dz is rounded to 16 bits as an operand of the products (not for
- * the bias), which leaves grad_x and grad_weight at most sqrt(2) times as far
- * off as their own rounding; without an activation it is grad_y, exactly.  The
+ * In bfloat16 SiLU's dz is rounded to 16 bits as an operand of the products
+ * (not for the bias, nor of up to four outputs), which leaves grad_x and
+ * grad_weight at most sqrt(2) times as far off as their own rounding; the
+ * others' is grad_y or zero, exactly (float32 tensors round nothing).  The
  * tensor cores truncate their sums, of 16 terms at a time, by at most 2^-23: of
  * grad_weight's, over rows, they are added up in float32 every 2^14 rows, so
- * that terms of one sign lose at most 2^-13, a 32nd of a result's own rounding. */
+ * that terms of one sign lose at most 2^-12, a 16th of a result's own rounding. */
 int pulsar_linear_backward(pulsar_learn_t h, const void* grad_y, const void* x,
                            const void* weight, const void* pre, int64_t rows, int64_t inputs,
                            int64_t outputs, int act, int dtype, void* grad_x, void* grad_weight,

@@ -27,7 +27,10 @@ namespace {
 // half as long again: an MMA reads 128 rows of A whatever its columns.)
 //
 // 1M x 64 -> 64 with SiLU in 32 bits: 94 us, 5.7 TB/s of measured 6.8 (its bytes
-// take 79); 777600 x 64 -> 64 in 16 bits 50 us, with a residual 62 (29 and 44).
+// take 79), storing z too 125 (118); 777600 x 64 -> 64 in 16 bits with ReLU 45 us,
+// storing z too 48, with a residual 64 (29, 44 and 44).  In 32 bits a residual, eight
+// vectors of it in flight, does not fit the registers (336 bytes of spills are read
+// again): 1M x 64 -> 64 with SiLU and a residual 171 us, storing z too 214 (118, 158).
 // Bound by the warps' work on a tile, not by its bytes: operands (LDS, three
 // conversions, STS), the exchange and the activation, whose exponential and
 // reciprocal are half of the bfloat16 tile's time on their pipe.

@@ -22,7 +22,10 @@ namespace {
 // -> 4096 in 16 bits: 83 us (101 by single CTAs), dx 82 (95), dW 79 (89); by the
 // operations 73 at the rate of a library's product in a burst, 81 in a long run.
 // dx and dW have 256 and 64 tiles for 76 pairs, which is 84 % of them busy; the
-// MMAs of a 256 x 256 tile follow each other at 1.05 times their own time.
+// MMAs of a 256 x 256 tile follow each other at 1.05 times their own time.  (The
+// outputs' kernels that store parts spill some 200 bytes: 300 x 4096 -> 256 in 16
+// bits 12 us with the join.  dW's drained ones spill up to 100: their times at
+// kDrain.)
 //
 // In 32 bits the tensor cores' accumulation, which truncates, would be what
 // limits the result (of K = 2048, some 2^-18.5 of it): hi hi and the other

@@ -454,7 +454,8 @@ def orthogonalize_workspace(batch: int, m: int, n: int, dtype) -> int:
 
 @functools.lru_cache(maxsize=1024)   # a function of the sizes alone
 def linear_workspace(rows: int, inputs: int, outputs: int, dtype) -> int:
-    """Bytes of workspace of Learner.linear and linear_backward."""
+    """Bytes of workspace of Learner.linear (of up to eight rows it needs none) and
+    linear_backward, tensors at any alignment."""
     return _bytes(load().pulsar_linear_workspace(rows, inputs, outputs, _dtype_code(dtype)),
                   "pulsar_linear_workspace")
 
@@ -690,7 +691,8 @@ class Learner:
                         stream=None):
         """(grad_x, grad_weight, grad_bias) of `linear` for its x, weight and z (`pre`, needed
         where there is an activation); those not in `want` (and not given) are None and not
-        computed.  The residual's gradient is grad_y."""
+        computed.  The residual's gradient is grad_y.  In bfloat16 SiLU's dz is rounded to 16 bits
+        before the products (float32 tensors round nothing): include/pulsar.h says what that costs."""
         rows, inputs, outputs, a, dt, shape = self._layer(x, weight, act)
         dtype, f32 = x.dtype, self._torch.float32
         if a and pre is None:
