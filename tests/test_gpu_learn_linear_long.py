@@ -96,3 +96,29 @@ def test_narrow_against_64_bits(rows, inputs, outputs):
         assert not ref.outside(dx[part], v, e).any()
     ops.status()
     ops.close()
+
+
+@pytest.mark.parametrize("rows,inputs,outputs", [(2 * 152 * 128 * 128 + 5, 64, 64), (200_000, 2560, 1024),
+                                                 (1_000_000, 300, 301)])
+def test_captured_and_on_two_streams(rows, inputs, outputs):
+    """A captured call, replayed beside another handle's on another stream, leaves an eager call's bits."""
+    from splat_rendering_gb300 import pulsar as pl
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, dy, w = (torch.randn(s, device="cuda", generator=g, dtype=BF16)
+                for s in ((rows, inputs), (rows, outputs), (outputs, inputs)))
+    a, b = (pl.Learner(workspace_bytes=pl.linear_workspace(rows, inputs, outputs, BF16)) for _ in range(2))
+    want = a.linear_backward(dy, x, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = a.linear_backward(dy, x, w)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = b.linear_backward(dy, x, w)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) and torch.equal(r, q) for p, q, r in zip(got, want, other))
+    for o in (a, b):
+        assert o.status() == 0
+        o.close()
